@@ -71,7 +71,8 @@ typedef enum {
     SCUTE_ERR_CUDA = 6,         /* a CUDA runtime call failed (see last_error)     */
     SCUTE_ERR_TIMEOUT = 7,      /* a bounded device-side wait gave up              */
     SCUTE_ERR_UNSUPPORTED = 8,  /* valid but outside what this build supports      */
-    SCUTE_ERR_NO_DEVICE = 9     /* no usable sm_103 device                        */
+    SCUTE_ERR_NO_DEVICE = 9,    /* no usable sm_103 device                        */
+    SCUTE_ERR_PAGES = 10        /* cache pages ran out, or a page, slot or length is out of range */
 } scute_status;
 
 /* Limits of this build. */
@@ -238,7 +239,8 @@ scute_status scute_linear_batch_host(scute_ctx *ctx, const scute_call *calls, in
                                      void *stream);
 
 /* Synchronise the device and return (then clear) the device status word:
- * SCUTE_OK, SCUTE_ERR_BAD_ADAPTER or SCUTE_ERR_TIMEOUT (timeout wins). */
+ * SCUTE_OK, SCUTE_ERR_TIMEOUT, SCUTE_ERR_BAD_ADAPTER or SCUTE_ERR_PAGES (the
+ * first of these that was recorded, in this order). */
 scute_status scute_sync_status(scute_ctx *ctx);
 
 /* Token indexing alone, for inspection.  Runs the same kernel scute_linear
@@ -297,6 +299,212 @@ scute_status scute_index_tokens_noalloc(const int8_t *method_of_adapter, int32_t
                                         const int32_t *adapter_ids, int64_t n, int32_t *perm,
                                         int32_t *aid_sorted, int32_t *seg_start, int32_t *seg_aid,
                                         int32_t *counts, int32_t *flags, void *stream);
+
+/* ---------------------------------------------------------------- the decoder block's other operators
+ * The adapted layer computes a transformer block's projections; the calls of
+ * this section do what a serving step needs between them, on the context's
+ * device and in its dtype: cache pages and slots for every request's new
+ * tokens (scute_kv_resize), rotary positions and the cache write
+ * (scute_kv_append), attention of one new token of each request over the
+ * paged cache (scute_paged_attention), and the norms, gate and residual that
+ * close a sub-block (scute_residual_norm).  The article leaves these to the
+ * serving engine; they have no counterpart in it.
+ *
+ * All four are asynchronous on `stream`, allocate nothing and can be captured
+ * in a CUDA graph.  They read lengths, tables and slots on the device, so a
+ * captured step stays valid while those change.  Arguments the host can see
+ * are checked before anything is enqueued; what only the device can see (a
+ * length beyond the block table, a page outside the pool, too few free pages)
+ * never reads or writes out of range and is recorded in the status word:
+ * scute_sync_status then returns SCUTE_ERR_PAGES.  Calls on one context must
+ * be ordered on the device (they share its workspace). */
+
+/* Element type of a cache: BF16 or E4M3 (8-bit float, 4 exponent and 3
+ * mantissa bits) in a bf16 context, FP32 in an fp32 context. */
+typedef enum { SCUTE_KV_BF16 = 0, SCUTE_KV_FP32 = 1, SCUTE_KV_E4M3 = 2 } scute_kv_dtype;
+
+/* A paged key/value cache.  The pools and tables are the caller's; the library
+ * keeps nothing of them.  Cache slot p * page_size + t is token t of page p;
+ * its key of head h is the head_dim consecutive elements at
+ *     k + p * page_stride + t * token_stride + h * head_stride
+ * and its value the same place of v (strides in elements).  Head-major pages
+ * ([page][head][token][dim]) and token-major ones ([page][token][head][dim])
+ * are both strides of this form.  Token t of request r lies in page
+ * block_table[r * table_stride + t / page_size].
+ *   k, v            16-byte aligned; strides multiples of 16 bytes, at least head_dim;
+ *   head_dim        a multiple of 16, 16..256;
+ *   n_pages * page_size  at most 2^31 - 1; offsets are computed in 64 bits;
+ *   k_scale, v_scale  NULL, or device float [kv_heads]: a stored element stands
+ *                   for itself times its head's scale (an E4M3 cache is
+ *                   written as value / scale, rounded to nearest, saturated);
+ *   block_table     needed by scute_paged_attention only. */
+typedef struct {
+    void *k, *v;
+    int32_t dtype;                /* scute_kv_dtype */
+    int32_t n_pages, page_size, kv_heads, head_dim;
+    int64_t page_stride, token_stride, head_stride;
+    const int32_t *block_table;   /* device [n_req][table_stride] */
+    int64_t table_stride;
+    int32_t table_cols;           /* entries of a row that may be read */
+    const float *k_scale, *v_scale;
+} scute_kv_cache;
+
+#define SCUTE_MAX_REQUESTS 16384
+#define SCUTE_MAX_HEAD_DIM 256
+
+/* Give each request the pages of its new length, and each new token its slot.
+ * Request r has len_in[r] cached tokens in pages block_table[r][0 ..
+ * ceil(len_in[r] / page_size)) and shall have len_new[r].
+ *   - A request that shrinks (to 0: it has ended) gives up its last pages.
+ *     They go on top of the free list, in the order of requests and, within
+ *     one, of its table.  Its table row is left as it is.
+ *   - A request that grows takes its pages from the top of the free list (the
+ *     ones just given up included), in the order of requests; they are
+ *     written behind its old ones in its row.  Requests are served while both
+ *     last: a request that needs pages is refused when it and those before it
+ *     need more than there are; then, of the rest, one is refused when its new
+ *     tokens and those before it (of requests not refused for pages) are more
+ *     than max_new.
+ *     A refused request keeps its length and takes nothing
+ *     (SCUTE_ERR_PAGES); a request that grows within its last page is never
+ *     refused for want of pages.
+ *   - The new tokens of served requests, in order, are the step's token rows:
+ *     slot_map[i], positions[i] and token_req[i] are row i's cache slot, its
+ *     position in its request and its request.  Rows beyond them, up to
+ *     max_new, get -1, 0 and -1 (scute_kv_append skips slot -1), so that a
+ *     captured step can have a fixed number of rows.
+ *   - cu_new [n_req + 1]: request r's rows are cu_new[r] .. cu_new[r + 1).
+ * len_in, len_new, len_out  device int32 [n_req]; len_out may be len_in.  A
+ *     length outside 0 .. table_cols * page_size is an error
+ *     (SCUTE_ERR_PAGES): as len_in it counts as the nearest one inside, as
+ *     len_new the request keeps its length;
+ * free_pages  device int32 [n_free_max], the free list: pages free_pages[0 ..
+ *     *free_in), the top last.  Entries from the new count on keep what they
+ *     held;
+ * free_in, free_out  device int32: the list's count; free_out may be free_in.
+ * n_req is 0..SCUTE_MAX_REQUESTS, n_req * table_cols and n_free_max at most
+ * 2^31 - 1, max_new 0..2^30.  A step's pages are fixed by
+ * the arguments alone, whatever order the device works in. */
+scute_status scute_kv_resize(scute_ctx *ctx, const int32_t *len_in, const int32_t *len_new, int n_req,
+                             int32_t *block_table, int64_t table_stride, int table_cols, int page_size,
+                             int32_t *free_pages, int64_t n_free_max, const int32_t *free_in,
+                             int32_t *free_out, int32_t *len_out, int32_t *cu_new, int32_t *slot_map,
+                             int32_t *positions, int32_t *token_req, int64_t max_new, void *stream);
+
+/* Rotary positions.  Pair i of a head's first rotary_dim elements is turned by
+ * the angle whose cosine and sine stand in row p of the table:
+ *     (a, b) -> (a cos - b sin, b cos + a sin),
+ *     cos = cos_sin[p][i], sin = cos_sin[p][rotary_dim / 2 + i].
+ * Pair i is elements i and i + rotary_dim / 2, or 2i and 2i + 1 when
+ * `interleaved`; elements from rotary_dim on pass unchanged.  With several axes
+ * (time, height, width of an image or video token) the pairs are cut into
+ * consecutive sections, and p is the token's position on its section's axis.
+ *   cos_sin     device float [n_pos][rotary_dim] (scute_rope_table);
+ *   positions   device int32, axis a of token t at a * axis_stride + t; a
+ *               position outside 0..n_pos-1 counts as the nearest one inside
+ *               and is recorded (SCUTE_ERR_PAGES);
+ *   n_axes      1..4; section[a] pairs each, rotary_dim / 2 in all (with one
+ *               axis, section is not read);
+ *   rotary_dim  even, 2..head_dim. */
+typedef struct {
+    const float *cos_sin;
+    int32_t n_pos, rotary_dim, interleaved, n_axes;
+    int32_t section[4];
+    const int32_t *positions;
+    int64_t axis_stride;
+} scute_rope;
+
+/* Fill a rotary table: cos_sin[p][i] = cos(p f_i), cos_sin[p][rotary_dim / 2 + i]
+ * = sin(p f_i), computed in 64 bits, with f_i = inv_freq[i] (device double
+ * [rotary_dim / 2]: a stretched context's own frequencies) or, when inv_freq is
+ * NULL, theta^(-2i / rotary_dim). */
+scute_status scute_rope_table(scute_ctx *ctx, float *cos_sin, int n_pos, int rotary_dim, double theta,
+                              const double *inv_freq, void *stream);
+
+/* Write the keys and values of n token rows into the cache, keys (and queries)
+ * turned by their positions.
+ *   slot_map  device int32 [n]: row t's cache slot, or -1 for none; a slot
+ *             outside the pool is skipped and recorded (SCUTE_ERR_PAGES).  Two
+ *             rows may not name one slot;
+ *   k, v      context dtype, head h of row t at t * k_stride + h * head_dim
+ *             (v_stride); q [q_heads heads] the same way, written to q_out
+ *             (which may be q) for every row, those without a slot too;
+ *             q NULL: keys and values only;
+ *   rope      NULL: no turning (q must then be NULL).
+ * Strides are in elements, at least heads * head_dim; no alignment beyond the
+ * element's is needed (16-byte aligned rows are fastest).  Sums are in 32 bits,
+ * rounded once.  n is 0..2^24. */
+scute_status scute_kv_append(scute_ctx *ctx, const scute_kv_cache *kv, const int32_t *slot_map, int64_t n,
+                             const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                             const void *q, int64_t q_stride, int q_heads, void *q_out,
+                             int64_t q_out_stride, const scute_rope *rope, void *stream);
+
+/* Attention of one new token of each request over its cached tokens:
+ *     out[r][h] = sum_t p_t v_t,  p = softmax over t of score(q[r][h] . k_t),
+ * over the last kv_len[r] cached tokens (with window > 0: the last
+ * min(kv_len[r], window) of them), k_t and v_t of key/value head h / (q_heads /
+ * kv_heads).  score(x) = scale x, or softcap tanh(scale x / softcap) with
+ * softcap > 0.  A request without tokens gets zeros (and an lse of -infinity).
+ *   q, out    context dtype [n_req][q_heads * head_dim], rows q_stride and
+ *             out_stride elements apart; 16-byte aligned, strides multiples of
+ *             16 bytes; out may be q;
+ *   kv_len    device int32 [n_req]; more than table_cols * page_size counts as
+ *             that many and is recorded; so is a table entry outside the pool,
+ *             whose tokens are left out (SCUTE_ERR_PAGES).  Nothing beyond a
+ *             request's length is read;
+ *   lse       NULL, or device float [n_req][q_heads]: log sum exp of the scores
+ *             (joins this result with one over other tokens);
+ *   scale     0: 1 / sqrt(head_dim).
+ * n_req is 0..SCUTE_MAX_REQUESTS; q_heads a multiple of kv_heads.  Scores,
+ * softmax statistics and sums are held in 32 bits.  The work is cut over the
+ * whole batch's tokens, whatever request they belong to, and joined in a fixed
+ * order: the same call gives the same bits. */
+typedef struct {
+    const void *q;
+    int64_t q_stride;
+    void *out;
+    int64_t out_stride;
+    float *lse;
+    const int32_t *kv_len;
+    int32_t n_req, q_heads;
+    float scale, softcap;
+    int32_t window;
+} scute_attention;
+scute_status scute_paged_attention(scute_ctx *ctx, const scute_kv_cache *kv, const scute_attention *a,
+                                   void *stream);
+
+/* The end of a sub-block and the beginning of the next, for n token rows:
+ *     h = residual + scale * gate * post(y),   out = pre(h).
+ * post and pre are norms over a row of d: x / sqrt(mean(x^2) + eps) * w + b, or
+ * with `layer` the same of x - mean(x).  Everything between is held in 32 bits;
+ * out and residual_out are each rounded once (pre reads h before its rounding).
+ *   y, residual, out, residual_out   context dtype, rows of d elements their
+ *              stride apart; residual NULL counts as zeros; residual_out
+ *              (NULL: not written) may be residual; out NULL: no norm after;
+ *   post_w, post_b, pre_w, pre_b   device float [d]; post_w NULL: no norm of
+ *              y (post_b must then be NULL); pre_w NULL: ones; biases NULL: zeros;
+ *   gate_vec   NULL, or device float [d]; gate_rows NULL, or context dtype
+ *              [n][d], rows gate_stride apart; at most one of the two;
+ *   n 0..2^24, d 1..SCUTE_MAX_NORM_DIM, eps >= 0; no alignment beyond the
+ *   element's is needed (16-byte aligned rows are fastest). */
+#define SCUTE_MAX_NORM_DIM 32768
+typedef struct {
+    const void *y;
+    int64_t y_stride;
+    const void *residual;
+    int64_t residual_stride;
+    void *residual_out;
+    int64_t residual_out_stride;
+    void *out;
+    int64_t out_stride;
+    const float *post_w, *post_b, *pre_w, *pre_b;
+    const float *gate_vec;
+    const void *gate_rows;
+    int64_t gate_stride;
+    float scale, eps;
+    int32_t layer;
+} scute_norm;
+scute_status scute_residual_norm(scute_ctx *ctx, const scute_norm *a, int64_t n, int d, void *stream);
 
 /* ---------------------------------------------------------------- byte model
  * Zero-parameter byte and time model (article, section "Where is the cheapest
@@ -408,7 +616,11 @@ enum {
     SCUTE_KIND_VERA_SHRINK = 5,  /* VeRA shared shrink GEMM                    */
     SCUTE_KIND_VERA_EXPAND = 6,  /* VeRA shared expand GEMM                    */
     SCUTE_KIND_OFT_PASS = 7,     /* rotation as its own pass (scute_set_variant) */
-    SCUTE_KIND_S_PASS = 8        /* s as its own pass (scute_set_variant)      */
+    SCUTE_KIND_S_PASS = 8,       /* s as its own pass (scute_set_variant)      */
+    SCUTE_KIND_KV_RESIZE = 9,    /* scute_kv_resize                            */
+    SCUTE_KIND_KV_APPEND = 10,   /* scute_kv_append                            */
+    SCUTE_KIND_ATTENTION = 11,   /* scute_paged_attention                      */
+    SCUTE_KIND_NORM = 12         /* scute_residual_norm                        */
 };
 scute_status scute_timing_enable(scute_ctx *ctx, int enable);
 scute_status scute_timing_reset(scute_ctx *ctx);

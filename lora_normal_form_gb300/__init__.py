@@ -21,7 +21,7 @@ LORA, DORA, IA3, VERA, OFT, NF = range(6)
 METHOD_ID = {"lora": LORA, "dora": DORA, "ia3": IA3, "vera": VERA, "oft": OFT, "nf": NF}
 BF16, FP32 = 0, 1
 STATUS = {0: "OK", 1: "ERR_ARG", 2: "ERR_SHAPE", 3: "ERR_DTYPE", 4: "ERR_OOM", 5: "ERR_BAD_ADAPTER",
-          6: "ERR_CUDA", 7: "ERR_TIMEOUT", 8: "ERR_UNSUPPORTED", 9: "ERR_NO_DEVICE"}
+          6: "ERR_CUDA", 7: "ERR_TIMEOUT", 8: "ERR_UNSUPPORTED", 9: "ERR_NO_DEVICE", 10: "ERR_PAGES"}
 MAX_TOKENS = 16384
 TIMING_SLOTS = 256
 BM_MAX_KERNELS = 64
@@ -76,6 +76,115 @@ class Call(ctypes.Structure):
 
 MAX_CALLS = 8
 
+# ------------------------------------------------------------------ paged cache and block operators
+KV_BF16, KV_FP32, KV_E4M3 = 0, 1, 2
+_KV_DTYPE = {"torch.bfloat16": KV_BF16, "torch.float32": KV_FP32, "torch.float8_e4m3fn": KV_E4M3}
+MAX_REQUESTS, MAX_HEAD_DIM, MAX_NORM_DIM = 16384, 256, 32768
+
+
+class _KvCacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("table_cols", ctypes.c_int32), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("n_pos", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("section", ctypes.c_int32 * 4),
+                ("positions", ctypes.c_void_p), ("axis_stride", ctypes.c_int64)]
+
+
+class _AttentionStruct(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_int64), ("lse", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("n_req", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("softcap", ctypes.c_float), ("window", ctypes.c_int32)]
+
+
+class _NormStruct(ctypes.Structure):
+    _fields_ = [("y", ctypes.c_void_p), ("y_stride", ctypes.c_int64), ("residual", ctypes.c_void_p),
+                ("residual_stride", ctypes.c_int64), ("residual_out", ctypes.c_void_p),
+                ("residual_out_stride", ctypes.c_int64), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+                ("post_w", ctypes.c_void_p), ("post_b", ctypes.c_void_p), ("pre_w", ctypes.c_void_p),
+                ("pre_b", ctypes.c_void_p), ("gate_vec", ctypes.c_void_p), ("gate_rows", ctypes.c_void_p),
+                ("gate_stride", ctypes.c_int64), ("scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("layer", ctypes.c_int32)]
+
+
+class KvCache:
+    """A paged key/value cache over the caller's tensors (scute_kv_cache).
+
+    ``k``, ``v``: device pools [n_pages, kv_heads, page_size, head_dim], or
+    [n_pages, page_size, kv_heads, head_dim] with ``token_major``; the strides
+    are taken from ``k`` and ``v`` must have the same.  ``block_table``: device
+    int32 [n_req, pages of a request] (attention only).  ``k_scale``,
+    ``v_scale``: device float32 [kv_heads] or None.  Holds references to the
+    tensors, copies nothing."""
+
+    def __init__(self, k, v, block_table=None, token_major=False, k_scale=None, v_scale=None):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ValueError("k and v must be 4-D pools of one shape, layout and type")
+        if str(k.dtype) not in _KV_DTYPE or k.stride(3) != 1:
+            raise ValueError("cache pools are bf16, fp32 or float8_e4m3fn with consecutive elements")
+        tok, head = (1, 2) if token_major else (2, 1)
+        self.tensors = (k, v, block_table, k_scale, v_scale)
+        self.page_size, self.kv_heads, self.head_dim = k.shape[tok], k.shape[head], k.shape[3]
+        # a dimension of one element may carry any stride: give it one that passes for its rows
+        def stride(dim):
+            return k.stride(dim) if k.shape[dim] > 1 else max(k.stride(dim), self.head_dim)
+        self.struct = _KvCacheStruct(k.data_ptr(), v.data_ptr(), _KV_DTYPE[str(k.dtype)], k.shape[0], self.page_size,
+                                     self.kv_heads, self.head_dim, stride(0), stride(tok), stride(head), None, 0, 0,
+                                     ptr(k_scale), ptr(v_scale))
+        for s in (k_scale, v_scale):
+            if s is not None and (s.numel() != self.kv_heads or not s.is_contiguous() or s.element_size() != 4):
+                raise ValueError("scales are float32, one for each key/value head")
+        if block_table is not None:
+            _check_table(block_table)
+            self.struct.block_table = block_table.data_ptr()
+            self.struct.table_stride = max(block_table.stride(0), block_table.shape[1])
+            self.struct.table_cols = block_table.shape[1]
+        self.ref = ctypes.byref(self.struct)
+
+
+class Rope:
+    """Rotary positions of a step's token rows (scute_rope).  ``cos_sin``: device
+    float32 [n_pos, rotary_dim]; ``positions``: device int32 [n] or [axes, n];
+    ``sections``: pairs of each axis (several axes)."""
+
+    def __init__(self, cos_sin, positions, sections=None, interleaved=False):
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        if positions.element_size() != 4 or positions.stride(-1) != 1 or not 1 <= axes <= 4:
+            raise ValueError("positions are int32, [n] or [axes, n] with at most 4 axes")
+        if cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.element_size() != 4:
+            raise ValueError("cos_sin is a contiguous float32 table")
+        if axes > 1 and (sections is None or len(sections) != axes):
+            raise ValueError("several axes need a section each")
+        self.tensors = (cos_sin, positions)
+        self.n = positions.shape[-1]
+        sec = (ctypes.c_int32 * 4)(*(list(sections)[:4] if axes > 1 else []))
+        self.struct = _RopeStruct(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0, axes,
+                                  sec, positions.data_ptr(), positions.stride(0) if axes > 1 else 0)
+        self.ref = ctypes.byref(self.struct)
+
+
+def _check_table(t):
+    if t.dim() != 2 or t.element_size() != 4 or (t.numel() > 1 and t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("a block table is int32 [n_req, pages] with consecutive rows")
+
+
+def _row_stride(t, cols):
+    """Elements between the rows of a [n, ...] tensor whose rows are ``cols``
+    consecutive elements."""
+    if t.dim() == 3:
+        if t.numel() and (t.stride(2) != 1 or t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+            raise ValueError("the heads of a row must be consecutive")
+    elif t.dim() != 2 or (t.numel() > 1 and t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("expected [n, d] or [n, heads, dim] with consecutive elements")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 _SIGS = {
@@ -114,6 +223,19 @@ _SIGS = {
                                            ctypes.c_int64, ctypes.c_int, ctypes.POINTER(ByteReport)]),
     "scute_predict_time": (ctypes.c_int, [ctypes.POINTER(ByteReport), ctypes.c_double, ctypes.c_double,
                                           ctypes.c_double, ctypes.POINTER(ctypes.c_double)]),
+    "scute_kv_resize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                       ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                                       ctypes.c_void_p, ctypes.c_int64] + [ctypes.c_void_p] * 7 +
+                        [ctypes.c_int64, ctypes.c_void_p]),
+    "scute_rope_table": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int,
+                                        ctypes.c_double, ctypes.c_void_p, ctypes.c_void_p]),
+    "scute_kv_append": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                       ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                       ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p,
+                                       ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]),
+    "scute_paged_attention": (ctypes.c_int, [ctypes.c_void_p] * 4),
+    "scute_residual_norm": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
+                                           ctypes.c_void_p]),
     "scute_launch_count": (ctypes.c_int64, [ctypes.c_void_p]),
     "scute_timing_enable": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int]),
     "scute_timing_reset": (ctypes.c_int, [ctypes.c_void_p]),
@@ -168,7 +290,7 @@ def _stream_handle(stream) -> Optional[int]:
     if stream is None:
         import sys
         torch = sys.modules.get("torch")
-        if torch is not None and torch.cuda.is_available() and torch.cuda.is_initialized():
+        if torch is not None and torch.cuda.is_initialized():
             return torch.cuda.current_stream().cuda_stream
         return None
     if isinstance(stream, int):
@@ -286,6 +408,44 @@ def scute_index_tokens_noalloc(method_of_adapter, ids, n, perm, aid_sorted, seg_
         raise ScuteError(code, why)
 
 
+def scute_kv_resize(ctx, len_in, len_new, n_req, block_table, table_stride, table_cols, page_size, free_pages,
+                    n_free_max, free_in, free_out, len_out, cu_new, slot_map, positions, token_req, max_new,
+                    stream=None):
+    _check(ctx, load().scute_kv_resize(ctx, ptr(len_in), ptr(len_new), n_req, ptr(block_table), table_stride,
+                                       table_cols, page_size, ptr(free_pages), n_free_max, ptr(free_in),
+                                       ptr(free_out), ptr(len_out), ptr(cu_new), ptr(slot_map), ptr(positions),
+                                       ptr(token_req), max_new, _stream_handle(stream)))
+
+
+def scute_rope_table(ctx, cos_sin, n_pos, rotary_dim, theta, inv_freq=None, stream=None):
+    _check(ctx, load().scute_rope_table(ctx, ptr(cos_sin), n_pos, rotary_dim, theta, ptr(inv_freq),
+                                        _stream_handle(stream)))
+
+
+def scute_kv_append(ctx, cache: KvCache, slot_map, n, k, k_stride, v, v_stride, q=None, q_stride=0, q_heads=0,
+                    q_out=None, q_out_stride=0, rope: Optional[Rope] = None, stream=None):
+    _check(ctx, load().scute_kv_append(ctx, cache.ref, ptr(slot_map), n, ptr(k), k_stride, ptr(v), v_stride, ptr(q),
+                                       q_stride, q_heads, ptr(q_out), q_out_stride,
+                                       None if rope is None else rope.ref, _stream_handle(stream)))
+
+
+def scute_paged_attention(ctx, cache: KvCache, q, q_stride, out, out_stride, lse, kv_len, n_req, q_heads,
+                          scale=0.0, softcap=0.0, window=0, stream=None):
+    a = _AttentionStruct(ptr(q), q_stride, ptr(out), out_stride, ptr(lse), ptr(kv_len), n_req, q_heads, scale,
+                         softcap, window)
+    _check(ctx, load().scute_paged_attention(ctx, cache.ref, ctypes.byref(a), _stream_handle(stream)))
+
+
+def scute_residual_norm(ctx, n, d, y, y_stride, residual=None, residual_stride=0, residual_out=None,
+                        residual_out_stride=0, out=None, out_stride=0, post_w=None, post_b=None, pre_w=None,
+                        pre_b=None, gate_vec=None, gate_rows=None, gate_stride=0, scale=1.0, eps=1e-5, layer=False,
+                        stream=None):
+    a = _NormStruct(ptr(y), y_stride, ptr(residual), residual_stride, ptr(residual_out), residual_out_stride, ptr(out),
+                    out_stride, ptr(post_w), ptr(post_b), ptr(pre_w), ptr(pre_b), ptr(gate_vec), ptr(gate_rows),
+                    gate_stride, scale, eps, 1 if layer else 0)
+    _check(ctx, load().scute_residual_norm(ctx, ctypes.byref(a), n, d, _stream_handle(stream)))
+
+
 def scute_byte_model(layer: BmLayer, ids_host, n) -> dict:
     rep = ByteReport()
     code = load().scute_byte_model(ctypes.byref(layer), ptr(ids_host), n, ctypes.byref(rep))
@@ -392,7 +552,8 @@ def scute_timing_read(ctx, max_slots: int = TIMING_SLOTS) -> list:
     return [float(buf[i]) for i in range(n.value)]
 
 
-KIND_NAMES = ("step", "index", "rotate", "base_gemm", "lowrank", "vera_shrink", "vera_expand", "oft_pass", "s_pass")
+KIND_NAMES = ("step", "index", "rotate", "base_gemm", "lowrank", "vera_shrink", "vera_expand", "oft_pass", "s_pass",
+              "kv_resize", "kv_append", "attention", "norm")
 
 
 def scute_timing_kinds(ctx, max_slots: int = TIMING_SLOTS) -> list:

@@ -3,10 +3,10 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (BF16, FP32, METHOD_ID, scute_add_layer, scute_create, scute_debug_index, scute_destroy,
-               scute_launch_count, scute_linear, scute_linear_batch, scute_linear_batch_host,
-               scute_linear_host, scute_predict_batch, scute_predict_bytes,
-               scute_register_adapter, scute_set_shared, scute_set_variant, scute_sync_status,
+from . import (BF16, FP32, METHOD_ID, KvCache, Rope, _check_table, _row_stride, scute_add_layer, scute_create, scute_debug_index, scute_destroy,
+               scute_kv_append, scute_kv_resize, scute_launch_count, scute_linear, scute_linear_batch, scute_linear_batch_host,
+               scute_linear_host, scute_paged_attention, scute_predict_batch, scute_predict_bytes,
+               scute_register_adapter, scute_residual_norm, scute_rope_table, scute_set_shared, scute_set_variant, scute_sync_status,
                scute_timing_enable,
                scute_timing_kinds, scute_timing_read, scute_timing_reset, scute_unregister_adapter)
 
@@ -100,6 +100,69 @@ class Context:
     def linear_batch_host(self, calls, ids_host, out_dtype: str = "bf16", stream=None):
         scute_linear_batch_host(self.handle, list(calls), ids_host, int(ids_host.shape[0]),
                                 BF16 if out_dtype == "bf16" else FP32, stream)
+
+    # ---------------------------------------------------------------- between the projections
+    def kv_resize(self, len_in, len_new, block_table, page_size: int, free_pages, free_in, free_out, len_out, cu_new,
+                  slot_map, positions, token_req, stream=None):
+        """Pages for every request's new length, slots for its new tokens (device
+        int32 tensors; scute.h has the layout).  The step has ``slot_map.numel()``
+        token rows."""
+        _check_table(block_table)
+        n, cols = len_in.numel(), block_table.shape[1]
+        scute_kv_resize(self.handle, len_in, len_new, n, block_table,
+                        block_table.stride(0) if block_table.shape[0] > 1 else max(cols, block_table.stride(0)), cols,
+                        page_size, free_pages, free_pages.numel(), free_in, free_out, len_out, cu_new, slot_map,
+                        positions, token_req, slot_map.numel(), stream)
+
+    def rope_table(self, cos_sin, theta: float = 10000.0, inv_freq=None, stream=None):
+        """Fill the float32 table ``cos_sin`` [n_pos, rotary_dim]."""
+        scute_rope_table(self.handle, cos_sin, cos_sin.shape[0], cos_sin.shape[1], theta, inv_freq, stream)
+
+    def kv_append(self, cache: KvCache, slot_map, k, v, q=None, q_out=None, rope: Rope = None, stream=None):
+        """Write k and v [n, kv_heads, dim] (or [n, kv_heads * dim]) into the cache;
+        keys, and queries into ``q_out``, turned by ``rope``."""
+        n, d = slot_map.shape[0], cache.head_dim
+        row = cache.kv_heads * d
+        if k.shape[0] != n or v.shape[0] != n or (q is not None and q.shape[0] != n) or \
+                (rope is not None and rope.n < n):
+            raise ValueError("slot_map, k, v, q and positions differ in rows")
+        if k.numel() != n * row or v.numel() != n * row:
+            raise ValueError("k and v rows are kv_heads * head_dim elements")
+        q_row = 0 if q is None or n == 0 else q.numel() // n
+        if q is not None and (q_row % d or q_out is None or q_out.shape != q.shape):
+            raise ValueError("q rows are heads * head_dim elements, and q_out has q's shape")
+        scute_kv_append(self.handle, cache, slot_map, n, k, _row_stride(k, row), v, _row_stride(v, row), q,
+                        0 if q is None else _row_stride(q, q_row), q_row // d, q_out,
+                        0 if q is None else _row_stride(q_out, q_row), rope, stream)
+
+    def paged_attention(self, cache: KvCache, q, kv_len, out, scale: float = 0.0, softcap: float = 0.0,
+                        window: int = 0, lse=None, stream=None):
+        """One new token of each request over its cached tokens: q and out
+        [n_req, q_heads, dim] (or [n_req, q_heads * dim])."""
+        n = kv_len.shape[0]
+        table = cache.tensors[2]
+        if q.shape[0] != n or out.shape != q.shape or table is None or table.shape[0] < n:
+            raise ValueError("q, out, kv_len and the block table differ in requests")
+        row = 0 if n == 0 else q.numel() // n
+        if row % cache.head_dim or (lse is not None and lse.numel() * cache.head_dim != q.numel()):
+            raise ValueError("q rows are heads * head_dim elements, and lse has one value for each")
+        scute_paged_attention(self.handle, cache, q, _row_stride(q, row), out, _row_stride(out, row), lse, kv_len, n,
+                              max(row // cache.head_dim, cache.kv_heads if n == 0 else 0), scale, softcap, window,
+                              stream)
+
+    def residual_norm(self, y, out=None, residual=None, residual_out=None, pre_w=None, pre_b=None, post_w=None,
+                      post_b=None, gate=None, scale: float = 1.0, eps: float = 1e-5, layer: bool = False, stream=None):
+        """h = residual + scale * gate * post(y), out = pre(h), for rows [n, d].
+        ``gate``: float32 [d], or the context's dtype [n, d]."""
+        n, d = y.shape
+        rows = gate is not None and gate.dim() == 2
+        for t in (out, residual, residual_out, gate if rows else None):
+            if t is not None and t.shape != y.shape:
+                raise ValueError("y, residual, out and a row gate must have one shape")
+        st = lambda t: 0 if t is None else _row_stride(t, d)  # noqa: E731
+        scute_residual_norm(self.handle, n, d, y, st(y), residual, st(residual), residual_out, st(residual_out), out,
+                            st(out), post_w, post_b, pre_w, pre_b, None if rows else gate, gate if rows else None,
+                            st(gate) if rows else 0, scale, eps, layer, stream)
 
     def sync_status(self) -> int:
         return scute_sync_status(self.handle)

@@ -2,59 +2,25 @@
 // fold rule, the per-call launch plan of the adapted linear layer, the byte
 // model and the timing counters.  See include/scute.h for the contract.
 #include <atomic>
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
 #include <mutex>
 #include <string>
 #include <vector>
 
-#include "ctx.h"
+#include "host.h"
 
 using namespace scute;
 
 namespace {
-
-scute_status fail(scute_ctx *c, scute_status s, const char *fmt, ...) {
-    if (c) {
-        va_list ap;
-        va_start(ap, fmt);
-        vsnprintf(c->err, sizeof(c->err), fmt, ap);
-        va_end(ap);
-    }
-    return s;
-}
-
-#define CU_TRY(ctx, expr)                                                                      \
-    do {                                                                                       \
-        cudaError_t _e = (expr);                                                               \
-        if (_e != cudaSuccess) {                                                               \
-            (void)cudaGetLastError();                                                          \
-            if (_e == cudaErrorMemoryAllocation)                                               \
-                return fail(ctx, SCUTE_ERR_OOM, "%s: %s", #expr, cudaGetErrorString(_e));      \
-            return fail(ctx, SCUTE_ERR_CUDA, "%s: %s", #expr, cudaGetErrorString(_e));         \
-        }                                                                                      \
-    } while (0)
-
-// Keeps the context's device current for the duration of one API call.
-struct DeviceGuard {
-    int prev = -1;
-    bool changed = false;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) == cudaSuccess && prev != dev) {
-            if (cudaSetDevice(dev) == cudaSuccess) changed = true;
-        }
-    }
-    ~DeviceGuard() {
-        if (changed) cudaSetDevice(prev);
-    }
-};
 
 // Test hook scute_debug_fail_alloc: while positive, counts the library's
 // device allocations down; the allocation that brings it from 1 to 0 fails as
 // if the device were out of memory (nothing is allocated for it).
 std::atomic<int> g_fail_alloc{0};
 
+}  // namespace
+
+namespace scute {
 cudaError_t dev_malloc(void **p, size_t bytes) {
     int k = g_fail_alloc.load();
     while (k > 0) {
@@ -68,6 +34,9 @@ cudaError_t dev_malloc(void **p, size_t bytes) {
     }
     return cudaMalloc(p, bytes);
 }
+}  // namespace scute
+
+namespace {
 
 bool encode_map_box(scute_ctx *c, CUtensorMap *m, const void *base, uint64_t inner, uint64_t rows, int box_rows);
 
@@ -150,12 +119,6 @@ bool layer_ok(const scute_ctx *c, int layer) {
     return layer >= 0 && layer < c->max_layers && c->layers[layer].present;
 }
 
-void count_launch(scute_ctx *c, int k) { c->launches += k; }
-
-// Timing ring (scute_timing_*): while enabled, every launch (or launch pair)
-// of the hot path is bracketed by an event pair on its stream, tagged with its
-// kind.  Event records made while the stream is being captured become graph
-// nodes, re-recorded on every replay.
 // The device address of a pinned, mapped host buffer (null for pageable
 // memory, device memory, or any pointer the runtime does not know).
 const void *mapped_host(const void *p) {
@@ -166,31 +129,6 @@ const void *mapped_host(const void *p) {
     }
     return at.type == cudaMemoryTypeHost ? at.devicePointer : nullptr;
 }
-
-struct TimedLaunch {
-    scute_ctx *c;
-    cudaStream_t st;
-    int slot = -1;
-    unsigned flags = cudaEventRecordDefault;
-    cudaError_t begin() {
-        if (!c->timing) return cudaSuccess;
-        cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-        cudaError_t e = cudaStreamIsCapturing(st, &cs);
-        if (e != cudaSuccess) return e;
-        if (cs == cudaStreamCaptureStatusActive) flags = cudaEventRecordExternal;
-        slot = c->t_next;
-        return cudaEventRecordWithFlags(c->ev[slot][0], st, flags);
-    }
-    cudaError_t end(int kind) {
-        if (!c->timing || slot < 0) return cudaSuccess;
-        const cudaError_t e = cudaEventRecordWithFlags(c->ev[slot][1], st, flags);
-        c->ev_kind[slot] = kind;
-        c->t_next = (slot + 1) % SCUTE_TIMING_SLOTS;
-        if (c->t_used < SCUTE_TIMING_SLOTS) ++c->t_used;
-        slot = -1;
-        return e;
-    }
-};
 
 }  // namespace
 
@@ -258,6 +196,9 @@ scute_status scute_create(scute_ctx **out, int device, scute_dtype dtype, int ma
               dev_malloc((void **)&c->gpart, sizeof(float) * PART_WORKSPACE_FLOATS) == cudaSuccess &&
               dev_malloc((void **)&c->step_sync, sizeof(int) * STEP_SYNC_INTS) == cudaSuccess &&
               cudaMemset(c->step_sync, 0, sizeof(int) * STEP_SYNC_INTS) == cudaSuccess &&
+              dev_malloc((void **)&c->att_part, sizeof(float) * attend_part_floats(c->num_sms)) == cudaSuccess &&
+              dev_malloc((void **)&c->srv_ctr, sizeof(int) * (1 + attend_ctrs(c->num_sms))) == cudaSuccess &&
+              cudaMemset(c->srv_ctr, 0, sizeof(int) * (1 + attend_ctrs(c->num_sms))) == cudaSuccess &&
               cudaDeviceGetAttribute(&c->smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device) ==
                   cudaSuccess;
     c->step_bn_max = max_tokens <= 64 ? 64 : 128;
@@ -283,7 +224,7 @@ void scute_destroy(scute_ctx *c) {
     void *bufs[] = {c->d_slots, c->d_method, c->d_perm, c->d_aid, c->d_seg_start, c->d_seg_aid, c->d_seg_unit, c->d_seg_tile, c->vs_ctr, c->vs_part,
                     c->d_meta, c->d_status, c->d_err, c->v_part, c->gpart, c->xs, c->U, c->st_x,
                     c->st_out, c->st_ids, c->tmp, c->step_xs, c->step_U, c->step_pre, c->step_part,
-                    c->step_sync, c->step_hx, c->step_hout, c->var_x};
+                    c->step_sync, c->step_hx, c->step_hout, c->var_x, c->att_part, c->srv_ctr};
     for (void *p : bufs)
         if (p) cudaFree(p);
     if (c->ev_made)
@@ -1358,6 +1299,8 @@ scute_status scute_sync_status(scute_ctx *c) {
     CU_TRY(c, cudaMemset(c->d_status, 0, sizeof(int)));
     if (s & STATUS_TIMEOUT) return fail(c, SCUTE_ERR_TIMEOUT, "a device-side wait timed out");
     if (s & STATUS_BAD_ADAPTER) return fail(c, SCUTE_ERR_BAD_ADAPTER, "a token id named no registered adapter");
+    if (s & STATUS_PAGES)
+        return fail(c, SCUTE_ERR_PAGES, "cache pages ran out, or a page, slot, length or position was out of range");
     return SCUTE_OK;
 }
 

@@ -101,6 +101,8 @@ struct scute_ctx {
     std::vector<int64_t> last_plan;   // scute_debug_step_plan: the last decode launch's plan
     void *var_x = nullptr;       // rotated copies of the calls' x (separate rotation pass)
     size_t var_x_cols = 0;
+    float *att_part = nullptr;   // attention: partial sums of rows that several CTAs share
+    int *srv_ctr = nullptr;      // arrival counters of the cache and attention kernels (zero between launches)
     PFN_encodeTiled encode = nullptr;
     int64_t launches = 0;
     bool timing = false;

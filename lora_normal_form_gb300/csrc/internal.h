@@ -17,7 +17,7 @@ enum : int {
 };
 
 // Device status word bits (read back by scute_sync_status).
-enum : int { STATUS_BAD_ADAPTER = 1, STATUS_TIMEOUT = 2 };
+enum : int { STATUS_BAD_ADAPTER = 1, STATUS_TIMEOUT = 2, STATUS_PAGES = 4 };
 
 constexpr int OFT_BLK = 32;
 constexpr int MAX_RANK = 64;          // owned low-rank term
@@ -352,6 +352,89 @@ struct VsTcArgs {
 cudaError_t launch_vera_shrink_tc(const VsTcArgs &p, int grid, cudaStream_t st, bool pdl);
 // beside: a VeRA shrink is launched right after it, to run beside it
 cudaError_t launch_lr_shrink_tc(const LrTcArgs &p, int grid, cudaStream_t st, bool pdl, bool beside);
+
+// ---------------------------------------------------------------- paged cache
+// Element types of a cache (the codes of SCUTE_KV_*).
+enum : int { KV_BF16 = 0, KV_FP32 = 1, KV_E4M3 = 2 };
+struct KvView {
+    void *k, *v;
+    int dtype;
+    int n_pages, page_size, heads, dim;
+    long long page_stride, token_stride, head_stride;   // elements
+    const int32_t *table;
+    long long table_stride;
+    int table_cols;
+    const float *k_scale, *v_scale;
+};
+
+struct ResizeArgs {
+    const int32_t *len_in, *len_new;
+    int n_req, cols, page_size;
+    int32_t *table;
+    long long table_stride;
+    int32_t *free_pages;
+    long long n_free_max;
+    const int32_t *free_in;
+    int32_t *free_out, *len_out, *cu_new, *slot_map, *positions, *token_req;
+    int max_new;
+    int *ctr;                  // arrivals of the launch's CTAs (zero between launches)
+    int *status;
+};
+cudaError_t launch_kv_resize(const ResizeArgs &a, int num_sms, cudaStream_t st);
+
+struct AppendArgs {
+    KvView kv;
+    const int32_t *slot_map;
+    int n;
+    const void *k, *v, *q;
+    void *q_out;
+    long long k_stride, v_stride, q_stride, q_out_stride;
+    int q_heads;
+    int rot, interleaved, n_axes, n_pos;   // rot 0: no turning
+    int bound[4];                          // pairs before the end of each axis's section
+    const float *cos_sin;
+    const int32_t *positions;
+    long long axis_stride;
+    int *status;
+};
+cudaError_t launch_kv_append(bool f32, const AppendArgs &a, int num_sms, cudaStream_t st);
+cudaError_t launch_rope_table(float *cos_sin, int n_pos, int rot, double theta, const double *inv_freq,
+                              cudaStream_t st);
+
+// ---------------------------------------------------------------- attention of one new token
+constexpr int ATT_HEADS = 16;      // query heads of one key/value head that one work row takes
+constexpr int ATT_MAX_DIM = 256;
+struct AttendArgs {
+    KvView kv;
+    const void *q;
+    void *out;
+    long long q_stride, out_stride;
+    float *lse;
+    const int32_t *kv_len;
+    int n_req, q_heads, group;
+    float scale, softcap;
+    int window;
+    float *part;               // partial sums of rows that several CTAs share
+    int *ctr;                  // arrivals at such a row (zero between launches)
+    int *status;
+};
+size_t attend_part_floats(int num_sms);
+int attend_ctrs(int num_sms);
+cudaError_t launch_attend(const AttendArgs &a, int num_sms, cudaStream_t st);
+
+// ---------------------------------------------------------------- norms around a sub-block
+struct NormArgs {
+    const void *y, *residual;
+    void *residual_out, *out;
+    long long y_stride, residual_stride, residual_out_stride, out_stride;
+    const float *post_w, *post_b, *pre_w, *pre_b, *gate_vec;
+    const void *gate_rows;
+    long long gate_stride;
+    float scale, eps;
+    int layer;
+    int n, d;
+};
+cudaError_t launch_residual_norm(bool f32, const NormArgs &a, int num_sms, cudaStream_t st);
 
 // registration-time kernels
 cudaError_t launch_transpose_w(bool f32, const void *W, int rows, int cols, void *Wt, int kdim,

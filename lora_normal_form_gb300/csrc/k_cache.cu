@@ -1,0 +1,323 @@
+// The paged cache's bookkeeping and writes: pages and slots from request
+// lengths (kv_resize), rotary positions and the cache write (kv_append), and
+// the rotary table.
+#include <cuda_fp8.h>
+
+#include "internal.h"
+
+namespace scute {
+
+namespace {
+
+// ---------------------------------------------------------------- kv_resize
+// Request r has o = len_in tokens in have = ceil(o / page) pages and wants w =
+// len_new in want = ceil(w / page).  With drop = max(have - want, 0), need =
+// max(want - have, 0) and their exclusive prefix sums over the requests,
+//   freed page j (0 <= j < P = sum drop) belongs to the last r whose drop_at <= j;
+//   the list then holds L = F + P pages, and the k-th page taken is its entry
+//   L - 1 - k: a freed page again, or one of the F there were.
+// A request is refused when need > 0 and need_at + need > L, or when its new
+// tokens' inclusive prefix (over requests not refused so far) passes max_new.
+// Both prefixes only grow, so the requests that do take pages are the first
+// ones that need any, and their k run from 0 without a gap.  Nothing that is
+// read is written: rows of shrinking requests are only read, the rows of
+// growing ones written behind their old pages, and list entries are written
+// only from F on.  So no thread waits for another, except that the lengths and
+// the count, which may be written in place, follow a launch-wide arrival count.
+constexpr int RS_THREADS = 512;
+
+__device__ __forceinline__ int pages_of(int tokens, int page) {
+    return (int)(((long long)tokens + page - 1) / page);
+}
+
+// Last i in [0, n] with at[i] <= x, for at[0] = 0 <= x and at rising.
+__device__ __forceinline__ int last_at_most(const int *at, int n, int x) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (at[mid] <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// Exclusive prefix sum over the CTA's threads; *total receives the sum.
+__device__ __forceinline__ unsigned long long cta_exclusive(unsigned long long x, unsigned long long *warp_sum,
+                                                            unsigned long long *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned long long inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    unsigned long long before = 0, all = 0;
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+        const unsigned long long s = warp_sum[w];
+        before += w < warp ? s : 0;
+        all += s;
+    }
+    __syncthreads();
+    *total = all;
+    return before + inc - x;
+}
+
+struct Span {
+    int o, w;      // old and wanted length, inside the row
+    bool bad;
+};
+__device__ __forceinline__ Span span_of(const ResizeArgs &a, int r) {
+    const int cap = a.cols * a.page_size;
+    const int o = a.len_in[r], w = a.len_new[r];
+    Span s;
+    s.bad = o < 0 || o > cap || w < 0 || w > cap;
+    s.o = o < 0 ? 0 : o > cap ? cap : o;
+    s.w = w < 0 || w > cap ? s.o : w;
+    return s;
+}
+
+__global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs a) {
+    extern __shared__ int sm[];
+    __shared__ unsigned long long warp_sum[RS_THREADS / 32];
+    __shared__ int s_taken, s_rows, s_flag, s_last;
+    const int n = a.n_req, t = threadIdx.x;
+    int *drop_at = sm, *need_at = sm + (n + 1), *cu = sm + 2 * (n + 1);
+    if (t == 0) s_taken = s_rows = s_flag = 0;
+    const int per = (n + RS_THREADS - 1) / RS_THREADS;
+    const int r0 = min(n, t * per), r1 = min(n, r0 + per);
+
+    // pages given up and needed: one scan of both sums (each below 2^31)
+    unsigned long long mine = 0;
+    bool bad = false;
+    for (int r = r0; r < r1; ++r) {
+        const Span s = span_of(a, r);
+        bad |= s.bad;
+        const int have = pages_of(s.o, a.page_size), want = pages_of(s.w, a.page_size);
+        mine += (unsigned long long)(unsigned)max(have - want, 0) << 32 | (unsigned)max(want - have, 0);
+    }
+    unsigned long long total;
+    unsigned long long run = cta_exclusive(mine, warp_sum, &total);
+    const int P = (int)(total >> 32);
+    int F = *a.free_in;
+    if (F < 0 || F > a.n_free_max) {
+        bad = true;
+        F = F < 0 ? 0 : (int)a.n_free_max;
+    }
+    const long long L = (long long)F + P;
+
+    // new tokens of the requests that get their pages
+    unsigned long long rows = 0;
+    for (int r = r0; r < r1; ++r) {
+        const Span s = span_of(a, r);
+        const int have = pages_of(s.o, a.page_size), want = pages_of(s.w, a.page_size);
+        drop_at[r] = (int)(run >> 32);
+        need_at[r] = (int)(run & 0xffffffffu);
+        const int need = max(want - have, 0);
+        if (s.w > s.o && (need == 0 || need_at[r] + (long long)need <= L)) rows += s.w - s.o;
+        run += (unsigned long long)(unsigned)max(have - want, 0) << 32 | (unsigned)need;
+    }
+    if (t == RS_THREADS - 1) {
+        drop_at[n] = (int)(total >> 32);
+        need_at[n] = (int)(total & 0xffffffffu);
+    }
+    unsigned long long all_rows;
+    unsigned long long at = cta_exclusive(rows, warp_sum, &all_rows);
+    int taken = 0, served = 0;
+    for (int r = r0; r < r1; ++r) {
+        const Span s = span_of(a, r);
+        const int need = max(pages_of(s.w, a.page_size) - pages_of(s.o, a.page_size), 0);
+        cu[r] = (int)min(at, (unsigned long long)a.max_new + 1);
+        if (s.w > s.o) {
+            const bool paged = need == 0 || need_at[r] + (long long)need <= L;
+            if (paged) at += s.w - s.o;
+            if (paged && at <= (unsigned long long)a.max_new) {
+                served = (int)at;
+                if (need) taken = need_at[r] + need;
+            } else {
+                bad = true;
+            }
+        }
+    }
+    if (taken) atomicMax(&s_taken, taken);
+    if (served) atomicMax(&s_rows, served);
+    if (bad) s_flag = 1;
+    __syncthreads();
+    const int A = s_taken, T = s_rows;
+    for (int r = r0; r < r1; ++r) cu[r] = min(cu[r], T);
+    if (t == 0) cu[n] = T;
+    __syncthreads();
+    const long long left = L - A;
+
+    // the k-th page taken from the top of the list
+    auto taken_page = [&](int k) -> int {
+        const long long at_list = L - 1 - k;
+        if (at_list < F) return a.free_pages[at_list];
+        const int j = (int)(at_list - F), r = last_at_most(drop_at, n, j);
+        const int want = pages_of(span_of(a, r).w, a.page_size);
+        return a.table[(long long)r * a.table_stride + want + (j - drop_at[r])];
+    };
+    const int step = gridDim.x * RS_THREADS, g0 = blockIdx.x * RS_THREADS + t;
+    for (int k = g0; k < A; k += step) {
+        const int r = last_at_most(need_at, n, k);
+        const int have = pages_of(span_of(a, r).o, a.page_size);
+        a.table[(long long)r * a.table_stride + have + (k - need_at[r])] = taken_page(k);
+    }
+    for (long long j = g0; F + j < left; j += step) {
+        if (F + j >= a.n_free_max) {
+            s_flag = 1;
+            break;
+        }
+        const int r = last_at_most(drop_at, n, (int)j);
+        const int want = pages_of(span_of(a, r).w, a.page_size);
+        a.free_pages[F + j] = a.table[(long long)r * a.table_stride + want + ((int)j - drop_at[r])];
+    }
+    for (long long i = g0; i < a.max_new; i += step) {
+        int slot = -1, pos = 0, r = -1;
+        if (i < T) {
+            r = last_at_most(cu, n, (int)i);
+            const int o = span_of(a, r).o;
+            pos = o + ((int)i - cu[r]);
+            const int pg = pos / a.page_size, have = pages_of(o, a.page_size);
+            const int page = pg < have ? a.table[(long long)r * a.table_stride + pg] : taken_page(need_at[r] + (pg - have));
+            slot = page * a.page_size + (pos - pg * a.page_size);
+        }
+        a.slot_map[i] = slot;
+        a.positions[i] = pos;
+        a.token_req[i] = r;
+    }
+    for (int r = g0; r <= n; r += step) a.cu_new[r] = cu[r];
+
+    // lengths and the count, once every CTA has read them
+    __threadfence();
+    __syncthreads();
+    if (t == 0) {
+        s_last = atomicAdd(a.ctr, 1) == (int)gridDim.x - 1;
+        if (s_flag) atomicOr(a.status, STATUS_PAGES);
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    for (int r = t; r < n; r += RS_THREADS) {
+        const Span s = span_of(a, r);
+        a.len_out[r] = s.w > s.o ? s.o + (cu[r + 1] - cu[r]) : s.w;
+    }
+    if (t == 0) {
+        *a.free_out = (int)min(left, a.n_free_max);
+        *a.ctr = 0;
+    }
+}
+
+// ---------------------------------------------------------------- kv_append
+template <typename T> __device__ __forceinline__ float to_f(T x) { return (float)x; }
+template <typename T> __device__ __forceinline__ T from_f(float x) { return (T)x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// One thread turns one pair, or passes one element, of one head of one row.
+template <typename T>
+__global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
+    const int row = blockIdx.x, dim = a.kv.dim, half = a.rot / 2;
+    const int slot = a.slot_map[row];
+    const bool in = slot >= 0 && slot < (long long)a.kv.n_pages * a.kv.page_size;
+    if (slot < -1 || (slot >= 0 && !in)) atomicOr(a.status, STATUS_PAGES);
+    const int per_head = dim - half;                // pairs, then the elements that pass
+    const int heads = a.q_heads + 2 * a.kv.heads;
+    const long long at = in ? (slot / a.kv.page_size) * a.kv.page_stride + (slot % a.kv.page_size) * a.kv.token_stride : 0;
+    for (int i = threadIdx.x; i < heads * per_head; i += blockDim.x) {
+        const int h = i / per_head, e = i - h * per_head;
+        const int kind = h < a.q_heads ? 0 : h < a.q_heads + a.kv.heads ? 1 : 2;     // q, k, v
+        const int hk = kind == 0 ? h : kind == 1 ? h - a.q_heads : h - a.q_heads - a.kv.heads;
+        if (kind && !in) continue;
+        const T *src = reinterpret_cast<const T *>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
+                       (long long)row * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + hk * dim;
+        int e0, e1 = -1;
+        if (e < half) {
+            e0 = a.interleaved ? 2 * e : e;
+            e1 = a.interleaved ? 2 * e + 1 : e + half;
+        } else {
+            e0 = e + half;
+        }
+        float x0 = to_f(src[e0]), x1 = e1 >= 0 ? to_f(src[e1]) : 0.f;
+        if (kind < 2 && e1 >= 0) {
+            int ax = 0;
+            while (ax < 3 && e >= a.bound[ax]) ++ax;
+            int p = a.positions[ax * a.axis_stride + row];
+            if (p < 0 || p >= a.n_pos) {
+                atomicOr(a.status, STATUS_PAGES);
+                p = p < 0 ? 0 : a.n_pos - 1;
+            }
+            const float c = a.cos_sin[(long long)p * a.rot + e], s = a.cos_sin[(long long)p * a.rot + half + e];
+            const float y0 = x0 * c - x1 * s;
+            x1 = x1 * c + x0 * s;
+            x0 = y0;
+        }
+        if (kind == 0) {
+            T *dst = reinterpret_cast<T *>(a.q_out) + (long long)row * a.q_out_stride + hk * dim;
+            dst[e0] = from_f<T>(x0);
+            if (e1 >= 0) dst[e1] = from_f<T>(x1);
+        } else {
+            const float *scale = kind == 1 ? a.kv.k_scale : a.kv.v_scale;
+            if (scale) {
+                x0 /= scale[hk];
+                x1 /= scale[hk];
+            }
+            void *pool = kind == 1 ? a.kv.k : a.kv.v;
+            const long long o = at + hk * a.kv.head_stride;
+            if (a.kv.dtype == KV_E4M3) {
+                __nv_fp8_e4m3 *dst = reinterpret_cast<__nv_fp8_e4m3 *>(pool) + o;
+                dst[e0] = __nv_fp8_e4m3(x0);
+                if (e1 >= 0) dst[e1] = __nv_fp8_e4m3(x1);
+            } else {
+                T *dst = reinterpret_cast<T *>(pool) + o;
+                dst[e0] = from_f<T>(x0);
+                if (e1 >= 0) dst[e1] = from_f<T>(x1);
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256) rope_table_kernel(float *out, int n_pos, int half, double theta,
+                                                         const double *inv_freq) {
+    const long long step = (long long)gridDim.x * blockDim.x, all = (long long)n_pos * half;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += step) {
+        const long long p = i / half;
+        const int j = (int)(i - p * half);
+        const double f = inv_freq ? inv_freq[j] : pow(theta, -(double)j / half);
+        double s, c;
+        sincos((double)p * f, &s, &c);
+        out[p * 2 * half + j] = (float)c;
+        out[p * 2 * half + half + j] = (float)s;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_resize(const ResizeArgs &a, int num_sms, cudaStream_t st) {
+    static std::atomic<unsigned long long> done{0};
+    const size_t smem = sizeof(int) * 3 * ((size_t)a.n_req + 1);
+    if (smem > 40 * 1024) {
+        const cudaError_t e = allow_max_dynamic_smem(kv_resize_kernel, done);
+        if (e != cudaSuccess) return e;
+    }
+    (void)num_sms;
+    kv_resize_kernel<<<1, RS_THREADS, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_append(bool f32, const AppendArgs &a, int num_sms, cudaStream_t st) {
+    (void)num_sms;
+    if (f32) kv_append_kernel<float><<<a.n, 256, 0, st>>>(a);
+    else kv_append_kernel<__nv_bfloat16><<<a.n, 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_rope_table(float *cos_sin, int n_pos, int rot, double theta, const double *inv_freq,
+                              cudaStream_t st) {
+    const long long all = (long long)n_pos * (rot / 2);
+    const int grid = (int)min((all + 255) / 256, (long long)4096);
+    rope_table_kernel<<<grid, 256, 0, st>>>(cos_sin, n_pos, rot / 2, theta, inv_freq);
+    return cudaGetLastError();
+}
+
+}  // namespace scute
