@@ -195,7 +195,8 @@ scute_status scute_paged_attention(scute_ctx *c, const scute_kv_cache *kv, const
     if (t->q_stride < row || t->out_stride < row || t->q_stride % per16 || t->out_stride % per16)
         return fail(c, SCUTE_ERR_SHAPE, "q or out stride is below a row or not a multiple of 16 bytes");
     if (kv->table_cols < 1 || kv->table_stride < kv->table_cols ||
-        (int64_t)kv->table_cols * kv->page_size > 0x7fffffff)
+        (int64_t)kv->table_cols * kv->page_size > (1 << 30) ||
+        (int64_t)kv->table_cols * kv->page_size * t->n_req > (1ll << 35))
         return fail(c, SCUTE_ERR_SHAPE, "block table of %d columns, row pitch %lld", kv->table_cols,
                     (long long)kv->table_stride);
     if (!std::isfinite(t->scale) || !std::isfinite(t->softcap) || t->softcap < 0.f || t->window < 0)
