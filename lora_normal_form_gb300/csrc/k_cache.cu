@@ -277,6 +277,177 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
     }
 }
 
+// 16 bytes of a row as 32-bit values; the stores of a cache's types.
+template <typename T> struct Piece;
+template <> struct Piece<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void open(const uint4 v, float *x) {
+        x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
+        x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+    }
+    static __device__ __forceinline__ void store(float *p, const float *x) {
+        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+};
+template <> struct Piece<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void open(const uint4 v, float *x) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *x) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ void store(__nv_fp8_e4m3 *p, const float *x) {
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const __nv_fp8x4_e4m3 b(make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+            w[i] = b.__x;
+        }
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    }
+};
+
+// 16 bytes at a time.  A head is cut into `items`: pieces j and j + half / VE,
+// which the pairs (i, i + half) join, and behind them single pieces; with
+// interleaved pairs, single pieces only.  A row's threads (per_row of them, a
+// multiple of the items or cut to one) keep their item from head to head, so that
+// its cosines and sines are fetched once; heads are taken three at a time, loads first.
+template <typename T, typename KV>
+__global__ void __launch_bounds__(256) kv_append_vec_kernel(const AppendArgs a, int per_row) {
+    constexpr int VE = Piece<T>::N, U = 3;
+    const int rows = blockDim.x / per_row, sub = threadIdx.x / per_row, t = threadIdx.x - sub * per_row;
+    const int row = blockIdx.x * rows + sub;
+    if (row >= a.n) return;
+    const int dim = a.kv.dim, half = a.rot / 2;
+    const int joined = a.interleaved ? 0 : half / VE;
+    const int items = dim / VE - joined, heads = a.q_heads + 2 * a.kv.heads;
+    const int stride = per_row / items;                 // heads between a thread's turns
+    const int item = t % items;
+    int h = t / items;
+    if (h >= stride) return;
+    const bool two = item < joined;
+    const int d0 = (two ? item : item + joined) * VE, d1 = d0 + half;
+    const bool turned = two || (a.interleaved && d0 < a.rot);
+
+    const int slot = a.slot_map[row];
+    const bool in = slot >= 0 && slot < (long long)a.kv.n_pages * a.kv.page_size;
+    if (slot < -1 || (slot >= 0 && !in)) atomicOr(a.status, STATUS_PAGES);
+    const long long at = in ? (slot / a.kv.page_size) * a.kv.page_stride + (slot % a.kv.page_size) * a.kv.token_stride : 0;
+
+    // the item's cosines and sines: VE pairs (half as many where they are interleaved)
+    float c[VE], s[VE];
+    if (turned) {
+        const int pairs = two ? VE : VE / 2, p0 = two ? d0 : d0 / 2;
+        int last_ax = -1;
+        long long base = 0;
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            if (e >= pairs) break;
+            int ax = 0;
+            while (ax < 3 && p0 + e >= a.bound[ax]) ++ax;
+            if (ax != last_ax) {
+                int p = a.positions[ax * a.axis_stride + row];
+                if (p < 0 || p >= a.n_pos) {
+                    bad = true;
+                    p = p < 0 ? 0 : a.n_pos - 1;
+                }
+                base = (long long)p * a.rot + p0;
+                last_ax = ax;
+            }
+            c[e] = a.cos_sin[base + e];
+            s[e] = a.cos_sin[base + half + e];
+        }
+        if (bad) atomicOr(a.status, STATUS_PAGES);
+    }
+
+    for (; h < heads; h += U * stride) {
+        uint4 x0[U], x1[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int hh = h + u * stride;
+            const int kind = hh < a.q_heads ? 0 : hh < a.q_heads + a.kv.heads ? 1 : 2;     // q, k, v
+            if (hh >= heads || (kind && !in)) continue;
+            const int hk = kind == 0 ? hh : kind == 1 ? hh - a.q_heads : hh - a.q_heads - a.kv.heads;
+            const T *src = reinterpret_cast<const T *>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
+                           (long long)row * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + hk * dim;
+            x0[u] = *reinterpret_cast<const uint4 *>(src + d0);
+            if (two) x1[u] = *reinterpret_cast<const uint4 *>(src + d1);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int hh = h + u * stride;
+            const int kind = hh < a.q_heads ? 0 : hh < a.q_heads + a.kv.heads ? 1 : 2;
+            if (hh >= heads || (kind && !in)) continue;
+            const int hk = kind == 0 ? hh : kind == 1 ? hh - a.q_heads : hh - a.q_heads - a.kv.heads;
+            float y0[VE], y1[VE];
+            Piece<T>::open(x0[u], y0);
+            if (two) Piece<T>::open(x1[u], y1);
+            if (turned && kind < 2) {
+                if (two) {
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        const float w = y0[e] * c[e] - y1[e] * s[e];
+                        y1[e] = y1[e] * c[e] + y0[e] * s[e];
+                        y0[e] = w;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VE / 2; ++e) {
+                        const float w = y0[2 * e] * c[e] - y0[2 * e + 1] * s[e];
+                        y0[2 * e + 1] = y0[2 * e + 1] * c[e] + y0[2 * e] * s[e];
+                        y0[2 * e] = w;
+                    }
+                }
+            }
+            if (kind == 0) {
+                T *dst = reinterpret_cast<T *>(a.q_out) + (long long)row * a.q_out_stride + hk * dim;
+                Piece<T>::store(dst + d0, y0);
+                if (two) Piece<T>::store(dst + d1, y1);
+            } else {
+                const float *scale = kind == 1 ? a.kv.k_scale : a.kv.v_scale;
+                if (scale) {
+                    const float f = scale[hk];
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        y0[e] /= f;
+                        if (two) y1[e] /= f;
+                    }
+                }
+                KV *dst = reinterpret_cast<KV *>(kind == 1 ? a.kv.k : a.kv.v) + at + hk * a.kv.head_stride;
+                Piece<T>::store(dst + d0, y0);
+                if (two) Piece<T>::store(dst + d1, y1);
+            }
+        }
+    }
+}
+
+// Whether a call's rows and rotary halves can be taken 16 bytes at a time.
+template <typename T>
+bool by_pieces(const AppendArgs &a) {
+    constexpr int VE = Piece<T>::N;
+    if (a.interleaved ? a.rot % VE : (a.rot / 2) % VE) return false;
+    uintptr_t p = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
+    long long s = a.k_stride % VE | a.v_stride % VE;
+    if (a.q_heads) {
+        p |= reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.q_out);
+        s |= a.q_stride % VE | a.q_out_stride % VE;
+    }
+    return (p & 15) == 0 && s == 0;
+}
+
 __global__ void __launch_bounds__(256) rope_table_kernel(float *out, int n_pos, int half, double theta,
                                                          const double *inv_freq) {
     const long long step = (long long)gridDim.x * blockDim.x, all = (long long)n_pos * half;
@@ -300,15 +471,26 @@ cudaError_t launch_kv_resize(const ResizeArgs &a, int num_sms, cudaStream_t st) 
         const cudaError_t e = allow_max_dynamic_smem(kv_resize_kernel, done);
         if (e != cudaSuccess) return e;
     }
-    (void)num_sms;
-    kv_resize_kernel<<<1, RS_THREADS, smem, st>>>(a);
+    // every CTA scans the requests for itself and takes its share of the rows
+    const long long rows = a.max_new > a.n_req ? a.max_new : a.n_req;
+    const int grid = (int)min((long long)num_sms, (rows + RS_THREADS - 1) / RS_THREADS + (rows == 0));
+    kv_resize_kernel<<<grid, RS_THREADS, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 cudaError_t launch_kv_append(bool f32, const AppendArgs &a, int num_sms, cudaStream_t st) {
-    (void)num_sms;
-    if (f32) kv_append_kernel<float><<<a.n, 256, 0, st>>>(a);
-    else kv_append_kernel<__nv_bfloat16><<<a.n, 256, 0, st>>>(a);
+    if (f32 ? by_pieces<float>(a) : by_pieces<__nv_bfloat16>(a)) {
+        // few rows: a CTA for each, every head at once; many: 64 threads for a row
+        const int per_row = a.n <= 4 * num_sms ? 256 : 64, rows = 256 / per_row;
+        const int grid = (a.n + rows - 1) / rows;
+        if (f32) kv_append_vec_kernel<float, float><<<grid, 256, 0, st>>>(a, per_row);
+        else if (a.kv.dtype == KV_E4M3) kv_append_vec_kernel<__nv_bfloat16, __nv_fp8_e4m3><<<grid, 256, 0, st>>>(a, per_row);
+        else kv_append_vec_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 256, 0, st>>>(a, per_row);
+    } else if (f32) {
+        kv_append_kernel<float><<<a.n, 256, 0, st>>>(a);
+    } else {
+        kv_append_kernel<__nv_bfloat16><<<a.n, 256, 0, st>>>(a);
+    }
     return cudaGetLastError();
 }
 
