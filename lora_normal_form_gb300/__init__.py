@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -131,6 +132,7 @@ class KvCache:
         tok, head = (1, 2) if token_major else (2, 1)
         self.tensors = (k, v, block_table, k_scale, v_scale)
         self.page_size, self.kv_heads, self.head_dim = k.shape[tok], k.shape[head], k.shape[3]
+        self.kv_row, self.requests = self.kv_heads * self.head_dim, 0
         # a dimension of one element may carry any stride: give it one that passes for its rows
         def stride(dim):
             return k.stride(dim) if k.shape[dim] > 1 else max(k.stride(dim), self.head_dim)
@@ -145,6 +147,7 @@ class KvCache:
             self.struct.block_table = block_table.data_ptr()
             self.struct.table_stride = max(block_table.stride(0), block_table.shape[1])
             self.struct.table_cols = block_table.shape[1]
+            self.requests = block_table.shape[0]
         self.ref = ctypes.byref(self.struct)
 
 
@@ -174,15 +177,17 @@ def _check_table(t):
         raise ValueError("a block table is int32 [n_req, pages] with consecutive rows")
 
 
-def _row_stride(t, cols):
-    """Elements between the rows of a [n, ...] tensor whose rows are ``cols``
-    consecutive elements."""
-    if t.dim() == 3:
-        if t.numel() and (t.stride(2) != 1 or t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-            raise ValueError("the heads of a row must be consecutive")
-    elif t.dim() != 2 or (t.numel() > 1 and t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("expected [n, d] or [n, heads, dim] with consecutive elements")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+def _rows(t, n, cols):
+    """Elements between the rows of ``t``: [n, cols], or [n, heads, dim] with
+    consecutive heads."""
+    shape, st = t.shape, t.stride()
+    if len(shape) == 3:
+        ok = shape[0] == n and shape[1] * shape[2] == cols and st[2] == 1 and (st[1] == shape[2] or shape[1] == 1)
+    else:
+        ok = len(shape) == 2 and shape[0] == n and shape[1] == cols and (st[1] == 1 or cols == 1)
+    if not ok and n:
+        raise ValueError(f"expected {n} rows of {cols} consecutive elements, got shape {tuple(shape)}, strides {st}")
+    return st[0] if n > 1 else max(st[0], cols)
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -272,10 +277,12 @@ def ptr(x) -> Optional[int]:
     """Address of a torch tensor, numpy array, int or None."""
     if x is None:
         return None
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     if hasattr(x, "ctypes"):
         if not x.flags["C_CONTIGUOUS"]:
             raise ValueError("numpy array must be C-contiguous")
@@ -288,9 +295,11 @@ def _stream_handle(stream) -> Optional[int]:
     for None, torch's current stream on the current device (so that calls
     made under ``torch.cuda.stream(s)`` are ordered with that stream's work)."""
     if stream is None:
-        import sys
         torch = sys.modules.get("torch")
         if torch is not None and torch.cuda.is_initialized():
+            c = torch._C
+            if hasattr(c, "_cuda_getCurrentRawStream"):     # the same handle without a Stream object
+                return c._cuda_getCurrentRawStream(c._cuda_getDevice())
             return torch.cuda.current_stream().cuda_stream
         return None
     if isinstance(stream, int):

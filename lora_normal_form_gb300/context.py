@@ -3,7 +3,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (BF16, FP32, METHOD_ID, KvCache, Rope, _check_table, _row_stride, scute_add_layer, scute_create, scute_debug_index, scute_destroy,
+from . import (BF16, FP32, METHOD_ID, KvCache, Rope, _check_table, _rows, scute_add_layer, scute_create, scute_debug_index, scute_destroy,
                scute_kv_append, scute_kv_resize, scute_launch_count, scute_linear, scute_linear_batch, scute_linear_batch_host,
                scute_linear_host, scute_paged_attention, scute_predict_batch, scute_predict_bytes,
                scute_register_adapter, scute_residual_norm, scute_rope_table, scute_set_shared, scute_set_variant, scute_sync_status,
@@ -121,48 +121,42 @@ class Context:
     def kv_append(self, cache: KvCache, slot_map, k, v, q=None, q_out=None, rope: Rope = None, stream=None):
         """Write k and v [n, kv_heads, dim] (or [n, kv_heads * dim]) into the cache;
         keys, and queries into ``q_out``, turned by ``rope``."""
-        n, d = slot_map.shape[0], cache.head_dim
-        row = cache.kv_heads * d
-        if k.shape[0] != n or v.shape[0] != n or (q is not None and q.shape[0] != n) or \
-                (rope is not None and rope.n < n):
-            raise ValueError("slot_map, k, v, q and positions differ in rows")
-        if k.numel() != n * row or v.numel() != n * row:
-            raise ValueError("k and v rows are kv_heads * head_dim elements")
-        q_row = 0 if q is None or n == 0 else q.numel() // n
-        if q is not None and (q_row % d or q_out is None or q_out.shape != q.shape):
-            raise ValueError("q rows are heads * head_dim elements, and q_out has q's shape")
-        scute_kv_append(self.handle, cache, slot_map, n, k, _row_stride(k, row), v, _row_stride(v, row), q,
-                        0 if q is None else _row_stride(q, q_row), q_row // d, q_out,
-                        0 if q is None else _row_stride(q_out, q_row), rope, stream)
+        n, row = slot_map.shape[0], cache.kv_row
+        q_heads = q_stride = q_out_stride = 0
+        if q is not None:
+            q_row = q.numel() // n if n else cache.head_dim
+            q_heads = q_row // cache.head_dim
+            if q_out is None or q_heads * cache.head_dim != q_row:
+                raise ValueError("q rows are heads * head_dim elements, and need q_out")
+            q_stride, q_out_stride = _rows(q, n, q_row), _rows(q_out, n, q_row)
+        if rope is not None and rope.n < n:
+            raise ValueError("fewer positions than rows")
+        scute_kv_append(self.handle, cache, slot_map, n, k, _rows(k, n, row), v, _rows(v, n, row), q, q_stride,
+                        q_heads, q_out, q_out_stride, rope, stream)
 
     def paged_attention(self, cache: KvCache, q, kv_len, out, scale: float = 0.0, softcap: float = 0.0,
                         window: int = 0, lse=None, stream=None):
         """One new token of each request over its cached tokens: q and out
         [n_req, q_heads, dim] (or [n_req, q_heads * dim])."""
-        n = kv_len.shape[0]
-        table = cache.tensors[2]
-        if q.shape[0] != n or out.shape != q.shape or table is None or table.shape[0] < n:
-            raise ValueError("q, out, kv_len and the block table differ in requests")
-        row = 0 if n == 0 else q.numel() // n
-        if row % cache.head_dim or (lse is not None and lse.numel() * cache.head_dim != q.numel()):
-            raise ValueError("q rows are heads * head_dim elements, and lse has one value for each")
-        scute_paged_attention(self.handle, cache, q, _row_stride(q, row), out, _row_stride(out, row), lse, kv_len, n,
-                              max(row // cache.head_dim, cache.kv_heads if n == 0 else 0), scale, softcap, window,
-                              stream)
+        n, dim = kv_len.shape[0], cache.head_dim
+        row = q.numel() // n if n else cache.kv_row
+        if row % dim or cache.requests < n or (lse is not None and lse.numel() * dim != n * row):
+            raise ValueError("q rows are heads * head_dim elements, lse has one value for each head, and the block "
+                             "table a row for each request")
+        scute_paged_attention(self.handle, cache, q, _rows(q, n, row), out, _rows(out, n, row), lse, kv_len, n,
+                              row // dim, scale, softcap, window, stream)
 
     def residual_norm(self, y, out=None, residual=None, residual_out=None, pre_w=None, pre_b=None, post_w=None,
                       post_b=None, gate=None, scale: float = 1.0, eps: float = 1e-5, layer: bool = False, stream=None):
         """h = residual + scale * gate * post(y), out = pre(h), for rows [n, d].
         ``gate``: float32 [d], or the context's dtype [n, d]."""
         n, d = y.shape
-        rows = gate is not None and gate.dim() == 2
-        for t in (out, residual, residual_out, gate if rows else None):
-            if t is not None and t.shape != y.shape:
-                raise ValueError("y, residual, out and a row gate must have one shape")
-        st = lambda t: 0 if t is None else _row_stride(t, d)  # noqa: E731
-        scute_residual_norm(self.handle, n, d, y, st(y), residual, st(residual), residual_out, st(residual_out), out,
-                            st(out), post_w, post_b, pre_w, pre_b, None if rows else gate, gate if rows else None,
-                            st(gate) if rows else 0, scale, eps, layer, stream)
+        gate_vec, gate_rows = (None, gate) if gate is not None and gate.dim() == 2 else (gate, None)
+        scute_residual_norm(self.handle, n, d, y, _rows(y, n, d),
+                            residual, 0 if residual is None else _rows(residual, n, d),
+                            residual_out, 0 if residual_out is None else _rows(residual_out, n, d),
+                            out, 0 if out is None else _rows(out, n, d), post_w, post_b, pre_w, pre_b, gate_vec,
+                            gate_rows, 0 if gate_rows is None else _rows(gate_rows, n, d), scale, eps, layer, stream)
 
     def sync_status(self) -> int:
         return scute_sync_status(self.handle)
