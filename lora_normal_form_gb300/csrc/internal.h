@@ -414,6 +414,7 @@ struct AttendArgs {
     int n_req, q_heads, group;
     float scale, softcap;
     int window;
+    int page_shift;            // log2 of the page size, or -1
     float *part;               // partial sums of rows that several CTAs share
     int *ctr;                  // arrivals at such a row (zero between launches)
     int *status;

@@ -2,6 +2,7 @@
 #include <cuda_fp8.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace scute {
 
@@ -124,33 +125,68 @@ __global__ void __launch_bounds__(128) attend_kernel(const AttendArgs a) {
 // operand of 16 rows and the query heads as the one of 8 columns:
 //     S^T [16 tokens x 8 heads] = K [16 x D] Q^T,
 //     O^T [D x 8 heads] += V^T [D x 16 tokens] P^T,
-// so a group of 4 or 8 query heads wastes little, and both operands come from
-// the cache straight into registers: a product's inner index may be numbered in
-// any way that both operands share, so lane (g, c) = (lane / 4, lane % 4) takes 16
-// consecutive bytes of token g's (and g + 8's) key, the query's fragment the
-// same elements; and 16 consecutive bytes of the values of tokens 2c, 2c + 1,
-// 2c + 8, 2c + 9, of which pairs of tokens are interleaved by byte permutes.
-// Nothing is staged in shared memory, and no warp waits for another inside a row.
+// so a group of 4 or 8 query heads wastes little.  A product's inner index may
+// be numbered in any way that both operands share, so lane (g, c) = (lane / 4,
+// lane % 4) takes 16 consecutive bytes of token g's (and g + 8's) key and the
+// query's fragment the same elements; and 16 consecutive bytes of the values of
+// tokens 2c, 2c + 1, 2c + 8, 2c + 9, of which pairs of tokens are interleaved by
+// byte permutes.
 //
-// The work is one sequence of units (UT tokens of one request and head row),
-// cut into equal contiguous ranges, one per CTA; the warps of a CTA take every
-// fourth tile of a unit run and merge their maxima, sums and outputs in shared
-// memory when the row ends.  A row that several CTAs share is joined by the
-// last of them to arrive, in the order of the CTAs.
-constexpr int AW = 4;              // warps of a CTA
+// The work is one sequence of tiles (TT tokens of one request and head row),
+// with ROW_COST places before each row's first for what a row costs beside its
+// tiles, cut into equal contiguous ranges, one per CTA, whatever rows they
+// fall in.  In a CTA one warp looks the pages up and brings the tokens' key and
+// value rows into a ring of stages by 16-byte asynchronous copies, running ahead
+// over the ends of rows (a page may end anywhere in a tile); the others take the
+// tiles in turn, each with its own maximum, sums and outputs, and merge them in
+// shared memory where a row ends.  Of a row that several CTAs share each leaves
+// its part in the workspace, arrives at the row's counter when its whole range is
+// done, and the last to arrive joins the parts in the order of the CTAs.
+constexpr int CW = 4;                     // warps that compute
+constexpr int PW = 2;                     // warps that fetch
+constexpr int AT_THREADS = 32 * (CW + PW);
+constexpr int QS = 2;                     // rows whose queries may be waiting
+constexpr int MAX_STAGES = 32;
+constexpr int ROW_COST = 5;               // tiles
+constexpr uint64_t WAIT_NS = 2000000000ull;
 
-__device__ __forceinline__ uint4 ldg16(const void *p) {
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    const uint64_t t0 = ptx::globaltimer();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (ptx::mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (ptx::globaltimer() - t0 > WAIT_NS) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    return ptx::mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag);
+}
+__device__ __forceinline__ uint4 lds16(uint32_t p) {
     uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p));
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(p));
     return r;
 }
-__device__ __forceinline__ uint2 ldg8(const void *p) {
+__device__ __forceinline__ uint2 lds8(uint32_t p) {
     uint2 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(p));
     return r;
 }
+// 16 bytes from global to shared memory, or 16 zero bytes.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+                 "r"(real ? 16 : 0)
+                 : "memory");
+}
+// One of the barrier's arrivals, when this thread's copies so far have arrived.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(CW * 32) : "memory"); }
 template <bool F16>
 __device__ __forceinline__ void mma16816(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -188,32 +224,20 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return y;
 }
 
-// The batch's work list: units of UT tokens, rows (request, key/value head, head
-// chunk) in this order; every row has a unit, an empty request's too.
-struct Plan {
-    int hz;                  // rows of a request
-    int upt;                 // tokens of a unit
-    long long total;         // units
-    int ctas;                // CTAs that have any
-};
+// The batch's work list.  Row (request r, key/value head and head chunk) takes
+// ROW_COST places and then one for each of its tiles, an empty request's row one
+// tile all the same; places_at[r] = places of one row of each request before r.
 __device__ __forceinline__ void seen_of(const AttendArgs &a, int r, int *first, int *len, bool *bad) {
     const int cap = a.kv.table_cols * a.kv.page_size;
-    int n = a.kv_len[r];
+    int n = __ldg(a.kv_len + r);
     *bad = n < 0 || n > cap;
     n = n < 0 ? 0 : n > cap ? cap : n;
     *len = n;
     *first = a.window > 0 ? max(0, n - a.window) : 0;
 }
-__device__ __forceinline__ long long range_start(const Plan &p, int cta) { return p.total * cta / p.ctas; }
-// The CTA whose range holds unit x.
-__device__ __forceinline__ int owner_of(const Plan &p, long long x) {
-    return (int)(((x + 1) * p.ctas - 1) / p.total);
-}
-
-// units_at[r] = units of the requests before r (one head row), for r <= n_req.
-__device__ __forceinline__ void plan_units(const AttendArgs &a, int upt, int *units_at, int *warp_sum) {
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, n = a.n_req, threads = AW * 32;
-    const int per = (n + threads - 1) / threads, r0 = min(n, t * per), r1 = min(n, r0 + per);
+__device__ __forceinline__ void plan_places(const AttendArgs &a, int tt, int *places_at, int *warp_sum) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, n = a.n_req;
+    const int per = (n + AT_THREADS - 1) / AT_THREADS, r0 = min(n, t * per), r1 = min(n, r0 + per);
     int mine = 0;
     bool any = false;
     for (int r = r0; r < r1; ++r) {
@@ -221,7 +245,7 @@ __device__ __forceinline__ void plan_units(const AttendArgs &a, int upt, int *un
         bool bad;
         seen_of(a, r, &first, &len, &bad);
         any |= bad;
-        mine += max(1, (len - first + upt - 1) / upt);
+        mine += ROW_COST + max(1, (len - first + tt - 1) / tt);
     }
     if (any && blockIdx.x == 0) atomicOr(a.status, STATUS_PAGES);
     int inc = mine;
@@ -234,17 +258,87 @@ __device__ __forceinline__ void plan_units(const AttendArgs &a, int upt, int *un
     __syncthreads();
     int at = inc - mine;
 #pragma unroll
-    for (int w = 0; w < AW; ++w) at += w < warp ? warp_sum[w] : 0;
+    for (int w = 0; w < CW + PW; ++w) at += w < warp ? warp_sum[w] : 0;
     for (int r = r0; r < r1; ++r) {
         int first, len;
         bool bad;
         seen_of(a, r, &first, &len, &bad);
-        units_at[r] = at;
-        at += max(1, (len - first + upt - 1) / upt);
+        places_at[r] = at;
+        at += ROW_COST + max(1, (len - first + tt - 1) / tt);
     }
-    if (t == threads - 1) units_at[n] = at;
+    if (t == AT_THREADS - 1) places_at[n] = at;
     __syncthreads();
 }
+
+// Walks a CTA's range of places, row by row.
+struct Walk {
+    const AttendArgs &a;
+    const int *places_at;
+    int hz, Z, tt;
+    long long total, end;
+    int ctas;
+    // the row: its first place, request, head and chunk, tiles; tokens [first, len)
+    long long base;
+    int r, hk, z, tiles, first, len;
+    int t0, t1;              // the range's tiles of it
+
+    __device__ __forceinline__ Walk(const AttendArgs &args, const int *at, int heads_chunk, int tile)
+        : a(args), places_at(at), tt(tile) {
+        Z = (a.group + heads_chunk - 1) / heads_chunk;
+        hz = a.kv.heads * Z;
+        total = (long long)at[a.n_req] * hz;
+        // a CTA's warps have a tile each, or the batch has no more
+        ctas = (int)min((long long)gridDim.x, (total + CW - 1) / CW);
+    }
+    __device__ __forceinline__ long long start(int cta) const { return total * cta / ctas; }
+    // The CTA whose range holds place x.
+    __device__ __forceinline__ int owner(long long x) const { return (int)(((x + 1) * ctas - 1) / total); }
+    __device__ __forceinline__ int first_owner() const { return owner(base + ROW_COST); }
+    __device__ __forceinline__ int last_owner() const { return owner(base + ROW_COST + tiles - 1); }
+    __device__ __forceinline__ void request() {
+        bool bad;
+        seen_of(a, r, &first, &len, &bad);
+        tiles = places_at[r + 1] - places_at[r] - ROW_COST;
+    }
+    __device__ __forceinline__ void cut(long long from) {
+        t0 = (int)max(0ll, from - base - ROW_COST);
+        t1 = (int)min((long long)tiles, end - base - ROW_COST);
+    }
+    // At the first row of CTA cta's range that has tiles in it.
+    __device__ __forceinline__ void open(int cta) {
+        const long long x = start(cta);
+        end = start(cta + 1);
+        r = 0;
+        for (int hi = a.n_req - 1; r < hi;) {
+            const int mid = (r + hi + 1) >> 1;
+            if ((long long)places_at[mid] * hz <= x) r = mid;
+            else hi = mid - 1;
+        }
+        request();
+        const long long in = x - (long long)places_at[r] * hz;
+        const int row = (int)(in / (tiles + ROW_COST));
+        base = (long long)places_at[r] * hz + (long long)row * (tiles + ROW_COST);
+        hk = row / Z;
+        z = row - hk * Z;
+        cut(x);
+    }
+    // Whether there is a row left; next() goes on to the next one.
+    __device__ __forceinline__ bool more() const { return base + ROW_COST < end; }
+    __device__ __forceinline__ void next() {
+        base += tiles + ROW_COST;
+        if (++z == Z) {
+            z = 0;
+            if (++hk == a.kv.heads) {
+                hk = 0;
+                if (++r < a.n_req) request();
+            }
+        }
+        cut(base);
+    }
+    __device__ __forceinline__ int from() const { return first + t0 * tt; }
+    __device__ __forceinline__ int to() const { return (int)min((long long)len, first + (long long)t1 * tt); }
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+};
 
 // A CTA's share of a row: unnormalised output of every head and dimension, its
 // maximum (in powers of two) and its sum.
@@ -257,198 +351,303 @@ __device__ __forceinline__ PartView part_of(const AttendArgs &a, int slot) {
     return {p, p + ATT_HEADS, p + 2 * ATT_HEADS};
 }
 
-template <bool FP8, int DC, int NT, int MINB>
-__global__ void __launch_bounds__(AW * 32, MINB) attend_mma_kernel(const AttendArgs a) {
-    // 16-token tiles of one pass: 4 KB of keys where two tiles (a lane finds one
-    // token's place) can make that
-    constexpr int MT = DC * (FP8 ? 1 : 2) <= 128 ? 2 : 1;
-    constexpr int TT = 16 * MT, UT = AW * TT;
+// Four elements of the output of one head, times f.
+__device__ __forceinline__ void put(const AttendArgs &a, int r, int h, int d, float4 x, float f) {
+    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) + r * a.out_stride + (long long)h * a.kv.dim + d;
+    uint2 y;
+    y.x = pack_bf16(x.x * f, x.y * f);
+    y.y = pack_bf16(x.z * f, x.w * f);
+    *reinterpret_cast<uint2 *>(out) = y;
+}
+
+// Sizes of one instance.  A stage holds a tile's key rows, then its value rows.
+// The 16-byte pieces of a row are permuted within 128 bytes so that the lanes of
+// a quarter warp read different banks, of the keys (rows 2i and 2i + 1, four
+// neighbouring pieces of each) as of the values (rows 0, 2, 4, 6, two pieces of each).
+template <bool FP8, int DC, int NT>
+struct Shape {
+    static constexpr int ESZ = FP8 ? 1 : 2, ROW = DC * ESZ;
+    static constexpr int MT = ROW <= 128 ? 2 : 1;         // 16-token steps of a tile
+    static constexpr int TT = 16 * MT, HC = 8 * NT;
+    static constexpr int STAGE = 2 * TT * ROW;
+    // the permutation, as bits of a byte address, of row i
+    static __device__ __forceinline__ uint32_t swizzle(int i) {
+        return ROW == 64 ? (i >> 1 & 3) << 5 : ((i & 1) << 6) ^ ((i >> 1 & 3) << 5);
+    }
+    static __device__ __forceinline__ uint32_t place(int i, int piece) {
+        return (i * ROW + piece * 16) ^ swizzle(i);
+    }
+    static constexpr int O_LD = DC + 4;                   // floats between heads
+    static constexpr int O_BYTES = CW * HC * O_LD * 4, Q_BYTES = HC * DC * 2;
+    static constexpr int FIXED = O_BYTES + QS * Q_BYTES + CW * HC * 8 + HC * 8 + (2 * MAX_STAGES + 2 * QS) * 8 +
+                                 MAX_STAGES * 4 + 64;
+    static_assert(STAGE % 16 == 0 && O_BYTES % 16 == 0 && Q_BYTES % 16 == 0, "alignment");
+    static size_t smem(int stages, int n_req) { return FIXED + (size_t)stages * STAGE + 4 * ((size_t)n_req + 1); }
+};
+
+template <bool FP8, int DC, int NT>
+__global__ void __launch_bounds__(AT_THREADS, 2) attend_mma_kernel(const AttendArgs a, int stages) {
+    using S = Shape<FP8, DC, NT>;
+    constexpr int MT = S::MT, TT = S::TT, HC = S::HC, ESZ = S::ESZ;
     constexpr int KE = FP8 ? 16 : 8;                 // elements of 16 bytes
     constexpr int KP = DC / (4 * KE);                // key pieces of a lane, each four lanes wide
     constexpr int VE = FP8 && DC > 64 ? 16 : 8;      // elements of a value piece, eight lanes wide
     constexpr int VP = DC / (8 * VE);
-    constexpr int VW = FP8 ? VE / 4 : VE / 2;        // its words
+    constexpr int VW = VE * ESZ / 4;                 // its words
     constexpr int OT = VE / 2;                       // 16-row output tiles of a value piece
-    constexpr int HC = 8 * NT, ESZ = FP8 ? 1 : 2;
-    constexpr int SO_LD = DC + 4;                    // floats between heads in shared memory
 
-    extern __shared__ int units_at[];
-    __shared__ int s_warp[AW];
-    __shared__ int s_last;
-    __shared__ float s_m[AW][HC], s_l[AW][HC], s_top[HC], s_sum[HC];
-    __shared__ __align__(16) float s_o[HC][SO_LD];
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t *const s_ring = smem;
+    float *const s_o = reinterpret_cast<float *>(smem + (size_t)stages * S::STAGE);   // [CW][HC][O_LD]
+    uint8_t *const s_q = reinterpret_cast<uint8_t *>(s_o) + S::O_BYTES;               // [QS][HC][D]
+    float *const s_m = reinterpret_cast<float *>(s_q + QS * S::Q_BYTES);              // [CW][HC]
+    float *const s_l = s_m + CW * HC;                                                 // [CW][HC]
+    float *const s_top = s_l + CW * HC, *const s_sum = s_top + HC;                    // [HC]
+    uint64_t *const s_bar = reinterpret_cast<uint64_t *>(s_sum + HC);
+    unsigned *const s_ok = reinterpret_cast<unsigned *>(s_bar + 2 * MAX_STAGES + 2 * QS);   // [stage] tokens that count
+    int *const s_misc = reinterpret_cast<int *>(s_ok + MAX_STAGES);
+    volatile int *const s_abort = s_misc, *const s_last = s_misc + 1;      // [2]
+    int *const s_warp = s_misc + 3;
+    int *const places_at = s_misc + 16;
+    auto full = [&](int i) { return ptx::smem_u32(s_bar + i); };
+    auto empty = [&](int i) { return ptx::smem_u32(s_bar + MAX_STAGES + i); };
+    auto q_full = [&](int i) { return ptx::smem_u32(s_bar + 2 * MAX_STAGES + i); };
+    auto q_empty = [&](int i) { return ptx::smem_u32(s_bar + 2 * MAX_STAGES + QS + i); };
 
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, g = lane >> 2, c = lane & 3;
-    const int D = a.kv.dim, Z = (a.group + HC - 1) / HC;
-    plan_units(a, UT, units_at, s_warp);
-    Plan plan;
-    plan.hz = a.kv.heads * Z;
-    plan.upt = UT;
-    plan.total = (long long)units_at[a.n_req] * plan.hz;
-    plan.ctas = (int)min((long long)gridDim.x, plan.total);
-    const int cta = blockIdx.x;
-    if (cta >= plan.ctas) return;
-    long long at = range_start(plan, cta);
-    const long long end = range_start(plan, cta + 1);
-
-    // the request of the first unit
-    int r = 0;
-    {
-        int hi = a.n_req - 1;
-        while (r < hi) {
-            const int mid = (r + hi + 1) >> 1;
-            if ((long long)units_at[mid] * plan.hz <= at) r = mid;
-            else hi = mid - 1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int D = a.kv.dim, row_bytes = D * ESZ;
+    if (threadIdx.x == 0) {
+        *s_abort = 0;
+        for (int i = 0; i < stages; ++i) {
+            ptx::mbar_init(full(i), 33);      // the copies of 32 lanes, and the count of tokens
+            ptx::mbar_init(empty(i), 1);
         }
+        for (int i = 0; i < QS; ++i) {
+            ptx::mbar_init(q_full(i), 32);
+            ptx::mbar_init(q_empty(i), CW);
+        }
+        ptx::fence_mbar_init();
     }
-    while (at < end) {
-        while ((long long)units_at[r + 1] * plan.hz <= at) ++r;
-        const int ur = units_at[r + 1] - units_at[r];
-        const long long in_req = at - (long long)units_at[r] * plan.hz;
-        const int row = (int)(in_req / ur), u0 = (int)(in_req - (long long)row * ur);
-        const int u1 = (int)min((long long)ur, u0 + (end - at));
-        const int hk = row / Z, z = row - hk * Z;
-        const int h0 = hk * a.group + z * HC, nh = min(HC, a.group - z * HC);
-        int first, len;
-        bool bad;
-        seen_of(a, r, &first, &len, &bad);
+    plan_places(a, TT, places_at, s_warp);
+    Walk w(a, places_at, HC, TT);
+    const int cta = blockIdx.x;
+    if (cta >= w.ctas) return;
+    w.open(cta);
 
-        // queries: the fragments' elements are those of the keys' pieces
-        uint32_t qf[NT][KP][KE / 2];
-        float mul[NT][2];         // score to power-of-two exponent (without a cap), per head of this lane's columns
-        const float ks = a.kv.k_scale ? a.kv.k_scale[hk] : 1.f;
+    if (warp < PW) {
+        // ------------------------------------------------ the warp that fetches
+        // Spans of up to 128 tokens; the pages of the next span are looked up
+        // before this one's rows are sent for.
+        constexpr int SPAN = 128;
+        const long long tok_bytes = a.kv.token_stride * ESZ;
+        int hk = w.hk, z = w.z, r = w.r, stop = w.to(), pos = w.from();
+        bool opens = true, more = w.more();
+        auto look_up = [&](int of, int from, int until, int *page) {
+            const int32_t *table = a.kv.table + of * a.kv.table_stride;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int h = nt * 8 + g;
-            const __nv_bfloat16 *q =
-                reinterpret_cast<const __nv_bfloat16 *>(a.q) + r * a.q_stride + (long long)(h0 + h) * D;
-#pragma unroll
-            for (int p = 0; p < KP; ++p)
-#pragma unroll
-                for (int e = 0; e < KE / 8; ++e) {
-                    const int d = (p * 4 + c) * KE + e * 8;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (h < nh && d < D) x = *reinterpret_cast<const uint4 *>(q + d);
-                    qf[nt][p][e * 4 + 0] = x.x;
-                    qf[nt][p][e * 4 + 1] = x.y;
-                    qf[nt][p][e * 4 + 2] = x.z;
-                    qf[nt][p][e * 4 + 3] = x.w;
-                }
-            float back = 1.f;
-            if constexpr (FP8) {
-                // 16-bit halves have 11 bits where bf16 has 8: scaled by a power of
-                // two that takes the head's largest element to 2^8 or below, every
-                // element down to 2^-22 of it stays exact
-                float big = 0.f;
-#pragma unroll
-                for (int p = 0; p < KP; ++p)
-#pragma unroll
-                    for (int e = 0; e < KE / 2; ++e) {
-                        const uint32_t w = qf[nt][p][e];
-                        big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))));
-                    }
-                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                int ex = 0;
-                if (big > 0.f && big < INFINITY) frexpf(big, &ex);
-                ex = max(-100, min(100, ex - 8));
-                const float down = ldexpf(1.f, -ex);
-                back = ldexpf(1.f, ex);
-#pragma unroll
-                for (int p = 0; p < KP; ++p)
-#pragma unroll
-                    for (int e = 0; e < KE / 2; ++e) {
-                        const uint32_t w = qf[nt][p][e];
-                        qf[nt][p][e] = pack_f16(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down);
-                    }
+            for (int k = 0; k < SPAN / 32; ++k) {
+                const int i = from + k * 32 + lane;
+                page[k] = i < until ? __ldg(table + (a.page_shift >= 0 ? i >> a.page_shift : i / a.kv.page_size)) : -1;
             }
-            mul[nt][0] = __shfl_sync(0xffffffffu, back, (2 * c) * 4) * ks * a.scale;
-            mul[nt][1] = __shfl_sync(0xffffffffu, back, (2 * c + 1) * 4) * ks * a.scale;
+        };
+        int page[SPAN / 32];
+        if (more) look_up(r, pos, stop, page);
+        bool bad = false;
+        int st = 0, turn = 0, qst = 0;          // the next stage, whose it is to fill, the next slot of queries
+        unsigned ph = 1, qph = 1;
+        while (more && !*s_abort) {
+            const bool last = pos + SPAN >= stop;
+            if (last) w.next();
+            const int next_pos = last ? w.from() : pos + SPAN, next_stop = last ? w.to() : stop;
+            int next_page[SPAN / 32];
+            if (last) more = w.more();
+            if (more) look_up(w.r, next_pos, next_stop, next_page);
+            if (opens && pos < stop) {
+                if (warp == 0) {
+                    if (!wait_bar(q_empty(qst), qph, s_abort)) break;
+                    const int h0 = hk * a.group + z * HC, nh = min(HC, a.group - z * HC);
+                    const __nv_bfloat16 *q = reinterpret_cast<const __nv_bfloat16 *>(a.q) + r * a.q_stride + (long long)h0 * D;
+                    for (int i = lane; i < nh * D / 8; i += 32)
+                        copy16(ptx::smem_u32(s_q + qst * S::Q_BYTES) + i * 16, q + i * 8, true);
+                    copies_arrive(q_full(qst));
+                }
+                if (++qst == QS) qst = 0, qph ^= 1;
+            }
+            const char *kb = reinterpret_cast<const char *>(a.kv.k) + hk * a.kv.head_stride * ESZ;
+            const char *vb = reinterpret_cast<const char *>(a.kv.v) + hk * a.kv.head_stride * ESZ;
+            bool gone = false;
+#pragma unroll
+            for (int k = 0; k < SPAN / 32; ++k) {
+                if (pos + k * 32 >= stop || gone) break;
+                const int i = pos + k * 32 + lane;
+                long long place = -1;
+                if (i < stop) {
+                    if (page[k] < 0 || page[k] >= a.kv.n_pages) {
+                        bad = true;
+                    } else {
+                        const int in = a.page_shift >= 0 ? i & (a.kv.page_size - 1) : i % a.kv.page_size;
+                        place = ((long long)page[k] * a.kv.page_stride + (long long)in * a.kv.token_stride) * ESZ;
+                    }
+                }
+                const unsigned all = __ballot_sync(0xffffffffu, place >= 0);
+#pragma unroll
+                for (int m = 0; m < 32 / TT; ++m) {
+                    if (pos + k * 32 + m * TT >= stop) break;
+                    if (turn == warp) {
+                        if (!wait_bar(empty(st), ph, s_abort)) {
+                            gone = true;
+                            break;
+                        }
+                        const unsigned ok = TT == 32 ? all : all >> (m * 16) & 0xffffu;
+                        const uint32_t kd = ptx::smem_u32(s_ring + (size_t)st * S::STAGE), vd = kd + TT * S::ROW;
+                        constexpr int LR = S::ROW / 16, RI = 32 / LR;      // lanes of a row, rows of an instruction
+                        const int piece = lane % LR, row0 = lane / LR;
+                        const bool in_row = piece * 16 < row_bytes;
+                        // a tile inside one page steps by the token's stride
+                        const long long place0 = __shfl_sync(0xffffffffu, place, m * TT);
+                        const bool one_page = __all_sync(
+                            0xffffffffu, lane / TT != m || i >= stop || place == place0 + (lane - m * TT) * tok_bytes);
+                        if (one_page) {
+                            const int rows = place0 >= 0 ? min(TT, stop - (pos + k * 32 + m * TT)) : 0;
+                            const long long from = place0 >= 0 ? place0 + row0 * tok_bytes + piece * 16 : 0;
+                            const char *ks = kb + from, *vs = vb + from;
+#pragma unroll
+                            for (int n = 0; n < TT / RI; ++n) {
+                                const int row = n * RI + row0;
+                                const bool real = in_row && row < rows;
+                                const uint32_t to = S::place(row, piece);
+                                copy16(kd + to, real ? ks : kb, real);
+                                copy16(vd + to, real ? vs : vb, real);
+                                ks += RI * tok_bytes;
+                                vs += RI * tok_bytes;
+                            }
+                        } else {
+#pragma unroll
+                            for (int n = 0; n < TT / RI; ++n) {
+                                const int row = n * RI + row0;
+                                const long long p = __shfl_sync(0xffffffffu, place, m * TT + row);
+                                const bool real = in_row && p >= 0;
+                                const uint32_t to = S::place(row, piece);
+                                copy16(kd + to, real ? kb + p + piece * 16 : kb, real);
+                                copy16(vd + to, real ? vb + p + piece * 16 : vb, real);
+                            }
+                        }
+                        copies_arrive(full(st));
+                        if (lane == 0) {
+                            s_ok[st] = ok;
+                            ptx::mbar_arrive(full(st));
+                        }
+                    }
+                    if (++turn == PW) turn = 0;
+                    if (++st == stages) st = 0, ph ^= 1;
+                }
+            }
+            if (gone) break;
+            opens = last;
+            r = w.r, hk = w.hk, z = w.z;
+            pos = next_pos;
+            stop = next_stop;
+#pragma unroll
+            for (int k = 0; k < SPAN / 32; ++k) page[k] = next_page[k];
         }
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, STATUS_PAGES);
+        // nothing of this warp's may be on its way when the CTA ends
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (*s_abort && lane == 0) atomicOr(a.status, STATUS_TIMEOUT);
+        return;
+    }
+
+    // ---------------------------------------------------- the warps that compute
+    const int cw = warp - PW, t = threadIdx.x - 32 * PW, g = lane >> 2, c = lane & 3;
+    int st = cw, qst = 0;                   // this warp's next stage, the next row's queries
+    unsigned ph = 0, qph = 0, seq = 0;      // tiles of the CTA so far
+    // what the end joins: the rows that began before this range, and go on behind it
+    struct Shared {
+        int r, hk, h0, nh, c0, c1;
+    } head = {-1}, tail = {-1};
+    for (; w.more(); w.next()) {
+        const int h0 = w.hk * a.group + w.z * HC, nh = min(HC, a.group - w.z * HC);
+        const int tiles = w.to() > w.from() ? (w.to() - w.from() + TT - 1) / TT : 0;
 
         float o[NT][VP][OT][4] = {};
         float top[NT][2], sum[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY, sum[nt][0] = sum[nt][1] = 0.f;
 
-        const char *kb = reinterpret_cast<const char *>(a.kv.k) + hk * a.kv.head_stride * ESZ;
-        const char *vb = reinterpret_cast<const char *>(a.kv.v) + hk * a.kv.head_stride * ESZ;
-        const int stop = min(len, first + u1 * UT);
-        const int32_t *table = a.kv.table + r * a.kv.table_stride;
-
-        // lane i finds token i of a pass: its page, one pass ahead of its place
-        auto page_at = [&](int tok) -> int {
-            const int i = tok + (lane & (TT - 1));
-            return i < stop ? table[i / a.kv.page_size] : -1;
-        };
-        auto place_of = [&](int tok, int page) -> long long {
-            const int i = tok + (lane & (TT - 1));
-            if (i >= stop) return -1;
-            if (page < 0 || page >= a.kv.n_pages) {
-                atomicOr(a.status, STATUS_PAGES);
-                return -1;
-            }
-            return ((long long)page * a.kv.page_stride + (long long)(i % a.kv.page_size) * a.kv.token_stride) * ESZ;
-        };
-        uint4 kr[MT][2][KP];
-        uint32_t vr[MT][4][VP][VW];
-        auto load_k = [&](long long place) {
+        if (tiles) {
+            // queries: the fragments' elements are those of the keys' pieces
+            uint32_t qf[NT][KP][KE / 2];
+            float mul[NT][2];         // product to score, per head of this lane's columns
+            const float ks = a.kv.k_scale ? a.kv.k_scale[w.hk] : 1.f;
+            wait_bar(q_full(qst), qph, s_abort);
+            const uint32_t qs = ptx::smem_u32(s_q + qst * S::Q_BYTES);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int nt = 0; nt < NT; ++nt) {
+                const int h = nt * 8 + g;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const long long p = __shfl_sync(0xffffffffu, place, m * 16 + i * 8 + g);
+                for (int p = 0; p < KP; ++p)
 #pragma unroll
-                    for (int j = 0; j < KP; ++j) {
-                        const int d = (j * 4 + c) * KE;
-                        kr[m][i][j] = make_uint4(0, 0, 0, 0);
-                        if (p >= 0 && (DC == 16 * KP || d < D)) kr[m][i][j] = ldg16(kb + p + d * ESZ);
+                    for (int e = 0; e < KE / 8; ++e) {
+                        const int d = (p * 4 + c) * KE + e * 8;
+                        uint4 x = make_uint4(0, 0, 0, 0);
+                        if (h < nh && d < D) x = lds16(qs + (h * D + d) * 2);
+                        qf[nt][p][e * 4 + 0] = x.x;
+                        qf[nt][p][e * 4 + 1] = x.y;
+                        qf[nt][p][e * 4 + 2] = x.z;
+                        qf[nt][p][e * 4 + 3] = x.w;
                     }
-                }
-        };
-        auto load_v = [&](long long place) {
+                float back = 1.f;
+                if constexpr (FP8) {
+                    // 16-bit halves have 11 bits where bf16 has 8: scaled by a power of
+                    // two that takes the head's largest element below 2^8, every element
+                    // down to 2^-22 of it stays exact
+                    float big = 0.f;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+                    for (int p = 0; p < KP; ++p)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const long long p = __shfl_sync(0xffffffffu, place, m * 16 + 2 * c + (i & 1) + (i >> 1) * 8);
-#pragma unroll
-                    for (int j = 0; j < VP; ++j) {
-                        const int d = (j * 8 + g) * VE;
-                        const bool in = p >= 0 && d < D;
-                        if constexpr (VW == 4) {
-                            uint4 x = make_uint4(0, 0, 0, 0);
-                            if (in) x = ldg16(vb + p + d * ESZ);
-                            vr[m][i][j][0] = x.x, vr[m][i][j][1] = x.y, vr[m][i][j][2] = x.z, vr[m][i][j][3] = x.w;
-                        } else {
-                            uint2 x = make_uint2(0, 0);
-                            if (in) x = ldg8(vb + p + d * ESZ);
-                            vr[m][i][j][0] = x.x, vr[m][i][j][1] = x.y;
+                        for (int e = 0; e < KE / 2; ++e) {
+                            const uint32_t w = qf[nt][p][e];
+                            big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))));
                         }
-                    }
+                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                    int ex = 0;
+                    if (big > 0.f && big < INFINITY) frexpf(big, &ex);
+                    ex = max(-100, min(100, ex - 8));
+                    const float down = ldexpf(1.f, -ex);
+                    back = ldexpf(1.f, ex);
+#pragma unroll
+                    for (int p = 0; p < KP; ++p)
+#pragma unroll
+                        for (int e = 0; e < KE / 2; ++e) {
+                            const uint32_t w = qf[nt][p][e];
+                            qf[nt][p][e] = pack_f16(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down);
+                        }
                 }
-        };
+                mul[nt][0] = __shfl_sync(0xffffffffu, back, (2 * c) * 4) * ks * a.scale;
+                mul[nt][1] = __shfl_sync(0xffffffffu, back, (2 * c + 1) * 4) * ks * a.scale;
+                if (!(a.softcap > 0.f)) mul[nt][0] *= LOG2E, mul[nt][1] *= LOG2E;
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(q_empty(qst));
+            if (++qst == QS) qst = 0, qph ^= 1;
 
-        int tok = first + u0 * UT + warp * TT;
-        if (tok < stop) {
-            long long place = place_of(tok, page_at(tok));
-            int page_next = page_at(tok + UT);
-            load_k(place);
-            load_v(place);
-            for (;;) {
-                const unsigned ok = __ballot_sync(0xffffffffu, place >= 0);
-                const int next = tok + UT;
-                const bool more = next < stop;
-                const long long place_next = more ? place_of(next, page_next) : -1;
-                if (more) page_next = page_at(next + UT);
+            // tile n of the CTA is warp n mod CW's, and the ring a multiple of CW
+            // long: a stage has one reader for good, which has seen every earlier
+            // filling of it, so that the parity it waits for is never ambiguous
+            for (unsigned n = seq + ((unsigned)(cw - (int)(seq % CW) + CW) % CW); n < seq + tiles; n += CW) {
+                wait_bar(full(st), ph, s_abort);
+                const unsigned ok = *(volatile unsigned *)(s_ok + st);
+                const uint32_t kd = ptx::smem_u32(s_ring + (size_t)st * S::STAGE), vd = kd + TT * S::ROW;
 
-                float s[MT][NT][4] = {};
+                float sc[MT][NT][4] = {};
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int j = 0; j < KP; ++j) {
-                        const uint32_t w0[4] = {kr[m][0][j].x, kr[m][0][j].y, kr[m][0][j].z, kr[m][0][j].w};
-                        const uint32_t w1[4] = {kr[m][1][j].x, kr[m][1][j].y, kr[m][1][j].z, kr[m][1][j].w};
+                        const uint4 x = lds16(kd + S::place(m * 16 + g, j * 4 + c));
+                        const uint4 y = lds16(kd + S::place(m * 16 + g + 8, j * 4 + c));
+                        const uint32_t w0[4] = {x.x, x.y, x.z, x.w}, w1[4] = {y.x, y.y, y.z, y.w};
                         if constexpr (FP8) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
@@ -456,106 +655,126 @@ __global__ void __launch_bounds__(AW * 32, MINB) attend_mma_kernel(const AttendA
                                 const uint32_t a1 = e4m3x2_f16x2(w1[e]), a3 = e4m3x2_f16x2(w1[e] >> 16);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
-                                    mma16816<true>(s[m][nt], a0, a1, a2, a3, qf[nt][j][2 * e], qf[nt][j][2 * e + 1]);
+                                    mma16816<true>(sc[m][nt], a0, a1, a2, a3, qf[nt][j][2 * e], qf[nt][j][2 * e + 1]);
                             }
                         } else {
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
-                                    mma16816<false>(s[m][nt], w0[2 * e], w1[2 * e], w0[2 * e + 1], w1[2 * e + 1],
+                                    mma16816<false>(sc[m][nt], w0[2 * e], w1[2 * e], w0[2 * e + 1], w1[2 * e + 1],
                                                     qf[nt][j][2 * e], qf[nt][j][2 * e + 1]);
                         }
                     }
-                if (more) load_k(place_next);
+                uint32_t vr[MT][4][VP][VW];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int tok = m * 16 + 2 * c + (k & 1) + (k >> 1) * 8;
+#pragma unroll
+                        for (int j = 0; j < VP; ++j) {
+                            if constexpr (VW == 4) {
+                                const uint4 x = lds16(vd + S::place(tok, j * 8 + g));
+                                vr[m][k][j][0] = x.x, vr[m][k][j][1] = x.y, vr[m][k][j][2] = x.z, vr[m][k][j][3] = x.w;
+                            } else {
+                                const uint2 x = lds8(vd + S::place(tok, g >> 1) + (g & 1) * 8);
+                                vr[m][k][j][0] = x.x, vr[m][k][j][1] = x.y;
+                            }
+                        }
+                    }
 
-                // running maximum and sum, in powers of two
-                uint32_t pf[MT][NT][2][2];            // [tokens 0-7, 8-15][weights, what their rounding left]
+                // scores in powers of two; the reference of the weights moves only
+                // when a score passes it by more than 2^8, so that the outputs are
+                // seldom scaled (weights are then at most 2^8, exact in any type here)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float x = s[m][nt][i] * mul[nt][i & 1];
-                            if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
-                            x *= LOG2E;
-                            if (!(ok >> (m * 16 + (i >> 1) * 8 + g) & 1)) x = -INFINITY;
-                            s[m][nt][i] = x;
-                            mx[i & 1] = fmaxf(mx[i & 1], x);
+                        for (int k = 0; k < 4; ++k) {
+                            float x = sc[m][nt][k] * mul[nt][k & 1];
+                            if (a.softcap > 0.f) x = a.softcap * LOG2E * tanhf(x / a.softcap);
+                            if (!(ok >> (m * 16 + (k >> 1) * 8 + g) & 1)) x = -INFINITY;
+                            sc[m][nt][k] = x;
+                            mx[k & 1] = fmaxf(mx[k & 1], x);
                         }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float x = mx[i];
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                        mx[i] = fmaxf(x, top[nt][i]);
-                    }
-                    if (__any_sync(0xffffffffu, mx[0] != top[nt][0] || mx[1] != top[nt][1])) {
+                    if (__any_sync(0xffffffffu, mx[0] > top[nt][0] + 8.f || mx[1] > top[nt][1] + 8.f)) {
                         float al[2];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            al[i] = mx[i] == top[nt][i] ? 1.f : exp2f(top[nt][i] - mx[i]);
-                            top[nt][i] = mx[i];
-                            sum[nt][i] *= al[i];
+                        for (int k = 0; k < 2; ++k) {
+                            float x = mx[k];
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                            x = fmaxf(x, top[nt][k]);
+                            al[k] = x == top[nt][k] ? 1.f : exp2f(top[nt][k] - x);
+                            top[nt][k] = x;
+                            sum[nt][k] *= al[k];
                         }
 #pragma unroll
                         for (int j = 0; j < VP; ++j)
 #pragma unroll
-                            for (int i = 0; i < OT; ++i) {
-                                o[nt][j][i][0] *= al[0];
-                                o[nt][j][i][1] *= al[1];
-                                o[nt][j][i][2] *= al[0];
-                                o[nt][j][i][3] *= al[1];
+                            for (int k = 0; k < OT; ++k) {
+                                o[nt][j][k][0] *= al[0];
+                                o[nt][j][k][1] *= al[1];
+                                o[nt][j][k][2] *= al[0];
+                                o[nt][j][k][3] *= al[1];
                             }
                     }
+                }
+                uint32_t pf[MT][NT][2][2];            // [tokens 0-7, 8-15][weights, what their rounding left]
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
                     const float ref[2] = {top[nt][0] == -INFINITY ? 0.f : top[nt][0],
                                           top[nt][1] == -INFINITY ? 0.f : top[nt][1]};
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
                         float p[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            p[i] = exp2f(s[m][nt][i] - ref[i & 1]);
-                            sum[nt][i & 1] += p[i];
+                        for (int k = 0; k < 4; ++k) {
+                            p[k] = exp2f(sc[m][nt][k] - ref[k & 1]);
+                            sum[nt][k & 1] += p[k];
                         }
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                        for (int k = 0; k < 2; ++k) {
                             if constexpr (FP8) {
-                                pf[m][nt][i][0] = transpose8(pack_f16(p[2 * i], p[2 * i + 1]));
+                                pf[m][nt][k][0] = transpose8(pack_f16(p[2 * k], p[2 * k + 1]));
                             } else {
                                 // bf16 keeps 8 bits of a weight: a second product takes the rest
-                                const uint32_t hi = pack_bf16(p[2 * i], p[2 * i + 1]);
-                                const float r0 = p[2 * i] - __uint_as_float(hi << 16);
-                                const float r1 = p[2 * i + 1] - __uint_as_float(hi & 0xffff0000u);
-                                pf[m][nt][i][0] = transpose8(hi);
-                                pf[m][nt][i][1] = transpose8(pack_bf16(r0, r1));
+                                const uint32_t hi = pack_bf16(p[2 * k], p[2 * k + 1]);
+                                const float r0 = p[2 * k] - __uint_as_float(hi << 16);
+                                const float r1 = p[2 * k + 1] - __uint_as_float(hi & 0xffff0000u);
+                                pf[m][nt][k][0] = transpose8(hi);
+                                pf[m][nt][k][1] = transpose8(pack_bf16(r0, r1));
                             }
                         }
                     }
                 }
-
+                // the stage's values are in registers: it may be filled again
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(empty(st));
+                if ((st += CW) >= stages) st = cw, ph ^= 1;
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
                     for (int j = 0; j < VP; ++j)
 #pragma unroll
-                        for (int w = 0; w < VW; ++w) {
-                            const uint32_t x0 = vr[m][0][j][w], x1 = vr[m][1][j][w];
-                            const uint32_t x2 = vr[m][2][j][w], x3 = vr[m][3][j][w];
+                        for (int i = 0; i < VW; ++i) {
+                            const uint32_t x0 = vr[m][0][j][i], x1 = vr[m][1][j][i];
+                            const uint32_t x2 = vr[m][2][j][i], x3 = vr[m][3][j][i];
                             if constexpr (FP8) {
                                 const uint32_t y0 = __byte_perm(x0, x1, 0x5140), y1 = __byte_perm(x0, x1, 0x7362);
                                 const uint32_t y2 = __byte_perm(x2, x3, 0x5140), y3 = __byte_perm(x2, x3, 0x7362);
 #pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const uint32_t ya = i ? y1 : y0, yb = i ? y3 : y2;
+                                for (int k = 0; k < 2; ++k) {
+                                    const uint32_t ya = k ? y1 : y0, yb = k ? y3 : y2;
                                     const uint32_t a0 = e4m3x2_f16x2(ya), a1 = e4m3x2_f16x2(ya >> 16);
                                     const uint32_t a2 = e4m3x2_f16x2(yb), a3 = e4m3x2_f16x2(yb >> 16);
 #pragma unroll
                                     for (int nt = 0; nt < NT; ++nt)
-                                        mma16816<true>(o[nt][j][2 * w + i], a0, a1, a2, a3, pf[m][nt][0][0],
+                                        mma16816<true>(o[nt][j][2 * i + k], a0, a1, a2, a3, pf[m][nt][0][0],
                                                        pf[m][nt][1][0]);
                                 }
                             } else {
@@ -563,16 +782,13 @@ __global__ void __launch_bounds__(AW * 32, MINB) attend_mma_kernel(const AttendA
                                 const uint32_t a2 = __byte_perm(x2, x3, 0x5410), a3 = __byte_perm(x2, x3, 0x7632);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
-                                    mma16816<false>(o[nt][j][w], a0, a1, a2, a3, pf[m][nt][0][0], pf[m][nt][1][0]);
-                                    mma16816<false>(o[nt][j][w], a0, a1, a2, a3, pf[m][nt][0][1], pf[m][nt][1][1]);
+                                    mma16816<false>(o[nt][j][i], a0, a1, a2, a3, pf[m][nt][0][0], pf[m][nt][1][0]);
+                                    mma16816<false>(o[nt][j][i], a0, a1, a2, a3, pf[m][nt][0][1], pf[m][nt][1][1]);
                                 }
                             }
                         }
-                if (!more) break;
-                load_v(place_next);
-                place = place_next;
-                tok = next;
             }
+            seq += tiles;
         }
 
         // the warps' shares of the row
@@ -584,151 +800,161 @@ __global__ void __launch_bounds__(AW * 32, MINB) attend_mma_kernel(const AttendA
                 x += __shfl_xor_sync(0xffffffffu, x, 4);
                 x += __shfl_xor_sync(0xffffffffu, x, 8);
                 x += __shfl_xor_sync(0xffffffffu, x, 16);
-                sum[nt][i] = x;
                 if (g == 0) {
-                    s_m[warp][nt * 8 + 2 * c + i] = top[nt][i];
-                    s_l[warp][nt * 8 + 2 * c + i] = x;
+                    s_m[cw * HC + nt * 8 + 2 * c + i] = top[nt][i];
+                    s_l[cw * HC + nt * 8 + 2 * c + i] = x;
                 }
             }
-        __syncthreads();
+        consumers_sync();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float f[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int h = nt * 8 + 2 * c + i;
+                float m = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < CW; ++x) m = fmaxf(m, s_m[x * HC + h]);
+                f[i] = m > -INFINITY ? exp2f(top[nt][i] - m) : 0.f;
+            }
+            float *p0 = s_o + (cw * HC + nt * 8 + 2 * c) * S::O_LD, *p1 = p0 + S::O_LD;
+#pragma unroll
+            for (int j = 0; j < VP; ++j)
+#pragma unroll
+                for (int i = 0; i < OT; i += 2) {
+                    const int d = (j * 8 + g) * VE + 2 * i;
+                    *reinterpret_cast<float4 *>(p0 + d) = make_float4(o[nt][j][i][0] * f[0], o[nt][j][i][2] * f[0],
+                                                                      o[nt][j][i + 1][0] * f[0], o[nt][j][i + 1][2] * f[0]);
+                    *reinterpret_cast<float4 *>(p1 + d) = make_float4(o[nt][j][i][1] * f[1], o[nt][j][i][3] * f[1],
+                                                                      o[nt][j][i + 1][1] * f[1], o[nt][j][i + 1][3] * f[1]);
+                }
+        }
         if (t < HC) {
             float m = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int w = 0; w < AW; ++w) m = fmaxf(m, s_m[w][t]);
+            for (int x = 0; x < CW; ++x) m = fmaxf(m, s_m[x * HC + t]);
             if (m > -INFINITY)
 #pragma unroll
-                for (int w = 0; w < AW; ++w) l += s_l[w][t] * exp2f(s_m[w][t] - m);
+                for (int x = 0; x < CW; ++x) l += s_l[x * HC + t] * exp2f(s_m[x * HC + t] - m);
             s_top[t] = m;
             s_sum[t] = l;
         }
-        __syncthreads();
-#pragma unroll 1
-        for (int w = 0; w < AW; ++w) {
-            if (warp == w) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int ha = nt * 8 + 2 * c;
-                    const float m0 = s_top[ha], m1 = s_top[ha + 1];
-                    const float f0 = m0 > -INFINITY ? exp2f(top[nt][0] - m0) : 0.f;
-                    const float f1 = m1 > -INFINITY ? exp2f(top[nt][1] - m1) : 0.f;
-#pragma unroll
-                    for (int j = 0; j < VP; ++j)
-#pragma unroll
-                        for (int i = 0; i < OT; ++i) {
-                            const int d = (j * 8 + g) * VE + 2 * i;
-                            float2 *p0 = reinterpret_cast<float2 *>(&s_o[ha][d]);
-                            float2 *p1 = reinterpret_cast<float2 *>(&s_o[ha + 1][d]);
-                            float2 x = make_float2(o[nt][j][i][0] * f0, o[nt][j][i][2] * f0);
-                            float2 y = make_float2(o[nt][j][i][1] * f1, o[nt][j][i][3] * f1);
-                            if (w) {
-                                x.x += p0->x, x.y += p0->y;
-                                y.x += p1->x, y.y += p1->y;
-                            }
-                            *p0 = x;
-                            *p1 = y;
-                        }
-                }
-            }
-            __syncthreads();
-        }
+        consumers_sync();
 
-        const float vs = a.kv.v_scale ? a.kv.v_scale[hk] : 1.f;
-        __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) + r * a.out_stride + (long long)h0 * D;
-        float *lse = a.lse ? a.lse + (long long)r * a.q_heads + h0 : nullptr;
-        if (u0 == 0 && u1 == ur) {
-            for (int i = t; i < nh * (D / 2); i += AW * 32) {
-                const int h = i / (D / 2), d = 2 * (i - h * (D / 2));
-                const float f = s_sum[h] > 0.f ? vs / s_sum[h] : 0.f;
-                *reinterpret_cast<uint32_t *>(out + h * D + d) = pack_bf16(s_o[h][d] * f, s_o[h][d + 1] * f);
+        auto merged = [&](int h, int d) {
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int x = 0; x < CW; ++x) {
+                const float4 v = *reinterpret_cast<const float4 *>(s_o + (x * HC + h) * S::O_LD + d);
+                y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
             }
-            if (lse && t < nh) lse[t] = (s_top[t] + log2f(s_sum[t])) * LN2;
-        } else {
-            const long long row0 = at - u0;
-            const int c0 = owner_of(plan, row0), c1 = owner_of(plan, row0 + ur - 1);
-            const PartView p = part_of(a, 2 * cta + (u0 == 0 ? 1 : 0));
-            for (int i = t; i < nh * (D / 4); i += AW * 32) {
+            return y;
+        };
+        if (w.whole()) {
+            const float vs = a.kv.v_scale ? a.kv.v_scale[w.hk] : 1.f;
+            for (int i = t; i < nh * (D / 4); i += CW * 32) {
                 const int h = i / (D / 4), d = 4 * (i - h * (D / 4));
-                *reinterpret_cast<float4 *>(p.o + h * D + d) = *reinterpret_cast<float4 *>(&s_o[h][d]);
+                put(a, w.r, h0 + h, d, merged(h, d), s_sum[h] > 0.f ? vs / s_sum[h] : 0.f);
+            }
+            if (a.lse && t < nh) a.lse[(long long)w.r * a.q_heads + h0 + t] = (s_top[t] + log2f(s_sum[t])) * LN2;
+        } else {
+            const PartView p = part_of(a, 2 * cta + (w.t0 == 0 ? 1 : 0));
+            for (int i = t; i < nh * (D / 4); i += CW * 32) {
+                const int h = i / (D / 4), d = 4 * (i - h * (D / 4));
+                *reinterpret_cast<float4 *>(p.o + h * D + d) = merged(h, d);
             }
             if (t < nh) p.m[t] = s_top[t], p.l[t] = s_sum[t];
-            __threadfence();
-            __syncthreads();
-            if (t == 0) {
-                s_last = atomicAdd(a.ctr + c0, 1) == c1 - c0;
-                if (s_last) a.ctr[c0] = 0;
-            }
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                const int parts = c1 - c0 + 1;
-                auto slot = [&](int i) { return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i); };
-                for (int h = warp; h < nh; h += AW) {
-                    float m = -INFINITY;
-                    for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(part_of(a, slot(i)).m + h));
-#pragma unroll
-                    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-                    float l = 0.f;
-                    if (m > -INFINITY)
-                        for (int i = lane; i < parts; i += 32) {
-                            const PartView q = part_of(a, slot(i));
-                            l += __ldcg(q.l + h) * exp2f(__ldcg(q.m + h) - m);
-                        }
-#pragma unroll
-                    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-                    if (lane == 0) s_top[h] = m, s_sum[h] = l;
-                }
-                __syncthreads();
-                for (int i = t; i < nh * (D / 4); i += AW * 32) {
-                    const int h = i / (D / 4), d = 4 * (i - h * (D / 4));
-                    const float m = s_top[h];
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (m > -INFINITY)
-#pragma unroll 4
-                        for (int k = 0; k < parts; ++k) {
-                            const PartView q = part_of(a, slot(k));
-                            const float w = exp2f(__ldcg(q.m + h) - m);
-                            const float4 y = __ldcg(reinterpret_cast<const float4 *>(q.o + h * D + d));
-                            x.x += w * y.x, x.y += w * y.y, x.z += w * y.z, x.w += w * y.w;
-                        }
-                    const float f = s_sum[h] > 0.f ? vs / s_sum[h] : 0.f;
-                    uint2 y;
-                    y.x = pack_bf16(x.x * f, x.y * f);
-                    y.y = pack_bf16(x.z * f, x.w * f);
-                    *reinterpret_cast<uint2 *>(out + h * D + d) = y;
-                }
-                if (lse && t < nh) lse[t] = (s_top[t] + log2f(s_sum[t])) * LN2;
-            }
+            (w.t0 == 0 ? tail : head) = Shared{w.r, w.hk, h0, nh, w.first_owner(), w.last_owner()};
         }
-        __syncthreads();
-        at += u1 - u0;
+    }
+
+    // arrive at the shared rows; the last to arrive joins
+    if (head.r < 0 && tail.r < 0) return;
+    __threadfence();
+    consumers_sync();
+    if (t < 2) {
+        const Shared &row = t ? tail : head;
+        int last = 0;
+        if (row.r >= 0) {
+            last = atomicAdd(a.ctr + row.c0, 1) == row.c1 - row.c0;
+            if (last) a.ctr[row.c0] = 0;
+        }
+        s_last[t] = last;
+    }
+    consumers_sync();
+    __threadfence();
+    for (int which = 0; which < 2; ++which) {
+        if (!s_last[which]) continue;
+        const Shared row = which ? tail : head;
+        const int parts = row.c1 - row.c0 + 1;
+        auto slot = [&](int i) { return i == 0 ? 2 * row.c0 + 1 : 2 * (row.c0 + i); };
+        consumers_sync();
+        for (int h = cw; h < row.nh; h += CW) {
+            float m = -INFINITY;
+            for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(part_of(a, slot(i)).m + h));
+#pragma unroll
+            for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+            float l = 0.f;
+            if (m > -INFINITY)
+                for (int i = lane; i < parts; i += 32) {
+                    const PartView q = part_of(a, slot(i));
+                    l += __ldcg(q.l + h) * exp2f(__ldcg(q.m + h) - m);
+                }
+#pragma unroll
+            for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+            if (lane == 0) s_top[h] = m, s_sum[h] = l;
+        }
+        consumers_sync();
+        const float vs = a.kv.v_scale ? a.kv.v_scale[row.hk] : 1.f;
+        for (int i = t; i < row.nh * (D / 4); i += CW * 32) {
+            const int h = i / (D / 4), d = 4 * (i - h * (D / 4));
+            const float m = s_top[h];
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (m > -INFINITY)
+#pragma unroll 8
+                for (int k = 0; k < parts; ++k) {
+                    const PartView q = part_of(a, slot(k));
+                    const float f = exp2f(__ldcg(q.m + h) - m);
+                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(q.o + h * D + d));
+                    x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+                }
+            put(a, row.r, row.h0 + h, d, x, s_sum[h] > 0.f ? vs / s_sum[h] : 0.f);
+        }
+        if (a.lse && t < row.nh) a.lse[(long long)row.r * a.q_heads + row.h0 + t] = (s_top[t] + log2f(s_sum[t])) * LN2;
     }
 }
 
-// CTAs of a launch: every SM's, as many as reside (a CTA never waits for
-// another, so more would only be slower).
-template <bool FP8, int DC, int NT, int MINB>
+template <bool FP8, int DC, int NT>
 cudaError_t launch_mma(const AttendArgs &a, int num_sms, cudaStream_t st) {
+    using S = Shape<FP8, DC, NT>;
     static std::atomic<unsigned long long> done{0};
-    const size_t smem = sizeof(int) * ((size_t)a.n_req + 1);
-    if (smem > 16 * 1024) {
-        const cudaError_t e = allow_max_dynamic_smem(attend_mma_kernel<FP8, DC, NT, MINB>, done);
-        if (e != cudaSuccess) return e;
+    const cudaError_t e = allow_max_dynamic_smem(attend_mma_kernel<FP8, DC, NT>, done);
+    if (e != cudaSuccess) return e;
+    // two CTAs on an SM, so that one streams while the other ends a row; one where
+    // a large batch's list leaves too little room for two rings
+    int per_sm = 2;
+    long long stages = (113 * 1024 - (long long)S::smem(0, a.n_req)) / S::STAGE / CW * CW;
+    if (stages < CW) {
+        per_sm = 1;
+        stages = (226 * 1024 - (long long)S::smem(0, a.n_req)) / S::STAGE / CW * CW;
     }
-    attend_mma_kernel<FP8, DC, NT, MINB><<<num_sms * MINB, AW * 32, smem, st>>>(a);
+    if (stages > MAX_STAGES) stages = MAX_STAGES;
+    attend_mma_kernel<FP8, DC, NT>
+        <<<num_sms * per_sm, AT_THREADS, S::smem((int)stages, a.n_req), st>>>(a, (int)stages);
     return cudaGetLastError();
 }
 
 template <bool FP8>
 cudaError_t launch_by_dim(const AttendArgs &a, int num_sms, cudaStream_t st) {
     const int D = a.kv.dim;
-    if (D > 128) return launch_mma<FP8, 256, 1, 2>(a, num_sms, st);
-    if (D > 64) return a.group > 8 ? launch_mma<FP8, 128, 2, 2>(a, num_sms, st) : launch_mma<FP8, 128, 1, 3>(a, num_sms, st);
-    return a.group > 8 ? launch_mma<FP8, 64, 2, 3>(a, num_sms, st) : launch_mma<FP8, 64, 1, 3>(a, num_sms, st);
+    if (D > 128) return launch_mma<FP8, 256, 1>(a, num_sms, st);
+    if (D > 64) return a.group > 8 ? launch_mma<FP8, 128, 2>(a, num_sms, st) : launch_mma<FP8, 128, 1>(a, num_sms, st);
+    return a.group > 8 ? launch_mma<FP8, 64, 2>(a, num_sms, st) : launch_mma<FP8, 64, 1>(a, num_sms, st);
 }
 
 }  // namespace
 
-constexpr int ATT_CTAS = 4;      // CTAs of an SM, at most
+constexpr int ATT_CTAS = 2;      // CTAs of an SM, at most
 size_t attend_part_floats(int num_sms) { return (size_t)num_sms * ATT_CTAS * 2 * PART_FLOATS; }
 int attend_ctrs(int num_sms) { return num_sms * ATT_CTAS; }
 
