@@ -455,7 +455,7 @@ scute_status scute_kv_append(scute_ctx *ctx, const scute_kv_cache *kv, const int
  *   lse       NULL, or device float [n_req][q_heads]: log sum exp of the scores
  *             (joins this result with one over other tokens);
  *   scale     0: 1 / sqrt(head_dim).
- * n_req is 0..SCUTE_MAX_REQUESTS; table_cols * page_size at most 2^30, and 2^34
+ * n_req is 0..SCUTE_MAX_REQUESTS; table_cols * page_size at most 2^30, and 2^33
  * over all requests; q_heads a multiple of kv_heads.  Scores,
  * softmax statistics and sums are held in 32 bits.  The work is cut over the
  * whole batch's tokens, whatever request they belong to, and joined in a fixed

@@ -1,136 +1,4 @@
 // Attention of one new token of each request over its paged cache.
-#include <cuda_fp8.h>
-
-#include "internal.h"
-#include "ptx.cuh"
-
-namespace scute {
-
-namespace {
-
-__device__ __forceinline__ float ld(const float *p) { return *p; }
-__device__ __forceinline__ void st(float *p, float x) { *p = x; }
-
-constexpr int AT_HEADS = 8, AT_TILE = 32;
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-
-// One CTA per request, key/value head and up to 8 of its query heads: tiles of
-// 32 tokens with a running maximum and sum.  IO: type of q and out, KV: of the cache.
-template <typename IO, typename KV>
-__global__ void __launch_bounds__(128) attend_kernel(const AttendArgs a) {
-    __shared__ float sq[AT_HEADS][ATT_MAX_DIM];
-    __shared__ float sp[AT_HEADS][AT_TILE];
-    __shared__ float s_alpha[AT_HEADS];
-    __shared__ long long s_off[AT_TILE];
-    const int r = blockIdx.x, hk = blockIdx.y, D = a.kv.dim, t = threadIdx.x;
-    const int h0 = blockIdx.z * AT_HEADS, nh = min(AT_HEADS, a.group - h0);
-    const long long cap = (long long)a.kv.table_cols * a.kv.page_size;
-    int len = a.kv_len[r];
-    if (len < 0 || len > cap) {
-        if (t == 0) atomicOr(a.status, STATUS_PAGES);
-        len = len < 0 ? 0 : (int)cap;
-    }
-    const int first = a.window > 0 ? max(0, len - a.window) : 0;
-    const IO *q = reinterpret_cast<const IO *>(a.q) + r * a.q_stride + (long long)(hk * a.group + h0) * D;
-    const float ks = a.kv.k_scale ? a.kv.k_scale[hk] : 1.f;
-    for (int i = t; i < nh * D; i += 128) sq[i / D][i % D] = ld(q + i) * (ks * a.scale);
-    const KV *k = reinterpret_cast<const KV *>(a.kv.k) + hk * a.kv.head_stride;
-    const KV *v = reinterpret_cast<const KV *>(a.kv.v) + hk * a.kv.head_stride;
-    const int lane = t & 31, warp = t >> 5;
-    float acc[AT_HEADS][2] = {};
-    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};    // heads warp and warp + 4
-    for (int t0 = first; t0 < len; t0 += AT_TILE) {
-        __syncthreads();
-        if (t < AT_TILE) {
-            long long off = -1;
-            if (t0 + t < len) {
-                const int page = a.kv.table[r * a.kv.table_stride + (t0 + t) / a.kv.page_size];
-                if (page >= 0 && page < a.kv.n_pages)
-                    off = page * a.kv.page_stride + ((t0 + t) % a.kv.page_size) * a.kv.token_stride;
-                else
-                    atomicOr(a.status, STATUS_PAGES);
-            }
-            s_off[t] = off;
-        }
-        __syncthreads();
-        {
-            const int tok = t >> 2, part = t & 3;
-            const long long off = s_off[tok];
-            float s[AT_HEADS] = {};
-            if (off >= 0)
-                for (int i = part; i < D; i += 4) {
-                    const float x = ld(k + off + i);
-                    for (int h = 0; h < nh; ++h) s[h] += x * sq[h][i];
-                }
-            for (int h = 0; h < nh; ++h) {
-                float x = s[h];
-                x += __shfl_xor_sync(0xffffffffu, x, 1);
-                x += __shfl_xor_sync(0xffffffffu, x, 2);
-                if (a.softcap > 0.f) x = a.softcap * tanhf(x / a.softcap);
-                if (part == 0) sp[h][tok] = off >= 0 ? x : -INFINITY;
-            }
-        }
-        __syncthreads();
-        for (int j = 0; j < 2; ++j) {
-            const int h = warp + 4 * j;
-            if (h >= nh) break;
-            const float x = sp[h][lane];
-            float m = x;
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            m = fmaxf(m, top[j]);
-            const float ref = m == -INFINITY ? 0.f : m;
-            const float p = expf(x - ref), alpha = expf(top[j] - ref);
-            float all = p;
-            for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-            sum[j] = sum[j] * alpha + all;
-            top[j] = m;
-            sp[h][lane] = p;
-            if (lane == 0) s_alpha[h] = alpha;
-        }
-        __syncthreads();
-        for (int h = 0; h < nh; ++h) {
-            acc[h][0] *= s_alpha[h];
-            acc[h][1] *= s_alpha[h];
-        }
-        for (int tok = 0; tok < AT_TILE; ++tok) {
-            const long long off = s_off[tok];
-            if (off < 0) continue;
-            for (int e = 0; e < 2; ++e) {
-                const int i = t + 128 * e;
-                if (i >= D) break;
-                const float x = ld(v + off + i);
-                for (int h = 0; h < nh; ++h) acc[h][e] += sp[h][tok] * x;
-            }
-        }
-    }
-    __syncthreads();
-    for (int j = 0; j < 2; ++j) {
-        const int h = warp + 4 * j;
-        if (h < nh && lane == 0) {
-            s_alpha[h] = sum[j] > 0.f ? 1.f / sum[j] : 0.f;
-            if (a.lse) a.lse[(long long)r * a.q_heads + hk * a.group + h0 + h] = top[j] + logf(sum[j]);
-        }
-    }
-    __syncthreads();
-    const float vs = a.kv.v_scale ? a.kv.v_scale[hk] : 1.f;
-    IO *out = reinterpret_cast<IO *>(a.out) + r * a.out_stride + (long long)(hk * a.group + h0) * D;
-    for (int h = 0; h < nh; ++h)
-        for (int e = 0; e < 2; ++e)
-            if (t + 128 * e < D) st(out + h * D + t + 128 * e, acc[h][e] * s_alpha[h] * vs);
-}
-
-
-// ---------------------------------------------------------------- 16- and 8-bit caches
-// The products run on the warp-wide matrix instructions with the cache as the
-// operand of 16 rows and the query heads as the one of 8 columns:
-//     S^T [16 tokens x 8 heads] = K [16 x D] Q^T,
-//     O^T [D x 8 heads] += V^T [D x 16 tokens] P^T,
-// so a group of 4 or 8 query heads wastes little.  A product's inner index may
-// be numbered in any way that both operands share, so lane (g, c) = (lane / 4,
-// lane % 4) takes 16 consecutive bytes of token g's (and g + 8's) key and the
-// query's fragment the same elements; and 16 consecutive bytes of the values of
-// tokens 2c, 2c + 1, 2c + 8, 2c + 9, of which pairs of tokens are interleaved by
-// byte permutes.
 //
 // The work is one sequence of tiles (TT tokens of one request and head row),
 // with ROW_COST places before each row's first for what a row costs beside its
@@ -142,12 +10,21 @@ __global__ void __launch_bounds__(128) attend_kernel(const AttendArgs a) {
 // shared memory where a row ends.  Of a row that several CTAs share each leaves
 // its part in the workspace, arrives at the row's counter when its whole range is
 // done, and the last to arrive joins the parts in the order of the CTAs.
-constexpr int CW = 4;                     // warps that compute
-constexpr int PW = 2;                     // warps that fetch
-constexpr int AT_THREADS = 32 * (CW + PW);
+#include <cuda_fp8.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace scute {
+
+namespace {
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr int ATT_CTAS = 4;               // CTAs of an SM, at most
 constexpr int QS = 2;                     // rows whose queries may be waiting
 constexpr int MAX_STAGES = 32;
-constexpr int ROW_COST = 5;               // tiles
+constexpr int ROW_COST = 3;               // tiles
+constexpr int MIN_TILES = 4;              // of a CTA's range, where the batch has enough
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
@@ -186,7 +63,18 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real)
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(CW * 32) : "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void sync_threads() { asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory"); }
+__device__ __forceinline__ float reduce_max(float x) {        // over the lanes of one column
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float reduce_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
 template <bool F16>
 __device__ __forceinline__ void mma16816(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -202,17 +90,30 @@ __device__ __forceinline__ void mma16816(float *c, uint32_t a0, uint32_t a1, uin
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// 2^x; results below the normal range are zero.
+__device__ __forceinline__ float pow2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-// Two e4m3 values (the low 16 bits) as two halves.
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {
+// Two e4m3 values, the low or the high 16 bits of a word, as two halves.
+__device__ __forceinline__ uint32_t halves_lo(uint32_t x) {
     uint32_t y;
-    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(y) : "r"(x));
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(y) : "r"(x));
     return y;
 }
+__device__ __forceinline__ uint32_t halves_hi(uint32_t x) {
+    uint32_t y;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(y) : "r"(x));
+    return y;
+}
+// A capped score, in powers of two (kept out of the loop's code).
+__device__ __noinline__ float capped(float x, float cap) { return cap * LOG2E * tanhf(x / cap); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t y;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
@@ -223,6 +124,459 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
     return y;
 }
+
+// A stage holds a tile's key rows, then its value rows (ROW bytes each).  The
+// 16-byte pieces of a row are permuted within 128 bytes so that the lanes of a
+// quarter warp read different banks, of the keys (rows 2i and 2i + 1, four
+// neighbouring pieces of each) as of the values (rows 0, 2, 4, 6, two pieces of each).
+template <int ROW>
+__device__ __forceinline__ uint32_t place_of(int row, int piece) {
+    const uint32_t turn = ROW == 64 ? (row >> 1 & 3) << 5 : ((row & 1) << 6) ^ ((row >> 1 & 3) << 5);
+    return (row * ROW + piece * 16) ^ turn;
+}
+
+// ---------------------------------------------------------------- 16- and 8-bit caches
+// The products run on the warp-wide matrix instructions with the cache as the
+// operand of 16 rows and the query heads as the one of 8 columns:
+//     S^T [16 tokens x 8 heads] = K [16 x D] Q^T,
+//     O^T [D x 8 heads] += V^T [D x 16 tokens] P^T,
+// so a group of 4 or 8 query heads wastes little.  A product's inner index may
+// be numbered in any way that both operands share, so lane (g, c) = (lane / 4,
+// lane % 4) takes 16 consecutive bytes of token g's (and g + 8's) key and the
+// query's fragment the same elements; and 16 consecutive bytes of the values of
+// tokens 2c, 2c + 1, 2c + 8, 2c + 9, of which pairs of tokens are interleaved by
+// byte permutes.  The work per byte is small (2 x 8 products for each element,
+// about a tenth of these instructions' rate at full memory bandwidth), so the
+// larger tiles of the asynchronous matrix unit would gain nothing here.
+template <bool FP8, int DC, int NT>
+struct MmaMath {
+    using IO = __nv_bfloat16;
+    static constexpr int ESZ = FP8 ? 1 : 2, ROW = DC * ESZ;
+    static constexpr int MT = ROW <= 128 ? 2 : 1;         // 16-token steps of a tile
+    static constexpr int TT = 16 * MT, HC = 8 * NT;
+    static constexpr int P_BYTES = 0;
+    static constexpr int KE = FP8 ? 16 : 8;               // elements of 16 bytes
+    static constexpr int KP = DC / (4 * KE);              // key pieces of a lane, each four lanes wide
+    static constexpr int VE = FP8 && DC > 64 ? 16 : 8;    // elements of a value piece, eight lanes wide
+    static constexpr int VP = DC / (8 * VE);
+    static constexpr int VW = VE * ESZ / 4;               // its words
+    static constexpr int OT = VE / 2;                     // 16-row output tiles of a value piece
+
+    const int lane, g, c;
+    uint32_t qf[NT][KP][KE / 2];
+    float mul[NT][2];             // product to score, per head of this lane's columns
+    float o[NT][VP][OT][4], top[NT][2], sum[NT][2];
+
+    __device__ __forceinline__ MmaMath(int l, uint32_t) : lane(l), g(l >> 2), c(l & 3) {}
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            top[nt][0] = top[nt][1] = -INFINITY;
+            sum[nt][0] = sum[nt][1] = 0.f;
+#pragma unroll
+            for (int j = 0; j < VP; ++j)
+#pragma unroll
+                for (int i = 0; i < OT; ++i) o[nt][j][i][0] = o[nt][j][i][1] = o[nt][j][i][2] = o[nt][j][i][3] = 0.f;
+        }
+    }
+    // The row's queries, [nh][D] in shared memory: the fragments' elements are those
+    // of the keys' pieces.
+    __device__ __forceinline__ void queries(uint32_t qs, int nh, int D, float scale) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int h = nt * 8 + g;
+#pragma unroll
+            for (int p = 0; p < KP; ++p)
+#pragma unroll
+                for (int e = 0; e < KE / 8; ++e) {
+                    const int d = (p * 4 + c) * KE + e * 8;
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (h < nh && d < D) x = lds16(qs + (h * D + d) * 2);
+                    qf[nt][p][e * 4 + 0] = x.x;
+                    qf[nt][p][e * 4 + 1] = x.y;
+                    qf[nt][p][e * 4 + 2] = x.z;
+                    qf[nt][p][e * 4 + 3] = x.w;
+                }
+            float back = 1.f;
+            if constexpr (FP8) {
+                // 16-bit halves have 11 bits where bf16 has 8: scaled by a power of
+                // two that takes the head's largest element below 2^8, every element
+                // down to 2^-22 of it stays exact
+                float big = 0.f;
+#pragma unroll
+                for (int p = 0; p < KP; ++p)
+#pragma unroll
+                    for (int e = 0; e < KE / 2; ++e) {
+                        const uint32_t w = qf[nt][p][e];
+                        big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))));
+                    }
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                int ex = 0;
+                if (big > 0.f && big < INFINITY) frexpf(big, &ex);
+                ex = max(-100, min(100, ex - 8));
+                const float down = ldexpf(1.f, -ex);
+                back = ldexpf(1.f, ex);
+#pragma unroll
+                for (int p = 0; p < KP; ++p)
+#pragma unroll
+                    for (int e = 0; e < KE / 2; ++e) {
+                        const uint32_t w = qf[nt][p][e];
+                        qf[nt][p][e] = pack_f16(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down);
+                    }
+            }
+            mul[nt][0] = __shfl_sync(0xffffffffu, back, (2 * c) * 4) * scale;
+            mul[nt][1] = __shfl_sync(0xffffffffu, back, (2 * c + 1) * 4) * scale;
+        }
+    }
+    // One tile: keys at kd, values at vd, bit i of ok whether token i counts;
+    // release() when the stage is in registers.
+    template <typename F>
+    __device__ __forceinline__ void tile(uint32_t kd, uint32_t vd, unsigned ok, float softcap, F release) {
+        // two accumulators, so that a product seldom waits for the one before it
+        float sc[MT][NT][4] = {}, sd[MT][NT][4] = {};
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < KP; ++j) {
+                const uint4 x = lds16(kd + place_of<ROW>(m * 16 + g, j * 4 + c));
+                const uint4 y = lds16(kd + place_of<ROW>(m * 16 + g + 8, j * 4 + c));
+                const uint32_t w0[4] = {x.x, x.y, x.z, x.w}, w1[4] = {y.x, y.y, y.z, y.w};
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t a0 = halves_lo(w0[e]), a2 = halves_hi(w0[e]);
+                        const uint32_t a1 = halves_lo(w1[e]), a3 = halves_hi(w1[e]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816<true>(e & 1 ? sd[m][nt] : sc[m][nt], a0, a1, a2, a3, qf[nt][j][2 * e],
+                                           qf[nt][j][2 * e + 1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816<false>(e & 1 ? sd[m][nt] : sc[m][nt], w0[2 * e], w1[2 * e], w0[2 * e + 1],
+                                            w1[2 * e + 1], qf[nt][j][2 * e], qf[nt][j][2 * e + 1]);
+                }
+            }
+        uint32_t vr[MT][4][VP][VW];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int tok = m * 16 + 2 * c + (k & 1) + (k >> 1) * 8;
+#pragma unroll
+                for (int j = 0; j < VP; ++j) {
+                    if constexpr (VW == 4) {
+                        const uint4 x = lds16(vd + place_of<ROW>(tok, j * 8 + g));
+                        vr[m][k][j][0] = x.x, vr[m][k][j][1] = x.y, vr[m][k][j][2] = x.z, vr[m][k][j][3] = x.w;
+                    } else {
+                        const uint2 x = lds8(vd + place_of<ROW>(tok, g >> 1) + (g & 1) * 8);
+                        vr[m][k][j][0] = x.x, vr[m][k][j][1] = x.y;
+                    }
+                }
+            }
+        release();
+
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sc[m][nt][k] = (sc[m][nt][k] + sd[m][nt][k]) * mul[nt][k & 1];
+        if (softcap > 0.f) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sc[m][nt][k] = capped(sc[m][nt][k], softcap);
+        }
+        if (ok != (TT == 32 ? 0xffffffffu : 0xffffu)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (!(ok >> (m * 16 + (k >> 1) * 8 + g) & 1)) sc[m][nt][k] = -INFINITY;
+        }
+        // scores in powers of two; the reference of the weights moves only when a
+        // score passes it by more than 2^8, so that the outputs are seldom scaled
+        // (weights are then at most 2^8, which every type here holds)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mx[k & 1] = fmaxf(mx[k & 1], sc[m][nt][k]);
+            if (__any_sync(0xffffffffu, mx[0] > top[nt][0] + 8.f || mx[1] > top[nt][1] + 8.f)) {
+                float al[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float x = fmaxf(reduce_max(mx[k]), top[nt][k]);
+                    al[k] = x == top[nt][k] ? 1.f : exp2f(top[nt][k] - x);
+                    top[nt][k] = x;
+                    sum[nt][k] *= al[k];
+                }
+#pragma unroll
+                for (int j = 0; j < VP; ++j)
+#pragma unroll
+                    for (int k = 0; k < OT; ++k) {
+                        o[nt][j][k][0] *= al[0];
+                        o[nt][j][k][1] *= al[1];
+                        o[nt][j][k][2] *= al[0];
+                        o[nt][j][k][3] *= al[1];
+                    }
+            }
+        }
+        uint32_t pf[MT][NT][2][2];            // [tokens 0-7, 8-15][weights, what their rounding left]
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float ref[2] = {top[nt][0] == -INFINITY ? 0.f : top[nt][0], top[nt][1] == -INFINITY ? 0.f : top[nt][1]};
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                float p[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    p[k] = pow2(sc[m][nt][k] - ref[k & 1]);
+                    sum[nt][k & 1] += p[k];
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if constexpr (FP8) {
+                        pf[m][nt][k][0] = transpose8(pack_f16(p[2 * k], p[2 * k + 1]));
+                    } else {
+                        // bf16 keeps 8 bits of a weight: a second product takes the rest
+                        const uint32_t hi = pack_bf16(p[2 * k], p[2 * k + 1]);
+                        const float r0 = p[2 * k] - __uint_as_float(hi << 16);
+                        const float r1 = p[2 * k + 1] - __uint_as_float(hi & 0xffff0000u);
+                        pf[m][nt][k][0] = transpose8(hi);
+                        pf[m][nt][k][1] = transpose8(pack_bf16(r0, r1));
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < VP; ++j)
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+                    const uint32_t x0 = vr[m][0][j][i], x1 = vr[m][1][j][i];
+                    const uint32_t x2 = vr[m][2][j][i], x3 = vr[m][3][j][i];
+                    if constexpr (FP8) {
+                        const uint32_t y0 = __byte_perm(x0, x1, 0x5140), y1 = __byte_perm(x0, x1, 0x7362);
+                        const uint32_t y2 = __byte_perm(x2, x3, 0x5140), y3 = __byte_perm(x2, x3, 0x7362);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t ya = k ? y1 : y0, yb = k ? y3 : y2;
+                            const uint32_t a0 = halves_lo(ya), a1 = halves_hi(ya);
+                            const uint32_t a2 = halves_lo(yb), a3 = halves_hi(yb);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<true>(o[nt][j][2 * i + k], a0, a1, a2, a3, pf[m][nt][0][0], pf[m][nt][1][0]);
+                        }
+                    } else {
+                        const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
+                        const uint32_t a2 = __byte_perm(x2, x3, 0x5410), a3 = __byte_perm(x2, x3, 0x7632);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816<false>(o[nt][j][i], a0, a1, a2, a3, pf[m][nt][0][0], pf[m][nt][1][0]);
+                            mma16816<false>(o[nt][j][i], a0, a1, a2, a3, pf[m][nt][0][1], pf[m][nt][1][1]);
+                        }
+                    }
+                }
+    }
+    // The warp's maximum and sum of every head, to m and l.
+    __device__ __forceinline__ void stats(float *m, float *l) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float x = reduce_sum(sum[nt][i]);
+                if (x != x && top[nt][i] == -INFINITY) top[nt][i] = 0.f;      // no number: not an empty share
+                if (g == 0) {
+                    m[nt * 8 + 2 * c + i] = top[nt][i];
+                    l[nt * 8 + 2 * c + i] = x;
+                }
+            }
+    }
+    // The warp's outputs, [HC] rows of `ld` floats, relative to the maxima `all`.
+    __device__ __forceinline__ void outputs(float *to, int ld, const float (&all)[NT][2]) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float f[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) f[i] = all[nt][i] > -INFINITY ? exp2f(top[nt][i] - all[nt][i]) : 0.f;
+            float *p0 = to + (nt * 8 + 2 * c) * ld, *p1 = p0 + ld;
+#pragma unroll
+            for (int j = 0; j < VP; ++j)
+#pragma unroll
+                for (int i = 0; i < OT; i += 2) {
+                    const int d = (j * 8 + g) * VE + 2 * i;
+                    *reinterpret_cast<float4 *>(p0 + d) = make_float4(o[nt][j][i][0] * f[0], o[nt][j][i][2] * f[0],
+                                                                      o[nt][j][i + 1][0] * f[0], o[nt][j][i + 1][2] * f[0]);
+                    *reinterpret_cast<float4 *>(p1 + d) = make_float4(o[nt][j][i][1] * f[1], o[nt][j][i][3] * f[1],
+                                                                      o[nt][j][i + 1][1] * f[1], o[nt][j][i + 1][3] * f[1]);
+                }
+        }
+    }
+    // Merge the maxima of CW warps and write this warp's outputs.
+    template <int CW>
+    __device__ __forceinline__ void finish(const float *s_m, float *to, int ld) {
+        float all[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                all[nt][i] = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < CW; ++x) all[nt][i] = fmaxf(all[nt][i], s_m[x * HC + nt * 8 + 2 * c + i]);
+            }
+        outputs(to, ld, all);
+    }
+};
+
+// ---------------------------------------------------------------- 32-bit caches
+// Sums in 32 bits throughout, NH heads at a time.  Scores: lane (g, c) multiplies
+// every fourth 16-byte piece of token g's key, and the four lanes of a token add
+// up.  Outputs: a lane owns DC / 32 neighbouring elements and takes the tile's
+// tokens one after another, their weights from shared memory.
+template <int DC, int NH>
+struct FmaMath {
+    using IO = float;
+    static constexpr int ESZ = 4, ROW = DC * 4;
+    static constexpr int TT = DC <= 64 ? 16 : 8, MT = TT / 8, HC = NH;
+    static constexpr int P_BYTES = HC * TT * 4;
+    static constexpr int KP = DC / 16;                    // key pieces of a lane
+    static constexpr int E = DC / 32;                     // outputs of a lane
+
+    const int lane, g, c;
+    const uint32_t ps;            // this warp's weights, [HC][TT]
+    uint32_t qs;
+    int D;
+    float mul, o[NH][E], top[NH], sum[NH];
+
+    __device__ __forceinline__ FmaMath(int l, uint32_t weights) : lane(l), g(l >> 2), c(l & 3), ps(weights) {}
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            top[h] = -INFINITY, sum[h] = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[h][e] = 0.f;
+        }
+    }
+    __device__ __forceinline__ void queries(uint32_t q, int, int dim, float scale) { qs = q, D = dim, mul = scale; }
+    template <typename F>
+    __device__ __forceinline__ void tile(uint32_t kd, uint32_t vd, unsigned ok, float softcap, F release) {
+        float s[MT][NH] = {};
+#pragma unroll
+        for (int j = 0; j < KP; ++j) {
+            const int d = (j * 4 + c) * 4;
+            float k[MT][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const uint4 x = lds16(kd + place_of<ROW>(m * 8 + g, j * 4 + c));
+                k[m][0] = __uint_as_float(x.x), k[m][1] = __uint_as_float(x.y);
+                k[m][2] = __uint_as_float(x.z), k[m][3] = __uint_as_float(x.w);
+            }
+            if (d < D)
+#pragma unroll
+                for (int h = 0; h < NH; ++h) {      // rows behind the last head are not read back
+                    const uint4 x = lds16(qs + (h * D + d) * 4);
+                    const float q[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[m][h] = fmaf(k[m][e], q[e], s[m][h]);
+                }
+        }
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                float x = s[m][h];
+                x += __shfl_xor_sync(0xffffffffu, x, 1);
+                x += __shfl_xor_sync(0xffffffffu, x, 2);
+                x *= mul;
+                if (softcap > 0.f) x = capped(x, softcap);
+                if (!(ok >> (m * 8 + g) & 1)) x = -INFINITY;
+                s[m][h] = x;
+                mx = fmaxf(mx, x);
+            }
+            if (__any_sync(0xffffffffu, mx > top[h] + 8.f)) {
+                const float x = fmaxf(reduce_max(mx), top[h]);
+                const float al = x == top[h] ? 1.f : exp2f(top[h] - x);
+                top[h] = x;
+                sum[h] *= al;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[h][e] *= al;
+            }
+            const float ref = top[h] == -INFINITY ? 0.f : top[h];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const float p = exp2f(s[m][h] - ref);
+                sum[h] += p;
+                if (c == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(ps + (h * TT + m * 8 + g) * 4), "f"(p) : "memory");
+            }
+        }
+        __syncwarp();
+        constexpr int B = 4;                 // tokens at a time
+#pragma unroll
+        for (int t0 = 0; t0 < TT; t0 += B) {
+            float v[B][E];
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                if constexpr (E == 2) {
+                    const uint2 x = lds8(vd + place_of<ROW>(t0 + i, lane >> 1) + (lane & 1) * 8);
+                    v[i][0] = __uint_as_float(x.x), v[i][1] = __uint_as_float(x.y);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E / 4; ++e) {
+                        const uint4 x = lds16(vd + place_of<ROW>(t0 + i, lane * (E / 4) + e));
+                        v[i][4 * e] = __uint_as_float(x.x), v[i][4 * e + 1] = __uint_as_float(x.y);
+                        v[i][4 * e + 2] = __uint_as_float(x.z), v[i][4 * e + 3] = __uint_as_float(x.w);
+                    }
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                const uint4 x = lds16(ps + (h * TT + t0) * 4);
+                const float p[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
+#pragma unroll
+                for (int i = 0; i < B; ++i)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[h][e] = fmaf(p[i], v[i][e], o[h][e]);
+            }
+        }
+        release();
+    }
+    __device__ __forceinline__ void stats(float *m, float *l) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            const float x = reduce_sum(sum[h]);
+            if (x != x && top[h] == -INFINITY) top[h] = 0.f;
+            if (lane == 0) m[h] = top[h], l[h] = x;
+        }
+    }
+    template <int CW>
+    __device__ __forceinline__ void finish(const float *s_m, float *to, int ld) {
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            float all = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < CW; ++x) all = fmaxf(all, s_m[x * HC + h]);
+            const float f = all > -INFINITY ? exp2f(top[h] - all) : 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) to[h * ld + lane * E + e] = o[h][e] * f;
+        }
+    }
+};
 
 // The batch's work list.  Row (request r, key/value head and head chunk) takes
 // ROW_COST places and then one for each of its tiles, an empty request's row one
@@ -236,8 +590,8 @@ __device__ __forceinline__ void seen_of(const AttendArgs &a, int r, int *first, 
     *first = a.window > 0 ? max(0, n - a.window) : 0;
 }
 __device__ __forceinline__ void plan_places(const AttendArgs &a, int tt, int *places_at, int *warp_sum) {
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, n = a.n_req;
-    const int per = (n + AT_THREADS - 1) / AT_THREADS, r0 = min(n, t * per), r1 = min(n, r0 + per);
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, n = a.n_req, threads = blockDim.x;
+    const int per = (n + threads - 1) / threads, r0 = min(n, t * per), r1 = min(n, r0 + per);
     int mine = 0;
     bool any = false;
     for (int r = r0; r < r1; ++r) {
@@ -257,8 +611,7 @@ __device__ __forceinline__ void plan_places(const AttendArgs &a, int tt, int *pl
     if (lane == 31) warp_sum[warp] = inc;
     __syncthreads();
     int at = inc - mine;
-#pragma unroll
-    for (int w = 0; w < CW + PW; ++w) at += w < warp ? warp_sum[w] : 0;
+    for (int w = 0; w < warp; ++w) at += warp_sum[w];
     for (int r = r0; r < r1; ++r) {
         int first, len;
         bool bad;
@@ -266,7 +619,7 @@ __device__ __forceinline__ void plan_places(const AttendArgs &a, int tt, int *pl
         places_at[r] = at;
         at += ROW_COST + max(1, (len - first + tt - 1) / tt);
     }
-    if (t == AT_THREADS - 1) places_at[n] = at;
+    if (t == threads - 1) places_at[n] = at;
     __syncthreads();
 }
 
@@ -282,13 +635,12 @@ struct Walk {
     int r, hk, z, tiles, first, len;
     int t0, t1;              // the range's tiles of it
 
-    __device__ __forceinline__ Walk(const AttendArgs &args, const int *at, int heads_chunk, int tile)
+    __device__ __forceinline__ Walk(const AttendArgs &args, const int *at, int heads_chunk, int tile, int min_tiles)
         : a(args), places_at(at), tt(tile) {
         Z = (a.group + heads_chunk - 1) / heads_chunk;
         hz = a.kv.heads * Z;
         total = (long long)at[a.n_req] * hz;
-        // a CTA's warps have a tile each, or the batch has no more
-        ctas = (int)min((long long)gridDim.x, (total + CW - 1) / CW);
+        ctas = (int)min((long long)gridDim.x, (total + min_tiles - 1) / min_tiles);
     }
     __device__ __forceinline__ long long start(int cta) const { return total * cta / ctas; }
     // The CTA whose range holds place x.
@@ -316,7 +668,7 @@ struct Walk {
         }
         request();
         const long long in = x - (long long)places_at[r] * hz;
-        const int row = (int)(in / (tiles + ROW_COST));
+        const int row = in < 1ll << 31 ? (int)((unsigned)in / (unsigned)(tiles + ROW_COST)) : (int)(in / (tiles + ROW_COST));
         base = (long long)places_at[r] * hz + (long long)row * (tiles + ROW_COST);
         hk = row / Z;
         z = row - hk * Z;
@@ -352,55 +704,117 @@ __device__ __forceinline__ PartView part_of(const AttendArgs &a, int slot) {
 }
 
 // Four elements of the output of one head, times f.
+template <typename IO>
 __device__ __forceinline__ void put(const AttendArgs &a, int r, int h, int d, float4 x, float f) {
-    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) + r * a.out_stride + (long long)h * a.kv.dim + d;
-    uint2 y;
-    y.x = pack_bf16(x.x * f, x.y * f);
-    y.y = pack_bf16(x.z * f, x.w * f);
-    *reinterpret_cast<uint2 *>(out) = y;
+    IO *out = reinterpret_cast<IO *>(a.out) + r * a.out_stride + (long long)h * a.kv.dim + d;
+    if constexpr (sizeof(IO) == 4) {
+        *reinterpret_cast<float4 *>(out) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+    } else {
+        uint2 y;
+        y.x = pack_bf16(x.x * f, x.y * f);
+        y.y = pack_bf16(x.z * f, x.w * f);
+        *reinterpret_cast<uint2 *>(out) = y;
+    }
 }
 
-// Sizes of one instance.  A stage holds a tile's key rows, then its value rows.
-// The 16-byte pieces of a row are permuted within 128 bytes so that the lanes of
-// a quarter warp read different banks, of the keys (rows 2i and 2i + 1, four
-// neighbouring pieces of each) as of the values (rows 0, 2, 4, 6, two pieces of each).
-template <bool FP8, int DC, int NT>
+// A row that several CTAs share, as its joiner needs it.
+struct SharedRow {
+    int r, hk, h0, nh, c0, c1;          // request, heads; its first and last CTA
+};
+// Join the parts of up to two rows (n_head and n_tail groups of four outputs):
+// IT groups of a thread and B parts at a time, all their loads on the way at once.
+template <typename IO, int IT, int B, int THREADS>
+__device__ __noinline__ void join_parts(const AttendArgs &a, const SharedRow &head, const SharedRow &tail, int n_head,
+                                        int n_tail, int t) {
+    const int D = a.kv.dim;
+    for (int i0 = t; i0 < n_head + n_tail; i0 += IT * THREADS) {
+        float m[IT], l[IT];
+        float4 x[IT];
+        int parts[IT], first[IT], h[IT], d[IT], most = 0;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int at = i0 + i * THREADS;
+            const bool in_tail = at >= n_head;
+            const int e = in_tail ? at - n_head : at;
+            first[i] = in_tail ? tail.c0 : head.c0;
+            parts[i] = at >= n_head + n_tail ? 0 : (in_tail ? tail.c1 : head.c1) - first[i] + 1;
+            most = max(most, parts[i]);
+            h[i] = e / (D / 4);
+            d[i] = 4 * (e - h[i] * (D / 4));
+            m[i] = -INFINITY, l[i] = 0.f;
+            x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int k0 = 0; k0 < most; k0 += B) {
+            float pm[IT][B], pl[IT][B];
+            float4 po[IT][B];
+#pragma unroll
+            for (int i = 0; i < IT; ++i)
+#pragma unroll
+                for (int k = 0; k < B; ++k) {
+                    pm[i][k] = -INFINITY;
+                    if (k0 + k < parts[i]) {
+                        const PartView q = part_of(a, k0 + k ? 2 * (first[i] + k0 + k) : 2 * first[i] + 1);
+                        pm[i][k] = __ldcg(q.m + h[i]);
+                        pl[i][k] = __ldcg(q.l + h[i]);
+                        po[i][k] = __ldcg(reinterpret_cast<const float4 *>(q.o + h[i] * D + d[i]));
+                    }
+                }
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                float top = m[i];
+#pragma unroll
+                for (int k = 0; k < B; ++k) top = fmaxf(top, pm[i][k]);
+                if (top == -INFINITY) continue;
+                const float f = exp2f(m[i] - top);
+                l[i] *= f, x[i].x *= f, x[i].y *= f, x[i].z *= f, x[i].w *= f;
+                m[i] = top;
+#pragma unroll
+                for (int k = 0; k < B; ++k)
+                    if (pm[i][k] > -INFINITY) {
+                        const float e = exp2f(pm[i][k] - top);
+                        l[i] += e * pl[i][k];
+                        x[i].x += e * po[i][k].x, x[i].y += e * po[i][k].y;
+                        x[i].z += e * po[i][k].z, x[i].w += e * po[i][k].w;
+                    }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+            if (parts[i]) {
+                const SharedRow &row = i0 + i * THREADS >= n_head ? tail : head;
+                const float vs = a.kv.v_scale ? a.kv.v_scale[row.hk] : 1.f;
+                put<IO>(a, row.r, row.h0 + h[i], d[i], x[i], l[i] == 0.f ? 0.f : vs / l[i]);
+                if (a.lse && d[i] == 0) a.lse[(long long)row.r * a.q_heads + row.h0 + h[i]] = (m[i] + log2f(l[i])) * LN2;
+            }
+    }
+}
+
+// Sizes of one instance: CW warps of a CTA compute, PW fetch, CTAS of them share an SM.
+template <typename M, int DC, int CW, int PW, int CTAS>
 struct Shape {
-    static constexpr int ESZ = FP8 ? 1 : 2, ROW = DC * ESZ;
-    static constexpr int MT = ROW <= 128 ? 2 : 1;         // 16-token steps of a tile
-    static constexpr int TT = 16 * MT, HC = 8 * NT;
-    static constexpr int STAGE = 2 * TT * ROW;
-    // the permutation, as bits of a byte address, of row i
-    static __device__ __forceinline__ uint32_t swizzle(int i) {
-        return ROW == 64 ? (i >> 1 & 3) << 5 : ((i & 1) << 6) ^ ((i >> 1 & 3) << 5);
-    }
-    static __device__ __forceinline__ uint32_t place(int i, int piece) {
-        return (i * ROW + piece * 16) ^ swizzle(i);
-    }
+    static constexpr int THREADS = 32 * (CW + PW);
+    static constexpr int STAGE = 2 * M::TT * M::ROW;
     static constexpr int O_LD = DC + 4;                   // floats between heads
-    static constexpr int O_BYTES = CW * HC * O_LD * 4, Q_BYTES = HC * DC * 2;
-    static constexpr int FIXED = O_BYTES + QS * Q_BYTES + CW * HC * 8 + HC * 8 + (2 * MAX_STAGES + 2 * QS) * 8 +
-                                 MAX_STAGES * 4 + 64;
-    static_assert(STAGE % 16 == 0 && O_BYTES % 16 == 0 && Q_BYTES % 16 == 0, "alignment");
+    static constexpr int O_BYTES = CW * M::HC * O_LD * 4, Q_BYTES = M::HC * DC * (int)sizeof(typename M::IO);
+    static constexpr int FIXED = O_BYTES + QS * Q_BYTES + CW * M::P_BYTES + CW * M::HC * 8 + M::HC * 8 +
+                                 (2 * MAX_STAGES + 2 * QS) * 8 + MAX_STAGES * 4 + 64;
+    static_assert(STAGE % 128 == 0 && O_BYTES % 16 == 0 && Q_BYTES % 16 == 0 && M::P_BYTES % 16 == 0, "alignment");
     static size_t smem(int stages, int n_req) { return FIXED + (size_t)stages * STAGE + 4 * ((size_t)n_req + 1); }
 };
 
-template <bool FP8, int DC, int NT>
-__global__ void __launch_bounds__(AT_THREADS, 2) attend_mma_kernel(const AttendArgs a, int stages) {
-    using S = Shape<FP8, DC, NT>;
-    constexpr int MT = S::MT, TT = S::TT, HC = S::HC, ESZ = S::ESZ;
-    constexpr int KE = FP8 ? 16 : 8;                 // elements of 16 bytes
-    constexpr int KP = DC / (4 * KE);                // key pieces of a lane, each four lanes wide
-    constexpr int VE = FP8 && DC > 64 ? 16 : 8;      // elements of a value piece, eight lanes wide
-    constexpr int VP = DC / (8 * VE);
-    constexpr int VW = VE * ESZ / 4;                 // its words
-    constexpr int OT = VE / 2;                       // 16-row output tiles of a value piece
+template <typename M, int DC, int CW, int PW, int CTAS>
+__global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const AttendArgs a, int stages) {
+    using S = Shape<M, DC, CW, PW, CTAS>;
+    using IO = typename M::IO;
+    constexpr int TT = M::TT, HC = M::HC, ESZ = M::ESZ;
+    constexpr unsigned ALL = TT == 32 ? 0xffffffffu : (1u << TT) - 1;
 
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *const s_ring = smem;
     float *const s_o = reinterpret_cast<float *>(smem + (size_t)stages * S::STAGE);   // [CW][HC][O_LD]
     uint8_t *const s_q = reinterpret_cast<uint8_t *>(s_o) + S::O_BYTES;               // [QS][HC][D]
-    float *const s_m = reinterpret_cast<float *>(s_q + QS * S::Q_BYTES);              // [CW][HC]
+    uint8_t *const s_p = s_q + QS * S::Q_BYTES;                                       // [CW] weights of a tile
+    float *const s_m = reinterpret_cast<float *>(s_p + CW * M::P_BYTES);              // [CW][HC]
     float *const s_l = s_m + CW * HC;                                                 // [CW][HC]
     float *const s_top = s_l + CW * HC, *const s_sum = s_top + HC;                    // [HC]
     uint64_t *const s_bar = reinterpret_cast<uint64_t *>(s_sum + HC);
@@ -429,7 +843,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) attend_mma_kernel(const AttendA
         ptx::fence_mbar_init();
     }
     plan_places(a, TT, places_at, s_warp);
-    Walk w(a, places_at, HC, TT);
+    Walk w(a, places_at, HC, TT, MIN_TILES);
     const int cta = blockIdx.x;
     if (cta >= w.ctas) return;
     w.open(cta);
@@ -466,9 +880,10 @@ __global__ void __launch_bounds__(AT_THREADS, 2) attend_mma_kernel(const AttendA
                 if (warp == 0) {
                     if (!wait_bar(q_empty(qst), qph, s_abort)) break;
                     const int h0 = hk * a.group + z * HC, nh = min(HC, a.group - z * HC);
-                    const __nv_bfloat16 *q = reinterpret_cast<const __nv_bfloat16 *>(a.q) + r * a.q_stride + (long long)h0 * D;
-                    for (int i = lane; i < nh * D / 8; i += 32)
-                        copy16(ptx::smem_u32(s_q + qst * S::Q_BYTES) + i * 16, q + i * 8, true);
+                    constexpr int QE = 16 / sizeof(IO);
+                    const IO *q = reinterpret_cast<const IO *>(a.q) + r * a.q_stride + (long long)h0 * D;
+                    for (int i = lane; i < nh * D / QE; i += 32)
+                        copy16(ptx::smem_u32(s_q + qst * S::Q_BYTES) + i * 16, q + i * QE, true);
                     copies_arrive(q_full(qst));
                 }
                 if (++qst == QS) qst = 0, qph ^= 1;
@@ -498,38 +913,43 @@ __global__ void __launch_bounds__(AT_THREADS, 2) attend_mma_kernel(const AttendA
                             gone = true;
                             break;
                         }
-                        const unsigned ok = TT == 32 ? all : all >> (m * 16) & 0xffffu;
-                        const uint32_t kd = ptx::smem_u32(s_ring + (size_t)st * S::STAGE), vd = kd + TT * S::ROW;
-                        constexpr int LR = S::ROW / 16, RI = 32 / LR;      // lanes of a row, rows of an instruction
-                        const int piece = lane % LR, row0 = lane / LR;
-                        const bool in_row = piece * 16 < row_bytes;
+                        const unsigned ok = all >> (m * TT) & ALL;
+                        const uint32_t kd = ptx::smem_u32(s_ring + (size_t)st * S::STAGE), vd = kd + TT * M::ROW;
+                        // lanes of a row, rows of an instruction, and its instructions where it is longer
+                        constexpr int LR = M::ROW >= 512 ? 32 : M::ROW / 16, RI = 32 / LR, CS = M::ROW / 16 / LR;
+                        const int row0 = lane / LR;
                         // a tile inside one page steps by the token's stride
                         const long long place0 = __shfl_sync(0xffffffffu, place, m * TT);
                         const bool one_page = __all_sync(
                             0xffffffffu, lane / TT != m || i >= stop || place == place0 + (lane - m * TT) * tok_bytes);
-                        if (one_page) {
-                            const int rows = place0 >= 0 ? min(TT, stop - (pos + k * 32 + m * TT)) : 0;
-                            const long long from = place0 >= 0 ? place0 + row0 * tok_bytes + piece * 16 : 0;
-                            const char *ks = kb + from, *vs = vb + from;
 #pragma unroll
-                            for (int n = 0; n < TT / RI; ++n) {
-                                const int row = n * RI + row0;
-                                const bool real = in_row && row < rows;
-                                const uint32_t to = S::place(row, piece);
-                                copy16(kd + to, real ? ks : kb, real);
-                                copy16(vd + to, real ? vs : vb, real);
-                                ks += RI * tok_bytes;
-                                vs += RI * tok_bytes;
-                            }
-                        } else {
+                        for (int cs = 0; cs < CS; ++cs) {
+                            const int piece = cs * LR + lane % LR;
+                            const bool in_row = piece * 16 < row_bytes;
+                            if (one_page) {
+                                const int rows = place0 >= 0 ? min(TT, stop - (pos + k * 32 + m * TT)) : 0;
+                                const long long from = place0 >= 0 ? place0 + row0 * tok_bytes + piece * 16 : 0;
+                                const char *ks = kb + from, *vs = vb + from;
 #pragma unroll
-                            for (int n = 0; n < TT / RI; ++n) {
-                                const int row = n * RI + row0;
-                                const long long p = __shfl_sync(0xffffffffu, place, m * TT + row);
-                                const bool real = in_row && p >= 0;
-                                const uint32_t to = S::place(row, piece);
-                                copy16(kd + to, real ? kb + p + piece * 16 : kb, real);
-                                copy16(vd + to, real ? vb + p + piece * 16 : vb, real);
+                                for (int n = 0; n < TT / RI; ++n) {
+                                    const int row = n * RI + row0;
+                                    const bool real = in_row && row < rows;
+                                    const uint32_t to = place_of<M::ROW>(row, piece);
+                                    copy16(kd + to, real ? ks : kb, real);
+                                    copy16(vd + to, real ? vs : vb, real);
+                                    ks += RI * tok_bytes;
+                                    vs += RI * tok_bytes;
+                                }
+                            } else {
+#pragma unroll
+                                for (int n = 0; n < TT / RI; ++n) {
+                                    const int row = n * RI + row0;
+                                    const long long p = __shfl_sync(0xffffffffu, place, m * TT + row);
+                                    const bool real = in_row && p >= 0;
+                                    const uint32_t to = place_of<M::ROW>(row, piece);
+                                    copy16(kd + to, real ? kb + p + piece * 16 : kb, real);
+                                    copy16(vd + to, real ? vb + p + piece * 16 : vb, real);
+                                }
                             }
                         }
                         copies_arrive(full(st));
@@ -558,277 +978,43 @@ __global__ void __launch_bounds__(AT_THREADS, 2) attend_mma_kernel(const AttendA
     }
 
     // ---------------------------------------------------- the warps that compute
-    const int cw = warp - PW, t = threadIdx.x - 32 * PW, g = lane >> 2, c = lane & 3;
+    const int cw = warp - PW, t = threadIdx.x - 32 * PW;
     int st = cw, qst = 0;                   // this warp's next stage, the next row's queries
     unsigned ph = 0, qph = 0, seq = 0;      // tiles of the CTA so far
     // what the end joins: the rows that began before this range, and go on behind it
-    struct Shared {
-        int r, hk, h0, nh, c0, c1;
-    } head = {-1}, tail = {-1};
+    SharedRow head = {-1}, tail = {-1};
+    M math(lane, ptx::smem_u32(s_p + cw * M::P_BYTES));
     for (; w.more(); w.next()) {
         const int h0 = w.hk * a.group + w.z * HC, nh = min(HC, a.group - w.z * HC);
         const int tiles = w.to() > w.from() ? (w.to() - w.from() + TT - 1) / TT : 0;
-
-        float o[NT][VP][OT][4] = {};
-        float top[NT][2], sum[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = -INFINITY, sum[nt][0] = sum[nt][1] = 0.f;
-
+        math.reset();
         if (tiles) {
-            // queries: the fragments' elements are those of the keys' pieces
-            uint32_t qf[NT][KP][KE / 2];
-            float mul[NT][2];         // product to score, per head of this lane's columns
-            const float ks = a.kv.k_scale ? a.kv.k_scale[w.hk] : 1.f;
+            const float scale = (a.kv.k_scale ? a.kv.k_scale[w.hk] : 1.f) * a.scale;
             wait_bar(q_full(qst), qph, s_abort);
-            const uint32_t qs = ptx::smem_u32(s_q + qst * S::Q_BYTES);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int h = nt * 8 + g;
-#pragma unroll
-                for (int p = 0; p < KP; ++p)
-#pragma unroll
-                    for (int e = 0; e < KE / 8; ++e) {
-                        const int d = (p * 4 + c) * KE + e * 8;
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (h < nh && d < D) x = lds16(qs + (h * D + d) * 2);
-                        qf[nt][p][e * 4 + 0] = x.x;
-                        qf[nt][p][e * 4 + 1] = x.y;
-                        qf[nt][p][e * 4 + 2] = x.z;
-                        qf[nt][p][e * 4 + 3] = x.w;
-                    }
-                float back = 1.f;
-                if constexpr (FP8) {
-                    // 16-bit halves have 11 bits where bf16 has 8: scaled by a power of
-                    // two that takes the head's largest element below 2^8, every element
-                    // down to 2^-22 of it stays exact
-                    float big = 0.f;
-#pragma unroll
-                    for (int p = 0; p < KP; ++p)
-#pragma unroll
-                        for (int e = 0; e < KE / 2; ++e) {
-                            const uint32_t w = qf[nt][p][e];
-                            big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))));
-                        }
-                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                    int ex = 0;
-                    if (big > 0.f && big < INFINITY) frexpf(big, &ex);
-                    ex = max(-100, min(100, ex - 8));
-                    const float down = ldexpf(1.f, -ex);
-                    back = ldexpf(1.f, ex);
-#pragma unroll
-                    for (int p = 0; p < KP; ++p)
-#pragma unroll
-                        for (int e = 0; e < KE / 2; ++e) {
-                            const uint32_t w = qf[nt][p][e];
-                            qf[nt][p][e] = pack_f16(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down);
-                        }
-                }
-                mul[nt][0] = __shfl_sync(0xffffffffu, back, (2 * c) * 4) * ks * a.scale;
-                mul[nt][1] = __shfl_sync(0xffffffffu, back, (2 * c + 1) * 4) * ks * a.scale;
-                if (!(a.softcap > 0.f)) mul[nt][0] *= LOG2E, mul[nt][1] *= LOG2E;
-            }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(q_empty(qst));
-            if (++qst == QS) qst = 0, qph ^= 1;
-
+            math.queries(ptx::smem_u32(s_q + qst * S::Q_BYTES), nh, D, a.softcap > 0.f ? scale : scale * LOG2E);
             // tile n of the CTA is warp n mod CW's, and the ring a multiple of CW
             // long: a stage has one reader for good, which has seen every earlier
             // filling of it, so that the parity it waits for is never ambiguous
             for (unsigned n = seq + ((unsigned)(cw - (int)(seq % CW) + CW) % CW); n < seq + tiles; n += CW) {
                 wait_bar(full(st), ph, s_abort);
                 const unsigned ok = *(volatile unsigned *)(s_ok + st);
-                const uint32_t kd = ptx::smem_u32(s_ring + (size_t)st * S::STAGE), vd = kd + TT * S::ROW;
-
-                float sc[MT][NT][4] = {};
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int j = 0; j < KP; ++j) {
-                        const uint4 x = lds16(kd + S::place(m * 16 + g, j * 4 + c));
-                        const uint4 y = lds16(kd + S::place(m * 16 + g + 8, j * 4 + c));
-                        const uint32_t w0[4] = {x.x, x.y, x.z, x.w}, w1[4] = {y.x, y.y, y.z, y.w};
-                        if constexpr (FP8) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t a0 = e4m3x2_f16x2(w0[e]), a2 = e4m3x2_f16x2(w0[e] >> 16);
-                                const uint32_t a1 = e4m3x2_f16x2(w1[e]), a3 = e4m3x2_f16x2(w1[e] >> 16);
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    mma16816<true>(sc[m][nt], a0, a1, a2, a3, qf[nt][j][2 * e], qf[nt][j][2 * e + 1]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    mma16816<false>(sc[m][nt], w0[2 * e], w1[2 * e], w0[2 * e + 1], w1[2 * e + 1],
-                                                    qf[nt][j][2 * e], qf[nt][j][2 * e + 1]);
-                        }
-                    }
-                uint32_t vr[MT][4][VP][VW];
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int tok = m * 16 + 2 * c + (k & 1) + (k >> 1) * 8;
-#pragma unroll
-                        for (int j = 0; j < VP; ++j) {
-                            if constexpr (VW == 4) {
-                                const uint4 x = lds16(vd + S::place(tok, j * 8 + g));
-                                vr[m][k][j][0] = x.x, vr[m][k][j][1] = x.y, vr[m][k][j][2] = x.z, vr[m][k][j][3] = x.w;
-                            } else {
-                                const uint2 x = lds8(vd + S::place(tok, g >> 1) + (g & 1) * 8);
-                                vr[m][k][j][0] = x.x, vr[m][k][j][1] = x.y;
-                            }
-                        }
-                    }
-
-                // scores in powers of two; the reference of the weights moves only
-                // when a score passes it by more than 2^8, so that the outputs are
-                // seldom scaled (weights are then at most 2^8, exact in any type here)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            float x = sc[m][nt][k] * mul[nt][k & 1];
-                            if (a.softcap > 0.f) x = a.softcap * LOG2E * tanhf(x / a.softcap);
-                            if (!(ok >> (m * 16 + (k >> 1) * 8 + g) & 1)) x = -INFINITY;
-                            sc[m][nt][k] = x;
-                            mx[k & 1] = fmaxf(mx[k & 1], x);
-                        }
-                    if (__any_sync(0xffffffffu, mx[0] > top[nt][0] + 8.f || mx[1] > top[nt][1] + 8.f)) {
-                        float al[2];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            float x = mx[k];
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                            x = fmaxf(x, top[nt][k]);
-                            al[k] = x == top[nt][k] ? 1.f : exp2f(top[nt][k] - x);
-                            top[nt][k] = x;
-                            sum[nt][k] *= al[k];
-                        }
-#pragma unroll
-                        for (int j = 0; j < VP; ++j)
-#pragma unroll
-                            for (int k = 0; k < OT; ++k) {
-                                o[nt][j][k][0] *= al[0];
-                                o[nt][j][k][1] *= al[1];
-                                o[nt][j][k][2] *= al[0];
-                                o[nt][j][k][3] *= al[1];
-                            }
-                    }
-                }
-                uint32_t pf[MT][NT][2][2];            // [tokens 0-7, 8-15][weights, what their rounding left]
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float ref[2] = {top[nt][0] == -INFINITY ? 0.f : top[nt][0],
-                                          top[nt][1] == -INFINITY ? 0.f : top[nt][1]};
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        float p[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            p[k] = exp2f(sc[m][nt][k] - ref[k & 1]);
-                            sum[nt][k & 1] += p[k];
-                        }
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            if constexpr (FP8) {
-                                pf[m][nt][k][0] = transpose8(pack_f16(p[2 * k], p[2 * k + 1]));
-                            } else {
-                                // bf16 keeps 8 bits of a weight: a second product takes the rest
-                                const uint32_t hi = pack_bf16(p[2 * k], p[2 * k + 1]);
-                                const float r0 = p[2 * k] - __uint_as_float(hi << 16);
-                                const float r1 = p[2 * k + 1] - __uint_as_float(hi & 0xffff0000u);
-                                pf[m][nt][k][0] = transpose8(hi);
-                                pf[m][nt][k][1] = transpose8(pack_bf16(r0, r1));
-                            }
-                        }
-                    }
-                }
-                // the stage's values are in registers: it may be filled again
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(empty(st));
+                const uint32_t kd = ptx::smem_u32(s_ring + (size_t)st * S::STAGE);
+                math.tile(kd, kd + TT * M::ROW, ok, a.softcap, [&] {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(empty(st));
+                });
                 if ((st += CW) >= stages) st = cw, ph ^= 1;
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int j = 0; j < VP; ++j)
-#pragma unroll
-                        for (int i = 0; i < VW; ++i) {
-                            const uint32_t x0 = vr[m][0][j][i], x1 = vr[m][1][j][i];
-                            const uint32_t x2 = vr[m][2][j][i], x3 = vr[m][3][j][i];
-                            if constexpr (FP8) {
-                                const uint32_t y0 = __byte_perm(x0, x1, 0x5140), y1 = __byte_perm(x0, x1, 0x7362);
-                                const uint32_t y2 = __byte_perm(x2, x3, 0x5140), y3 = __byte_perm(x2, x3, 0x7362);
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const uint32_t ya = k ? y1 : y0, yb = k ? y3 : y2;
-                                    const uint32_t a0 = e4m3x2_f16x2(ya), a1 = e4m3x2_f16x2(ya >> 16);
-                                    const uint32_t a2 = e4m3x2_f16x2(yb), a3 = e4m3x2_f16x2(yb >> 16);
-#pragma unroll
-                                    for (int nt = 0; nt < NT; ++nt)
-                                        mma16816<true>(o[nt][j][2 * i + k], a0, a1, a2, a3, pf[m][nt][0][0],
-                                                       pf[m][nt][1][0]);
-                                }
-                            } else {
-                                const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
-                                const uint32_t a2 = __byte_perm(x2, x3, 0x5410), a3 = __byte_perm(x2, x3, 0x7632);
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    mma16816<false>(o[nt][j][i], a0, a1, a2, a3, pf[m][nt][0][0], pf[m][nt][1][0]);
-                                    mma16816<false>(o[nt][j][i], a0, a1, a2, a3, pf[m][nt][0][1], pf[m][nt][1][1]);
-                                }
-                            }
-                        }
             }
             seq += tiles;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(q_empty(qst));
+            if (++qst == QS) qst = 0, qph ^= 1;
         }
 
         // the warps' shares of the row
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float x = sum[nt][i];
-                x += __shfl_xor_sync(0xffffffffu, x, 4);
-                x += __shfl_xor_sync(0xffffffffu, x, 8);
-                x += __shfl_xor_sync(0xffffffffu, x, 16);
-                if (g == 0) {
-                    s_m[cw * HC + nt * 8 + 2 * c + i] = top[nt][i];
-                    s_l[cw * HC + nt * 8 + 2 * c + i] = x;
-                }
-            }
-        consumers_sync();
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float f[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int h = nt * 8 + 2 * c + i;
-                float m = -INFINITY;
-#pragma unroll
-                for (int x = 0; x < CW; ++x) m = fmaxf(m, s_m[x * HC + h]);
-                f[i] = m > -INFINITY ? exp2f(top[nt][i] - m) : 0.f;
-            }
-            float *p0 = s_o + (cw * HC + nt * 8 + 2 * c) * S::O_LD, *p1 = p0 + S::O_LD;
-#pragma unroll
-            for (int j = 0; j < VP; ++j)
-#pragma unroll
-                for (int i = 0; i < OT; i += 2) {
-                    const int d = (j * 8 + g) * VE + 2 * i;
-                    *reinterpret_cast<float4 *>(p0 + d) = make_float4(o[nt][j][i][0] * f[0], o[nt][j][i][2] * f[0],
-                                                                      o[nt][j][i + 1][0] * f[0], o[nt][j][i + 1][2] * f[0]);
-                    *reinterpret_cast<float4 *>(p1 + d) = make_float4(o[nt][j][i][1] * f[1], o[nt][j][i][3] * f[1],
-                                                                      o[nt][j][i + 1][1] * f[1], o[nt][j][i + 1][3] * f[1]);
-                }
-        }
+        math.stats(s_m + cw * HC, s_l + cw * HC);
+        sync_threads<CW * 32>();
+        math.template finish<CW>(s_m, s_o + cw * HC * S::O_LD, S::O_LD);
         if (t < HC) {
             float m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -839,8 +1025,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) attend_mma_kernel(const AttendA
             s_top[t] = m;
             s_sum[t] = l;
         }
-        consumers_sync();
-
+        sync_threads<CW * 32>();
         auto merged = [&](int h, int d) {
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -854,7 +1039,7 @@ __global__ void __launch_bounds__(AT_THREADS, 2) attend_mma_kernel(const AttendA
             const float vs = a.kv.v_scale ? a.kv.v_scale[w.hk] : 1.f;
             for (int i = t; i < nh * (D / 4); i += CW * 32) {
                 const int h = i / (D / 4), d = 4 * (i - h * (D / 4));
-                put(a, w.r, h0 + h, d, merged(h, d), s_sum[h] > 0.f ? vs / s_sum[h] : 0.f);
+                put<IO>(a, w.r, h0 + h, d, merged(h, d), s_sum[h] == 0.f ? 0.f : vs / s_sum[h]);
             }
             if (a.lse && t < nh) a.lse[(long long)w.r * a.q_heads + h0 + t] = (s_top[t] + log2f(s_sum[t])) * LN2;
         } else {
@@ -864,16 +1049,16 @@ __global__ void __launch_bounds__(AT_THREADS, 2) attend_mma_kernel(const AttendA
                 *reinterpret_cast<float4 *>(p.o + h * D + d) = merged(h, d);
             }
             if (t < nh) p.m[t] = s_top[t], p.l[t] = s_sum[t];
-            (w.t0 == 0 ? tail : head) = Shared{w.r, w.hk, h0, nh, w.first_owner(), w.last_owner()};
+            (w.t0 == 0 ? tail : head) = SharedRow{w.r, w.hk, h0, nh, w.first_owner(), w.last_owner()};
         }
     }
 
     // arrive at the shared rows; the last to arrive joins
     if (head.r < 0 && tail.r < 0) return;
     __threadfence();
-    consumers_sync();
+    sync_threads<CW * 32>();
     if (t < 2) {
-        const Shared &row = t ? tail : head;
+        const SharedRow &row = t ? tail : head;
         int last = 0;
         if (row.r >= 0) {
             last = atomicAdd(a.ctr + row.c0, 1) == row.c1 - row.c0;
@@ -881,89 +1066,67 @@ __global__ void __launch_bounds__(AT_THREADS, 2) attend_mma_kernel(const AttendA
         }
         s_last[t] = last;
     }
-    consumers_sync();
+    sync_threads<CW * 32>();
     __threadfence();
-    for (int which = 0; which < 2; ++which) {
-        if (!s_last[which]) continue;
-        const Shared row = which ? tail : head;
-        const int parts = row.c1 - row.c0 + 1;
-        auto slot = [&](int i) { return i == 0 ? 2 * row.c0 + 1 : 2 * (row.c0 + i); };
-        consumers_sync();
-        for (int h = cw; h < row.nh; h += CW) {
-            float m = -INFINITY;
-            for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(part_of(a, slot(i)).m + h));
-#pragma unroll
-            for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-            float l = 0.f;
-            if (m > -INFINITY)
-                for (int i = lane; i < parts; i += 32) {
-                    const PartView q = part_of(a, slot(i));
-                    l += __ldcg(q.l + h) * exp2f(__ldcg(q.m + h) - m);
-                }
-#pragma unroll
-            for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-            if (lane == 0) s_top[h] = m, s_sum[h] = l;
-        }
-        consumers_sync();
-        const float vs = a.kv.v_scale ? a.kv.v_scale[row.hk] : 1.f;
-        for (int i = t; i < row.nh * (D / 4); i += CW * 32) {
-            const int h = i / (D / 4), d = 4 * (i - h * (D / 4));
-            const float m = s_top[h];
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (m > -INFINITY)
-#pragma unroll 8
-                for (int k = 0; k < parts; ++k) {
-                    const PartView q = part_of(a, slot(k));
-                    const float f = exp2f(__ldcg(q.m + h) - m);
-                    const float4 y = __ldcg(reinterpret_cast<const float4 *>(q.o + h * D + d));
-                    x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
-                }
-            put(a, row.r, row.h0 + h, d, x, s_sum[h] > 0.f ? vs / s_sum[h] : 0.f);
-        }
-        if (a.lse && t < row.nh) a.lse[(long long)row.r * a.q_heads + row.h0 + t] = (s_top[t] + log2f(s_sum[t])) * LN2;
-    }
+    const int n_head = s_last[0] ? head.nh * (D / 4) : 0, n_tail = s_last[1] ? tail.nh * (D / 4) : 0;
+    const int most = max(n_head ? head.c1 - head.c0 : 0, n_tail ? tail.c1 - tail.c0 : 0) + 1;
+    // few long rows have many parts, many rows have few
+    if (most > 4) join_parts<IO, 1, 16, CW * 32>(a, head, tail, n_head, n_tail, t);
+    else join_parts<IO, 4, 4, CW * 32>(a, head, tail, n_head, n_tail, t);
 }
 
-template <bool FP8, int DC, int NT>
-cudaError_t launch_mma(const AttendArgs &a, int num_sms, cudaStream_t st) {
-    using S = Shape<FP8, DC, NT>;
+template <typename M, int DC, int CW, int PW, int CTAS>
+cudaError_t launch_shape(const AttendArgs &a, int num_sms, cudaStream_t st) {
+    using S = Shape<M, DC, CW, PW, CTAS>;
+    static_assert(CTAS <= ATT_CTAS, "workspace");
     static std::atomic<unsigned long long> done{0};
-    const cudaError_t e = allow_max_dynamic_smem(attend_mma_kernel<FP8, DC, NT>, done);
+    const auto kernel = attend_kernel<M, DC, CW, PW, CTAS>;
+    const cudaError_t e = allow_max_dynamic_smem(kernel, done);
     if (e != cudaSuccess) return e;
-    // two CTAs on an SM, so that one streams while the other ends a row; one where
-    // a large batch's list leaves too little room for two rings
-    int per_sm = 2;
-    long long stages = (113 * 1024 - (long long)S::smem(0, a.n_req)) / S::STAGE / CW * CW;
-    if (stages < CW) {
-        per_sm = 1;
-        stages = (226 * 1024 - (long long)S::smem(0, a.n_req)) / S::STAGE / CW * CW;
+    // as many CTAs on an SM as its registers allow; fewer where a large batch's
+    // list leaves too little room for their rings
+    int per_sm = CTAS;
+    long long stages = 0;
+    for (; per_sm >= 1; --per_sm) {
+        stages = ((228 / per_sm - 1) * 1024 - (long long)S::smem(0, a.n_req)) / S::STAGE / CW * CW;
+        if (stages >= CW) break;
     }
-    if (stages > MAX_STAGES) stages = MAX_STAGES;
-    attend_mma_kernel<FP8, DC, NT>
-        <<<num_sms * per_sm, AT_THREADS, S::smem((int)stages, a.n_req), st>>>(a, (int)stages);
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    if (stages > MAX_STAGES) stages = MAX_STAGES / CW * CW;
+    kernel<<<num_sms * per_sm, S::THREADS, S::smem((int)stages, a.n_req), st>>>(a, (int)stages);
     return cudaGetLastError();
 }
 
 template <bool FP8>
-cudaError_t launch_by_dim(const AttendArgs &a, int num_sms, cudaStream_t st) {
+cudaError_t launch_mma(const AttendArgs &a, int num_sms, cudaStream_t st) {
     const int D = a.kv.dim;
-    if (D > 128) return launch_mma<FP8, 256, 1>(a, num_sms, st);
-    if (D > 64) return a.group > 8 ? launch_mma<FP8, 128, 2>(a, num_sms, st) : launch_mma<FP8, 128, 1>(a, num_sms, st);
-    return a.group > 8 ? launch_mma<FP8, 64, 2>(a, num_sms, st) : launch_mma<FP8, 64, 1>(a, num_sms, st);
+    const bool wide = a.group > 8;
+    if (D > 128) return launch_shape<MmaMath<FP8, 256, 1>, 256, 4, 2, 2>(a, num_sms, st);
+    if (D > 64)
+        return wide ? launch_shape<MmaMath<FP8, 128, 2>, 128, 4, 2, 2>(a, num_sms, st)
+                    : launch_shape<MmaMath<FP8, 128, 1>, 128, 2, 1, 4>(a, num_sms, st);
+    return wide ? launch_shape<MmaMath<FP8, 64, 2>, 64, 4, 2, 2>(a, num_sms, st)
+                : launch_shape<MmaMath<FP8, 64, 1>, 64, 2, 1, 4>(a, num_sms, st);
+}
+template <int DC, int CW, int PW, int CTAS>
+cudaError_t launch_fma(const AttendArgs &a, int num_sms, cudaStream_t st) {
+    if (a.group == 1) return launch_shape<FmaMath<DC, 1>, DC, CW, PW, CTAS>(a, num_sms, st);
+    if (a.group == 2) return launch_shape<FmaMath<DC, 2>, DC, CW, PW, CTAS>(a, num_sms, st);
+    if (a.group <= 4) return launch_shape<FmaMath<DC, 4>, DC, CW, PW, CTAS>(a, num_sms, st);
+    return launch_shape<FmaMath<DC, 8>, DC, CW, PW, CTAS>(a, num_sms, st);
 }
 
 }  // namespace
 
-constexpr int ATT_CTAS = 2;      // CTAs of an SM, at most
 size_t attend_part_floats(int num_sms) { return (size_t)num_sms * ATT_CTAS * 2 * PART_FLOATS; }
 int attend_ctrs(int num_sms) { return num_sms * ATT_CTAS; }
 
 cudaError_t launch_attend(const AttendArgs &a, int num_sms, cudaStream_t st) {
-    if (a.kv.dtype == KV_BF16) return launch_by_dim<false>(a, num_sms, st);
-    if (a.kv.dtype == KV_E4M3) return launch_by_dim<true>(a, num_sms, st);
-    const dim3 grid(a.n_req, a.kv.heads, (a.group + AT_HEADS - 1) / AT_HEADS);
-    attend_kernel<float, float><<<grid, 128, 0, st>>>(a);
-    return cudaGetLastError();
+    if (a.kv.dtype == KV_BF16) return launch_mma<false>(a, num_sms, st);
+    if (a.kv.dtype == KV_E4M3) return launch_mma<true>(a, num_sms, st);
+    if (a.kv.dim <= 64) return launch_fma<64, 2, 1, 4>(a, num_sms, st);
+    if (a.kv.dim <= 128) return launch_fma<128, 2, 1, 4>(a, num_sms, st);
+    return launch_fma<256, 4, 2, 2>(a, num_sms, st);
 }
 
 }  // namespace scute

@@ -196,7 +196,7 @@ scute_status scute_paged_attention(scute_ctx *c, const scute_kv_cache *kv, const
         return fail(c, SCUTE_ERR_SHAPE, "q or out stride is below a row or not a multiple of 16 bytes");
     if (kv->table_cols < 1 || kv->table_stride < kv->table_cols ||
         (int64_t)kv->table_cols * kv->page_size > (1 << 30) ||
-        (int64_t)kv->table_cols * kv->page_size * t->n_req > (1ll << 34))
+        (int64_t)kv->table_cols * kv->page_size * t->n_req > (1ll << 33))
         return fail(c, SCUTE_ERR_SHAPE, "block table of %d columns, row pitch %lld", kv->table_cols,
                     (long long)kv->table_stride);
     if (!std::isfinite(t->scale) || !std::isfinite(t->softcap) || t->softcap < 0.f || t->window < 0)
