@@ -107,15 +107,22 @@ template <> struct Vec<__nv_bfloat16> {
 };
 
 // The row in registers: a row's threads hold NV 16-byte vectors each.  WARP: a
-// warp for a row and shuffles alone; otherwise a CTA for a row.
-template <typename T, int NV, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 1024) residual_norm_vec_kernel(const NormArgs a) {
+// warp for a row and shuffles alone; otherwise a CTA for a row.  The launch has
+// as many CTAs as reside, and each fetches its next row before it is done with
+// the one it has (rows that fill the registers: after).  FULL: with means taken
+// off or biases.  HELD: a thread keeps its columns' factors from row to row, post_w,
+// the gate and the scale as one; fetched anew for every row they are half of all
+// that passes through L1.
+template <typename T, int NV, bool WARP, bool FULL, bool HELD>
+__global__ void __launch_bounds__(WARP || HELD ? 256 : 1024, HELD ? (FULL ? 2 : 3) : 1)
+    residual_norm_vec_kernel(const NormArgs a) {
     constexpr int VE = Vec<T>::N;
+    constexpr bool AHEAD = NV <= 2;
     __shared__ float red[2][32];
     const int d = a.d, nvec = d / VE;
     const int per_row = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
-    const long long r = WARP ? (long long)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
-    if (WARP && r >= a.n) return;
+    const int step = WARP ? gridDim.x * 8 : gridDim.x;
+    const float inv_d = 1.f / d;
     int turn = 0;
     auto row_sum = [&](float x) -> float {
 #pragma unroll
@@ -125,96 +132,159 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024) residual_norm_vec_kernel(co
         if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = x;
         __syncthreads();
         const int warps = blockDim.x >> 5;
-        float s = (threadIdx.x & 31) < warps ? red[turn][threadIdx.x & 31] : 0.f;
+        float s = 0.f;
+        if (HELD) {           // eight warps at most
+            for (int w = 0; w < warps; ++w) s += red[turn][w];
+        } else {
+            s = (threadIdx.x & 31) < warps ? red[turn][threadIdx.x & 31] : 0.f;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        }
         turn ^= 1;
         return s;
     };
-    float x[NV][VE];
-    uint4 res[NV];             // as stored, until it is added
-    const T *y = reinterpret_cast<const T *>(a.y) + r * a.y_stride;
-    const T *rs = reinterpret_cast<const T *>(a.residual) + r * a.residual_stride;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int i = v * per_row + t;
-        uint4 in = make_uint4(0, 0, 0, 0);
-        res[v] = in;
-        if (i < nvec) {
-            in = *reinterpret_cast<const uint4 *>(y + i * VE);
-            if (a.residual) res[v] = *reinterpret_cast<const uint4 *>(rs + i * VE);
-        }
-        Vec<T>::open(in, x[v]);
-    }
-    // (mean, 1 / deviation); the squares are summed after the mean is taken off
-    auto stats = [&](float *mean, float *rstd) {
-        float m = 0.f, q = 0.f;
-        if (a.layer) {
-#pragma unroll
-            for (int v = 0; v < NV; ++v)
-#pragma unroll
-                for (int e = 0; e < VE; ++e) m += x[v][e];
-            m = row_sum(m) / d;
-        }
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (v * per_row + t < nvec)
-#pragma unroll
-                for (int e = 0; e < VE; ++e) q += (x[v][e] - m) * (x[v][e] - m);
-        *mean = m;
-        *rstd = rsqrtf(row_sum(q) / d + a.eps);
-    };
-    auto affine = [&](float *z, const float *w, const float *b, int at, float mean, float rstd) {
+    // a vector's factors and terms: y's with the gate and the scale, and h's
+    auto y_factors = [&](int at, float *cw, float *cb) {
         float f[4];
 #pragma unroll
         for (int e = 0; e < VE; e += 4) {
-            if (w) Vec<float>::load(w + at + e, f);
-            else f[0] = f[1] = f[2] = f[3] = 1.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[e + i] = (z[e + i] - mean) * rstd * f[i];
-            if (b) {
-                Vec<float>::load(b + at + e, f);
+            for (int k = 0; k < 4; ++k) f[k] = a.scale;
+            if (a.gate_vec) {
+                Vec<float>::load(a.gate_vec + at + e, f);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) z[e + i] += f[i];
+                for (int k = 0; k < 4; ++k) f[k] *= a.scale;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) cw[e + k] = f[k];
+            if (FULL) {
+                float g[4] = {0.f, 0.f, 0.f, 0.f};
+                if (a.post_b) Vec<float>::load(a.post_b + at + e, g);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) cb[e + k] = g[k] * f[k];
+            }
+            if (a.post_w) {
+                Vec<float>::load(a.post_w + at + e, f);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) cw[e + k] *= f[k];
             }
         }
     };
-    float mean = 0.f, rstd = 1.f;
-    if (a.post_w) stats(&mean, &rstd);
+    auto h_factors = [&](int at, float *pw, float *pb) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int i = v * per_row + t;
-        if (i >= nvec) continue;
-        if (a.post_w) affine(x[v], a.post_w, a.post_b, i * VE, mean, rstd);
-        if (a.gate_vec) {
-            float f[4];
+        for (int e = 0; e < VE; e += 4) {
 #pragma unroll
-            for (int e = 0; e < VE; e += 4) {
-                Vec<float>::load(a.gate_vec + i * VE + e, f);
+            for (int k = 0; k < 4; ++k) pw[e + k] = 1.f;
+            if (a.pre_w) Vec<float>::load(a.pre_w + at + e, pw + e);
+            if (FULL) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[v][e + k] *= f[k];
+                for (int k = 0; k < 4; ++k) pb[e + k] = 0.f;
+                if (a.pre_b) Vec<float>::load(a.pre_b + at + e, pb + e);
             }
-        } else if (a.gate_rows) {
-            float f[VE];
-            Vec<T>::load(reinterpret_cast<const T *>(a.gate_rows) + r * a.gate_stride + i * VE, f);
-#pragma unroll
-            for (int e = 0; e < VE; ++e) x[v][e] *= f[e];
         }
-        float old[VE];
-        Vec<T>::open(res[v], old);
+    };
+    constexpr int HV = HELD ? NV : 1, HF = HELD && FULL ? NV : 1;
+    float cw[HV][VE], pw[HV][VE], cb[HF][VE], pb[HF][VE];
+    if (HELD)
 #pragma unroll
-        for (int e = 0; e < VE; ++e) x[v][e] = fmaf(a.scale, x[v][e], old[e]);
-        if (a.residual_out)
-            Vec<T>::store(reinterpret_cast<T *>(a.residual_out) + r * a.residual_out_stride + i * VE, x[v]);
-    }
-    if (!a.out) return;
-    stats(&mean, &rstd);
+        for (int v = 0; v < NV; ++v)
+            if (v * per_row + t < nvec) {
+                y_factors((v * per_row + t) * VE, cw[v], cb[FULL ? v : 0]);
+                h_factors((v * per_row + t) * VE, pw[v], pb[FULL ? v : 0]);
+            }
+
+    uint4 y_in[NV], r_in[NV];          // the next row, as stored
+    auto fetch = [&](long long r) {
+        const T *y = reinterpret_cast<const T *>(a.y) + r * a.y_stride;
+        const T *rs = reinterpret_cast<const T *>(a.residual) + r * a.residual_stride;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int i = v * per_row + t;
-        if (i >= nvec) continue;
-        affine(x[v], a.pre_w, a.pre_b, i * VE, mean, rstd);
-        Vec<T>::store(reinterpret_cast<T *>(a.out) + r * a.out_stride + i * VE, x[v]);
+        for (int v = 0; v < NV; ++v) {
+            const int i = v * per_row + t;
+            y_in[v] = r_in[v] = make_uint4(0, 0, 0, 0);
+            if (i < nvec) {
+                y_in[v] = *reinterpret_cast<const uint4 *>(y + i * VE);
+                if (a.residual) r_in[v] = *reinterpret_cast<const uint4 *>(rs + i * VE);
+            }
+        }
+    };
+    long long r = WARP ? (long long)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
+    if (r < a.n) fetch(r);
+    for (; r < a.n; r += step) {
+        float x[NV][VE];
+        uint4 res[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            Vec<T>::open(y_in[v], x[v]);
+            res[v] = r_in[v];
+        }
+        if (AHEAD && r + step < a.n) fetch(r + step);
+        // (mean, 1 / deviation); the squares are summed after the mean is taken off
+        auto stats = [&](float *mean, float *rstd) {
+            float m = 0.f, q = 0.f;
+            if (FULL && a.layer) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) m += x[v][e];
+                m = row_sum(m) * inv_d;
+            }
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                if (!FULL || v * per_row + t < nvec)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        const float z = FULL ? x[v][e] - m : x[v][e];
+                        q = fmaf(z, z, q);
+                    }
+            *mean = m;
+            *rstd = rsqrtf(row_sum(q) * inv_d + a.eps);
+        };
+        float mean = 0.f, rstd = 1.f;
+        if (a.post_w) stats(&mean, &rstd);
+        float mw[VE], mb[VE];                      // where they are not held
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int i = v * per_row + t;
+            if (i >= nvec) continue;
+            if (!HELD) y_factors(i * VE, mw, mb);
+            const float *fw = HELD ? cw[HELD ? v : 0] : mw, *fb = HELD ? cb[HF > 1 ? v : 0] : mb;
+            float old[VE], gate[VE];
+            Vec<T>::open(res[v], old);
+            if (a.gate_rows) {
+                Vec<T>::load(reinterpret_cast<const T *>(a.gate_rows) + r * a.gate_stride + i * VE, gate);
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    float z = (FULL ? x[v][e] - mean : x[v][e]) * rstd * fw[e];
+                    if (FULL) z += fb[e];
+                    x[v][e] = fmaf(z, gate[e], old[e]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    const float z = (FULL ? x[v][e] - mean : x[v][e]) * rstd;
+                    x[v][e] = fmaf(z, fw[e], FULL ? fb[e] + old[e] : old[e]);
+                }
+            }
+            if (a.residual_out)
+                Vec<T>::store(reinterpret_cast<T *>(a.residual_out) + r * a.residual_out_stride + i * VE, x[v]);
+        }
+        if (a.out) {
+            stats(&mean, &rstd);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int i = v * per_row + t;
+                if (i >= nvec) continue;
+                if (!HELD) h_factors(i * VE, mw, mb);
+                const float *fw = HELD ? pw[HELD ? v : 0] : mw, *fb = HELD ? pb[HF > 1 ? v : 0] : mb;
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    const float z = (FULL ? x[v][e] - mean : x[v][e]) * rstd;
+                    x[v][e] = FULL ? fmaf(z, fw[e], fb[e]) : z * fw[e];
+                }
+                Vec<T>::store(reinterpret_cast<T *>(a.out) + r * a.out_stride + i * VE, x[v]);
+            }
+        }
+        if (!AHEAD && r + step < a.n) fetch(r + step);
     }
 }
 
@@ -233,21 +303,41 @@ bool by_vectors(const NormArgs &a) {
     return (p & 15) == 0 && s == 0;
 }
 
+template <typename T, int NV, bool WARP, bool FULL, bool HELD>
+void launch_one(const NormArgs &a, int threads, int num_sms, cudaStream_t s) {
+    const auto kernel = residual_norm_vec_kernel<T, NV, WARP, FULL, HELD>;
+    // CTAs that reside on an SM at once, by its registers (looked up once) and threads
+    static const int regs = [&] {
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? (f.numRegs + 7) / 8 * 8 : 64;
+    }();
+    const int by_regs = 65536 / (regs * threads), by_threads = 2048 / threads;
+    const int per_sm = by_regs < 1 ? 1 : by_regs < by_threads ? by_regs : by_threads;
+    const long long rows = WARP ? (a.n + 7) / 8 : a.n, room = (long long)num_sms * per_sm;
+    kernel<<<(int)(rows < room ? rows : room), threads, 0, s>>>(a);
+}
+template <typename T, int NV, bool WARP, bool HELD>
+void launch_vec(const NormArgs &a, int threads, int num_sms, cudaStream_t s) {
+    if (a.layer || a.post_b || a.pre_b) launch_one<T, NV, WARP, true, HELD>(a, threads, num_sms, s);
+    else launch_one<T, NV, WARP, false, HELD>(a, threads, num_sms, s);
+}
+
 template <typename T>
 cudaError_t launch(const NormArgs &a, int num_sms, cudaStream_t s) {
     constexpr int VE = Vec<T>::N;
     if (by_vectors<T>(a)) {
         const int nvec = a.d / VE;
-        if (nvec <= 32) residual_norm_vec_kernel<T, 1, true><<<(a.n + 7) / 8, 256, 0, s>>>(a);
-        else if (nvec <= 64) residual_norm_vec_kernel<T, 2, true><<<(a.n + 7) / 8, 256, 0, s>>>(a);
-        else {
-            auto threads = [&](int nv) { return ((nvec + nv - 1) / nv + 31) / 32 * 32; };
-            const bool few = a.n <= num_sms;
-            if (threads(1) <= (few ? 1024 : 256)) residual_norm_vec_kernel<T, 1, false><<<a.n, threads(1), 0, s>>>(a);
-            else if (threads(2) <= (few ? 1024 : 512)) residual_norm_vec_kernel<T, 2, false><<<a.n, threads(2), 0, s>>>(a);
-            else if (threads(4) <= 1024) residual_norm_vec_kernel<T, 4, false><<<a.n, threads(4), 0, s>>>(a);
-            else if constexpr (VE == 4) residual_norm_vec_kernel<T, 8, false><<<a.n, threads(8), 0, s>>>(a);
-        }
+        auto threads = [&](int nv) { return ((nvec + nv - 1) / nv + 31) / 32 * 32; };
+        // a thread's factors are worth holding where it has several rows
+        const bool few = a.n <= num_sms, many = a.n >= 8 * num_sms;
+        if (nvec <= 32) launch_vec<T, 1, true, false>(a, 256, num_sms, s);
+        else if (nvec <= 64) launch_vec<T, 2, true, false>(a, 256, num_sms, s);
+        else if (many && threads(1) <= 256) launch_vec<T, 1, false, true>(a, threads(1), num_sms, s);
+        else if (many && threads(2) <= 256) launch_vec<T, 2, false, true>(a, threads(2), num_sms, s);
+        else if (threads(1) <= (few ? 1024 : 256)) launch_vec<T, 1, false, false>(a, threads(1), num_sms, s);
+        else if (threads(2) <= (few ? 1024 : 512)) launch_vec<T, 2, false, false>(a, threads(2), num_sms, s);
+        else if (threads(4) <= 1024) launch_vec<T, 4, false, false>(a, threads(4), num_sms, s);
+        else if constexpr (VE == 4) launch_vec<T, 8, false, false>(a, threads(8), num_sms, s);
         return cudaGetLastError();
     }
     static std::atomic<unsigned long long> done{0};
