@@ -370,6 +370,7 @@ struct KvView {
 struct ResizeArgs {
     const int32_t *len_in, *len_new;
     int n_req, cols, page_size;
+    int page_shift;            // log2 of the page size, or -1
     int32_t *table;
     long long table_stride;
     int32_t *free_pages;

@@ -24,10 +24,14 @@ namespace {
 // growing ones written behind their old pages, and list entries are written
 // only from F on.  So no thread waits for another, except that the lengths and
 // the count, which may be written in place, follow a launch-wide arrival count.
-constexpr int RS_THREADS = 512;
+constexpr int RS_THREADS = 1024;       // at most
 
-__device__ __forceinline__ int pages_of(int tokens, int page) {
-    return (int)(((long long)tokens + page - 1) / page);
+// Pages of so many tokens (at most 2^31 - 1 with a page's rounding); page of a position.
+__device__ __forceinline__ int page_index(const ResizeArgs &a, int pos) {
+    return a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
+}
+__device__ __forceinline__ int pages_of(const ResizeArgs &a, int tokens) {
+    return tokens == 0 ? 0 : page_index(a, tokens - 1) + 1;
 }
 
 // Last i in [0, n] with at[i] <= x, for at[0] = 0 <= x and at rising.
@@ -78,6 +82,8 @@ __device__ __forceinline__ Span span_of(const ResizeArgs &a, int r) {
     return s;
 }
 
+// ITEMS consecutive requests of a thread, held in registers.
+template <int ITEMS>
 __global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs a) {
     extern __shared__ int sm[];
     __shared__ unsigned long long warp_sum[RS_THREADS / 32];
@@ -85,67 +91,77 @@ __global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs 
     const int n = a.n_req, t = threadIdx.x;
     int *drop_at = sm, *need_at = sm + (n + 1), *cu = sm + 2 * (n + 1);
     if (t == 0) s_taken = s_rows = s_flag = 0;
-    const int per = (n + RS_THREADS - 1) / RS_THREADS;
-    const int r0 = min(n, t * per), r1 = min(n, r0 + per);
-
-    // pages given up and needed: one scan of both sums (each below 2^31)
-    unsigned long long mine = 0;
-    bool bad = false;
-    for (int r = r0; r < r1; ++r) {
-        const Span s = span_of(a, r);
-        bad |= s.bad;
-        const int have = pages_of(s.o, a.page_size), want = pages_of(s.w, a.page_size);
-        mine += (unsigned long long)(unsigned)max(have - want, 0) << 32 | (unsigned)max(want - have, 0);
-    }
-    unsigned long long total;
-    unsigned long long run = cta_exclusive(mine, warp_sum, &total);
-    const int P = (int)(total >> 32);
+    const int r0 = t * ITEMS;
     int F = *a.free_in;
+    Span sp[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        sp[i] = {0, 0, false};
+        if (r0 + i < n) sp[i] = span_of(a, r0 + i);
+    }
+    bool bad = false;
     if (F < 0 || F > a.n_free_max) {
         bad = true;
         F = F < 0 ? 0 : (int)a.n_free_max;
     }
+
+    // pages given up and needed: one scan of both sums (each below 2^31)
+    int need[ITEMS], drop[ITEMS];
+    unsigned long long mine = 0;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        bad |= sp[i].bad;
+        const int have = pages_of(a, sp[i].o), want = pages_of(a, sp[i].w);
+        need[i] = max(want - have, 0);
+        drop[i] = max(have - want, 0);
+        mine += (unsigned long long)(unsigned)drop[i] << 32 | (unsigned)need[i];
+    }
+    unsigned long long total;
+    unsigned long long run = cta_exclusive(mine, warp_sum, &total);
+    const int P = (int)(total >> 32);
     const long long L = (long long)F + P;
 
     // new tokens of the requests that get their pages
     unsigned long long rows = 0;
-    for (int r = r0; r < r1; ++r) {
-        const Span s = span_of(a, r);
-        const int have = pages_of(s.o, a.page_size), want = pages_of(s.w, a.page_size);
-        drop_at[r] = (int)(run >> 32);
-        need_at[r] = (int)(run & 0xffffffffu);
-        const int need = max(want - have, 0);
-        if (s.w > s.o && (need == 0 || need_at[r] + (long long)need <= L)) rows += s.w - s.o;
-        run += (unsigned long long)(unsigned)max(have - want, 0) << 32 | (unsigned)need;
+    int first_need = (int)(run & 0xffffffffu), at_need = first_need, at_drop = (int)(run >> 32);
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        if (r0 + i < n) drop_at[r0 + i] = at_drop, need_at[r0 + i] = at_need;
+        if (sp[i].w > sp[i].o && (need[i] == 0 || at_need + (long long)need[i] <= L)) rows += sp[i].w - sp[i].o;
+        at_drop += drop[i];
+        at_need += need[i];
     }
-    if (t == RS_THREADS - 1) {
-        drop_at[n] = (int)(total >> 32);
+    if (t == 0) {
+        drop_at[n] = P;
         need_at[n] = (int)(total & 0xffffffffu);
     }
     unsigned long long all_rows;
     unsigned long long at = cta_exclusive(rows, warp_sum, &all_rows);
-    int taken = 0, served = 0;
-    for (int r = r0; r < r1; ++r) {
-        const Span s = span_of(a, r);
-        const int need = max(pages_of(s.w, a.page_size) - pages_of(s.o, a.page_size), 0);
-        cu[r] = (int)min(at, (unsigned long long)a.max_new + 1);
-        if (s.w > s.o) {
-            const bool paged = need == 0 || need_at[r] + (long long)need <= L;
-            if (paged) at += s.w - s.o;
+    int taken = 0, served = 0, mine_at[ITEMS];
+    at_need = first_need;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        mine_at[i] = (int)min(at, (unsigned long long)a.max_new + 1);
+        if (sp[i].w > sp[i].o) {
+            const bool paged = need[i] == 0 || at_need + (long long)need[i] <= L;
+            if (paged) at += sp[i].w - sp[i].o;
             if (paged && at <= (unsigned long long)a.max_new) {
                 served = (int)at;
-                if (need) taken = need_at[r] + need;
+                if (need[i]) taken = at_need + need[i];
             } else {
                 bad = true;
             }
         }
+        at_need += need[i];
     }
     if (taken) atomicMax(&s_taken, taken);
     if (served) atomicMax(&s_rows, served);
     if (bad) s_flag = 1;
     __syncthreads();
     const int A = s_taken, T = s_rows;
-    for (int r = r0; r < r1; ++r) cu[r] = min(cu[r], T);
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+        if (r0 + i < n) cu[r0 + i] = min(mine_at[i], T);
     if (t == 0) cu[n] = T;
     __syncthreads();
     const long long left = L - A;
@@ -155,13 +171,13 @@ __global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs 
         const long long at_list = L - 1 - k;
         if (at_list < F) return a.free_pages[at_list];
         const int j = (int)(at_list - F), r = last_at_most(drop_at, n, j);
-        const int want = pages_of(span_of(a, r).w, a.page_size);
+        const int want = pages_of(a, span_of(a, r).w);
         return a.table[(long long)r * a.table_stride + want + (j - drop_at[r])];
     };
-    const int step = gridDim.x * RS_THREADS, g0 = blockIdx.x * RS_THREADS + t;
+    const int step = gridDim.x * blockDim.x, g0 = blockIdx.x * blockDim.x + t;
     for (int k = g0; k < A; k += step) {
         const int r = last_at_most(need_at, n, k);
-        const int have = pages_of(span_of(a, r).o, a.page_size);
+        const int have = pages_of(a, span_of(a, r).o);
         a.table[(long long)r * a.table_stride + have + (k - need_at[r])] = taken_page(k);
     }
     for (long long j = g0; F + j < left; j += step) {
@@ -170,7 +186,7 @@ __global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs 
             break;
         }
         const int r = last_at_most(drop_at, n, (int)j);
-        const int want = pages_of(span_of(a, r).w, a.page_size);
+        const int want = pages_of(a, span_of(a, r).w);
         a.free_pages[F + j] = a.table[(long long)r * a.table_stride + want + ((int)j - drop_at[r])];
     }
     for (long long i = g0; i < a.max_new; i += step) {
@@ -179,7 +195,7 @@ __global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs 
             r = last_at_most(cu, n, (int)i);
             const int o = span_of(a, r).o;
             pos = o + ((int)i - cu[r]);
-            const int pg = pos / a.page_size, have = pages_of(o, a.page_size);
+            const int pg = page_index(a, pos), have = pages_of(a, o);
             const int page = pg < have ? a.table[(long long)r * a.table_stride + pg] : taken_page(need_at[r] + (pg - have));
             slot = page * a.page_size + (pos - pg * a.page_size);
         }
@@ -190,23 +206,36 @@ __global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs 
     for (int r = g0; r <= n; r += step) a.cu_new[r] = cu[r];
 
     // lengths and the count, once every CTA has read them
-    __threadfence();
+    if (gridDim.x > 1) __threadfence();
     __syncthreads();
     if (t == 0) {
-        s_last = atomicAdd(a.ctr, 1) == (int)gridDim.x - 1;
+        s_last = gridDim.x == 1 || atomicAdd(a.ctr, 1) == (int)gridDim.x - 1;
         if (s_flag) atomicOr(a.status, STATUS_PAGES);
     }
     __syncthreads();
     if (!s_last) return;
-    __threadfence();
-    for (int r = t; r < n; r += RS_THREADS) {
-        const Span s = span_of(a, r);
-        a.len_out[r] = s.w > s.o ? s.o + (cu[r + 1] - cu[r]) : s.w;
+    if (gridDim.x > 1) __threadfence();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const int r = r0 + i;
+        if (r < n) a.len_out[r] = sp[i].w > sp[i].o ? sp[i].o + (cu[r + 1] - cu[r]) : sp[i].w;
     }
     if (t == 0) {
         *a.free_out = (int)min(left, a.n_free_max);
-        *a.ctr = 0;
+        if (gridDim.x > 1) *a.ctr = 0;
     }
+}
+
+template <int ITEMS>
+cudaError_t launch_resize(const ResizeArgs &a, int grid, int threads, cudaStream_t st) {
+    static std::atomic<unsigned long long> done{0};
+    const size_t smem = sizeof(int) * 3 * ((size_t)a.n_req + 1);
+    if (smem > 40 * 1024) {
+        const cudaError_t e = allow_max_dynamic_smem(kv_resize_kernel<ITEMS>, done);
+        if (e != cudaSuccess) return e;
+    }
+    kv_resize_kernel<ITEMS><<<grid, threads, smem, st>>>(a);
+    return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------- kv_append
@@ -323,10 +352,14 @@ template <> struct Piece<__nv_bfloat16> {
 // which the pairs (i, i + half) join, and behind them single pieces; with
 // interleaved pairs, single pieces only.  A row's threads (per_row of them, a
 // multiple of the items or cut to one) keep their item from head to head, so that
-// its cosines and sines are fetched once; heads are taken three at a time, loads first.
+// its cosines and sines are fetched once; heads are taken U at a time, loads first.
+#ifndef AU
+#define AU 2
+#define AB 4
+#endif
 template <typename T, typename KV>
-__global__ void __launch_bounds__(256) kv_append_vec_kernel(const AppendArgs a, int per_row) {
-    constexpr int VE = Piece<T>::N, U = 3;
+__global__ void __launch_bounds__(256, AB) kv_append_vec_kernel(const AppendArgs a, int per_row) {
+    constexpr int VE = Piece<T>::N, U = AU;
     const int rows = blockDim.x / per_row, sub = threadIdx.x / per_row, t = threadIdx.x - sub * per_row;
     const int row = blockIdx.x * rows + sub;
     if (row >= a.n) return;
@@ -341,10 +374,26 @@ __global__ void __launch_bounds__(256) kv_append_vec_kernel(const AppendArgs a, 
     const int d0 = (two ? item : item + joined) * VE, d1 = d0 + half;
     const bool turned = two || (a.interleaved && d0 < a.rot);
 
+    // a head's row in q, k or v
+    auto source = [&](int hh) -> const T * {
+        const bool q = hh < a.q_heads, k = hh < a.q_heads + a.kv.heads;
+        const T *base = reinterpret_cast<const T *>(q ? a.q : k ? a.k : a.v);
+        const long long ld = q ? a.q_stride : k ? a.k_stride : a.v_stride;
+        return base + row * ld + (hh - (q ? 0 : k ? a.q_heads : a.q_heads + a.kv.heads)) * dim;
+    };
+    uint4 x0[U], x1[U];
+    auto load = [&](int from) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int hh = from + u * stride;
+            if (hh >= heads) continue;
+            const T *src = source(hh);
+            x0[u] = *reinterpret_cast<const uint4 *>(src + d0);
+            if (two) x1[u] = *reinterpret_cast<const uint4 *>(src + d1);
+        }
+    };
     const int slot = a.slot_map[row];
-    const bool in = slot >= 0 && slot < (long long)a.kv.n_pages * a.kv.page_size;
-    if (slot < -1 || (slot >= 0 && !in)) atomicOr(a.status, STATUS_PAGES);
-    const long long at = in ? (slot / a.kv.page_size) * a.kv.page_stride + (slot % a.kv.page_size) * a.kv.token_stride : 0;
+    load(h);
 
     // the item's cosines and sines: VE pairs (half as many where they are interleaved)
     float c[VE], s[VE];
@@ -356,8 +405,7 @@ __global__ void __launch_bounds__(256) kv_append_vec_kernel(const AppendArgs a, 
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
             if (e >= pairs) break;
-            int ax = 0;
-            while (ax < 3 && p0 + e >= a.bound[ax]) ++ax;
+            const int i = p0 + e, ax = (i >= a.bound[0]) + (i >= a.bound[1]) + (i >= a.bound[2]);
             if (ax != last_ax) {
                 int p = a.positions[ax * a.axis_stride + row];
                 if (p < 0 || p >= a.n_pos) {
@@ -372,24 +420,16 @@ __global__ void __launch_bounds__(256) kv_append_vec_kernel(const AppendArgs a, 
         }
         if (bad) atomicOr(a.status, STATUS_PAGES);
     }
+    const bool in = slot >= 0 && slot < (long long)a.kv.n_pages * a.kv.page_size;
+    if (slot < -1 || (slot >= 0 && !in)) atomicOr(a.status, STATUS_PAGES);
+    const long long at = in ? (slot / a.kv.page_size) * a.kv.page_stride + (slot % a.kv.page_size) * a.kv.token_stride : 0;
 
-    for (; h < heads; h += U * stride) {
-        uint4 x0[U], x1[U];
+    for (;;) {
+        const int next = h + U * stride;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int hh = h + u * stride;
             const int kind = hh < a.q_heads ? 0 : hh < a.q_heads + a.kv.heads ? 1 : 2;     // q, k, v
-            if (hh >= heads || (kind && !in)) continue;
-            const int hk = kind == 0 ? hh : kind == 1 ? hh - a.q_heads : hh - a.q_heads - a.kv.heads;
-            const T *src = reinterpret_cast<const T *>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
-                           (long long)row * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + hk * dim;
-            x0[u] = *reinterpret_cast<const uint4 *>(src + d0);
-            if (two) x1[u] = *reinterpret_cast<const uint4 *>(src + d1);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int hh = h + u * stride;
-            const int kind = hh < a.q_heads ? 0 : hh < a.q_heads + a.kv.heads ? 1 : 2;
             if (hh >= heads || (kind && !in)) continue;
             const int hk = kind == 0 ? hh : kind == 1 ? hh - a.q_heads : hh - a.q_heads - a.kv.heads;
             float y0[VE], y1[VE];
@@ -431,6 +471,9 @@ __global__ void __launch_bounds__(256) kv_append_vec_kernel(const AppendArgs a, 
                 if (two) Piece<T>::store(dst + d1, y1);
             }
         }
+        if (next >= heads) break;
+        h = next;
+        load(h);
     }
 }
 
@@ -465,17 +508,14 @@ __global__ void __launch_bounds__(256) rope_table_kernel(float *out, int n_pos, 
 }  // namespace
 
 cudaError_t launch_kv_resize(const ResizeArgs &a, int num_sms, cudaStream_t st) {
-    static std::atomic<unsigned long long> done{0};
-    const size_t smem = sizeof(int) * 3 * ((size_t)a.n_req + 1);
-    if (smem > 40 * 1024) {
-        const cudaError_t e = allow_max_dynamic_smem(kv_resize_kernel, done);
-        if (e != cudaSuccess) return e;
-    }
-    // every CTA scans the requests for itself and takes its share of the rows
-    const long long rows = a.max_new > a.n_req ? a.max_new : a.n_req;
-    const int grid = (int)min((long long)num_sms, (rows + RS_THREADS - 1) / RS_THREADS + (rows == 0));
-    kv_resize_kernel<<<grid, RS_THREADS, smem, st>>>(a);
-    return cudaGetLastError();
+    // every CTA scans the requests for itself and takes its share of the rows; a
+    // small step is one CTA's, which needs no launch-wide arrival
+    const int n = a.n_req, threads = n <= 256 ? 256 : RS_THREADS;
+    const long long rows = a.max_new > n ? a.max_new : n;
+    const int grid = (int)min((long long)num_sms, (rows + threads - 1) / threads + (rows == 0));
+    if (n <= RS_THREADS) return launch_resize<1>(a, grid, threads, st);
+    if (n <= 4 * RS_THREADS) return launch_resize<4>(a, grid, threads, st);
+    return launch_resize<16>(a, grid, threads, st);
 }
 
 cudaError_t launch_kv_append(bool f32, const AppendArgs &a, int num_sms, cudaStream_t st) {

@@ -11,6 +11,9 @@ namespace {
 
 bool aligned(const void *p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
+// log2 of a power of two, -1 of any other number.
+int shift_of(int x) { return (x & (x - 1)) == 0 ? __builtin_ctz(x) : -1; }
+
 int kv_esz(int dtype) { return dtype == SCUTE_KV_FP32 ? 4 : dtype == SCUTE_KV_BF16 ? 2 : 1; }
 
 scute_status check_cache(scute_ctx *c, const scute_kv_cache *kv, KvView *out) {
@@ -80,6 +83,7 @@ scute_status scute_kv_resize(scute_ctx *c, const int32_t *len_in, const int32_t 
     a.n_req = n_req;
     a.cols = table_cols;
     a.page_size = page_size;
+    a.page_shift = shift_of(page_size);
     a.table = block_table;
     a.table_stride = table_stride;
     a.free_pages = free_pages;
@@ -218,9 +222,7 @@ scute_status scute_paged_attention(scute_ctx *c, const scute_kv_cache *kv, const
     a.scale = t->scale != 0.f ? t->scale : 1.f / sqrtf((float)kv->head_dim);
     a.softcap = t->softcap;
     a.window = t->window;
-    a.page_shift = -1;
-    for (int i = 0; i < 31; ++i)
-        if (kv->page_size == 1 << i) a.page_shift = i;
+    a.page_shift = shift_of(kv->page_size);
     a.part = c->att_part;
     a.ctr = c->srv_ctr + 1;
     a.status = c->d_status;
