@@ -378,6 +378,7 @@ struct ResizeArgs {
     const int32_t *free_in;
     int32_t *free_out, *len_out, *cu_new, *slot_map, *positions, *token_req;
     int max_new;
+    int in_place;              // len_out or free_out may lie where len_in or free_in does
     int *ctr;                  // arrivals of the launch's CTAs (zero between launches)
     int *status;
 };

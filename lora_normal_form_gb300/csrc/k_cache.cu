@@ -22,8 +22,8 @@ namespace {
 // ones that need any, and their k run from 0 without a gap.  Nothing that is
 // read is written: rows of shrinking requests are only read, the rows of
 // growing ones written behind their old pages, and list entries are written
-// only from F on.  So no thread waits for another, except that the lengths and
-// the count, which may be written in place, follow a launch-wide arrival count.
+// only from F on.  So no thread waits for another, except that lengths and a
+// count that are written in place follow a launch-wide arrival count.
 constexpr int RS_THREADS = 1024;       // at most
 
 // Pages of so many tokens (at most 2^31 - 1 with a page's rounding); page of a position.
@@ -57,47 +57,80 @@ __device__ __forceinline__ unsigned long long cta_exclusive(unsigned long long x
     }
     if (lane == 31) warp_sum[warp] = inc;
     __syncthreads();
-    unsigned long long before = 0, all = 0;
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) {
-        const unsigned long long s = warp_sum[w];
-        before += w < warp ? s : 0;
-        all += s;
+    if (warp == 0) {
+        const unsigned long long own = lane < (int)blockDim.x / 32 ? warp_sum[lane] : 0;
+        unsigned long long sum = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        warp_sum[lane] = sum - own;
+        if (lane == 31) warp_sum[32] = sum;
     }
     __syncthreads();
-    *total = all;
-    return before + inc - x;
+    *total = warp_sum[32];
+    const unsigned long long before = warp_sum[warp] + inc - x;
+    __syncthreads();
+    return before;
 }
 
 struct Span {
     int o, w;      // old and wanted length, inside the row
     bool bad;
 };
-__device__ __forceinline__ Span span_of(const ResizeArgs &a, int r) {
+__device__ __forceinline__ Span span_of(const ResizeArgs &a, int o, int w) {
     const int cap = a.cols * a.page_size;
-    const int o = a.len_in[r], w = a.len_new[r];
     Span s;
     s.bad = o < 0 || o > cap || w < 0 || w > cap;
     s.o = o < 0 ? 0 : o > cap ? cap : o;
     s.w = w < 0 || w > cap ? s.o : w;
     return s;
 }
+__device__ __forceinline__ Span span_of(const ResizeArgs &a, int r) { return span_of(a, a.len_in[r], a.len_new[r]); }
+// Entries between the kernel's lists, in shared memory (16-byte aligned).
+__host__ __device__ inline int list_pitch(int n) { return (n + 4) & ~3; }
+
+// A thread's entries of a list.
+template <int ITEMS>
+__device__ __forceinline__ void put_list(int *list, int r0, int n, const int (&x)[ITEMS]) {
+    if (ITEMS % 4 == 0 && r0 + ITEMS <= n) {
+#pragma unroll
+        for (int i = 0; i + 3 < ITEMS; i += 4) *reinterpret_cast<int4 *>(list + r0 + i) = make_int4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i)
+            if (r0 + i < n) list[r0 + i] = x[i];
+    }
+}
 
 // ITEMS consecutive requests of a thread, held in registers.
 template <int ITEMS>
 __global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs a) {
-    extern __shared__ int sm[];
-    __shared__ unsigned long long warp_sum[RS_THREADS / 32];
+    extern __shared__ __align__(16) int sm[];
+    __shared__ unsigned long long warp_sum[33];
     __shared__ int s_taken, s_rows, s_flag, s_last;
     const int n = a.n_req, t = threadIdx.x;
-    int *drop_at = sm, *need_at = sm + (n + 1), *cu = sm + 2 * (n + 1);
+    const int pitch = list_pitch(n);
+    int *drop_at = sm, *need_at = sm + pitch, *cu = sm + 2 * pitch;
+    // lengths, where the batch leaves room for them
+    constexpr bool KEEP = ITEMS <= 4;
+    int *old_of = sm + 3 * pitch, *new_of = sm + 4 * pitch;
     if (t == 0) s_taken = s_rows = s_flag = 0;
     const int r0 = t * ITEMS;
     int F = *a.free_in;
     Span sp[ITEMS];
+    if (ITEMS == 4 && r0 + 3 < n && ((reinterpret_cast<uintptr_t>(a.len_in) | reinterpret_cast<uintptr_t>(a.len_new)) & 15) == 0) {
+        const int4 o = *reinterpret_cast<const int4 *>(a.len_in + r0), w = *reinterpret_cast<const int4 *>(a.len_new + r0);
+        const int ov[4] = {o.x, o.y, o.z, o.w}, wv[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        sp[i] = {0, 0, false};
-        if (r0 + i < n) sp[i] = span_of(a, r0 + i);
+        for (int i = 0; i < ITEMS; ++i) sp[i] = span_of(a, ov[i & 3], wv[i & 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            sp[i] = {0, 0, false};
+            if (r0 + i < n) sp[i] = span_of(a, r0 + i);
+        }
     }
     bool bad = false;
     if (F < 0 || F > a.n_free_max) {
@@ -123,14 +156,18 @@ __global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs 
 
     // new tokens of the requests that get their pages
     unsigned long long rows = 0;
+    int drops[ITEMS], needs[ITEMS], olds[ITEMS], news[ITEMS];
     int first_need = (int)(run & 0xffffffffu), at_need = first_need, at_drop = (int)(run >> 32);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-        if (r0 + i < n) drop_at[r0 + i] = at_drop, need_at[r0 + i] = at_need;
+        drops[i] = at_drop, needs[i] = at_need, olds[i] = sp[i].o, news[i] = sp[i].w;
         if (sp[i].w > sp[i].o && (need[i] == 0 || at_need + (long long)need[i] <= L)) rows += sp[i].w - sp[i].o;
         at_drop += drop[i];
         at_need += need[i];
     }
+    put_list(drop_at, r0, n, drops);
+    put_list(need_at, r0, n, needs);
+    if (KEEP) put_list(old_of, r0, n, olds), put_list(new_of, r0, n, news);
     if (t == 0) {
         drop_at[n] = P;
         need_at[n] = (int)(total & 0xffffffffu);
@@ -154,30 +191,36 @@ __global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs 
         }
         at_need += need[i];
     }
-    if (taken) atomicMax(&s_taken, taken);
-    if (served) atomicMax(&s_rows, served);
+    taken = __reduce_max_sync(0xffffffffu, taken);
+    served = __reduce_max_sync(0xffffffffu, served);
+    if ((t & 31) == 0) {
+        atomicMax(&s_taken, taken);
+        atomicMax(&s_rows, served);
+    }
     if (bad) s_flag = 1;
     __syncthreads();
     const int A = s_taken, T = s_rows;
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i)
-        if (r0 + i < n) cu[r0 + i] = min(mine_at[i], T);
+    for (int i = 0; i < ITEMS; ++i) mine_at[i] = min(mine_at[i], T);
+    put_list(cu, r0, n, mine_at);
     if (t == 0) cu[n] = T;
     __syncthreads();
     const long long left = L - A;
 
+    auto old_len = [&](int r) { return KEEP ? old_of[r] : span_of(a, r).o; };
+    auto new_len = [&](int r) { return KEEP ? new_of[r] : span_of(a, r).w; };
     // the k-th page taken from the top of the list
     auto taken_page = [&](int k) -> int {
         const long long at_list = L - 1 - k;
         if (at_list < F) return a.free_pages[at_list];
         const int j = (int)(at_list - F), r = last_at_most(drop_at, n, j);
-        const int want = pages_of(a, span_of(a, r).w);
+        const int want = pages_of(a, new_len(r));
         return a.table[(long long)r * a.table_stride + want + (j - drop_at[r])];
     };
     const int step = gridDim.x * blockDim.x, g0 = blockIdx.x * blockDim.x + t;
     for (int k = g0; k < A; k += step) {
         const int r = last_at_most(need_at, n, k);
-        const int have = pages_of(a, span_of(a, r).o);
+        const int have = pages_of(a, old_len(r));
         a.table[(long long)r * a.table_stride + have + (k - need_at[r])] = taken_page(k);
     }
     for (long long j = g0; F + j < left; j += step) {
@@ -186,14 +229,14 @@ __global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs 
             break;
         }
         const int r = last_at_most(drop_at, n, (int)j);
-        const int want = pages_of(a, span_of(a, r).w);
+        const int want = pages_of(a, new_len(r));
         a.free_pages[F + j] = a.table[(long long)r * a.table_stride + want + ((int)j - drop_at[r])];
     }
     for (long long i = g0; i < a.max_new; i += step) {
         int slot = -1, pos = 0, r = -1;
         if (i < T) {
             r = last_at_most(cu, n, (int)i);
-            const int o = span_of(a, r).o;
+            const int o = old_len(r);
             pos = o + ((int)i - cu[r]);
             const int pg = page_index(a, pos), have = pages_of(a, o);
             const int page = pg < have ? a.table[(long long)r * a.table_stride + pg] : taken_page(need_at[r] + (pg - have));
@@ -205,16 +248,18 @@ __global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs 
     }
     for (int r = g0; r <= n; r += step) a.cu_new[r] = cu[r];
 
-    // lengths and the count, once every CTA has read them
-    if (gridDim.x > 1) __threadfence();
+    // lengths and the count: where they are written in place, by the last CTA to
+    // have read them
+    const bool arrive = a.in_place && gridDim.x > 1;
+    if (arrive) __threadfence();
     __syncthreads();
     if (t == 0) {
-        s_last = gridDim.x == 1 || atomicAdd(a.ctr, 1) == (int)gridDim.x - 1;
+        s_last = arrive ? atomicAdd(a.ctr, 1) == (int)gridDim.x - 1 : blockIdx.x == 0;
         if (s_flag) atomicOr(a.status, STATUS_PAGES);
     }
     __syncthreads();
     if (!s_last) return;
-    if (gridDim.x > 1) __threadfence();
+    if (arrive) __threadfence();
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         const int r = r0 + i;
@@ -222,14 +267,14 @@ __global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs 
     }
     if (t == 0) {
         *a.free_out = (int)min(left, a.n_free_max);
-        if (gridDim.x > 1) *a.ctr = 0;
+        if (arrive) *a.ctr = 0;
     }
 }
 
 template <int ITEMS>
 cudaError_t launch_resize(const ResizeArgs &a, int grid, int threads, cudaStream_t st) {
     static std::atomic<unsigned long long> done{0};
-    const size_t smem = sizeof(int) * 3 * ((size_t)a.n_req + 1);
+    const size_t smem = sizeof(int) * (ITEMS <= 4 ? 5 : 3) * (size_t)list_pitch(a.n_req);
     if (smem > 40 * 1024) {
         const cudaError_t e = allow_max_dynamic_smem(kv_resize_kernel<ITEMS>, done);
         if (e != cudaSuccess) return e;

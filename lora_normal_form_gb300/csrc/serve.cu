@@ -96,6 +96,9 @@ scute_status scute_kv_resize(scute_ctx *c, const int32_t *len_in, const int32_t 
     a.positions = positions;
     a.token_req = token_req;
     a.max_new = (int)max_new;
+    const auto overlap = [](const int32_t *p, const int32_t *q, int64_t k) { return p < q + k && q < p + k; };
+    a.in_place = free_in == free_out || overlap(len_in, len_out, n_req) || overlap(len_new, len_out, n_req) ||
+                 overlap(len_in, free_out, n_req) || overlap(len_new, free_out, n_req) || overlap(len_out, free_in, n_req);
     a.ctr = c->srv_ctr;
     a.status = c->d_status;
     TimedLaunch tl{c, st};
