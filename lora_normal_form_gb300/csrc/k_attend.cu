@@ -53,7 +53,14 @@ __device__ __forceinline__ uint2 lds8(uint32_t p) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(p));
     return r;
 }
-// 16 bytes from global to shared memory, or 16 zero bytes.
+// 16 bytes from global to shared memory, or 16 zero bytes; of the cache's rows
+// with an L2 policy (they are read once: what else a step keeps in L2, its code
+// among it, shall stay there).
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(real ? 16 : 0), "l"(policy)
+                 : "memory");
+}
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
                  "r"(real ? 16 : 0)
@@ -623,6 +630,11 @@ __device__ __forceinline__ void plan_places(const AttendArgs &a, int tt, int *pl
     __syncthreads();
 }
 
+// x / y of numbers that mostly fit 32 bits (a 64-bit division is a long routine).
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+    return ((x | y) >> 32) == 0 ? (long long)((unsigned)x / (unsigned)y) : x / y;
+}
+
 // Walks a CTA's range of places, row by row.
 struct Walk {
     const AttendArgs &a;
@@ -640,11 +652,11 @@ struct Walk {
         Z = (a.group + heads_chunk - 1) / heads_chunk;
         hz = a.kv.heads * Z;
         total = (long long)at[a.n_req] * hz;
-        ctas = (int)min((long long)gridDim.x, (total + min_tiles - 1) / min_tiles);
+        ctas = (int)min((long long)gridDim.x, quotient(total + min_tiles - 1, min_tiles));
     }
-    __device__ __forceinline__ long long start(int cta) const { return total * cta / ctas; }
+    __device__ __forceinline__ long long start(int cta) const { return quotient(total * cta, ctas); }
     // The CTA whose range holds place x.
-    __device__ __forceinline__ int owner(long long x) const { return (int)(((x + 1) * ctas - 1) / total); }
+    __device__ __forceinline__ int owner(long long x) const { return (int)quotient((x + 1) * ctas - 1, total); }
     __device__ __forceinline__ int first_owner() const { return owner(base + ROW_COST); }
     __device__ __forceinline__ int last_owner() const { return owner(base + ROW_COST + tiles - 1); }
     __device__ __forceinline__ void request() {
@@ -668,7 +680,7 @@ struct Walk {
         }
         request();
         const long long in = x - (long long)places_at[r] * hz;
-        const int row = in < 1ll << 31 ? (int)((unsigned)in / (unsigned)(tiles + ROW_COST)) : (int)(in / (tiles + ROW_COST));
+        const int row = (int)quotient(in, tiles + ROW_COST);
         base = (long long)places_at[r] * hz + (long long)row * (tiles + ROW_COST);
         hk = row / Z;
         z = row - hk * Z;
@@ -721,71 +733,74 @@ __device__ __forceinline__ void put(const AttendArgs &a, int r, int h, int d, fl
 struct SharedRow {
     int r, hk, h0, nh, c0, c1;          // request, heads; its first and last CTA
 };
-// Join the parts of up to two rows (n_head and n_tail groups of four outputs):
-// IT groups of a thread and B parts at a time, all their loads on the way at once.
-template <typename IO, int IT, int B, int THREADS>
-__device__ __noinline__ void join_parts(const AttendArgs &a, const SharedRow &head, const SharedRow &tail, int n_head,
-                                        int n_tail, int t) {
-    const int D = a.kv.dim;
-    for (int i0 = t; i0 < n_head + n_tail; i0 += IT * THREADS) {
-        float m[IT], l[IT];
-        float4 x[IT];
-        int parts[IT], first[IT], h[IT], d[IT], most = 0;
+// Join the parts of up to two rows (row i: shared[i] where last[i]): as many
+// parts at a time as `room` bytes of shared memory hold, brought there at once.
+template <typename IO, int HC, int DC, int THREADS>
+__device__ __forceinline__ void join_parts(const AttendArgs &a, const SharedRow &head, const SharedRow &tail, bool last_head,
+                                           bool last_tail, uint8_t *buf, int room, int t) {
+    constexpr int IT = (HC * DC / 4 + THREADS - 1) / THREADS;      // groups of four outputs of a thread
+    const int D = a.kv.dim, n_head = last_head ? head.c1 - head.c0 + 1 : 0, n_tail = last_tail ? tail.c1 - tail.c0 + 1 : 0;
+    const int nh = max(last_head ? head.nh : 0, last_tail ? tail.nh : 0);
+    const int bytes = (2 * ATT_HEADS + nh * D) * 4, pieces = bytes / 16, cap = room / bytes;
+    float m[2][IT], l[2][IT];
+    float4 x[2][IT];
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int at = i0 + i * THREADS;
-            const bool in_tail = at >= n_head;
-            const int e = in_tail ? at - n_head : at;
-            first[i] = in_tail ? tail.c0 : head.c0;
-            parts[i] = at >= n_head + n_tail ? 0 : (in_tail ? tail.c1 : head.c1) - first[i] + 1;
-            most = max(most, parts[i]);
-            h[i] = e / (D / 4);
-            d[i] = 4 * (e - h[i] * (D / 4));
-            m[i] = -INFINITY, l[i] = 0.f;
-            x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int i = 0; i < IT; ++i) m[w][i] = -INFINITY, l[w][i] = 0.f, x[w][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < n_head + n_tail; p0 += cap) {
+        const int p1 = min(p0 + cap, n_head + n_tail);
+        sync_threads<THREADS>();
+        for (int at = p0; at < p1; ++at) {
+            const int k = at < n_head ? at : at - n_head, c0 = at < n_head ? head.c0 : tail.c0;
+            const float *from = part_of(a, k ? 2 * (c0 + k) : 2 * c0 + 1).m;
+            const uint32_t to = ptx::smem_u32(buf) + (at - p0) * bytes;
+            for (int e = t; e < pieces; e += THREADS) copy16(to + e * 16, from + e * 4, true);
         }
-        for (int k0 = 0; k0 < most; k0 += B) {
-            float pm[IT][B], pl[IT][B];
-            float4 po[IT][B];
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        sync_threads<THREADS>();
 #pragma unroll
-            for (int i = 0; i < IT; ++i)
-#pragma unroll
-                for (int k = 0; k < B; ++k) {
-                    pm[i][k] = -INFINITY;
-                    if (k0 + k < parts[i]) {
-                        const PartView q = part_of(a, k0 + k ? 2 * (first[i] + k0 + k) : 2 * first[i] + 1);
-                        pm[i][k] = __ldcg(q.m + h[i]);
-                        pl[i][k] = __ldcg(q.l + h[i]);
-                        po[i][k] = __ldcg(reinterpret_cast<const float4 *>(q.o + h[i] * D + d[i]));
-                    }
-                }
+        for (int w = 0; w < 2; ++w) {
+            const int from = max(w ? n_head : 0, p0), to = min(w ? n_head + n_tail : n_head, p1);
+            const int items = (w ? tail.nh : head.nh) * (D / 4);
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
-                float top = m[i];
-#pragma unroll
-                for (int k = 0; k < B; ++k) top = fmaxf(top, pm[i][k]);
+                const int e = t + i * THREADS;
+                if (e >= items || from >= to) break;
+                const float *part = reinterpret_cast<const float *>(buf + (from - p0) * bytes), *pm = part + e / (D / 4);
+                const int ld = bytes / 4, k1 = to - from;
+                float top = m[w][i];
+#pragma unroll 4
+                for (int k = 0; k < k1; ++k) top = fmaxf(top, pm[k * ld]);
                 if (top == -INFINITY) continue;
-                const float f = exp2f(m[i] - top);
-                l[i] *= f, x[i].x *= f, x[i].y *= f, x[i].z *= f, x[i].w *= f;
-                m[i] = top;
-#pragma unroll
-                for (int k = 0; k < B; ++k)
-                    if (pm[i][k] > -INFINITY) {
-                        const float e = exp2f(pm[i][k] - top);
-                        l[i] += e * pl[i][k];
-                        x[i].x += e * po[i][k].x, x[i].y += e * po[i][k].y;
-                        x[i].z += e * po[i][k].z, x[i].w += e * po[i][k].w;
-                    }
+                const float f = pow2(m[w][i] - top);
+                float4 z = x[w][i];
+                float sum = l[w][i] * f;
+                z.x *= f, z.y *= f, z.z *= f, z.w *= f;
+#pragma unroll 2
+                for (int k = 0; k < k1; ++k) {
+                    const float g = pow2(pm[k * ld] - top);
+                    const float4 y = *reinterpret_cast<const float4 *>(part + k * ld + 2 * ATT_HEADS + 4 * e);
+                    sum += pm[k * ld + ATT_HEADS] * g;
+                    z.x += y.x * g, z.y += y.y * g, z.z += y.z * g, z.w += y.w * g;
+                }
+                m[w][i] = top, l[w][i] = sum, x[w][i] = z;
             }
         }
+    }
 #pragma unroll
-        for (int i = 0; i < IT; ++i)
-            if (parts[i]) {
-                const SharedRow &row = i0 + i * THREADS >= n_head ? tail : head;
-                const float vs = a.kv.v_scale ? a.kv.v_scale[row.hk] : 1.f;
-                put<IO>(a, row.r, row.h0 + h[i], d[i], x[i], l[i] == 0.f ? 0.f : vs / l[i]);
-                if (a.lse && d[i] == 0) a.lse[(long long)row.r * a.q_heads + row.h0 + h[i]] = (m[i] + log2f(l[i])) * LN2;
-            }
+    for (int w = 0; w < 2; ++w) {
+        if (!(w ? last_tail : last_head)) continue;
+        const SharedRow &row = w ? tail : head;
+        const float vs = a.kv.v_scale ? a.kv.v_scale[row.hk] : 1.f;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int e = t + i * THREADS;
+            if (e >= row.nh * (D / 4)) break;
+            const int h = e / (D / 4), d = 4 * (e - h * (D / 4));
+            put<IO>(a, row.r, row.h0 + h, d, x[w][i], l[w][i] == 0.f ? 0.f : vs / l[w][i]);
+            if (a.lse && d == 0) a.lse[(long long)row.r * a.q_heads + row.h0 + h] = (m[w][i] + log2f(l[w][i])) * LN2;
+        }
     }
 }
 
@@ -798,6 +813,7 @@ struct Shape {
     static constexpr int O_BYTES = CW * M::HC * O_LD * 4, Q_BYTES = M::HC * DC * (int)sizeof(typename M::IO);
     static constexpr int FIXED = O_BYTES + QS * Q_BYTES + CW * M::P_BYTES + CW * M::HC * 8 + M::HC * 8 +
                                  (2 * MAX_STAGES + 2 * QS) * 8 + MAX_STAGES * 4 + 64;
+    static_assert(CW * STAGE >= (2 * ATT_HEADS + M::HC * DC) * 4, "the ring holds a part");
     static_assert(STAGE % 128 == 0 && O_BYTES % 16 == 0 && Q_BYTES % 16 == 0 && M::P_BYTES % 16 == 0, "alignment");
     static size_t smem(int stages, int n_req) { return FIXED + (size_t)stages * STAGE + 4 * ((size_t)n_req + 1); }
 };
@@ -853,6 +869,7 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
         // Spans of up to 128 tokens; the pages of the next span are looked up
         // before this one's rows are sent for.
         constexpr int SPAN = 128;
+        const uint64_t policy = ptx::make_policy_evict_first();
         const long long tok_bytes = a.kv.token_stride * ESZ;
         int hk = w.hk, z = w.z, r = w.r, stop = w.to(), pos = w.from();
         bool opens = true, more = w.more();
@@ -935,8 +952,8 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
                                     const int row = n * RI + row0;
                                     const bool real = in_row && row < rows;
                                     const uint32_t to = place_of<M::ROW>(row, piece);
-                                    copy16(kd + to, real ? ks : kb, real);
-                                    copy16(vd + to, real ? vs : vb, real);
+                                    copy16(kd + to, real ? ks : kb, real, policy);
+                                    copy16(vd + to, real ? vs : vb, real, policy);
                                     ks += RI * tok_bytes;
                                     vs += RI * tok_bytes;
                                 }
@@ -947,8 +964,8 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
                                     const long long p = __shfl_sync(0xffffffffu, place, m * TT + row);
                                     const bool real = in_row && p >= 0;
                                     const uint32_t to = place_of<M::ROW>(row, piece);
-                                    copy16(kd + to, real ? kb + p + piece * 16 : kb, real);
-                                    copy16(vd + to, real ? vb + p + piece * 16 : vb, real);
+                                    copy16(kd + to, real ? kb + p + piece * 16 : kb, real, policy);
+                                    copy16(vd + to, real ? vb + p + piece * 16 : vb, real, policy);
                                 }
                             }
                         }
@@ -1055,24 +1072,22 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
 
     // arrive at the shared rows; the last to arrive joins
     if (head.r < 0 && tail.r < 0) return;
-    __threadfence();
     sync_threads<CW * 32>();
     if (t < 2) {
         const SharedRow &row = t ? tail : head;
         int last = 0;
         if (row.r >= 0) {
+            __threadfence();          // the CTA's parts, which the barrier above has ordered before this
             last = atomicAdd(a.ctr + row.c0, 1) == row.c1 - row.c0;
             if (last) a.ctr[row.c0] = 0;
+            __threadfence();
         }
         s_last[t] = last;
     }
     sync_threads<CW * 32>();
-    __threadfence();
-    const int n_head = s_last[0] ? head.nh * (D / 4) : 0, n_tail = s_last[1] ? tail.nh * (D / 4) : 0;
-    const int most = max(n_head ? head.c1 - head.c0 : 0, n_tail ? tail.c1 - tail.c0 : 0) + 1;
-    // few long rows have many parts, many rows have few
-    if (most > 4) join_parts<IO, 1, 16, CW * 32>(a, head, tail, n_head, n_tail, t);
-    else join_parts<IO, 4, 4, CW * 32>(a, head, tail, n_head, n_tail, t);
+    const bool last_head = s_last[0], last_tail = s_last[1];
+    if (last_head || last_tail)          // the ring is empty by now
+        join_parts<IO, HC, DC, CW * 32>(a, head, tail, last_head, last_tail, s_ring, stages * S::STAGE, t);
 }
 
 template <typename M, int DC, int CW, int PW, int CTAS>
