@@ -353,6 +353,24 @@ cudaError_t launch_vera_shrink_tc(const VsTcArgs &p, int grid, cudaStream_t st, 
 // beside: a VeRA shrink is launched right after it, to run beside it
 cudaError_t launch_lr_shrink_tc(const LrTcArgs &p, int grid, cudaStream_t st, bool pdl, bool beside);
 
+// Launch of a kernel that begins with griddepcontrol.wait: it may be set up
+// while the kernel before it on the stream still runs (programmatic dependent
+// launch), and reads nothing before that one has ended.
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---------------------------------------------------------------- paged cache
 // Element types of a cache (the codes of SCUTE_KV_*).
 enum : int { KV_BF16 = 0, KV_FP32 = 1, KV_E4M3 = 2 };

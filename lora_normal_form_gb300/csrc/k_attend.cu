@@ -858,6 +858,8 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
         }
         ptx::fence_mbar_init();
     }
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
     plan_places(a, TT, places_at, s_warp);
     Walk w(a, places_at, HC, TT, MIN_TILES);
     const int cta = blockIdx.x;
@@ -1108,8 +1110,7 @@ cudaError_t launch_shape(const AttendArgs &a, int num_sms, cudaStream_t st) {
     }
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
     if (stages > MAX_STAGES) stages = MAX_STAGES / CW * CW;
-    kernel<<<num_sms * per_sm, S::THREADS, S::smem((int)stages, a.n_req), st>>>(a, (int)stages);
-    return cudaGetLastError();
+    return launch_chained(kernel, num_sms * per_sm, S::THREADS, S::smem((int)stages, a.n_req), st, a, (int)stages);
 }
 
 template <bool FP8>

@@ -4,6 +4,7 @@
 #include <cuda_fp8.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace scute {
 
@@ -118,6 +119,8 @@ __global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs 
     int *old_of = sm + 3 * pitch, *new_of = sm + 4 * pitch;
     if (t == 0) s_taken = s_rows = s_flag = 0;
     const int r0 = t * ITEMS;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
     int F = *a.free_in;
     Span sp[ITEMS];
     if (ITEMS == 4 && r0 + 3 < n && ((reinterpret_cast<uintptr_t>(a.len_in) | reinterpret_cast<uintptr_t>(a.len_new)) & 15) == 0) {
@@ -279,8 +282,7 @@ cudaError_t launch_resize(const ResizeArgs &a, int grid, int threads, cudaStream
         const cudaError_t e = allow_max_dynamic_smem(kv_resize_kernel<ITEMS>, done);
         if (e != cudaSuccess) return e;
     }
-    kv_resize_kernel<ITEMS><<<grid, threads, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_chained(kv_resize_kernel<ITEMS>, grid, threads, smem, st, a);
 }
 
 // ---------------------------------------------------------------- kv_append
@@ -292,6 +294,8 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
 template <typename T>
 __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
     const int row = blockIdx.x, dim = a.kv.dim, half = a.rot / 2;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
     const int slot = a.slot_map[row];
     const bool in = slot >= 0 && slot < (long long)a.kv.n_pages * a.kv.page_size;
     if (slot < -1 || (slot >= 0 && !in)) atomicOr(a.status, STATUS_PAGES);
@@ -398,13 +402,9 @@ template <> struct Piece<__nv_bfloat16> {
 // interleaved pairs, single pieces only.  A row's threads (per_row of them, a
 // multiple of the items or cut to one) keep their item from head to head, so that
 // its cosines and sines are fetched once; heads are taken U at a time, loads first.
-#ifndef AU
-#define AU 2
-#define AB 4
-#endif
 template <typename T, typename KV>
-__global__ void __launch_bounds__(256, AB) kv_append_vec_kernel(const AppendArgs a, int per_row) {
-    constexpr int VE = Piece<T>::N, U = AU;
+__global__ void __launch_bounds__(256, 4) kv_append_vec_kernel(const AppendArgs a, int per_row) {
+    constexpr int VE = Piece<T>::N, U = 2;
     const int rows = blockDim.x / per_row, sub = threadIdx.x / per_row, t = threadIdx.x - sub * per_row;
     const int row = blockIdx.x * rows + sub;
     if (row >= a.n) return;
@@ -437,6 +437,8 @@ __global__ void __launch_bounds__(256, AB) kv_append_vec_kernel(const AppendArgs
             if (two) x1[u] = *reinterpret_cast<const uint4 *>(src + d1);
         }
     };
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
     const int slot = a.slot_map[row];
     load(h);
 
@@ -568,15 +570,13 @@ cudaError_t launch_kv_append(bool f32, const AppendArgs &a, int num_sms, cudaStr
         // few rows: a CTA for each, every head at once; many: 64 threads for a row
         const int per_row = a.n <= 4 * num_sms ? 256 : 64, rows = 256 / per_row;
         const int grid = (a.n + rows - 1) / rows;
-        if (f32) kv_append_vec_kernel<float, float><<<grid, 256, 0, st>>>(a, per_row);
-        else if (a.kv.dtype == KV_E4M3) kv_append_vec_kernel<__nv_bfloat16, __nv_fp8_e4m3><<<grid, 256, 0, st>>>(a, per_row);
-        else kv_append_vec_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 256, 0, st>>>(a, per_row);
-    } else if (f32) {
-        kv_append_kernel<float><<<a.n, 256, 0, st>>>(a);
-    } else {
-        kv_append_kernel<__nv_bfloat16><<<a.n, 256, 0, st>>>(a);
+        if (f32) return launch_chained(kv_append_vec_kernel<float, float>, grid, 256, 0, st, a, per_row);
+        if (a.kv.dtype == KV_E4M3)
+            return launch_chained(kv_append_vec_kernel<__nv_bfloat16, __nv_fp8_e4m3>, grid, 256, 0, st, a, per_row);
+        return launch_chained(kv_append_vec_kernel<__nv_bfloat16, __nv_bfloat16>, grid, 256, 0, st, a, per_row);
     }
-    return cudaGetLastError();
+    if (f32) return launch_chained(kv_append_kernel<float>, a.n, 256, 0, st, a);
+    return launch_chained(kv_append_kernel<__nv_bfloat16>, a.n, 256, 0, st, a);
 }
 
 cudaError_t launch_rope_table(float *cos_sin, int n_pos, int rot, double theta, const double *inv_freq,

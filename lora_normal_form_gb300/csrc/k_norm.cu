@@ -1,6 +1,7 @@
 // The end of a sub-block and the beginning of the next in one pass:
 //     h = residual + scale * gate * post(y),   out = pre(h).
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace scute {
 
@@ -45,6 +46,8 @@ __global__ void __launch_bounds__(256) residual_norm_kernel(const NormArgs a) {
     __shared__ float warp_sum[8];
     const long long r = blockIdx.x;
     const int d = a.d;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
     const T *y = reinterpret_cast<const T *>(a.y) + r * a.y_stride;
     for (int i = threadIdx.x; i < d; i += blockDim.x) row[i] = ld(y + i);
     float mean = 0.f, rstd = 1.f;
@@ -183,6 +186,8 @@ __global__ void __launch_bounds__(WARP || HELD ? 256 : 1024, HELD ? (FULL ? 2 : 
             }
         }
     };
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
     constexpr int HV = HELD ? NV : 1, HF = HELD && FULL ? NV : 1;
     float cw[HV][VE], pw[HV][VE], cb[HF][VE], pb[HF][VE];
     if (HELD)
@@ -304,7 +309,7 @@ bool by_vectors(const NormArgs &a) {
 }
 
 template <typename T, int NV, bool WARP, bool FULL, bool HELD>
-void launch_one(const NormArgs &a, int threads, int num_sms, cudaStream_t s) {
+cudaError_t launch_one(const NormArgs &a, int threads, int num_sms, cudaStream_t s) {
     const auto kernel = residual_norm_vec_kernel<T, NV, WARP, FULL, HELD>;
     // CTAs that reside on an SM at once, by its registers (looked up once) and threads
     static const int regs = [&] {
@@ -314,12 +319,12 @@ void launch_one(const NormArgs &a, int threads, int num_sms, cudaStream_t s) {
     const int by_regs = 65536 / (regs * threads), by_threads = 2048 / threads;
     const int per_sm = by_regs < 1 ? 1 : by_regs < by_threads ? by_regs : by_threads;
     const long long rows = WARP ? (a.n + 7) / 8 : a.n, room = (long long)num_sms * per_sm;
-    kernel<<<(int)(rows < room ? rows : room), threads, 0, s>>>(a);
+    return launch_chained(kernel, (int)(rows < room ? rows : room), threads, 0, s, a);
 }
 template <typename T, int NV, bool WARP, bool HELD>
-void launch_vec(const NormArgs &a, int threads, int num_sms, cudaStream_t s) {
-    if (a.layer || a.post_b || a.pre_b) launch_one<T, NV, WARP, true, HELD>(a, threads, num_sms, s);
-    else launch_one<T, NV, WARP, false, HELD>(a, threads, num_sms, s);
+cudaError_t launch_vec(const NormArgs &a, int threads, int num_sms, cudaStream_t s) {
+    if (a.layer || a.post_b || a.pre_b) return launch_one<T, NV, WARP, true, HELD>(a, threads, num_sms, s);
+    return launch_one<T, NV, WARP, false, HELD>(a, threads, num_sms, s);
 }
 
 template <typename T>
@@ -330,15 +335,14 @@ cudaError_t launch(const NormArgs &a, int num_sms, cudaStream_t s) {
         auto threads = [&](int nv) { return ((nvec + nv - 1) / nv + 31) / 32 * 32; };
         // a thread's factors are worth holding where it has several rows
         const bool few = a.n <= num_sms, many = a.n >= 8 * num_sms;
-        if (nvec <= 32) launch_vec<T, 1, true, false>(a, 256, num_sms, s);
-        else if (nvec <= 64) launch_vec<T, 2, true, false>(a, 256, num_sms, s);
-        else if (many && threads(1) <= 256) launch_vec<T, 1, false, true>(a, threads(1), num_sms, s);
-        else if (many && threads(2) <= 256) launch_vec<T, 2, false, true>(a, threads(2), num_sms, s);
-        else if (threads(1) <= (few ? 1024 : 256)) launch_vec<T, 1, false, false>(a, threads(1), num_sms, s);
-        else if (threads(2) <= (few ? 1024 : 512)) launch_vec<T, 2, false, false>(a, threads(2), num_sms, s);
-        else if (threads(4) <= 1024) launch_vec<T, 4, false, false>(a, threads(4), num_sms, s);
-        else if constexpr (VE == 4) launch_vec<T, 8, false, false>(a, threads(8), num_sms, s);
-        return cudaGetLastError();
+        if (nvec <= 32) return launch_vec<T, 1, true, false>(a, 256, num_sms, s);
+        if (nvec <= 64) return launch_vec<T, 2, true, false>(a, 256, num_sms, s);
+        if (many && threads(1) <= 256) return launch_vec<T, 1, false, true>(a, threads(1), num_sms, s);
+        if (many && threads(2) <= 256) return launch_vec<T, 2, false, true>(a, threads(2), num_sms, s);
+        if (threads(1) <= (few ? 1024 : 256)) return launch_vec<T, 1, false, false>(a, threads(1), num_sms, s);
+        if (threads(2) <= (few ? 1024 : 512)) return launch_vec<T, 2, false, false>(a, threads(2), num_sms, s);
+        if (threads(4) <= 1024) return launch_vec<T, 4, false, false>(a, threads(4), num_sms, s);
+        if constexpr (VE == 4) return launch_vec<T, 8, false, false>(a, threads(8), num_sms, s);
     }
     static std::atomic<unsigned long long> done{0};
     const size_t smem = sizeof(float) * a.d;
@@ -346,8 +350,7 @@ cudaError_t launch(const NormArgs &a, int num_sms, cudaStream_t s) {
         const cudaError_t e = allow_max_dynamic_smem(residual_norm_kernel<T>, done);
         if (e != cudaSuccess) return e;
     }
-    residual_norm_kernel<T><<<a.n, 256, smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_chained(residual_norm_kernel<T>, a.n, 256, smem, s, a);
 }
 
 }  // namespace
