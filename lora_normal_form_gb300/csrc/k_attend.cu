@@ -20,7 +20,7 @@ namespace scute {
 namespace {
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-constexpr int ATT_CTAS = 4;               // CTAs of an SM, at most
+constexpr int ATT_CTAS = 6;               // CTAs of an SM, at most
 constexpr int QS = 2;                     // rows whose queries may be waiting
 constexpr int MAX_STAGES = 32;
 constexpr int ROW_COST = 3;               // tiles
@@ -61,10 +61,13 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real,
                  "l"(reinterpret_cast<uint64_t>(src)), "r"(real ? 16 : 0), "l"(policy)
                  : "memory");
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
-                 "r"(real ? 16 : 0)
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "l"(policy)
                  : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
 }
 // One of the barrier's arrivals, when this thread's copies so far have arrived.
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
@@ -137,9 +140,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // quarter warp read different banks, of the keys (rows 2i and 2i + 1, four
 // neighbouring pieces of each) as of the values (rows 0, 2, 4, 6, two pieces of each).
 template <int ROW>
+__device__ __forceinline__ constexpr uint32_t turn_of(int row) {
+    return ROW == 64 ? (row >> 1 & 3) << 5 : ((row & 1) << 6) ^ ((row >> 1 & 3) << 5);
+}
+template <int ROW>
 __device__ __forceinline__ uint32_t place_of(int row, int piece) {
-    const uint32_t turn = ROW == 64 ? (row >> 1 & 3) << 5 : ((row & 1) << 6) ^ ((row >> 1 & 3) << 5);
-    return (row * ROW + piece * 16) ^ turn;
+    return (row * ROW + piece * 16) ^ turn_of<ROW>(row);
 }
 
 // ---------------------------------------------------------------- 16- and 8-bit caches
@@ -168,6 +174,10 @@ struct MmaMath {
     static constexpr int VP = DC / (8 * VE);
     static constexpr int VW = VE * ESZ / 4;               // its words
     static constexpr int OT = VE / 2;                     // 16-row output tiles of a value piece
+    // Small instances take a tile's values from shared memory at once, beside the
+    // keys; in the others they would not fit the registers (a spill goes to L2
+    // here: shared memory leaves L1 little) and come piece by piece.
+    static constexpr bool EARLY = NT == 1 && DC <= 128;
 
     const int lane, g, c;
     uint32_t qf[NT][KP][KE / 2];
@@ -240,8 +250,9 @@ struct MmaMath {
     // release() when the stage is in registers.
     template <typename F>
     __device__ __forceinline__ void tile(uint32_t kd, uint32_t vd, unsigned ok, float softcap, F release) {
-        // two accumulators, so that a product seldom waits for the one before it
-        float sc[MT][NT][4] = {}, sd[MT][NT][4] = {};
+        // two chains of products, so that one seldom waits for the one before it
+        constexpr int TWO = NT == 1;
+        float sc[MT][NT][4] = {}, sd[MT][TWO ? NT : 1][4] = {};
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -256,7 +267,7 @@ struct MmaMath {
                         const uint32_t a1 = halves_lo(w1[e]), a3 = halves_hi(w1[e]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma16816<true>(e & 1 ? sd[m][nt] : sc[m][nt], a0, a1, a2, a3, qf[nt][j][2 * e],
+                            mma16816<true>(TWO && (e & 1) ? sd[m][TWO ? nt : 0] : sc[m][nt], a0, a1, a2, a3, qf[nt][j][2 * e],
                                            qf[nt][j][2 * e + 1]);
                     }
                 } else {
@@ -264,35 +275,38 @@ struct MmaMath {
                     for (int e = 0; e < 2; ++e)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma16816<false>(e & 1 ? sd[m][nt] : sc[m][nt], w0[2 * e], w1[2 * e], w0[2 * e + 1],
+                            mma16816<false>(TWO && (e & 1) ? sd[m][TWO ? nt : 0] : sc[m][nt], w0[2 * e], w1[2 * e], w0[2 * e + 1],
                                             w1[2 * e + 1], qf[nt][j][2 * e], qf[nt][j][2 * e + 1]);
                 }
             }
-        uint32_t vr[MT][4][VP][VW];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int tok = m * 16 + 2 * c + (k & 1) + (k >> 1) * 8;
-#pragma unroll
-                for (int j = 0; j < VP; ++j) {
-                    if constexpr (VW == 4) {
-                        const uint4 x = lds16(vd + place_of<ROW>(tok, j * 8 + g));
-                        vr[m][k][j][0] = x.x, vr[m][k][j][1] = x.y, vr[m][k][j][2] = x.z, vr[m][k][j][3] = x.w;
-                    } else {
-                        const uint2 x = lds8(vd + place_of<ROW>(tok, g >> 1) + (g & 1) * 8);
-                        vr[m][k][j][0] = x.x, vr[m][k][j][1] = x.y;
-                    }
-                }
+        uint32_t vr[MT][4][EARLY ? VP : 1][VW];
+        auto values = [&](int m, int k, int j) {
+            const int tok = m * 16 + 2 * c + (k & 1) + (k >> 1) * 8;
+            uint32_t *to = vr[m][k][EARLY ? j : 0];
+            if constexpr (VW == 4) {
+                const uint4 x = lds16(vd + place_of<ROW>(tok, j * 8 + g));
+                to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w;
+            } else {
+                const uint2 x = lds8(vd + place_of<ROW>(tok, g >> 1) + (g & 1) * 8);
+                to[0] = x.x, to[1] = x.y;
             }
-        release();
+        };
+        if constexpr (EARLY) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int j = 0; j < VP; ++j) values(m, k, j);
+            release();
+        }
 
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) sc[m][nt][k] = (sc[m][nt][k] + sd[m][nt][k]) * mul[nt][k & 1];
+                for (int k = 0; k < 4; ++k) sc[m][nt][k] = (TWO ? sc[m][nt][k] + sd[m][TWO ? nt : 0][k] : sc[m][nt][k]) * mul[nt][k & 1];
         if (softcap > 0.f) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -370,11 +384,15 @@ struct MmaMath {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int j = 0; j < VP; ++j)
+            for (int j = 0; j < VP; ++j) {
+                if constexpr (!EARLY) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) values(m, k, j);
+                }
 #pragma unroll
                 for (int i = 0; i < VW; ++i) {
-                    const uint32_t x0 = vr[m][0][j][i], x1 = vr[m][1][j][i];
-                    const uint32_t x2 = vr[m][2][j][i], x3 = vr[m][3][j][i];
+                    const uint32_t x0 = vr[m][0][EARLY ? j : 0][i], x1 = vr[m][1][EARLY ? j : 0][i];
+                    const uint32_t x2 = vr[m][2][EARLY ? j : 0][i], x3 = vr[m][3][EARLY ? j : 0][i];
                     if constexpr (FP8) {
                         const uint32_t y0 = __byte_perm(x0, x1, 0x5140), y1 = __byte_perm(x0, x1, 0x7362);
                         const uint32_t y2 = __byte_perm(x2, x3, 0x5140), y3 = __byte_perm(x2, x3, 0x7362);
@@ -397,6 +415,8 @@ struct MmaMath {
                         }
                     }
                 }
+            }
+        if constexpr (!EARLY) release();
     }
     // The warp's maximum and sum of every head, to m and l.
     __device__ __forceinline__ void stats(float *m, float *l) {
@@ -601,6 +621,7 @@ __device__ __forceinline__ void plan_places(const AttendArgs &a, int tt, int *pl
     const int per = (n + threads - 1) / threads, r0 = min(n, t * per), r1 = min(n, r0 + per);
     int mine = 0;
     bool any = false;
+#pragma unroll 8
     for (int r = r0; r < r1; ++r) {
         int first, len;
         bool bad;
@@ -733,73 +754,78 @@ __device__ __forceinline__ void put(const AttendArgs &a, int r, int h, int d, fl
 struct SharedRow {
     int r, hk, h0, nh, c0, c1;          // request, heads; its first and last CTA
 };
-// Join the parts of up to two rows (row i: shared[i] where last[i]): as many
-// parts at a time as `room` bytes of shared memory hold, brought there at once.
-template <typename IO, int HC, int DC, int THREADS>
+// Join the parts of up to two rows, as many parts at a time as `room` bytes of
+// shared memory hold, brought there at once; those of both rows where they fit.
+template <typename IO, int THREADS>
 __device__ __forceinline__ void join_parts(const AttendArgs &a, const SharedRow &head, const SharedRow &tail, bool last_head,
                                            bool last_tail, uint8_t *buf, int room, int t) {
-    constexpr int IT = (HC * DC / 4 + THREADS - 1) / THREADS;      // groups of four outputs of a thread
+    constexpr int IT = 4;                // groups of four outputs of a thread at a time
     const int D = a.kv.dim, n_head = last_head ? head.c1 - head.c0 + 1 : 0, n_tail = last_tail ? tail.c1 - tail.c0 + 1 : 0;
     const int nh = max(last_head ? head.nh : 0, last_tail ? tail.nh : 0);
-    const int bytes = (2 * ATT_HEADS + nh * D) * 4, pieces = bytes / 16, cap = room / bytes;
-    float m[2][IT], l[2][IT];
-    float4 x[2][IT];
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-        for (int i = 0; i < IT; ++i) m[w][i] = -INFINITY, l[w][i] = 0.f, x[w][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = 0; p0 < n_head + n_tail; p0 += cap) {
-        const int p1 = min(p0 + cap, n_head + n_tail);
+    const int bytes = (2 * ATT_HEADS + nh * D) * 4, pieces = bytes / 16, cap = room / bytes, ld = bytes / 4;
+    auto bring = [&](int p0, int p1) {   // of the two rows' parts in turn
         sync_threads<THREADS>();
         for (int at = p0; at < p1; ++at) {
             const int k = at < n_head ? at : at - n_head, c0 = at < n_head ? head.c0 : tail.c0;
             const float *from = part_of(a, k ? 2 * (c0 + k) : 2 * c0 + 1).m;
             const uint32_t to = ptx::smem_u32(buf) + (at - p0) * bytes;
-            for (int e = t; e < pieces; e += THREADS) copy16(to + e * 16, from + e * 4, true);
+            for (int e = t; e < pieces; e += THREADS) copy16(to + e * 16, from + e * 4);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         sync_threads<THREADS>();
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            const int from = max(w ? n_head : 0, p0), to = min(w ? n_head + n_tail : n_head, p1);
-            const int items = (w ? tail.nh : head.nh) * (D / 4);
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const int e = t + i * THREADS;
-                if (e >= items || from >= to) break;
-                const float *part = reinterpret_cast<const float *>(buf + (from - p0) * bytes), *pm = part + e / (D / 4);
-                const int ld = bytes / 4, k1 = to - from;
-                float top = m[w][i];
-#pragma unroll 4
-                for (int k = 0; k < k1; ++k) top = fmaxf(top, pm[k * ld]);
-                if (top == -INFINITY) continue;
-                const float f = pow2(m[w][i] - top);
-                float4 z = x[w][i];
-                float sum = l[w][i] * f;
-                z.x *= f, z.y *= f, z.z *= f, z.w *= f;
-#pragma unroll 2
-                for (int k = 0; k < k1; ++k) {
-                    const float g = pow2(pm[k * ld] - top);
-                    const float4 y = *reinterpret_cast<const float4 *>(part + k * ld + 2 * ATT_HEADS + 4 * e);
-                    sum += pm[k * ld + ATT_HEADS] * g;
-                    z.x += y.x * g, z.y += y.y * g, z.z += y.z * g, z.w += y.w * g;
-                }
-                m[w][i] = top, l[w][i] = sum, x[w][i] = z;
-            }
-        }
-    }
-#pragma unroll
+    };
+    const bool once = n_head + n_tail <= cap;
+    if (once) bring(0, n_head + n_tail);
+#pragma unroll 1
     for (int w = 0; w < 2; ++w) {
         if (!(w ? last_tail : last_head)) continue;
         const SharedRow &row = w ? tail : head;
+        const int q0 = w ? n_head : 0, q1 = w ? n_head + n_tail : n_head, items = row.nh * (D / 4);
         const float vs = a.kv.v_scale ? a.kv.v_scale[row.hk] : 1.f;
+#pragma unroll 1
+        for (int g0 = 0; g0 < items; g0 += IT * THREADS) {
+            float m[IT], l[IT];
+            float4 x[IT];
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int e = t + i * THREADS;
-            if (e >= row.nh * (D / 4)) break;
-            const int h = e / (D / 4), d = 4 * (e - h * (D / 4));
-            put<IO>(a, row.r, row.h0 + h, d, x[w][i], l[w][i] == 0.f ? 0.f : vs / l[w][i]);
-            if (a.lse && d == 0) a.lse[(long long)row.r * a.q_heads + row.h0 + h] = (m[w][i] + log2f(l[w][i])) * LN2;
+            for (int i = 0; i < IT; ++i) m[i] = -INFINITY, l[i] = 0.f, x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int p0 = q0; p0 < q1; p0 += cap) {
+                const int p1 = once ? q1 : min(p0 + cap, q1);
+                if (!once) bring(p0, p1);
+                const float *parts = reinterpret_cast<const float *>(buf) + (once ? q0 * ld : 0);
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                    const int e = g0 + t + i * THREADS;
+                    if (e >= items) break;
+                    const float *pm = parts + e / (D / 4);
+                    const int k1 = p1 - p0;
+                    float top = m[i];
+#pragma unroll 4
+                    for (int k = 0; k < k1; ++k) top = fmaxf(top, pm[k * ld]);
+                    if (top == -INFINITY) continue;
+                    const float f = pow2(m[i] - top);
+                    float4 z = x[i];
+                    float sum = l[i] * f;
+                    z.x *= f, z.y *= f, z.z *= f, z.w *= f;
+#pragma unroll 2
+                    for (int k = 0; k < k1; ++k) {
+                        const float g = pow2(pm[k * ld] - top);
+                        const float4 y = *reinterpret_cast<const float4 *>(parts + k * ld + 2 * ATT_HEADS + 4 * e);
+                        sum += pm[k * ld + ATT_HEADS] * g;
+                        z.x += y.x * g, z.y += y.y * g, z.z += y.z * g, z.w += y.w * g;
+                    }
+                    m[i] = top, l[i] = sum, x[i] = z;
+                }
+                if (once) break;
+            }
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int e = g0 + t + i * THREADS;
+                if (e >= items) break;
+                const int h = e / (D / 4), d = 4 * (e - h * (D / 4));
+                put<IO>(a, row.r, row.h0 + h, d, x[i], l[i] == 0.f ? 0.f : vs / l[i]);
+                if (a.lse && d == 0) a.lse[(long long)row.r * a.q_heads + row.h0 + h] = (m[i] + log2f(l[i])) * LN2;
+            }
         }
     }
 }
@@ -902,7 +928,7 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
                     constexpr int QE = 16 / sizeof(IO);
                     const IO *q = reinterpret_cast<const IO *>(a.q) + r * a.q_stride + (long long)h0 * D;
                     for (int i = lane; i < nh * D / QE; i += 32)
-                        copy16(ptx::smem_u32(s_q + qst * S::Q_BYTES) + i * 16, q + i * QE, true);
+                        copy16(ptx::smem_u32(s_q + qst * S::Q_BYTES) + i * 16, q + i * QE);
                     copies_arrive(q_full(qst));
                 }
                 if (++qst == QS) qst = 0, qph ^= 1;
@@ -941,26 +967,27 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
                         const long long place0 = __shfl_sync(0xffffffffu, place, m * TT);
                         const bool one_page = __all_sync(
                             0xffffffffu, lane / TT != m || i >= stop || place == place0 + (lane - m * TT) * tok_bytes);
+                        const int rows = place0 >= 0 ? min(TT, stop - (pos + k * 32 + m * TT)) : 0;
 #pragma unroll
                         for (int cs = 0; cs < CS; ++cs) {
                             const int piece = cs * LR + lane % LR;
                             const bool in_row = piece * 16 < row_bytes;
-                            if (one_page) {
-                                const int rows = place0 >= 0 ? min(TT, stop - (pos + k * 32 + m * TT)) : 0;
-                                const long long from = place0 >= 0 ? place0 + row0 * tok_bytes + piece * 16 : 0;
-                                const char *ks = kb + from, *vs = vb + from;
+                            // row n * RI + row0 lies at n * RI rows from row0's place, but for
+                            // the permutation, whose bits of the two add up
+                            const uint32_t lane_at = place_of<M::ROW>(row0, piece);
+                            const long long from = place0 >= 0 ? place0 + row0 * tok_bytes + piece * 16 : 0;
+                            const char *ks = kb + from, *vs = vb + from;
+                            if (one_page && rows == TT && row_bytes == M::ROW) {
 #pragma unroll
                                 for (int n = 0; n < TT / RI; ++n) {
-                                    const int row = n * RI + row0;
-                                    const bool real = in_row && row < rows;
-                                    const uint32_t to = place_of<M::ROW>(row, piece);
-                                    copy16(kd + to, real ? ks : kb, real, policy);
-                                    copy16(vd + to, real ? vs : vb, real, policy);
+                                    const uint32_t to = n * RI * M::ROW + (lane_at ^ turn_of<M::ROW>(n * RI));
+                                    copy16(kd + to, ks, policy);
+                                    copy16(vd + to, vs, policy);
                                     ks += RI * tok_bytes;
                                     vs += RI * tok_bytes;
                                 }
                             } else {
-#pragma unroll
+#pragma unroll 2
                                 for (int n = 0; n < TT / RI; ++n) {
                                     const int row = n * RI + row0;
                                     const long long p = __shfl_sync(0xffffffffu, place, m * TT + row);
@@ -1089,7 +1116,7 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
     sync_threads<CW * 32>();
     const bool last_head = s_last[0], last_tail = s_last[1];
     if (last_head || last_tail)          // the ring is empty by now
-        join_parts<IO, HC, DC, CW * 32>(a, head, tail, last_head, last_tail, s_ring, stages * S::STAGE, t);
+        join_parts<IO, CW * 32>(a, head, tail, last_head, last_tail, s_ring, stages * S::STAGE, t);
 }
 
 template <typename M, int DC, int CW, int PW, int CTAS>
@@ -1117,7 +1144,7 @@ template <bool FP8>
 cudaError_t launch_mma(const AttendArgs &a, int num_sms, cudaStream_t st) {
     const int D = a.kv.dim;
     const bool wide = a.group > 8;
-    if (D > 128) return launch_shape<MmaMath<FP8, 256, 1>, 256, 4, 2, 2>(a, num_sms, st);
+    if (D > 128) return launch_shape<MmaMath<FP8, 256, 1>, 256, 2, 2, 2>(a, num_sms, st);
     if (D > 64)
         return wide ? launch_shape<MmaMath<FP8, 128, 2>, 128, 4, 2, 2>(a, num_sms, st)
                     : launch_shape<MmaMath<FP8, 128, 1>, 128, 2, 1, 4>(a, num_sms, st);
@@ -1140,7 +1167,7 @@ int attend_ctrs(int num_sms) { return num_sms * ATT_CTAS; }
 cudaError_t launch_attend(const AttendArgs &a, int num_sms, cudaStream_t st) {
     if (a.kv.dtype == KV_BF16) return launch_mma<false>(a, num_sms, st);
     if (a.kv.dtype == KV_E4M3) return launch_mma<true>(a, num_sms, st);
-    if (a.kv.dim <= 64) return launch_fma<64, 2, 1, 4>(a, num_sms, st);
+    if (a.kv.dim <= 64) return launch_fma<64, 2, 1, 6>(a, num_sms, st);
     if (a.kv.dim <= 128) return launch_fma<128, 2, 1, 4>(a, num_sms, st);
     return launch_fma<256, 4, 2, 2>(a, num_sms, st);
 }
