@@ -884,6 +884,10 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
         }
         ptx::fence_mbar_init();
     }
+    // behind a head's elements every row of a stage stays zero
+    if (row_bytes < M::ROW)
+        for (int i = threadIdx.x; i < stages * S::STAGE / 16; i += S::THREADS)
+            reinterpret_cast<uint4 *>(s_ring)[i] = make_uint4(0, 0, 0, 0);
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     plan_places(a, TT, places_at, s_warp);
@@ -977,24 +981,27 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
                             const uint32_t lane_at = place_of<M::ROW>(row0, piece);
                             const long long from = place0 >= 0 ? place0 + row0 * tok_bytes + piece * 16 : 0;
                             const char *ks = kb + from, *vs = vb + from;
-                            if (one_page && rows == TT && row_bytes == M::ROW) {
+                            if (one_page && rows == TT) {
+                                if (in_row)              // the rest is zero for good
 #pragma unroll
-                                for (int n = 0; n < TT / RI; ++n) {
-                                    const uint32_t to = n * RI * M::ROW + (lane_at ^ turn_of<M::ROW>(n * RI));
-                                    copy16(kd + to, ks, policy);
-                                    copy16(vd + to, vs, policy);
-                                    ks += RI * tok_bytes;
-                                    vs += RI * tok_bytes;
-                                }
+                                    for (int n = 0; n < TT / RI; ++n) {
+                                        const uint32_t to = n * RI * M::ROW + (lane_at ^ turn_of<M::ROW>(n * RI));
+                                        copy16(kd + to, ks, policy);
+                                        copy16(vd + to, vs, policy);
+                                        ks += RI * tok_bytes;
+                                        vs += RI * tok_bytes;
+                                    }
                             } else {
 #pragma unroll 2
                                 for (int n = 0; n < TT / RI; ++n) {
                                     const int row = n * RI + row0;
                                     const long long p = __shfl_sync(0xffffffffu, place, m * TT + row);
-                                    const bool real = in_row && p >= 0;
+                                    const bool real = p >= 0;
                                     const uint32_t to = place_of<M::ROW>(row, piece);
-                                    copy16(kd + to, real ? kb + p + piece * 16 : kb, real, policy);
-                                    copy16(vd + to, real ? vb + p + piece * 16 : vb, real, policy);
+                                    if (in_row) {
+                                        copy16(kd + to, real ? kb + p + piece * 16 : kb, real, policy);
+                                        copy16(vd + to, real ? vb + p + piece * 16 : vb, real, policy);
+                                    }
                                 }
                             }
                         }
