@@ -902,6 +902,8 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
         // before this one's rows are sent for.
         constexpr int SPAN = 128;
         const uint64_t policy = ptx::make_policy_evict_first();
+        // pages in which a tile of 32 tokens mostly lies at once
+        const bool whole_tiles = TT <= 16 || a.kv.page_size % TT == 0;
         const long long tok_bytes = a.kv.token_stride * ESZ;
         int hk = w.hk, z = w.z, r = w.r, stop = w.to(), pos = w.from();
         bool opens = true, more = w.more();
@@ -967,40 +969,54 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
                         // lanes of a row, rows of an instruction, and its instructions where it is longer
                         constexpr int LR = M::ROW >= 512 ? 32 : M::ROW / 16, RI = 32 / LR, CS = M::ROW / 16 / LR;
                         const int row0 = lane / LR;
-                        // a tile inside one page steps by the token's stride
-                        const long long place0 = __shfl_sync(0xffffffffu, place, m * TT);
-                        const bool one_page = __all_sync(
-                            0xffffffffu, lane / TT != m || i >= stop || place == place0 + (lane - m * TT) * tok_bytes);
-                        const int rows = place0 >= 0 ? min(TT, stop - (pos + k * 32 + m * TT)) : 0;
+                        // rows of the tile that lie in one page step by the token's stride
+                        auto one_page = [&](int f, int count) {        // tokens f .. of the 32
+                            const long long place0 = __shfl_sync(0xffffffffu, place, f);
+                            return place0 >= 0 && pos + k * 32 + f + count <= stop &&
+                                   __all_sync(0xffffffffu, lane / count != f / count ||
+                                                               place == place0 + (lane - f) * tok_bytes);
+                        };
+                        auto send = [&](int f, int n0, int n1) {
+                            const long long from = __shfl_sync(0xffffffffu, place, f) + row0 * tok_bytes;
 #pragma unroll
-                        for (int cs = 0; cs < CS; ++cs) {
-                            const int piece = cs * LR + lane % LR;
-                            const bool in_row = piece * 16 < row_bytes;
-                            // row n * RI + row0 lies at n * RI rows from row0's place, but for
-                            // the permutation, whose bits of the two add up
-                            const uint32_t lane_at = place_of<M::ROW>(row0, piece);
-                            const long long from = place0 >= 0 ? place0 + row0 * tok_bytes + piece * 16 : 0;
-                            const char *ks = kb + from, *vs = vb + from;
-                            if (one_page && rows == TT) {
-                                if (in_row)              // the rest is zero for good
+                            for (int cs = 0; cs < CS; ++cs) {
+                                const int piece = cs * LR + lane % LR;
+                                if (piece * 16 >= row_bytes) continue;           // zero for good
+                                // row n * RI + row0 lies n * RI rows from row0's place, but for
+                                // the permutation, whose bits of the two add up
+                                const uint32_t lane_at = place_of<M::ROW>(row0, piece);
+                                const char *ks = kb + from + piece * 16, *vs = vb + from + piece * 16;
 #pragma unroll
-                                    for (int n = 0; n < TT / RI; ++n) {
-                                        const uint32_t to = n * RI * M::ROW + (lane_at ^ turn_of<M::ROW>(n * RI));
-                                        copy16(kd + to, ks, policy);
-                                        copy16(vd + to, vs, policy);
-                                        ks += RI * tok_bytes;
-                                        vs += RI * tok_bytes;
-                                    }
-                            } else {
+                                for (int n = n0; n < n1; ++n) {
+                                    const uint32_t to = n * RI * M::ROW + (lane_at ^ turn_of<M::ROW>(n * RI));
+                                    copy16(kd + to, ks, policy);
+                                    copy16(vd + to, vs, policy);
+                                    ks += RI * tok_bytes;
+                                    vs += RI * tok_bytes;
+                                }
+                            }
+                        };
+                        constexpr int SUB = TT < 16 ? TT : 16;
+                        if (whole_tiles && one_page(m * TT, TT)) {
+                            send(m * TT, 0, TT / RI);
+                        } else {
+#pragma unroll
+                            for (int u = 0; u < TT / SUB; ++u) {
+                                if ((TT > SUB || !whole_tiles) && one_page(m * TT + u * SUB, SUB)) {
+                                    send(m * TT + u * SUB, u * SUB / RI, (u + 1) * SUB / RI);
+                                    continue;
+                                }
 #pragma unroll 2
-                                for (int n = 0; n < TT / RI; ++n) {
+                                for (int n = u * SUB / RI; n < (u + 1) * SUB / RI; ++n) {
                                     const int row = n * RI + row0;
                                     const long long p = __shfl_sync(0xffffffffu, place, m * TT + row);
-                                    const bool real = p >= 0;
-                                    const uint32_t to = place_of<M::ROW>(row, piece);
-                                    if (in_row) {
-                                        copy16(kd + to, real ? kb + p + piece * 16 : kb, real, policy);
-                                        copy16(vd + to, real ? vb + p + piece * 16 : vb, real, policy);
+#pragma unroll
+                                    for (int cs = 0; cs < CS; ++cs) {
+                                        const int piece = cs * LR + lane % LR;
+                                        if (piece * 16 >= row_bytes) continue;
+                                        const uint32_t to = place_of<M::ROW>(row, piece);
+                                        copy16(kd + to, p >= 0 ? kb + p + piece * 16 : kb, p >= 0, policy);
+                                        copy16(vd + to, p >= 0 ? vb + p + piece * 16 : vb, p >= 0, policy);
                                     }
                                 }
                             }
