@@ -610,7 +610,7 @@ struct FmaMath {
 // tile all the same; places_at[r] = places of one row of each request before r.
 __device__ __forceinline__ void seen_of(const AttendArgs &a, int r, int *first, int *len, bool *bad) {
     const int cap = a.kv.table_cols * a.kv.page_size;
-    int n = __ldg(a.kv_len + r);
+    int n = a.kv_len[r];
     *bad = n < 0 || n > cap;
     n = n < 0 ? 0 : n > cap ? cap : n;
     *len = n;
@@ -912,7 +912,7 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
 #pragma unroll
             for (int k = 0; k < SPAN / 32; ++k) {
                 const int i = from + k * 32 + lane;
-                page[k] = i < until ? __ldg(table + (a.page_shift >= 0 ? i >> a.page_shift : i / a.kv.page_size)) : -1;
+                page[k] = i < until ? table[a.page_shift >= 0 ? i >> a.page_shift : i / a.kv.page_size] : -1;
             }
         };
         int page[SPAN / 32];
