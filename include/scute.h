@@ -481,7 +481,8 @@ scute_status scute_paged_attention(scute_ctx *ctx, const scute_kv_cache *kv, con
  * out and residual_out are each rounded once (pre reads h before its rounding).
  *   y, residual, out, residual_out   context dtype, rows of d elements their
  *              stride apart; residual NULL counts as zeros; residual_out
- *              (NULL: not written) may be residual; out NULL: no norm after;
+ *              (NULL: not written) may be residual; out may be y (NULL: no norm
+ *              after);
  *   post_w, post_b, pre_w, pre_b   device float [d]; post_w NULL: no norm of
  *              y (post_b must then be NULL); pre_w NULL: ones; biases NULL: zeros;
  *   gate_vec   NULL, or device float [d]; gate_rows NULL, or context dtype

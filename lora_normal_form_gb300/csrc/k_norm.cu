@@ -111,16 +111,17 @@ template <> struct Vec<__nv_bfloat16> {
 
 // The row in registers: a row's threads hold NV 16-byte vectors each.  WARP: a
 // warp for a row and shuffles alone; otherwise a CTA for a row.  The launch has
-// as many CTAs as reside, and each fetches its next row before it is done with
-// the one it has (rows that fill the registers: after).  FULL: with means taken
+// as many CTAs as reside, and each fetches its next row or two before it is done
+// with the one it has (rows that fill the registers: after).  FULL: with means taken
 // off or biases.  HELD: a thread keeps its columns' factors from row to row, post_w,
 // the gate and the scale as one; fetched anew for every row they are half of all
 // that passes through L1.
 template <typename T, int NV, bool WARP, bool FULL, bool HELD>
-__global__ void __launch_bounds__(WARP || HELD ? 256 : 1024, HELD ? (FULL ? 2 : 3) : 1)
+__global__ void __launch_bounds__(WARP || HELD ? 256 : 1024, HELD ? 2 : 1)
     residual_norm_vec_kernel(const NormArgs a) {
     constexpr int VE = Vec<T>::N;
-    constexpr bool AHEAD = NV <= 2;
+    constexpr int AHEAD = HELD ? 2 : NV <= 2 ? 1 : 0;      // rows fetched ahead
+    constexpr int BUF = AHEAD == 2 ? 2 : 1;
     __shared__ float red[2][32];
     const int d = a.d, nvec = d / VE;
     const int per_row = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
@@ -198,31 +199,30 @@ __global__ void __launch_bounds__(WARP || HELD ? 256 : 1024, HELD ? (FULL ? 2 : 
                 h_factors((v * per_row + t) * VE, pw[v], pb[FULL ? v : 0]);
             }
 
-    uint4 y_in[NV], r_in[NV];          // the next row, as stored
-    auto fetch = [&](long long r) {
+    uint4 y_in[BUF][NV], r_in[BUF][NV];          // rows as stored
+    auto fetch = [&](int b, long long r) {
         const T *y = reinterpret_cast<const T *>(a.y) + r * a.y_stride;
         const T *rs = reinterpret_cast<const T *>(a.residual) + r * a.residual_stride;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int i = v * per_row + t;
-            y_in[v] = r_in[v] = make_uint4(0, 0, 0, 0);
+            y_in[b][v] = r_in[b][v] = make_uint4(0, 0, 0, 0);
             if (i < nvec) {
-                y_in[v] = *reinterpret_cast<const uint4 *>(y + i * VE);
-                if (a.residual) r_in[v] = *reinterpret_cast<const uint4 *>(rs + i * VE);
+                y_in[b][v] = *reinterpret_cast<const uint4 *>(y + i * VE);
+                if (a.residual) r_in[b][v] = *reinterpret_cast<const uint4 *>(rs + i * VE);
             }
         }
     };
     long long r = WARP ? (long long)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
-    if (r < a.n) fetch(r);
-    for (; r < a.n; r += step) {
+    auto one_row = [&](int b) {
         float x[NV][VE];
         uint4 res[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            Vec<T>::open(y_in[v], x[v]);
-            res[v] = r_in[v];
+            Vec<T>::open(y_in[b][v], x[v]);
+            res[v] = r_in[b][v];
         }
-        if (AHEAD && r + step < a.n) fetch(r + step);
+        if (AHEAD && r + AHEAD * step < a.n) fetch(b, r + AHEAD * step);
         // (mean, 1 / deviation); the squares are summed after the mean is taken off
         auto stats = [&](float *mean, float *rstd) {
             float m = 0.f, q = 0.f;
@@ -289,7 +289,17 @@ __global__ void __launch_bounds__(WARP || HELD ? 256 : 1024, HELD ? (FULL ? 2 : 
                 Vec<T>::store(reinterpret_cast<T *>(a.out) + r * a.out_stride + i * VE, x[v]);
             }
         }
-        if (!AHEAD && r + step < a.n) fetch(r + step);
+        if (!AHEAD && r + step < a.n) fetch(b, r + step);
+    };
+    if (r < a.n) fetch(0, r);
+    if (BUF == 2 && r + step < a.n) fetch(BUF - 1, r + step);
+    while (r < a.n) {
+        one_row(0);
+        r += step;
+        if (BUF == 2 && r < a.n) {
+            one_row(BUF - 1);
+            r += step;
+        }
     }
 }
 
