@@ -122,12 +122,16 @@ __global__ void __launch_bounds__(WARP || HELD ? 256 : 1024, HELD ? 2 : 1)
     constexpr int VE = Vec<T>::N;
     constexpr int AHEAD = HELD ? 2 : NV <= 2 ? 1 : 0;      // rows fetched ahead
     constexpr int BUF = AHEAD == 2 ? 2 : 1;
-    __shared__ float red[2][32];
+    __shared__ __align__(16) float red[2][32];
     const int d = a.d, nvec = d / VE;
     const int per_row = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
     const int step = WARP ? gridDim.x * 8 : gridDim.x;
     const float inv_d = 1.f / d;
     int turn = 0;
+    if (HELD) {
+        if (threadIdx.x < 64) red[threadIdx.x >> 5][threadIdx.x & 31] = 0.f;
+        __syncthreads();
+    }
     auto row_sum = [&](float x) -> float {
 #pragma unroll
         for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -135,12 +139,12 @@ __global__ void __launch_bounds__(WARP || HELD ? 256 : 1024, HELD ? 2 : 1)
         // two buffers in turn: a warp can be one sum ahead of the slowest, not two
         if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = x;
         __syncthreads();
-        const int warps = blockDim.x >> 5;
         float s = 0.f;
-        if (HELD) {           // eight warps at most
-            for (int w = 0; w < warps; ++w) s += red[turn][w];
+        if (HELD) {           // eight warps at most; the places of those there are not stay zero
+            const float4 p = *reinterpret_cast<const float4 *>(red[turn]), q = *reinterpret_cast<const float4 *>(red[turn] + 4);
+            s = (p.x + p.y) + (p.z + p.w) + ((q.x + q.y) + (q.z + q.w));
         } else {
-            s = (threadIdx.x & 31) < warps ? red[turn][threadIdx.x & 31] : 0.f;
+            s = (threadIdx.x & 31) < (blockDim.x >> 5) ? red[turn][threadIdx.x & 31] : 0.f;
 #pragma unroll
             for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         }
