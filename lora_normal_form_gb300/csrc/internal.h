@@ -413,6 +413,7 @@ struct AppendArgs {
     int rot, interleaved, n_axes, n_pos;   // rot 0: no turning
     int bound[4];                          // pairs before the end of each axis's section
     const float *cos_sin;
+    int table16;                           // its rows may be read 16 bytes at a time
     const int32_t *positions;
     long long axis_stride;
     int *status;

@@ -759,18 +759,27 @@ struct SharedRow {
 template <typename IO, int THREADS>
 __device__ __forceinline__ void join_parts(const AttendArgs &a, const SharedRow &head, const SharedRow &tail, bool last_head,
                                            bool last_tail, uint8_t *buf, int room, int t) {
-    constexpr int IT = 4;                // groups of four outputs of a thread at a time
+    constexpr int IT = 2;                // groups of four outputs of a thread at a time
     const int D = a.kv.dim, n_head = last_head ? head.c1 - head.c0 + 1 : 0, n_tail = last_tail ? tail.c1 - tail.c0 + 1 : 0;
     const int nh = max(last_head ? head.nh : 0, last_tail ? tail.nh : 0);
     const int bytes = (2 * ATT_HEADS + nh * D) * 4, pieces = bytes / 16, cap = room / bytes, ld = bytes / 4;
+    auto bring_row = [&](int c0, int k0, int k1, uint32_t to) {      // a row's parts k0 .. k1
+        for (int e = t; e < pieces; e += THREADS) {
+            const float *from = part_of(a, 2 * (c0 + k0)).m + e * 4;
+            uint32_t at = to + e * 16;
+#pragma unroll 4
+            for (int k = k0; k < k1; ++k) {
+                copy16(at, k ? from : from + PART_FLOATS);           // the first one's is its CTA's second slot
+                at += bytes;
+                from += 2 * PART_FLOATS;
+            }
+        }
+    };
     auto bring = [&](int p0, int p1) {   // of the two rows' parts in turn
         sync_threads<THREADS>();
-        for (int at = p0; at < p1; ++at) {
-            const int k = at < n_head ? at : at - n_head, c0 = at < n_head ? head.c0 : tail.c0;
-            const float *from = part_of(a, k ? 2 * (c0 + k) : 2 * c0 + 1).m;
-            const uint32_t to = ptx::smem_u32(buf) + (at - p0) * bytes;
-            for (int e = t; e < pieces; e += THREADS) copy16(to + e * 16, from + e * 4);
-        }
+        const uint32_t to = ptx::smem_u32(buf);
+        if (p0 < n_head) bring_row(head.c0, p0, min(p1, n_head), to);
+        if (p1 > n_head) bring_row(tail.c0, max(p0 - n_head, 0), p1 - n_head, to + max(n_head - p0, 0) * bytes);
         asm volatile("cp.async.wait_all;" ::: "memory");
         sync_threads<THREADS>();
     };
@@ -793,29 +802,40 @@ __device__ __forceinline__ void join_parts(const AttendArgs &a, const SharedRow 
                 const int p1 = once ? q1 : min(p0 + cap, q1);
                 if (!once) bring(p0, p1);
                 const float *parts = reinterpret_cast<const float *>(buf) + (once ? q0 * ld : 0);
+                // the groups side by side, so that their loads overlap (past the row's
+                // end the last one's again)
+                const int k1 = p1 - p0;
+                const float *pm[IT];
+                float top[IT];
 #pragma unroll
                 for (int i = 0; i < IT; ++i) {
-                    const int e = g0 + t + i * THREADS;
-                    if (e >= items) break;
-                    const float *pm = parts + e / (D / 4);
-                    const int k1 = p1 - p0;
-                    float top = m[i];
-#pragma unroll 4
-                    for (int k = 0; k < k1; ++k) top = fmaxf(top, pm[k * ld]);
-                    if (top == -INFINITY) continue;
-                    const float f = pow2(m[i] - top);
-                    float4 z = x[i];
-                    float sum = l[i] * f;
-                    z.x *= f, z.y *= f, z.z *= f, z.w *= f;
-#pragma unroll 2
-                    for (int k = 0; k < k1; ++k) {
-                        const float g = pow2(pm[k * ld] - top);
-                        const float4 y = *reinterpret_cast<const float4 *>(parts + k * ld + 2 * ATT_HEADS + 4 * e);
-                        sum += pm[k * ld + ATT_HEADS] * g;
-                        z.x += y.x * g, z.y += y.y * g, z.z += y.z * g, z.w += y.w * g;
-                    }
-                    m[i] = top, l[i] = sum, x[i] = z;
+                    const int e = min(g0 + t + i * THREADS, items - 1);
+                    pm[i] = parts + e / (D / 4);
+                    top[i] = m[i];
                 }
+#pragma unroll 4
+                for (int k = 0; k < k1; ++k)
+#pragma unroll
+                    for (int i = 0; i < IT; ++i) top[i] = fmaxf(top[i], pm[i][k * ld]);
+                float ref[IT];
+                const float4 *py[IT];
+#pragma unroll
+                for (int i = 0; i < IT; ++i) {
+                    ref[i] = top[i] == -INFINITY ? 0.f : top[i];
+                    py[i] = reinterpret_cast<const float4 *>(parts + 2 * ATT_HEADS) + min(g0 + t + i * THREADS, items - 1);
+                    const float f = pow2(m[i] - ref[i]);
+                    l[i] *= f, x[i].x *= f, x[i].y *= f, x[i].z *= f, x[i].w *= f;
+                    m[i] = top[i];
+                }
+#pragma unroll 4
+                for (int k = 0; k < k1; ++k)
+#pragma unroll
+                    for (int i = 0; i < IT; ++i) {
+                        const float g = pow2(pm[i][k * ld] - ref[i]);
+                        const float4 y = py[i][k * (ld / 4)];
+                        l[i] += pm[i][k * ld + ATT_HEADS] * g;
+                        x[i].x += y.x * g, x[i].y += y.y * g, x[i].z += y.z * g, x[i].w += y.w * g;
+                    }
                 if (once) break;
             }
 #pragma unroll

@@ -419,12 +419,12 @@ __global__ void __launch_bounds__(256, 4) kv_append_vec_kernel(const AppendArgs 
     const int d0 = (two ? item : item + joined) * VE, d1 = d0 + half;
     const bool turned = two || (a.interleaved && d0 < a.rot);
 
-    // a head's row in q, k or v
+    // the row in q, k and v, and a head's in one of them
+    const T *const q_row = reinterpret_cast<const T *>(a.q) + row * a.q_stride;
+    const T *const k_row = reinterpret_cast<const T *>(a.k) + row * a.k_stride - a.q_heads * dim;
+    const T *const v_row = reinterpret_cast<const T *>(a.v) + row * a.v_stride - (a.q_heads + a.kv.heads) * dim;
     auto source = [&](int hh) -> const T * {
-        const bool q = hh < a.q_heads, k = hh < a.q_heads + a.kv.heads;
-        const T *base = reinterpret_cast<const T *>(q ? a.q : k ? a.k : a.v);
-        const long long ld = q ? a.q_stride : k ? a.k_stride : a.v_stride;
-        return base + row * ld + (hh - (q ? 0 : k ? a.q_heads : a.q_heads + a.kv.heads)) * dim;
+        return (hh < a.q_heads ? q_row : hh < a.q_heads + a.kv.heads ? k_row : v_row) + hh * dim;
     };
     uint4 x0[U], x1[U];
     auto load = [&](int from) {
@@ -446,24 +446,38 @@ __global__ void __launch_bounds__(256, 4) kv_append_vec_kernel(const AppendArgs 
     float c[VE], s[VE];
     if (turned) {
         const int pairs = two ? VE : VE / 2, p0 = two ? d0 : d0 / 2;
-        int last_ax = -1;
-        long long base = 0;
+        auto axis_of = [&](int i) { return (i >= a.bound[0]) + (i >= a.bound[1]) + (i >= a.bound[2]); };
         bool bad = false;
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            if (e >= pairs) break;
-            const int i = p0 + e, ax = (i >= a.bound[0]) + (i >= a.bound[1]) + (i >= a.bound[2]);
-            if (ax != last_ax) {
-                int p = a.positions[ax * a.axis_stride + row];
-                if (p < 0 || p >= a.n_pos) {
-                    bad = true;
-                    p = p < 0 ? 0 : a.n_pos - 1;
-                }
-                base = (long long)p * a.rot + p0;
-                last_ax = ax;
+        auto row_of = [&](int ax) {
+            int p = a.positions[ax * a.axis_stride + row];
+            if (p < 0 || p >= a.n_pos) {
+                bad = true;
+                p = p < 0 ? 0 : a.n_pos - 1;
             }
-            c[e] = a.cos_sin[base + e];
-            s[e] = a.cos_sin[base + half + e];
+            return a.cos_sin + (long long)p * a.rot + p0;
+        };
+        const int ax = axis_of(p0);
+        if (pairs % 4 == 0 && a.table16 && ax == axis_of(p0 + pairs - 1)) {
+            const float *at = row_of(ax);
+#pragma unroll
+            for (int e = 0; e < VE; e += 4) {
+                if (e >= pairs) break;
+                const float4 x = *reinterpret_cast<const float4 *>(at + e), y = *reinterpret_cast<const float4 *>(at + half + e);
+                c[e] = x.x, c[e + 1] = x.y, c[e + 2] = x.z, c[e + 3] = x.w;
+                s[e] = y.x, s[e + 1] = y.y, s[e + 2] = y.z, s[e + 3] = y.w;
+            }
+        } else {                     // an axis ends among the item's pairs
+            int last_ax = ax;
+            const float *at = row_of(ax);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                if (e >= pairs) break;
+                const int next = axis_of(p0 + e);
+                if (next != last_ax) at = row_of(next);
+                last_ax = next;
+                c[e] = at[e];
+                s[e] = at[half + e];
+            }
         }
         if (bad) atomicOr(a.status, STATUS_PAGES);
     }
@@ -471,18 +485,20 @@ __global__ void __launch_bounds__(256, 4) kv_append_vec_kernel(const AppendArgs 
     if (slot < -1 || (slot >= 0 && !in)) atomicOr(a.status, STATUS_PAGES);
     const long long at = in ? (slot / a.kv.page_size) * a.kv.page_stride + (slot % a.kv.page_size) * a.kv.token_stride : 0;
 
+    T *const q_to = reinterpret_cast<T *>(a.q_out) + row * a.q_out_stride;
+    KV *const k_to = reinterpret_cast<KV *>(a.kv.k) + at - a.q_heads * a.kv.head_stride;
+    KV *const v_to = reinterpret_cast<KV *>(a.kv.v) + at - (a.q_heads + a.kv.heads) * a.kv.head_stride;
     for (;;) {
         const int next = h + U * stride;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int hh = h + u * stride;
-            const int kind = hh < a.q_heads ? 0 : hh < a.q_heads + a.kv.heads ? 1 : 2;     // q, k, v
-            if (hh >= heads || (kind && !in)) continue;
-            const int hk = kind == 0 ? hh : kind == 1 ? hh - a.q_heads : hh - a.q_heads - a.kv.heads;
+            const bool is_q = hh < a.q_heads, is_v = hh >= a.q_heads + a.kv.heads;
+            if (hh >= heads || (!is_q && !in)) continue;
             float y0[VE], y1[VE];
             Piece<T>::open(x0[u], y0);
             if (two) Piece<T>::open(x1[u], y1);
-            if (turned && kind < 2) {
+            if (turned && !is_v) {
                 if (two) {
 #pragma unroll
                     for (int e = 0; e < VE; ++e) {
@@ -499,21 +515,21 @@ __global__ void __launch_bounds__(256, 4) kv_append_vec_kernel(const AppendArgs 
                     }
                 }
             }
-            if (kind == 0) {
-                T *dst = reinterpret_cast<T *>(a.q_out) + (long long)row * a.q_out_stride + hk * dim;
+            if (is_q) {
+                T *dst = q_to + hh * dim;
                 Piece<T>::store(dst + d0, y0);
                 if (two) Piece<T>::store(dst + d1, y1);
             } else {
-                const float *scale = kind == 1 ? a.kv.k_scale : a.kv.v_scale;
+                const float *scale = is_v ? a.kv.v_scale : a.kv.k_scale;
                 if (scale) {
-                    const float f = scale[hk];
+                    const float f = scale[hh - a.q_heads - (is_v ? a.kv.heads : 0)];
 #pragma unroll
                     for (int e = 0; e < VE; ++e) {
                         y0[e] /= f;
                         if (two) y1[e] /= f;
                     }
                 }
-                KV *dst = reinterpret_cast<KV *>(kind == 1 ? a.kv.k : a.kv.v) + at + hk * a.kv.head_stride;
+                KV *dst = (is_v ? v_to : k_to) + hh * a.kv.head_stride;
                 Piece<T>::store(dst + d0, y0);
                 if (two) Piece<T>::store(dst + d1, y1);
             }

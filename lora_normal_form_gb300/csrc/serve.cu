@@ -176,6 +176,7 @@ scute_status scute_kv_append(scute_ctx *c, const scute_kv_cache *kv, const int32
         a.n_axes = rope->n_axes;
         a.n_pos = rope->n_pos;
         a.cos_sin = rope->cos_sin;
+        a.table16 = aligned(rope->cos_sin, 16) && rope->rotary_dim % 8 == 0;
         a.positions = rope->positions;
         a.axis_stride = rope->axis_stride;
     }
