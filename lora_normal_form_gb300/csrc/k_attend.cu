@@ -1,15 +1,36 @@
-// Attention of one new token of each request over its paged cache.
+// Attention of one new token of each request over its paged cache:
+//     out = sum_t p_t v_t,   p_t = exp(s_t - m) / sum_u exp(s_u - m),
+// s_t the score of token t and m any number near the scores' maximum.  One pass:
+// every warp keeps a reference m, the sum l of its weights and the unnormalised
+// outputs o; two such triples join as m = max(m1, m2), l = l1 e^(m1 - m) + l2
+// e^(m2 - m), o likewise.  Exponents are taken in powers of two.
+//
+// What bounds it: the cache, 2 x tokens x heads x dim elements read once (at most
+// 16 operations a byte).  Measured on a GB300 whose copy rate is 6775 GB/s, 32
+// query heads on 8 key/value heads of 128 (device time of a graph's launch):
+//     4 requests of 100 to 131072 tokens, bf16      278 us, 6830 GB/s
+//     64 requests of 500 to 8192 tokens, bf16        90 us, 6260 GB/s
+//     the same lengths to 16384, e4m3                99 us, 6060 GB/s
+//     256 requests of 1 to 600 tokens, bf16          40 us, 3690 GB/s (the rows' ends)
+//     1 request of 777 tokens                       9.8 us (the dependent steps: lengths
+//         1.7, pages and cache rows 3.3, arrival 1.0, joining and storing 2.1)
 //
 // The work is one sequence of tiles (TT tokens of one request and head row),
 // with ROW_COST places before each row's first for what a row costs beside its
-// tiles, cut into equal contiguous ranges, one per CTA, whatever rows they
-// fall in.  In a CTA one warp looks the pages up and brings the tokens' key and
-// value rows into a ring of stages by 16-byte asynchronous copies, running ahead
-// over the ends of rows (a page may end anywhere in a tile); the others take the
-// tiles in turn, each with its own maximum, sums and outputs, and merge them in
-// shared memory where a row ends.  Of a row that several CTAs share each leaves
-// its part in the workspace, arrives at the row's counter when its whole range is
-// done, and the last to arrive joins the parts in the order of the CTAs.
+// tiles, cut into equal contiguous ranges, one per CTA, whatever rows they fall
+// in: any batch, one long request or many short ones, fills the GPU alike.  In a
+// CTA one or two warps look the pages up and bring the tokens' key and value rows
+// into a ring of stages by 16-byte asynchronous copies, running ahead over the
+// ends of rows (a page may end anywhere in a tile); the others take the tiles in
+// turn, each with its own triple, and join them in shared memory where a row
+// ends.  Of a row that several CTAs share each leaves its triple in the workspace,
+// arrives at the row's counter when its whole range is done, and the last to
+// arrive joins them in the order of the CTAs, so that results do not depend on
+// which that is.
+//
+// Instead of the copies, one bulk copy for each token row costs about 20 ns of
+// its SM each (64 requests: 322 us), and cache rows loaded straight to registers
+// leave the warps waiting (145 us).
 #include <cuda_fp8.h>
 
 #include "internal.h"
@@ -23,8 +44,12 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr int ATT_CTAS = 6;               // CTAs of an SM, at most
 constexpr int QS = 2;                     // rows whose queries may be waiting
 constexpr int MAX_STAGES = 32;
-constexpr int ROW_COST = 3;               // tiles
-constexpr int MIN_TILES = 4;              // of a CTA's range, where the batch has enough
+// What a row costs beside its tiles, in tiles: with 1, 256 short requests take
+// 43.0 us and one request 12.2, with 3 40.4 and 9.8, with 6 42.5 and 9.8.
+constexpr int ROW_COST = 3;
+// The least places of a range, so that a small batch is not cut to parts whose
+// joining costs more: one request takes 11.0 us with 2, 9.7 with 4, 11.8 with 8.
+constexpr int MIN_TILES = 4;
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
@@ -159,8 +184,12 @@ __device__ __forceinline__ uint32_t place_of(int row, int piece) {
 // query's fragment the same elements; and 16 consecutive bytes of the values of
 // tokens 2c, 2c + 1, 2c + 8, 2c + 9, of which pairs of tokens are interleaved by
 // byte permutes.  The work per byte is small (2 x 8 products for each element,
-// about a tenth of these instructions' rate at full memory bandwidth), so the
-// larger tiles of the asynchronous matrix unit would gain nothing here.
+// about a tenth of these instructions' rate at full memory bandwidth; the tensor
+// pipe is 13 % busy), so the larger tiles of the asynchronous matrix unit, 128 rows
+// of which one new token fills at most 16, would gain nothing here.  A tile's
+// values are read from shared memory piece by piece, behind the weights: all of
+// them at once beside the keys costs registers (64 requests 91.2 against 89.9 us,
+// e4m3 101.9 against 98.5).
 template <bool FP8, int DC, int NT>
 struct MmaMath {
     using IO = __nv_bfloat16;
@@ -174,10 +203,6 @@ struct MmaMath {
     static constexpr int VP = DC / (8 * VE);
     static constexpr int VW = VE * ESZ / 4;               // its words
     static constexpr int OT = VE / 2;                     // 16-row output tiles of a value piece
-    // Small instances take a tile's values from shared memory at once, beside the
-    // keys; in the others they would not fit the registers (a spill goes to L2
-    // here: shared memory leaves L1 little) and come piece by piece.
-    static constexpr bool EARLY = NT == 1 && DC <= 128;
 
     const int lane, g, c;
     uint32_t qf[NT][KP][KE / 2];
@@ -279,10 +304,10 @@ struct MmaMath {
                                             w1[2 * e + 1], qf[nt][j][2 * e], qf[nt][j][2 * e + 1]);
                 }
             }
-        uint32_t vr[MT][4][EARLY ? VP : 1][VW];
+        uint32_t vr[4][VW];
         auto values = [&](int m, int k, int j) {
             const int tok = m * 16 + 2 * c + (k & 1) + (k >> 1) * 8;
-            uint32_t *to = vr[m][k][EARLY ? j : 0];
+            uint32_t *to = vr[k];
             if constexpr (VW == 4) {
                 const uint4 x = lds16(vd + place_of<ROW>(tok, j * 8 + g));
                 to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w;
@@ -291,16 +316,6 @@ struct MmaMath {
                 to[0] = x.x, to[1] = x.y;
             }
         };
-        if constexpr (EARLY) {
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int j = 0; j < VP; ++j) values(m, k, j);
-            release();
-        }
-
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -385,14 +400,11 @@ struct MmaMath {
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int j = 0; j < VP; ++j) {
-                if constexpr (!EARLY) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) values(m, k, j);
-                }
+                for (int k = 0; k < 4; ++k) values(m, k, j);
 #pragma unroll
                 for (int i = 0; i < VW; ++i) {
-                    const uint32_t x0 = vr[m][0][EARLY ? j : 0][i], x1 = vr[m][1][EARLY ? j : 0][i];
-                    const uint32_t x2 = vr[m][2][EARLY ? j : 0][i], x3 = vr[m][3][EARLY ? j : 0][i];
+                    const uint32_t x0 = vr[0][i], x1 = vr[1][i], x2 = vr[2][i], x3 = vr[3][i];
                     if constexpr (FP8) {
                         const uint32_t y0 = __byte_perm(x0, x1, 0x5140), y1 = __byte_perm(x0, x1, 0x7362);
                         const uint32_t y2 = __byte_perm(x2, x3, 0x5140), y3 = __byte_perm(x2, x3, 0x7362);
@@ -416,7 +428,7 @@ struct MmaMath {
                     }
                 }
             }
-        if constexpr (!EARLY) release();
+        release();
     }
     // The warp's maximum and sum of every head, to m and l.
     __device__ __forceinline__ void stats(float *m, float *l) {
@@ -469,7 +481,10 @@ struct MmaMath {
 };
 
 // ---------------------------------------------------------------- 32-bit caches
-// Sums in 32 bits throughout, NH heads at a time.  Scores: lane (g, c) multiplies
+// Sums in 32 bits throughout, NH heads at a time (16-bit or three-part products
+// would not keep them).  With one to two heads a key bound by memory (64 requests
+// of one head of 64: 112 us, 6430 GB/s), from eight on by the FMAs and the shared
+// memory that feeds them (32 requests, 8 heads of 128: 210 us, 3460 GB/s).  Scores: lane (g, c) multiplies
 // every fourth 16-byte piece of token g's key, and the four lanes of a token add
 // up.  Outputs: a lane owns DC / 32 neighbouring elements and takes the tile's
 // tokens one after another, their weights from shared memory.
@@ -922,7 +937,9 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
         // before this one's rows are sent for.
         constexpr int SPAN = 128;
         const uint64_t policy = ptx::make_policy_evict_first();
-        // pages in which a tile of 32 tokens mostly lies at once
+        // pages in which a tile of 32 tokens lies at once: one check and one base for
+        // it (e4m3, pages of 32 or 256 tokens: 94.4 us against 98.4 by halves); in
+        // others the check is lost (pages of 16: 106.6 us, by halves 98.7)
         const bool whole_tiles = TT <= 16 || a.kv.page_size % TT == 0;
         const long long tok_bytes = a.kv.token_stride * ESZ;
         int hk = w.hk, z = w.z, r = w.r, stop = w.to(), pos = w.from();
@@ -1183,17 +1200,32 @@ cudaError_t launch_shape(const AttendArgs &a, int num_sms, cudaStream_t st) {
     return launch_chained(kernel, num_sms * per_sm, S::THREADS, S::smem((int)stages, a.n_req), st, a, (int)stages);
 }
 
+// Shapes: (computing warps, fetching warps, CTAs of an SM), each the fastest of those
+// that fit the registers and leave the ring 100 KB or more of an SM.  Few warps in
+// many small CTAs end their rows independently of each other; many heads or long
+// ones take more registers or more products for each byte that is fetched.  Device
+// times in us, 64 requests of 500 to 8192 tokens (e4m3: to 16384) where not said:
+//     group <= 8, dim <= 128   2,1,4: 90.3, 256 short requests 40.4; 4,2,2: 100.4, 59.6
+//       e4m3, dim <= 64        2,1,6: 74.9, 2,1,5: 78.7, 2,1,4: 87.8; bf16 67.4, -, 61.1
+//     group > 8: 16 heads at a time, each key fetched once: 79.9 (4,2,2); in eights
+//       with the shape above 104.6; 16 with 2,1,4: 135.3
+//       dim <= 64              2,1,4: 69.5, 4,2,2: 89.9
+//     dim > 128                4,2,2: 70.8, 2,2,2: 79.3, 2,1,3: 102.3 (32 requests)
 template <bool FP8>
 cudaError_t launch_mma(const AttendArgs &a, int num_sms, cudaStream_t st) {
     const int D = a.kv.dim;
     const bool wide = a.group > 8;
-    if (D > 128) return launch_shape<MmaMath<FP8, 256, 1>, 256, 2, 2, 2>(a, num_sms, st);
+    if (D > 128) return launch_shape<MmaMath<FP8, 256, 1>, 256, 4, 2, 2>(a, num_sms, st);
     if (D > 64)
         return wide ? launch_shape<MmaMath<FP8, 128, 2>, 128, 4, 2, 2>(a, num_sms, st)
                     : launch_shape<MmaMath<FP8, 128, 1>, 128, 2, 1, 4>(a, num_sms, st);
-    return wide ? launch_shape<MmaMath<FP8, 64, 2>, 64, 4, 2, 2>(a, num_sms, st)
-                : launch_shape<MmaMath<FP8, 64, 1>, 64, 2, 1, 4>(a, num_sms, st);
+    return wide ? launch_shape<MmaMath<FP8, 64, 2>, 64, 2, 1, 4>(a, num_sms, st)
+                : launch_shape<MmaMath<FP8, 64, 1>, 64, 2, 1, FP8 ? 6 : 4>(a, num_sms, st);
 }
+// 32-bit caches, in the same way (group 4, 32 requests):
+//     dim <= 64   2,1,5: 134.0, 2,1,6: 148.4, 2,1,4: 143.4 (64 requests)
+//     dim <= 128  2,1,4: 141.2, 4,2,2: 185.5
+//     dim > 128   2,1,3: 221.4, 4,2,2: 235.3, 2,2,2: 288.7
 template <int DC, int CW, int PW, int CTAS>
 cudaError_t launch_fma(const AttendArgs &a, int num_sms, cudaStream_t st) {
     if (a.group == 1) return launch_shape<FmaMath<DC, 1>, DC, CW, PW, CTAS>(a, num_sms, st);
@@ -1210,9 +1242,9 @@ int attend_ctrs(int num_sms) { return num_sms * ATT_CTAS; }
 cudaError_t launch_attend(const AttendArgs &a, int num_sms, cudaStream_t st) {
     if (a.kv.dtype == KV_BF16) return launch_mma<false>(a, num_sms, st);
     if (a.kv.dtype == KV_E4M3) return launch_mma<true>(a, num_sms, st);
-    if (a.kv.dim <= 64) return launch_fma<64, 2, 1, 6>(a, num_sms, st);
+    if (a.kv.dim <= 64) return launch_fma<64, 2, 1, 5>(a, num_sms, st);
     if (a.kv.dim <= 128) return launch_fma<128, 2, 1, 4>(a, num_sms, st);
-    return launch_fma<256, 4, 2, 2>(a, num_sms, st);
+    return launch_fma<256, 2, 1, 3>(a, num_sms, st);
 }
 
 }  // namespace scute
