@@ -39,7 +39,8 @@ __device__ __forceinline__ void row_stats(const float *row, int d, int layer, fl
     *rstd = rsqrtf(cta_sum(q, warp_sum) / d + eps);
 }
 
-// Any d and alignment: one CTA per row, the row in shared memory in 32 bits.
+// Any d and alignment: one CTA per row, the row in shared memory in 32 bits.  What
+// it costs: 8772 rows of 4096 take 180 us, with 16-byte vectors 47.
 template <typename T>
 __global__ void __launch_bounds__(256) residual_norm_kernel(const NormArgs a) {
     extern __shared__ float row[];
@@ -109,6 +110,11 @@ template <> struct Vec<__nv_bfloat16> {
     }
 };
 
+// Four rows of d for each token (y, residual, h, out), so bound by memory: 8772 rows
+// of 4096 with both norms, bf16, take 47.0 us, 6120 GB/s (90 % of the copy rate);
+// 64 rows 2.8 us, of which a launch of nothing is 1.5.  The row stays in registers
+// between the two norms, so that every element is read and written once.
+//
 // The row in registers: a row's threads hold NV 16-byte vectors each.  WARP: a
 // warp for a row and shuffles alone; otherwise a CTA for a row.  The launch has
 // as many CTAs as reside, and each fetches its next row or two before it is done
@@ -116,8 +122,8 @@ template <> struct Vec<__nv_bfloat16> {
 // off or biases.  HELD: a thread keeps its columns' factors from row to row, post_w,
 // the gate and the scale as one; fetched anew for every row they are half of all
 // that passes through L1.
-template <typename T, int NV, bool WARP, bool FULL, bool HELD>
-__global__ void __launch_bounds__(WARP || HELD ? 256 : 1024, HELD ? 2 : 1)
+template <typename T, int NV, bool WARP, bool FULL, bool HELD, int MOST>
+__global__ void __launch_bounds__(MOST, MOST == 256 || (!HELD && MOST == 512) ? 2 : 1)
     residual_norm_vec_kernel(const NormArgs a) {
     constexpr int VE = Vec<T>::N;
     constexpr int AHEAD = HELD ? 2 : NV <= 2 ? 1 : 0;      // rows fetched ahead
@@ -140,9 +146,12 @@ __global__ void __launch_bounds__(WARP || HELD ? 256 : 1024, HELD ? 2 : 1)
         if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = x;
         __syncthreads();
         float s = 0.f;
-        if (HELD) {           // eight warps at most; the places of those there are not stay zero
-            const float4 p = *reinterpret_cast<const float4 *>(red[turn]), q = *reinterpret_cast<const float4 *>(red[turn] + 4);
-            s = (p.x + p.y) + (p.z + p.w) + ((q.x + q.y) + (q.z + q.w));
+        if (HELD) {           // the places of warps there are not stay zero
+#pragma unroll
+            for (int w = 0; w < MOST / 32; w += 4) {
+                const float4 p = *reinterpret_cast<const float4 *>(red[turn] + w);
+                s += (p.x + p.y) + (p.z + p.w);
+            }
         } else {
             s = (threadIdx.x & 31) < (blockDim.x >> 5) ? red[turn][threadIdx.x & 31] : 0.f;
 #pragma unroll
@@ -322,9 +331,9 @@ bool by_vectors(const NormArgs &a) {
     return (p & 15) == 0 && s == 0;
 }
 
-template <typename T, int NV, bool WARP, bool FULL, bool HELD>
+template <typename T, int NV, bool WARP, bool FULL, bool HELD, int MOST>
 cudaError_t launch_one(const NormArgs &a, int threads, int num_sms, cudaStream_t s) {
-    const auto kernel = residual_norm_vec_kernel<T, NV, WARP, FULL, HELD>;
+    const auto kernel = residual_norm_vec_kernel<T, NV, WARP, FULL, HELD, MOST>;
     // CTAs that reside on an SM at once, by its registers (looked up once) and threads
     static const int regs = [&] {
         cudaFuncAttributes f;
@@ -335,10 +344,10 @@ cudaError_t launch_one(const NormArgs &a, int threads, int num_sms, cudaStream_t
     const long long rows = WARP ? (a.n + 7) / 8 : a.n, room = (long long)num_sms * per_sm;
     return launch_chained(kernel, (int)(rows < room ? rows : room), threads, 0, s, a);
 }
-template <typename T, int NV, bool WARP, bool HELD>
+template <typename T, int NV, bool WARP, bool HELD, int MOST>
 cudaError_t launch_vec(const NormArgs &a, int threads, int num_sms, cudaStream_t s) {
-    if (a.layer || a.post_b || a.pre_b) return launch_one<T, NV, WARP, true, HELD>(a, threads, num_sms, s);
-    return launch_one<T, NV, WARP, false, HELD>(a, threads, num_sms, s);
+    if (a.layer || a.post_b || a.pre_b) return launch_one<T, NV, WARP, true, HELD, MOST>(a, threads, num_sms, s);
+    return launch_one<T, NV, WARP, false, HELD, MOST>(a, threads, num_sms, s);
 }
 
 template <typename T>
@@ -347,16 +356,25 @@ cudaError_t launch(const NormArgs &a, int num_sms, cudaStream_t s) {
     if (by_vectors<T>(a)) {
         const int nvec = a.d / VE;
         auto threads = [&](int nv) { return ((nvec + nv - 1) / nv + 31) / 32 * 32; };
-        // a thread's factors are worth holding where it has several rows
-        const bool few = a.n <= num_sms, many = a.n >= 8 * num_sms;
-        if (nvec <= 32) return launch_vec<T, 1, true, false>(a, 256, num_sms, s);
-        if (nvec <= 64) return launch_vec<T, 2, true, false>(a, 256, num_sms, s);
-        if (many && threads(1) <= 256) return launch_vec<T, 1, false, true>(a, threads(1), num_sms, s);
-        if (many && threads(2) <= 256) return launch_vec<T, 2, false, true>(a, threads(2), num_sms, s);
-        if (threads(1) <= (few ? 1024 : 256)) return launch_vec<T, 1, false, false>(a, threads(1), num_sms, s);
-        if (threads(2) <= (few ? 1024 : 512)) return launch_vec<T, 2, false, false>(a, threads(2), num_sms, s);
-        if (threads(4) <= 1024) return launch_vec<T, 4, false, false>(a, threads(4), num_sms, s);
-        if constexpr (VE == 4) return launch_vec<T, 8, false, false>(a, threads(8), num_sms, s);
+        // Short rows: a warp for each (16384 rows of 256, bf16: 5.5 us, a CTA each 6.3;
+        // of 512 the other way, 13.8 and 12.9).  A thread's factors are worth holding
+        // where it has a few rows (600 rows of 4096 with both norms 4.3 us, not held 4.5;
+        // 8772 rows 47.2 and 48.7), with more threads, so fewer CTAs, where it has many
+        // (4000 rows of 8192 with biases 61.4 and 76.4, but 600 fp32 rows of 4096 6.7 and
+        // 6.3).  Few rows: one vector to a thread (64 rows of 4096 2.8 us, two 3.1), up to
+        // 512 threads (64 rows of 8192: 3.7 with two, 4.0 with one and 1024).  Longer
+        // rows: two vectors and 1024 threads before four and 512 (2400 rows of 14336 53.1
+        // and 70.8 us).
+        const bool few = a.n <= num_sms, some = a.n >= 2 * num_sms, many = a.n >= 8 * num_sms;
+        if (nvec <= 32) return launch_vec<T, 1, true, false, 256>(a, 256, num_sms, s);
+        if (some && threads(1) <= 256) return launch_vec<T, 1, false, true, 256>(a, threads(1), num_sms, s);
+        if (some && threads(2) <= 256) return launch_vec<T, 2, false, true, 256>(a, threads(2), num_sms, s);
+        if (many && threads(2) <= 512) return launch_vec<T, 2, false, true, 512>(a, threads(2), num_sms, s);
+        if (threads(1) <= (few ? 512 : 256)) return launch_vec<T, 1, false, false, 512>(a, threads(1), num_sms, s);
+        if (threads(2) <= 512) return launch_vec<T, 2, false, false, 512>(a, threads(2), num_sms, s);
+        if (threads(2) <= 1024) return launch_vec<T, 2, false, false, 1024>(a, threads(2), num_sms, s);
+        if (threads(4) <= 1024) return launch_vec<T, 4, false, false, 1024>(a, threads(4), num_sms, s);
+        if constexpr (VE == 4) return launch_vec<T, 8, false, false, 1024>(a, threads(8), num_sms, s);
     }
     static std::atomic<unsigned long long> done{0};
     const size_t smem = sizeof(float) * a.d;

@@ -167,6 +167,22 @@ def test_attention_split_over_the_gpu(scute, contexts, kind, lens):
     assert ctx.sync_status() == 0
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "fp8"])
+def test_attention_most_requests(scute, contexts, kind):
+    """As many requests as a call takes (fewer CTAs fit an SM then), mostly short or empty."""
+    g = np.random.default_rng(16384)
+    lens = g.integers(0, 4, 16384)
+    lens[[0, 5000, 16383]] = 900, 3000, 40
+    cache, tokens = make_cache(scute, g, lens, 1, 64, 16, kind, False)
+    q = torch.from_numpy(g.standard_normal((len(lens), 2, 64), dtype=np.float32))
+    q = q.cuda().to(DT["fp32" if kind == "fp32" else "bf16"])
+    out, lse = torch.full_like(q, float("nan")), torch.empty(q.shape[:2], device="cuda")
+    ctx = ctx_of(contexts, kind)
+    ctx.paged_attention(cache, q, i32(lens), out, lse=lse)
+    assert ctx.sync_status() == 0
+    check_attend(out, lse, q, tokens, kind, 2)
+
+
 def test_attention_large_scores_and_one_token_dominates(scute, contexts):
     """Scores of +-2000 (nothing overflows, the maximum moves from tile to tile)
     and values whose weights all vanish but one."""
@@ -570,6 +586,17 @@ def test_residual_norm(scute, contexts, kind, n, d, post, pre, gate, layer, bias
         w = np.abs(n64(nw))
         tol = soft * np.abs(o) + w * (step + soft * np.abs(h)) / np.maximum(size, 1e-3) + (soft if layer else 0)
         assert np.all(np.abs(f64(out) - o) <= tol + rel * np.abs(o) + 1e-30)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,d,post,pre,gate,layer,bias", [
+    (700, 480, True, True, "vec", False, False), (331, 2048, True, True, "rows", False, False),
+    (1300, 4096, True, True, None, False, False), (1250, 4096, False, True, "vec", True, True),
+    (1300, 5120, True, True, None, True, True), (2000, 1000, True, True, "rows", True, True),
+    (320, 14336, True, True, "vec", False, False)])
+def test_residual_norm_many_rows(scute, contexts, kind, n, d, post, pre, gate, layer, bias):
+    """Several rows to a CTA: rows fetched ahead, factors held from row to row."""
+    test_residual_norm(scute, contexts, kind, n, d, post, pre, gate, layer, bias, True, True, 0)
 
 
 def test_residual_norm_in_place_strided_and_zero_rows(scute, contexts):
