@@ -25,6 +25,12 @@ namespace {
 // growing ones written behind their old pages, and list entries are written
 // only from F on.  So no thread waits for another, except that lengths and a
 // count that are written in place follow a launch-wide arrival count.
+//
+// Bound by latency: lengths, two scans, a binary search for every row in shared
+// memory, the page, the stores.  64 requests of one new token take 3.5 us (a launch
+// of nothing 1.5), 4096 with their prompts 10.6 (all in one CTA 126).  Every CTA
+// scans all requests for itself, which costs less than a second launch would; 256
+// threads are enough up to 256 requests (3.5 us against 4.4 with 1024).
 constexpr int RS_THREADS = 1024;       // at most
 
 // Pages of so many tokens (at most 2^31 - 1 with a page's rounding); page of a position.
@@ -290,7 +296,9 @@ template <typename T> __device__ __forceinline__ float to_f(T x) { return (float
 template <typename T> __device__ __forceinline__ T from_f(float x) { return (T)x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// One thread turns one pair, or passes one element, of one head of one row.
+// Any strides and rotary halves: one thread turns one pair, or passes one element,
+// of one head of one row.  What it costs: 8772 rows of 48 heads of 128 take 137 us,
+// 16 bytes at a time 38.
 template <typename T>
 __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
     const int row = blockIdx.x, dim = a.kv.dim, half = a.rot / 2;
@@ -402,6 +410,9 @@ template <> struct Piece<__nv_bfloat16> {
 // interleaved pairs, single pieces only.  A row's threads (per_row of them, a
 // multiple of the items or cut to one) keep their item from head to head, so that
 // its cosines and sines are fetched once; heads are taken U at a time, loads first.
+// Bound by memory: 8772 rows of 32 + 2 x 8 heads of 128 with positions of three
+// axes, bf16, take 38.0 us, 5800 GB/s (86 % of the copy rate).  U = 3 or 6, 5 or 6
+// CTAs on an SM and 128 threads for a row are slower.
 template <typename T, typename KV>
 __global__ void __launch_bounds__(256, 4) kv_append_vec_kernel(const AppendArgs a, int per_row) {
     constexpr int VE = Piece<T>::N, U = 2;
@@ -583,7 +594,9 @@ cudaError_t launch_kv_resize(const ResizeArgs &a, int num_sms, cudaStream_t st) 
 
 cudaError_t launch_kv_append(bool f32, const AppendArgs &a, int num_sms, cudaStream_t st) {
     if (f32 ? by_pieces<float>(a) : by_pieces<__nv_bfloat16>(a)) {
-        // few rows: a CTA for each, every head at once; many: 64 threads for a row
+        // few rows: a CTA for each, every head at once (64 rows 2.3 us, 64 threads each
+        // 3.7; 608 rows 3.6 and 3.9); many: 64 threads for a row, whose cosines are
+        // fetched fewer times (1216 rows 5.4 us, 256 threads 6.4; 8772 rows 38.0 and 61.6)
         const int per_row = a.n <= 4 * num_sms ? 256 : 64, rows = 256 / per_row;
         const int grid = (a.n + rows - 1) / rows;
         if (f32) return launch_chained(kv_append_vec_kernel<float, float>, grid, 256, 0, st, a, per_row);
