@@ -177,9 +177,19 @@ def _check_table(t):
         raise ValueError("a block table is int32 [n_req, pages] with consecutive rows")
 
 
-def _rows(t, n, cols):
+def _flat(count, *tensors):
+    """Check that each is None or ``count`` consecutive 4-byte elements."""
+    for t in tensors:
+        if t is not None and (t.nbytes != 4 * count or not t.is_contiguous()):
+            raise ValueError(f"expected {count} consecutive 4-byte elements, got shape {tuple(t.shape)}, strides "
+                             f"{t.stride()}, {t.dtype}")
+
+
+def _rows(t, n, cols, size=None):
     """Elements between the rows of ``t``: [n, cols], or [n, heads, dim] with
-    consecutive heads."""
+    consecutive heads; elements of ``size`` bytes."""
+    if size is not None and t.element_size() != size:
+        raise ValueError(f"expected elements of {size} bytes, got {t.dtype}")
     shape, st = t.shape, t.stride()
     if len(shape) == 3:
         ok = shape[0] == n and shape[1] * shape[2] == cols and st[2] == 1 and (st[1] == shape[2] or shape[1] == 1)

@@ -3,7 +3,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (BF16, FP32, METHOD_ID, KvCache, Rope, _check_table, _rows, scute_add_layer, scute_create, scute_debug_index, scute_destroy,
+from . import (BF16, FP32, METHOD_ID, KvCache, Rope, _check_table, _flat, _rows, scute_add_layer, scute_create, scute_debug_index, scute_destroy,
                scute_kv_append, scute_kv_resize, scute_launch_count, scute_linear, scute_linear_batch, scute_linear_batch_host,
                scute_linear_host, scute_paged_attention, scute_predict_batch, scute_predict_bytes,
                scute_register_adapter, scute_residual_norm, scute_rope_table, scute_set_shared, scute_set_variant, scute_sync_status,
@@ -17,6 +17,7 @@ class Context:
     def __init__(self, dtype: str = "bf16", max_tokens: int = 1024, max_adapters: int = 64,
                  max_layers: int = 16, device: int = 0):
         self.dtype = dtype
+        self.esz = 2 if dtype == "bf16" else 4
         self.device = device
         self.max_tokens = max_tokens
         self.handle = scute_create(device, BF16 if dtype == "bf16" else FP32, max_tokens, max_adapters,
@@ -108,11 +109,20 @@ class Context:
         int32 tensors; scute.h has the layout).  The step has ``slot_map.numel()``
         token rows."""
         _check_table(block_table)
-        n, cols = len_in.numel(), block_table.shape[1]
+        n, (requests, cols) = len_in.numel(), block_table.shape
+        rows, n_free = slot_map.numel(), free_pages.numel()
+        if not (requests >= n and len_in.nbytes == len_new.nbytes == len_out.nbytes == 4 * n
+                and cu_new.nbytes == 4 * n + 4 and free_in.nbytes == free_out.nbytes == 4
+                and slot_map.nbytes == positions.nbytes == token_req.nbytes == 4 * rows and free_pages.nbytes == 4 * n_free
+                and len_in.is_contiguous() and len_new.is_contiguous() and len_out.is_contiguous()
+                and cu_new.is_contiguous() and slot_map.is_contiguous() and positions.is_contiguous()
+                and token_req.is_contiguous() and free_pages.is_contiguous()):
+            raise ValueError("kv_resize takes consecutive int32 elements: lengths of the requests, a count of free "
+                             "pages, cu_new one longer, token rows of one number, and a table row for each request")
         scute_kv_resize(self.handle, len_in, len_new, n, block_table,
-                        block_table.stride(0) if block_table.shape[0] > 1 else max(cols, block_table.stride(0)), cols,
-                        page_size, free_pages, free_pages.numel(), free_in, free_out, len_out, cu_new, slot_map,
-                        positions, token_req, slot_map.numel(), stream)
+                        block_table.stride(0) if requests > 1 else max(cols, block_table.stride(0)), cols,
+                        page_size, free_pages, n_free, free_in, free_out, len_out, cu_new, slot_map,
+                        positions, token_req, rows, stream)
 
     def rope_table(self, cos_sin, theta: float = 10000.0, inv_freq=None, stream=None):
         """Fill the float32 table ``cos_sin`` [n_pos, rotary_dim]."""
@@ -121,42 +131,45 @@ class Context:
     def kv_append(self, cache: KvCache, slot_map, k, v, q=None, q_out=None, rope: Rope = None, stream=None):
         """Write k and v [n, kv_heads, dim] (or [n, kv_heads * dim]) into the cache;
         keys, and queries into ``q_out``, turned by ``rope``."""
-        n, row = slot_map.shape[0], cache.kv_row
+        n, row, size = slot_map.shape[0], cache.kv_row, self.esz
+        _flat(n, slot_map)
         q_heads = q_stride = q_out_stride = 0
         if q is not None:
             q_row = q.numel() // n if n else cache.head_dim
             q_heads = q_row // cache.head_dim
             if q_out is None or q_heads * cache.head_dim != q_row:
                 raise ValueError("q rows are heads * head_dim elements, and need q_out")
-            q_stride, q_out_stride = _rows(q, n, q_row), _rows(q_out, n, q_row)
+            q_stride, q_out_stride = _rows(q, n, q_row, size), _rows(q_out, n, q_row, size)
         if rope is not None and rope.n < n:
             raise ValueError("fewer positions than rows")
-        scute_kv_append(self.handle, cache, slot_map, n, k, _rows(k, n, row), v, _rows(v, n, row), q, q_stride,
+        scute_kv_append(self.handle, cache, slot_map, n, k, _rows(k, n, row, size), v, _rows(v, n, row, size), q, q_stride,
                         q_heads, q_out, q_out_stride, rope, stream)
 
     def paged_attention(self, cache: KvCache, q, kv_len, out, scale: float = 0.0, softcap: float = 0.0,
                         window: int = 0, lse=None, stream=None):
         """One new token of each request over its cached tokens: q and out
         [n_req, q_heads, dim] (or [n_req, q_heads * dim])."""
-        n, dim = kv_len.shape[0], cache.head_dim
+        n, dim, size = kv_len.shape[0], cache.head_dim, self.esz
         row = q.numel() // n if n else cache.kv_row
-        if row % dim or cache.requests < n or (lse is not None and lse.numel() * dim != n * row):
-            raise ValueError("q rows are heads * head_dim elements, lse has one value for each head, and the block "
-                             "table a row for each request")
-        scute_paged_attention(self.handle, cache, q, _rows(q, n, row), out, _rows(out, n, row), lse, kv_len, n,
+        if row % dim or cache.requests < n :
+            raise ValueError("q rows are heads * head_dim elements, and the block table has a row for each request")
+        _flat(n, kv_len)
+        _flat(n * row // dim, lse)
+        scute_paged_attention(self.handle, cache, q, _rows(q, n, row, size), out, _rows(out, n, row, size), lse, kv_len, n,
                               row // dim, scale, softcap, window, stream)
 
     def residual_norm(self, y, out=None, residual=None, residual_out=None, pre_w=None, pre_b=None, post_w=None,
                       post_b=None, gate=None, scale: float = 1.0, eps: float = 1e-5, layer: bool = False, stream=None):
         """h = residual + scale * gate * post(y), out = pre(h), for rows [n, d].
         ``gate``: float32 [d], or the context's dtype [n, d]."""
-        n, d = y.shape
+        (n, d), size = y.shape, self.esz
         gate_vec, gate_rows = (None, gate) if gate is not None and gate.dim() == 2 else (gate, None)
-        scute_residual_norm(self.handle, n, d, y, _rows(y, n, d),
-                            residual, 0 if residual is None else _rows(residual, n, d),
-                            residual_out, 0 if residual_out is None else _rows(residual_out, n, d),
-                            out, 0 if out is None else _rows(out, n, d), post_w, post_b, pre_w, pre_b, gate_vec,
-                            gate_rows, 0 if gate_rows is None else _rows(gate_rows, n, d), scale, eps, layer, stream)
+        _flat(d, post_w, post_b, pre_w, pre_b, gate_vec)
+        scute_residual_norm(self.handle, n, d, y, _rows(y, n, d, size),
+                            residual, 0 if residual is None else _rows(residual, n, d, size),
+                            residual_out, 0 if residual_out is None else _rows(residual_out, n, d, size),
+                            out, 0 if out is None else _rows(out, n, d, size), post_w, post_b, pre_w, pre_b, gate_vec,
+                            gate_rows, 0 if gate_rows is None else _rows(gate_rows, n, d, size), scale, eps, layer, stream)
 
     def sync_status(self) -> int:
         return scute_sync_status(self.handle)

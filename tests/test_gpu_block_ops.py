@@ -709,3 +709,36 @@ def test_refusals(scute, contexts):
                      (1, dict(theta=0.0)), (1, dict(theta=float("nan")))]:
         refused(scute, code, lambda: T(**kw))
     assert ctx.launch_count() == before and ctx.sync_status() == 0
+
+
+def test_wrong_sizes_types_and_strides_are_refused(scute, contexts):
+    """What the tensors themselves show: a kernel would read past them, or other values."""
+    ctx, f32 = contexts["bf16"], contexts["fp32"]
+    before = ctx.launch_count()
+    z = lambda *s, t=torch.bfloat16: torch.zeros(*s, device="cuda", dtype=t)  # noqa: E731
+    whole = lambda *s: torch.zeros(*s, device="cuda", dtype=torch.int32)  # noqa: E731
+    cache = scute.KvCache(z(4, 2, 16, 64), z(4, 2, 16, 64), whole(2, 2))
+    q, out, w = z(2, 4, 64), z(2, 4, 64), z(64, t=torch.float32)
+    rope = scute.Rope(z(10, 64, t=torch.float32), whole(3))
+    k, slots, y = z(3, 2, 64), whole(3), z(2, 64)
+    steps = dict(len_in=whole(2), len_new=whole(2), block_table=whole(2, 2), page_size=16, free_pages=whole(4),
+                 free_in=whole(1), free_out=whole(1), len_out=whole(2), cu_new=whole(3), slot_map=whole(2),
+                 positions=whole(2), token_req=whole(2))
+    bad = [lambda: ctx.paged_attention(cache, q, whole(4)[::2], out), lambda: ctx.paged_attention(cache, q, whole(2).long(), out),
+           lambda: ctx.paged_attention(cache, q.float(), whole(2), out),
+           lambda: ctx.paged_attention(cache, q, whole(2), out, lse=z(2, 4)),
+           lambda: ctx.paged_attention(cache, q, whole(2), out, lse=z(2, 8, t=torch.float32)[:, ::2]),
+           lambda: ctx.kv_append(cache, whole(6)[::2], k, k), lambda: ctx.kv_append(cache, slots.long(), k, k),
+           lambda: ctx.kv_append(cache, slots, k.float(), k), lambda: ctx.kv_append(cache, slots, k, k[:2]),
+           lambda: ctx.kv_append(cache, slots, k, k, q=k, q_out=k.float(), rope=rope),
+           lambda: ctx.residual_norm(y, y, pre_w=w[:63]), lambda: ctx.residual_norm(y, y, pre_w=w.bfloat16()),
+           lambda: ctx.residual_norm(y, y, gate=w.bfloat16()), lambda: ctx.residual_norm(y, y, residual=y.float()),
+           lambda: f32.residual_norm(y, y), lambda: ctx.residual_norm(y, y[:1])]
+    bad += [lambda kw=kw: ctx.kv_resize(**{**steps, **kw}) for kw in (
+        dict(len_new=whole(1)), dict(len_in=whole(4)[::2]), dict(len_out=whole(2).long()), dict(cu_new=whole(2)),
+        dict(positions=whole(1)), dict(token_req=whole(3)), dict(slot_map=whole(4)[::2]), dict(free_in=whole(1).long()),
+        dict(free_out=whole(0)), dict(free_pages=whole(8)[::2]), dict(block_table=whole(1, 2)))]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    assert ctx.launch_count() == before
