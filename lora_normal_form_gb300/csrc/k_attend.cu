@@ -8,10 +8,10 @@
 // What bounds it: the cache, 2 x tokens x heads x dim elements read once (at most
 // 16 operations a byte).  Measured on a GB300 whose copy rate is 6775 GB/s, 32
 // query heads on 8 key/value heads of 128 (device time of a graph's launch):
-//     4 requests of 100 to 131072 tokens, bf16      278 us, 6830 GB/s
-//     64 requests of 500 to 8192 tokens, bf16        90 us, 6260 GB/s
-//     the same lengths to 16384, e4m3                99 us, 6060 GB/s
-//     256 requests of 1 to 600 tokens, bf16          40 us, 3690 GB/s (the rows' ends)
+//     4 requests of 100003 to 131072 tokens, bf16   278 us, 6830 GB/s
+//     64 requests of 200 to 8192 tokens, bf16        90 us, 6260 GB/s
+//     64 of 500 to 16384, e4m3, 64 query heads       99 us, 6060 GB/s
+//     256 requests of up to 1000 tokens, bf16        40 us, 3690 GB/s (the rows' ends)
 //     1 request of 777 tokens                       9.8 us (the dependent steps: lengths
 //         1.7, pages and cache rows 3.3, arrival 1.0, joining and storing 2.1)
 //
@@ -1204,7 +1204,7 @@ cudaError_t launch_shape(const AttendArgs &a, int num_sms, cudaStream_t st) {
 // that fit the registers and leave the ring 100 KB or more of an SM.  Few warps in
 // many small CTAs end their rows independently of each other; many heads or long
 // ones take more registers or more products for each byte that is fetched.  Device
-// times in us, 64 requests of 500 to 8192 tokens (e4m3: to 16384) where not said:
+// times in us, 64 requests of up to 8192 tokens (e4m3: to 16384) where not said:
 //     group <= 8, dim <= 128   2,1,4: 90.3, 256 short requests 40.4; 4,2,2: 100.4, 59.6
 //       e4m3, dim <= 64        2,1,6: 74.9, 2,1,5: 78.7, 2,1,4: 87.8; bf16 67.4, -, 61.1
 //     group > 8: 16 heads at a time, each key fetched once: 79.9 (4,2,2); in eights
