@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import sys
 from typing import Optional
 
@@ -114,6 +115,16 @@ class _NormStruct(ctypes.Structure):
                 ("layer", ctypes.c_int32)]
 
 
+def _packer(cls):
+    """``struct`` form of a structure, whose fields take less time to fill."""
+    codes = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f"}
+    form = "@" + "".join(codes[t] for _, t in cls._fields_)
+    return struct.Struct(f"{form}{ctypes.sizeof(cls) - struct.calcsize(form)}x")
+
+
+_ATTENTION, _NORM = _packer(_AttentionStruct), _packer(_NormStruct)
+
+
 class KvCache:
     """A paged key/value cache over the caller's tensors (scute_kv_cache).
 
@@ -191,10 +202,12 @@ def _rows(t, n, cols, size=None):
     if size is not None and t.element_size() != size:
         raise ValueError(f"expected elements of {size} bytes, got {t.dtype}")
     shape, st = t.shape, t.stride()
-    if len(shape) == 3:
+    if shape == (n, cols):
+        ok = st[1] == 1 or cols == 1
+    elif len(shape) == 3:
         ok = shape[0] == n and shape[1] * shape[2] == cols and st[2] == 1 and (st[1] == shape[2] or shape[1] == 1)
     else:
-        ok = len(shape) == 2 and shape[0] == n and shape[1] == cols and (st[1] == 1 or cols == 1)
+        ok = False
     if not ok and n:
         raise ValueError(f"expected {n} rows of {cols} consecutive elements, got shape {tuple(shape)}, strides {st}")
     return st[0] if n > 1 else max(st[0], cols)
@@ -450,19 +463,19 @@ def scute_kv_append(ctx, cache: KvCache, slot_map, n, k, k_stride, v, v_stride, 
 
 def scute_paged_attention(ctx, cache: KvCache, q, q_stride, out, out_stride, lse, kv_len, n_req, q_heads,
                           scale=0.0, softcap=0.0, window=0, stream=None):
-    a = _AttentionStruct(ptr(q), q_stride, ptr(out), out_stride, ptr(lse), ptr(kv_len), n_req, q_heads, scale,
-                         softcap, window)
-    _check(ctx, load().scute_paged_attention(ctx, cache.ref, ctypes.byref(a), _stream_handle(stream)))
+    a = _ATTENTION.pack(ptr(q) or 0, q_stride, ptr(out) or 0, out_stride, ptr(lse) or 0, ptr(kv_len) or 0, n_req,
+                        q_heads, scale, softcap, window)
+    _check(ctx, load().scute_paged_attention(ctx, cache.ref, a, _stream_handle(stream)))
 
 
 def scute_residual_norm(ctx, n, d, y, y_stride, residual=None, residual_stride=0, residual_out=None,
                         residual_out_stride=0, out=None, out_stride=0, post_w=None, post_b=None, pre_w=None,
                         pre_b=None, gate_vec=None, gate_rows=None, gate_stride=0, scale=1.0, eps=1e-5, layer=False,
                         stream=None):
-    a = _NormStruct(ptr(y), y_stride, ptr(residual), residual_stride, ptr(residual_out), residual_out_stride, ptr(out),
-                    out_stride, ptr(post_w), ptr(post_b), ptr(pre_w), ptr(pre_b), ptr(gate_vec), ptr(gate_rows),
-                    gate_stride, scale, eps, 1 if layer else 0)
-    _check(ctx, load().scute_residual_norm(ctx, ctypes.byref(a), n, d, _stream_handle(stream)))
+    a = _NORM.pack(ptr(y) or 0, y_stride, ptr(residual) or 0, residual_stride, ptr(residual_out) or 0,
+                   residual_out_stride, ptr(out) or 0, out_stride, ptr(post_w) or 0, ptr(post_b) or 0, ptr(pre_w) or 0,
+                   ptr(pre_b) or 0, ptr(gate_vec) or 0, ptr(gate_rows) or 0, gate_stride, scale, eps, 1 if layer else 0)
+    _check(ctx, load().scute_residual_norm(ctx, a, n, d, _stream_handle(stream)))
 
 
 def scute_byte_model(layer: BmLayer, ids_host, n) -> dict:
