@@ -202,6 +202,10 @@ struct MmaMath {
     static constexpr int VE = FP8 && DC > 64 ? 16 : 8;    // elements of a value piece, eight lanes wide
     static constexpr int VP = DC / (8 * VE);
     static constexpr int VW = VE * ESZ / 4;               // its words
+    // How far below the largest score the reference is set, in powers of two.  16-bit
+    // weights of an 8-bit cache end at 2^-24: set 2^7 below, with weights up to 2^15,
+    // tokens count down to 2^-31 of the largest weight, of which a million are 2^-11.
+    static constexpr float ABOVE = FP8 ? 7.f : 0.f;
     static constexpr int OT = VE / 2;                     // 16-row output tiles of a value piece
 
     const int lane, g, c;
@@ -340,8 +344,8 @@ struct MmaMath {
                         if (!(ok >> (m * 16 + (k >> 1) * 8 + g) & 1)) sc[m][nt][k] = -INFINITY;
         }
         // scores in powers of two; the reference of the weights moves only when a
-        // score passes it by more than 2^8, so that the outputs are seldom scaled
-        // (weights are then at most 2^8, which every type here holds)
+        // score passes where it was set by more than 2^8, so that the outputs are
+        // seldom scaled
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float mx[2] = {-INFINITY, -INFINITY};
@@ -349,11 +353,11 @@ struct MmaMath {
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) mx[k & 1] = fmaxf(mx[k & 1], sc[m][nt][k]);
-            if (__any_sync(0xffffffffu, mx[0] > top[nt][0] + 8.f || mx[1] > top[nt][1] + 8.f)) {
+            if (__any_sync(0xffffffffu, mx[0] > top[nt][0] + (ABOVE + 8.f) || mx[1] > top[nt][1] + (ABOVE + 8.f))) {
                 float al[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float x = fmaxf(reduce_max(mx[k]), top[nt][k]);
+                    const float x = fmaxf(reduce_max(mx[k]) - ABOVE, top[nt][k]);
                     al[k] = x == top[nt][k] ? 1.f : exp2f(top[nt][k] - x);
                     top[nt][k] = x;
                     sum[nt][k] *= al[k];

@@ -194,6 +194,23 @@ def test_attention_large_scores_and_one_token_dominates(scute, contexts):
     check_attend(out, lse, q, tokens, "bf16", 4)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "fp8"])
+def test_attention_long_tail_of_small_weights(scute, contexts, kind):
+    """One token 2^26 times as heavy as each of 20000 others, whose sum still counts
+    (many requests on the same pages, so that a warp takes most of a row)."""
+    n, L, D = 700, 20000, 64
+    k, v = torch.zeros(L // 16, 1, 16, D), torch.ones(L // 16, 1, 16, D)
+    k[0, 0, 0], v[0, 0, 0] = 1.5, 0.0
+    cache = scute.KvCache(k.to(DT[kind]).cuda(), v.to(DT[kind]).cuda(), i32(np.tile(np.arange(L // 16), (n, 1))))
+    q = torch.full((n, 1, D), 1.5, device="cuda").to(DT["fp32" if kind == "fp32" else "bf16"])
+    out, lse = torch.empty_like(q), torch.empty(n, 1, device="cuda")
+    ctx = ctx_of(contexts, kind)
+    ctx.paged_attention(cache, q, i32([L] * n), out, lse=lse)
+    assert ctx.sync_status() == 0
+    one = f64(k).reshape(-1, 1, D), f64(v).reshape(-1, 1, D)
+    check_attend(out, lse, q, [one] * n, kind, 1)
+
+
 def test_attention_strided_in_place_on_another_stream_without_lse(scute, contexts):
     g = np.random.default_rng(11)
     lens = [40, 0, 333]
