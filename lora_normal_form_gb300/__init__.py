@@ -131,7 +131,8 @@ class KvCache:
     ``k``, ``v``: device pools [n_pages, kv_heads, page_size, head_dim], or
     [n_pages, page_size, kv_heads, head_dim] with ``token_major``; the strides
     are taken from ``k`` and ``v`` must have the same.  ``block_table``: device
-    int32 [n_req, pages of a request] (attention only).  ``k_scale``,
+    int32 [n_req, pages of a request] (attention only), a row of its own for each
+    request (not one row expanded).  ``k_scale``,
     ``v_scale``: device float32 [kv_heads] or None.  Holds references to the
     tensors, copies nothing."""
 
@@ -155,10 +156,13 @@ class KvCache:
                 raise ValueError("scales are float32, one for each key/value head")
         if block_table is not None:
             _check_table(block_table)
+            requests, cols = block_table.shape
+            # the pitch of one row or none is never used
+            pitch = block_table.stride(0) if requests > 1 else cols
+            if pitch < cols:
+                raise ValueError(f"a block table's rows may not overlap: {cols} entries, {pitch} apart")
             self.struct.block_table = block_table.data_ptr()
-            self.struct.table_stride = max(block_table.stride(0), block_table.shape[1])
-            self.struct.table_cols = block_table.shape[1]
-            self.requests = block_table.shape[0]
+            self.struct.table_stride, self.struct.table_cols, self.requests = pitch, cols, requests
         self.ref = ctypes.byref(self.struct)
 
 
