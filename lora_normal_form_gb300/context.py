@@ -125,7 +125,13 @@ class Context:
                         positions, token_req, rows, stream)
 
     def rope_table(self, cos_sin, theta: float = 10000.0, inv_freq=None, stream=None):
-        """Fill the float32 table ``cos_sin`` [n_pos, rotary_dim]."""
+        """Fill the float32 table ``cos_sin`` [n_pos, rotary_dim]; ``inv_freq``:
+        float64 [rotary_dim / 2]."""
+        if cos_sin.dim() != 2 or not cos_sin.is_contiguous() or str(cos_sin.dtype) != "torch.float32":
+            raise ValueError("cos_sin is a contiguous float32 table")
+        if inv_freq is not None and (str(inv_freq.dtype) != "torch.float64" or not inv_freq.is_contiguous()
+                                     or 2 * inv_freq.numel() != cos_sin.shape[1]):
+            raise ValueError("inv_freq is consecutive float64, one for each pair")
         scute_rope_table(self.handle, cos_sin, cos_sin.shape[0], cos_sin.shape[1], theta, inv_freq, stream)
 
     def kv_append(self, cache: KvCache, slot_map, k, v, q=None, q_out=None, rope: Rope = None, stream=None):

@@ -57,3 +57,18 @@ def test_cache_refuses_tables_whose_rows_overlap(lib):
         assert (c.struct.table_stride, c.struct.table_cols, c.requests) == (cols, cols, rows)
     with pytest.raises(ValueError):
         lib.KvCache(pool, pool, whole(1, 1).expand(8, 1))
+
+
+# ---------------------------------------------------------------- the rotary table
+def test_rope_table_refuses_what_it_would_read_or_write_wrongly(lib):
+    """Frequencies are 64-bit: 32-bit ones of the right number would be read to
+    twice their length."""
+    ctx, out, inv = no_handle(lib), half(9, 6, t=torch.float32), half(3, t=torch.float64)
+    refused_by_library(lib, lambda: ctx.rope_table(out, 10000.0))
+    refused_by_library(lib, lambda: ctx.rope_table(out, inv_freq=inv))
+    for bad in (inv.float(), inv[:2], half(4, t=torch.float64), half(6, t=torch.float64)[::2], half(3, 1, t=torch.float64)[:2]):
+        with pytest.raises(ValueError):
+            ctx.rope_table(out, inv_freq=bad)
+    for bad in (out.double(), out.bfloat16(), whole(9, 6), out.t(), out[:, :4], out[::2], out.view(9, 2, 3), out.view(-1)):
+        with pytest.raises(ValueError):
+            ctx.rope_table(bad, inv_freq=None)
