@@ -152,7 +152,7 @@ class KvCache:
                                      self.kv_heads, self.head_dim, stride(0), stride(tok), stride(head), None, 0, 0,
                                      ptr(k_scale), ptr(v_scale))
         for s in (k_scale, v_scale):
-            if s is not None and (s.numel() != self.kv_heads or not s.is_contiguous() or s.element_size() != 4):
+            if s is not None and (s.numel() != self.kv_heads or not s.is_contiguous() or s.dtype is not _torch().float32):
                 raise ValueError("scales are float32, one for each key/value head")
         if block_table is not None:
             _check_table(block_table)
@@ -173,9 +173,9 @@ class Rope:
 
     def __init__(self, cos_sin, positions, sections=None, interleaved=False):
         axes = 1 if positions.dim() == 1 else positions.shape[0]
-        if positions.element_size() != 4 or positions.stride(-1) != 1 or not 1 <= axes <= 4:
+        if positions.dtype is not _torch().int32 or positions.stride(-1) != 1 or not 1 <= axes <= 4:
             raise ValueError("positions are int32, [n] or [axes, n] with at most 4 axes")
-        if cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.element_size() != 4:
+        if cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.dtype is not _torch().float32:
             raise ValueError("cos_sin is a contiguous float32 table")
         if axes > 1 and (sections is None or len(sections) != axes):
             raise ValueError("several axes need a section each")
@@ -187,24 +187,29 @@ class Rope:
         self.ref = ctypes.byref(self.struct)
 
 
+def _torch():
+    """torch, which has been imported where there is a tensor to check."""
+    return sys.modules["torch"]
+
+
 def _check_table(t):
-    if t.dim() != 2 or t.element_size() != 4 or (t.numel() > 1 and t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2 or t.dtype is not _torch().int32 or (t.numel() > 1 and t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError("a block table is int32 [n_req, pages] with consecutive rows")
 
 
-def _flat(count, *tensors):
-    """Check that each is None or ``count`` consecutive 4-byte elements."""
+def _flat(dtype, count, *tensors):
+    """Check that each is None or ``count`` consecutive elements of a type."""
     for t in tensors:
-        if t is not None and (t.nbytes != 4 * count or not t.is_contiguous()):
-            raise ValueError(f"expected {count} consecutive 4-byte elements, got shape {tuple(t.shape)}, strides "
+        if t is not None and (t.dtype is not dtype or t.numel() != count or not t.is_contiguous()):
+            raise ValueError(f"expected {count} consecutive elements of {dtype}, got shape {tuple(t.shape)}, strides "
                              f"{t.stride()}, {t.dtype}")
 
 
-def _rows(t, n, cols, size=None):
+def _rows(t, n, cols, dtype=None):
     """Elements between the rows of ``t``: [n, cols], or [n, heads, dim] with
-    consecutive heads; elements of ``size`` bytes."""
-    if size is not None and t.element_size() != size:
-        raise ValueError(f"expected elements of {size} bytes, got {t.dtype}")
+    consecutive heads; elements of a type."""
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"expected elements of {dtype}, got {t.dtype}")
     shape, st = t.shape, t.stride()
     if shape == (n, cols):
         ok = st[1] == 1 or cols == 1

@@ -3,7 +3,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (BF16, FP32, METHOD_ID, KvCache, Rope, _check_table, _flat, _rows, scute_add_layer, scute_create, scute_debug_index, scute_destroy,
+from . import (BF16, FP32, METHOD_ID, KvCache, Rope, _check_table, _flat, _rows, _torch, scute_add_layer, scute_create, scute_debug_index, scute_destroy,
                scute_kv_append, scute_kv_resize, scute_launch_count, scute_linear, scute_linear_batch, scute_linear_batch_host,
                scute_linear_host, scute_paged_attention, scute_predict_batch, scute_predict_bytes,
                scute_register_adapter, scute_residual_norm, scute_rope_table, scute_set_shared, scute_set_variant, scute_sync_status,
@@ -17,7 +17,6 @@ class Context:
     def __init__(self, dtype: str = "bf16", max_tokens: int = 1024, max_adapters: int = 64,
                  max_layers: int = 16, device: int = 0):
         self.dtype = dtype
-        self.esz = 2 if dtype == "bf16" else 4
         self.device = device
         self.max_tokens = max_tokens
         self.handle = scute_create(device, BF16 if dtype == "bf16" else FP32, max_tokens, max_adapters,
@@ -103,6 +102,9 @@ class Context:
                                 BF16 if out_dtype == "bf16" else FP32, stream)
 
     # ---------------------------------------------------------------- between the projections
+    def _type(self):
+        return _torch().bfloat16 if self.dtype == "bf16" else _torch().float32
+
     def kv_resize(self, len_in, len_new, block_table, page_size: int, free_pages, free_in, free_out, len_out, cu_new,
                   slot_map, positions, token_req, stream=None):
         """Pages for every request's new length, slots for its new tokens (device
@@ -111,7 +113,9 @@ class Context:
         _check_table(block_table)
         n, (requests, cols) = len_in.numel(), block_table.shape
         rows, n_free = slot_map.numel(), free_pages.numel()
-        if not (requests >= n and len_in.nbytes == len_new.nbytes == len_out.nbytes == 4 * n
+        if not (len_in.dtype is len_new.dtype is len_out.dtype is cu_new.dtype is free_in.dtype is free_out.dtype
+                is slot_map.dtype is positions.dtype is token_req.dtype is free_pages.dtype is _torch().int32
+                and requests >= n and len_in.nbytes == len_new.nbytes == len_out.nbytes == 4 * n
                 and cu_new.nbytes == 4 * n + 4 and free_in.nbytes == free_out.nbytes == 4
                 and slot_map.nbytes == positions.nbytes == token_req.nbytes == 4 * rows and free_pages.nbytes == 4 * n_free
                 and len_in.is_contiguous() and len_new.is_contiguous() and len_out.is_contiguous()
@@ -127,9 +131,9 @@ class Context:
     def rope_table(self, cos_sin, theta: float = 10000.0, inv_freq=None, stream=None):
         """Fill the float32 table ``cos_sin`` [n_pos, rotary_dim]; ``inv_freq``:
         float64 [rotary_dim / 2]."""
-        if cos_sin.dim() != 2 or not cos_sin.is_contiguous() or str(cos_sin.dtype) != "torch.float32":
+        if cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.dtype is not _torch().float32:
             raise ValueError("cos_sin is a contiguous float32 table")
-        if inv_freq is not None and (str(inv_freq.dtype) != "torch.float64" or not inv_freq.is_contiguous()
+        if inv_freq is not None and (inv_freq.dtype is not _torch().float64 or not inv_freq.is_contiguous()
                                      or 2 * inv_freq.numel() != cos_sin.shape[1]):
             raise ValueError("inv_freq is consecutive float64, one for each pair")
         scute_rope_table(self.handle, cos_sin, cos_sin.shape[0], cos_sin.shape[1], theta, inv_freq, stream)
@@ -137,45 +141,45 @@ class Context:
     def kv_append(self, cache: KvCache, slot_map, k, v, q=None, q_out=None, rope: Rope = None, stream=None):
         """Write k and v [n, kv_heads, dim] (or [n, kv_heads * dim]) into the cache;
         keys, and queries into ``q_out``, turned by ``rope``."""
-        n, row, size = slot_map.shape[0], cache.kv_row, self.esz
-        _flat(n, slot_map)
+        n, row, io = slot_map.shape[0], cache.kv_row, self._type()
+        _flat(_torch().int32, n, slot_map)
         q_heads = q_stride = q_out_stride = 0
         if q is not None:
             q_row = q.numel() // n if n else cache.head_dim
             q_heads = q_row // cache.head_dim
             if q_out is None or q_heads * cache.head_dim != q_row:
                 raise ValueError("q rows are heads * head_dim elements, and need q_out")
-            q_stride, q_out_stride = _rows(q, n, q_row, size), _rows(q_out, n, q_row, size)
+            q_stride, q_out_stride = _rows(q, n, q_row, io), _rows(q_out, n, q_row, io)
         if rope is not None and rope.n < n:
             raise ValueError("fewer positions than rows")
-        scute_kv_append(self.handle, cache, slot_map, n, k, _rows(k, n, row, size), v, _rows(v, n, row, size), q, q_stride,
+        scute_kv_append(self.handle, cache, slot_map, n, k, _rows(k, n, row, io), v, _rows(v, n, row, io), q, q_stride,
                         q_heads, q_out, q_out_stride, rope, stream)
 
     def paged_attention(self, cache: KvCache, q, kv_len, out, scale: float = 0.0, softcap: float = 0.0,
                         window: int = 0, lse=None, stream=None):
         """One new token of each request over its cached tokens: q and out
         [n_req, q_heads, dim] (or [n_req, q_heads * dim])."""
-        n, dim, size = kv_len.shape[0], cache.head_dim, self.esz
+        n, dim, io = kv_len.shape[0], cache.head_dim, self._type()
         row = q.numel() // n if n else cache.kv_row
         if row % dim or cache.requests < n :
             raise ValueError("q rows are heads * head_dim elements, and the block table has a row for each request")
-        _flat(n, kv_len)
-        _flat(n * row // dim, lse)
-        scute_paged_attention(self.handle, cache, q, _rows(q, n, row, size), out, _rows(out, n, row, size), lse, kv_len, n,
+        _flat(_torch().int32, n, kv_len)
+        _flat(_torch().float32, n * row // dim, lse)
+        scute_paged_attention(self.handle, cache, q, _rows(q, n, row, io), out, _rows(out, n, row, io), lse, kv_len, n,
                               row // dim, scale, softcap, window, stream)
 
     def residual_norm(self, y, out=None, residual=None, residual_out=None, pre_w=None, pre_b=None, post_w=None,
                       post_b=None, gate=None, scale: float = 1.0, eps: float = 1e-5, layer: bool = False, stream=None):
         """h = residual + scale * gate * post(y), out = pre(h), for rows [n, d].
         ``gate``: float32 [d], or the context's dtype [n, d]."""
-        (n, d), size = y.shape, self.esz
+        (n, d), io = y.shape, self._type()
         gate_vec, gate_rows = (None, gate) if gate is not None and gate.dim() == 2 else (gate, None)
-        _flat(d, post_w, post_b, pre_w, pre_b, gate_vec)
-        scute_residual_norm(self.handle, n, d, y, _rows(y, n, d, size),
-                            residual, 0 if residual is None else _rows(residual, n, d, size),
-                            residual_out, 0 if residual_out is None else _rows(residual_out, n, d, size),
-                            out, 0 if out is None else _rows(out, n, d, size), post_w, post_b, pre_w, pre_b, gate_vec,
-                            gate_rows, 0 if gate_rows is None else _rows(gate_rows, n, d, size), scale, eps, layer, stream)
+        _flat(_torch().float32, d, post_w, post_b, pre_w, pre_b, gate_vec)
+        scute_residual_norm(self.handle, n, d, y, _rows(y, n, d, io),
+                            residual, 0 if residual is None else _rows(residual, n, d, io),
+                            residual_out, 0 if residual_out is None else _rows(residual_out, n, d, io),
+                            out, 0 if out is None else _rows(out, n, d, io), post_w, post_b, pre_w, pre_b, gate_vec,
+                            gate_rows, 0 if gate_rows is None else _rows(gate_rows, n, d, io), scale, eps, layer, stream)
 
     def sync_status(self) -> int:
         return scute_sync_status(self.handle)

@@ -20,7 +20,7 @@ def lib():
 
 def no_handle(lib, dtype="bf16"):
     c = object.__new__(lib.Context)
-    c.dtype, c.esz, c.handle, c.device = dtype, 2 if dtype == "bf16" else 4, None, 0
+    c.dtype, c.handle, c.device = dtype, None, 0
     return c
 
 
@@ -72,3 +72,44 @@ def test_rope_table_refuses_what_it_would_read_or_write_wrongly(lib):
     for bad in (out.double(), out.bfloat16(), whole(9, 6), out.t(), out[:, :4], out[::2], out.view(9, 2, 3), out.view(-1)):
         with pytest.raises(ValueError):
             ctx.rope_table(bad, inv_freq=None)
+
+
+# ---------------------------------------------------------------- types of the right size
+def test_other_types_of_the_same_size_are_refused(lib):
+    """float16 is no bf16, and neither float32 nor an unsigned or int32 tensor the
+    other: the kernels would read the bits as another type's numbers."""
+    ctx, f32 = no_handle(lib), no_handle(lib, "fp32")
+    f16, real = lambda *s: half(*s, t=torch.float16), lambda *s: half(*s, t=torch.float32)  # noqa: E731
+    pool = half(4, 2, 16, 64)
+    cache = lib.KvCache(pool, pool, whole(2, 2))
+    for kw in (dict(block_table=real(2, 2)), dict(k_scale=whole(2)), dict(v_scale=whole(2))):
+        with pytest.raises(ValueError):
+            lib.KvCache(pool, pool, **kw)
+    for args in ((real(10, 64), real(3)), (whole(10, 64), whole(3))):
+        with pytest.raises(ValueError):
+            lib.Rope(*args)
+    rope, k, q, y, w = lib.Rope(real(10, 64), whole(3)), half(3, 2, 64), half(2, 4, 64), half(2, 64), real(64)
+    lens, slots = whole(2), whole(3)
+    attend = lambda q=q, lens=lens, out=q, **kw: ctx.paged_attention(cache, q, lens, out, **kw)  # noqa: E731
+    append = lambda slots=slots, k=k, v=k, q=k, q_out=k: ctx.kv_append(cache, slots, k, v, q=q, q_out=q_out, rope=rope)  # noqa: E731
+    norm = lambda y=y, out=y, **kw: ctx.residual_norm(y, out, **kw)  # noqa: E731
+    steps = dict(len_in=whole(2), len_new=whole(2), block_table=whole(2, 2), page_size=16, free_pages=whole(4),
+                 free_in=whole(1), free_out=whole(1), len_out=whole(2), cu_new=whole(3), slot_map=whole(2),
+                 positions=whole(2), token_req=whole(2))
+    good = [attend, lambda: attend(lse=real(2, 4)), append, norm, lambda: norm(pre_w=w, gate=y, residual=y, residual_out=y),
+            lambda: norm(gate=w), lambda: ctx.kv_resize(**steps), lambda: f32.residual_norm(real(2, 64), real(2, 64))]
+    bad = [lambda: attend(q=f16(2, 4, 64)), lambda: attend(out=f16(2, 4, 64)), lambda: attend(q=q.view(torch.int16)),
+           lambda: attend(lens=real(2)), lambda: attend(lse=whole(2, 4)),
+           lambda: append(slots=real(3)), lambda: append(k=f16(3, 2, 64)), lambda: append(v=f16(3, 2, 64)),
+           lambda: append(q=f16(3, 2, 64)), lambda: append(q_out=f16(3, 2, 64)),
+           lambda: norm(y=f16(2, 64)), lambda: norm(out=f16(2, 64)), lambda: norm(residual=f16(2, 64)),
+           lambda: norm(residual_out=f16(2, 64)), lambda: norm(gate=f16(2, 64)), lambda: norm(gate=whole(64)),
+           lambda: f32.residual_norm(whole(2, 64), real(2, 64)), lambda: f32.residual_norm(real(2, 64), whole(2, 64))]
+    bad += [lambda n=n: norm(out=y, **{n: whole(64)}) for n in ("pre_w", "pre_b", "post_w", "post_b")]
+    bad += [lambda n=n: ctx.kv_resize(**{**steps, n: real(*steps[n].shape)}) for n in steps if n != "page_size"]
+    for call in good:
+        refused_by_library(lib, call)
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            raise AssertionError(i)
