@@ -145,9 +145,9 @@ class KvCache:
         self.tensors = (k, v, block_table, k_scale, v_scale)
         self.page_size, self.kv_heads, self.head_dim = k.shape[tok], k.shape[head], k.shape[3]
         self.kv_row, self.requests = self.kv_heads * self.head_dim, 0
-        # a dimension of one element may carry any stride: give it one that passes for its rows
+        # a dimension of one element may carry any stride, which is never used: give it one that passes
         def stride(dim):
-            return k.stride(dim) if k.shape[dim] > 1 else max(k.stride(dim), self.head_dim)
+            return k.stride(dim) if k.shape[dim] > 1 else self.head_dim
         self.struct = _KvCacheStruct(k.data_ptr(), v.data_ptr(), _KV_DTYPE[str(k.dtype)], k.shape[0], self.page_size,
                                      self.kv_heads, self.head_dim, stride(0), stride(tok), stride(head), None, 0, 0,
                                      ptr(k_scale), ptr(v_scale))
@@ -173,7 +173,7 @@ class Rope:
 
     def __init__(self, cos_sin, positions, sections=None, interleaved=False):
         axes = 1 if positions.dim() == 1 else positions.shape[0]
-        if positions.dtype is not _torch().int32 or positions.stride(-1) != 1 or not 1 <= axes <= 4:
+        if positions.dtype is not _torch().int32 or (positions.stride(-1) != 1 and positions.shape[-1] > 1) or not 1 <= axes <= 4:
             raise ValueError("positions are int32, [n] or [axes, n] with at most 4 axes")
         if cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.dtype is not _torch().float32:
             raise ValueError("cos_sin is a contiguous float32 table")
@@ -219,7 +219,7 @@ def _rows(t, n, cols, dtype=None):
         ok = False
     if not ok and n:
         raise ValueError(f"expected {n} rows of {cols} consecutive elements, got shape {tuple(shape)}, strides {st}")
-    return st[0] if n > 1 else max(st[0], cols)
+    return st[0] if n > 1 else cols          # one row's pitch is never used
 
 
 _lib: Optional[ctypes.CDLL] = None

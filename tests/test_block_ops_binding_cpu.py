@@ -113,3 +113,22 @@ def test_other_types_of_the_same_size_are_refused(lib):
         with pytest.raises(ValueError):
             call()
             raise AssertionError(i)
+
+
+# ---------------------------------------------------------------- dimensions of one element
+def test_strides_of_dimensions_of_one_element_do_not_count(lib):
+    """One row, page, head or token may carry any stride: the library gets one
+    that passes (rows' and pools' strides are multiples of 16 bytes there)."""
+    row = half(1, 1031)[:, :512]
+    assert row.stride(0) == 1031 and lib._rows(row, 1, 512, torch.bfloat16) == 512
+    assert lib._rows(half(1, 1031)[:, :512].view(1, 8, 64), 1, 512) == 512
+    pool = torch.zeros(4 * 16 * 64 + 72, dtype=torch.bfloat16)
+    for shape, strides in (((4, 1, 16, 64), (1024, 1031, 64, 1)), ((1, 2, 16, 64), (2061, 1024, 64, 1)),
+                           ((2, 2, 1, 64), (128, 64, 67, 1))):
+        k = pool.as_strided(shape, strides)
+        c = lib.KvCache(k, k)
+        assert all(s >= 64 and s % 8 == 0 for s in (c.struct.page_stride, c.struct.head_stride, c.struct.token_stride))
+    at = whole(12).as_strided((2, 1), (5, 3))
+    assert lib.Rope(half(10, 64, t=torch.float32), at, sections=[16, 16]).struct.axis_stride == 5
+    with pytest.raises(ValueError):
+        lib.Rope(half(10, 64, t=torch.float32), whole(12).as_strided((2, 2), (5, 3)), sections=[16, 16])
