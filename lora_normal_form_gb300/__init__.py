@@ -309,12 +309,10 @@ def ptr(x) -> Optional[int]:
     """Address of a torch tensor, numpy array, int or None."""
     if x is None:
         return None
-    try:
-        return x.data_ptr()
-    except AttributeError:
-        pass
     if isinstance(x, int):
         return x
+    if hasattr(x, "data_ptr"):
+        return x.data_ptr()
     if hasattr(x, "ctypes"):
         if not x.flags["C_CONTIGUOUS"]:
             raise ValueError("numpy array must be C-contiguous")

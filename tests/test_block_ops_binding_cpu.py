@@ -132,3 +132,30 @@ def test_strides_of_dimensions_of_one_element_do_not_count(lib):
     assert lib.Rope(half(10, 64, t=torch.float32), at, sections=[16, 16]).struct.axis_stride == 5
     with pytest.raises(ValueError):
         lib.Rope(half(10, 64, t=torch.float32), whole(12).as_strided((2, 2), (5, 3)), sections=[16, 16])
+
+
+# ---------------------------------------------------------------- addresses
+def test_addresses_are_taken_without_exceptions(lib):
+    """An integer, an array and a tensor: none by way of an exception raised and
+    caught (eight times an integer's own cost, on every call that passes one)."""
+    import sys
+
+    import numpy as np
+
+    a, t, raised = np.arange(3.0), half(3), []
+
+    def watch(frame, event, arg):
+        if event == "exception":
+            raised.append(frame.f_code.co_name)
+        return watch
+
+    before = sys.gettrace()
+    sys.settrace(watch)
+    try:
+        got = [lib.ptr(x) for x in (None, 4096, True, a, t)]
+    finally:
+        sys.settrace(before)
+    assert got == [None, 4096, True, a.ctypes.data, t.data_ptr()] and not raised
+    for bad in (a[::2], "x", 1.5):
+        with pytest.raises((ValueError, TypeError)):
+            lib.ptr(bad)
