@@ -372,7 +372,9 @@ typedef struct {
  *     slot_map[i], positions[i] and token_req[i] are row i's cache slot, its
  *     position in its request and its request.  Rows beyond them, up to
  *     max_new, get -1, 0 and -1 (scute_kv_append skips slot -1), so that a
- *     captured step can have a fixed number of rows.
+ *     captured step can have a fixed number of rows.  A row whose page number
+ *     (of the table or the free list) is negative, or so large that no slot of
+ *     31 bits comes of it, gets INT32_MIN and is recorded (SCUTE_ERR_PAGES).
  *   - cu_new [n_req + 1]: request r's rows are cu_new[r] .. cu_new[r + 1).
  * len_in, len_new, len_out  device int32 [n_req]; len_out may be len_in.  A
  *     length outside 0 .. table_cols * page_size is an error

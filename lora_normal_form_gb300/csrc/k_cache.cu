@@ -1,6 +1,8 @@
 // The paged cache's bookkeeping and writes: pages and slots from request
 // lengths (kv_resize), rotary positions and the cache write (kv_append), and
 // the rotary table.
+#include <climits>
+
 #include <cuda_fp8.h>
 
 #include "internal.h"
@@ -241,6 +243,7 @@ __global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs 
         const int want = pages_of(a, new_len(r));
         a.free_pages[F + j] = a.table[(long long)r * a.table_stride + want + ((int)j - drop_at[r])];
     }
+    bool unslotted = false;
     for (long long i = g0; i < a.max_new; i += step) {
         int slot = -1, pos = 0, r = -1;
         if (i < T) {
@@ -249,12 +252,18 @@ __global__ void __launch_bounds__(RS_THREADS) kv_resize_kernel(const ResizeArgs 
             pos = o + ((int)i - cu[r]);
             const int pg = page_index(a, pos), have = pages_of(a, o);
             const int page = pg < have ? a.table[(long long)r * a.table_stride + pg] : taken_page(need_at[r] + (pg - have));
-            slot = page * a.page_size + (pos - pg * a.page_size);
+            // page numbers are not checked before: one that forms no slot must become
+            // neither the mark of a padding row nor, cut to 32 bits, another's slot
+            const long long at_slot = (long long)page * a.page_size + (pos - pg * a.page_size);
+            const bool none = (unsigned long long)at_slot > INT_MAX;      // a negative page's too
+            unslotted |= none;
+            slot = none ? INT_MIN : (int)at_slot;
         }
         a.slot_map[i] = slot;
         a.positions[i] = pos;
         a.token_req[i] = r;
     }
+    if (unslotted) s_flag = 1;
     for (int r = g0; r <= n; r += step) a.cu_new[r] = cu[r];
 
     // lengths and the count: where they are written in place, by the last CTA to
