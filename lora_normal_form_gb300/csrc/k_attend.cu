@@ -775,16 +775,22 @@ struct SharedRow {
 };
 // Join the parts of up to two rows, as many parts at a time as `room` bytes of
 // shared memory hold, brought there at once; those of both rows where they fit.
+// How a row's parts are grouped depends on that row alone (its parts, heads and the
+// room): which CTA is the last of a row, and whether it joins another one beside it,
+// is a race, and a row joined in other groups has other bits.  A row whose parts fit
+// is joined in one group, alone or beside another; one whose parts do not, in groups
+// of as many as fit alone.
 template <typename IO, int THREADS>
 __device__ __forceinline__ void join_parts(const AttendArgs &a, const SharedRow &head, const SharedRow &tail, bool last_head,
                                            bool last_tail, uint8_t *buf, int room, int t) {
     constexpr int IT = 2;                // groups of four outputs of a thread at a time
-    const int D = a.kv.dim, n_head = last_head ? head.c1 - head.c0 + 1 : 0, n_tail = last_tail ? tail.c1 - tail.c0 + 1 : 0;
-    const int nh = max(last_head ? head.nh : 0, last_tail ? tail.nh : 0);
-    const int bytes = (2 * ATT_HEADS + nh * D) * 4, pieces = bytes / 16, cap = room / bytes, ld = bytes / 4;
-    auto bring_row = [&](int c0, int k0, int k1, uint32_t to) {      // a row's parts k0 .. k1
+    const int D = a.kv.dim;
+    auto parts_of = [&](const SharedRow &row, bool last) { return last ? row.c1 - row.c0 + 1 : 0; };
+    auto bytes_of = [&](const SharedRow &row) { return (2 * ATT_HEADS + row.nh * D) * 4; };      // of a part
+    auto bring_row = [&](const SharedRow &row, int k0, int k1, uint32_t to) {      // a row's parts k0 .. k1
+        const int bytes = bytes_of(row), pieces = bytes / 16;
         for (int e = t; e < pieces; e += THREADS) {
-            const float *from = part_of(a, 2 * (c0 + k0)).m + e * 4;
+            const float *from = part_of(a, 2 * (row.c0 + k0)).m + e * 4;
             uint32_t at = to + e * 16;
 #pragma unroll 4
             for (int k = k0; k < k1; ++k) {
@@ -794,21 +800,23 @@ __device__ __forceinline__ void join_parts(const AttendArgs &a, const SharedRow 
             }
         }
     };
-    auto bring = [&](int p0, int p1) {   // of the two rows' parts in turn
+    const uint32_t room_at = ptx::smem_u32(buf);
+    const int n_head = parts_of(head, last_head), n_tail = parts_of(tail, last_tail);
+    const int head_bytes = n_head ? n_head * bytes_of(head) : 0, tail_bytes = n_tail ? n_tail * bytes_of(tail) : 0;
+    const bool once = head_bytes + tail_bytes <= room;
+    if (once) {
         sync_threads<THREADS>();
-        const uint32_t to = ptx::smem_u32(buf);
-        if (p0 < n_head) bring_row(head.c0, p0, min(p1, n_head), to);
-        if (p1 > n_head) bring_row(tail.c0, max(p0 - n_head, 0), p1 - n_head, to + max(n_head - p0, 0) * bytes);
+        if (n_head) bring_row(head, 0, n_head, room_at);
+        if (n_tail) bring_row(tail, 0, n_tail, room_at + head_bytes);
         asm volatile("cp.async.wait_all;" ::: "memory");
         sync_threads<THREADS>();
-    };
-    const bool once = n_head + n_tail <= cap;
-    if (once) bring(0, n_head + n_tail);
+    }
 #pragma unroll 1
     for (int w = 0; w < 2; ++w) {
         if (!(w ? last_tail : last_head)) continue;
         const SharedRow &row = w ? tail : head;
-        const int q0 = w ? n_head : 0, q1 = w ? n_head + n_tail : n_head, items = row.nh * (D / 4);
+        const int count = w ? n_tail : n_head, items = row.nh * (D / 4);
+        const int bytes = bytes_of(row), ld = bytes / 4, cap = once ? count : room / bytes;
         const float vs = a.kv.v_scale ? a.kv.v_scale[row.hk] : 1.f;
 #pragma unroll 1
         for (int g0 = 0; g0 < items; g0 += IT * THREADS) {
@@ -817,10 +825,15 @@ __device__ __forceinline__ void join_parts(const AttendArgs &a, const SharedRow 
 #pragma unroll
             for (int i = 0; i < IT; ++i) m[i] = -INFINITY, l[i] = 0.f, x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-            for (int p0 = q0; p0 < q1; p0 += cap) {
-                const int p1 = once ? q1 : min(p0 + cap, q1);
-                if (!once) bring(p0, p1);
-                const float *parts = reinterpret_cast<const float *>(buf) + (once ? q0 * ld : 0);
+            for (int p0 = 0; p0 < count; p0 += cap) {
+                const int p1 = min(p0 + cap, count);
+                if (!once) {
+                    sync_threads<THREADS>();
+                    bring_row(row, p0, p1, room_at);
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    sync_threads<THREADS>();
+                }
+                const float *parts = reinterpret_cast<const float *>(buf + (once && w ? head_bytes : 0));
                 // the groups side by side, so that their loads overlap (past the row's
                 // end the last one's again)
                 const int k1 = p1 - p0;
@@ -855,7 +868,6 @@ __device__ __forceinline__ void join_parts(const AttendArgs &a, const SharedRow 
                         l[i] += pm[i][k * ld + ATT_HEADS] * g;
                         x[i].x += y.x * g, x[i].y += y.y * g, x[i].z += y.z * g, x[i].w += y.w * g;
                     }
-                if (once) break;
             }
 #pragma unroll
             for (int i = 0; i < IT; ++i) {

@@ -5,7 +5,7 @@ Definitions and bounds as in ``test_gpu_block_ops.py``."""
 import numpy as np
 import pytest
 
-from test_gpu_block_ops import PAGES, i32
+from test_gpu_block_ops import DT, PAGES, check_attend, ctx_of, i32, make_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +70,31 @@ def test_append_skips_and_records_what_forms_no_slot(scute, contexts):
     assert ctx.sync_status() == PAGES
     for p in pools:
         assert p[1, :, 1].eq(1).all() and p.sum() == 128
+
+
+# ---------------------------------------------------------------- joins
+@pytest.mark.parametrize("kind,D,group,H", [("fp32", 128, 12, 4), ("fp32", 128, 9, 4), ("bf16", 256, 12, 2), ("bf16", 128, 20, 2),
+                                            ("fp8", 128, 20, 2), ("bf16", 128, 4, 4)])
+def test_shared_rows_of_unequal_head_chunks_give_the_same_bits(scute, contexts, kind, D, group, H):
+    """A group that is no multiple of the heads taken at a time has rows of two
+    sizes.  Rows of about 13 parts do not fit the join's memory at once in the
+    larger size: how their parts are grouped may depend on the row alone, not on
+    which CTA happened to be last for it and what else that one had to join."""
+    g = np.random.default_rng(group + D)
+    lens = [4003, 4511, 5000, 5520, 6007, 4750]
+    cache, tokens = make_cache(scute, g, lens, H, D, 16, kind, False)
+    q = torch.from_numpy(g.standard_normal((len(lens), H * group, D), dtype=np.float32) * 2)
+    q = q.cuda().to(DT["fp32" if kind == "fp32" else "bf16"])
+    ctx, at = ctx_of(contexts, kind), i32(lens)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    ctx.paged_attention(cache, q, at, out, lse=lse)
+    assert ctx.sync_status() == 0
+    check_attend(out, lse, q, tokens, kind, group)
+    outs, lses = [torch.empty_like(out) for _ in range(200)], [torch.empty_like(lse) for _ in range(200)]
+    side = torch.zeros(1 << 26, device="cuda")
+    for i, (o, s) in enumerate(zip(outs, lses)):
+        if i % 2:
+            side.add_(1.0)             # another state of the L2, another order of arrival
+        ctx.paged_attention(cache, q, at, o, lse=s)
+    for o, s in zip(outs, lses):
+        assert torch.equal(o, out) and torch.equal(s, lse)
