@@ -102,8 +102,14 @@ class Context:
                                 BF16 if out_dtype == "bf16" else FP32, stream)
 
     # ---------------------------------------------------------------- between the projections
-    def _type(self):
-        return _torch().bfloat16 if self.dtype == "bf16" else _torch().float32
+    _types = None
+
+    def _dtypes(self):
+        """torch's types of rows, of whole numbers and of vectors, looked up at the first call."""
+        if self._types is None:
+            t = _torch()
+            self._types = t.bfloat16 if self.dtype == "bf16" else t.float32, t.int32, t.float32
+        return self._types
 
     def kv_resize(self, len_in, len_new, block_table, page_size: int, free_pages, free_in, free_out, len_out, cu_new,
                   slot_map, positions, token_req, stream=None):
@@ -114,7 +120,7 @@ class Context:
         n, (requests, cols) = len_in.numel(), block_table.shape
         rows, n_free = slot_map.numel(), free_pages.numel()
         if not (len_in.dtype is len_new.dtype is len_out.dtype is cu_new.dtype is free_in.dtype is free_out.dtype
-                is slot_map.dtype is positions.dtype is token_req.dtype is free_pages.dtype is _torch().int32
+                is slot_map.dtype is positions.dtype is token_req.dtype is free_pages.dtype is self._dtypes()[1]
                 and requests >= n and len_in.nbytes == len_new.nbytes == len_out.nbytes == 4 * n
                 and cu_new.nbytes == 4 * n + 4 and free_in.nbytes == free_out.nbytes == 4
                 and slot_map.nbytes == positions.nbytes == token_req.nbytes == 4 * rows and free_pages.nbytes == 4 * n_free
@@ -141,8 +147,8 @@ class Context:
     def kv_append(self, cache: KvCache, slot_map, k, v, q=None, q_out=None, rope: Rope = None, stream=None):
         """Write k and v [n, kv_heads, dim] (or [n, kv_heads * dim]) into the cache;
         keys, and queries into ``q_out``, turned by ``rope``."""
-        n, row, io = slot_map.shape[0], cache.kv_row, self._type()
-        _flat(_torch().int32, n, slot_map)
+        n, row, (io, int32, _) = slot_map.shape[0], cache.kv_row, self._dtypes()
+        _flat(int32, n, slot_map)
         q_heads = q_stride = q_out_stride = 0
         if q is not None:
             q_row = q.numel() // n if n else cache.head_dim
@@ -159,12 +165,12 @@ class Context:
                         window: int = 0, lse=None, stream=None):
         """One new token of each request over its cached tokens: q and out
         [n_req, q_heads, dim] (or [n_req, q_heads * dim])."""
-        n, dim, io = kv_len.shape[0], cache.head_dim, self._type()
+        n, dim, (io, int32, float32) = kv_len.shape[0], cache.head_dim, self._dtypes()
         row = q.numel() // n if n else cache.kv_row
-        if row % dim or cache.requests < n :
+        if row % dim or cache.requests < n:
             raise ValueError("q rows are heads * head_dim elements, and the block table has a row for each request")
-        _flat(_torch().int32, n, kv_len)
-        _flat(_torch().float32, n * row // dim, lse)
+        _flat(int32, n, kv_len)
+        _flat(float32, n * row // dim, lse)
         scute_paged_attention(self.handle, cache, q, _rows(q, n, row, io), out, _rows(out, n, row, io), lse, kv_len, n,
                               row // dim, scale, softcap, window, stream)
 
@@ -172,9 +178,9 @@ class Context:
                       post_b=None, gate=None, scale: float = 1.0, eps: float = 1e-5, layer: bool = False, stream=None):
         """h = residual + scale * gate * post(y), out = pre(h), for rows [n, d].
         ``gate``: float32 [d], or the context's dtype [n, d]."""
-        (n, d), io = y.shape, self._type()
+        (n, d), (io, _, float32) = y.shape, self._dtypes()
         gate_vec, gate_rows = (None, gate) if gate is not None and gate.dim() == 2 else (gate, None)
-        _flat(_torch().float32, d, post_w, post_b, pre_w, pre_b, gate_vec)
+        _flat(float32, d, post_w, post_b, pre_w, pre_b, gate_vec)
         scute_residual_norm(self.handle, n, d, y, _rows(y, n, d, io),
                             residual, 0 if residual is None else _rows(residual, n, d, io),
                             residual_out, 0 if residual_out is None else _rows(residual_out, n, d, io),
