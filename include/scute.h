@@ -636,8 +636,14 @@ scute_status scute_timing_kinds(const scute_ctx *ctx, int *kinds_out, int max, i
  * waits for a count that no CTA ever reaches: its bounded waits run out (about
  * 2 s), every CTA drains what it issued, frees TMEM and returns, and
  * scute_sync_status then reports SCUTE_ERR_TIMEOUT.  The context stays usable;
- * the hook applies to that one launch only.  Nothing traps or faults. */
+ * the hook applies to that one launch only.  Nothing traps or faults.
+ * SCUTE_INJECT_STALL_ATTENTION does the same to the context's next
+ * scute_paged_attention: its fetching warps never get a stage of cached tokens
+ * back, so that their waits and the computing warps' run out (where a CTA's
+ * share of the tokens is more than its stages hold); its outputs are then
+ * undefined.  what = 0 takes either hook back. */
 #define SCUTE_INJECT_STALL 1
+#define SCUTE_INJECT_STALL_ATTENTION 2
 scute_status scute_debug_inject(scute_ctx *ctx, int what);
 
 /* Separate-pass placements of two live slots, for validating the byte and

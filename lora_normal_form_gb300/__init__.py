@@ -550,7 +550,7 @@ def scute_timing_reset(ctx):
     _check(ctx, load().scute_timing_reset(ctx))
 
 
-INJECT_STALL = 1
+INJECT_STALL, INJECT_STALL_ATTENTION = 1, 2
 
 
 def scute_debug_inject(ctx, what: int) -> None:

@@ -1367,8 +1367,10 @@ scute_status scute_set_variant(scute_ctx *c, int flags) {
 
 scute_status scute_debug_inject(scute_ctx *c, int what) {
     if (!c) return SCUTE_ERR_ARG;
-    if (what != 0 && what != SCUTE_INJECT_STALL) return fail(c, SCUTE_ERR_ARG, "unknown injection %d", what);
-    c->inject = what;
+    if (what != 0 && what != SCUTE_INJECT_STALL && what != SCUTE_INJECT_STALL_ATTENTION)
+        return fail(c, SCUTE_ERR_ARG, "unknown injection %d", what);
+    c->inject = what == SCUTE_INJECT_STALL ? what : 0;
+    c->inject_attend = what == SCUTE_INJECT_STALL_ATTENTION;
     return SCUTE_OK;
 }
 

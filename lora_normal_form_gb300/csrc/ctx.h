@@ -97,6 +97,7 @@ struct scute_ctx {
     int step_bn_max = 64;
     int smem_optin = 0;
     int inject = 0;              // scute_debug_inject, consumed by the next decode launch
+    bool inject_attend = false;  // the same for the next attention launch
     int variant = 0;             // scute_set_variant: slots placed in separate passes
     std::vector<int64_t> last_plan;   // scute_debug_step_plan: the last decode launch's plan
     void *var_x = nullptr;       // rotated copies of the calls' x (separate rotation pass)

@@ -439,6 +439,7 @@ struct AttendArgs {
     float *part;               // partial sums of rows that several CTAs share
     int *ctr;                  // arrivals at such a row (zero between launches)
     int *status;
+    int hold;                  // 1: stages are never given back (test hook of the waits' end)
 };
 size_t attend_part_floats(int num_sms);
 int attend_ctrs(int num_sms);

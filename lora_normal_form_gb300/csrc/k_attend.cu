@@ -52,21 +52,27 @@ constexpr int ROW_COST = 3;
 constexpr int MIN_TILES = 4;
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
+// A whole warp's wait, ended by the warp's votes alone.  Lanes that poll each for
+// itself see the barrier complete, the time pass and the CTA's abort at their own
+// moments: one could be past the wait while another gave up, and neither would come
+// to the other's next shuffle.  (Polled again, a completed barrier is still complete:
+// it goes on only after this warp's own arrival or filling.)
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    constexpr unsigned ALL_LANES = 0xffffffffu;
     const uint64_t t0 = ptx::globaltimer();
     for (;;) {
+        if (__any_sync(ALL_LANES, *abort_flag != 0)) return false;
 #pragma unroll 1
         for (int i = 0; i < 32; ++i)
-            if (ptx::mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (ptx::globaltimer() - t0 > WAIT_NS) {
+            if (__all_sync(ALL_LANES, ptx::mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(ALL_LANES, ptx::globaltimer() - t0 > WAIT_NS)) {
             *abort_flag = 1;
             return false;
         }
     }
 }
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
-    return ptx::mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag);
+    return __all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity)) || wait_long(bar, parity, abort_flag);
 }
 __device__ __forceinline__ uint4 lds16(uint32_t p) {
     uint4 r;
@@ -927,7 +933,7 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
         *s_abort = 0;
         for (int i = 0; i < stages; ++i) {
             ptx::mbar_init(full(i), 33);      // the copies of 32 lanes, and the count of tokens
-            ptx::mbar_init(empty(i), 1);
+            ptx::mbar_init(empty(i), 1 + a.hold);
         }
         for (int i = 0; i < QS; ++i) {
             ptx::mbar_init(q_full(i), 32);
@@ -973,7 +979,8 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
         bool bad = false;
         int st = 0, turn = 0, qst = 0;          // the next stage, whose it is to fill, the next slot of queries
         unsigned ph = 1, qph = 1;
-        while (more && !*s_abort) {
+        // (a wait that ran out ends this warp's work; another warp's ends at this one's next wait)
+        while (more) {
             const bool last = pos + SPAN >= stop;
             if (last) w.next();
             const int next_pos = last ? w.from() : pos + SPAN, next_stop = last ? w.to() : stop;
@@ -1103,6 +1110,7 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
     const int cw = warp - PW, t = threadIdx.x - 32 * PW;
     int st = cw, qst = 0;                   // this warp's next stage, the next row's queries
     unsigned ph = 0, qph = 0, seq = 0;      // tiles of the CTA so far
+    bool live = true;                       // until a wait ran out: then no tile is there to be read
     // what the end joins: the rows that began before this range, and go on behind it
     SharedRow head = {-1}, tail = {-1};
     M math(lane, ptx::smem_u32(s_p + cw * M::P_BYTES));
@@ -1112,13 +1120,14 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
         math.reset();
         if (tiles) {
             const float scale = (a.kv.k_scale ? a.kv.k_scale[w.hk] : 1.f) * a.scale;
-            wait_bar(q_full(qst), qph, s_abort);
-            math.queries(ptx::smem_u32(s_q + qst * S::Q_BYTES), nh, D, a.softcap > 0.f ? scale : scale * LOG2E);
+            live = live && wait_bar(q_full(qst), qph, s_abort);
+            if (live) math.queries(ptx::smem_u32(s_q + qst * S::Q_BYTES), nh, D, a.softcap > 0.f ? scale : scale * LOG2E);
             // tile n of the CTA is warp n mod CW's, and the ring a multiple of CW
             // long: a stage has one reader for good, which has seen every earlier
             // filling of it, so that the parity it waits for is never ambiguous
-            for (unsigned n = seq + ((unsigned)(cw - (int)(seq % CW) + CW) % CW); n < seq + tiles; n += CW) {
-                wait_bar(full(st), ph, s_abort);
+            for (unsigned n = seq + ((unsigned)(cw - (int)(seq % CW) + CW) % CW); live && n < seq + tiles; n += CW) {
+                live = wait_bar(full(st), ph, s_abort);
+                if (!live) break;
                 const unsigned ok = *(volatile unsigned *)(s_ok + st);
                 const uint32_t kd = ptx::smem_u32(s_ring + (size_t)st * S::STAGE);
                 math.tile(kd, kd + TT * M::ROW, ok, a.softcap, [&] {
@@ -1175,6 +1184,8 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
         }
     }
 
+    // a fetching warp may have ended before the wait that ran out
+    if (!live && lane == 0) atomicOr(a.status, STATUS_TIMEOUT);
     // arrive at the shared rows; the last to arrive joins
     if (head.r < 0 && tail.r < 0) return;
     sync_threads<CW * 32>();

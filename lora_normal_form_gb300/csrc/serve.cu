@@ -230,6 +230,8 @@ scute_status scute_paged_attention(scute_ctx *c, const scute_kv_cache *kv, const
     a.part = c->att_part;
     a.ctr = c->srv_ctr + 1;
     a.status = c->d_status;
+    a.hold = c->inject_attend ? 1 : 0;
+    c->inject_attend = false;
     TimedLaunch tl{c, st};
     CU_TRY(c, tl.begin());
     CU_TRY(c, launch_attend(a, c->num_sms, st));

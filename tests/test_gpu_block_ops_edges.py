@@ -2,6 +2,8 @@
 cache slots that a page number cannot form, joins whose grouping must not depend
 on which CTA comes last, weights rounded to fewer bits, waits that run out.
 Definitions and bounds as in ``test_gpu_block_ops.py``."""
+import time
+
 import numpy as np
 import pytest
 
@@ -10,6 +12,8 @@ from test_gpu_block_ops import DT, PAGES, check_attend, ctx_of, i32, make_cache
 pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
+
+TIMEOUT = 7      # SCUTE_ERR_TIMEOUT
 
 
 @pytest.fixture(scope="module")
@@ -98,3 +102,28 @@ def test_shared_rows_of_unequal_head_chunks_give_the_same_bits(scute, contexts, 
         ctx.paged_attention(cache, q, at, o, lse=s)
     for o, s in zip(outs, lses):
         assert torch.equal(o, out) and torch.equal(s, lse)
+
+
+# ---------------------------------------------------------------- waits
+@pytest.mark.parametrize("kind,D,group", [("bf16", 128, 4), ("bf16", 128, 16), ("fp8", 64, 4), ("fp32", 128, 4), ("bf16", 256, 8)])
+def test_attention_whose_waits_run_out_reports_and_recovers(scute, contexts, kind, D, group):
+    """A launch whose stages are never given back (test hook): the fetching warps'
+    waits and the computing warps' run out together, after 2 s.  The launch ends,
+    the status says so, and the next call on the context is right."""
+    g = np.random.default_rng(D)
+    lens = [120000, 0, 5, 80000] if kind == "fp8" else [30000, 0, 5, 20000]     # beyond every ring
+    cache, tokens = make_cache(scute, g, lens, 2, D, 16, kind, False)
+    q = torch.from_numpy(g.standard_normal((len(lens), 2 * group, D), dtype=np.float32))
+    q = q.cuda().to(DT["fp32" if kind == "fp32" else "bf16"])
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    ctx = ctx_of(contexts, kind)
+    scute.scute_debug_inject(ctx.handle, scute.INJECT_STALL_ATTENTION)
+    t0 = time.time()
+    ctx.paged_attention(cache, q, i32(lens), out, lse=lse)
+    assert ctx.sync_status() == TIMEOUT
+    assert 0.5 < time.time() - t0 < 60.0
+    for _ in range(2):             # the hook was for that launch; counters are back at zero
+        out.fill_(float("nan"))
+        ctx.paged_attention(cache, q, i32(lens), out, lse=lse)
+        assert ctx.sync_status() == 0
+        check_attend(out, lse, q, tokens, kind, group)
