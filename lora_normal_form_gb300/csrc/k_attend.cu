@@ -394,9 +394,13 @@ struct MmaMath {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if constexpr (FP8) {
-                        pf[m][nt][k][0] = transpose8(pack_f16(p[2 * k], p[2 * k + 1]));
+                        // a half keeps 11 bits of a weight (and none below 2^-24), two 22
+                        const uint32_t hi = pack_f16(p[2 * k], p[2 * k + 1]);
+                        const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                        pf[m][nt][k][0] = transpose8(hi);
+                        pf[m][nt][k][1] = transpose8(pack_f16(p[2 * k] - back.x, p[2 * k + 1] - back.y));
                     } else {
-                        // bf16 keeps 8 bits of a weight: a second product takes the rest
+                        // bf16 keeps 8 bits of a weight, two parts 16
                         const uint32_t hi = pack_bf16(p[2 * k], p[2 * k + 1]);
                         const float r0 = p[2 * k] - __uint_as_float(hi << 16);
                         const float r1 = p[2 * k + 1] - __uint_as_float(hi & 0xffff0000u);
@@ -424,8 +428,10 @@ struct MmaMath {
                             const uint32_t a0 = halves_lo(ya), a1 = halves_hi(ya);
                             const uint32_t a2 = halves_lo(yb), a3 = halves_hi(yb);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
+                            for (int nt = 0; nt < NT; ++nt) {
                                 mma16816<true>(o[nt][j][2 * i + k], a0, a1, a2, a3, pf[m][nt][0][0], pf[m][nt][1][0]);
+                                mma16816<true>(o[nt][j][2 * i + k], a0, a1, a2, a3, pf[m][nt][0][1], pf[m][nt][1][1]);
+                            }
                         }
                     } else {
                         const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);

@@ -7,7 +7,7 @@ import time
 import numpy as np
 import pytest
 
-from test_gpu_block_ops import DT, PAGES, check_attend, ctx_of, i32, make_cache
+from test_gpu_block_ops import DT, HB, PAGES, U, check_attend, ctx_of, f64, i32, make_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +127,39 @@ def test_attention_whose_waits_run_out_reports_and_recovers(scute, contexts, kin
         ctx.paged_attention(cache, q, i32(lens), out, lse=lse)
         assert ctx.sync_status() == 0
         check_attend(out, lse, q, tokens, kind, group)
+
+
+# ---------------------------------------------------------------- weights
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "fp32"])
+@pytest.mark.parametrize("D,group,page", [(64, 1, 16), (64, 16, 16), (128, 4, 16), (128, 16, 16), (128, 8, 1), (256, 8, 16)])
+def test_attention_keeps_the_bits_of_its_weights(scute, contexts, kind, D, group, page):
+    """Two tokens with values of +1 and -1 and scores s and 0: the output is
+    tanh(s / 2), next to nothing for the s of 2^-11 to 2^-8 here, beside weights
+    of a half each.  Queries and keys have one element that is not zero, so that
+    the scores are exact but for one rounding each.  What is left:
+      * the output's rounding, 2 h |ref| (none in fp32, 2 u |ref|);
+      * a weight: its exponent (below 8) rounded to 2^-22 and hence ln 2 2^-22 of
+        it, the exponential 2^-22, sums and the division 3 u, 2^-20 in all;
+      * with a bf16 cache its two bf16 parts, 2^-17 (2^-9 had it one part; an
+        e4m3 cache's two fp16 parts 2^-22 are inside the 2^-20, one part 2^-12 is not)."""
+    g = np.random.default_rng(D + group)
+    n = 40
+    k, v = torch.zeros(2 if page == 1 else 1, 1, page, D), torch.zeros(2 if page == 1 else 1, 1, page, D)
+    first, second = ((0, 0, 0), (1, 0, 0)) if page == 1 else ((0, 0, 0), (0, 0, 1))
+    k[first][D // 2] = 1.0
+    v[first], v[second] = 1.0, -1.0
+    table = i32(np.tile(np.arange(k.shape[0]), (n, 1)))
+    cache = scute.KvCache(k.to(DT[kind]).cuda(), v.to(DT[kind]).cuda(), table)
+    io = DT["fp32" if kind == "fp32" else "bf16"]
+    q = torch.zeros(n, group, D)
+    s = (2.0 ** g.uniform(-11, -8, (n, group)) * g.choice([-1.0, 1.0], (n, group))).astype(np.float32)
+    q[:, :, D // 2] = torch.from_numpy(s)
+    q = q.to(io).cuda()
+    out, lse = torch.empty_like(q), torch.empty(n, group, device="cuda")
+    ctx = ctx_of(contexts, kind)
+    ctx.paged_attention(cache, q, i32([2] * n), out, lse=lse, scale=1.0)
+    assert ctx.sync_status() == 0
+    ref = np.tanh(f64(q)[:, :, D // 2] / 2)[:, :, None]
+    tol = 2.0 ** -20 + (2.0 ** -17 if kind == "bf16" else 0) + (2 * U if kind == "fp32" else 2 * HB) * np.abs(ref)
+    err = np.abs(f64(out) - ref)
+    assert np.all(err <= tol), float((err / tol).max())
