@@ -59,12 +59,14 @@ class Decoder:
         self.table = torch.full((n, -(-max_len // page_size)), -1, dtype=torch.int32, **dev)
         self.free = torch.arange(pages, dtype=torch.int32, **dev)
         self.free_count = torch.full((1,), pages, dtype=torch.int32, **dev)
-        self.slots, self.positions = whole(n), whole(n)
+        self.slots, self.positions = whole(n), whole(n)              # of the step's rows, packed
+        self.row_slots, self.row_positions = whole(n), whole(n)      # of the requests
+        self.none, self.start = whole(n) - 1, whole(n)
         self.caches = [scute.KvCache(new(pages, kv_heads, page_size, dim), new(pages, kv_heads, page_size, dim), self.table)
                        for _ in range(layers)]
         self.cos_sin = torch.empty(max_len, dim, **dev)
         ctx.rope_table(self.cos_sin, theta)
-        self.rope = scute.Rope(self.cos_sin, self.positions)
+        self.rope = scute.Rope(self.cos_sin, self.row_positions)
         # one step's activations
         self.ids = whole(n)
         self.x, self.h, self.a = new(n, hidden), new(n, hidden), new(n, hidden)
@@ -77,18 +79,24 @@ class Decoder:
         their ``length`` (the others keep theirs, or end where ``want`` is 0) and
         return the final hidden rows, row i for request i.
 
-        All requests take a token here, so that row i is request i's; a step with
-        idle requests gives their rows slot -1 by way of ``cu`` and ``req``."""
+        A request that takes no token (it keeps its length, ends, or is refused
+        for want of pages, which the status word says) gets slot -1: nothing of
+        its row is written to the cache, and its final row means nothing."""
         ctx, io = self.ctx, self.ctx.dtype
         lid = lambda i, p: self.layer_ids[f"{i}.{p}"]  # noqa: E731
         ctx.kv_resize(self.length, self.want, self.table, self.page_size, self.free, self.free_count, self.free_count,
                       self.length, self.cu, self.slots, self.positions, self.req)
+        # the new tokens' rows come packed, request r's (if it has one) at cu[r]; the
+        # step's own rows stay with their requests
+        took, at = self.cu[1:] > self.cu[:-1], self.cu[:-1].clamp(max=len(self.cu) - 2)
+        torch.where(took, self.slots[at], self.none, out=self.row_slots)
+        torch.where(took, self.positions[at], self.start, out=self.row_positions)
         self.h.copy_(self.x)
         ctx.residual_norm(self.h, self.a, pre_w=self.norms[0], eps=self.eps)
         for i in range(self.layers):
             ctx.linear_batch([(self.a, lid(i, "q"), self.q), (self.a, lid(i, "k"), self.k),
                               (self.a, lid(i, "v"), self.v)], self.ids, io)
-            ctx.kv_append(self.caches[i], self.slots, self.k, self.v, q=self.q, q_out=self.qr, rope=self.rope)
+            ctx.kv_append(self.caches[i], self.row_slots, self.k, self.v, q=self.q, q_out=self.qr, rope=self.rope)
             ctx.paged_attention(self.caches[i], self.qr, self.length, self.att)
             ctx.linear(self.att, self.ids, lid(i, "o"), self.out, io)
             ctx.residual_norm(self.out, self.a, residual=self.h, residual_out=self.h, pre_w=self.norms[2 * i + 1],
