@@ -5,14 +5,18 @@
 // outputs o; two such triples join as m = max(m1, m2), l = l1 e^(m1 - m) + l2
 // e^(m2 - m), o likewise.  Exponents are taken in powers of two.
 //
-// What bounds it: the cache, 2 x tokens x heads x dim elements read once (at most
-// 16 operations a byte).  Measured on a GB300 whose copy rate is 6775 GB/s, 32
-// query heads on 8 key/value heads of 128 (device time of a graph's launch):
+// What bounds it: the cache, 2 x tokens x heads x dim elements read once, and for
+// each byte 2 x group / element size operations (4 with 4 bf16 heads to a key, 32
+// with 16 e4m3 ones).  Up to 8 heads to a key and 128 elements to a head that is
+// memory, as measured here; beyond, and in fp32 from 4 heads on, the products, the
+// conversions and the softmax of each (token, head).  On a GB300 whose copy rate is
+// 6775 GB/s, 32 query heads on 8 key/value heads of 128 (device time of a graph's
+// launch):
 //     4 requests of 100003 to 131072 tokens, bf16   278 us, 6830 GB/s
 //     64 requests of 200 to 8192 tokens, bf16        90 us, 6260 GB/s
-//     64 of 500 to 16384, e4m3, 64 query heads       99 us, 6060 GB/s
+//     64 of 500 to 16384, e4m3, 64 query heads      102 us, 5880 GB/s
 //     256 requests of up to 1000 tokens, bf16        40 us, 3690 GB/s (the rows' ends)
-//     1 request of 777 tokens                       9.8 us (the dependent steps: lengths
+//     1 request of 777 tokens                       9.7 us (the dependent steps: lengths
 //         1.7, pages and cache rows 3.3, arrival 1.0, joining and storing 2.1)
 //
 // The work is one sequence of tiles (TT tokens of one request and head row),
@@ -45,10 +49,10 @@ constexpr int ATT_CTAS = 6;               // CTAs of an SM, at most
 constexpr int QS = 2;                     // rows whose queries may be waiting
 constexpr int MAX_STAGES = 32;
 // What a row costs beside its tiles, in tiles: with 1, 256 short requests take
-// 43.0 us and one request 12.2, with 3 40.4 and 9.8, with 6 42.5 and 9.8.
+// 44.2 us and one request 12.2, with 3 40.2 and 9.7, with 6 42.2 and 9.6.
 constexpr int ROW_COST = 3;
 // The least places of a range, so that a small batch is not cut to parts whose
-// joining costs more: one request takes 11.0 us with 2, 9.7 with 4, 11.8 with 8.
+// joining costs more: one request takes 11.1 us with 2, 9.7 with 4, 11.9 with 8.
 constexpr int MIN_TILES = 4;
 constexpr uint64_t WAIT_NS = 2000000000ull;
 
@@ -189,13 +193,23 @@ __device__ __forceinline__ uint32_t place_of(int row, int piece) {
 // lane % 4) takes 16 consecutive bytes of token g's (and g + 8's) key and the
 // query's fragment the same elements; and 16 consecutive bytes of the values of
 // tokens 2c, 2c + 1, 2c + 8, 2c + 9, of which pairs of tokens are interleaved by
-// byte permutes.  The work per byte is small (2 x 8 products for each element,
-// about a tenth of these instructions' rate at full memory bandwidth; the tensor
-// pipe is 13 % busy), so the larger tiles of the asynchronous matrix unit, 128 rows
-// of which one new token fills at most 16, would gain nothing here.  A tile's
-// values are read from shared memory piece by piece, behind the weights: all of
-// them at once beside the keys costs registers (64 requests 91.2 against 89.9 us,
-// e4m3 101.9 against 98.5).
+// byte permutes.  The work per byte is small up to 8 heads (8 products for each
+// element of a key, 2 x 8 for one of a value, whose weights come in two parts: about
+// a tenth of these instructions' rate at full memory bandwidth; the tensor pipe is
+// 13 % busy), so the larger tiles of the asynchronous matrix unit, 128 rows of which
+// one new token fills at most 16, would gain nothing here.  A tile's values are read
+// from shared memory piece by piece, behind the weights: all of them at once beside
+// the keys costs registers (64 requests 91.2 against 89.9 us, e4m3, its weights in
+// one part then, 101.9 against 98.5).
+//
+// Weights.  l sums them in 32 bits.  The second product takes them in two parts of
+// the cache's own width, a number rounded and what that left, each in a product of
+// its own: 16 bits of a weight with bf16 parts, 22 with the e4m3 cache's halves (and
+// down to 2^-24 beside weights up to 2^15).  One part would keep 8 and 11 bits.  It
+// costs nothing where memory bounds (bf16) and little with e4m3: 64 requests 102.2
+// us against 99.1, heads of 64 79.5 against 75.1, 16 heads to a key 105.5 against
+// 98.7.  A third bf16 part brings the outputs no nearer to 64 bits, whose distance
+// is then the products' accumulation (1e-6 of the output before its rounding).
 template <bool FP8, int DC, int NT>
 struct MmaMath {
     using IO = __nv_bfloat16;
@@ -497,13 +511,15 @@ struct MmaMath {
 };
 
 // ---------------------------------------------------------------- 32-bit caches
-// Sums in 32 bits throughout, NH heads at a time (16-bit or three-part products
-// would not keep them).  With one to two heads a key bound by memory (64 requests
-// of one head of 64: 112 us, 6430 GB/s), from eight on by the FMAs and the shared
-// memory that feeds them (32 requests, 8 heads of 128: 210 us, 3460 GB/s).  Scores: lane (g, c) multiplies
-// every fourth 16-byte piece of token g's key, and the four lanes of a token add
-// up.  Outputs: a lane owns DC / 32 neighbouring elements and takes the tile's
-// tokens one after another, their weights from shared memory.
+// Sums in 32 bits throughout, NH heads at a time, on fp32 FMAs (16-bit products
+// would not keep 32 bits; three-part ones on the matrix instructions would, and are
+// not tried).  With one to two heads a key bound by memory (64 requests of one head
+// of 64: 111 us, 6470 GB/s), from eight on by the FMAs and the shared memory that
+// feeds them (32 requests, 8 heads of 128: 213 us, 3410 GB/s; 16 heads read every key
+// twice: 213 us, 1700 GB/s).  Scores: lane (g, c) multiplies every fourth 16-byte
+// piece of token g's key, and the four lanes of a token add up.  Outputs: a lane owns
+// DC / 32 neighbouring elements and takes the tile's tokens one after another, their
+// weights from shared memory.
 template <int DC, int NH>
 struct FmaMath {
     using IO = float;
@@ -966,8 +982,8 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
         constexpr int SPAN = 128;
         const uint64_t policy = ptx::make_policy_evict_first();
         // pages in which a tile of 32 tokens lies at once: one check and one base for
-        // it (e4m3, pages of 32 or 256 tokens: 94.4 us against 98.4 by halves); in
-        // others the check is lost (pages of 16: 106.6 us, by halves 98.7)
+        // it (e4m3, pages of 32 or 256 tokens: 98.6 us against 102.9 by halves); in
+        // others the check is lost (pages of 16: 111.8 us, by halves 107.7)
         const bool whole_tiles = TT <= 16 || a.kv.page_size % TT == 0;
         const long long tok_bytes = a.kv.token_stride * ESZ;
         int hk = w.hk, z = w.z, r = w.r, stop = w.to(), pos = w.from();
@@ -1234,16 +1250,22 @@ cudaError_t launch_shape(const AttendArgs &a, int num_sms, cudaStream_t st) {
 }
 
 // Shapes: (computing warps, fetching warps, CTAs of an SM), each the fastest of those
-// that fit the registers and leave the ring 100 KB or more of an SM.  Few warps in
-// many small CTAs end their rows independently of each other; many heads or long
-// ones take more registers or more products for each byte that is fetched.  Device
-// times in us, 64 requests of up to 8192 tokens (e4m3: to 16384) where not said:
-//     group <= 8, dim <= 128   2,1,4: 90.3, 256 short requests 40.4; 4,2,2: 100.4, 59.6
-//       e4m3, dim <= 64        2,1,6: 74.9, 2,1,5: 78.7, 2,1,4: 87.8; bf16 67.4, -, 61.1
-//     group > 8: 16 heads at a time, each key fetched once: 79.9 (4,2,2); in eights
-//       with the shape above 104.6; 16 with 2,1,4: 135.3
-//       dim <= 64              2,1,4: 69.5, 4,2,2: 89.9
-//     dim > 128                4,2,2: 70.8, 2,2,2: 79.3, 2,1,3: 102.3 (32 requests)
+// measured.  Few warps in many small CTAs end their rows independently of each other;
+// many heads or long ones take more registers or more products for each byte that is
+// fetched.  Not all of them hold their values in the registers that their CTAs leave:
+// per thread, bf16 spills 148 bytes in the shape of 16 heads of 128 and 76 in that of
+// dim > 128, e4m3 256 and 112, and 48 with heads of 64.  Device times in us, 64
+// requests of up to 8192 tokens (e4m3: to 16384) where not said:
+//     group <= 8, dim <= 128   2,1,4: 90.5, 256 short requests 40.2; 4,2,2: 100.3, 59.5
+//                              e4m3 2,1,4: 101.8, 4,2,2: 118.1
+//       dim <= 64              bf16 2,1,4: 62.0, 2,1,5: 63.6
+//                              e4m3 2,1,6: 79.6, 2,1,5: 82.1, 2,1,4: 90.0
+//     group > 8: 16 heads at a time, each key fetched once: 76.4 (4,2,2); in eights
+//       with the shape above 105.2; 16 with 2,1,4: 131.1 (e4m3 105.2, 109.8, 159.9;
+//       40 heads on one key, in eights 55.7 and 58.0 in sixteens)
+//       dim <= 64              2,1,4: 69.7, 4,2,2: 90.6 (e4m3 98.3, 129.9)
+//     dim > 128                4,2,2: 72.0, 2,2,2: 80.1, 2,1,3: 101.5 (32 requests);
+//                              e4m3, 4 heads 138.6, 144.8, 136.3
 template <bool FP8>
 cudaError_t launch_mma(const AttendArgs &a, int num_sms, cudaStream_t st) {
     const int D = a.kv.dim;
@@ -1255,10 +1277,12 @@ cudaError_t launch_mma(const AttendArgs &a, int num_sms, cudaStream_t st) {
     return wide ? launch_shape<MmaMath<FP8, 64, 2>, 64, 2, 1, 4>(a, num_sms, st)
                 : launch_shape<MmaMath<FP8, 64, 1>, 64, 2, 1, FP8 ? 6 : 4>(a, num_sms, st);
 }
-// 32-bit caches, in the same way (group 4, 32 requests):
-//     dim <= 64   2,1,5: 134.0, 2,1,6: 148.4, 2,1,4: 143.4 (64 requests)
-//     dim <= 128  2,1,4: 141.2, 4,2,2: 185.5
-//     dim > 128   2,1,3: 221.4, 4,2,2: 235.3, 2,2,2: 288.7
+// 32-bit caches, in the same way (group 4, 32 requests; 8 heads at a time spill 440
+// bytes with dim > 128, 100 with dim <= 64):
+//     dim <= 64   2,1,5: 133.6, 2,1,6: 149.1, 2,1,4: 145.4 (64 requests)
+//     dim <= 128  2,1,4: 141.6, 4,2,2: 192.3
+//     dim > 128   2,1,3: 220.2, 4,2,2: 235.9, 2,2,2: 285.9 (one head 141.3, 156.4, 149.9;
+//                 eight, where the spills weigh, 495, 540, 435)
 template <int DC, int CW, int PW, int CTAS>
 cudaError_t launch_fma(const AttendArgs &a, int num_sms, cudaStream_t st) {
     if (a.group == 1) return launch_shape<FmaMath<DC, 1>, DC, CW, PW, CTAS>(a, num_sms, st);

@@ -29,10 +29,14 @@ namespace {
 // count that are written in place follow a launch-wide arrival count.
 //
 // Bound by latency: lengths, two scans, a binary search for every row in shared
-// memory, the page, the stores.  64 requests of one new token take 3.5 us (a launch
-// of nothing 1.5), 4096 with their prompts 10.6 (all in one CTA 126).  Every CTA
-// scans all requests for itself, which costs less than a second launch would; 256
-// threads are enough up to 256 requests (3.5 us against 4.4 with 1024).
+// memory, the page, the stores.  64 requests of one new token take 3.6 us (a launch
+// of nothing 1.5), 4096 with their prompts 10.6 to 11.8 by the draw (all in one CTA
+// 126).  Every CTA scans all requests for itself, which costs less than a second
+// launch would; 256 threads are enough up to 256 requests (3.5 us against 4.4 with
+// 1024).  Pages that come back are handed on one to a thread, each with a search and
+// a dependent load, by as many CTAs as the new rows want: 256 requests of 4096 tokens
+// that end in a step of few rows take 143 us in pages of 16, 2.2 ms in pages of one
+// (1.2 us of bytes).
 constexpr int RS_THREADS = 1024;       // at most
 
 // Pages of so many tokens (at most 2^31 - 1 with a page's rounding); page of a position.
@@ -420,8 +424,10 @@ template <> struct Piece<__nv_bfloat16> {
 // multiple of the items or cut to one) keep their item from head to head, so that
 // its cosines and sines are fetched once; heads are taken U at a time, loads first.
 // Bound by memory: 8772 rows of 32 + 2 x 8 heads of 128 with positions of three
-// axes, bf16, take 38.0 us, 5800 GB/s (86 % of the copy rate).  U = 3 or 6, 5 or 6
-// CTAs on an SM and 128 threads for a row are slower.
+// axes, bf16, take 38.0 us, 5800 GB/s (86 % of the copy rate), fp32 67.6 us (95 %),
+// bf16 rows to an e4m3 cache 40.3 us (74 %: fewer bytes, and its divisions).  U = 3 or
+// 6, 5 or 6 CTAs on an SM and 128 threads for a row are slower.  The 64 registers of
+// four CTAs on an SM leave the two bf16 forms 36 bytes of spills.
 template <typename T, typename KV>
 __global__ void __launch_bounds__(256, 4) kv_append_vec_kernel(const AppendArgs a, int per_row) {
     constexpr int VE = Piece<T>::N, U = 2;

@@ -121,7 +121,11 @@ template <> struct Vec<__nv_bfloat16> {
 // with the one it has (rows that fill the registers: after).  FULL: with means taken
 // off or biases.  HELD: a thread keeps its columns' factors from row to row, post_w,
 // the gate and the scale as one; fetched anew for every row they are half of all
-// that passes through L1.
+// that passes through L1.  Rows of more than 16384 elements do not fit the 64
+// registers of 1024 threads (bf16, 4 vectors: 312 bytes of spills, 468 with means or
+// biases; fp32, 8: 740 and 988): 1000 rows of 32768, bf16, reach 0.56 of the copy
+// rate; nor do held factors and biases the 128 of 512 (64 bytes; 4000 layer norms of
+// 8192 0.63).
 template <typename T, int NV, bool WARP, bool FULL, bool HELD, int MOST>
 __global__ void __launch_bounds__(MOST, MOST == 256 || (!HELD && MOST == 512) ? 2 : 1)
     residual_norm_vec_kernel(const NormArgs a) {
