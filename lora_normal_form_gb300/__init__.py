@@ -193,7 +193,7 @@ def _torch():
 
 
 def _check_table(t):
-    if t.dim() != 2 or t.dtype is not _torch().int32 or (t.numel() > 1 and t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2 or t.dtype is not _torch().int32 or (t.stride(1) != 1 and t.shape[1] > 1 and t.numel() > 1):
         raise ValueError("a block table is int32 [n_req, pages] with consecutive rows")
 
 
@@ -305,13 +305,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
+_tensor = None          # torch.Tensor, once one has been given
+
+
 def ptr(x) -> Optional[int]:
     """Address of a torch tensor, numpy array, int or None."""
+    global _tensor
+    if type(x) is _tensor:          # most calls' arguments
+        return x.data_ptr()
     if x is None:
         return None
     if isinstance(x, int):
         return x
     if hasattr(x, "data_ptr"):
+        if type(x) is getattr(sys.modules.get("torch"), "Tensor", None):
+            _tensor = type(x)
         return x.data_ptr()
     if hasattr(x, "ctypes"):
         if not x.flags["C_CONTIGUOUS"]:

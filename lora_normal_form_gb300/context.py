@@ -121,9 +121,9 @@ class Context:
         rows, n_free = slot_map.numel(), free_pages.numel()
         if not (len_in.dtype is len_new.dtype is len_out.dtype is cu_new.dtype is free_in.dtype is free_out.dtype
                 is slot_map.dtype is positions.dtype is token_req.dtype is free_pages.dtype is self._dtypes()[1]
-                and requests >= n and len_in.nbytes == len_new.nbytes == len_out.nbytes == 4 * n
+                and requests >= n and len_new.nbytes == len_out.nbytes == 4 * n
                 and cu_new.nbytes == 4 * n + 4 and free_in.nbytes == free_out.nbytes == 4
-                and slot_map.nbytes == positions.nbytes == token_req.nbytes == 4 * rows and free_pages.nbytes == 4 * n_free
+                and positions.nbytes == token_req.nbytes == 4 * rows
                 and len_in.is_contiguous() and len_new.is_contiguous() and len_out.is_contiguous()
                 and cu_new.is_contiguous() and slot_map.is_contiguous() and positions.is_contiguous()
                 and token_req.is_contiguous() and free_pages.is_contiguous()):
