@@ -317,7 +317,8 @@ scute_status scute_index_tokens_noalloc(const int8_t *method_of_adapter, int32_t
  * length beyond the block table, a page outside the pool, too few free pages)
  * never reads or writes out of range and is recorded in the status word:
  * scute_sync_status then returns SCUTE_ERR_PAGES.  Calls on one context must
- * be ordered on the device (they share its workspace). */
+ * be ordered on the device (they share its workspace, 30 MB on 152 SMs, which
+ * scute_create allocates). */
 
 /* Element type of a cache: BF16 or E4M3 (8-bit float, 4 exponent and 3
  * mantissa bits) in a bf16 context, FP32 in an fp32 context. */
