@@ -394,6 +394,79 @@ scute_status scute_kv_resize(scute_ctx *ctx, const int32_t *len_in, const int32_
                              int32_t *free_out, int32_t *len_out, int32_t *cu_new, int32_t *slot_map,
                              int32_t *positions, int32_t *token_req, int64_t max_new, void *stream);
 
+/* Rows of a new block table that continue rows of an old one: several samples of
+ * one prompt, beams, a batch whose ended requests are closed up, tokens given
+ * back.  Row r of the new table takes the first len_new[r] cached tokens of row
+ * source[r] of the old one, or nothing; old rows that no new row continues are
+ * let go.
+ *   - Full pages are shared, not copied: extra[p] is the number of rows that hold
+ *     page p beyond the first one (0 of a page held once, or free).  Each old row's
+ *     pages lose a holder and each new row's full pages gain one.
+ *   - A row's last page, where its tokens fill it only in part, is the row's own:
+ *     when nobody else holds it, it stays with the first new row that ends in it;
+ *     every other such row gets a page from the top of the free list (the ones
+ *     just given up included), in the order of the new rows, whose first
+ *     copy_tokens[r] tokens shall be copied from page copy_from[r] to page
+ *     copy_to[r] (scute_kv_copy, for every layer); other rows have -1, -1 and 0.
+ *     So a new row may take tokens behind its last one (scute_kv_resize) without
+ *     writing to a page that another row reads.
+ *   - Pages that nobody holds any more go on top of the free list, in the order of
+ *     their numbers.
+ *   - When the list is empty, a row that needs a copy ends at its full pages
+ *     instead (len_out says so; SCUTE_ERR_PAGES).
+ * Pages held by something else than the old table's rows (a prompt kept for
+ * requests to come) count in `extra` as one holder more each.  scute_kv_resize
+ * does not read or write `extra`: it may take pages for rows of the new table, and
+ * may take pages back only from rows that share none (a row with shared pages is
+ * let go, or shortened, here).
+ *   table_in, len_in    device int32 [n_in][table_in_stride], [n_in]: only read;
+ *   source, len_new     device int32 [n_out]: a row of table_in or -1, and its
+ *                       tokens (len_new NULL: all).  A source outside -1..n_in - 1
+ *                       counts as -1, a len_new outside 0..len_in[source] as the
+ *                       nearest inside, a len_in outside 0..table_cols * page_size
+ *                       likewise; each is recorded (SCUTE_ERR_PAGES);
+ *   table_out, len_out  device int32 [n_out][table_out_stride], [n_out]; neither
+ *                       may overlap table_in or len_in.  Entries behind a row's
+ *                       pages are left as they were;
+ *   extra               device int32 [n_pages], changed in place.  A page number
+ *                       outside 0..n_pages - 1 is taken over uncounted and
+ *                       recorded, as is a page with more rows than holders;
+ *   free_pages, n_free_max, free_in, free_out   the list as for scute_kv_resize;
+ *                       entries from the new count on keep what they held, and
+ *                       pages beyond n_free_max entries are lost (SCUTE_ERR_PAGES);
+ *   copy_from, copy_to, copy_tokens   device int32 [n_out].
+ * n_in and n_out are 0..SCUTE_MAX_REQUESTS, n_pages 0..2^30, table_cols * page_size
+ * and a table's entries at most 2^31 - 1.  What the step does is fixed by the
+ * arguments alone. */
+typedef struct {
+    const int32_t *table_in, *len_in;
+    int64_t table_in_stride;
+    const int32_t *source, *len_new;
+    int32_t *table_out, *len_out;
+    int64_t table_out_stride;
+    int32_t n_in, n_out, table_cols, page_size, n_pages;
+    int32_t *extra, *free_pages;
+    int64_t n_free_max;
+    const int32_t *free_in;
+    int32_t *free_out, *copy_from, *copy_to, *copy_tokens;
+} scute_fork;
+scute_status scute_kv_fork(scute_ctx *ctx, const scute_fork *f, void *stream);
+
+/* Copy pages of several caches of one shape (the layers' caches of a model): for
+ * each i < n with copy_to[i] >= 0, the first tokens[i] tokens of page copy_from[i]
+ * (tokens NULL: all of the page), keys and values of every head, to page
+ * copy_to[i] of the same pool.
+ *   caches     HOST array [n_caches], 1..SCUTE_MAX_CACHES, of one dtype, size and
+ *              strides;
+ *   copy_from, copy_to, tokens   device int32 [n]; copy_to -1: nothing.  A page
+ *              outside the pool is skipped, a count outside 0..page_size is cut to
+ *              it, and each recorded (SCUTE_ERR_PAGES).  No page may be written
+ *              twice, or read as well as written;
+ *   n          0..2^20. */
+#define SCUTE_MAX_CACHES 1024
+scute_status scute_kv_copy(scute_ctx *ctx, const scute_kv_cache *caches, int n_caches, const int32_t *copy_from,
+                           const int32_t *copy_to, const int32_t *tokens, int64_t n, void *stream);
+
 /* Rotary positions.  Pair i of a head's first rotary_dim elements is turned by
  * the angle whose cosine and sine stand in row p of the table:
  *     (a, b) -> (a cos - b sin, b cos + a sin),
@@ -442,6 +515,30 @@ scute_status scute_kv_append(scute_ctx *ctx, const scute_kv_cache *kv, const int
                              const void *q, int64_t q_stride, int q_heads, void *q_out,
                              int64_t q_out_stride, const scute_rope *rope, void *stream);
 
+/* Norms of every head's queries and keys, in the same pass:
+ * scute_kv_append of x / sqrt(mean(x^2) + eps) * w in place of each head x of q
+ * and of k (with `layer`: of x - mean(x) in place of x), the mean over the head's
+ * head_dim elements.  The norm comes before the turning, values are not normed;
+ * everything between is in 32 bits, rounded once.
+ *   q_w, k_w   device float, or NULL: q's (k's) heads are not normed; at least one
+ *              of them.  Head h's weights are the head_dim floats at h * q_w_stride
+ *              (k_w_stride): 0 for weights that all heads share, or at least
+ *              head_dim;
+ *   eps        >= 0.
+ * rope NULL: no turning, of q as of k (q may then be given).  q NULL: q_w is not
+ * read.  Everything else as for scute_kv_append. */
+typedef struct {
+    const float *q_w, *k_w;
+    int64_t q_w_stride, k_w_stride;
+    float eps;
+    int32_t layer;
+} scute_head_norm;
+scute_status scute_kv_append_norm(scute_ctx *ctx, const scute_kv_cache *kv, const int32_t *slot_map, int64_t n,
+                                  const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                  const void *q, int64_t q_stride, int q_heads, void *q_out,
+                                  int64_t q_out_stride, const scute_rope *rope, const scute_head_norm *norm,
+                                  void *stream);
+
 /* Attention of one new token of each request over its cached tokens:
  *     out[r][h] = sum_t p_t v_t,  p = softmax over t of score(q[r][h] . k_t),
  * over the last kv_len[r] cached tokens (with window > 0: the last
@@ -479,6 +576,13 @@ typedef struct {
 } scute_attention;
 scute_status scute_paged_attention(scute_ctx *ctx, const scute_kv_cache *kv, const scute_attention *a,
                                    void *stream);
+
+/* The same over the first tokens of a context and its last ones: request r's new
+ * token sees the cached tokens t < sinks and t >= kv_len[r] - a->window, each
+ * once, and with a->window = 0 all of them.  The tokens between are not read.
+ * sinks is 0 (scute_paged_attention) .. 2^30; everything else as above. */
+scute_status scute_paged_attention_sinks(scute_ctx *ctx, const scute_kv_cache *kv, const scute_attention *a,
+                                         int32_t sinks, void *stream);
 
 /* The end of a sub-block and the beginning of the next, for n token rows:
  *     h = residual + scale * gate * post(y),   out = pre(h).
@@ -628,7 +732,9 @@ enum {
     SCUTE_KIND_KV_RESIZE = 9,    /* scute_kv_resize                            */
     SCUTE_KIND_KV_APPEND = 10,   /* scute_kv_append                            */
     SCUTE_KIND_ATTENTION = 11,   /* scute_paged_attention                      */
-    SCUTE_KIND_NORM = 12         /* scute_residual_norm                        */
+    SCUTE_KIND_NORM = 12,        /* scute_residual_norm                        */
+    SCUTE_KIND_KV_FORK = 13,     /* scute_kv_fork                              */
+    SCUTE_KIND_KV_COPY = 14      /* scute_kv_copy                              */
 };
 scute_status scute_timing_enable(scute_ctx *ctx, int enable);
 scute_status scute_timing_reset(scute_ctx *ctx);

@@ -115,6 +115,21 @@ class _NormStruct(ctypes.Structure):
                 ("layer", ctypes.c_int32)]
 
 
+class _HeadNormStruct(ctypes.Structure):
+    _fields_ = [("q_w", ctypes.c_void_p), ("k_w", ctypes.c_void_p), ("q_w_stride", ctypes.c_int64),
+                ("k_w_stride", ctypes.c_int64), ("eps", ctypes.c_float), ("layer", ctypes.c_int32)]
+
+
+class _ForkStruct(ctypes.Structure):
+    _fields_ = [("table_in", ctypes.c_void_p), ("len_in", ctypes.c_void_p), ("table_in_stride", ctypes.c_int64),
+                ("source", ctypes.c_void_p), ("len_new", ctypes.c_void_p), ("table_out", ctypes.c_void_p),
+                ("len_out", ctypes.c_void_p), ("table_out_stride", ctypes.c_int64), ("n_in", ctypes.c_int32),
+                ("n_out", ctypes.c_int32), ("table_cols", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("extra", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+                ("n_free_max", ctypes.c_int64), ("free_in", ctypes.c_void_p), ("free_out", ctypes.c_void_p),
+                ("copy_from", ctypes.c_void_p), ("copy_to", ctypes.c_void_p), ("copy_tokens", ctypes.c_void_p)]
+
+
 def _packer(cls):
     """``struct`` form of a structure, whose fields take less time to fill."""
     codes = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f"}
@@ -122,7 +137,7 @@ def _packer(cls):
     return struct.Struct(f"{form}{ctypes.sizeof(cls) - struct.calcsize(form)}x")
 
 
-_ATTENTION, _NORM = _packer(_AttentionStruct), _packer(_NormStruct)
+_ATTENTION, _NORM, _FORK = _packer(_AttentionStruct), _packer(_NormStruct), _packer(_ForkStruct)
 
 
 class KvCache:
@@ -185,6 +200,45 @@ class Rope:
         self.struct = _RopeStruct(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0, axes,
                                   sec, positions.data_ptr(), positions.stride(0) if axes > 1 else 0)
         self.ref = ctypes.byref(self.struct)
+
+
+class KvCaches:
+    """The caches of a model's layers, of one type, size and layout, as
+    ``kv_copy`` takes them (the tensors stay those of the ``KvCache`` objects)."""
+
+    def __init__(self, caches):
+        self.caches = tuple(caches)
+        if not self.caches or not all(isinstance(c, KvCache) for c in self.caches):
+            raise ValueError("KvCaches takes one KvCache or more")
+        self.struct = (_KvCacheStruct * len(self.caches))(*(c.struct for c in self.caches))
+
+
+class HeadNorm:
+    """Norms of every head's queries and keys (scute_head_norm): ``q_w``, ``k_w``
+    device float32 [head_dim], or [heads, head_dim] with weights for each head;
+    None: not normed (one of them at least).  ``layer``: the mean is taken off
+    first."""
+
+    def __init__(self, q_w=None, k_w=None, eps: float = 1e-6, layer: bool = False):
+        if q_w is None and k_w is None:
+            raise ValueError("no weights to norm with")
+        strides = []
+        for w in (q_w, k_w):
+            if w is not None and (w.dtype is not _torch().float32 or w.dim() not in (1, 2) or w.numel() == 0
+                                  or (w.stride(-1) != 1 and w.shape[-1] > 1)
+                                  or (w.dim() == 2 and w.shape[0] > 1 and w.stride(0) < w.shape[1])):
+                raise ValueError("norm weights are float32 [head_dim] or [heads, head_dim] with consecutive rows")
+            # one head's weights are everybody's
+            strides.append(0 if w is None or w.dim() == 1 or w.shape[0] == 1 else w.stride(0))
+        self.tensors = (q_w, k_w)
+        self.struct = _HeadNormStruct(ptr(q_w), ptr(k_w), strides[0], strides[1], eps, 1 if layer else 0)
+        self.ref = ctypes.byref(self.struct)
+
+    def check(self, head_dim: int, q_heads: int, kv_heads: int):
+        for w, heads in zip(self.tensors, (q_heads, kv_heads)):
+            if w is not None and heads and (w.shape[-1] != head_dim or (w.dim() == 2 and w.shape[0] != heads)):
+                raise ValueError(f"norm weights of {heads} heads of {head_dim} are [{head_dim}] or [{heads}, {head_dim}], "
+                                 f"got {tuple(w.shape)}")
 
 
 def _torch():
@@ -270,7 +324,15 @@ _SIGS = {
                                        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
                                        ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p,
                                        ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]),
+    "scute_kv_append_norm": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                            ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                            ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p,
+                                            ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "scute_kv_fork": (ctypes.c_int, [ctypes.c_void_p] * 3),
+    "scute_kv_copy": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
     "scute_paged_attention": (ctypes.c_int, [ctypes.c_void_p] * 4),
+    "scute_paged_attention_sinks": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_int32, ctypes.c_void_p]),
     "scute_residual_norm": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
                                            ctypes.c_void_p]),
     "scute_launch_count": (ctypes.c_int64, [ctypes.c_void_p]),
@@ -476,11 +538,39 @@ def scute_kv_append(ctx, cache: KvCache, slot_map, n, k, k_stride, v, v_stride, 
                                        None if rope is None else rope.ref, _stream_handle(stream)))
 
 
+def scute_kv_append_norm(ctx, cache: KvCache, slot_map, n, k, k_stride, v, v_stride, q=None, q_stride=0, q_heads=0,
+                         q_out=None, q_out_stride=0, rope: Optional[Rope] = None, norm: Optional[HeadNorm] = None,
+                         stream=None):
+    _check(ctx, load().scute_kv_append_norm(ctx, cache.ref, ptr(slot_map), n, ptr(k), k_stride, ptr(v), v_stride,
+                                            ptr(q), q_stride, q_heads, ptr(q_out), q_out_stride,
+                                            None if rope is None else rope.ref, None if norm is None else norm.ref,
+                                            _stream_handle(stream)))
+
+
+def scute_kv_fork(ctx, table_in, len_in, table_in_stride, source, len_new, table_out, len_out, table_out_stride, n_in,
+                  n_out, table_cols, page_size, n_pages, extra, free_pages, n_free_max, free_in, free_out, copy_from,
+                  copy_to, copy_tokens, stream=None):
+    at = lambda x: ptr(x) or 0  # noqa: E731
+    f = _FORK.pack(at(table_in), at(len_in), table_in_stride, at(source), at(len_new), at(table_out), at(len_out),
+                   table_out_stride, n_in, n_out, table_cols, page_size, n_pages, at(extra), at(free_pages), n_free_max,
+                   at(free_in), at(free_out), at(copy_from), at(copy_to), at(copy_tokens))
+    _check(ctx, load().scute_kv_fork(ctx, f, _stream_handle(stream)))
+
+
+def scute_kv_copy(ctx, caches: KvCaches, copy_from, copy_to, tokens, n, stream=None):
+    _check(ctx, load().scute_kv_copy(ctx, caches.struct, len(caches.caches), ptr(copy_from), ptr(copy_to), ptr(tokens), n,
+                                     _stream_handle(stream)))
+
+
 def scute_paged_attention(ctx, cache: KvCache, q, q_stride, out, out_stride, lse, kv_len, n_req, q_heads,
-                          scale=0.0, softcap=0.0, window=0, stream=None):
+                          scale=0.0, softcap=0.0, window=0, stream=None, sinks=0):
+    """``sinks``: scute_paged_attention_sinks where it is not 0."""
     a = _ATTENTION.pack(ptr(q) or 0, q_stride, ptr(out) or 0, out_stride, ptr(lse) or 0, ptr(kv_len) or 0, n_req,
                         q_heads, scale, softcap, window)
-    _check(ctx, load().scute_paged_attention(ctx, cache.ref, a, _stream_handle(stream)))
+    if sinks:
+        _check(ctx, load().scute_paged_attention_sinks(ctx, cache.ref, a, sinks, _stream_handle(stream)))
+    else:
+        _check(ctx, load().scute_paged_attention(ctx, cache.ref, a, _stream_handle(stream)))
 
 
 def scute_residual_norm(ctx, n, d, y, y_stride, residual=None, residual_stride=0, residual_out=None,
@@ -600,7 +690,7 @@ def scute_timing_read(ctx, max_slots: int = TIMING_SLOTS) -> list:
 
 
 KIND_NAMES = ("step", "index", "rotate", "base_gemm", "lowrank", "vera_shrink", "vera_expand", "oft_pass", "s_pass",
-              "kv_resize", "kv_append", "attention", "norm")
+              "kv_resize", "kv_append", "attention", "norm", "kv_fork", "kv_copy")
 
 
 def scute_timing_kinds(ctx, max_slots: int = TIMING_SLOTS) -> list:

@@ -3,8 +3,8 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (BF16, FP32, METHOD_ID, KvCache, Rope, _check_table, _flat, _rows, _torch, scute_add_layer, scute_create, scute_debug_index, scute_destroy,
-               scute_kv_append, scute_kv_resize, scute_launch_count, scute_linear, scute_linear_batch, scute_linear_batch_host,
+from . import (BF16, FP32, METHOD_ID, HeadNorm, KvCache, KvCaches, Rope, _check_table, _flat, _rows, _torch, scute_add_layer, scute_create, scute_debug_index, scute_destroy,
+               scute_kv_append, scute_kv_append_norm, scute_kv_copy, scute_kv_fork, scute_kv_resize, scute_launch_count, scute_linear, scute_linear_batch, scute_linear_batch_host,
                scute_linear_host, scute_paged_attention, scute_predict_batch, scute_predict_bytes,
                scute_register_adapter, scute_residual_norm, scute_rope_table, scute_set_shared, scute_set_variant, scute_sync_status,
                scute_timing_enable,
@@ -144,9 +144,11 @@ class Context:
             raise ValueError("inv_freq is consecutive float64, one for each pair")
         scute_rope_table(self.handle, cos_sin, cos_sin.shape[0], cos_sin.shape[1], theta, inv_freq, stream)
 
-    def kv_append(self, cache: KvCache, slot_map, k, v, q=None, q_out=None, rope: Rope = None, stream=None):
+    def kv_append(self, cache: KvCache, slot_map, k, v, q=None, q_out=None, rope: Rope = None, stream=None,
+                  norm: HeadNorm = None):
         """Write k and v [n, kv_heads, dim] (or [n, kv_heads * dim]) into the cache;
-        keys, and queries into ``q_out``, turned by ``rope``."""
+        keys, and queries into ``q_out``, turned by ``rope``; their heads normed
+        first with ``norm``."""
         n, row, (io, int32, _) = slot_map.shape[0], cache.kv_row, self._dtypes()
         _flat(int32, n, slot_map)
         q_heads = q_stride = q_out_stride = 0
@@ -158,13 +160,49 @@ class Context:
             q_stride, q_out_stride = _rows(q, n, q_row, io), _rows(q_out, n, q_row, io)
         if rope is not None and rope.n < n:
             raise ValueError("fewer positions than rows")
-        scute_kv_append(self.handle, cache, slot_map, n, k, _rows(k, n, row, io), v, _rows(v, n, row, io), q, q_stride,
-                        q_heads, q_out, q_out_stride, rope, stream)
+        if norm is None:
+            scute_kv_append(self.handle, cache, slot_map, n, k, _rows(k, n, row, io), v, _rows(v, n, row, io), q, q_stride,
+                            q_heads, q_out, q_out_stride, rope, stream)
+        else:
+            norm.check(cache.head_dim, q_heads, cache.kv_heads)
+            scute_kv_append_norm(self.handle, cache, slot_map, n, k, _rows(k, n, row, io), v, _rows(v, n, row, io), q,
+                                 q_stride, q_heads, q_out, q_out_stride, rope, norm, stream)
+
+    def kv_fork(self, table_in, len_in, source, table_out, len_out, page_size: int, extra, free_pages, free_in, free_out,
+                copy_from, copy_to, copy_tokens, len_new=None, stream=None):
+        """Row r of ``table_out`` takes the first ``len_new[r]`` tokens (None: all) of row
+        ``source[r]`` (-1: nothing) of ``table_in``: full pages shared, a last page in
+        part the row's own (device int32 tensors; scute.h has the rules).  What is to
+        be copied for that, ``kv_copy`` copies."""
+        for t in (table_in, table_out):
+            _check_table(t)
+        int32, n_in, n_out = self._dtypes()[1], len_in.numel(), source.numel()
+        cols, pitch = table_in.shape[1], []
+        for t, n in ((table_in, n_in), (table_out, n_out)):
+            pitch.append(t.stride(0) if t.shape[0] > 1 else max(cols, t.stride(0)))
+            if t.shape[0] < n or t.shape[1] != cols or pitch[-1] < cols:
+                raise ValueError("kv_fork takes two block tables of as many columns, a row of its own for each request")
+        _flat(int32, n_in, len_in)
+        _flat(int32, n_out, source, len_new, len_out, copy_from, copy_to, copy_tokens)
+        _flat(int32, 1, free_in, free_out)
+        _flat(int32, extra.numel(), extra)
+        _flat(int32, free_pages.numel(), free_pages)
+        scute_kv_fork(self.handle, table_in, len_in, pitch[0], source, len_new, table_out, len_out, pitch[1], n_in, n_out,
+                      cols, page_size, extra.numel(), extra, free_pages, free_pages.numel(), free_in, free_out, copy_from,
+                      copy_to, copy_tokens, stream)
+
+    def kv_copy(self, caches: KvCaches, copy_from, copy_to, copy_tokens=None, stream=None):
+        """The first ``copy_tokens[i]`` tokens (None: all) of page ``copy_from[i]`` to page
+        ``copy_to[i]`` (-1: nothing) in every one of the caches."""
+        n = copy_to.numel()
+        _flat(self._dtypes()[1], n, copy_from, copy_to, copy_tokens)
+        scute_kv_copy(self.handle, caches, copy_from, copy_to, copy_tokens, n, stream)
 
     def paged_attention(self, cache: KvCache, q, kv_len, out, scale: float = 0.0, softcap: float = 0.0,
-                        window: int = 0, lse=None, stream=None):
+                        window: int = 0, lse=None, stream=None, sinks: int = 0):
         """One new token of each request over its cached tokens: q and out
-        [n_req, q_heads, dim] (or [n_req, q_heads * dim])."""
+        [n_req, q_heads, dim] (or [n_req, q_heads * dim]).  ``window``: the last that
+        many of them, and the first ``sinks``."""
         n, dim, (io, int32, float32) = kv_len.shape[0], cache.head_dim, self._dtypes()
         row = q.numel() // n if n else cache.kv_row
         if row % dim or cache.requests < n:
@@ -172,7 +210,7 @@ class Context:
         _flat(int32, n, kv_len)
         _flat(float32, n * row // dim, lse)
         scute_paged_attention(self.handle, cache, q, _rows(q, n, row, io), out, _rows(out, n, row, io), lse, kv_len, n,
-                              row // dim, scale, softcap, window, stream)
+                              row // dim, scale, softcap, window, stream, sinks)
 
     def residual_norm(self, y, out=None, residual=None, residual_out=None, pre_w=None, pre_b=None, post_w=None,
                       post_b=None, gate=None, scale: float = 1.0, eps: float = 1e-5, layer: bool = False, stream=None):

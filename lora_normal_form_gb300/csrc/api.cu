@@ -199,6 +199,7 @@ scute_status scute_create(scute_ctx **out, int device, scute_dtype dtype, int ma
               dev_malloc((void **)&c->att_part, sizeof(float) * attend_part_floats(c->num_sms)) == cudaSuccess &&
               dev_malloc((void **)&c->srv_ctr, sizeof(int) * (1 + attend_ctrs(c->num_sms))) == cudaSuccess &&
               cudaMemset(c->srv_ctr, 0, sizeof(int) * (1 + attend_ctrs(c->num_sms))) == cudaSuccess &&
+              dev_malloc((void **)&c->fork_ws, sizeof(int) * FORK_WS_INTS) == cudaSuccess &&
               cudaDeviceGetAttribute(&c->smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device) ==
                   cudaSuccess;
     c->step_bn_max = max_tokens <= 64 ? 64 : 128;
@@ -224,7 +225,8 @@ void scute_destroy(scute_ctx *c) {
     void *bufs[] = {c->d_slots, c->d_method, c->d_perm, c->d_aid, c->d_seg_start, c->d_seg_aid, c->d_seg_unit, c->d_seg_tile, c->vs_ctr, c->vs_part,
                     c->d_meta, c->d_status, c->d_err, c->v_part, c->gpart, c->xs, c->U, c->st_x,
                     c->st_out, c->st_ids, c->tmp, c->step_xs, c->step_U, c->step_pre, c->step_part,
-                    c->step_sync, c->step_hx, c->step_hout, c->var_x, c->att_part, c->srv_ctr};
+                    c->step_sync, c->step_hx, c->step_hout, c->var_x, c->att_part, c->srv_ctr,
+                    c->fork_ws};
     for (void *p : bufs)
         if (p) cudaFree(p);
     if (c->ev_made)

@@ -104,6 +104,7 @@ struct scute_ctx {
     size_t var_x_cols = 0;
     float *att_part = nullptr;   // attention: partial sums of rows that several CTAs share
     int *srv_ctr = nullptr;      // arrival counters of the cache and attention kernels (zero between launches)
+    int *fork_ws = nullptr;      // kv_fork: what its steps tell each other (FORK_WS_INTS)
     PFN_encodeTiled encode = nullptr;
     int64_t launches = 0;
     bool timing = false;

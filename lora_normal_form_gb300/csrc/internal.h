@@ -419,6 +419,46 @@ struct AppendArgs {
     int *status;
 };
 cudaError_t launch_kv_append(bool f32, const AppendArgs &a, int num_sms, cudaStream_t st);
+struct HeadNormArgs {
+    const float *q_w, *k_w;                // null: not normed
+    long long q_stride, k_stride;          // floats between heads' weights (0: the same for all)
+    float eps;
+    int layer;
+};
+cudaError_t launch_kv_append_norm(bool f32, const AppendArgs &a, const HeadNormArgs &w, int num_sms, cudaStream_t st);
+
+// ---------------------------------------------------------------- rows that share pages
+struct ForkArgs {
+    const int32_t *table_in, *len_in;
+    long long in_stride;
+    const int32_t *source, *len_new;
+    int32_t *table_out, *len_out;
+    long long out_stride;
+    int n_in, n_out, cols, page_size, n_pages;
+    int page_shift;            // log2 of the page size, or -1
+    int32_t *extra, *free_pages;
+    long long n_free_max;
+    const int32_t *free_in;
+    int32_t *free_out, *copy_from, *copy_to, *copy_tokens;
+    int *ws;                   // FORK_WS_INTS
+    int *status;
+};
+constexpr int FORK_MAX_CTAS = 1024;
+constexpr int FORK_WS_INTS = 16 + FORK_MAX_CTAS + 16384 / 32;   // list count; freed pages of each CTA; rows that copy, by bit
+// launches: how many kernels it took
+cudaError_t launch_kv_fork(const ForkArgs &a, int num_sms, int *launches, cudaStream_t st);
+
+constexpr int COPY_POOLS = 128;    // pools of one launch
+struct PageCopyArgs {
+    void *pool[COPY_POOLS];
+    int pools;
+    int heads, page_size, n_pages, n;
+    int row_bytes;                                       // of one token and head
+    long long page_bytes, token_bytes, head_bytes;       // strides
+    const int32_t *from, *to, *tokens;
+    int *status;
+};
+cudaError_t launch_kv_copy(const PageCopyArgs &a, int num_sms, cudaStream_t st);
 cudaError_t launch_rope_table(float *cos_sin, int n_pos, int rot, double theta, const double *inv_freq,
                               cudaStream_t st);
 
@@ -435,6 +475,7 @@ struct AttendArgs {
     int n_req, q_heads, group;
     float scale, softcap;
     int window;
+    int sinks;                 // first tokens that a window leaves visible
     int page_shift;            // log2 of the page size, or -1
     float *part;               // partial sums of rows that several CTAs share
     int *ctr;                  // arrivals at such a row (zero between launches)

@@ -655,14 +655,21 @@ struct FmaMath {
 // The batch's work list.  Row (request r, key/value head and head chunk) takes
 // ROW_COST places and then one for each of its tiles, an empty request's row one
 // tile all the same; places_at[r] = places of one row of each request before r.
+//
+// Which tokens a request sees: positions first .. len - 1 of a sequence in which the
+// tokens that stay visible before a window stand directly before it, token_of(first,
+// i) the token at position i (a window from token f on, of whose S = min(sinks, f)
+// tokens before stay: first = f - S, and positions below f are tokens 0 .. S - 1).
 __device__ __forceinline__ void seen_of(const AttendArgs &a, int r, int *first, int *len, bool *bad) {
     const int cap = a.kv.table_cols * a.kv.page_size;
     int n = a.kv_len[r];
     *bad = n < 0 || n > cap;
     n = n < 0 ? 0 : n > cap ? cap : n;
     *len = n;
-    *first = a.window > 0 ? max(0, n - a.window) : 0;
+    const int f = a.window > 0 ? max(0, n - a.window) : 0;
+    *first = f - min(f, a.sinks);
 }
+__device__ __forceinline__ int token_of(const AttendArgs &a, int first, int i) { return i - (i < first + a.sinks ? first : 0); }
 __device__ __forceinline__ void plan_places(const AttendArgs &a, int tt, int *places_at, int *warp_sum) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, n = a.n_req, threads = blockDim.x;
     const int per = (n + threads - 1) / threads, r0 = min(n, t * per), r1 = min(n, r0 + per);
@@ -986,18 +993,18 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
         // others the check is lost (pages of 16: 111.8 us, by halves 107.7)
         const bool whole_tiles = TT <= 16 || a.kv.page_size % TT == 0;
         const long long tok_bytes = a.kv.token_stride * ESZ;
-        int hk = w.hk, z = w.z, r = w.r, stop = w.to(), pos = w.from();
+        int hk = w.hk, z = w.z, r = w.r, first = w.first, stop = w.to(), pos = w.from();
         bool opens = true, more = w.more();
-        auto look_up = [&](int of, int from, int until, int *page) {
+        auto look_up = [&](int of, int skip, int from, int until, int *page) {
             const int32_t *table = a.kv.table + of * a.kv.table_stride;
 #pragma unroll
             for (int k = 0; k < SPAN / 32; ++k) {
-                const int i = from + k * 32 + lane;
-                page[k] = i < until ? table[a.page_shift >= 0 ? i >> a.page_shift : i / a.kv.page_size] : -1;
+                const int i = from + k * 32 + lane, token = token_of(a, skip, i);
+                page[k] = i < until ? table[a.page_shift >= 0 ? token >> a.page_shift : token / a.kv.page_size] : -1;
             }
         };
         int page[SPAN / 32];
-        if (more) look_up(r, pos, stop, page);
+        if (more) look_up(r, first, pos, stop, page);
         bool bad = false;
         int st = 0, turn = 0, qst = 0;          // the next stage, whose it is to fill, the next slot of queries
         unsigned ph = 1, qph = 1;
@@ -1008,7 +1015,7 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
             const int next_pos = last ? w.from() : pos + SPAN, next_stop = last ? w.to() : stop;
             int next_page[SPAN / 32];
             if (last) more = w.more();
-            if (more) look_up(w.r, next_pos, next_stop, next_page);
+            if (more) look_up(w.r, w.first, next_pos, next_stop, next_page);
             if (opens && pos < stop) {
                 if (warp == 0) {
                     if (!wait_bar(q_empty(qst), qph, s_abort)) break;
@@ -1033,7 +1040,8 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
                     if (page[k] < 0 || page[k] >= a.kv.n_pages) {
                         bad = true;
                     } else {
-                        const int in = a.page_shift >= 0 ? i & (a.kv.page_size - 1) : i % a.kv.page_size;
+                        const int token = token_of(a, first, i);
+                        const int in = a.page_shift >= 0 ? token & (a.kv.page_size - 1) : token % a.kv.page_size;
                         place = ((long long)page[k] * a.kv.page_stride + (long long)in * a.kv.token_stride) * ESZ;
                     }
                 }
@@ -1115,7 +1123,7 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
             }
             if (gone) break;
             opens = last;
-            r = w.r, hk = w.hk, z = w.z;
+            r = w.r, hk = w.hk, z = w.z, first = w.first;
             pos = next_pos;
             stop = next_stop;
 #pragma unroll

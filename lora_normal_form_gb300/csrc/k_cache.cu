@@ -566,6 +566,302 @@ __global__ void __launch_bounds__(256, 4) kv_append_vec_kernel(const AppendArgs 
     }
 }
 
+// ---------------------------------------------------------------- kv_append with normed heads
+// Each head x of q and k becomes x / sqrt(mean(x^2) + eps) w (of x - mean(x) with
+// `layer`) before it is turned; the statistics are the head's own, so that a head is
+// read once, held in registers, and written once.
+//
+// Any strides and rotary halves: a warp takes a head, a lane its pairs (and the
+// elements behind them) lane, lane + 32, ...
+template <typename T>
+__global__ void __launch_bounds__(256) kv_append_norm_kernel(const AppendArgs a, const HeadNormArgs w) {
+    constexpr int UNITS = 8;                        // of a lane: 256 elements without pairs
+    const int row = blockIdx.x, lane = threadIdx.x & 31, dim = a.kv.dim, half = a.rot / 2;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int slot = a.slot_map[row];
+    const bool in = slot >= 0 && slot < (long long)a.kv.n_pages * a.kv.page_size;
+    if (slot < -1 || (slot >= 0 && !in)) atomicOr(a.status, STATUS_PAGES);
+    const int units = dim - half, heads = a.q_heads + 2 * a.kv.heads;
+    const long long at = in ? (slot / a.kv.page_size) * a.kv.page_stride + (slot % a.kv.page_size) * a.kv.token_stride : 0;
+    for (int h = threadIdx.x >> 5; h < heads; h += blockDim.x >> 5) {
+        const int kind = h < a.q_heads ? 0 : h < a.q_heads + a.kv.heads ? 1 : 2;     // q, k, v
+        const int hk = kind == 0 ? h : kind == 1 ? h - a.q_heads : h - a.q_heads - a.kv.heads;
+        if (kind && !in) continue;
+        const T *src = reinterpret_cast<const T *>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
+                       (long long)row * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + hk * dim;
+        auto first_of = [&](int e) { return e < half ? (a.interleaved ? 2 * e : e) : e + half; };
+        auto second_of = [&](int e) { return a.interleaved ? 2 * e + 1 : e + half; };
+        float x[UNITS], y[UNITS];
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const int e = lane + 32 * u;
+            x[u] = e < units ? to_f(src[first_of(e)]) : 0.f;
+            y[u] = e < half ? to_f(src[second_of(e)]) : 0.f;
+        }
+        const float *weight = kind == 0 ? w.q_w : kind == 1 ? w.k_w : nullptr;
+        if (weight) {
+            weight += hk * (kind == 0 ? w.q_stride : w.k_stride);
+            auto total = [&](float z) {
+#pragma unroll
+                for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+                return z;
+            };
+            if (w.layer) {
+                float sum = 0.f;
+#pragma unroll
+                for (int u = 0; u < UNITS; ++u) sum += x[u] + y[u];
+                const float mean = total(sum) / dim;
+#pragma unroll
+                for (int u = 0; u < UNITS; ++u) {
+                    const int e = lane + 32 * u;
+                    if (e < units) x[u] -= mean;
+                    if (e < half) y[u] -= mean;
+                }
+            }
+            float sum = 0.f;
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) sum += x[u] * x[u] + y[u] * y[u];
+            const float f = 1.f / sqrtf(total(sum) / dim + w.eps);
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) {
+                const int e = lane + 32 * u;
+                if (e < units) x[u] = x[u] * f * weight[first_of(e)];
+                if (e < half) y[u] = y[u] * f * weight[second_of(e)];
+            }
+        }
+        const float *scale = kind == 1 ? a.kv.k_scale : kind == 2 ? a.kv.v_scale : nullptr;
+        const float div = scale ? scale[hk] : 1.f;
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            const int e = lane + 32 * u;
+            if (e >= units) continue;
+            const int e0 = first_of(e), e1 = e < half ? second_of(e) : -1;
+            float x0 = x[u], x1 = y[u];
+            if (kind < 2 && e1 >= 0) {
+                int ax = 0;
+                while (ax < 3 && e >= a.bound[ax]) ++ax;
+                int p = a.positions[ax * a.axis_stride + row];
+                if (p < 0 || p >= a.n_pos) {
+                    atomicOr(a.status, STATUS_PAGES);
+                    p = p < 0 ? 0 : a.n_pos - 1;
+                }
+                const float c = a.cos_sin[(long long)p * a.rot + e], s = a.cos_sin[(long long)p * a.rot + half + e];
+                const float y0 = x0 * c - x1 * s;
+                x1 = x1 * c + x0 * s;
+                x0 = y0;
+            }
+            if (kind == 0) {
+                T *dst = reinterpret_cast<T *>(a.q_out) + (long long)row * a.q_out_stride + hk * dim;
+                dst[e0] = from_f<T>(x0);
+                if (e1 >= 0) dst[e1] = from_f<T>(x1);
+                continue;
+            }
+            if (scale) x0 /= div, x1 /= div;
+            void *pool = kind == 1 ? a.kv.k : a.kv.v;
+            const long long o = at + hk * a.kv.head_stride;
+            if (a.kv.dtype == KV_E4M3) {
+                __nv_fp8_e4m3 *dst = reinterpret_cast<__nv_fp8_e4m3 *>(pool) + o;
+                dst[e0] = __nv_fp8_e4m3(x0);
+                if (e1 >= 0) dst[e1] = __nv_fp8_e4m3(x1);
+            } else {
+                T *dst = reinterpret_cast<T *>(pool) + o;
+                dst[e0] = from_f<T>(x0);
+                if (e1 >= 0) dst[e1] = from_f<T>(x1);
+            }
+        }
+    }
+}
+
+// 16 bytes at a time, items as in kv_append_vec_kernel; a head is `lanes` neighbouring
+// lanes' (a power of two, so that they add up by shuffles), NI items each.  Every lane
+// of a warp goes through the same number of heads.
+template <typename T, typename KV, int NI>
+__global__ void __launch_bounds__(256) kv_append_norm_vec_kernel(const AppendArgs a, const HeadNormArgs w, int per_row,
+                                                                 int lanes) {
+    constexpr int VE = Piece<T>::N, U = 2;
+    constexpr unsigned ALL = 0xffffffffu;
+    const int rows = blockDim.x / per_row, sub = threadIdx.x / per_row, t = threadIdx.x - sub * per_row;
+    const int row = blockIdx.x * rows + sub;
+    if (row >= a.n) return;                             // whole warps: a row has 64 threads or more
+    const int dim = a.kv.dim, half = a.rot / 2;
+    const int joined = a.interleaved ? 0 : half / VE;
+    const int items = dim / VE - joined, heads = a.q_heads + 2 * a.kv.heads;
+    const int stride = per_row / lanes, li = t & (lanes - 1), h_first = t / lanes;
+    int d0[NI], d1[NI];
+    bool here[NI], two[NI], turned[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int item = li + i * lanes;
+        here[i] = item < items;
+        two[i] = item < joined;
+        d0[i] = (two[i] ? item : item + joined) * VE;
+        d1[i] = d0[i] + half;
+        turned[i] = here[i] && (two[i] || (a.interleaved && d0[i] < a.rot));
+    }
+    const T *const q_row = reinterpret_cast<const T *>(a.q) + row * a.q_stride;
+    const T *const k_row = reinterpret_cast<const T *>(a.k) + row * a.k_stride - a.q_heads * dim;
+    const T *const v_row = reinterpret_cast<const T *>(a.v) + row * a.v_stride - (a.q_heads + a.kv.heads) * dim;
+    uint4 x0[U][NI], x1[U][NI];
+    auto load = [&](int from) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int hh = from + u * stride;
+            const T *src = (hh < a.q_heads ? q_row : hh < a.q_heads + a.kv.heads ? k_row : v_row) + hh * dim;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                x0[u][i] = x1[u][i] = make_uint4(0, 0, 0, 0);
+                if (hh >= heads || !here[i]) continue;
+                x0[u][i] = *reinterpret_cast<const uint4 *>(src + d0[i]);
+                if (two[i]) x1[u][i] = *reinterpret_cast<const uint4 *>(src + d1[i]);
+            }
+        }
+    };
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int slot = a.slot_map[row];
+    load(h_first);
+
+    // the items' cosines and sines
+    float c[NI][VE], s[NI][VE];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        if (!turned[i]) continue;
+        const int pairs = two[i] ? VE : VE / 2, p0 = two[i] ? d0[i] : d0[i] / 2;
+        auto axis_of = [&](int e) { return (e >= a.bound[0]) + (e >= a.bound[1]) + (e >= a.bound[2]); };
+        auto row_of = [&](int ax) {
+            int p = a.positions[ax * a.axis_stride + row];
+            if (p < 0 || p >= a.n_pos) {
+                bad = true;
+                p = p < 0 ? 0 : a.n_pos - 1;
+            }
+            return a.cos_sin + (long long)p * a.rot + p0;
+        };
+        const int ax = axis_of(p0);
+        const float *at = row_of(ax);
+        if (pairs % 4 == 0 && a.table16 && ax == axis_of(p0 + pairs - 1)) {
+#pragma unroll
+            for (int e = 0; e < VE; e += 4) {
+                if (e >= pairs) break;
+                const float4 x = *reinterpret_cast<const float4 *>(at + e), y = *reinterpret_cast<const float4 *>(at + half + e);
+                c[i][e] = x.x, c[i][e + 1] = x.y, c[i][e + 2] = x.z, c[i][e + 3] = x.w;
+                s[i][e] = y.x, s[i][e + 1] = y.y, s[i][e + 2] = y.z, s[i][e + 3] = y.w;
+            }
+        } else {
+            int last_ax = ax;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                if (e >= pairs) break;
+                const int next = axis_of(p0 + e);
+                if (next != last_ax) at = row_of(next);
+                last_ax = next;
+                c[i][e] = at[e];
+                s[i][e] = at[half + e];
+            }
+        }
+    }
+    const bool in = slot >= 0 && slot < (long long)a.kv.n_pages * a.kv.page_size;
+    if (bad || slot < -1 || (slot >= 0 && !in)) atomicOr(a.status, STATUS_PAGES);
+    const long long at = in ? (slot / a.kv.page_size) * a.kv.page_stride + (slot % a.kv.page_size) * a.kv.token_stride : 0;
+
+    T *const q_to = reinterpret_cast<T *>(a.q_out) + row * a.q_out_stride;
+    KV *const k_to = reinterpret_cast<KV *>(a.kv.k) + at - a.q_heads * a.kv.head_stride;
+    KV *const v_to = reinterpret_cast<KV *>(a.kv.v) + at - (a.q_heads + a.kv.heads) * a.kv.head_stride;
+    for (int h0 = 0;; h0 += U * stride) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int hh = h0 + h_first + u * stride;
+            const bool is_q = hh < a.q_heads, is_v = hh >= a.q_heads + a.kv.heads;
+            const float *weight = is_q ? w.q_w : is_v ? nullptr : w.k_w;
+            float y0[NI][VE], y1[NI][VE];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                Piece<T>::open(x0[u][i], y0[i]);
+                Piece<T>::open(x1[u][i], y1[i]);
+            }
+            if (__any_sync(ALL, weight != nullptr)) {
+                auto total = [&](float z) {
+                    for (int o = lanes >> 1; o; o >>= 1) z += __shfl_xor_sync(ALL, z, o);
+                    return z;
+                };
+                float mean = 0.f, sum = 0.f;
+                if (w.layer) {
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) mean += y0[i][e] + y1[i][e];
+                    mean = total(mean) / dim;
+                }
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        const float z0 = here[i] ? y0[i][e] - mean : 0.f, z1 = two[i] ? y1[i][e] - mean : 0.f;
+                        sum += z0 * z0 + z1 * z1;
+                    }
+                const float f = 1.f / sqrtf(total(sum) / dim + w.eps);
+                if (weight && hh < heads) {
+                    weight += is_q ? hh * w.q_stride : (hh - a.q_heads) * w.k_stride;
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) {
+                        if (!here[i]) continue;
+#pragma unroll
+                        for (int e = 0; e < VE; e += 4) {
+                            const float4 g = *reinterpret_cast<const float4 *>(weight + d0[i] + e);
+                            y0[i][e] = (y0[i][e] - mean) * f * g.x, y0[i][e + 1] = (y0[i][e + 1] - mean) * f * g.y;
+                            y0[i][e + 2] = (y0[i][e + 2] - mean) * f * g.z, y0[i][e + 3] = (y0[i][e + 3] - mean) * f * g.w;
+                            if (!two[i]) continue;
+                            const float4 k = *reinterpret_cast<const float4 *>(weight + d1[i] + e);
+                            y1[i][e] = (y1[i][e] - mean) * f * k.x, y1[i][e + 1] = (y1[i][e + 1] - mean) * f * k.y;
+                            y1[i][e + 2] = (y1[i][e + 2] - mean) * f * k.z, y1[i][e + 3] = (y1[i][e + 3] - mean) * f * k.w;
+                        }
+                    }
+                }
+            }
+            if (hh >= heads || (!is_q && !in)) continue;
+            const float *scale = is_q ? nullptr : is_v ? a.kv.v_scale : a.kv.k_scale;
+            const float div = scale ? scale[hh - a.q_heads - (is_v ? a.kv.heads : 0)] : 1.f;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                if (!here[i]) continue;
+                if (turned[i] && !is_v) {
+                    if (two[i]) {
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) {
+                            const float z = y0[i][e] * c[i][e] - y1[i][e] * s[i][e];
+                            y1[i][e] = y1[i][e] * c[i][e] + y0[i][e] * s[i][e];
+                            y0[i][e] = z;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < VE / 2; ++e) {
+                            const float z = y0[i][2 * e] * c[i][e] - y0[i][2 * e + 1] * s[i][e];
+                            y0[i][2 * e + 1] = y0[i][2 * e + 1] * c[i][e] + y0[i][2 * e] * s[i][e];
+                            y0[i][2 * e] = z;
+                        }
+                    }
+                }
+                if (is_q) {
+                    T *dst = q_to + hh * dim;
+                    Piece<T>::store(dst + d0[i], y0[i]);
+                    if (two[i]) Piece<T>::store(dst + d1[i], y1[i]);
+                    continue;
+                }
+                if (scale) {
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) y0[i][e] /= div, y1[i][e] /= div;
+                }
+                KV *dst = (is_v ? v_to : k_to) + hh * a.kv.head_stride;
+                Piece<T>::store(dst + d0[i], y0[i]);
+                if (two[i]) Piece<T>::store(dst + d1[i], y1[i]);
+            }
+        }
+        if (h0 + U * stride >= heads) break;
+        load(h0 + U * stride + h_first);
+    }
+}
+
 // Whether a call's rows and rotary halves can be taken 16 bytes at a time.
 template <typename T>
 bool by_pieces(const AppendArgs &a) {
@@ -621,6 +917,23 @@ cudaError_t launch_kv_append(bool f32, const AppendArgs &a, int num_sms, cudaStr
     }
     if (f32) return launch_chained(kv_append_kernel<float>, a.n, 256, 0, st, a);
     return launch_chained(kv_append_kernel<__nv_bfloat16>, a.n, 256, 0, st, a);
+}
+
+cudaError_t launch_kv_append_norm(bool f32, const AppendArgs &a, const HeadNormArgs &w, int num_sms, cudaStream_t st) {
+    const bool weights16 = ((reinterpret_cast<uintptr_t>(w.q_w) | reinterpret_cast<uintptr_t>(w.k_w)) & 15) == 0 &&
+                           (w.q_stride | w.k_stride) % 4 == 0;
+    if (weights16 && (f32 ? by_pieces<float>(a) : by_pieces<__nv_bfloat16>(a))) {
+        const int ve = f32 ? 4 : 8, items = a.kv.dim / ve - (a.interleaved ? 0 : a.rot / 2 / ve);
+        int lanes = 1;
+        while (lanes < items && lanes < 32) lanes *= 2;
+        const int per_row = a.n <= 4 * num_sms ? 256 : 64, rows = 256 / per_row, grid = (a.n + rows - 1) / rows;
+        const auto run = [&](auto kernel) { return launch_chained(kernel, grid, 256, 0, st, a, w, per_row, lanes); };
+        if (f32) return items > 32 ? run(kv_append_norm_vec_kernel<float, float, 2>) : run(kv_append_norm_vec_kernel<float, float, 1>);
+        if (a.kv.dtype == KV_E4M3) return run(kv_append_norm_vec_kernel<__nv_bfloat16, __nv_fp8_e4m3, 1>);
+        return run(kv_append_norm_vec_kernel<__nv_bfloat16, __nv_bfloat16, 1>);
+    }
+    if (f32) return launch_chained(kv_append_norm_kernel<float>, a.n, 256, 0, st, a, w);
+    return launch_chained(kv_append_norm_kernel<__nv_bfloat16>, a.n, 256, 0, st, a, w);
 }
 
 cudaError_t launch_rope_table(float *cos_sin, int n_pos, int rot, double theta, const double *inv_freq,

@@ -1,0 +1,346 @@
+// Rows of a block table that continue rows of another one (kv_fork), and the copy
+// of the pages that they cannot share (kv_copy).
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace scute {
+
+namespace {
+
+// ---------------------------------------------------------------- kv_fork
+// Four steps, each over the whole grid and each needing all of the one before:
+//   count   every page of an old row loses a holder, every full page of a new row
+//           gains one (a page at the same place of the old row and the new row of
+//           one number does neither: most pages of a beam's new row are its old
+//           one's).  Afterwards extra[p] < 0 says that nobody holds page p whole;
+//   claim   a new row whose last page, filled in part, is such a page claims it:
+//           the smallest row's mark stays, r - INT_MAX, below every count;
+//   settle  rows whose claim stayed keep the page, others that end in part get their
+//           bit set (they copy); pages left without holder are counted by ranges;
+//   assign  with L = F + P entries in the list (F old ones, P pages given up, in the
+//           order of their numbers), the n-th copying row takes entry L - 1 - n: an
+//           old entry, or the page of rank L - 1 - n - F, whose own thread finds the
+//           row through the bits; the others of the P are written to the list.
+// No step waits for another's threads, so that the order in which the device works
+// decides nothing.
+constexpr int FK_THREADS = 512;
+constexpr int FK_LIST = 0, FK_FREED = 16, FK_BITS = FK_FREED + FORK_MAX_CTAS;    // the workspace's parts
+constexpr int FK_CLAIM = -(1 << 30);                  // claims are below, counts above
+constexpr int FK_SPAN = 256;                          // table entries that a warp takes at a time
+constexpr int FK_WORDS = 16384 / 32;
+
+__device__ __forceinline__ int page_index(const ForkArgs &a, int pos) {
+    return a.page_shift >= 0 ? pos >> a.page_shift : pos / a.page_size;
+}
+__device__ __forceinline__ int pages_of(const ForkArgs &a, int tokens) { return tokens == 0 ? 0 : page_index(a, tokens - 1) + 1; }
+__device__ __forceinline__ int old_len(const ForkArgs &a, int r, bool *bad) {
+    const int cap = a.cols * a.page_size, n = a.len_in[r];
+    if (n < 0 || n > cap) *bad = true;
+    return n < 0 ? 0 : n > cap ? cap : n;
+}
+// A new row's source (-1: none) and tokens.
+struct NewRow {
+    int source, len;
+};
+__device__ __forceinline__ NewRow new_row(const ForkArgs &a, int r, bool *bad) {
+    int s = a.source[r];
+    if (s < -1 || s >= a.n_in) *bad = true, s = -1;
+    if (s < 0) return {-1, 0};
+    const int have = old_len(a, s, bad);
+    int n = have;
+    if (a.len_new) {
+        n = a.len_new[r];
+        if (n < 0 || n > have) *bad = true;
+        n = n < 0 ? 0 : n > have ? have : n;
+    }
+    return {s, n};
+}
+__device__ __forceinline__ bool in_pool(const ForkArgs &a, int p) { return (unsigned)p < (unsigned)a.n_pages; }
+__device__ __forceinline__ int now(const int *p) { return *(const volatile int *)p; }
+
+__device__ __forceinline__ void fork_count(const ForkArgs &a, int cta, int ctas) {
+    const int lane = threadIdx.x & 31;
+    const int rows = max(a.n_in, a.n_out), spans = (a.cols + FK_SPAN - 1) / FK_SPAN;
+    const long long items = (long long)rows * spans, step = (long long)ctas * (FK_THREADS / 32);
+    bool bad = false;
+    for (long long i = (long long)cta * (FK_THREADS / 32) + (threadIdx.x >> 5); i < items; i += step) {
+        const int r = (int)(i / spans), j0 = (int)(i - (long long)r * spans) * FK_SPAN;
+        int have = 0, full = 0;
+        const int32_t *old = a.table_in, *from = a.table_in;
+        if (r < a.n_in) {
+            have = pages_of(a, old_len(a, r, &bad));
+            old += r * a.in_stride;
+        }
+        if (r < a.n_out) {
+            const NewRow x = new_row(a, r, &bad);
+            full = page_index(a, x.len);
+            from += max(x.source, 0) * a.in_stride;
+        }
+        int32_t *to = a.table_out + r * a.out_stride;
+        int p[FK_SPAN / 32], q[FK_SPAN / 32];
+#pragma unroll
+        for (int k = 0; k < FK_SPAN / 32; ++k) {
+            const int j = j0 + k * 32 + lane;
+            p[k] = j < have ? old[j] : -1;
+            q[k] = j < full ? from[j] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < FK_SPAN / 32; ++k) {
+            const int j = j0 + k * 32 + lane;
+            if (j < full) to[j] = q[k];
+            bad |= (j < have && !in_pool(a, p[k])) || (j < full && !in_pool(a, q[k]));
+            if (j < have && j < full && p[k] == q[k]) continue;
+            if (j < have && in_pool(a, p[k])) atomicSub(a.extra + p[k], 1);
+            if (j < full && in_pool(a, q[k])) atomicAdd(a.extra + q[k], 1);
+        }
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, STATUS_PAGES);
+}
+
+// The page of a new row's last tokens where they do not fill it (-1: none).
+__device__ __forceinline__ int last_page(const ForkArgs &a, int r, NewRow *x) {
+    bool bad = false;                                  // recorded by the first step
+    *x = new_row(a, r, &bad);
+    const int full = page_index(a, x->len);
+    return x->len > full * a.page_size ? a.table_in[x->source * a.in_stride + full] : -1;
+}
+
+__device__ __forceinline__ void fork_claim(const ForkArgs &a, int cta, int ctas) {
+    for (int r = cta * FK_THREADS + threadIdx.x; r < a.n_out; r += ctas * FK_THREADS) {
+        NewRow x;
+        const int p = last_page(a, r, &x);
+        if (in_pool(a, p) && now(a.extra + p) < 0) atomicMin(a.extra + p, r - INT32_MAX);
+    }
+}
+
+// Exclusive prefix sum over the CTA's threads; *total receives the sum.
+__device__ __forceinline__ int cta_exclusive(int x, int *warp_sum, int *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < FK_THREADS / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        all += warp_sum[w];
+    }
+    __syncthreads();
+    *total = all;
+    return before + inc - x;
+}
+
+// A CTA's range of pages.
+__device__ __forceinline__ void range_of(const ForkArgs &a, int cta, int ctas, int *p0, int *p1) {
+    const int each = (a.n_pages + ctas - 1) / ctas;
+    *p0 = (int)min((long long)cta * each, (long long)a.n_pages);
+    *p1 = (int)min((long long)*p0 + each, (long long)a.n_pages);
+}
+
+__device__ __forceinline__ void fork_settle(const ForkArgs &a, int cta, int ctas, int *warp_sum) {
+    bool bad = false;
+    const int n32 = (a.n_out + 31) & ~31;
+    for (int r = cta * FK_THREADS + threadIdx.x; r < n32; r += ctas * FK_THREADS) {
+        bool copies = false;
+        if (r < a.n_out) {
+            NewRow x;
+            const int p = last_page(a, r, &x), full = page_index(a, x.len);
+            const bool in_part = x.len > full * a.page_size;
+            const bool keeps = in_part && (!in_pool(a, p) || now(a.extra + p) == r - INT32_MAX);
+            copies = in_part && !keeps;
+            if (keeps) {
+                a.table_out[r * a.out_stride + full] = p;
+                if (in_pool(a, p)) a.extra[p] = 0;      // another row that asks sees the claim or the holder: not its own
+                else bad = true;
+            }
+            a.len_out[r] = x.len;
+            a.copy_from[r] = copies ? p : -1;
+            a.copy_to[r] = -1;
+            a.copy_tokens[r] = copies ? x.len - full * a.page_size : 0;
+        }
+        const unsigned bits = __ballot_sync(0xffffffffu, copies);
+        if ((threadIdx.x & 31) == 0) a.ws[FK_BITS + r / 32] = (int)bits;
+    }
+    int p0, p1, mine = 0, total;
+    range_of(a, cta, ctas, &p0, &p1);
+#pragma unroll 4
+    for (int p = p0 + threadIdx.x; p < p1; p += FK_THREADS) {
+        const int e = now(a.extra + p);
+        if (e < 0 && e > FK_CLAIM) {
+            ++mine;
+            if (e < -1) bad = true;                     // more rows than holders
+        }
+    }
+    cta_exclusive(mine, warp_sum, &total);
+    if (threadIdx.x == 0) a.ws[FK_FREED + cta] = total;
+    if (cta == 0 && threadIdx.x == 0) {
+        int F = *a.free_in;
+        if (F < 0 || F > a.n_free_max) {
+            bad = true;
+            F = F < 0 ? 0 : (int)a.n_free_max;
+        }
+        a.ws[FK_LIST] = F;
+    }
+    if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0) atomicOr(a.status, STATUS_PAGES);
+}
+
+struct AssignShared {
+    int warp_sum[FK_THREADS / 32];
+    unsigned bits[FK_WORDS];
+    int before[FK_WORDS];          // copying rows before each word's
+};
+__device__ __forceinline__ void fork_assign(const ForkArgs &a, int cta, int ctas, AssignShared &s) {
+    static_assert(FK_WORDS <= FK_THREADS && FORK_MAX_CTAS <= 2 * FK_THREADS, "one word and two ranges of a thread");
+    const int t = threadIdx.x, lane = t & 31, words = (a.n_out + 31) / 32;
+    const unsigned word = t < words ? (unsigned)now(a.ws + FK_BITS + t) : 0u;
+    const int F = now(a.ws + FK_LIST);
+    int copies, P, mine_before, total;
+    s.bits[t] = word;
+    s.before[t] = cta_exclusive(__popc(word), s.warp_sum, &copies);
+    int ahead = 0, all = 0;
+    for (int i = t; i < ctas; i += FK_THREADS) {
+        const int x = now(a.ws + FK_FREED + i);
+        all += x;
+        if (i < cta) ahead += x;
+    }
+    cta_exclusive(all, s.warp_sum, &P);
+    cta_exclusive(ahead, s.warp_sum, &mine_before);
+    const long long L = (long long)F + P, left = max(L - copies, 0ll);
+    bool bad = false;
+
+    auto give = [&](int r, int page) {                  // the copying row r its page
+        const int full = page_index(a, a.len_out[r]);
+        a.table_out[r * a.out_stride + full] = page;
+        a.copy_to[r] = page;
+    };
+    // rows that take an old entry, and rows for which nothing is left
+    for (int r = cta * FK_THREADS + t; r < a.n_out; r += ctas * FK_THREADS) {
+        const unsigned w = s.bits[r >> 5];
+        if (!(w >> (r & 31) & 1)) continue;
+        const int nth = s.before[r >> 5] + __popc(w & ((1u << (r & 31)) - 1));
+        const long long at = L - 1 - nth;
+        if (at < 0) {
+            bad = true;
+            a.len_out[r] = page_index(a, a.len_out[r]) * a.page_size;
+            a.copy_from[r] = -1;
+            a.copy_tokens[r] = 0;
+        } else if (at < F) {
+            give(r, a.free_pages[at]);
+        }
+    }
+    // pages that nobody holds any more
+    int p0, p1, rank = mine_before;
+    range_of(a, cta, ctas, &p0, &p1);
+    for (int base = p0; base < p1; base += FK_THREADS) {
+        const int p = base + t, e = p < p1 ? now(a.extra + p) : 0;
+        const bool gone = e < 0;                        // (the claims are settled)
+        const int k = rank + cta_exclusive(gone, s.warp_sum, &total);
+        rank += total;
+        if (!gone) continue;
+        a.extra[p] = 0;
+        const long long at = (long long)F + k;
+        if (at < left) {
+            if (at < a.n_free_max) a.free_pages[at] = p;
+            else bad = true;
+            continue;
+        }
+        const int nth = (int)(L - 1 - at);
+        int lo = 0, hi = words - 1;                     // the last word with at most nth rows before it
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s.before[mid] <= nth) lo = mid;
+            else hi = mid - 1;
+        }
+        give(lo * 32 + __fns(s.bits[lo], 0, nth - s.before[lo] + 1), p);
+    }
+    if (cta == 0 && t == 0) *a.free_out = (int)min(left, a.n_free_max);
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, STATUS_PAGES);
+}
+
+template <int STEP>
+__global__ void __launch_bounds__(FK_THREADS) fork_step_kernel(const ForkArgs a) {
+    __shared__ AssignShared s;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    if (STEP == 0) fork_count(a, blockIdx.x, gridDim.x);
+    if (STEP == 1) fork_claim(a, blockIdx.x, gridDim.x);
+    if (STEP == 2) fork_settle(a, blockIdx.x, gridDim.x, s.warp_sum);
+    if (STEP == 3) fork_assign(a, blockIdx.x, gridDim.x, s);
+}
+
+// ---------------------------------------------------------------- kv_copy
+// A CTA takes one row's page in one pool, 16 bytes to a thread at a time, in the order
+// in which the page's tokens and heads lie.
+constexpr int CP_THREADS = 256;
+__global__ void __launch_bounds__(CP_THREADS) kv_copy_kernel(const PageCopyArgs a) {
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int i = blockIdx.x, to = a.to[i];
+    if (to == -1) return;
+    const int from = a.from[i];
+    int tokens = a.tokens ? a.tokens[i] : a.page_size;
+    const bool out = (unsigned)from >= (unsigned)a.n_pages || (unsigned)to >= (unsigned)a.n_pages;
+    if ((out || tokens < 0 || tokens > a.page_size) && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, STATUS_PAGES);
+    if (out) return;
+    tokens = tokens < 0 ? 0 : min(tokens, a.page_size);
+    char *pool = static_cast<char *>(a.pool[blockIdx.y]);
+    const char *src = pool + from * a.page_bytes;
+    char *dst = pool + to * a.page_bytes;
+    // rows of one token and head, the inner of the two the one with the smaller stride
+    const bool token_in = a.token_bytes < a.head_bytes;
+    const int pieces = a.row_bytes / 16, inner = token_in ? tokens : a.heads;
+    const long long in_step = token_in ? a.token_bytes : a.head_bytes, out_step = token_in ? a.head_bytes : a.token_bytes;
+    const long long all = (long long)tokens * a.heads * pieces;
+    constexpr int U = 4;
+    for (long long e0 = threadIdx.x; e0 < all; e0 += U * CP_THREADS) {
+        uint4 x[U];
+        long long at[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long e = e0 + u * CP_THREADS;
+            if (e >= all) continue;
+            const long long row = e / pieces, o = row / inner;
+            at[u] = o * out_step + (row - o * inner) * in_step + (e - row * pieces) * 16;
+            x[u] = *reinterpret_cast<const uint4 *>(src + at[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (e0 + u * CP_THREADS < all) *reinterpret_cast<uint4 *>(dst + at[u]) = x[u];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_fork(const ForkArgs &a, int num_sms, int *launches, cudaStream_t st) {
+    const int warps = FK_THREADS / 32;
+    const long long rows = max(a.n_in, a.n_out), items = rows * ((a.cols + FK_SPAN - 1) / FK_SPAN);
+    const int most = min(num_sms, FORK_MAX_CTAS);
+    const int row_grid = max(1, min(most, (a.n_out + FK_THREADS - 1) / FK_THREADS));
+    const int page_grid = max(row_grid, (int)min((long long)most, ((long long)a.n_pages + 4 * FK_THREADS - 1) / (4 * FK_THREADS)));
+    *launches = 4;
+    cudaError_t e = launch_chained(fork_step_kernel<0>, (int)max(1ll, min(4ll * most, (items + warps - 1) / warps)), FK_THREADS, 0, st, a);
+    if (e == cudaSuccess) e = launch_chained(fork_step_kernel<1>, row_grid, FK_THREADS, 0, st, a);
+    if (e == cudaSuccess) e = launch_chained(fork_step_kernel<2>, page_grid, FK_THREADS, 0, st, a);
+    if (e == cudaSuccess) e = launch_chained(fork_step_kernel<3>, page_grid, FK_THREADS, 0, st, a);
+    return e;
+}
+
+cudaError_t launch_kv_copy(const PageCopyArgs &a, int num_sms, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.n, (unsigned)a.pools, 1);
+    cfg.blockDim = dim3(CP_THREADS, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_copy_kernel, a);
+}
+
+}  // namespace scute

@@ -1,6 +1,6 @@
-// Entry points of the decoder block's other operators: the paged cache, the
-// rotary append, attention of one new token and the residual norm.  Arguments
-// are checked here; include/scute.h has the contract.
+// Entry points of the decoder block's other operators: the paged cache and rows
+// that share its pages, the rotary append, attention of one new token and the
+// residual norm.  Arguments are checked here; include/scute.h has the contract.
 #include <cmath>
 
 #include "host.h"
@@ -49,6 +49,142 @@ scute_status check_cache(scute_ctx *c, const scute_kv_cache *kv, KvView *out) {
     out->table_cols = kv->table_cols;
     out->k_scale = kv->k_scale;
     out->v_scale = kv->v_scale;
+    return SCUTE_OK;
+}
+
+// scute_kv_append, and with `norm` scute_kv_append_norm.
+scute_status append(scute_ctx *c, const scute_kv_cache *kv, const int32_t *slot_map, int64_t n, const void *k, int64_t k_stride,
+                    const void *v, int64_t v_stride, const void *q, int64_t q_stride, int q_heads, void *q_out,
+                    int64_t q_out_stride, const scute_rope *rope, const scute_head_norm *norm, void *stream) {
+    AppendArgs a{};
+    scute_status s = check_cache(c, kv, &a.kv);
+    if (s) return s;
+    if (n < 0 || n > (1 << 24)) return fail(c, SCUTE_ERR_ARG, "n out of range");
+    if (q && (q_heads < 1 || q_heads > (1 << 16))) return fail(c, SCUTE_ERR_SHAPE, "q_heads = %d", q_heads);
+    const int64_t kv_row = (int64_t)kv->kv_heads * kv->head_dim, q_row = (int64_t)q_heads * kv->head_dim;
+    if (k_stride < kv_row || v_stride < kv_row || (q && (q_stride < q_row || q_out_stride < q_row)))
+        return fail(c, SCUTE_ERR_SHAPE, "a row stride is below heads * head_dim");
+    if (q && !rope && !norm) return fail(c, SCUTE_ERR_ARG, "q without rotary positions");
+    HeadNormArgs w{};
+    if (norm) {
+        if (!(norm->eps >= 0.f) || !std::isfinite(norm->eps)) return fail(c, SCUTE_ERR_ARG, "bad eps");
+        if (!norm->q_w && !norm->k_w) return fail(c, SCUTE_ERR_ARG, "no weights to norm with");
+        for (int64_t stride : {norm->q_w ? norm->q_w_stride : 0, norm->k_w ? norm->k_w_stride : 0})
+            if (stride != 0 && stride < kv->head_dim)
+                return fail(c, SCUTE_ERR_SHAPE, "norm weights %lld apart", (long long)stride);
+        if (!aligned(norm->q_w, 4) || !aligned(norm->k_w, 4)) return fail(c, SCUTE_ERR_ARG, "weights are not aligned to their elements");
+        w.q_w = q ? norm->q_w : nullptr;
+        w.k_w = norm->k_w;
+        w.q_stride = norm->q_w ? norm->q_w_stride : 0;
+        w.k_stride = norm->k_w ? norm->k_w_stride : 0;
+        w.eps = norm->eps;
+        w.layer = norm->layer != 0;
+    }
+    if (rope) {
+        if (rope->rotary_dim < 2 || rope->rotary_dim % 2 || rope->rotary_dim > kv->head_dim || rope->n_pos < 1 ||
+            rope->n_axes < 1 || rope->n_axes > 4)
+            return fail(c, SCUTE_ERR_SHAPE, "rotary_dim %d, %d positions, %d axes", rope->rotary_dim, rope->n_pos,
+                        rope->n_axes);
+        int sum = 0;
+        for (int i = 0; i < rope->n_axes; ++i) {
+            const int part = rope->n_axes == 1 ? rope->rotary_dim / 2 : rope->section[i];
+            if (part < 0 || part > rope->rotary_dim / 2) return fail(c, SCUTE_ERR_SHAPE, "rotary section %d", part);
+            sum += part;
+            a.bound[i] = sum;
+        }
+        for (int i = rope->n_axes; i < 4; ++i) a.bound[i] = sum;
+        if (sum != rope->rotary_dim / 2)
+            return fail(c, SCUTE_ERR_SHAPE, "rotary sections sum to %d, not %d", sum, rope->rotary_dim / 2);
+        if (rope->axis_stride < 0) return fail(c, SCUTE_ERR_SHAPE, "negative axis stride");
+    }
+    if (n == 0) return SCUTE_OK;
+    if (!slot_map || !k || !v || (q && !q_out) || (rope && (!rope->cos_sin || !rope->positions)))
+        return fail(c, SCUTE_ERR_ARG, "null argument");
+    if (!aligned(k, c->esz) || !aligned(v, c->esz) || !aligned(q, c->esz) || !aligned(q_out, c->esz))
+        return fail(c, SCUTE_ERR_ARG, "an input is not aligned to its elements");
+    DeviceGuard dg(c->device);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    a.slot_map = slot_map;
+    a.n = (int)n;
+    a.k = k;
+    a.v = v;
+    a.q = q;
+    a.q_out = q_out;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_stride = q_stride;
+    a.q_out_stride = q_out_stride;
+    a.q_heads = q ? q_heads : 0;
+    if (rope) {
+        a.rot = rope->rotary_dim;
+        a.interleaved = rope->interleaved != 0;
+        a.n_axes = rope->n_axes;
+        a.n_pos = rope->n_pos;
+        a.cos_sin = rope->cos_sin;
+        a.table16 = aligned(rope->cos_sin, 16) && rope->rotary_dim % 8 == 0;
+        a.positions = rope->positions;
+        a.axis_stride = rope->axis_stride;
+    }
+    a.status = c->d_status;
+    TimedLaunch tl{c, st};
+    CU_TRY(c, tl.begin());
+    CU_TRY(c, norm ? launch_kv_append_norm(c->dtype == SCUTE_FP32, a, w, c->num_sms, st)
+                   : launch_kv_append(c->dtype == SCUTE_FP32, a, c->num_sms, st));
+    count_launch(c, 1);
+    CU_TRY(c, tl.end(SCUTE_KIND_KV_APPEND));
+    return SCUTE_OK;
+}
+
+// scute_paged_attention, and with sinks scute_paged_attention_sinks.
+scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attention *t, int32_t sinks, void *stream) {
+    if (!t) return fail(c, SCUTE_ERR_ARG, "null argument");
+    AttendArgs a{};
+    scute_status s = check_cache(c, kv, &a.kv);
+    if (s) return s;
+    if (t->n_req < 0 || t->n_req > SCUTE_MAX_REQUESTS)
+        return fail(c, SCUTE_ERR_ARG, "n_req = %d outside 0..%d", t->n_req, SCUTE_MAX_REQUESTS);
+    if (t->q_heads < 1 || t->q_heads % kv->kv_heads || t->q_heads > (1 << 16))
+        return fail(c, SCUTE_ERR_SHAPE, "%d query heads on %d key/value heads", t->q_heads, kv->kv_heads);
+    const int64_t row = (int64_t)t->q_heads * kv->head_dim, per16 = 16 / c->esz;
+    if (t->q_stride < row || t->out_stride < row || t->q_stride % per16 || t->out_stride % per16)
+        return fail(c, SCUTE_ERR_SHAPE, "q or out stride is below a row or not a multiple of 16 bytes");
+    if (kv->table_cols < 1 || kv->table_stride < kv->table_cols ||
+        (int64_t)kv->table_cols * kv->page_size > (1 << 30) ||
+        (int64_t)kv->table_cols * kv->page_size * t->n_req > (1ll << 33))
+        return fail(c, SCUTE_ERR_SHAPE, "block table of %d columns, row pitch %lld", kv->table_cols,
+                    (long long)kv->table_stride);
+    if (!std::isfinite(t->scale) || !std::isfinite(t->softcap) || t->softcap < 0.f || t->window < 0)
+        return fail(c, SCUTE_ERR_ARG, "bad scale, softcap or window");
+    if (sinks < 0 || sinks > (1 << 30)) return fail(c, SCUTE_ERR_ARG, "sinks = %d outside 0..2^30", sinks);
+    if (t->n_req == 0) return SCUTE_OK;
+    if (!t->q || !t->out || !t->kv_len || !kv->block_table) return fail(c, SCUTE_ERR_ARG, "null argument");
+    if (!aligned(t->q, 16) || !aligned(t->out, 16)) return fail(c, SCUTE_ERR_ARG, "q and out must be 16-byte aligned");
+    DeviceGuard dg(c->device);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    a.q = t->q;
+    a.out = t->out;
+    a.q_stride = t->q_stride;
+    a.out_stride = t->out_stride;
+    a.lse = t->lse;
+    a.kv_len = t->kv_len;
+    a.n_req = t->n_req;
+    a.q_heads = t->q_heads;
+    a.group = t->q_heads / kv->kv_heads;
+    a.scale = t->scale != 0.f ? t->scale : 1.f / sqrtf((float)kv->head_dim);
+    a.softcap = t->softcap;
+    a.window = t->window;
+    a.sinks = sinks;
+    a.page_shift = shift_of(kv->page_size);
+    a.part = c->att_part;
+    a.ctr = c->srv_ctr + 1;
+    a.status = c->d_status;
+    a.hold = c->inject_attend ? 1 : 0;
+    c->inject_attend = false;
+    TimedLaunch tl{c, st};
+    CU_TRY(c, tl.begin());
+    CU_TRY(c, launch_attend(a, c->num_sms, st));
+    count_launch(c, 1);
+    CU_TRY(c, tl.end(SCUTE_KIND_ATTENTION));
     return SCUTE_OK;
 }
 
@@ -126,118 +262,137 @@ scute_status scute_kv_append(scute_ctx *c, const scute_kv_cache *kv, const int32
                              int64_t k_stride, const void *v, int64_t v_stride, const void *q, int64_t q_stride,
                              int q_heads, void *q_out, int64_t q_out_stride, const scute_rope *rope, void *stream) {
     if (!c) return SCUTE_ERR_ARG;
-    AppendArgs a{};
-    scute_status s = check_cache(c, kv, &a.kv);
-    if (s) return s;
-    if (n < 0 || n > (1 << 24)) return fail(c, SCUTE_ERR_ARG, "n out of range");
-    if (q && (q_heads < 1 || q_heads > (1 << 16))) return fail(c, SCUTE_ERR_SHAPE, "q_heads = %d", q_heads);
-    const int64_t kv_row = (int64_t)kv->kv_heads * kv->head_dim, q_row = (int64_t)q_heads * kv->head_dim;
-    if (k_stride < kv_row || v_stride < kv_row || (q && (q_stride < q_row || q_out_stride < q_row)))
-        return fail(c, SCUTE_ERR_SHAPE, "a row stride is below heads * head_dim");
-    if (q && !rope) return fail(c, SCUTE_ERR_ARG, "q without rotary positions");
-    if (rope) {
-        if (rope->rotary_dim < 2 || rope->rotary_dim % 2 || rope->rotary_dim > kv->head_dim || rope->n_pos < 1 ||
-            rope->n_axes < 1 || rope->n_axes > 4)
-            return fail(c, SCUTE_ERR_SHAPE, "rotary_dim %d, %d positions, %d axes", rope->rotary_dim, rope->n_pos,
-                        rope->n_axes);
-        int sum = 0;
-        for (int i = 0; i < rope->n_axes; ++i) {
-            const int part = rope->n_axes == 1 ? rope->rotary_dim / 2 : rope->section[i];
-            if (part < 0 || part > rope->rotary_dim / 2) return fail(c, SCUTE_ERR_SHAPE, "rotary section %d", part);
-            sum += part;
-            a.bound[i] = sum;
-        }
-        for (int i = rope->n_axes; i < 4; ++i) a.bound[i] = sum;
-        if (sum != rope->rotary_dim / 2)
-            return fail(c, SCUTE_ERR_SHAPE, "rotary sections sum to %d, not %d", sum, rope->rotary_dim / 2);
-        if (rope->axis_stride < 0) return fail(c, SCUTE_ERR_SHAPE, "negative axis stride");
-    }
-    if (n == 0) return SCUTE_OK;
-    if (!slot_map || !k || !v || (q && !q_out) || (rope && (!rope->cos_sin || !rope->positions)))
+    return append(c, kv, slot_map, n, k, k_stride, v, v_stride, q, q_stride, q_heads, q_out, q_out_stride, rope, nullptr, stream);
+}
+
+scute_status scute_kv_append_norm(scute_ctx *c, const scute_kv_cache *kv, const int32_t *slot_map, int64_t n, const void *k,
+                                  int64_t k_stride, const void *v, int64_t v_stride, const void *q, int64_t q_stride,
+                                  int q_heads, void *q_out, int64_t q_out_stride, const scute_rope *rope,
+                                  const scute_head_norm *norm, void *stream) {
+    if (!c) return SCUTE_ERR_ARG;
+    if (!norm) return fail(c, SCUTE_ERR_ARG, "null argument");
+    return append(c, kv, slot_map, n, k, k_stride, v, v_stride, q, q_stride, q_heads, q_out, q_out_stride, rope, norm, stream);
+}
+
+scute_status scute_kv_fork(scute_ctx *c, const scute_fork *f, void *stream) {
+    if (!c) return SCUTE_ERR_ARG;
+    if (!f) return fail(c, SCUTE_ERR_ARG, "null argument");
+    if (f->n_in < 0 || f->n_in > SCUTE_MAX_REQUESTS || f->n_out < 0 || f->n_out > SCUTE_MAX_REQUESTS)
+        return fail(c, SCUTE_ERR_ARG, "%d old rows, %d new ones: outside 0..%d", f->n_in, f->n_out, SCUTE_MAX_REQUESTS);
+    if (f->n_pages < 0 || f->n_pages > (1 << 30) || f->n_free_max < 0 || f->n_free_max > 0x7fffffff)
+        return fail(c, SCUTE_ERR_ARG, "n_pages or n_free_max out of range");
+    if (f->page_size < 1 || f->table_cols < 1 || f->table_in_stride < f->table_cols || f->table_out_stride < f->table_cols)
+        return fail(c, SCUTE_ERR_SHAPE, "pages of %d tokens, %d table columns, row pitches %lld and %lld", f->page_size,
+                    f->table_cols, (long long)f->table_in_stride, (long long)f->table_out_stride);
+    const int64_t rows = f->n_in > f->n_out ? f->n_in : f->n_out;
+    if (rows * f->table_cols > 0x7fffffff || (int64_t)f->table_cols * f->page_size > 0x7fffffff)
+        return fail(c, SCUTE_ERR_SHAPE, "block table beyond 2^31 - 1 entries, or a row beyond 2^31 - 1 tokens");
+    if (!f->free_in || !f->free_out || (f->n_free_max > 0 && !f->free_pages) || (f->n_pages > 0 && !f->extra) ||
+        (f->n_in > 0 && (!f->table_in || !f->len_in)) ||
+        (f->n_out > 0 && (!f->source || !f->table_out || !f->len_out || !f->copy_from || !f->copy_to || !f->copy_tokens)))
         return fail(c, SCUTE_ERR_ARG, "null argument");
-    if (!aligned(k, c->esz) || !aligned(v, c->esz) || !aligned(q, c->esz) || !aligned(q_out, c->esz))
-        return fail(c, SCUTE_ERR_ARG, "an input is not aligned to its elements");
+    if (f->n_in > 0 && f->n_out > 0) {
+        const struct { const int32_t *p; int64_t n; } in[2] = {{f->table_in, (f->n_in - 1) * f->table_in_stride + f->table_cols}, {f->len_in, f->n_in}},
+                                       out[2] = {{f->table_out, (f->n_out - 1) * f->table_out_stride + f->table_cols}, {f->len_out, f->n_out}};
+        for (const auto &x : in)
+            for (const auto &y : out)
+                if (x.p < y.p + y.n && y.p < x.p + x.n) return fail(c, SCUTE_ERR_ARG, "new rows overlap the old ones");
+    }
     DeviceGuard dg(c->device);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    a.slot_map = slot_map;
-    a.n = (int)n;
-    a.k = k;
-    a.v = v;
-    a.q = q;
-    a.q_out = q_out;
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
-    a.q_stride = q_stride;
-    a.q_out_stride = q_out_stride;
-    a.q_heads = q ? q_heads : 0;
-    if (rope) {
-        a.rot = rope->rotary_dim;
-        a.interleaved = rope->interleaved != 0;
-        a.n_axes = rope->n_axes;
-        a.n_pos = rope->n_pos;
-        a.cos_sin = rope->cos_sin;
-        a.table16 = aligned(rope->cos_sin, 16) && rope->rotary_dim % 8 == 0;
-        a.positions = rope->positions;
-        a.axis_stride = rope->axis_stride;
+    ForkArgs a{};
+    a.table_in = f->table_in;
+    a.len_in = f->len_in;
+    a.in_stride = f->table_in_stride;
+    a.source = f->source;
+    a.len_new = f->len_new;
+    a.table_out = f->table_out;
+    a.len_out = f->len_out;
+    a.out_stride = f->table_out_stride;
+    a.n_in = f->n_in;
+    a.n_out = f->n_out;
+    a.cols = f->table_cols;
+    a.page_size = f->page_size;
+    a.page_shift = shift_of(f->page_size);
+    a.n_pages = f->n_pages;
+    a.extra = f->extra;
+    a.free_pages = f->free_pages;
+    a.n_free_max = f->n_free_max;
+    a.free_in = f->free_in;
+    a.free_out = f->free_out;
+    a.copy_from = f->copy_from;
+    a.copy_to = f->copy_to;
+    a.copy_tokens = f->copy_tokens;
+    a.ws = c->fork_ws;
+    a.status = c->d_status;
+    int launches = 0;
+    TimedLaunch tl{c, st};
+    CU_TRY(c, tl.begin());
+    CU_TRY(c, launch_kv_fork(a, c->num_sms, &launches, st));
+    count_launch(c, launches);
+    CU_TRY(c, tl.end(SCUTE_KIND_KV_FORK));
+    return SCUTE_OK;
+}
+
+scute_status scute_kv_copy(scute_ctx *c, const scute_kv_cache *caches, int n_caches, const int32_t *copy_from,
+                           const int32_t *copy_to, const int32_t *tokens, int64_t n, void *stream) {
+    if (!c) return SCUTE_ERR_ARG;
+    if (!caches || n_caches < 1 || n_caches > SCUTE_MAX_CACHES)
+        return fail(c, SCUTE_ERR_ARG, "n_caches = %d outside 1..%d", n_caches, SCUTE_MAX_CACHES);
+    if (n < 0 || n > (1 << 20)) return fail(c, SCUTE_ERR_ARG, "n out of range");
+    KvView one{}, next{};
+    scute_status s = check_cache(c, &caches[0], &one);
+    for (int i = 0; i < n_caches; ++i) {
+        if (s) return s;
+        s = check_cache(c, &caches[i], &next);
+        if (!s && (next.dtype != one.dtype || next.n_pages != one.n_pages || next.page_size != one.page_size ||
+                   next.heads != one.heads || next.dim != one.dim || next.page_stride != one.page_stride ||
+                   next.token_stride != one.token_stride || next.head_stride != one.head_stride))
+            return fail(c, SCUTE_ERR_SHAPE, "cache %d is not of the first one's type, size and strides", i);
     }
+    if (s) return s;
+    if (n == 0) return SCUTE_OK;
+    if (!copy_from || !copy_to) return fail(c, SCUTE_ERR_ARG, "null argument");
+    DeviceGuard dg(c->device);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int esz = kv_esz(one.dtype);
+    PageCopyArgs a{};
+    a.heads = one.heads;
+    a.page_size = one.page_size;
+    a.n_pages = one.n_pages;
+    a.n = (int)n;
+    a.row_bytes = one.dim * esz;
+    a.page_bytes = one.page_stride * esz;
+    a.token_bytes = one.token_stride * esz;
+    a.head_bytes = one.head_stride * esz;
+    a.from = copy_from;
+    a.to = copy_to;
+    a.tokens = tokens;
     a.status = c->d_status;
     TimedLaunch tl{c, st};
     CU_TRY(c, tl.begin());
-    CU_TRY(c, launch_kv_append(c->dtype == SCUTE_FP32, a, c->num_sms, st));
-    count_launch(c, 1);
-    CU_TRY(c, tl.end(SCUTE_KIND_KV_APPEND));
+    for (int first = 0; first < n_caches; first += COPY_POOLS / 2) {
+        a.pools = 0;
+        for (int i = first; i < n_caches && i < first + COPY_POOLS / 2; ++i) {
+            a.pool[a.pools++] = caches[i].k;
+            a.pool[a.pools++] = caches[i].v;
+        }
+        CU_TRY(c, launch_kv_copy(a, c->num_sms, st));
+        count_launch(c, 1);
+    }
+    CU_TRY(c, tl.end(SCUTE_KIND_KV_COPY));
     return SCUTE_OK;
 }
 
 scute_status scute_paged_attention(scute_ctx *c, const scute_kv_cache *kv, const scute_attention *t, void *stream) {
     if (!c) return SCUTE_ERR_ARG;
-    if (!t) return fail(c, SCUTE_ERR_ARG, "null argument");
-    AttendArgs a{};
-    scute_status s = check_cache(c, kv, &a.kv);
-    if (s) return s;
-    if (t->n_req < 0 || t->n_req > SCUTE_MAX_REQUESTS)
-        return fail(c, SCUTE_ERR_ARG, "n_req = %d outside 0..%d", t->n_req, SCUTE_MAX_REQUESTS);
-    if (t->q_heads < 1 || t->q_heads % kv->kv_heads || t->q_heads > (1 << 16))
-        return fail(c, SCUTE_ERR_SHAPE, "%d query heads on %d key/value heads", t->q_heads, kv->kv_heads);
-    const int64_t row = (int64_t)t->q_heads * kv->head_dim, per16 = 16 / c->esz;
-    if (t->q_stride < row || t->out_stride < row || t->q_stride % per16 || t->out_stride % per16)
-        return fail(c, SCUTE_ERR_SHAPE, "q or out stride is below a row or not a multiple of 16 bytes");
-    if (kv->table_cols < 1 || kv->table_stride < kv->table_cols ||
-        (int64_t)kv->table_cols * kv->page_size > (1 << 30) ||
-        (int64_t)kv->table_cols * kv->page_size * t->n_req > (1ll << 33))
-        return fail(c, SCUTE_ERR_SHAPE, "block table of %d columns, row pitch %lld", kv->table_cols,
-                    (long long)kv->table_stride);
-    if (!std::isfinite(t->scale) || !std::isfinite(t->softcap) || t->softcap < 0.f || t->window < 0)
-        return fail(c, SCUTE_ERR_ARG, "bad scale, softcap or window");
-    if (t->n_req == 0) return SCUTE_OK;
-    if (!t->q || !t->out || !t->kv_len || !kv->block_table) return fail(c, SCUTE_ERR_ARG, "null argument");
-    if (!aligned(t->q, 16) || !aligned(t->out, 16)) return fail(c, SCUTE_ERR_ARG, "q and out must be 16-byte aligned");
-    DeviceGuard dg(c->device);
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    a.q = t->q;
-    a.out = t->out;
-    a.q_stride = t->q_stride;
-    a.out_stride = t->out_stride;
-    a.lse = t->lse;
-    a.kv_len = t->kv_len;
-    a.n_req = t->n_req;
-    a.q_heads = t->q_heads;
-    a.group = t->q_heads / kv->kv_heads;
-    a.scale = t->scale != 0.f ? t->scale : 1.f / sqrtf((float)kv->head_dim);
-    a.softcap = t->softcap;
-    a.window = t->window;
-    a.page_shift = shift_of(kv->page_size);
-    a.part = c->att_part;
-    a.ctr = c->srv_ctr + 1;
-    a.status = c->d_status;
-    a.hold = c->inject_attend ? 1 : 0;
-    c->inject_attend = false;
-    TimedLaunch tl{c, st};
-    CU_TRY(c, tl.begin());
-    CU_TRY(c, launch_attend(a, c->num_sms, st));
-    count_launch(c, 1);
-    CU_TRY(c, tl.end(SCUTE_KIND_ATTENTION));
-    return SCUTE_OK;
+    return attend(c, kv, t, 0, stream);
+}
+
+scute_status scute_paged_attention_sinks(scute_ctx *c, const scute_kv_cache *kv, const scute_attention *t, int32_t sinks,
+                                         void *stream) {
+    if (!c) return SCUTE_ERR_ARG;
+    return attend(c, kv, t, sinks, stream);
 }
 
 scute_status scute_residual_norm(scute_ctx *c, const scute_norm *t, int64_t n, int d, void *stream) {

@@ -106,3 +106,82 @@ def residual_norm(y, residual, post, pre, gate, scale, eps, layer):
         t = t * gate
     h = scale * t + (0.0 if residual is None else residual)
     return h, None if pre is None else norm(h, pre[0], pre[1], eps, layer)
+
+
+def seen(length, window=0, sinks=0):
+    """The cached tokens that a request's new token sees."""
+    return [t for t in range(length) if not window or t >= length - window or t < sinks]
+
+
+def head_norm(x, w, eps, layer):
+    """x [rows, heads, dim], each head normed by its own statistics; w [dim] or [heads, dim]."""
+    if layer:
+        x = x - x.mean(-1, keepdims=True)
+    return x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * w
+
+
+def fork(table_in, len_in, source, len_new, table_out, page_size, extra, free, n_free_max=None):
+    """Rows of a new block table that continue rows of an old one.  ``free``: list of
+    free pages, the top last.  Returns a dict (table, len_out, extra, free, copy_from,
+    copy_to, copy_tokens, ok)."""
+    n_in, cols = table_in.shape
+    extra, free, table, ok = [int(x) for x in extra], list(free), table_out.copy(), True
+    n_pages, cap = len(extra), cols * page_size
+    inside = lambda p: 0 <= p < n_pages  # noqa: E731
+    old = []
+    for x in len_in:
+        ok = ok and 0 <= x <= cap
+        old.append(min(max(int(x), 0), cap))
+    rows = []
+    for r, s in enumerate(source):
+        s = int(s)
+        if not -1 <= s < n_in:
+            ok, s = False, -1
+        have = old[s] if s >= 0 else 0
+        want = have if len_new is None or s < 0 else int(len_new[r])
+        ok = ok and 0 <= want <= have
+        rows.append((s, min(max(want, 0), have)))
+    for r in range(n_in):
+        for j in range(ceil_div(old[r], page_size)):
+            if inside(table_in[r, j]):
+                extra[table_in[r, j]] -= 1
+            else:
+                ok = False
+    for r, (s, n) in enumerate(rows):
+        for j in range(n // page_size):
+            table[r, j] = table_in[s, j]
+            if inside(table_in[s, j]):
+                extra[table_in[s, j]] += 1
+            else:
+                ok = False
+    n_out = len(rows)
+    len_out, copies = [n for _, n in rows], []
+    copy_from, copy_to, copy_tokens = ([-1] * n_out, [-1] * n_out, [0] * n_out)
+    held = [e >= 0 for e in extra]
+    claimed = set()
+    for r, (s, n) in enumerate(rows):
+        full, rest = divmod(n, page_size)
+        if not rest:
+            continue
+        p = int(table_in[s, full])
+        if not inside(p):
+            table[r, full], ok = p, False
+        elif not held[p] and p not in claimed:
+            claimed.add(p)
+            table[r, full] = p
+        else:
+            copies.append((r, p, full, rest))
+    for p in range(n_pages):
+        if extra[p] < 0:
+            if p not in claimed:
+                ok = ok and extra[p] == -1
+                free.append(p)
+            extra[p] = 0
+    for r, p, full, rest in copies:
+        if not free:
+            ok, len_out[r] = False, full * page_size
+            continue
+        table[r, full] = copy_to[r] = free.pop()
+        copy_from[r], copy_tokens[r] = p, rest
+    return {"table": table, "len_out": np.array(len_out, np.int64), "extra": np.array(extra, np.int64), "free": free,
+            "copy_from": np.array(copy_from), "copy_to": np.array(copy_to), "copy_tokens": np.array(copy_tokens), "ok": ok}

@@ -1,0 +1,372 @@
+"""Rows that share cache pages (kv_fork, kv_copy), the append with normed heads and
+attention with first tokens that stay visible, on the GPU against their float64
+definitions (``oracle/block_ops.py``).
+
+Tolerances, with u = 2^-24 (half a 32-bit step) and 2^-8 (half a bf16 step, of the value):
+  * fork and copy: whole numbers and bits, equal;
+  * a normed head of D elements: the sum of squares is off by (D + 2) u relative, its
+    root by half that and the division, the root and the mean by 3 u more; the mean
+    of a layer norm by (D + 2) u of the mean of |x|, which the weight and the factor
+    carry on; the turning by 3 u of |a| + |b|; then the output's own rounding;
+  * attention: as in the tests of the one-token attention (``check_attend``).
+"""
+import numpy as np
+import pytest
+
+from oracle import block_ops as OB
+from test_gpu_block_ops import DT, EDGES, PAGES, U, check_attend, ctx_of, f64, i32, make_cache
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def scute(gpu_lib):
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    return gpu_lib
+
+
+@pytest.fixture(scope="module")
+def contexts(scute):
+    c = {k: scute.Context(dtype=k, max_tokens=64, max_adapters=4, max_layers=1) for k in ("bf16", "fp32")}
+    yield c
+    for x in c.values():
+        x.close()
+
+
+# ---------------------------------------------------------------- fork
+class Fork:
+    """A random state of a paged cache whose rows share pages, and a step on it."""
+
+    def __init__(self, g, n_in, n_out, page, cols, spare=None, ends=0.2, wild=False):
+        self.page, self.cols = page, cols
+        cap = cols * page
+        self.len_in = g.integers(0, cap + 1, n_in)
+        self.len_in[g.random(n_in) < 0.2] = 0
+        need = -(-self.len_in // page)
+        spare = int(g.integers(0, n_out + 3)) if spare is None else spare
+        total = int(need.sum()) + spare + 5
+        order, at = g.permutation(total), 0
+        self.table = np.full((n_in, cols), -1, np.int64)
+        self.extra = np.zeros(total, np.int64)
+        for r in range(n_in):
+            k = 0
+            if r and g.random() < 0.6:            # shares the full pages of an earlier row's beginning
+                s = int(g.integers(0, r))
+                k = int(g.integers(0, min(self.len_in[r], self.len_in[s]) // page + 1))
+                self.table[r, :k] = self.table[s, :k]
+                self.extra[self.table[r, :k]] += 1
+            self.table[r, k:need[r]] = order[at:at + need[r] - k]
+            at += need[r] - k
+        for p in order[total - spare - 5:total - spare]:      # pages that others hold, one of them twice
+            self.extra[p] = g.integers(0, 2)
+        self.free = list(order[total - spare:]) if spare else []
+        self.n_pages = total
+        self.source = g.integers(0, n_in, n_out) if n_in else np.full(n_out, -1)
+        if n_in == n_out and g.random() < 0.4:
+            keep = g.random(n_out) < 0.6
+            self.source[keep] = np.arange(n_out)[keep]
+        self.source[g.random(n_out) < ends] = -1
+        have = np.where(self.source >= 0, self.len_in[self.source] if n_in else 0, 0)
+        self.len_new = np.where(g.random(n_out) < 0.5, have, (have * g.random(n_out)).astype(np.int64))
+        if wild:                                   # out of range: clipped, left out, recorded
+            self.source[0], self.len_new[-1] = n_in + 3, 10 ** 6
+            self.len_in[0] = cap + 7
+            self.table[0] = self.table[0].clip(0)
+            self.table[1, 0] = total + 9
+
+    def run(self, ctx, len_new=True, cols_out=None):
+        dev = lambda x: i32(np.asarray(x, np.int64))  # noqa: E731
+        n_out = len(self.source)
+        wide = torch.full((max(n_out, 1), self.cols + 3), -7, dtype=torch.int32, device="cuda")
+        table_out = wide[:, :self.cols]
+        extra, free = dev(self.extra), torch.full((self.n_pages,), -9, dtype=torch.int32, device="cuda")
+        free[:len(self.free)] = dev(self.free)
+        kept = free.clone()
+        count = dev([len(self.free)])
+        out = [torch.full((n_out,), -5, dtype=torch.int32, device="cuda") for _ in range(4)]
+        table_in, len_in = dev(self.table), dev(self.len_in)
+        ctx.kv_fork(table_in, len_in, dev(self.source), table_out, out[0], self.page, extra, free, count, count, *out[1:],
+                    len_new=dev(self.len_new) if len_new else None)
+        status = ctx.sync_status()
+        ref = OB.fork(self.table, self.len_in, self.source, self.len_new if len_new else None,
+                      np.full((n_out, self.cols), -7), self.page, self.extra, self.free)
+        assert status == (0 if ref["ok"] else PAGES)
+        for name, got in zip(("len_out", "copy_from", "copy_to", "copy_tokens"), out):
+            assert np.array_equal(got.cpu().numpy(), ref[name]), name
+        assert np.array_equal(table_out[:n_out].cpu().numpy(), ref["table"])
+        assert torch.all(wide[:, self.cols:] == -7)
+        assert np.array_equal(extra.cpu().numpy(), ref["extra"])
+        n = len(ref["free"])
+        assert int(count) == n and free[:n].cpu().tolist() == ref["free"]
+        assert torch.equal(free[n:], kept[n:])               # above the count the list keeps what it held
+        assert torch.equal(table_in, dev(self.table)) and torch.equal(len_in, dev(self.len_in))
+        return ref, table_out, out, extra, free, count
+
+
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("n_in,n_out,page,cols", [
+    (1, 1, 16, 3), (1, 64, 16, 40), (4, 4, 1, 30), (5, 3, 24, 7), (64, 64, 16, 33), (7, 300, 8, 5), (300, 7, 5, 9),
+    (1030, 1030, 16, 12), (33, 40, 64, 300), (3, 2, 16, 700), (2, 0, 16, 4), (0, 3, 16, 4)])
+def test_fork_rows(scute, contexts, n_in, n_out, page, cols, seed):
+    g = np.random.default_rng([seed, n_in, n_out, page])
+    Fork(g, n_in, n_out, page, cols).run(contexts["bf16"], len_new=seed != 1)
+
+
+@pytest.mark.parametrize("spare", [0, 1, 5])
+def test_fork_when_pages_run_out(scute, contexts, spare):
+    g = np.random.default_rng(spare)
+    f = Fork(g, 20, 60, 16, 6, spare=spare, ends=0.0)
+    ref = f.run(contexts["fp32"])[0]
+    assert not ref["ok"]
+
+
+def test_fork_clips_what_is_out_of_range(scute, contexts):
+    g = np.random.default_rng(9)
+    assert not Fork(g, 6, 9, 16, 5, wild=True).run(contexts["bf16"])[0]["ok"]
+
+
+def test_fork_most_rows(scute, contexts):
+    g = np.random.default_rng(16384)
+    Fork(g, 16384, 16384, 16, 4).run(contexts["bf16"])
+
+
+def test_fork_steps_keep_every_page_once(scute, contexts):
+    """Fifty steps of forks, ends and growth: each page is free, or held by as many rows
+    as its count says, and no row's last page in part is another's."""
+    ctx, g = contexts["bf16"], np.random.default_rng(77)
+    n, page, cols, total = 24, 8, 12, 400
+    whole = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    table, length = [whole(n, cols) - 1, whole(n, cols) - 1], [whole(n), whole(n)]
+    extra, free, count = whole(total), torch.arange(total, dtype=torch.int32, device="cuda"), whole(1) + total
+    cf, ct, cn, cu, rows = whole(n), whole(n), whole(n), whole(n + 1), n * 9
+    for step in range(50):
+        a, b = step % 2, 1 - step % 2
+        have = length[a].cpu().numpy()
+        want = np.minimum(have + g.integers(0, 9, n), cols * page)
+        ctx.kv_resize(length[a], i32(want), table[a], page, free, count, count, length[a], cu, whole(rows), whole(rows), whole(rows))
+        source = g.integers(-1, n, n)
+        cut = np.where(g.random(n) < 0.3, want[source] * g.random(n), want[source]).astype(np.int64)
+        cut[source < 0] = 0
+        ctx.kv_fork(table[a], length[a], i32(source), table[b], length[b], page, extra, free, count, count, cf, ct, cn,
+                    len_new=i32(cut))
+        assert ctx.sync_status() == 0
+        tab, lens, ex = table[b].cpu().numpy(), length[b].cpu().numpy(), extra.cpu().numpy()
+        holders = np.zeros(total, np.int64)
+        for r in range(n):
+            pages = tab[r, :-(-lens[r] // page)]
+            holders[pages] += 1
+            assert len(set(pages)) == len(pages)
+        for r in range(n):
+            if lens[r] % page:
+                assert holders[tab[r, lens[r] // page]] == 1
+        listed = free[:int(count)].cpu().numpy()
+        assert len(set(listed)) == len(listed) and np.all(holders[listed] == 0)
+        assert len(listed) + np.count_nonzero(holders) == total
+        assert np.array_equal(ex, np.maximum(holders - 1, 0)) and np.array_equal(lens, cut)
+
+
+# ---------------------------------------------------------------- copy
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "fp8"])
+@pytest.mark.parametrize("H,D,page,token_major,layers", [(2, 128, 16, False, 1), (3, 80, 24, True, 3), (1, 16, 1, False, 2),
+                                                         (8, 256, 5, False, 65)])
+def test_copy_pages(scute, contexts, kind, H, D, page, token_major, layers):
+    g = np.random.default_rng(H + D)
+    n, pages = 9, 40
+    shape = (pages, page, H, D) if token_major else (pages, H, page, D)
+    tt = {"bf16": torch.int16, "fp32": torch.int32, "fp8": torch.uint8}[kind]
+    draw = lambda: torch.from_numpy(g.integers(0, 100, shape)).to(tt).cuda()  # noqa: E731
+    pools = [(draw(), draw()) for _ in range(layers)]
+    order = g.permutation(pages)
+    src, dst = order[:n].copy(), order[n:2 * n].copy()
+    src[4] = src[5]                                      # two copies of one page
+    tokens = g.integers(0, page + 1, n)
+    dst[2] = -1
+    want = [tuple(x.clone() for x in kv) for kv in pools]
+    for use in (tokens, None):
+        for kv in want:
+            for x in kv:
+                for i in range(n):
+                    t = page if use is None else int(use[i])
+                    if dst[i] >= 0 and token_major:
+                        x[dst[i], :t] = x[src[i], :t]
+                    elif dst[i] >= 0:
+                        x[dst[i], :, :t] = x[src[i], :, :t]
+        caches = scute.KvCaches([scute.KvCache(k.view(DT[kind]), v.view(DT[kind]), token_major=token_major) for k, v in pools])
+        ctx = ctx_of(contexts, kind)
+        ctx.kv_copy(caches, i32(src), i32(dst), None if use is None else i32(use))
+        assert ctx.sync_status() == 0
+        for got, ref in zip(pools, want):
+            assert all(torch.equal(x, y) for x, y in zip(got, ref))
+
+
+def test_copy_leaves_out_what_is_out_of_range(scute, contexts):
+    pool = torch.arange(6 * 4 * 16 * 16, device="cuda").remainder(251).to(torch.bfloat16).view(6, 4, 16, 16)
+    k, v = pool.clone(), pool.clone() + 1
+    ctx = contexts["bf16"]
+    caches = scute.KvCaches([scute.KvCache(k, v)])
+    ctx.kv_copy(caches, i32([0, 6, 2, -1]), i32([1, 3, 6, 4]), i32([16, 16, 16, 16]))
+    assert ctx.sync_status() == PAGES
+    pool[1] = pool[0]
+    assert torch.equal(k, pool) and torch.equal(v[1], v[0]) and torch.equal(v[3:], pool[3:] + 1)
+    ctx.kv_copy(caches, i32([0]), i32([5]), i32([99]))
+    assert ctx.sync_status() == PAGES
+    pool[5] = pool[0]
+    assert torch.equal(k, pool)
+
+
+# ---------------------------------------------------------------- append with normed heads
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "fp8"])
+@pytest.mark.parametrize("H,group,D,rot,interleaved,layer,each,shift,axes", [
+    (8, 4, 128, 128, False, False, False, 0, 1), (2, 1, 128, 64, True, True, True, 0, 1), (1, 7, 80, 80, False, False, True, 0, 1),
+    (2, 3, 96, 48, False, True, False, 0, 3), (3, 2, 256, 256, False, False, False, 0, 1), (1, 2, 256, 256, True, True, False, 0, 1),
+    (2, 2, 64, 30, False, False, False, 0, 2), (1, 5, 16, 2, True, False, True, 0, 1), (2, 4, 128, 128, False, True, True, 1, 1),
+    (2, 2, 256, 0, False, False, False, 0, 1), (1, 1, 256, 0, False, True, False, 1, 1), (4, 8, 128, 128, False, False, False, 0, 1)])
+@pytest.mark.parametrize("n", [1, 37, 700])
+def test_append_normed_heads(scute, contexts, kind, H, group, D, rot, interleaved, layer, each, shift, axes, n):
+    g = np.random.default_rng([H, group, D, rot, n])
+    dt, page, eps = DT["fp32" if kind == "fp32" else "bf16"], 16, 1e-5
+    qh = H * group
+    wide = torch.from_numpy(g.standard_normal((n, (qh + 2 * H) * D + 8), dtype=np.float32) * 2 + 0.3).to(dt).cuda()
+    q, k, v = (wide[:, shift + a * D:shift + b * D] for a, b in ((0, qh), (qh, qh + H), (qh + H, qh + 2 * H)))
+    total = -(-n // page) + 2
+    slots = g.permutation(total * page)[:n]
+    slots[g.random(n) < 0.1] = -1
+    pools = [torch.zeros(total, H, page, D, dtype=dt, device="cuda").to(DT[kind]) for _ in range(2)]
+    ks = vs = None
+    if kind == "fp8":
+        ks, vs = (torch.from_numpy((0.02 + 0.03 * g.random(H)).astype(np.float32)).cuda() for _ in range(2))
+    cache = scute.KvCache(*pools, k_scale=ks, v_scale=vs)
+    weight = lambda h: torch.from_numpy(1 + 0.3 * g.standard_normal((h, D) if each else D, dtype=np.float32)).cuda()  # noqa: E731
+    qw, kw = weight(qh), weight(H)
+    rope = angle = None
+    if rot:
+        pos = g.integers(0, 500, (axes, n))
+        cs = torch.empty(500, rot, device="cuda")
+        ctx_of(contexts, kind).rope_table(cs, 10000.0)
+        pairs = rot // 2
+        sections = [pairs - (axes - 1) * (pairs // 4)] + [pairs // 4] * (axes - 1)
+        rope = scute.Rope(cs, i32(pos if axes > 1 else pos[0]), sections=sections, interleaved=interleaved)
+        angle = pos[np.repeat(np.arange(axes), sections)].T * (10000.0 ** (-np.arange(pairs) / pairs))     # [n, pairs]
+    out = torch.full((n, qh * D), float("nan"), dtype=dt, device="cuda")
+    ctx = ctx_of(contexts, kind)
+    ctx.kv_append(cache, i32(slots), k, v, q=q, q_out=out, rope=rope, norm=scute.HeadNorm(qw, kw, eps=eps, layer=layer))
+    assert ctx.sync_status() == 0
+
+    def ready(x, heads, w):
+        x, w = f64(x).reshape(n, heads, D), f64(w)
+        y = OB.head_norm(x, w, eps, layer)
+        mean = x.mean(-1, keepdims=True) if layer else 0.0
+        f = np.abs(w) / np.sqrt(((x - mean) ** 2).mean(-1, keepdims=True) + eps)
+        # the factor off by (D / 2 + 6) u; a layer norm's mean by (D + 2) u of mean |x|,
+        # which also moves the sum of squares by twice that times mean |x - mean| (0 but for rounding)
+        err = U * (D / 2 + 8) * np.abs(y) + (U * (D + 4) * np.abs(x).mean(-1, keepdims=True) * f if layer else 0.0)
+        if rot:
+            z = np.stack([OB.rope(y[r], angle[r], rot, interleaved) for r in range(n)])
+            part = np.stack([OB.rope(np.abs(y[r]), 0 * angle[r], rot, interleaved) for r in range(n)])
+            pair = (lambda m: m[..., :rot].reshape(n, heads, rot // 2, 2)[..., ::-1].reshape(n, heads, rot)) if interleaved else \
+                   (lambda m: np.concatenate([m[..., rot // 2:rot], m[..., :rot // 2]], -1))
+            other, other_err = pair(part), pair(err)
+            err = err.copy()
+            # the partner's error joins; cosines and sines in 32 bits, two products and a sum
+            err[..., :rot] = err[..., :rot] + other_err + 5 * U * (part[..., :rot] + other)
+            return z, err
+        return y, err
+
+    def close(got, ref, err, half_step):
+        err = err + half_step * 1.001 * np.abs(ref) + half_step * err + 1e-30
+        assert np.all(np.abs(got - ref) <= err), float((np.abs(got - ref) / err).max())
+
+    own = U if kind == "fp32" else 2.0 ** -8
+    zq, eq = ready(q, qh, qw)
+    close(f64(out).reshape(n, qh, D), zq, eq, own)
+    zk, ek = ready(k, H, kw)
+    zv = f64(v).reshape(n, H, D)
+    kept = np.nonzero(slots >= 0)[0]
+    at = slots[kept]
+    gk, gv = (f64(p)[at // page, :, at % page] for p in pools)
+    if kind == "fp8":
+        sk, sv = f64(ks)[None, :, None], f64(vs)[None, :, None]
+        for got, ref, err in ((gk, zk[kept] / sk, ek[kept] / sk), (gv, zv[kept] / sv, 0 * zv[kept])):
+            ref = np.clip(ref, -448, 448)
+            # e4m3: half a step is 2^-4 of the value, or 2^-10 below 2^-6
+            assert np.all(np.abs(got - ref) <= np.maximum(2.0 ** -4 * np.abs(ref), 2.0 ** -10) * 1.001 + err * 1.1 + U * np.abs(ref))
+    else:
+        close(gk, zk[kept], ek[kept], own)
+        assert np.array_equal(gv, zv[kept])
+    rest = np.ones(total * page, bool)
+    rest[at] = False
+    left = np.nonzero(rest)[0]
+    assert not f64(pools[0])[left // page, :, left % page].any() and not f64(pools[1])[left // page, :, left % page].any()
+
+
+def test_append_norms_keys_or_queries_alone_and_in_place(scute, contexts):
+    """q's weights alone leave k as kv_append writes it, and the other way round; q_out may be q."""
+    g = np.random.default_rng(4)
+    ctx, n, H, D = contexts["bf16"], 50, 2, 64
+    draw = lambda h: torch.from_numpy(g.standard_normal((n, h, D), dtype=np.float32)).bfloat16().cuda()  # noqa: E731
+    q, k, v, slots = draw(6), draw(H), draw(H), i32(np.arange(n))
+    cs = torch.empty(99, D, device="cuda")
+    ctx.rope_table(cs, 10000.0)
+    rope = scute.Rope(cs, i32(g.integers(0, 99, n)))
+    w = torch.rand(D, device="cuda") + 0.5
+
+    def run(norm, q=q, out=None, rope=rope):
+        pools = [torch.zeros(4, H, 16, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        out = torch.empty_like(q) if out is None else out
+        ctx.kv_append(scute.KvCache(*pools), slots, k, v, q=q, q_out=out, rope=rope, norm=norm)
+        return out, pools[0], pools[1]
+
+    plain, both = run(None), run(scute.HeadNorm(w, w))
+    only_q, only_k = run(scute.HeadNorm(q_w=w)), run(scute.HeadNorm(k_w=w))
+    assert torch.equal(only_q[0], both[0]) and torch.equal(only_q[1], plain[1])
+    assert torch.equal(only_k[0], plain[0]) and torch.equal(only_k[1], both[1])
+    assert all(torch.equal(x[2], plain[2]) for x in (both, only_q, only_k))
+    mine = q.clone()
+    run(scute.HeadNorm(w, w), q=mine, out=mine)
+    assert torch.equal(mine, both[0])
+    # keys and values alone
+    pools = [torch.zeros(4, H, 16, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ctx.kv_append(scute.KvCache(*pools), slots, k, v, rope=rope, norm=scute.HeadNorm(w, w))
+    assert torch.equal(pools[0], both[1])
+    assert ctx.sync_status() == 0
+
+
+# ---------------------------------------------------------------- first tokens that stay visible
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "fp8"])
+@pytest.mark.parametrize("window,sinks", [(1, 1), (16, 4), (20, 17), (64, 33), (100, 400), (100000, 5), (0, 7), (31, 1)])
+@pytest.mark.parametrize("H,group,D,page,token_major", [(2, 4, 128, 16, False), (1, 3, 80, 24, True), (2, 12, 64, 1, False)])
+def test_attention_window_and_first_tokens(scute, contexts, kind, window, sinks, H, group, D, page, token_major):
+    g = np.random.default_rng([window, sinks, D])
+    cache, tokens = make_cache(scute, g, EDGES, H, D, page, kind, token_major, scales=kind == "fp8")
+    q = torch.from_numpy(g.standard_normal((len(EDGES), H * group, D), dtype=np.float32) * 1.5)
+    q = q.cuda().to(DT["fp32" if kind == "fp32" else "bf16"])
+    out, lse = torch.full_like(q, float("nan")), torch.empty(q.shape[:2], device="cuda")
+    ctx = ctx_of(contexts, kind)
+    for _ in range(2):
+        ctx.paged_attention(cache, q, i32(EDGES), out, lse=lse, window=window, sinks=sinks)
+        assert ctx.sync_status() == 0
+        kept = [[x[OB.seen(len(x), window, sinks)] for x in kv] for kv in tokens]
+        check_attend(out, lse, q, kept, kind, group)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "fp8"])
+def test_attention_between_first_tokens_and_window_nothing_is_read(scute, contexts, kind):
+    """Long requests whose middle holds no numbers, split over the GPU, capped scores."""
+    g = np.random.default_rng(8)
+    lens, window, sinks = [9000, 40, 2047, 5000, 0, 1030], 1000, 20
+    cache, tokens = make_cache(scute, g, lens, 2, 64, 16, kind, False)
+    k, v, table = cache.tensors[:3]
+    tab = table.cpu().numpy()
+    for r, n in enumerate(lens):
+        gone = tab[r, -(-sinks // 16):max(0, n - window) // 16]
+        for x in (k, v):
+            (x.view(torch.uint8) if kind == "fp8" else x)[torch.from_numpy(gone.astype(np.int64)).cuda()] = 127 if kind == "fp8" else float("nan")
+    q = torch.from_numpy(g.standard_normal((len(lens), 8, 64), dtype=np.float32)).cuda().to(DT["fp32" if kind == "fp32" else "bf16"])
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    ctx = ctx_of(contexts, kind)
+    ctx.paged_attention(cache, q, i32(lens), out, lse=lse, window=window, sinks=sinks, softcap=20.0)
+    assert ctx.sync_status() == 0
+    kept = [[x[OB.seen(len(x), window, sinks)] for x in kv] for kv in tokens]
+    check_attend(out, lse, q, kept, kind, 4, softcap=20.0)
