@@ -584,6 +584,36 @@ scute_status scute_paged_attention(scute_ctx *ctx, const scute_kv_cache *kv, con
 scute_status scute_paged_attention_sinks(scute_ctx *ctx, const scute_kv_cache *kv, const scute_attention *a,
                                          int32_t sinks, void *stream);
 
+/* The same for a batch whose requests share the beginnings of their contexts (rows of
+ * scute_kv_fork, requests behind one system prompt), read once for each group of them
+ * instead of once for each request.  Group g is the requests start[g] .. start[g + 1) - 1,
+ * whose first len[g] cached tokens lie in the same pages: each of their rows of the
+ * block table names them (of a request with fewer tokens no row is read for them; it
+ * is attended alone, as are requests before start[0] and from start[n_groups] on).  The
+ * result is that of scute_paged_attention, summed in another order.
+ *   start       device int32 [n_groups + 1], not falling, 0..n_req; len device int32
+ *               [n_groups], 0..table_cols * page_size.  What lies outside counts as the
+ *               nearest inside and is recorded (SCUTE_ERR_PAGES);
+ *   n_groups    0..SCUTE_MAX_GROUPS;
+ *   work        device memory of at least scute_shared_bytes, 16-byte aligned, that
+ *               this call alone uses until it has ended; nothing in it needs to be set
+ *               before, or is kept for the next call;
+ *   a->window   must be 0.
+ * Heads of more than 128 elements, more than 128 query heads to a key/value head, and FP32
+ * caches are read for each request alone, as in scute_paged_attention. */
+#define SCUTE_MAX_GROUPS 1024
+typedef struct {
+    const int32_t *start, *len;
+    void *work;
+    int64_t work_bytes;
+    int32_t n_groups;
+} scute_shared;
+scute_status scute_paged_attention_shared(scute_ctx *ctx, const scute_kv_cache *kv, const scute_attention *a,
+                                          const scute_shared *s, void *stream);
+/* Bytes of `work` for calls of at most n_req requests on this context (-1: sizes that
+ * no call takes). */
+int64_t scute_shared_bytes(const scute_ctx *ctx, int n_req, int q_heads, int kv_heads, int head_dim);
+
 /* The end of a sub-block and the beginning of the next, for n token rows:
  *     h = residual + scale * gate * post(y),   out = pre(h).
  * post and pre are norms over a row of d: x / sqrt(mean(x^2) + eps) * w + b, or

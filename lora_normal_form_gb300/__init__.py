@@ -120,6 +120,11 @@ class _HeadNormStruct(ctypes.Structure):
                 ("k_w_stride", ctypes.c_int64), ("eps", ctypes.c_float), ("layer", ctypes.c_int32)]
 
 
+class _SharedStruct(ctypes.Structure):
+    _fields_ = [("start", ctypes.c_void_p), ("len", ctypes.c_void_p), ("work", ctypes.c_void_p),
+                ("work_bytes", ctypes.c_int64), ("n_groups", ctypes.c_int32)]
+
+
 class _ForkStruct(ctypes.Structure):
     _fields_ = [("table_in", ctypes.c_void_p), ("len_in", ctypes.c_void_p), ("table_in_stride", ctypes.c_int64),
                 ("source", ctypes.c_void_p), ("len_new", ctypes.c_void_p), ("table_out", ctypes.c_void_p),
@@ -241,6 +246,22 @@ class HeadNorm:
                                  f"got {tuple(w.shape)}")
 
 
+class Shared:
+    """Groups of a batch whose requests share the beginnings of their contexts
+    (scute_shared): requests ``start[g]`` .. ``start[g + 1] - 1`` the first ``length[g]``
+    tokens (device int32 [groups + 1] and [groups]).  ``work``: a tensor of
+    ``Context.shared_work``, for one call at a time."""
+
+    def __init__(self, start, length, work):
+        _flat(_torch().int32, length.numel() + 1, start)
+        _flat(_torch().int32, length.numel(), length)
+        if not work.is_contiguous():
+            raise ValueError("the workspace is consecutive bytes")
+        self.tensors = (start, length, work)
+        self.struct = _SharedStruct(ptr(start), ptr(length), ptr(work), work.nbytes, length.numel())
+        self.ref = ctypes.byref(self.struct)
+
+
 def _torch():
     """torch, which has been imported where there is a tensor to check."""
     return sys.modules["torch"]
@@ -332,6 +353,8 @@ _SIGS = {
     "scute_kv_copy": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                      ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
     "scute_paged_attention": (ctypes.c_int, [ctypes.c_void_p] * 4),
+    "scute_paged_attention_shared": (ctypes.c_int, [ctypes.c_void_p] * 5),
+    "scute_shared_bytes": (ctypes.c_int64, [ctypes.c_void_p] + [ctypes.c_int] * 4),
     "scute_paged_attention_sinks": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_int32, ctypes.c_void_p]),
     "scute_residual_norm": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
                                            ctypes.c_void_p]),
@@ -563,14 +586,25 @@ def scute_kv_copy(ctx, caches: KvCaches, copy_from, copy_to, tokens, n, stream=N
 
 
 def scute_paged_attention(ctx, cache: KvCache, q, q_stride, out, out_stride, lse, kv_len, n_req, q_heads,
-                          scale=0.0, softcap=0.0, window=0, stream=None, sinks=0):
-    """``sinks``: scute_paged_attention_sinks where it is not 0."""
+                          scale=0.0, softcap=0.0, window=0, stream=None, sinks=0, shared: Optional[Shared] = None):
+    """``sinks``, ``shared``: scute_paged_attention_sinks, scute_paged_attention_shared where given."""
     a = _ATTENTION.pack(ptr(q) or 0, q_stride, ptr(out) or 0, out_stride, ptr(lse) or 0, ptr(kv_len) or 0, n_req,
                         q_heads, scale, softcap, window)
-    if sinks:
+    if shared is not None:
+        if sinks:
+            raise ValueError("shared beginnings with a window's first tokens")
+        _check(ctx, load().scute_paged_attention_shared(ctx, cache.ref, a, shared.ref, _stream_handle(stream)))
+    elif sinks:
         _check(ctx, load().scute_paged_attention_sinks(ctx, cache.ref, a, sinks, _stream_handle(stream)))
     else:
         _check(ctx, load().scute_paged_attention(ctx, cache.ref, a, _stream_handle(stream)))
+
+
+def scute_shared_bytes(ctx, n_req, q_heads, kv_heads, head_dim) -> int:
+    n = load().scute_shared_bytes(ctx, n_req, q_heads, kv_heads, head_dim)
+    if n < 0:
+        raise ScuteError(2, f"no workspace for {n_req} requests of {q_heads} heads on {kv_heads} of {head_dim}")
+    return n
 
 
 def scute_residual_norm(ctx, n, d, y, y_stride, residual=None, residual_stride=0, residual_out=None,

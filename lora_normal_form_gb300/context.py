@@ -3,10 +3,10 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (BF16, FP32, METHOD_ID, HeadNorm, KvCache, KvCaches, Rope, _check_table, _flat, _rows, _torch, scute_add_layer, scute_create, scute_debug_index, scute_destroy,
+from . import (BF16, FP32, METHOD_ID, HeadNorm, KvCache, KvCaches, Rope, Shared, _check_table, _flat, _rows, _torch, scute_add_layer, scute_create, scute_debug_index, scute_destroy,
                scute_kv_append, scute_kv_append_norm, scute_kv_copy, scute_kv_fork, scute_kv_resize, scute_launch_count, scute_linear, scute_linear_batch, scute_linear_batch_host,
                scute_linear_host, scute_paged_attention, scute_predict_batch, scute_predict_bytes,
-               scute_register_adapter, scute_residual_norm, scute_rope_table, scute_set_shared, scute_set_variant, scute_sync_status,
+               scute_register_adapter, scute_residual_norm, scute_rope_table, scute_set_shared, scute_set_variant, scute_shared_bytes, scute_sync_status,
                scute_timing_enable,
                scute_timing_kinds, scute_timing_read, scute_timing_reset, scute_unregister_adapter)
 
@@ -199,10 +199,11 @@ class Context:
         scute_kv_copy(self.handle, caches, copy_from, copy_to, copy_tokens, n, stream)
 
     def paged_attention(self, cache: KvCache, q, kv_len, out, scale: float = 0.0, softcap: float = 0.0,
-                        window: int = 0, lse=None, stream=None, sinks: int = 0):
+                        window: int = 0, lse=None, stream=None, sinks: int = 0, shared: Shared = None):
         """One new token of each request over its cached tokens: q and out
         [n_req, q_heads, dim] (or [n_req, q_heads * dim]).  ``window``: the last that
-        many of them, and the first ``sinks``."""
+        many of them, and the first ``sinks``.  ``shared``: groups of requests with a
+        common beginning, read once for each group."""
         n, dim, (io, int32, float32) = kv_len.shape[0], cache.head_dim, self._dtypes()
         row = q.numel() // n if n else cache.kv_row
         if row % dim or cache.requests < n:
@@ -210,7 +211,12 @@ class Context:
         _flat(int32, n, kv_len)
         _flat(float32, n * row // dim, lse)
         scute_paged_attention(self.handle, cache, q, _rows(q, n, row, io), out, _rows(out, n, row, io), lse, kv_len, n,
-                              row // dim, scale, softcap, window, stream, sinks)
+                              row // dim, scale, softcap, window, stream, sinks, shared)
+
+    def shared_work(self, cache: KvCache, n_req: int, q_heads: int):
+        """A workspace for ``Shared``: calls of up to ``n_req`` requests on such a cache."""
+        t, at = _torch(), cache.tensors[0].device
+        return t.empty(scute_shared_bytes(self.handle, n_req, q_heads, cache.kv_heads, cache.head_dim), dtype=t.uint8, device=at)
 
     def residual_norm(self, y, out=None, residual=None, residual_out=None, pre_w=None, pre_b=None, post_w=None,
                       post_b=None, gate=None, scale: float = 1.0, eps: float = 1e-5, layer: bool = False, stream=None):

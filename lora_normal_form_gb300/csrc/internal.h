@@ -481,10 +481,45 @@ struct AttendArgs {
     int *ctr;                  // arrivals at such a row (zero between launches)
     int *status;
     int hold;                  // 1: stages are never given back (test hook of the waits' end)
+    // of a batch whose groups share their contexts' beginnings (k_shared.cu): null, or
+    const int *first;          // [request] its first token of its own
+    const int4 *piece;         // [request][key/value head] the parts that hold its heads over those before
+    const float2 *stat;        // [row] a part's maximum and sum
+    const float *part_o;       // and its outputs
 };
 size_t attend_part_floats(int num_sms);
 int attend_ctrs(int num_sms);
 cudaError_t launch_attend(const AttendArgs &a, int num_sms, cudaStream_t st);
+
+// ---------------------------------------------------------------- the beginning that a group's requests share
+constexpr int SHARED_MAX_GROUPS = 1024, SHARED_MAX_DIM = 128, SHARED_MAX_GROUP_HEADS = 128;
+constexpr int SHARED_TWIN = 1 << 30;
+// Parts: rows of (m, l) and of D outputs.  The heads of request r on key/value head h
+// have those of CTAs piece.x .. piece.y (SHARED_TWIN taken out; less than x: none): rows
+// piece.z + 256 CTA .. of piece.w & 0xffff rows, with SHARED_TWIN as many again directly
+// behind, the request's first head piece.w >> 16 of them; element d of row i at
+// (first row) D + d / 8 * rows * 8 + i * 8 + d % 8.
+struct SharedArgs {
+    KvView kv;
+    const void *q;
+    long long q_stride;
+    const int32_t *kv_len;
+    int n_req, group;          // query heads of a key/value head
+    int tile_req;              // requests of a stream's 128 rows
+    float scale, softcap;
+    int page_shift;
+    const int32_t *start, *len;
+    int n_groups;
+    int *first;
+    int4 *piece;
+    float2 *stat;
+    float *o;
+    int *status;
+    int hold;
+};
+// rows of parts that a batch may need
+inline long long shared_rows(long long n_req, long long q_heads, int num_sms) { return 2 * n_req * q_heads + 256ll * num_sms; }
+cudaError_t launch_shared(const SharedArgs &a, int num_sms, cudaStream_t st);
 
 // ---------------------------------------------------------------- norms around a sub-block
 struct NormArgs {

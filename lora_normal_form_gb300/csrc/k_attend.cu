@@ -660,16 +660,22 @@ struct FmaMath {
 // tokens that stay visible before a window stand directly before it, token_of(first,
 // i) the token at position i (a window from token f on, of whose S = min(sinks, f)
 // tokens before stay: first = f - S, and positions below f are tokens 0 .. S - 1).
+template <bool SHARED>
 __device__ __forceinline__ void seen_of(const AttendArgs &a, int r, int *first, int *len, bool *bad) {
     const int cap = a.kv.table_cols * a.kv.page_size;
     int n = a.kv_len[r];
     *bad = n < 0 || n > cap;
     n = n < 0 ? 0 : n > cap ? cap : n;
     *len = n;
-    const int f = a.window > 0 ? max(0, n - a.window) : 0;
-    *first = f - min(f, a.sinks);
+    if constexpr (SHARED) {
+        *first = a.first[r];
+    } else {
+        const int f = a.window > 0 ? max(0, n - a.window) : 0;
+        *first = f - min(f, a.sinks);
+    }
 }
 __device__ __forceinline__ int token_of(const AttendArgs &a, int first, int i) { return i - (i < first + a.sinks ? first : 0); }
+template <bool SHARED>
 __device__ __forceinline__ void plan_places(const AttendArgs &a, int tt, int *places_at, int *warp_sum) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, n = a.n_req, threads = blockDim.x;
     const int per = (n + threads - 1) / threads, r0 = min(n, t * per), r1 = min(n, r0 + per);
@@ -679,7 +685,7 @@ __device__ __forceinline__ void plan_places(const AttendArgs &a, int tt, int *pl
     for (int r = r0; r < r1; ++r) {
         int first, len;
         bool bad;
-        seen_of(a, r, &first, &len, &bad);
+        seen_of<SHARED>(a, r, &first, &len, &bad);
         any |= bad;
         mine += ROW_COST + max(1, (len - first + tt - 1) / tt);
     }
@@ -697,7 +703,7 @@ __device__ __forceinline__ void plan_places(const AttendArgs &a, int tt, int *pl
     for (int r = r0; r < r1; ++r) {
         int first, len;
         bool bad;
-        seen_of(a, r, &first, &len, &bad);
+        seen_of<SHARED>(a, r, &first, &len, &bad);
         places_at[r] = at;
         at += ROW_COST + max(1, (len - first + tt - 1) / tt);
     }
@@ -711,6 +717,7 @@ __device__ __forceinline__ long long quotient(long long x, long long y) {
 }
 
 // Walks a CTA's range of places, row by row.
+template <bool SHARED>
 struct Walk {
     const AttendArgs &a;
     const int *places_at;
@@ -736,7 +743,7 @@ struct Walk {
     __device__ __forceinline__ int last_owner() const { return owner(base + ROW_COST + tiles - 1); }
     __device__ __forceinline__ void request() {
         bool bad;
-        seen_of(a, r, &first, &len, &bad);
+        seen_of<SHARED>(a, r, &first, &len, &bad);
         tiles = places_at[r + 1] - places_at[r] - ROW_COST;
     }
     __device__ __forceinline__ void cut(long long from) {
@@ -804,6 +811,43 @@ __device__ __forceinline__ void put(const AttendArgs &a, int r, int h, int d, fl
     }
 }
 
+// Take in what the requests of a group share: the parts of head h (of the request's on
+// key/value head hk) that k_shared.cu left, in the order of their CTAs, into this head's
+// maximum, sum and four outputs from d on.
+__device__ __forceinline__ void add_shared(const AttendArgs &a, int r, int hk, int h, int d, float &m, float &l, float4 &x) {
+    const int4 piece = a.piece[(long long)r * a.kv.heads + hk];
+    if (piece.y < 0) return;
+    const int twin = piece.y & SHARED_TWIN ? 1 : 0, n = piece.w & 0xffff, i = (piece.w >> 16) + h;
+    const int parts = ((piece.y & ~SHARED_TWIN) - piece.x + 1) << twin;
+    constexpr int B = 4;                  // parts at a time
+#pragma unroll 1
+    for (int k0 = 0; k0 < parts; k0 += B) {
+        float2 s[B];
+        float4 y[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const int at = min(k0 + k, parts - 1);
+            const int row = piece.z + 256 * (piece.x + (at >> twin)) + (at & twin) * n;
+            s[k] = a.stat[row + i];
+            if (k0 + k >= parts) s[k].x = -INFINITY;
+            y[k] = *reinterpret_cast<const float4 *>(a.part_o + (long long)row * a.kv.dim + (d >> 3) * n * 8 + i * 8 + (d & 4));
+        }
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < B; ++k) top = fmaxf(top, s[k].x);
+        const float ref = top == -INFINITY ? 0.f : top, f = exp2f(m - ref);
+        l *= f, x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+        m = top;
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            if (s[k].x == -INFINITY) continue;           // no token: its outputs are not written
+            const float g = exp2f(s[k].x - ref);
+            l += s[k].y * g;
+            x.x += y[k].x * g, x.y += y[k].y * g, x.z += y[k].z * g, x.w += y[k].w * g;
+        }
+    }
+}
+
 // A row that several CTAs share, as its joiner needs it.
 struct SharedRow {
     int r, hk, h0, nh, c0, c1;          // request, heads; its first and last CTA
@@ -815,7 +859,7 @@ struct SharedRow {
 // is a race, and a row joined in other groups has other bits.  A row whose parts fit
 // is joined in one group, alone or beside another; one whose parts do not, in groups
 // of as many as fit alone.
-template <typename IO, int THREADS>
+template <typename IO, int THREADS, bool SHARED>
 __device__ __forceinline__ void join_parts(const AttendArgs &a, const SharedRow &head, const SharedRow &tail, bool last_head,
                                            bool last_tail, uint8_t *buf, int room, int t) {
     constexpr int IT = 2;                // groups of four outputs of a thread at a time
@@ -909,6 +953,7 @@ __device__ __forceinline__ void join_parts(const AttendArgs &a, const SharedRow 
                 const int e = g0 + t + i * THREADS;
                 if (e >= items) break;
                 const int h = e / (D / 4), d = 4 * (e - h * (D / 4));
+                if constexpr (SHARED) add_shared(a, row.r, row.hk, row.h0 - row.hk * a.group + h, d, m[i], l[i], x[i]);
                 put<IO>(a, row.r, row.h0 + h, d, x[i], l[i] == 0.f ? 0.f : vs / l[i]);
                 if (a.lse && d == 0) a.lse[(long long)row.r * a.q_heads + row.h0 + h] = (m[i] + log2f(l[i])) * LN2;
             }
@@ -930,7 +975,7 @@ struct Shape {
     static size_t smem(int stages, int n_req) { return FIXED + (size_t)stages * STAGE + 4 * ((size_t)n_req + 1); }
 };
 
-template <typename M, int DC, int CW, int PW, int CTAS>
+template <typename M, int DC, int CW, int PW, int CTAS, bool SHARED>
 __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const AttendArgs a, int stages) {
     using S = Shape<M, DC, CW, PW, CTAS>;
     using IO = typename M::IO;
@@ -976,8 +1021,8 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
             reinterpret_cast<uint4 *>(s_ring)[i] = make_uint4(0, 0, 0, 0);
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    plan_places(a, TT, places_at, s_warp);
-    Walk w(a, places_at, HC, TT, MIN_TILES);
+    plan_places<SHARED>(a, TT, places_at, s_warp);
+    Walk<SHARED> w(a, places_at, HC, TT, MIN_TILES);
     const int cta = blockIdx.x;
     if (cta >= w.ctas) return;
     w.open(cta);
@@ -1200,9 +1245,17 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
             const float vs = a.kv.v_scale ? a.kv.v_scale[w.hk] : 1.f;
             for (int i = t; i < nh * (D / 4); i += CW * 32) {
                 const int h = i / (D / 4), d = 4 * (i - h * (D / 4));
-                put<IO>(a, w.r, h0 + h, d, merged(h, d), s_sum[h] == 0.f ? 0.f : vs / s_sum[h]);
+                if constexpr (SHARED) {
+                    float m = s_top[h], l = s_sum[h];
+                    float4 x = merged(h, d);
+                    add_shared(a, w.r, w.hk, w.z * HC + h, d, m, l, x);
+                    put<IO>(a, w.r, h0 + h, d, x, l == 0.f ? 0.f : vs / l);
+                    if (a.lse && d == 0) a.lse[(long long)w.r * a.q_heads + h0 + h] = (m + log2f(l)) * LN2;
+                } else {
+                    put<IO>(a, w.r, h0 + h, d, merged(h, d), s_sum[h] == 0.f ? 0.f : vs / s_sum[h]);
+                }
             }
-            if (a.lse && t < nh) a.lse[(long long)w.r * a.q_heads + h0 + t] = (s_top[t] + log2f(s_sum[t])) * LN2;
+            if (!SHARED && a.lse && t < nh) a.lse[(long long)w.r * a.q_heads + h0 + t] = (s_top[t] + log2f(s_sum[t])) * LN2;
         } else {
             const PartView p = part_of(a, 2 * cta + (w.t0 == 0 ? 1 : 0));
             for (int i = t; i < nh * (D / 4); i += CW * 32) {
@@ -1233,15 +1286,15 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
     sync_threads<CW * 32>();
     const bool last_head = s_last[0], last_tail = s_last[1];
     if (last_head || last_tail)          // the ring is empty by now
-        join_parts<IO, CW * 32>(a, head, tail, last_head, last_tail, s_ring, stages * S::STAGE, t);
+        join_parts<IO, CW * 32, SHARED>(a, head, tail, last_head, last_tail, s_ring, stages * S::STAGE, t);
 }
 
-template <typename M, int DC, int CW, int PW, int CTAS>
+template <typename M, int DC, int CW, int PW, int CTAS, bool SHARED = false>
 cudaError_t launch_shape(const AttendArgs &a, int num_sms, cudaStream_t st) {
     using S = Shape<M, DC, CW, PW, CTAS>;
     static_assert(CTAS <= ATT_CTAS, "workspace");
     static std::atomic<unsigned long long> done{0};
-    const auto kernel = attend_kernel<M, DC, CW, PW, CTAS>;
+    const auto kernel = attend_kernel<M, DC, CW, PW, CTAS, SHARED>;
     const cudaError_t e = allow_max_dynamic_smem(kernel, done);
     if (e != cudaSuccess) return e;
     // as many CTAs on an SM as its registers allow; fewer where a large batch's
@@ -1274,16 +1327,20 @@ cudaError_t launch_shape(const AttendArgs &a, int num_sms, cudaStream_t st) {
 //       dim <= 64              2,1,4: 69.7, 4,2,2: 90.6 (e4m3 98.3, 129.9)
 //     dim > 128                4,2,2: 72.0, 2,2,2: 80.1, 2,1,3: 101.5 (32 requests);
 //                              e4m3, 4 heads 138.6, 144.8, 136.3
+// (a batch with shared beginnings in the same shapes, for the tokens of its own)
+template <bool FP8, bool SHARED>
+cudaError_t launch_mma_128(const AttendArgs &a, int num_sms, cudaStream_t st) {
+    const bool wide = a.group > 8;
+    if (a.kv.dim > 64)
+        return wide ? launch_shape<MmaMath<FP8, 128, 2>, 128, 4, 2, 2, SHARED>(a, num_sms, st)
+                    : launch_shape<MmaMath<FP8, 128, 1>, 128, 2, 1, 4, SHARED>(a, num_sms, st);
+    return wide ? launch_shape<MmaMath<FP8, 64, 2>, 64, 2, 1, 4, SHARED>(a, num_sms, st)
+                : launch_shape<MmaMath<FP8, 64, 1>, 64, 2, 1, FP8 ? 6 : 4, SHARED>(a, num_sms, st);
+}
 template <bool FP8>
 cudaError_t launch_mma(const AttendArgs &a, int num_sms, cudaStream_t st) {
-    const int D = a.kv.dim;
-    const bool wide = a.group > 8;
-    if (D > 128) return launch_shape<MmaMath<FP8, 256, 1>, 256, 4, 2, 2>(a, num_sms, st);
-    if (D > 64)
-        return wide ? launch_shape<MmaMath<FP8, 128, 2>, 128, 4, 2, 2>(a, num_sms, st)
-                    : launch_shape<MmaMath<FP8, 128, 1>, 128, 2, 1, 4>(a, num_sms, st);
-    return wide ? launch_shape<MmaMath<FP8, 64, 2>, 64, 2, 1, 4>(a, num_sms, st)
-                : launch_shape<MmaMath<FP8, 64, 1>, 64, 2, 1, FP8 ? 6 : 4>(a, num_sms, st);
+    if (a.kv.dim > 128) return launch_shape<MmaMath<FP8, 256, 1>, 256, 4, 2, 2>(a, num_sms, st);
+    return a.first ? launch_mma_128<FP8, true>(a, num_sms, st) : launch_mma_128<FP8, false>(a, num_sms, st);
 }
 // 32-bit caches, in the same way (group 4, 32 requests; 8 heads at a time spill 440
 // bytes with dim > 128, 100 with dim <= 64):

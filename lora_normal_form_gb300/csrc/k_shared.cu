@@ -1,0 +1,804 @@
+// Attention of one new token of each request over the beginning that the requests of
+// a group share: every request's query heads on one key/value head are rows of two
+// matrix products with the same keys and values, so that these are read once for the
+// group instead of once for each request:
+//     S [rows x tokens] = Q K^T,   O [rows x D] = P V,   P = 2^(S - m).
+// What it leaves is not an output but parts, a row's maximum m, sum l and unnormalised
+// O over some of the tokens, which the one-token attention takes in when it ends the
+// request's row over the tokens of its own (k_attend.cu).
+//
+// What bounds it.  A token costs 2 x D x size bytes and 2 x 2 x rows x D operations (the
+// second product twice over, see below, so 3 x 2): with bf16 keys 1.5 x rows
+// operations a byte, against the 286 where this GPU's tensor and memory rates
+// balance: memory up to 190 rows (48 requests of 4 heads to a key), the products beyond.
+//
+// Layout.  Work rows are (group, key/value head, up to 2 x 128 rows), their tiles of 128
+// tokens one sequence that is cut into equal contiguous ranges, one per CTA, as in
+// k_attend.cu.  In a CTA four warps bring keys and values to shared memory, each to a
+// ring of its own; one issues the products (tcgen05.mma); and two warpgroups each run
+// a stream of its own: scores in tensor memory, read back (a thread has a row), their
+// weights written over them, the second product from there, into outputs that stay in
+// tensor memory.  Up to 128 rows the streams take alternate tiles of the same rows, beyond
+// each takes 128 rows of every tile; either way one stream's products run under the
+// other's softmax.
+//
+// Weights go to the second product as two bf16 numbers, one rounded and what that left
+// (16 bits of a weight, 2^-17 of it, as in k_attend.cu), l sums them in 32 bits.  The
+// reference m moves only when a score passes it by more than 2^8, so that outputs are
+// seldom scaled.  Tokens behind the shared beginning's end are zero in shared memory and
+// their scores minus infinity.
+#include <cuda_fp8.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace scute {
+
+namespace {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr int TT = 128;                    // tokens of a tile
+constexpr int TILE = 128;                  // rows of a stream's tile
+constexpr int SOFT = 256, LOAD = 128, THREADS = SOFT + LOAD + 32;
+constexpr int ROW_COST = 2;                // what a work row costs beside its tiles, in tiles
+constexpr int MIN_TILES = 2;               // of a range
+// Tiles whose tokens' marks are kept: a tile's are read by its softmax, which the keys
+// SLOTS + 2 tiles on wait for (their slot is free when the products of two tiles on are
+// done, and those follow it).
+constexpr int OK_RING = 8;
+constexpr uint64_t WAIT_NS = 2000000000ull;
+constexpr unsigned ALL = 0xffffffffu;
+
+// A whole warp's bounded wait, decided by the warp's votes alone.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    const uint64_t t0 = ptx::globaltimer();
+    for (;;) {
+        if (__any_sync(ALL, *abort_flag != 0)) return false;
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (__all_sync(ALL, ptx::mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(ALL, ptx::globaltimer() - t0 > WAIT_NS)) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    return __all_sync(ALL, ptx::mbar_try_wait(bar, parity)) || wait_long(bar, parity, abort_flag);
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(real ? 16 : 0)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_left() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// This thread's writes to shared memory before, as the tensor cores and their like read it.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void sts16(uint32_t p, uint4 x) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+__device__ __forceinline__ float pow2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t y;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+__device__ __noinline__ float capped(float x, float cap) { return cap * LOG2E * tanhf(x / cap); }
+// Two e4m3 values (16 bits of a word) as two bf16 ones, exactly: 4 bits of significand.
+__device__ __forceinline__ uint32_t to_bf16(uint32_t pair) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(pair));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return pack_bf16(f.x, f.y);
+}
+
+// ---------------------------------------------------------------- tensor memory and products
+// 32 columns of this warp's 32 lanes, without a wait.
+__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at));
+}
+// The loads before have arrived (the registers pass through, so that no use moves above).
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// D (+)= A B^T with A in tensor memory.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
+}
+// A slab is 64 elements (128 bytes) of each of 128 rows, 8 rows a 1024-byte atom whose
+// 16-byte pieces are permuted within their row by the row's number.  Read along the 64
+// elements (queries, keys: K-major) or across the rows (values: the inner index of the
+// second product is the token, elements of a row lie along N; further slabs one SLAB on).
+constexpr uint32_t SLAB = 128 * 128;
+__device__ __forceinline__ uint32_t place_of(int row, int piece) {      // of a 16-byte piece in its slabs
+    return (piece >> 3) * SLAB + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ uint64_t slab_desc(uint32_t at, uint32_t lead_bytes) {
+    uint64_t d = (uint64_t)((at & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(lead_bytes >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+// fp32 sums of bf16 products, M = 128 rows, N columns; `across`: B read across its rows.
+constexpr uint32_t instr_desc(int n, bool across) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (across ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(TILE >> 4) << 24);
+}
+
+// ---------------------------------------------------------------- the plan
+// Groups, made by every CTA for itself: requests start[g] .. start[g + 1), the tokens
+// they share, the first request that has them all (whose row of the table is read), and
+// the places of the groups before.  A group of fewer than two such requests is left to
+// the one-token attention.
+struct Plan {
+    int start[SHARED_MAX_GROUPS + 1], tokens[SHARED_MAX_GROUPS], lead[SHARED_MAX_GROUPS];
+    int busy[SHARED_MAX_GROUPS];
+    long long at[SHARED_MAX_GROUPS + 1];
+    long long warp_sum[THREADS / 32];
+    int warp_max[THREADS / 32];
+};
+struct Bars {
+    uint64_t kfull[4], kempty[4], vfull[4], vempty[4], qfull, qempty, sfull[2], pfull[2], ofull[2], drain;
+    uint32_t tmem;
+    int abort;
+    unsigned ok[OK_RING][TT / 32];         // tokens that count, of the last tiles' keys
+};
+
+__device__ __forceinline__ int length_of(const SharedArgs &a, int r) {
+    const int cap = a.kv.table_cols * a.kv.page_size, n = a.kv_len[r];
+    return n < 0 ? 0 : n > cap ? cap : n;
+}
+// The last group that begins at request r or before (its start is at most r).
+__device__ __forceinline__ int group_of(const Plan &p, int n_groups, int r) {
+    int lo = 0, hi = n_groups - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.start[mid] <= r) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+__device__ __forceinline__ int requests_of(const Plan &p, int g) { return p.start[g + 1] - p.start[g]; }
+__device__ __forceinline__ int tiles_of(const Plan &p, int g) { return p.busy[g] < 2 ? 0 : (p.tokens[g] + TT - 1) / TT; }
+__device__ __forceinline__ int blocks_of(const SharedArgs &a, const Plan &p, int g) {
+    return (requests_of(p, g) + 2 * a.tile_req - 1) / (2 * a.tile_req);
+}
+
+__device__ __forceinline__ void make_plan(const SharedArgs &a, Plan &p) {
+    static_assert(SHARED_MAX_GROUPS + 1 <= 3 * THREADS, "three groups of a thread");
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, G = a.n_groups;
+    const int cap = a.kv.table_cols * a.kv.page_size;
+    bool bad = false;
+    // starts that do not fall (a running maximum), inside the batch
+    int s[3], top = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const int g = 3 * t + i;
+        s[i] = g <= G ? a.start[g] : 0;
+        if (s[i] < 0 || s[i] > a.n_req) bad = true;
+        s[i] = min(max(s[i], 0), a.n_req);
+        top = max(top, s[i]);
+    }
+    int run = top;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(ALL, run, o);
+        if (lane >= o) run = max(run, y);
+    }
+    if (lane == 31) p.warp_max[warp] = run;
+    int before = __shfl_up_sync(ALL, run, 1);
+    if (lane == 0) before = 0;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) before = max(before, p.warp_max[w]);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const int g = 3 * t + i;
+        if (g > G) break;
+        if (s[i] < before) bad = true;
+        before = max(before, s[i]);
+        p.start[g] = before;
+        if (g == G) break;
+        const int n = a.len[g];
+        if (n < 0 || n > cap) bad = true;
+        p.tokens[g] = min(max(n, 0), cap);
+        p.lead[g] = INT32_MAX;
+        p.busy[g] = 0;
+    }
+    __syncthreads();
+    for (int r = p.start[0] + t; r < p.start[G]; r += THREADS) {
+        const int n = a.kv_len[r];
+        if (n < 0 || n > cap) bad = true;
+        const int g = group_of(p, G, r);
+        if (p.tokens[g] > 0 && length_of(a, r) >= p.tokens[g]) {
+            atomicMin(&p.lead[g], r);
+            atomicAdd(&p.busy[g], 1);
+        }
+    }
+    if (bad && blockIdx.x == 0) atomicOr(a.status, STATUS_PAGES);
+    __syncthreads();
+    long long mine[3], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const int g = 3 * t + i;
+        const int tiles = g < G ? tiles_of(p, g) : 0;
+        mine[i] = tiles ? (long long)a.kv.heads * blocks_of(a, p, g) * (tiles + ROW_COST) : 0;
+        sum += mine[i];
+    }
+    long long inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(ALL, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) p.warp_sum[warp] = inc;
+    __syncthreads();
+    long long at = inc - sum;
+    for (int w = 0; w < warp; ++w) at += p.warp_sum[w];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const int g = 3 * t + i;
+        if (g <= G) p.at[g] = at;
+        at += mine[i];
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+    return ((x | y) >> 32) == 0 ? (long long)((unsigned)x / (unsigned)y) : x / y;
+}
+// How the places are cut.
+struct Cut {
+    long long total;
+    int ctas;
+    __device__ __forceinline__ Cut(const SharedArgs &a, const Plan &p) {
+        total = p.at[a.n_groups];
+        ctas = (int)min((long long)gridDim.x, quotient(total + MIN_TILES - 1, MIN_TILES));
+    }
+    __device__ __forceinline__ long long start(int cta) const { return quotient(total * cta, ctas); }
+    __device__ __forceinline__ int owner(long long x) const { return (int)quotient((x + 1) * ctas - 1, total); }
+};
+// A work row: its group, key/value head, block of requests, and where its parts go.
+struct WorkRow {
+    int g, hk, r0, requests;      // the block's first request and number of them
+    bool twin;                    // both streams take the same rows
+    int first_row;                // of its parts in the workspace, before the CTA's own offset
+};
+__device__ __forceinline__ WorkRow work_row(const SharedArgs &a, const Plan &p, int g, int row) {
+    WorkRow w;
+    const int blocks = blocks_of(a, p, g), all = requests_of(p, g);
+    w.g = g;
+    w.hk = row / blocks;
+    const int b = row - w.hk * blocks;
+    w.r0 = p.start[g] + b * 2 * a.tile_req;
+    w.requests = min(2 * a.tile_req, all - b * 2 * a.tile_req);
+    w.twin = w.requests <= a.tile_req;
+    // twice a row's room: a twin's streams each leave all of the rows
+    w.first_row = 2 * a.group * (p.start[g] * a.kv.heads + w.hk * all + b * 2 * a.tile_req);
+    return w;
+}
+__device__ __forceinline__ int stream_requests(const SharedArgs &a, const WorkRow &w, int x) {
+    return w.twin ? w.requests : x == 0 ? a.tile_req : w.requests - a.tile_req;
+}
+// First row of a CTA's part of stream x.
+__device__ __forceinline__ int part_row(const SharedArgs &a, const WorkRow &w, int cta, int x) {
+    return w.first_row + 2 * TILE * cta + (x ? stream_requests(a, w, 0) * a.group : 0);
+}
+
+// Walks a CTA's range, work row by work row: tiles t0 .. t1 of each.
+struct Walk {
+    const SharedArgs &a;
+    const Plan &p;
+    long long base, end;
+    int g, row, rows, tiles, t0, t1;
+    WorkRow w;
+    __device__ __forceinline__ Walk(const SharedArgs &args, const Plan &plan, const Cut &cut, int cta) : a(args), p(plan) {
+        const long long x = cut.start(cta);
+        end = cut.start(cta + 1);
+        g = 0;
+        for (int hi = a.n_groups - 1; g < hi;) {          // the last group whose places begin at x or before
+            const int mid = (g + hi + 1) >> 1;
+            if (p.at[mid] <= x) g = mid;
+            else hi = mid - 1;
+        }
+        group();
+        row = tiles ? (int)quotient(x - p.at[g], tiles + ROW_COST) : 0;
+        base = p.at[g] + (long long)row * (tiles + ROW_COST);
+        set(x);
+    }
+    __device__ __forceinline__ void group() {
+        tiles = tiles_of(p, g);
+        rows = tiles ? a.kv.heads * blocks_of(a, p, g) : 0;
+    }
+    __device__ __forceinline__ void set(long long from) {
+        t0 = (int)max(0ll, from - base - ROW_COST);
+        t1 = (int)min((long long)tiles, end - base - ROW_COST);
+        if (more()) w = work_row(a, p, g, row);
+    }
+    __device__ __forceinline__ bool more() const { return tiles > 0 && base + ROW_COST < end; }
+    __device__ __forceinline__ void next() {
+        base += tiles + ROW_COST;
+        if (++row == rows) {
+            row = 0;
+            do ++g;
+            while (g < a.n_groups && tiles_of(p, g) == 0);
+            if (g < a.n_groups) group();
+            else tiles = 0;
+        }
+        set(base);
+    }
+};
+
+// What the one-token attention needs of each request and key/value head.
+__device__ __forceinline__ void write_pieces(const SharedArgs &a, const Plan &p, const Cut &cut) {
+    const int H = a.kv.heads;
+    for (long long i = (long long)blockIdx.x * THREADS + threadIdx.x; i < (long long)a.n_req * H; i += (long long)gridDim.x * THREADS) {
+        const int r = (int)(i / H), hk = (int)(i - (long long)r * H);
+        int4 piece = make_int4(0, -1, 0, 0);
+        int first = 0;
+        if (r >= p.start[0] && r < p.start[a.n_groups]) {
+            const int g = group_of(p, a.n_groups, r), tiles = tiles_of(p, g);
+            if (tiles && length_of(a, r) >= p.tokens[g]) {
+                first = p.tokens[g];
+                const int b = (r - p.start[g]) / (2 * a.tile_req), blocks = blocks_of(a, p, g);
+                const int row = hk * blocks + b;
+                const WorkRow w = work_row(a, p, g, row);
+                const int x = !w.twin && r - w.r0 >= a.tile_req;
+                const long long base = p.at[g] + (long long)row * (tiles + ROW_COST) + ROW_COST;
+                piece.x = cut.owner(base);
+                piece.y = cut.owner(base + tiles - 1) | (w.twin ? SHARED_TWIN : 0);
+                piece.z = part_row(a, w, 0, x);
+                piece.w = stream_requests(a, w, x) * a.group | (r - w.r0 - x * a.tile_req) * a.group << 16;
+            }
+        }
+        a.piece[i] = piece;
+        if (hk == 0) a.first[r] = first;
+    }
+}
+
+// ---------------------------------------------------------------- the kernel
+template <bool FP8, int DC>
+struct Shape {
+    static constexpr int SLABS = DC / 64, TILE_BYTES = SLABS * SLAB;
+    static constexpr int SLOTS = DC == 64 ? 4 : 2;             // of keys, and of values
+    static constexpr int LAG = 2 * SLOTS - 2;                  // fillings on their way before the oldest is waited for
+    static constexpr int SMEM = 1024 + (2 + 2 * SLOTS) * TILE_BYTES + (int)sizeof(Plan) + (int)sizeof(Bars) + 64;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+template <bool FP8, int DC>
+__global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) {
+    using S = Shape<FP8, DC>;
+    constexpr int SLOTS = S::SLOTS, TB = S::TILE_BYTES, ESZ = FP8 ? 1 : 2;
+    constexpr int S_COL = 0, O_COL = 2 * TT;                   // columns of tensor memory
+    extern __shared__ uint8_t raw[];
+    uint8_t *const tiles_at = raw + ((1024 - (ptx::smem_u32(raw) & 1023)) & 1023);
+    const uint32_t q_at = ptx::smem_u32(tiles_at), k_at = q_at + 2 * TB, v_at = k_at + SLOTS * TB;
+    Bars &b = *reinterpret_cast<Bars *>(tiles_at + (2 + 2 * SLOTS) * TB);
+    Plan &p = *reinterpret_cast<Plan *>(reinterpret_cast<uint8_t *>(&b) + ((sizeof(Bars) + 15) & ~15));
+    volatile int *const abort_flag = &b.abort;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, D = a.kv.dim, H = a.kv.heads, G = a.group;
+    auto bar = [&](uint64_t &x) { return ptx::smem_u32(&x); };
+
+    if (tid == 0) {
+        b.abort = 0;
+        for (int i = 0; i < SLOTS; ++i) {
+            ptx::mbar_init(bar(b.kfull[i]), LOAD / 32);
+            ptx::mbar_init(bar(b.kempty[i]), 1 + a.hold);
+            ptx::mbar_init(bar(b.vfull[i]), LOAD / 32);
+            ptx::mbar_init(bar(b.vempty[i]), 1);
+        }
+        ptx::mbar_init(bar(b.qfull), LOAD / 32);
+        ptx::mbar_init(bar(b.qempty), 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(b.sfull[i]), 1);
+            ptx::mbar_init(bar(b.pfull[i]), 4);
+            ptx::mbar_init(bar(b.ofull[i]), 1);
+        }
+        ptx::mbar_init(bar(b.drain), 1);
+        ptx::fence_mbar_init();
+    }
+    // behind a head's elements every row of a tile stays zero
+    if (D < DC) {
+        for (int i = tid; i < (2 + 2 * SLOTS) * TB / 16; i += THREADS) sts16(q_at + i * 16, make_uint4(0, 0, 0, 0));
+        fence_async();
+    }
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    make_plan(a, p);
+    const Cut cut(a, p);
+    write_pieces(a, p, cut);
+    const int cta = blockIdx.x;
+    if (cta >= cut.ctas) return;
+    if (warp == 12) {
+        ptx::tmem_alloc(ptx::smem_u32(&b.tmem), 512);
+        ptx::tmem_relinquish();
+        ptx::tc_fence_before();
+    }
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = b.tmem;
+    Walk w(a, p, cut, cta);
+
+    if (warp < 8) {
+        // ------------------------------------------------ a stream's softmax: a thread has a row
+        const int x = warp >> 2, i = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + S_COL + x * TT + lanes, o_at = tmem + O_COL + x * DC + lanes;
+        unsigned s_phase = 0, o_phase = 0, seq = 0;
+        bool live = true;
+        for (; live && w.more(); w.next()) {
+            const float scale = (a.kv.k_scale ? a.kv.k_scale[w.w.hk] : 1.f) * a.scale;
+            const float mul = a.softcap > 0.f ? scale : scale * LOG2E;
+            float top = -INFINITY, sum[4] = {0.f, 0.f, 0.f, 0.f};
+            bool any = false;
+            const unsigned piece_seq = seq;
+            seq += w.t1 - w.t0;
+            for (int t = w.t0 + (w.w.twin ? x : 0); t < w.t1; t += w.w.twin ? 2 : 1) {
+                live = wait_bar(bar(b.sfull[x]), s_phase, abort_flag);
+                if (!live) break;
+                s_phase ^= 1;
+                ptx::tc_fence_after();
+                uint32_t r[32], r2[32];
+                float f = mul;
+                const volatile unsigned *ok = b.ok[(piece_seq + (t - w.t0)) % OK_RING];
+                if (a.softcap > 0.f || (ok[0] & ok[1] & ok[2] & ok[3]) != ALL) {     // scores as they count, put back
+#pragma unroll 1
+                    for (int c = 0; c < TT / 32; ++c) {
+                        uint32_t y[32];
+                        const unsigned count = ok[c];
+                        tmem_load(s_at + c * 32, y);
+                        tmem_loaded(y);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            float z = __uint_as_float(y[k]) * mul;
+                            if (a.softcap > 0.f) z = capped(z, a.softcap);
+                            y[k] = __float_as_uint(count >> k & 1 ? z : -INFINITY);
+                        }
+                        __syncwarp();
+                        tmem_store(s_at + c * 32, y);
+                    }
+                    tmem_stored();
+                    f = 1.f;
+                }
+                float mx = -INFINITY;
+                tmem_load(s_at, r);
+#pragma unroll
+                for (int c = 0; c < TT / 32; c += 2) {
+                    tmem_loaded(r);
+                    tmem_load(s_at + (c + 1) * 32, r2);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(r[k]) * f);
+                    tmem_loaded(r2);
+                    if (c + 2 < TT / 32) tmem_load(s_at + (c + 2) * 32, r);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(r2[k]) * f);
+                }
+                if (__any_sync(ALL, mx > top + 8.f)) {
+                    const float to = fmaxf(mx, top), al = to == top ? 1.f : exp2f(top - to);
+                    top = to;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sum[k] *= al;
+                    if (any) {
+#pragma unroll 1
+                        for (int c = 0; c < DC / 32; ++c) {
+                            tmem_load(o_at + c * 32, r);
+                            tmem_loaded(r);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * al);
+                            tmem_store(o_at + c * 32, r);
+                        }
+                        tmem_stored();
+                    }
+                }
+                any = true;
+                const float ref = top == -INFINITY ? 0.f : top;
+                tmem_load(s_at, r);
+#pragma unroll
+                for (int c = 0; c < TT / 32; ++c) {
+                    uint32_t(&now)[32] = c & 1 ? r2 : r;
+                    uint32_t(&then)[32] = c & 1 ? r : r2;
+                    tmem_loaded(now);
+                    if (c + 1 < TT / 32) tmem_load(s_at + (c + 1) * 32, then);
+                    uint32_t w2[32];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float p0 = pow2(fmaf(__uint_as_float(now[2 * k]), f, -ref));
+                        const float p1 = pow2(fmaf(__uint_as_float(now[2 * k + 1]), f, -ref));
+                        sum[k & 1] += p0;
+                        sum[2 + (k & 1)] += p1;
+                        const uint32_t hi = pack_bf16(p0, p1);
+                        w2[k] = hi;
+                        w2[16 + k] = pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
+                    }
+                    tmem_store(s_at + c * 32, w2);
+                }
+                tmem_stored();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(b.pfull[x]));
+            }
+            if (!live) break;
+            // the stream's part: [element / 8][row][8], so that a warp's stores are consecutive
+            const int n = stream_requests(a, w.w, x) * G, at = part_row(a, w.w, cta, x);
+            float l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            if (l != l && top == -INFINITY) top = 0.f;         // no number: not an empty part
+            if (i < n) a.stat[at + i] = make_float2(any ? top : -INFINITY, any ? l : 0.f);
+            if (any) {
+                live = wait_bar(bar(b.ofull[x]), o_phase, abort_flag);
+                if (!live) break;
+                o_phase ^= 1;
+                ptx::tc_fence_after();
+                float *to = a.o + (long long)at * D + i * 8;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t r[32];
+                    tmem_load(o_at + c, r);
+                    tmem_loaded(r);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (i >= n || c + 8 * k >= D) continue;
+                        float *y = to + (long long)(c / 8 + k) * n * 8;
+                        *reinterpret_cast<uint4 *>(y) = make_uint4(r[8 * k], r[8 * k + 1], r[8 * k + 2], r[8 * k + 3]);
+                        *reinterpret_cast<uint4 *>(y + 4) = make_uint4(r[8 * k + 4], r[8 * k + 5], r[8 * k + 6], r[8 * k + 7]);
+                    }
+                    __syncwarp();
+                }
+                ptx::tc_fence_before();
+            }
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------ keys, values and queries to shared memory
+        const int lw = warp - 8;                               // rows 32 lw .. of a tile are this warp's
+        const int pieces = D * ESZ / 16;
+        bool live = true, bad = false;
+        uint32_t waiting[S::LAG + 1];                          // barriers of the fillings on their way, the oldest first
+        int on_way = 0;
+        auto told = [&](uint32_t x) {                          // a filling has landed
+            fence_async();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(x);
+        };
+        auto sent = [&](uint32_t x) {
+            ptx::cp_async_commit();
+            if constexpr (FP8) {                               // (stored by this thread itself)
+                copies_left<0>();
+                told(x);
+            } else {
+#pragma unroll
+                for (int k = 0; k <= S::LAG; ++k)
+                    if (k == on_way) waiting[k] = x;
+                if (++on_way > S::LAG) {
+                    copies_left<S::LAG>();
+                    told(waiting[0]);
+#pragma unroll
+                    for (int k = 0; k < S::LAG; ++k) waiting[k] = waiting[k + 1];
+                    --on_way;
+                }
+            }
+        };
+        auto all_told = [&] {
+            copies_left<0>();
+#pragma unroll
+            for (int k = 0; k <= S::LAG; ++k)
+                if (k < on_way) told(waiting[k]);
+            on_way = 0;
+        };
+        int k_slot = 0, v_slot = 0;
+        unsigned k_phase = 1, v_phase = 1, q_phase = 1, seq = 0;
+        for (; live && w.more(); w.next()) {
+            // the queries: the block's rows, request by request
+            all_told();
+            live = wait_bar(bar(b.qempty), q_phase, abort_flag);
+            if (!live) break;
+            q_phase ^= 1;
+            const int q_pieces = D / 8, q_tiles = w.w.twin ? 1 : 2, tokens = p.tokens[w.g];
+            for (int x = 0; x < q_tiles; ++x) {
+                const int n = stream_requests(a, w.w, x), r0 = w.w.r0 + x * a.tile_req;
+                for (int e = lane; e < 32 * q_pieces; e += 32) {
+                    const int row = lw * 32 + e / q_pieces, piece = e % q_pieces, in = row / G, r = r0 + in;
+                    const bool real = in < n && length_of(a, r) >= tokens;
+                    const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q);
+                    if (real) src += r * a.q_stride + (long long)(w.w.hk * G + row - in * G) * D + piece * 8;
+                    copy16(q_at + x * TB + place_of(row, piece), src, real);
+                }
+            }
+            sent(bar(b.qfull));
+            const int32_t *table = a.kv.table + p.lead[w.g] * a.kv.table_stride;
+            const char *kb = reinterpret_cast<const char *>(a.kv.k) + w.w.hk * a.kv.head_stride * ESZ;
+            const char *vb = reinterpret_cast<const char *>(a.kv.v) + w.w.hk * a.kv.head_stride * ESZ;
+            auto page_of = [&](int t) {                        // of this lane's token of tile t
+                const int token = t * TT + lw * 32 + lane;
+                return t < w.t1 && token < tokens ? table[a.page_shift >= 0 ? token >> a.page_shift : token / a.kv.page_size] : -1;
+            };
+            auto place_in = [&](int t, int page) -> long long {
+                const int token = t * TT + lw * 32 + lane;
+                if (token >= tokens) return -1;
+                if (page < 0 || page >= a.kv.n_pages) {
+                    bad = true;
+                    return -1;
+                }
+                const int in = a.page_shift >= 0 ? token & (a.kv.page_size - 1) : token % a.kv.page_size;
+                return ((long long)page * a.kv.page_stride + (long long)in * a.kv.token_stride) * ESZ;
+            };
+            auto fill = [&](uint32_t slot, const char *from, long long place) {
+                if constexpr (FP8) {
+#pragma unroll 8
+                    for (int e = lane; e < 32 * pieces; e += 32) {
+                        const int row = e / pieces, piece = e - row * pieces;
+                        const long long at = __shfl_sync(ALL, place, row);
+                        uint4 y = make_uint4(0, 0, 0, 0);
+                        if (at >= 0) y = *reinterpret_cast<const uint4 *>(from + at + piece * 16);
+                        const uint32_t word[4] = {y.x, y.y, y.z, y.w};
+                        uint32_t out[8];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) out[2 * k] = to_bf16(word[k] & 0xffffu), out[2 * k + 1] = to_bf16(word[k] >> 16);
+                        sts16(slot + place_of(lw * 32 + row, 2 * piece), make_uint4(out[0], out[1], out[2], out[3]));
+                        sts16(slot + place_of(lw * 32 + row, 2 * piece + 1), make_uint4(out[4], out[5], out[6], out[7]));
+                    }
+                } else {
+#pragma unroll 8
+                    for (int e = lane; e < 32 * pieces; e += 32) {
+                        const int row = e / pieces, piece = e - row * pieces;
+                        const long long at = __shfl_sync(ALL, place, row);
+                        copy16(slot + place_of(lw * 32 + row, piece), at >= 0 ? from + at + piece * 16 : from, at >= 0);
+                    }
+                }
+            };
+            // keys run one tile ahead of values
+            long long now = -1;
+            int page = page_of(w.t0);
+            for (int t = w.t0; t <= w.t1; ++t) {
+                const long long before = now;
+                const int next_page = page_of(t + 1);
+                if (t < w.t1) {
+                    now = place_in(t, page);
+                    live = wait_bar(bar(b.kempty[k_slot]), k_phase, abort_flag);
+                    if (!live) break;
+                    const unsigned ok = __ballot_sync(ALL, now >= 0);
+                    if (lane == 0) *(volatile unsigned *)&b.ok[seq % OK_RING][lw] = ok;
+                    ++seq;
+                    fill(k_at + k_slot * TB, kb, now);
+                    sent(bar(b.kfull[k_slot]));
+                    if (++k_slot == SLOTS) k_slot = 0, k_phase ^= 1;
+                }
+                if (t > w.t0) {
+                    live = wait_bar(bar(b.vempty[v_slot]), v_phase, abort_flag);
+                    if (!live) break;
+                    fill(v_at + v_slot * TB, vb, before);
+                    sent(bar(b.vfull[v_slot]));
+                    if (++v_slot == SLOTS) v_slot = 0, v_phase ^= 1;
+                }
+                page = next_page;
+            }
+        }
+        all_told();
+        if (__any_sync(ALL, bad) && lane == 0) atomicOr(a.status, STATUS_PAGES);
+    } else {
+        // ------------------------------------------------ the products, step by step: stream s & 1 takes step s
+        constexpr uint32_t QK = instr_desc(TT, false), PV = instr_desc(DC, true);
+        int k_slot = 0, v_slot = 0;
+        unsigned k_phase = 0, v_phase = 0, q_phase = 0, p_phase[2] = {0, 0};
+        bool live = true;
+        for (; live && w.more(); w.next()) {
+            const bool twin = w.w.twin;
+            const int n = w.t1 - w.t0, steps = twin ? n : 2 * n;
+            live = wait_bar(bar(b.qfull), q_phase, abort_flag);
+            if (!live) break;
+            q_phase ^= 1;
+            auto scores = [&](int s) {
+                const int x = s & 1;
+                if (twin || x == 0) {
+                    live = wait_bar(bar(b.kfull[k_slot]), k_phase, abort_flag);
+                    if (!live) return;
+                }
+                if (lane == 0) {
+                    ptx::tc_fence_after();
+                    const uint32_t qa = q_at + (twin ? 0 : x) * TB, ka = k_at + k_slot * TB;
+#pragma unroll
+                    for (int k = 0; k < DC / 16; ++k) {
+                        const uint32_t off = (k / 4) * SLAB + (k % 4) * 32;
+                        ptx::mma_bf16(tmem + S_COL + x * TT, slab_desc(qa + off, 16), slab_desc(ka + off, 16), QK, k > 0);
+                    }
+                    ptx::mma_commit(bar(b.sfull[x]));
+                    if (twin || x == 1) ptx::mma_commit(bar(b.kempty[k_slot]));
+                    if (s == steps - 1) ptx::mma_commit(bar(b.qempty));
+                }
+                __syncwarp();
+                if ((twin || x == 1) && ++k_slot == SLOTS) k_slot = 0, k_phase ^= 1;
+            };
+            scores(0);
+            if (live && steps > 1) scores(1);
+            for (int s = 0; live && s < steps; ++s) {
+                const int x = s & 1;
+                live = wait_bar(bar(b.pfull[x]), p_phase[x], abort_flag);
+                if (!live) break;
+                p_phase[x] ^= 1;
+                if (twin || x == 0) {
+                    live = wait_bar(bar(b.vfull[v_slot]), v_phase, abort_flag);
+                    if (!live) break;
+                }
+                if (lane == 0) {
+                    ptx::tc_fence_after();
+                    const uint32_t va = v_at + v_slot * TB, pa = tmem + S_COL + x * TT, oa = tmem + O_COL + x * DC;
+#pragma unroll
+                    for (int k = 0; k < TT / 16; ++k) {
+                        const uint64_t vd = slab_desc(va + k * 2048, SLAB);
+                        const uint32_t col = pa + (k / 2) * 32 + (k % 2) * 8;
+                        mma_bf16_ta(oa, col, vd, PV, s > 1 || k > 0);
+                        mma_bf16_ta(oa, col + 16, vd, PV, 1);
+                    }
+                    if (twin || x == 1) ptx::mma_commit(bar(b.vempty[v_slot]));
+                    if (s + 2 >= steps) ptx::mma_commit(bar(b.ofull[x]));
+                }
+                __syncwarp();
+                if ((twin || x == 1) && ++v_slot == SLOTS) v_slot = 0, v_phase ^= 1;
+                if (s + 2 < steps) scores(s + 2);
+            }
+        }
+        // nothing may be under way when tensor and shared memory are given back
+        if (lane == 0) ptx::mma_commit(bar(b.drain));
+        __syncwarp();
+        const uint64_t t_end = ptx::globaltimer();
+        while (!__all_sync(ALL, ptx::mbar_try_wait(bar(b.drain), 0)) && __all_sync(ALL, ptx::globaltimer() - t_end < WAIT_NS)) {}
+        ptx::tc_fence_before();
+    }
+    __syncthreads();
+    if (b.abort && tid == 0) atomicOr(a.status, STATUS_TIMEOUT);
+    if (warp == 12) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <bool FP8, int DC>
+cudaError_t launch_shape(const SharedArgs &a, int num_sms, cudaStream_t st) {
+    using S = Shape<FP8, DC>;
+    static std::atomic<unsigned long long> done{0};
+    const auto kernel = shared_kernel<FP8, DC>;
+    const cudaError_t e = allow_max_dynamic_smem(kernel, done);
+    if (e != cudaSuccess) return e;
+    return launch_chained(kernel, num_sms, THREADS, S::SMEM, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_shared(const SharedArgs &a, int num_sms, cudaStream_t st) {
+    const bool wide = a.kv.dim > 64;
+    if (a.kv.dtype == KV_E4M3) return wide ? launch_shape<true, 128>(a, num_sms, st) : launch_shape<true, 64>(a, num_sms, st);
+    return wide ? launch_shape<false, 128>(a, num_sms, st) : launch_shape<false, 64>(a, num_sms, st);
+}
+
+}  // namespace scute

@@ -135,8 +135,24 @@ scute_status append(scute_ctx *c, const scute_kv_cache *kv, const int32_t *slot_
     return SCUTE_OK;
 }
 
-// scute_paged_attention, and with sinks scute_paged_attention_sinks.
-scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attention *t, int32_t sinks, void *stream) {
+// The parts of scute_shared's workspace, and its bytes (-1: too large).
+struct SharedWork {
+    int64_t piece, stat, o, bytes;
+};
+SharedWork shared_work(int64_t n_req, int64_t q_heads, int64_t kv_heads, int64_t dim, int num_sms) {
+    const int64_t rows = shared_rows(n_req, q_heads, num_sms);
+    SharedWork w;
+    w.piece = (4 * n_req + 15) / 16 * 16;
+    w.stat = w.piece + 16 * n_req * kv_heads;
+    w.o = w.stat + 8 * rows;
+    w.bytes = rows > 0x7fffffff ? -1 : w.o + 4 * rows * dim;
+    return w;
+}
+
+// scute_paged_attention, with sinks scute_paged_attention_sinks, with `sh`
+// scute_paged_attention_shared.
+scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attention *t, int32_t sinks, const scute_shared *sh,
+                    void *stream) {
     if (!t) return fail(c, SCUTE_ERR_ARG, "null argument");
     AttendArgs a{};
     scute_status s = check_cache(c, kv, &a.kv);
@@ -156,6 +172,17 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
     if (!std::isfinite(t->scale) || !std::isfinite(t->softcap) || t->softcap < 0.f || t->window < 0)
         return fail(c, SCUTE_ERR_ARG, "bad scale, softcap or window");
     if (sinks < 0 || sinks > (1 << 30)) return fail(c, SCUTE_ERR_ARG, "sinks = %d outside 0..2^30", sinks);
+    SharedWork w{};
+    if (sh) {
+        if (t->window != 0) return fail(c, SCUTE_ERR_ARG, "shared beginnings with a window");
+        if (sh->n_groups < 0 || sh->n_groups > SCUTE_MAX_GROUPS)
+            return fail(c, SCUTE_ERR_ARG, "n_groups = %d outside 0..%d", sh->n_groups, SCUTE_MAX_GROUPS);
+        w = shared_work(t->n_req, t->q_heads, kv->kv_heads, kv->head_dim, c->num_sms);
+        if (w.bytes < 0 || sh->work_bytes < w.bytes)
+            return fail(c, SCUTE_ERR_ARG, "a workspace of %lld bytes, %lld needed", (long long)sh->work_bytes, (long long)w.bytes);
+        if (t->n_req > 0 && sh->n_groups > 0 && (!sh->start || !sh->len || !sh->work)) return fail(c, SCUTE_ERR_ARG, "null argument");
+        if (!aligned(sh->work, 16)) return fail(c, SCUTE_ERR_ARG, "the workspace must be 16-byte aligned");
+    }
     if (t->n_req == 0) return SCUTE_OK;
     if (!t->q || !t->out || !t->kv_len || !kv->block_table) return fail(c, SCUTE_ERR_ARG, "null argument");
     if (!aligned(t->q, 16) || !aligned(t->out, 16)) return fail(c, SCUTE_ERR_ARG, "q and out must be 16-byte aligned");
@@ -180,8 +207,43 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
     a.status = c->d_status;
     a.hold = c->inject_attend ? 1 : 0;
     c->inject_attend = false;
+    // by type and size: heads that the shared kernel's tiles hold (its sums are those of
+    // 16-bit products, and 128 elements and rows are what its tensor memory takes)
+    const bool together = sh && sh->n_groups > 0 && kv->dtype != SCUTE_KV_FP32 && kv->head_dim <= SHARED_MAX_DIM &&
+                          a.group <= SHARED_MAX_GROUP_HEADS;
+    SharedArgs b{};
+    if (together) {
+        char *work = static_cast<char *>(sh->work);
+        b.kv = a.kv;
+        b.q = a.q;
+        b.q_stride = a.q_stride;
+        b.kv_len = a.kv_len;
+        b.n_req = a.n_req;
+        b.group = a.group;
+        b.tile_req = 128 / a.group;
+        b.scale = a.scale;
+        b.softcap = a.softcap;
+        b.page_shift = a.page_shift;
+        b.start = sh->start;
+        b.len = sh->len;
+        b.n_groups = sh->n_groups;
+        b.first = reinterpret_cast<int *>(work);
+        b.piece = reinterpret_cast<int4 *>(work + w.piece);
+        b.stat = reinterpret_cast<float2 *>(work + w.stat);
+        b.o = reinterpret_cast<float *>(work + w.o);
+        b.status = a.status;
+        b.hold = a.hold;
+        a.first = b.first;
+        a.piece = b.piece;
+        a.stat = b.stat;
+        a.part_o = b.o;
+    }
     TimedLaunch tl{c, st};
     CU_TRY(c, tl.begin());
+    if (together) {
+        CU_TRY(c, launch_shared(b, c->num_sms, st));
+        count_launch(c, 1);
+    }
     CU_TRY(c, launch_attend(a, c->num_sms, st));
     count_launch(c, 1);
     CU_TRY(c, tl.end(SCUTE_KIND_ATTENTION));
@@ -386,13 +448,27 @@ scute_status scute_kv_copy(scute_ctx *c, const scute_kv_cache *caches, int n_cac
 
 scute_status scute_paged_attention(scute_ctx *c, const scute_kv_cache *kv, const scute_attention *t, void *stream) {
     if (!c) return SCUTE_ERR_ARG;
-    return attend(c, kv, t, 0, stream);
+    return attend(c, kv, t, 0, nullptr, stream);
 }
 
 scute_status scute_paged_attention_sinks(scute_ctx *c, const scute_kv_cache *kv, const scute_attention *t, int32_t sinks,
                                          void *stream) {
     if (!c) return SCUTE_ERR_ARG;
-    return attend(c, kv, t, sinks, stream);
+    return attend(c, kv, t, sinks, nullptr, stream);
+}
+
+scute_status scute_paged_attention_shared(scute_ctx *c, const scute_kv_cache *kv, const scute_attention *t, const scute_shared *s,
+                                          void *stream) {
+    if (!c) return SCUTE_ERR_ARG;
+    if (!s) return fail(c, SCUTE_ERR_ARG, "null argument");
+    return attend(c, kv, t, 0, s, stream);
+}
+
+int64_t scute_shared_bytes(const scute_ctx *c, int n_req, int q_heads, int kv_heads, int head_dim) {
+    if (!c || n_req < 0 || n_req > SCUTE_MAX_REQUESTS || kv_heads < 1 || q_heads < 1 || q_heads > (1 << 16) || q_heads % kv_heads ||
+        head_dim < 16 || head_dim > SCUTE_MAX_HEAD_DIM || head_dim % 16)
+        return -1;
+    return shared_work(n_req, q_heads, kv_heads, head_dim, c->num_sms).bytes;
 }
 
 scute_status scute_residual_norm(scute_ctx *c, const scute_norm *t, int64_t n, int d, void *stream) {
