@@ -593,9 +593,10 @@ scute_status scute_paged_attention_sinks(scute_ctx *ctx, const scute_kv_cache *k
  * result is that of scute_paged_attention, summed in another order.
  *   start       device int32 [n_groups + 1], not falling, 0..n_req; len device int32
  *               [n_groups], 0..table_cols * page_size.  What lies outside counts as the
- *               nearest inside and is recorded (SCUTE_ERR_PAGES);
+ *               nearest inside and is recorded (SCUTE_ERR_PAGES), as is a start that
+ *               falls, with which the groups' outputs are undefined;
  *   n_groups    0..SCUTE_MAX_GROUPS;
- *   work        device memory of at least scute_shared_bytes, 16-byte aligned, that
+ *   work        device memory of at least scute_shared_bytes, 32-byte aligned, that
  *               this call alone uses until it has ended; nothing in it needs to be set
  *               before, or is kept for the next call;
  *   a->window   must be 0.

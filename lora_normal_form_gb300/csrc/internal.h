@@ -481,11 +481,13 @@ struct AttendArgs {
     int *ctr;                  // arrivals at such a row (zero between launches)
     int *status;
     int hold;                  // 1: stages are never given back (test hook of the waits' end)
-    // of a batch whose groups share their contexts' beginnings (k_shared.cu): null, or
-    const int *first;          // [request] its first token of its own
-    const int4 *piece;         // [request][key/value head] the parts that hold its heads over those before
-    const float2 *stat;        // [row] a part's maximum and sum
-    const float *part_o;       // and its outputs
+    // of a batch whose groups share the beginnings of their contexts (k_shared.cu; null:
+    // none): a request's row begins behind them, and its outputs stay parts, row (request,
+    // head) of stat and part_o
+    const int32_t *start, *shared_len;
+    int n_groups;
+    float2 *stat;
+    float *part_o;
 };
 size_t attend_part_floats(int num_sms);
 int attend_ctrs(int num_sms);
@@ -494,11 +496,11 @@ cudaError_t launch_attend(const AttendArgs &a, int num_sms, cudaStream_t st);
 // ---------------------------------------------------------------- the beginning that a group's requests share
 constexpr int SHARED_MAX_GROUPS = 1024, SHARED_MAX_DIM = 128, SHARED_MAX_GROUP_HEADS = 128;
 constexpr int SHARED_TWIN = 1 << 30;
-// Parts: rows of (m, l) and of D outputs.  The heads of request r on key/value head h
-// have those of CTAs piece.x .. piece.y (SHARED_TWIN taken out; less than x: none): rows
-// piece.z + 256 CTA .. of piece.w & 0xffff rows, with SHARED_TWIN as many again directly
-// behind, the request's first head piece.w >> 16 of them; element d of row i at
-// (first row) D + d / 8 * rows * 8 + i * 8 + d % 8.
+// Parts: rows of (m, l) and of D outputs, the batch's own (request, head) first.  The heads
+// of request r on key/value head h have those of CTAs piece.x .. piece.y (SHARED_TWIN
+// taken out; -1: none): rows piece.z + 256 CTA .. of piece.w & 0xffff rows, with
+// SHARED_TWIN as many again directly behind, the request's first head the one at
+// piece.w >> 16 of them.
 struct SharedArgs {
     KvView kv;
     const void *q;
@@ -508,18 +510,55 @@ struct SharedArgs {
     int tile_req;              // requests of a stream's 128 rows
     float scale, softcap;
     int page_shift;
-    const int32_t *start, *len;
+    const int32_t *start, *shared_len;
     int n_groups;
-    int *first;
     int4 *piece;
     float2 *stat;
     float *o;
     int *status;
     int hold;
 };
+struct JoinArgs {
+    const int4 *piece;
+    const float2 *stat;
+    const float *o;
+    const float *v_scale;
+    void *out;                 // bf16
+    long long out_stride;
+    float *lse;
+    int rows, q_heads, group, dim;
+};
+#ifdef __CUDACC__
+// A request's length as it counts, a group's first request, and the group whose shared
+// tokens a request of `length` has (-1: none): both kernels ask the same questions of the
+// same numbers.
+template <typename Args>
+__device__ __forceinline__ int length_of(const Args &a, int r) {
+    const int cap = a.kv.table_cols * a.kv.page_size, n = a.kv_len[r];
+    return n < 0 ? 0 : n > cap ? cap : n;
+}
+template <typename Args>
+__device__ __forceinline__ int shared_start(const Args &a, int g) {
+    const int s = a.start[g];
+    return s < 0 ? 0 : s > a.n_req ? a.n_req : s;
+}
+template <typename Args>
+__device__ __forceinline__ int shared_group(const Args &a, int r, int length, int *tokens) {
+    int lo = 0, hi = a.n_groups - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (shared_start(a, mid) <= r) lo = mid;
+        else hi = mid - 1;
+    }
+    const int cap = a.kv.table_cols * a.kv.page_size, n = a.shared_len[lo];
+    *tokens = n > cap ? cap : n;
+    return n > 0 && length >= *tokens && shared_start(a, lo) <= r && r < shared_start(a, lo + 1) ? lo : -1;
+}
+#endif
 // rows of parts that a batch may need
-inline long long shared_rows(long long n_req, long long q_heads, int num_sms) { return 2 * n_req * q_heads + 256ll * num_sms; }
+inline long long shared_rows(long long n_req, long long q_heads, int num_sms) { return 3 * n_req * q_heads + 256ll * num_sms; }
 cudaError_t launch_shared(const SharedArgs &a, int num_sms, cudaStream_t st);
+cudaError_t launch_join(const JoinArgs &a, cudaStream_t st);
 
 // ---------------------------------------------------------------- norms around a sub-block
 struct NormArgs {

@@ -668,7 +668,8 @@ __device__ __forceinline__ void seen_of(const AttendArgs &a, int r, int *first, 
     n = n < 0 ? 0 : n > cap ? cap : n;
     *len = n;
     if constexpr (SHARED) {
-        *first = a.first[r];
+        int tokens;
+        *first = shared_group(a, r, n, &tokens) >= 0 ? tokens : 0;
     } else {
         const int f = a.window > 0 ? max(0, n - a.window) : 0;
         *first = f - min(f, a.sinks);
@@ -811,41 +812,12 @@ __device__ __forceinline__ void put(const AttendArgs &a, int r, int h, int d, fl
     }
 }
 
-// Take in what the requests of a group share: the parts of head h (of the request's on
-// key/value head hk) that k_shared.cu left, in the order of their CTAs, into this head's
-// maximum, sum and four outputs from d on.
-__device__ __forceinline__ void add_shared(const AttendArgs &a, int r, int hk, int h, int d, float &m, float &l, float4 &x) {
-    const int4 piece = a.piece[(long long)r * a.kv.heads + hk];
-    if (piece.y < 0) return;
-    const int twin = piece.y & SHARED_TWIN ? 1 : 0, n = piece.w & 0xffff, i = (piece.w >> 16) + h;
-    const int parts = ((piece.y & ~SHARED_TWIN) - piece.x + 1) << twin;
-    constexpr int B = 4;                  // parts at a time
-#pragma unroll 1
-    for (int k0 = 0; k0 < parts; k0 += B) {
-        float2 s[B];
-        float4 y[B];
-#pragma unroll
-        for (int k = 0; k < B; ++k) {
-            const int at = min(k0 + k, parts - 1);
-            const int row = piece.z + 256 * (piece.x + (at >> twin)) + (at & twin) * n;
-            s[k] = a.stat[row + i];
-            if (k0 + k >= parts) s[k].x = -INFINITY;
-            y[k] = *reinterpret_cast<const float4 *>(a.part_o + (long long)row * a.kv.dim + (d >> 3) * n * 8 + i * 8 + (d & 4));
-        }
-        float top = m;
-#pragma unroll
-        for (int k = 0; k < B; ++k) top = fmaxf(top, s[k].x);
-        const float ref = top == -INFINITY ? 0.f : top, f = exp2f(m - ref);
-        l *= f, x.x *= f, x.y *= f, x.z *= f, x.w *= f;
-        m = top;
-#pragma unroll
-        for (int k = 0; k < B; ++k) {
-            if (s[k].x == -INFINITY) continue;           // no token: its outputs are not written
-            const float g = exp2f(s[k].x - ref);
-            l += s[k].y * g;
-            x.x += y[k].x * g, x.y += y[k].y * g, x.z += y[k].z * g, x.w += y[k].w * g;
-        }
-    }
+// Or, of a batch with shared beginnings, the unnormalised outputs of the request's own
+// tokens, for launch_join.
+__device__ __forceinline__ void put_part(const AttendArgs &a, int r, int h, int d, float4 x, float m, float l) {
+    const long long row = (long long)r * a.q_heads + h;
+    *reinterpret_cast<float4 *>(a.part_o + row * a.kv.dim + d) = x;
+    if (d == 0) a.stat[row] = make_float2(m, l);
 }
 
 // A row that several CTAs share, as its joiner needs it.
@@ -953,7 +925,10 @@ __device__ __forceinline__ void join_parts(const AttendArgs &a, const SharedRow 
                 const int e = g0 + t + i * THREADS;
                 if (e >= items) break;
                 const int h = e / (D / 4), d = 4 * (e - h * (D / 4));
-                if constexpr (SHARED) add_shared(a, row.r, row.hk, row.h0 - row.hk * a.group + h, d, m[i], l[i], x[i]);
+                if constexpr (SHARED) {
+                    put_part(a, row.r, row.h0 + h, d, x[i], m[i], l[i]);
+                    continue;
+                }
                 put<IO>(a, row.r, row.h0 + h, d, x[i], l[i] == 0.f ? 0.f : vs / l[i]);
                 if (a.lse && d == 0) a.lse[(long long)row.r * a.q_heads + row.h0 + h] = (m[i] + log2f(l[i])) * LN2;
             }
@@ -1019,12 +994,17 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
     if (row_bytes < M::ROW)
         for (int i = threadIdx.x; i < stages * S::STAGE / 16; i += S::THREADS)
             reinterpret_cast<uint4 *>(s_ring)[i] = make_uint4(0, 0, 0, 0);
-    ptx::grid_dep_wait();
+    // (with shared beginnings the launch before is k_shared.cu's, which has waited for what
+    // this one reads: only this one's end waits for it, for launch_join's sake)
+    if constexpr (!SHARED) ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     plan_places<SHARED>(a, TT, places_at, s_warp);
     Walk<SHARED> w(a, places_at, HC, TT, MIN_TILES);
     const int cta = blockIdx.x;
-    if (cta >= w.ctas) return;
+    if (cta >= w.ctas) {
+        if constexpr (SHARED) ptx::grid_dep_wait();
+        return;
+    }
     w.open(cta);
 
     if (warp < PW) {
@@ -1178,6 +1158,7 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
         // nothing of this warp's may be on its way when the CTA ends
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (*s_abort && lane == 0) atomicOr(a.status, STATUS_TIMEOUT);
+        if constexpr (SHARED) ptx::grid_dep_wait();
         return;
     }
 
@@ -1246,11 +1227,7 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
             for (int i = t; i < nh * (D / 4); i += CW * 32) {
                 const int h = i / (D / 4), d = 4 * (i - h * (D / 4));
                 if constexpr (SHARED) {
-                    float m = s_top[h], l = s_sum[h];
-                    float4 x = merged(h, d);
-                    add_shared(a, w.r, w.hk, w.z * HC + h, d, m, l, x);
-                    put<IO>(a, w.r, h0 + h, d, x, l == 0.f ? 0.f : vs / l);
-                    if (a.lse && d == 0) a.lse[(long long)w.r * a.q_heads + h0 + h] = (m + log2f(l)) * LN2;
+                    put_part(a, w.r, h0 + h, d, merged(h, d), s_top[h], s_sum[h]);
                 } else {
                     put<IO>(a, w.r, h0 + h, d, merged(h, d), s_sum[h] == 0.f ? 0.f : vs / s_sum[h]);
                 }
@@ -1270,7 +1247,10 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
     // a fetching warp may have ended before the wait that ran out
     if (!live && lane == 0) atomicOr(a.status, STATUS_TIMEOUT);
     // arrive at the shared rows; the last to arrive joins
-    if (head.r < 0 && tail.r < 0) return;
+    if (head.r < 0 && tail.r < 0) {
+        if constexpr (SHARED) ptx::grid_dep_wait();
+        return;
+    }
     sync_threads<CW * 32>();
     if (t < 2) {
         const SharedRow &row = t ? tail : head;
@@ -1287,6 +1267,7 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
     const bool last_head = s_last[0], last_tail = s_last[1];
     if (last_head || last_tail)          // the ring is empty by now
         join_parts<IO, CW * 32, SHARED>(a, head, tail, last_head, last_tail, s_ring, stages * S::STAGE, t);
+    if constexpr (SHARED) ptx::grid_dep_wait();
 }
 
 template <typename M, int DC, int CW, int PW, int CTAS, bool SHARED = false>
@@ -1340,7 +1321,7 @@ cudaError_t launch_mma_128(const AttendArgs &a, int num_sms, cudaStream_t st) {
 template <bool FP8>
 cudaError_t launch_mma(const AttendArgs &a, int num_sms, cudaStream_t st) {
     if (a.kv.dim > 128) return launch_shape<MmaMath<FP8, 256, 1>, 256, 4, 2, 2>(a, num_sms, st);
-    return a.first ? launch_mma_128<FP8, true>(a, num_sms, st) : launch_mma_128<FP8, false>(a, num_sms, st);
+    return a.start ? launch_mma_128<FP8, true>(a, num_sms, st) : launch_mma_128<FP8, false>(a, num_sms, st);
 }
 // 32-bit caches, in the same way (group 4, 32 requests; 8 heads at a time spill 440
 // bytes with dim > 128, 100 with dim <= 64):

@@ -36,7 +36,7 @@ namespace scute {
 
 namespace {
 
-constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr int TT = 128;                    // tokens of a tile
 constexpr int TILE = 128;                  // rows of a stream's tile
 constexpr int SOFT = 256, LOAD = 128, THREADS = SOFT + LOAD + 32;
@@ -76,6 +76,11 @@ __device__ __forceinline__ void copies_left() { asm volatile("cp.async.wait_grou
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void sts16(uint32_t p, uint4 x) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+__device__ __forceinline__ void store32(float *p, const uint32_t *x) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+                 "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
 }
 __device__ __forceinline__ float pow2(float x) {
     float y;
@@ -160,15 +165,12 @@ constexpr uint32_t instr_desc(int n, bool across) {
 
 // ---------------------------------------------------------------- the plan
 // Groups, made by every CTA for itself: requests start[g] .. start[g + 1), the tokens
-// they share, the first request that has them all (whose row of the table is read), and
-// the places of the groups before.  A group of fewer than two such requests is left to
-// the one-token attention.
+// they share, the first request that has them all (whose row of the table is read; no
+// such request: no places), and the places of the groups before.
 struct Plan {
     int start[SHARED_MAX_GROUPS + 1], tokens[SHARED_MAX_GROUPS], lead[SHARED_MAX_GROUPS];
-    int busy[SHARED_MAX_GROUPS];
     long long at[SHARED_MAX_GROUPS + 1];
     long long warp_sum[THREADS / 32];
-    int warp_max[THREADS / 32];
 };
 struct Bars {
     uint64_t kfull[4], kempty[4], vfull[4], vempty[4], qfull, qempty, sfull[2], pfull[2], ofull[2], drain;
@@ -177,22 +179,8 @@ struct Bars {
     unsigned ok[OK_RING][TT / 32];         // tokens that count, of the last tiles' keys
 };
 
-__device__ __forceinline__ int length_of(const SharedArgs &a, int r) {
-    const int cap = a.kv.table_cols * a.kv.page_size, n = a.kv_len[r];
-    return n < 0 ? 0 : n > cap ? cap : n;
-}
-// The last group that begins at request r or before (its start is at most r).
-__device__ __forceinline__ int group_of(const Plan &p, int n_groups, int r) {
-    int lo = 0, hi = n_groups - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.start[mid] <= r) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
 __device__ __forceinline__ int requests_of(const Plan &p, int g) { return p.start[g + 1] - p.start[g]; }
-__device__ __forceinline__ int tiles_of(const Plan &p, int g) { return p.busy[g] < 2 ? 0 : (p.tokens[g] + TT - 1) / TT; }
+__device__ __forceinline__ int tiles_of(const Plan &p, int g) { return p.lead[g] == INT32_MAX ? 0 : (p.tokens[g] + TT - 1) / TT; }
 __device__ __forceinline__ int blocks_of(const SharedArgs &a, const Plan &p, int g) {
     return (requests_of(p, g) + 2 * a.tile_req - 1) / (2 * a.tile_req);
 }
@@ -202,50 +190,26 @@ __device__ __forceinline__ void make_plan(const SharedArgs &a, Plan &p) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, G = a.n_groups;
     const int cap = a.kv.table_cols * a.kv.page_size;
     bool bad = false;
-    // starts that do not fall (a running maximum), inside the batch
-    int s[3], top = 0;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        const int g = 3 * t + i;
-        s[i] = g <= G ? a.start[g] : 0;
-        if (s[i] < 0 || s[i] > a.n_req) bad = true;
-        s[i] = min(max(s[i], 0), a.n_req);
-        top = max(top, s[i]);
-    }
-    int run = top;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(ALL, run, o);
-        if (lane >= o) run = max(run, y);
-    }
-    if (lane == 31) p.warp_max[warp] = run;
-    int before = __shfl_up_sync(ALL, run, 1);
-    if (lane == 0) before = 0;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) before = max(before, p.warp_max[w]);
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         const int g = 3 * t + i;
         if (g > G) break;
-        if (s[i] < before) bad = true;
-        before = max(before, s[i]);
-        p.start[g] = before;
+        const int s = shared_start(a, g);
+        bad |= s != a.start[g] || (g < G && shared_start(a, g + 1) < s);
+        p.start[g] = s;
         if (g == G) break;
-        const int n = a.len[g];
-        if (n < 0 || n > cap) bad = true;
+        const int n = a.shared_len[g];
+        bad |= n < 0 || n > cap;
         p.tokens[g] = min(max(n, 0), cap);
         p.lead[g] = INT32_MAX;
-        p.busy[g] = 0;
     }
     __syncthreads();
-    for (int r = p.start[0] + t; r < p.start[G]; r += THREADS) {
+    for (int r = t; r < a.n_req; r += THREADS) {
         const int n = a.kv_len[r];
-        if (n < 0 || n > cap) bad = true;
-        const int g = group_of(p, G, r);
-        if (p.tokens[g] > 0 && length_of(a, r) >= p.tokens[g]) {
-            atomicMin(&p.lead[g], r);
-            atomicAdd(&p.busy[g], 1);
-        }
+        bad |= n < 0 || n > cap;
+        int tokens;
+        const int g = shared_group(a, r, length_of(a, r), &tokens);
+        if (g >= 0) atomicMin(&p.lead[g], r);
     }
     if (bad && blockIdx.x == 0) atomicOr(a.status, STATUS_PAGES);
     __syncthreads();
@@ -306,7 +270,7 @@ __device__ __forceinline__ WorkRow work_row(const SharedArgs &a, const Plan &p, 
     w.requests = min(2 * a.tile_req, all - b * 2 * a.tile_req);
     w.twin = w.requests <= a.tile_req;
     // twice a row's room: a twin's streams each leave all of the rows
-    w.first_row = 2 * a.group * (p.start[g] * a.kv.heads + w.hk * all + b * 2 * a.tile_req);
+    w.first_row = a.n_req * a.kv.heads * a.group + 2 * a.group * (p.start[g] * a.kv.heads + w.hk * all + b * 2 * a.tile_req);
     return w;
 }
 __device__ __forceinline__ int stream_requests(const SharedArgs &a, const WorkRow &w, int x) {
@@ -367,12 +331,11 @@ __device__ __forceinline__ void write_pieces(const SharedArgs &a, const Plan &p,
     for (long long i = (long long)blockIdx.x * THREADS + threadIdx.x; i < (long long)a.n_req * H; i += (long long)gridDim.x * THREADS) {
         const int r = (int)(i / H), hk = (int)(i - (long long)r * H);
         int4 piece = make_int4(0, -1, 0, 0);
-        int first = 0;
-        if (r >= p.start[0] && r < p.start[a.n_groups]) {
-            const int g = group_of(p, a.n_groups, r), tiles = tiles_of(p, g);
-            if (tiles && length_of(a, r) >= p.tokens[g]) {
-                first = p.tokens[g];
-                const int b = (r - p.start[g]) / (2 * a.tile_req), blocks = blocks_of(a, p, g);
+        {
+            int tokens;
+            const int g = shared_group(a, r, length_of(a, r), &tokens);
+            if (g >= 0) {
+                const int tiles = tiles_of(p, g), b = (r - p.start[g]) / (2 * a.tile_req), blocks = blocks_of(a, p, g);
                 const int row = hk * blocks + b;
                 const WorkRow w = work_row(a, p, g, row);
                 const int x = !w.twin && r - w.r0 >= a.tile_req;
@@ -384,7 +347,6 @@ __device__ __forceinline__ void write_pieces(const SharedArgs &a, const Plan &p,
             }
         }
         a.piece[i] = piece;
-        if (hk == 0) a.first[r] = first;
     }
 }
 
@@ -399,7 +361,7 @@ struct Shape {
 };
 
 template <bool FP8, int DC>
-__global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) {
+__global__ void __launch_bounds__(THREADS) shared_kernel(const SharedArgs a) {
     using S = Shape<FP8, DC>;
     constexpr int SLOTS = S::SLOTS, TB = S::TILE_BYTES, ESZ = FP8 ? 1 : 2;
     constexpr int S_COL = 0, O_COL = 2 * TT;                   // columns of tensor memory
@@ -551,7 +513,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                 if (lane == 0) ptx::mbar_arrive(bar(b.pfull[x]));
             }
             if (!live) break;
-            // the stream's part: [element / 8][row][8], so that a warp's stores are consecutive
+            // the stream's part, 32 bytes of a row at a time
             const int n = stream_requests(a, w.w, x) * G, at = part_row(a, w.w, cta, x);
             float l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
             if (l != l && top == -INFINITY) top = 0.f;         // no number: not an empty part
@@ -561,7 +523,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                 if (!live) break;
                 o_phase ^= 1;
                 ptx::tc_fence_after();
-                float *to = a.o + (long long)at * D + i * 8;
+                float *to = a.o + (long long)(at + i) * D;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t r[32];
@@ -569,10 +531,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                     tmem_loaded(r);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        if (i >= n || c + 8 * k >= D) continue;
-                        float *y = to + (long long)(c / 8 + k) * n * 8;
-                        *reinterpret_cast<uint4 *>(y) = make_uint4(r[8 * k], r[8 * k + 1], r[8 * k + 2], r[8 * k + 3]);
-                        *reinterpret_cast<uint4 *>(y + 4) = make_uint4(r[8 * k + 4], r[8 * k + 5], r[8 * k + 6], r[8 * k + 7]);
+                        if (i < n && c + 8 * k < D) store32(to + c + 8 * k, &r[8 * k]);
                     }
                     __syncwarp();
                 }
@@ -582,7 +541,14 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
     } else if (warp < 12) {
         // ------------------------------------------------ keys, values and queries to shared memory
         const int lw = warp - 8;                               // rows 32 lw .. of a tile are this warp's
-        const int pieces = D * ESZ / 16;
+        // lanes of a row, rows of an instruction; a lane keeps its 16-byte piece
+        constexpr int LR = DC * ESZ / 16, RI = 32 / LR, INSTR = 32 / RI;
+        const int piece = lane % LR, row0 = lane / LR;
+        const bool here = piece * 16 < D * ESZ;                // the others' pieces are zero for good
+        const long long tok_bytes = a.kv.token_stride * ESZ;
+        const uint32_t lane_at = place_of(lw * 32 + row0, FP8 ? 2 * piece : piece);
+        // row n RI + row0 lies n RI rows from row0's place, but for the permutation
+        auto row_at = [&](int n) { return n * RI * 128 + (lane_at ^ (((n * RI) & 7) << 4)); };
         bool live = true, bad = false;
         uint32_t waiting[S::LAG + 1];                          // barriers of the fillings on their way, the oldest first
         int on_way = 0;
@@ -628,11 +594,11 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
             for (int x = 0; x < q_tiles; ++x) {
                 const int n = stream_requests(a, w.w, x), r0 = w.w.r0 + x * a.tile_req;
                 for (int e = lane; e < 32 * q_pieces; e += 32) {
-                    const int row = lw * 32 + e / q_pieces, piece = e % q_pieces, in = row / G, r = r0 + in;
+                    const int row = lw * 32 + e / q_pieces, q_piece = e % q_pieces, in = row / G, r = r0 + in;
                     const bool real = in < n && length_of(a, r) >= tokens;
                     const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q);
-                    if (real) src += r * a.q_stride + (long long)(w.w.hk * G + row - in * G) * D + piece * 8;
-                    copy16(q_at + x * TB + place_of(row, piece), src, real);
+                    if (real) src += r * a.q_stride + (long long)(w.w.hk * G + row - in * G) * D + q_piece * 8;
+                    copy16(q_at + x * TB + place_of(row, q_piece), src, real);
                 }
             }
             sent(bar(b.qfull));
@@ -653,55 +619,103 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                 const int in = a.page_shift >= 0 ? token & (a.kv.page_size - 1) : token % a.kv.page_size;
                 return ((long long)page * a.kv.page_stride + (long long)in * a.kv.token_stride) * ESZ;
             };
-            auto fill = [&](uint32_t slot, const char *from, long long place) {
-                if constexpr (FP8) {
-#pragma unroll 8
-                    for (int e = lane; e < 32 * pieces; e += 32) {
-                        const int row = e / pieces, piece = e - row * pieces;
-                        const long long at = __shfl_sync(ALL, place, row);
-                        uint4 y = make_uint4(0, 0, 0, 0);
-                        if (at >= 0) y = *reinterpret_cast<const uint4 *>(from + at + piece * 16);
-                        const uint32_t word[4] = {y.x, y.y, y.z, y.w};
-                        uint32_t out[8];
+            // the tile's rows: every lane's own, and whether its halves of 16 step by the
+            // token's stride (they lie in one page)
+            struct Rows {
+                long long place;
+                unsigned steps;
+            };
+            auto rows_of = [&](int t, int page) {
+                Rows y;
+                y.place = place_in(t, page);
+                y.steps = 0;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) out[2 * k] = to_bf16(word[k] & 0xffffu), out[2 * k + 1] = to_bf16(word[k] >> 16);
-                        sts16(slot + place_of(lw * 32 + row, 2 * piece), make_uint4(out[0], out[1], out[2], out[3]));
-                        sts16(slot + place_of(lw * 32 + row, 2 * piece + 1), make_uint4(out[4], out[5], out[6], out[7]));
-                    }
-                } else {
-#pragma unroll 8
-                    for (int e = lane; e < 32 * pieces; e += 32) {
-                        const int row = e / pieces, piece = e - row * pieces;
-                        const long long at = __shfl_sync(ALL, place, row);
-                        copy16(slot + place_of(lw * 32 + row, piece), at >= 0 ? from + at + piece * 16 : from, at >= 0);
+                for (int f = 0; f < 32; f += 16) {
+                    const long long p0 = __shfl_sync(ALL, y.place, f);
+                    if (__all_sync(ALL, (lane & 16) != f || (y.place >= 0 && y.place == p0 + (lane - f) * tok_bytes))) y.steps |= 1u << (f / 16);
+                }
+                return y;
+            };
+            // do(n, source) of every instruction, source null for tokens that do not count
+            auto each = [&](const Rows &y, const char *from, auto &&go) {
+#pragma unroll
+                for (int f = 0; f < 32; f += 16) {
+                    constexpr int N = 16 / RI;
+                    if (y.steps >> (f / 16) & 1) {
+                        const char *src = from + __shfl_sync(ALL, y.place, f) + row0 * tok_bytes + piece * 16;
+#pragma unroll
+                        for (int n = 0; n < N; ++n) {
+                            go(f / RI + n, src);
+                            src += RI * tok_bytes;
+                        }
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < N; ++n) {
+                            const long long at = __shfl_sync(ALL, y.place, f + n * RI + row0);
+                            go(f / RI + n, at >= 0 ? from + at + piece * 16 : nullptr);
+                        }
                     }
                 }
             };
-            // keys run one tile ahead of values
-            long long now = -1;
-            int page = page_of(w.t0);
+            auto copy = [&](uint32_t slot, const char *from, const Rows &y) {       // 16-bit rows, asynchronously
+                each(y, from, [&](int n, const char *src) {
+                    if (here) copy16(slot + row_at(n), src ? src : from, src != nullptr);
+                });
+            };
+            auto fetch = [&](uint4 (&x)[INSTR], const char *from, const Rows &y) {  // 8-bit rows, through registers
+                each(y, from, [&](int n, const char *src) {
+                    x[n] = make_uint4(0, 0, 0, 0);
+                    if (here && src) x[n] = *reinterpret_cast<const uint4 *>(src);
+                });
+            };
+            auto store = [&](uint32_t slot, const uint4 (&x)[INSTR]) {
+#pragma unroll
+                for (int n = 0; n < INSTR; ++n) {
+                    const uint32_t word[4] = {x[n].x, x[n].y, x[n].z, x[n].w}, at = slot + row_at(n);
+                    uint32_t out[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) out[2 * k] = to_bf16(word[k] & 0xffffu), out[2 * k + 1] = to_bf16(word[k] >> 16);
+                    if (!here) continue;
+                    sts16(at, make_uint4(out[0], out[1], out[2], out[3]));
+                    sts16(at ^ 16, make_uint4(out[4], out[5], out[6], out[7]));
+                }
+            };
+            // keys run one tile ahead of values; 8-bit ones are on their way while those
+            // before are waited for and stored
+            Rows now = rows_of(w.t0, page_of(w.t0)), before = now;
+            int page = page_of(w.t0 + 1);
+            uint4 kx[FP8 ? INSTR : 1], vx[FP8 ? INSTR : 1];
+            if constexpr (FP8) fetch(kx, kb, now);
             for (int t = w.t0; t <= w.t1; ++t) {
-                const long long before = now;
-                const int next_page = page_of(t + 1);
+                if constexpr (FP8)
+                    if (t > w.t0) fetch(vx, vb, before);
                 if (t < w.t1) {
-                    now = place_in(t, page);
+                    const unsigned ok = __ballot_sync(ALL, now.place >= 0);
                     live = wait_bar(bar(b.kempty[k_slot]), k_phase, abort_flag);
                     if (!live) break;
-                    const unsigned ok = __ballot_sync(ALL, now >= 0);
                     if (lane == 0) *(volatile unsigned *)&b.ok[seq % OK_RING][lw] = ok;
                     ++seq;
-                    fill(k_at + k_slot * TB, kb, now);
+                    if constexpr (FP8) store(k_at + k_slot * TB, kx);
+                    else copy(k_at + k_slot * TB, kb, now);
                     sent(bar(b.kfull[k_slot]));
                     if (++k_slot == SLOTS) k_slot = 0, k_phase ^= 1;
+                }
+                Rows next = now;
+                if (t + 1 < w.t1) {
+                    next = rows_of(t + 1, page);
+                    page = page_of(t + 2);
+                    if constexpr (FP8) fetch(kx, kb, next);
                 }
                 if (t > w.t0) {
                     live = wait_bar(bar(b.vempty[v_slot]), v_phase, abort_flag);
                     if (!live) break;
-                    fill(v_at + v_slot * TB, vb, before);
+                    if constexpr (FP8) store(v_at + v_slot * TB, vx);
+                    else copy(v_at + v_slot * TB, vb, before);
                     sent(bar(b.vfull[v_slot]));
                     if (++v_slot == SLOTS) v_slot = 0, v_phase ^= 1;
                 }
-                page = next_page;
+                before = now;
+                now = next;
             }
         }
         all_told();
@@ -793,7 +807,85 @@ cudaError_t launch_shape(const SharedArgs &a, int num_sms, cudaStream_t st) {
     return launch_chained(kernel, num_sms, THREADS, S::SMEM, st, a);
 }
 
+// ---------------------------------------------------------------- the parts of a request's heads, joined
+// out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the parts of a head: that of
+// its own tokens, and those of the tokens its group shares, in the order of their CTAs.
+// JG threads share the parts of four elements, so that a part's loads do not wait for
+// another's; a head's parts are then added up in shared memory in a fixed order.
+constexpr int JOIN_THREADS = 256, JG = 8;
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const JoinArgs a) {
+    __shared__ float s_m[JOIN_THREADS], s_l[JOIN_THREADS];
+    __shared__ float4 s_o[JOIN_THREADS];
+    const int quads = a.dim / 4, per = JOIN_THREADS / (JG * quads), t = threadIdx.x;
+    const int in = t / (JG * quads), rest = t - in * JG * quads, part0 = rest / quads, d = (rest - part0 * quads) * 4;
+    const int row = blockIdx.x * per + in;
+    const bool real = in < per && row < a.rows;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    float m = -INFINITY, l = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int r = real ? row / a.q_heads : 0, h = row - r * a.q_heads, hk = h / a.group;
+    if (real) {
+        const int4 piece = a.piece[(long long)r * (a.q_heads / a.group) + hk];
+        const int twin = piece.y >= 0 && piece.y & SHARED_TWIN ? 1 : 0, n = piece.w & 0xffff, i = (piece.w >> 16) + h - hk * a.group;
+        const int parts = 1 + (piece.y < 0 ? 0 : ((piece.y & ~SHARED_TWIN) - piece.x + 1) << twin);
+        constexpr int B = 4;
+#pragma unroll 1
+        for (int k0 = part0; k0 < parts; k0 += JG * B) {
+            float2 s[B];
+            float4 y[B];
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                const int at = k0 + k * JG;
+                s[k] = make_float2(-INFINITY, 0.f);
+                if (at >= parts) continue;
+                // the head's own part is the first one
+                const int shared = at - 1;
+                const int from = at == 0 ? row : piece.z + 256 * (piece.x + (shared >> twin)) + (shared & twin) * n + i;
+                s[k] = a.stat[from];
+                y[k] = *reinterpret_cast<const float4 *>(a.o + (long long)from * a.dim + d);
+            }
+            float top = m;
+#pragma unroll
+            for (int k = 0; k < B; ++k) top = fmaxf(top, s[k].x);
+            const float ref = top == -INFINITY ? 0.f : top, f = pow2(m - ref);
+            l *= f, x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+            m = top;
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                if (s[k].x == -INFINITY) continue;           // no token: its outputs may hold anything
+                const float g = pow2(s[k].x - ref);
+                l += s[k].y * g;
+                x.x += y[k].x * g, x.y += y[k].y * g, x.z += y[k].z * g, x.w += y[k].w * g;
+            }
+        }
+    }
+    s_m[t] = m, s_l[t] = l, s_o[t] = x;
+    __syncthreads();
+    if (!real || part0 != 0) return;
+#pragma unroll
+    for (int k = 1; k < JG; ++k) m = fmaxf(m, s_m[t + k * quads]);
+    const float ref = m == -INFINITY ? 0.f : m, f = pow2(s_m[t] - ref);
+    l *= f, x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+#pragma unroll
+    for (int k = 1; k < JG; ++k) {
+        const float g = pow2(s_m[t + k * quads] - ref);
+        const float4 y = s_o[t + k * quads];
+        l += s_l[t + k * quads] * g;
+        x.x += y.x * g, x.y += y.y * g, x.z += y.z * g, x.w += y.w * g;
+    }
+    const float vs = a.v_scale ? a.v_scale[hk] : 1.f, div = l == 0.f ? 0.f : vs / l;
+    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) + r * a.out_stride + (long long)h * a.dim + d;
+    *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16(x.x * div, x.y * div), pack_bf16(x.z * div, x.w * div));
+    if (a.lse && d == 0) a.lse[row] = (m + log2f(l)) * LN2;
+}
+
 }  // namespace
+
+cudaError_t launch_join(const JoinArgs &a, cudaStream_t st) {
+    const int per = JOIN_THREADS / (JG * (a.dim / 4));
+    return launch_chained(join_kernel, (a.rows + per - 1) / per, JOIN_THREADS, 0, st, a);
+}
 
 cudaError_t launch_shared(const SharedArgs &a, int num_sms, cudaStream_t st) {
     const bool wide = a.kv.dim > 64;

@@ -142,9 +142,9 @@ struct SharedWork {
 SharedWork shared_work(int64_t n_req, int64_t q_heads, int64_t kv_heads, int64_t dim, int num_sms) {
     const int64_t rows = shared_rows(n_req, q_heads, num_sms);
     SharedWork w;
-    w.piece = (4 * n_req + 15) / 16 * 16;
+    w.piece = 0;
     w.stat = w.piece + 16 * n_req * kv_heads;
-    w.o = w.stat + 8 * rows;
+    w.o = (w.stat + 8 * rows + 31) / 32 * 32;
     w.bytes = rows > 0x7fffffff ? -1 : w.o + 4 * rows * dim;
     return w;
 }
@@ -181,7 +181,7 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
         if (w.bytes < 0 || sh->work_bytes < w.bytes)
             return fail(c, SCUTE_ERR_ARG, "a workspace of %lld bytes, %lld needed", (long long)sh->work_bytes, (long long)w.bytes);
         if (t->n_req > 0 && sh->n_groups > 0 && (!sh->start || !sh->len || !sh->work)) return fail(c, SCUTE_ERR_ARG, "null argument");
-        if (!aligned(sh->work, 16)) return fail(c, SCUTE_ERR_ARG, "the workspace must be 16-byte aligned");
+        if (!aligned(sh->work, 32)) return fail(c, SCUTE_ERR_ARG, "the workspace must be 32-byte aligned");
     }
     if (t->n_req == 0) return SCUTE_OK;
     if (!t->q || !t->out || !t->kv_len || !kv->block_table) return fail(c, SCUTE_ERR_ARG, "null argument");
@@ -224,19 +224,14 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
         b.scale = a.scale;
         b.softcap = a.softcap;
         b.page_shift = a.page_shift;
-        b.start = sh->start;
-        b.len = sh->len;
-        b.n_groups = sh->n_groups;
-        b.first = reinterpret_cast<int *>(work);
+        b.start = a.start = sh->start;
+        b.shared_len = a.shared_len = sh->len;
+        b.n_groups = a.n_groups = sh->n_groups;
         b.piece = reinterpret_cast<int4 *>(work + w.piece);
-        b.stat = reinterpret_cast<float2 *>(work + w.stat);
-        b.o = reinterpret_cast<float *>(work + w.o);
+        b.stat = a.stat = reinterpret_cast<float2 *>(work + w.stat);
+        b.o = a.part_o = reinterpret_cast<float *>(work + w.o);
         b.status = a.status;
         b.hold = a.hold;
-        a.first = b.first;
-        a.piece = b.piece;
-        a.stat = b.stat;
-        a.part_o = b.o;
     }
     TimedLaunch tl{c, st};
     CU_TRY(c, tl.begin());
@@ -246,6 +241,22 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
     }
     CU_TRY(c, launch_attend(a, c->num_sms, st));
     count_launch(c, 1);
+    if (together) {
+        JoinArgs j{};
+        j.piece = b.piece;
+        j.stat = b.stat;
+        j.o = b.o;
+        j.v_scale = kv->v_scale;
+        j.out = a.out;
+        j.out_stride = a.out_stride;
+        j.lse = a.lse;
+        j.rows = a.n_req * a.q_heads;
+        j.q_heads = a.q_heads;
+        j.group = a.group;
+        j.dim = kv->head_dim;
+        CU_TRY(c, launch_join(j, st));
+        count_launch(c, 1);
+    }
     CU_TRY(c, tl.end(SCUTE_KIND_ATTENTION));
     return SCUTE_OK;
 }
