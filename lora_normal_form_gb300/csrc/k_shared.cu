@@ -14,9 +14,9 @@
 //
 // Layout.  Work rows are (group, key/value head, up to 2 x 128 rows), their tiles of 128
 // tokens one sequence that is cut into equal contiguous ranges, one per CTA, as in
-// k_attend.cu.  In a CTA four warps bring keys and values to shared memory, each to a
-// ring of its own; one issues the products (tcgen05.mma); and two warpgroups each run
-// a stream of its own: scores in tensor memory, read back (a thread has a row), their
+// k_attend.cu.  In a CTA four warps bring keys and four values to shared memory, each to
+// a ring of its own, and two warpgroups each run a stream of its own: scores in tensor
+// memory (tcgen05.mma, issued by one of its threads), read back (a thread has a row), their
 // weights written over them, the second product from there, into outputs that stay in
 // tensor memory.  Up to 128 rows the streams take alternate tiles of the same rows, beyond
 // each takes 128 rows of every tile; either way one stream's products run under the
@@ -27,6 +27,8 @@
 // reference m moves only when a score passes it by more than 2^8, so that outputs are
 // seldom scaled.  Tokens behind the shared beginning's end are zero in shared memory and
 // their scores minus infinity.
+#include <type_traits>
+
 #include <cuda_fp8.h>
 
 #include "internal.h"
@@ -39,7 +41,7 @@ namespace {
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr int TT = 128;                    // tokens of a tile
 constexpr int TILE = 128;                  // rows of a stream's tile
-constexpr int SOFT = 256, LOAD = 128, THREADS = SOFT + LOAD + 32;
+constexpr int SOFT = 256, LOAD = 256, THREADS = SOFT + LOAD;
 constexpr int ROW_COST = 2;                // what a work row costs beside its tiles, in tiles
 constexpr int MIN_TILES = 2;               // of a range
 // Tiles whose tokens' marks are kept: a tile's are read by its softmax, which the keys
@@ -179,6 +181,16 @@ struct Bars {
     unsigned ok[OK_RING][TT / 32];         // tokens that count, of the last tiles' keys
 };
 
+// shared_group (internal.h) from the plan's copies.
+__device__ __forceinline__ int group_of(const SharedArgs &a, const Plan &p, int r, int length) {
+    int lo = 0, hi = a.n_groups - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.start[mid] <= r) lo = mid;
+        else hi = mid - 1;
+    }
+    return p.tokens[lo] > 0 && length >= p.tokens[lo] && p.start[lo] <= r && r < p.start[lo + 1] ? lo : -1;
+}
 __device__ __forceinline__ int requests_of(const Plan &p, int g) { return p.start[g + 1] - p.start[g]; }
 __device__ __forceinline__ int tiles_of(const Plan &p, int g) { return p.lead[g] == INT32_MAX ? 0 : (p.tokens[g] + TT - 1) / TT; }
 __device__ __forceinline__ int blocks_of(const SharedArgs &a, const Plan &p, int g) {
@@ -190,25 +202,28 @@ __device__ __forceinline__ void make_plan(const SharedArgs &a, Plan &p) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, G = a.n_groups;
     const int cap = a.kv.table_cols * a.kv.page_size;
     bool bad = false;
+    // (everything that is read is asked for at once)
+    int start[4], tokens[3], length = t < a.n_req ? a.kv_len[t] : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) start[i] = 3 * t + i <= G ? a.start[3 * t + i] : 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) tokens[i] = 3 * t + i < G ? a.shared_len[3 * t + i] : 0;
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         const int g = 3 * t + i;
         if (g > G) break;
-        const int s = shared_start(a, g);
-        bad |= s != a.start[g] || (g < G && shared_start(a, g + 1) < s);
-        p.start[g] = s;
+        bad |= start[i] < 0 || start[i] > a.n_req || (g < G && start[i + 1] < start[i]);
+        p.start[g] = min(max(start[i], 0), a.n_req);
         if (g == G) break;
-        const int n = a.shared_len[g];
-        bad |= n < 0 || n > cap;
-        p.tokens[g] = min(max(n, 0), cap);
+        bad |= tokens[i] < 0 || tokens[i] > cap;
+        p.tokens[g] = min(max(tokens[i], 0), cap);
         p.lead[g] = INT32_MAX;
     }
     __syncthreads();
     for (int r = t; r < a.n_req; r += THREADS) {
-        const int n = a.kv_len[r];
-        bad |= n < 0 || n > cap;
-        int tokens;
-        const int g = shared_group(a, r, length_of(a, r), &tokens);
+        if (r != t) length = a.kv_len[r];
+        bad |= length < 0 || length > cap;
+        const int g = group_of(a, p, r, min(max(length, 0), cap));
         if (g >= 0) atomicMin(&p.lead[g], r);
     }
     if (bad && blockIdx.x == 0) atomicOr(a.status, STATUS_PAGES);
@@ -289,6 +304,8 @@ struct Walk {
     int g, row, rows, tiles, t0, t1;
     WorkRow w;
     __device__ __forceinline__ Walk(const SharedArgs &args, const Plan &plan, const Cut &cut, int cta) : a(args), p(plan) {
+        base = end = g = row = rows = tiles = t0 = t1 = 0;
+        if (cta >= cut.ctas) return;
         const long long x = cut.start(cta);
         end = cut.start(cta + 1);
         g = 0;
@@ -328,12 +345,11 @@ struct Walk {
 // What the one-token attention needs of each request and key/value head.
 __device__ __forceinline__ void write_pieces(const SharedArgs &a, const Plan &p, const Cut &cut) {
     const int H = a.kv.heads;
-    for (long long i = (long long)blockIdx.x * THREADS + threadIdx.x; i < (long long)a.n_req * H; i += (long long)gridDim.x * THREADS) {
+    for (long long i = (long long)blockIdx.x * SOFT + threadIdx.x; i < (long long)a.n_req * H; i += (long long)gridDim.x * SOFT) {
         const int r = (int)(i / H), hk = (int)(i - (long long)r * H);
         int4 piece = make_int4(0, -1, 0, 0);
         {
-            int tokens;
-            const int g = shared_group(a, r, length_of(a, r), &tokens);
+            const int g = group_of(a, p, r, length_of(a, r));
             if (g >= 0) {
                 const int tiles = tiles_of(p, g), b = (r - p.start[g]) / (2 * a.tile_req), blocks = blocks_of(a, p, g);
                 const int row = hk * blocks + b;
@@ -355,13 +371,12 @@ template <bool FP8, int DC>
 struct Shape {
     static constexpr int SLABS = DC / 64, TILE_BYTES = SLABS * SLAB;
     static constexpr int SLOTS = DC == 64 ? 4 : 2;             // of keys, and of values
-    static constexpr int LAG = 2 * SLOTS - 2;                  // fillings on their way before the oldest is waited for
     static constexpr int SMEM = 1024 + (2 + 2 * SLOTS) * TILE_BYTES + (int)sizeof(Plan) + (int)sizeof(Bars) + 64;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 template <bool FP8, int DC>
-__global__ void __launch_bounds__(THREADS) shared_kernel(const SharedArgs a) {
+__global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) {
     using S = Shape<FP8, DC>;
     constexpr int SLOTS = S::SLOTS, TB = S::TILE_BYTES, ESZ = FP8 ? 1 : 2;
     constexpr int S_COL = 0, O_COL = 2 * TT;                   // columns of tensor memory
@@ -377,19 +392,19 @@ __global__ void __launch_bounds__(THREADS) shared_kernel(const SharedArgs a) {
     if (tid == 0) {
         b.abort = 0;
         for (int i = 0; i < SLOTS; ++i) {
-            ptx::mbar_init(bar(b.kfull[i]), LOAD / 32);
-            ptx::mbar_init(bar(b.kempty[i]), 1 + a.hold);
-            ptx::mbar_init(bar(b.vfull[i]), LOAD / 32);
-            ptx::mbar_init(bar(b.vempty[i]), 1);
+            ptx::mbar_init(bar(b.kfull[i]), 4);
+            ptx::mbar_init(bar(b.kempty[i]), 2 + a.hold);
+            ptx::mbar_init(bar(b.vfull[i]), 4);
+            ptx::mbar_init(bar(b.vempty[i]), 2);
         }
-        ptx::mbar_init(bar(b.qfull), LOAD / 32);
-        ptx::mbar_init(bar(b.qempty), 1);
+        ptx::mbar_init(bar(b.qfull), 8);
+        ptx::mbar_init(bar(b.qempty), 2);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(bar(b.sfull[i]), 1);
             ptx::mbar_init(bar(b.pfull[i]), 4);
             ptx::mbar_init(bar(b.ofull[i]), 1);
         }
-        ptx::mbar_init(bar(b.drain), 1);
+        ptx::mbar_init(bar(b.drain), 2);
         ptx::fence_mbar_init();
     }
     // behind a head's elements every row of a tile stays zero
@@ -397,45 +412,78 @@ __global__ void __launch_bounds__(THREADS) shared_kernel(const SharedArgs a) {
         for (int i = tid; i < (2 + 2 * SLOTS) * TB / 16; i += THREADS) sts16(q_at + i * 16, make_uint4(0, 0, 0, 0));
         fence_async();
     }
-    ptx::grid_dep_wait();
-    ptx::grid_dep_launch();
-    make_plan(a, p);
-    const Cut cut(a, p);
-    write_pieces(a, p, cut);
-    const int cta = blockIdx.x;
-    if (cta >= cut.ctas) return;
-    if (warp == 12) {
+    if (warp == 0) {
         ptx::tmem_alloc(ptx::smem_u32(&b.tmem), 512);
         ptx::tmem_relinquish();
         ptx::tc_fence_before();
     }
-    __syncthreads();
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    make_plan(a, p);                       // (its barriers order what was written above)
     ptx::tc_fence_after();
     const uint32_t tmem = b.tmem;
+    const Cut cut(a, p);
+    const int cta = blockIdx.x;
     Walk w(a, p, cut, cta);
 
-    if (warp < 8) {
-        // ------------------------------------------------ a stream's softmax: a thread has a row
+    if (warp < SOFT / 32) {
+        // ------------------------------------------------ a stream: its softmax, a thread to a row; its first
+        // warp issues its products
+        constexpr uint32_t QK = instr_desc(TT, false), PV = instr_desc(DC, true);
         const int x = warp >> 2, i = (warp & 3) * 32 + lane;
+        const bool issues = (warp & 3) == 0;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_at = tmem + S_COL + x * TT + lanes, o_at = tmem + O_COL + x * DC + lanes;
-        unsigned s_phase = 0, o_phase = 0, seq = 0;
-        bool live = true;
+        const uint32_t s_col = tmem + S_COL + x * TT, o_col = tmem + O_COL + x * DC, s_at = s_col + lanes, o_at = o_col + lanes;
+        unsigned s_phase = 0, o_phase = 0, p_phase = 0, q_phase = 0, seq = 0;      // seq: tiles of the CTA before this work row's
+        bool live = true, first_row = true;
         for (; live && w.more(); w.next()) {
+            const bool twin = w.w.twin;
+            const int step = twin ? 2 : 1, t_first = w.t0 + (twin ? x : 0), uses = twin ? 2 : 1;
+            // tile t's slot of a ring, and the parity of its filling
+            auto slot_of = [&](int t) { return (seq + (t - w.t0)) % SLOTS; };
+            auto phase_of = [&](int t) { return (seq + (t - w.t0)) / SLOTS & 1; };
+            // scores of the stream's tile t (its weights before have been multiplied: the
+            // products of one thread run in the order of their issue)
+            auto scores = [&](int t) {
+                const int slot = slot_of(t);
+                live = wait_bar(bar(b.kfull[slot]), phase_of(t), abort_flag);
+                if (!live) return;
+                if (lane == 0) {
+                    ptx::tc_fence_after();
+                    const uint64_t qd = slab_desc(q_at + (twin ? 0 : x) * TB, 16), kd = slab_desc(k_at + slot * TB, 16);
+#pragma unroll
+                    for (int k = 0; k < DC / 16; ++k) {
+                        const uint32_t off = ((k / 4) * SLAB + (k % 4) * 32) >> 4;
+                        ptx::mma_bf16(s_col, qd + off, kd + off, QK, k > 0);
+                    }
+                    ptx::mma_commit(bar(b.sfull[x]));
+                    for (int k = 0; k < uses; ++k) ptx::mma_commit(bar(b.kempty[slot]));
+                    if (t + step >= w.t1) ptx::mma_commit(bar(b.qempty));
+                }
+                __syncwarp();
+            };
+            if (issues) {
+                live = wait_bar(bar(b.qfull), q_phase, abort_flag);
+                if (!live) break;
+                q_phase ^= 1;
+                if (t_first < w.t1) scores(t_first);
+                else if (lane == 0) ptx::mbar_arrive(bar(b.qempty));
+                if (!live) break;
+            }
+            if (first_row) write_pieces(a, p, cut);            // while the first scores are on their way
+            first_row = false;
             const float scale = (a.kv.k_scale ? a.kv.k_scale[w.w.hk] : 1.f) * a.scale;
             const float mul = a.softcap > 0.f ? scale : scale * LOG2E;
             float top = -INFINITY, sum[4] = {0.f, 0.f, 0.f, 0.f};
             bool any = false;
-            const unsigned piece_seq = seq;
-            seq += w.t1 - w.t0;
-            for (int t = w.t0 + (w.w.twin ? x : 0); t < w.t1; t += w.w.twin ? 2 : 1) {
+            for (int t = t_first; t < w.t1; t += step) {
                 live = wait_bar(bar(b.sfull[x]), s_phase, abort_flag);
                 if (!live) break;
                 s_phase ^= 1;
                 ptx::tc_fence_after();
                 uint32_t r[32], r2[32];
                 float f = mul;
-                const volatile unsigned *ok = b.ok[(piece_seq + (t - w.t0)) % OK_RING];
+                const volatile unsigned *ok = b.ok[(seq + (t - w.t0)) % OK_RING];
                 if (a.softcap > 0.f || (ok[0] & ok[1] & ok[2] & ok[3]) != ALL) {     // scores as they count, put back
 #pragma unroll 1
                     for (int c = 0; c < TT / 32; ++c) {
@@ -485,6 +533,7 @@ __global__ void __launch_bounds__(THREADS) shared_kernel(const SharedArgs a) {
                         tmem_stored();
                     }
                 }
+                const bool adds = any;
                 any = true;
                 const float ref = top == -INFINITY ? 0.f : top;
                 tmem_load(s_at, r);
@@ -511,8 +560,33 @@ __global__ void __launch_bounds__(THREADS) shared_kernel(const SharedArgs a) {
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(bar(b.pfull[x]));
+                if (!issues) continue;
+                const int slot = slot_of(t);
+                live = wait_bar(bar(b.pfull[x]), p_phase, abort_flag) && wait_bar(bar(b.vfull[slot]), phase_of(t), abort_flag);
+                if (!live) break;
+                p_phase ^= 1;
+                if (lane == 0) {
+                    ptx::tc_fence_after();
+                    const uint64_t vd = slab_desc(v_at + slot * TB, SLAB);
+#pragma unroll
+                    for (int k = 0; k < TT / 16; ++k) {
+                        const uint32_t col = s_col + (k / 2) * 32 + (k % 2) * 8;
+                        mma_bf16_ta(o_col, col, vd + k * (2048 >> 4), PV, adds || k > 0);
+                        mma_bf16_ta(o_col, col + 16, vd + k * (2048 >> 4), PV, 1);
+                    }
+                    for (int k = 0; k < uses; ++k) ptx::mma_commit(bar(b.vempty[slot]));
+                    if (t + step >= w.t1) ptx::mma_commit(bar(b.ofull[x]));
+                }
+                __syncwarp();
+                if (t + step < w.t1) scores(t + step);
+                if (!live) break;
             }
             if (!live) break;
+            // the work row's last values have come, whichever stream's they are: a slot's
+            // parity tells only two fillings apart
+            if (issues) live = wait_bar(bar(b.vfull[slot_of(w.t1 - 1)]), phase_of(w.t1 - 1), abort_flag);
+            if (!live) break;
+            seq += w.t1 - w.t0;
             // the stream's part, 32 bytes of a row at a time
             const int n = stream_requests(a, w.w, x) * G, at = part_row(a, w.w, cta, x);
             float l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -538,9 +612,19 @@ __global__ void __launch_bounds__(THREADS) shared_kernel(const SharedArgs a) {
                 ptx::tc_fence_before();
             }
         }
-    } else if (warp < 12) {
-        // ------------------------------------------------ keys, values and queries to shared memory
-        const int lw = warp - 8;                               // rows 32 lw .. of a tile are this warp's
+        if (first_row) write_pieces(a, p, cut);
+        if (issues) {
+            // nothing may be under way when tensor and shared memory are given back
+            if (lane == 0) ptx::mma_commit(bar(b.drain));
+            __syncwarp();
+            const uint64_t t0 = ptx::globaltimer();
+            while (!__all_sync(ALL, ptx::mbar_try_wait(bar(b.drain), 0)) && __all_sync(ALL, ptx::globaltimer() - t0 < WAIT_NS)) {}
+        }
+        ptx::tc_fence_before();
+    } else {
+        // ------------------------------------------------ four warps bring keys, four values; each a tile of queries
+        const bool keys = warp < SOFT / 32 + 4;
+        const int lw = warp & 3;                               // rows 32 lw .. of a tile are this warp's
         // lanes of a row, rows of an instruction; a lane keeps its 16-byte piece
         constexpr int LR = DC * ESZ / 16, RI = 32 / LR, INSTR = 32 / RI;
         const int piece = lane % LR, row0 = lane / LR;
@@ -548,10 +632,13 @@ __global__ void __launch_bounds__(THREADS) shared_kernel(const SharedArgs a) {
         const long long tok_bytes = a.kv.token_stride * ESZ;
         const uint32_t lane_at = place_of(lw * 32 + row0, FP8 ? 2 * piece : piece);
         // row n RI + row0 lies n RI rows from row0's place, but for the permutation
-        auto row_at = [&](int n) { return n * RI * 128 + (lane_at ^ (((n * RI) & 7) << 4)); };
+        constexpr int TURNS = 8 / RI;
+        uint32_t turned[TURNS];
+#pragma unroll
+        for (int n = 0; n < TURNS; ++n) turned[n] = lane_at ^ (n * RI << 4);
+        auto row_at = [&](int n) { return turned[n % TURNS] + n * RI * 128; };
         bool live = true, bad = false;
-        uint32_t waiting[S::LAG + 1];                          // barriers of the fillings on their way, the oldest first
-        int on_way = 0;
+        uint32_t waiting = 0;                                  // the barrier of the filling on its way (0: none)
         auto told = [&](uint32_t x) {                          // a filling has landed
             fence_async();
             __syncwarp();
@@ -559,52 +646,47 @@ __global__ void __launch_bounds__(THREADS) shared_kernel(const SharedArgs a) {
         };
         auto sent = [&](uint32_t x) {
             ptx::cp_async_commit();
-            if constexpr (FP8) {                               // (stored by this thread itself)
-                copies_left<0>();
-                told(x);
-            } else {
-#pragma unroll
-                for (int k = 0; k <= S::LAG; ++k)
-                    if (k == on_way) waiting[k] = x;
-                if (++on_way > S::LAG) {
-                    copies_left<S::LAG>();
-                    told(waiting[0]);
-#pragma unroll
-                    for (int k = 0; k < S::LAG; ++k) waiting[k] = waiting[k + 1];
-                    --on_way;
-                }
+            if (waiting) {
+                copies_left<1>();
+                told(waiting);
             }
+            waiting = x;
         };
         auto all_told = [&] {
             copies_left<0>();
-#pragma unroll
-            for (int k = 0; k <= S::LAG; ++k)
-                if (k < on_way) told(waiting[k]);
-            on_way = 0;
+            if (waiting) told(waiting);
+            waiting = 0;
         };
-        int k_slot = 0, v_slot = 0;
-        unsigned k_phase = 1, v_phase = 1, q_phase = 1, seq = 0;
+        const uint32_t ring = keys ? k_at : v_at;
+        uint64_t *const full = keys ? b.kfull : b.vfull, *const empty = keys ? b.kempty : b.vempty;
+        int slot = 0;
+        unsigned phase = 1, q_phase = 1, seq = 0;
         for (; live && w.more(); w.next()) {
             // the queries: the block's rows, request by request
             all_told();
             live = wait_bar(bar(b.qempty), q_phase, abort_flag);
             if (!live) break;
             q_phase ^= 1;
-            const int q_pieces = D / 8, q_tiles = w.w.twin ? 1 : 2, tokens = p.tokens[w.g];
-            for (int x = 0; x < q_tiles; ++x) {
-                const int n = stream_requests(a, w.w, x), r0 = w.w.r0 + x * a.tile_req;
-                for (int e = lane; e < 32 * q_pieces; e += 32) {
-                    const int row = lw * 32 + e / q_pieces, q_piece = e % q_pieces, in = row / G, r = r0 + in;
-                    const bool real = in < n && length_of(a, r) >= tokens;
-                    const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q);
-                    if (real) src += r * a.q_stride + (long long)(w.w.hk * G + row - in * G) * D + q_piece * 8;
-                    copy16(q_at + x * TB + place_of(row, q_piece), src, real);
+            const int tokens = p.tokens[w.g];
+            if (keys || !w.w.twin) {
+                constexpr int QL = DC / 8, QR = 32 / QL;       // lanes of a row, rows of an instruction
+                const int x = keys ? 0 : 1, n = stream_requests(a, w.w, x);
+                const int row = lw * 32 + lane, in = row / G, r = w.w.r0 + x * a.tile_req + in;
+                const bool real = in < n && length_of(a, r) >= tokens;
+                const long long own = real ? r * a.q_stride + (long long)(w.w.hk * G + row - in * G) * D : -1;
+                const int q_piece = lane % QL;
+                const uint32_t to = q_at + x * TB;
+#pragma unroll 4
+                for (int k = 0; k < 32 / QR; ++k) {
+                    const int in_tile = k * QR + lane / QL;
+                    const long long from = __shfl_sync(ALL, own, in_tile);
+                    const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (from >= 0 ? from + q_piece * 8 : 0);
+                    if (q_piece * 8 < D) copy16(to + place_of(lw * 32 + in_tile, q_piece), src, from >= 0);
                 }
             }
             sent(bar(b.qfull));
             const int32_t *table = a.kv.table + p.lead[w.g] * a.kv.table_stride;
-            const char *kb = reinterpret_cast<const char *>(a.kv.k) + w.w.hk * a.kv.head_stride * ESZ;
-            const char *vb = reinterpret_cast<const char *>(a.kv.v) + w.w.hk * a.kv.head_stride * ESZ;
+            const char *const from = reinterpret_cast<const char *>(keys ? a.kv.k : a.kv.v) + w.w.hk * a.kv.head_stride * ESZ;
             auto page_of = [&](int t) {                        // of this lane's token of tile t
                 const int token = t * TT + lw * 32 + lane;
                 return t < w.t1 && token < tokens ? table[a.page_shift >= 0 ? token >> a.page_shift : token / a.kv.page_size] : -1;
@@ -636,42 +718,44 @@ __global__ void __launch_bounds__(THREADS) shared_kernel(const SharedArgs a) {
                 }
                 return y;
             };
-            // do(n, source) of every instruction, source null for tokens that do not count
-            auto each = [&](const Rows &y, const char *from, auto &&go) {
+            // go(n, source, whether it counts) of every instruction
+            auto each = [&](const Rows &y, auto &&go) {
 #pragma unroll
                 for (int f = 0; f < 32; f += 16) {
                     constexpr int N = 16 / RI;
                     if (y.steps >> (f / 16) & 1) {
                         const char *src = from + __shfl_sync(ALL, y.place, f) + row0 * tok_bytes + piece * 16;
+                        if (here) {
 #pragma unroll
-                        for (int n = 0; n < N; ++n) {
-                            go(f / RI + n, src);
-                            src += RI * tok_bytes;
+                            for (int n = 0; n < N; ++n) {
+                                go(f / RI + n, src, std::true_type{});
+                                src += RI * tok_bytes;
+                            }
                         }
                     } else {
 #pragma unroll
                         for (int n = 0; n < N; ++n) {
                             const long long at = __shfl_sync(ALL, y.place, f + n * RI + row0);
-                            go(f / RI + n, at >= 0 ? from + at + piece * 16 : nullptr);
+                            if (here) go(f / RI + n, at >= 0 ? from + at + piece * 16 : from, at >= 0);
                         }
                     }
                 }
             };
-            auto copy = [&](uint32_t slot, const char *from, const Rows &y) {       // 16-bit rows, asynchronously
-                each(y, from, [&](int n, const char *src) {
-                    if (here) copy16(slot + row_at(n), src ? src : from, src != nullptr);
+            auto copy = [&](uint32_t to, const Rows &y) {                           // 16-bit rows, asynchronously
+                each(y, [&](int n, const char *src, auto real) {
+                    if constexpr (std::is_same_v<decltype(real), std::true_type>) ptx::cp_async16(to + row_at(n), src);
+                    else copy16(to + row_at(n), src, real);
                 });
             };
-            auto fetch = [&](uint4 (&x)[INSTR], const char *from, const Rows &y) {  // 8-bit rows, through registers
-                each(y, from, [&](int n, const char *src) {
-                    x[n] = make_uint4(0, 0, 0, 0);
-                    if (here && src) x[n] = *reinterpret_cast<const uint4 *>(src);
+            auto fetch = [&](uint4 (&x)[INSTR], const Rows &y) {                    // 8-bit rows, through registers
+                each(y, [&](int n, const char *src, auto real) {
+                    x[n] = real ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
                 });
             };
-            auto store = [&](uint32_t slot, const uint4 (&x)[INSTR]) {
+            auto store = [&](uint32_t to, const uint4 (&x)[INSTR]) {
 #pragma unroll
                 for (int n = 0; n < INSTR; ++n) {
-                    const uint32_t word[4] = {x[n].x, x[n].y, x[n].z, x[n].w}, at = slot + row_at(n);
+                    const uint32_t word[4] = {x[n].x, x[n].y, x[n].z, x[n].w}, at = to + row_at(n);
                     uint32_t out[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) out[2 * k] = to_bf16(word[k] & 0xffffu), out[2 * k + 1] = to_bf16(word[k] >> 16);
@@ -680,118 +764,39 @@ __global__ void __launch_bounds__(THREADS) shared_kernel(const SharedArgs a) {
                     sts16(at ^ 16, make_uint4(out[4], out[5], out[6], out[7]));
                 }
             };
-            // keys run one tile ahead of values; 8-bit ones are on their way while those
-            // before are waited for and stored
-            Rows now = rows_of(w.t0, page_of(w.t0)), before = now;
-            int page = page_of(w.t0 + 1);
-            uint4 kx[FP8 ? INSTR : 1], vx[FP8 ? INSTR : 1];
-            if constexpr (FP8) fetch(kx, kb, now);
-            for (int t = w.t0; t <= w.t1; ++t) {
-                if constexpr (FP8)
-                    if (t > w.t0) fetch(vx, vb, before);
-                if (t < w.t1) {
+            // (8-bit rows of a tile are on their way while the slot is waited for)
+            int page = page_of(w.t0);
+            Rows now = rows_of(w.t0, page);
+            page = page_of(w.t0 + 1);
+            uint4 x[FP8 ? INSTR : 1];
+            if constexpr (FP8) fetch(x, now), all_told();      // (no later copy tells of the queries)
+            for (int t = w.t0; t < w.t1; ++t) {
+                live = wait_bar(bar(empty[slot]), phase, abort_flag);
+                if (!live) break;
+                if (keys) {
                     const unsigned ok = __ballot_sync(ALL, now.place >= 0);
-                    live = wait_bar(bar(b.kempty[k_slot]), k_phase, abort_flag);
-                    if (!live) break;
                     if (lane == 0) *(volatile unsigned *)&b.ok[seq % OK_RING][lw] = ok;
                     ++seq;
-                    if constexpr (FP8) store(k_at + k_slot * TB, kx);
-                    else copy(k_at + k_slot * TB, kb, now);
-                    sent(bar(b.kfull[k_slot]));
-                    if (++k_slot == SLOTS) k_slot = 0, k_phase ^= 1;
                 }
-                Rows next = now;
-                if (t + 1 < w.t1) {
-                    next = rows_of(t + 1, page);
-                    page = page_of(t + 2);
-                    if constexpr (FP8) fetch(kx, kb, next);
+                if constexpr (FP8) {
+                    store(ring + slot * TB, x);
+                    if (t + 1 < w.t1) now = rows_of(t + 1, page), fetch(x, now);
+                    told(bar(full[slot]));
+                } else {
+                    copy(ring + slot * TB, now);
+                    if (t + 1 < w.t1) now = rows_of(t + 1, page);
+                    sent(bar(full[slot]));
                 }
-                if (t > w.t0) {
-                    live = wait_bar(bar(b.vempty[v_slot]), v_phase, abort_flag);
-                    if (!live) break;
-                    if constexpr (FP8) store(v_at + v_slot * TB, vx);
-                    else copy(v_at + v_slot * TB, vb, before);
-                    sent(bar(b.vfull[v_slot]));
-                    if (++v_slot == SLOTS) v_slot = 0, v_phase ^= 1;
-                }
-                before = now;
-                now = next;
+                page = page_of(t + 2);
+                if (++slot == SLOTS) slot = 0, phase ^= 1;
             }
         }
         all_told();
         if (__any_sync(ALL, bad) && lane == 0) atomicOr(a.status, STATUS_PAGES);
-    } else {
-        // ------------------------------------------------ the products, step by step: stream s & 1 takes step s
-        constexpr uint32_t QK = instr_desc(TT, false), PV = instr_desc(DC, true);
-        int k_slot = 0, v_slot = 0;
-        unsigned k_phase = 0, v_phase = 0, q_phase = 0, p_phase[2] = {0, 0};
-        bool live = true;
-        for (; live && w.more(); w.next()) {
-            const bool twin = w.w.twin;
-            const int n = w.t1 - w.t0, steps = twin ? n : 2 * n;
-            live = wait_bar(bar(b.qfull), q_phase, abort_flag);
-            if (!live) break;
-            q_phase ^= 1;
-            auto scores = [&](int s) {
-                const int x = s & 1;
-                if (twin || x == 0) {
-                    live = wait_bar(bar(b.kfull[k_slot]), k_phase, abort_flag);
-                    if (!live) return;
-                }
-                if (lane == 0) {
-                    ptx::tc_fence_after();
-                    const uint32_t qa = q_at + (twin ? 0 : x) * TB, ka = k_at + k_slot * TB;
-#pragma unroll
-                    for (int k = 0; k < DC / 16; ++k) {
-                        const uint32_t off = (k / 4) * SLAB + (k % 4) * 32;
-                        ptx::mma_bf16(tmem + S_COL + x * TT, slab_desc(qa + off, 16), slab_desc(ka + off, 16), QK, k > 0);
-                    }
-                    ptx::mma_commit(bar(b.sfull[x]));
-                    if (twin || x == 1) ptx::mma_commit(bar(b.kempty[k_slot]));
-                    if (s == steps - 1) ptx::mma_commit(bar(b.qempty));
-                }
-                __syncwarp();
-                if ((twin || x == 1) && ++k_slot == SLOTS) k_slot = 0, k_phase ^= 1;
-            };
-            scores(0);
-            if (live && steps > 1) scores(1);
-            for (int s = 0; live && s < steps; ++s) {
-                const int x = s & 1;
-                live = wait_bar(bar(b.pfull[x]), p_phase[x], abort_flag);
-                if (!live) break;
-                p_phase[x] ^= 1;
-                if (twin || x == 0) {
-                    live = wait_bar(bar(b.vfull[v_slot]), v_phase, abort_flag);
-                    if (!live) break;
-                }
-                if (lane == 0) {
-                    ptx::tc_fence_after();
-                    const uint32_t va = v_at + v_slot * TB, pa = tmem + S_COL + x * TT, oa = tmem + O_COL + x * DC;
-#pragma unroll
-                    for (int k = 0; k < TT / 16; ++k) {
-                        const uint64_t vd = slab_desc(va + k * 2048, SLAB);
-                        const uint32_t col = pa + (k / 2) * 32 + (k % 2) * 8;
-                        mma_bf16_ta(oa, col, vd, PV, s > 1 || k > 0);
-                        mma_bf16_ta(oa, col + 16, vd, PV, 1);
-                    }
-                    if (twin || x == 1) ptx::mma_commit(bar(b.vempty[v_slot]));
-                    if (s + 2 >= steps) ptx::mma_commit(bar(b.ofull[x]));
-                }
-                __syncwarp();
-                if ((twin || x == 1) && ++v_slot == SLOTS) v_slot = 0, v_phase ^= 1;
-                if (s + 2 < steps) scores(s + 2);
-            }
-        }
-        // nothing may be under way when tensor and shared memory are given back
-        if (lane == 0) ptx::mma_commit(bar(b.drain));
-        __syncwarp();
-        const uint64_t t_end = ptx::globaltimer();
-        while (!__all_sync(ALL, ptx::mbar_try_wait(bar(b.drain), 0)) && __all_sync(ALL, ptx::globaltimer() - t_end < WAIT_NS)) {}
-        ptx::tc_fence_before();
     }
     __syncthreads();
     if (b.abort && tid == 0) atomicOr(a.status, STATUS_TIMEOUT);
-    if (warp == 12) {
+    if (warp == 0) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, 512);
     }

@@ -128,3 +128,11 @@ def test_shared_groups_heads_and_pages(scute, contexts, kind, groups, H, group, 
     g = np.random.default_rng([H, group, D, page])
     b = Batch(scute, g, GROUPS[groups], H, group, D, page, kind, token_major, scales=kind == "fp8", before=2, behind=3)
     b.run(ctx_of(contexts, kind))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("H,group,D,n,T", [(8, 4, 128, 3, 30011), (8, 4, 128, 50, 20480), (4, 2, 64, 5, 50000), (2, 9, 128, 40, 9000)])
+def test_shared_long_beginnings(scute, contexts, kind, H, group, D, n, T):
+    """Many tiles to a CTA, work rows that several CTAs share, both ways of the streams."""
+    g = np.random.default_rng([H, n, T])
+    Batch(scute, g, [(n, T, lambda j: T + j % 5), (2, 700, lambda j: 710)], H, group, D, 16, kind, scales=kind == "fp8").run(ctx_of(contexts, kind))
