@@ -558,7 +558,7 @@ __device__ __forceinline__ int shared_group(const Args &a, int r, int length, in
 // rows of parts that a batch may need
 inline long long shared_rows(long long n_req, long long q_heads, int num_sms) { return 3 * n_req * q_heads + 256ll * num_sms; }
 cudaError_t launch_shared(const SharedArgs &a, int num_sms, cudaStream_t st);
-cudaError_t launch_join(const JoinArgs &a, cudaStream_t st);
+cudaError_t launch_join(const JoinArgs &a, int num_sms, int n_groups, cudaStream_t st);
 
 // ---------------------------------------------------------------- norms around a sub-block
 struct NormArgs {

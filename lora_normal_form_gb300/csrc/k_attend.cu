@@ -656,26 +656,46 @@ struct FmaMath {
 // ROW_COST places and then one for each of its tiles, an empty request's row one
 // tile all the same; places_at[r] = places of one row of each request before r.
 //
-// Which tokens a request sees: positions first .. len - 1 of a sequence in which the
-// tokens that stay visible before a window stand directly before it, token_of(first,
-// i) the token at position i (a window from token f on, of whose S = min(sinks, f)
-// tokens before stay: first = f - S, and positions below f are tokens 0 .. S - 1).
+// Which tokens a request sees.  A row's tiles run over positions first .. len - 1, each a
+// token's.  Without tokens that stay visible before a window (sinks) position and token
+// are one and first is the window's first token f.  With them, S = min(sinks, f) tokens in
+// front, the window's positions are its tokens' from wa on, f rounded down to a tile, and
+// those of the S tokens, rounded up to a tile, lie directly before wa; positions of tokens
+// between S and f do not count.  So tiles begin where tiles of the whole context would, and
+// lie in whole pages where those do, at the price of up to two tiles in part (200 requests
+// of 30 to 5000 tokens, window 1000, 24 in front, e4m3, pages of 16: NN us against 85.1
+// with the S tokens directly before f).
+struct Seen {
+    int first, len;
+    int wa, f, s;            // (with sinks)
+};
 template <bool SHARED>
-__device__ __forceinline__ void seen_of(const AttendArgs &a, int r, int *first, int *len, bool *bad) {
+__device__ __forceinline__ Seen seen_of(const AttendArgs &a, int r, int tt, bool *bad) {
     const int cap = a.kv.table_cols * a.kv.page_size;
     int n = a.kv_len[r];
     *bad = n < 0 || n > cap;
     n = n < 0 ? 0 : n > cap ? cap : n;
-    *len = n;
+    Seen y = {0, n, 0, 0, 0};
     if constexpr (SHARED) {
         int tokens;
-        *first = shared_group(a, r, n, &tokens) >= 0 ? tokens : 0;
+        y.first = shared_group(a, r, n, &tokens) >= 0 ? tokens : 0;
     } else {
-        const int f = a.window > 0 ? max(0, n - a.window) : 0;
-        *first = f - min(f, a.sinks);
+        y.first = a.window > 0 ? max(0, n - a.window) : 0;
+        if (a.sinks) {
+            y.f = y.first;
+            y.s = min(a.sinks, y.f);
+            y.wa = y.f - y.f % tt;
+            y.first = max(0, y.wa - (y.s + tt - 1) / tt * tt);
+        }
     }
+    return y;
 }
-__device__ __forceinline__ int token_of(const AttendArgs &a, int first, int i) { return i - (i < first + a.sinks ? first : 0); }
+// The token at position i (-1: none that counts).
+__device__ __forceinline__ int token_of(const AttendArgs &a, const Seen &y, int i) {
+    if (!a.sinks) return i;
+    const int token = i < y.wa ? i - y.first : i;
+    return token < y.s || token >= y.f ? token : -1;
+}
 template <bool SHARED>
 __device__ __forceinline__ void plan_places(const AttendArgs &a, int tt, int *places_at, int *warp_sum) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, n = a.n_req, threads = blockDim.x;
@@ -684,11 +704,10 @@ __device__ __forceinline__ void plan_places(const AttendArgs &a, int tt, int *pl
     bool any = false;
 #pragma unroll 8
     for (int r = r0; r < r1; ++r) {
-        int first, len;
         bool bad;
-        seen_of<SHARED>(a, r, &first, &len, &bad);
+        const Seen y = seen_of<SHARED>(a, r, tt, &bad);
         any |= bad;
-        mine += ROW_COST + max(1, (len - first + tt - 1) / tt);
+        mine += ROW_COST + max(1, (y.len - y.first + tt - 1) / tt);
     }
     if (any && blockIdx.x == 0) atomicOr(a.status, STATUS_PAGES);
     int inc = mine;
@@ -702,11 +721,10 @@ __device__ __forceinline__ void plan_places(const AttendArgs &a, int tt, int *pl
     int at = inc - mine;
     for (int w = 0; w < warp; ++w) at += warp_sum[w];
     for (int r = r0; r < r1; ++r) {
-        int first, len;
         bool bad;
-        seen_of<SHARED>(a, r, &first, &len, &bad);
+        const Seen y = seen_of<SHARED>(a, r, tt, &bad);
         places_at[r] = at;
-        at += ROW_COST + max(1, (len - first + tt - 1) / tt);
+        at += ROW_COST + max(1, (y.len - y.first + tt - 1) / tt);
     }
     if (t == threads - 1) places_at[n] = at;
     __syncthreads();
@@ -725,9 +743,10 @@ struct Walk {
     int hz, Z, tt;
     long long total, end;
     int ctas;
-    // the row: its first place, request, head and chunk, tiles; tokens [first, len)
+    // the row: its first place, request, head and chunk, tiles; positions [first, len)
     long long base;
-    int r, hk, z, tiles, first, len;
+    int r, hk, z, tiles;
+    Seen seen;
     int t0, t1;              // the range's tiles of it
 
     __device__ __forceinline__ Walk(const AttendArgs &args, const int *at, int heads_chunk, int tile, int min_tiles)
@@ -744,7 +763,7 @@ struct Walk {
     __device__ __forceinline__ int last_owner() const { return owner(base + ROW_COST + tiles - 1); }
     __device__ __forceinline__ void request() {
         bool bad;
-        seen_of<SHARED>(a, r, &first, &len, &bad);
+        seen = seen_of<SHARED>(a, r, tt, &bad);
         tiles = places_at[r + 1] - places_at[r] - ROW_COST;
     }
     __device__ __forceinline__ void cut(long long from) {
@@ -782,8 +801,8 @@ struct Walk {
         }
         cut(base);
     }
-    __device__ __forceinline__ int from() const { return first + t0 * tt; }
-    __device__ __forceinline__ int to() const { return (int)min((long long)len, first + (long long)t1 * tt); }
+    __device__ __forceinline__ int from() const { return seen.first + t0 * tt; }
+    __device__ __forceinline__ int to() const { return (int)min((long long)seen.len, seen.first + (long long)t1 * tt); }
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
 };
 
@@ -1018,18 +1037,19 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
         // others the check is lost (pages of 16: 111.8 us, by halves 107.7)
         const bool whole_tiles = TT <= 16 || a.kv.page_size % TT == 0;
         const long long tok_bytes = a.kv.token_stride * ESZ;
-        int hk = w.hk, z = w.z, r = w.r, first = w.first, stop = w.to(), pos = w.from();
+        int hk = w.hk, z = w.z, r = w.r, stop = w.to(), pos = w.from();
+        Seen seen = w.seen;
         bool opens = true, more = w.more();
-        auto look_up = [&](int of, int skip, int from, int until, int *page) {
+        auto look_up = [&](int of, const Seen &y, int from, int until, int *page) {
             const int32_t *table = a.kv.table + of * a.kv.table_stride;
 #pragma unroll
             for (int k = 0; k < SPAN / 32; ++k) {
-                const int i = from + k * 32 + lane, token = token_of(a, skip, i);
-                page[k] = i < until ? table[a.page_shift >= 0 ? token >> a.page_shift : token / a.kv.page_size] : -1;
+                const int i = from + k * 32 + lane, token = token_of(a, y, i);
+                page[k] = i < until && token >= 0 ? table[a.page_shift >= 0 ? token >> a.page_shift : token / a.kv.page_size] : -1;
             }
         };
         int page[SPAN / 32];
-        if (more) look_up(r, first, pos, stop, page);
+        if (more) look_up(r, seen, pos, stop, page);
         bool bad = false;
         int st = 0, turn = 0, qst = 0;          // the next stage, whose it is to fill, the next slot of queries
         unsigned ph = 1, qph = 1;
@@ -1040,7 +1060,7 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
             const int next_pos = last ? w.from() : pos + SPAN, next_stop = last ? w.to() : stop;
             int next_page[SPAN / 32];
             if (last) more = w.more();
-            if (more) look_up(w.r, w.first, next_pos, next_stop, next_page);
+            if (more) look_up(w.r, w.seen, next_pos, next_stop, next_page);
             if (opens && pos < stop) {
                 if (warp == 0) {
                     if (!wait_bar(q_empty(qst), qph, s_abort)) break;
@@ -1061,11 +1081,11 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
                 if (pos + k * 32 >= stop || gone) break;
                 const int i = pos + k * 32 + lane;
                 long long place = -1;
-                if (i < stop) {
+                const int token = token_of(a, seen, i);
+                if (i < stop && token >= 0) {
                     if (page[k] < 0 || page[k] >= a.kv.n_pages) {
                         bad = true;
                     } else {
-                        const int token = token_of(a, first, i);
                         const int in = a.page_shift >= 0 ? token & (a.kv.page_size - 1) : token % a.kv.page_size;
                         place = ((long long)page[k] * a.kv.page_stride + (long long)in * a.kv.token_stride) * ESZ;
                     }
@@ -1148,7 +1168,7 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
             }
             if (gone) break;
             opens = last;
-            r = w.r, hk = w.hk, z = w.z, first = w.first;
+            r = w.r, hk = w.hk, z = w.z, seen = w.seen;
             pos = next_pos;
             stop = next_stop;
 #pragma unroll

@@ -662,29 +662,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
         int slot = 0;
         unsigned phase = 1, q_phase = 1, seq = 0;
         for (; live && w.more(); w.next()) {
-            // the queries: the block's rows, request by request
-            all_told();
-            live = wait_bar(bar(b.qempty), q_phase, abort_flag);
-            if (!live) break;
-            q_phase ^= 1;
             const int tokens = p.tokens[w.g];
-            if (keys || !w.w.twin) {
-                constexpr int QL = DC / 8, QR = 32 / QL;       // lanes of a row, rows of an instruction
-                const int x = keys ? 0 : 1, n = stream_requests(a, w.w, x);
-                const int row = lw * 32 + lane, in = row / G, r = w.w.r0 + x * a.tile_req + in;
-                const bool real = in < n && length_of(a, r) >= tokens;
-                const long long own = real ? r * a.q_stride + (long long)(w.w.hk * G + row - in * G) * D : -1;
-                const int q_piece = lane % QL;
-                const uint32_t to = q_at + x * TB;
-#pragma unroll 4
-                for (int k = 0; k < 32 / QR; ++k) {
-                    const int in_tile = k * QR + lane / QL;
-                    const long long from = __shfl_sync(ALL, own, in_tile);
-                    const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (from >= 0 ? from + q_piece * 8 : 0);
-                    if (q_piece * 8 < D) copy16(to + place_of(lw * 32 + in_tile, q_piece), src, from >= 0);
-                }
-            }
-            sent(bar(b.qfull));
             const int32_t *table = a.kv.table + p.lead[w.g] * a.kv.table_stride;
             const char *const from = reinterpret_cast<const char *>(keys ? a.kv.k : a.kv.v) + w.w.hk * a.kv.head_stride * ESZ;
             auto page_of = [&](int t) {                        // of this lane's token of tile t
@@ -764,8 +742,30 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                     sts16(at ^ 16, make_uint4(out[4], out[5], out[6], out[7]));
                 }
             };
-            // (8-bit rows of a tile are on their way while the slot is waited for)
             int page = page_of(w.t0);
+            // the queries: the block's rows, request by request
+            all_told();
+            live = wait_bar(bar(b.qempty), q_phase, abort_flag);
+            if (!live) break;
+            q_phase ^= 1;
+            if (keys || !w.w.twin) {
+                constexpr int QL = DC / 8, QR = 32 / QL;       // lanes of a row, rows of an instruction
+                const int x = keys ? 0 : 1, n = stream_requests(a, w.w, x);
+                const int row = lw * 32 + lane, in = row / G, r = w.w.r0 + x * a.tile_req + in;
+                const bool real = in < n && length_of(a, r) >= tokens;
+                const long long own = real ? r * a.q_stride + (long long)(w.w.hk * G + row - in * G) * D : -1;
+                const int q_piece = lane % QL;
+                const uint32_t to = q_at + x * TB;
+#pragma unroll 4
+                for (int k = 0; k < 32 / QR; ++k) {
+                    const int in_tile = k * QR + lane / QL;
+                    const long long from = __shfl_sync(ALL, own, in_tile);
+                    const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (from >= 0 ? from + q_piece * 8 : 0);
+                    if (q_piece * 8 < D) copy16(to + place_of(lw * 32 + in_tile, q_piece), src, from >= 0);
+                }
+            }
+            sent(bar(b.qfull));
+            // (8-bit rows of a tile are on their way while the slot is waited for)
             Rows now = rows_of(w.t0, page);
             page = page_of(w.t0 + 1);
             uint4 x[FP8 ? INSTR : 1];
@@ -817,10 +817,11 @@ cudaError_t launch_shape(const SharedArgs &a, int num_sms, cudaStream_t st) {
 // its own tokens, and those of the tokens its group shares, in the order of their CTAs.
 // JG threads share the parts of four elements, so that a part's loads do not wait for
 // another's; a head's parts are then added up in shared memory in a fixed order.
-constexpr int JOIN_THREADS = 256, JG = 8;
+constexpr int JOIN_THREADS = 256;
+template <int JG, int B>
 __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const JoinArgs a) {
-    __shared__ float s_m[JOIN_THREADS], s_l[JOIN_THREADS];
-    __shared__ float4 s_o[JOIN_THREADS];
+    __shared__ float s_m[JG > 1 ? JOIN_THREADS : 1], s_l[JG > 1 ? JOIN_THREADS : 1];
+    __shared__ float4 s_o[JG > 1 ? JOIN_THREADS : 1];
     const int quads = a.dim / 4, per = JOIN_THREADS / (JG * quads), t = threadIdx.x;
     const int in = t / (JG * quads), rest = t - in * JG * quads, part0 = rest / quads, d = (rest - part0 * quads) * 4;
     const int row = blockIdx.x * per + in;
@@ -834,7 +835,6 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const JoinArgs a) {
         const int4 piece = a.piece[(long long)r * (a.q_heads / a.group) + hk];
         const int twin = piece.y >= 0 && piece.y & SHARED_TWIN ? 1 : 0, n = piece.w & 0xffff, i = (piece.w >> 16) + h - hk * a.group;
         const int parts = 1 + (piece.y < 0 ? 0 : ((piece.y & ~SHARED_TWIN) - piece.x + 1) << twin);
-        constexpr int B = 4;
 #pragma unroll 1
         for (int k0 = part0; k0 < parts; k0 += JG * B) {
             float2 s[B];
@@ -865,20 +865,23 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const JoinArgs a) {
             }
         }
     }
-    s_m[t] = m, s_l[t] = l, s_o[t] = x;
-    __syncthreads();
-    if (!real || part0 != 0) return;
+    if constexpr (JG > 1) {
+        s_m[t] = m, s_l[t] = l, s_o[t] = x;
+        __syncthreads();
+        if (!real || part0 != 0) return;
 #pragma unroll
-    for (int k = 1; k < JG; ++k) m = fmaxf(m, s_m[t + k * quads]);
-    const float ref = m == -INFINITY ? 0.f : m, f = pow2(s_m[t] - ref);
-    l *= f, x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+        for (int k = 1; k < JG; ++k) m = fmaxf(m, s_m[t + k * quads]);
+        const float ref = m == -INFINITY ? 0.f : m, f = pow2(s_m[t] - ref);
+        l *= f, x.x *= f, x.y *= f, x.z *= f, x.w *= f;
 #pragma unroll
-    for (int k = 1; k < JG; ++k) {
-        const float g = pow2(s_m[t + k * quads] - ref);
-        const float4 y = s_o[t + k * quads];
-        l += s_l[t + k * quads] * g;
-        x.x += y.x * g, x.y += y.y * g, x.z += y.z * g, x.w += y.w * g;
+        for (int k = 1; k < JG; ++k) {
+            const float g = pow2(s_m[t + k * quads] - ref);
+            const float4 y = s_o[t + k * quads];
+            l += s_l[t + k * quads] * g;
+            x.x += y.x * g, x.y += y.y * g, x.z += y.z * g, x.w += y.w * g;
+        }
     }
+    if (!real) return;
     const float vs = a.v_scale ? a.v_scale[hk] : 1.f, div = l == 0.f ? 0.f : vs / l;
     __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(a.out) + r * a.out_stride + (long long)h * a.dim + d;
     *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16(x.x * div, x.y * div), pack_bf16(x.z * div, x.w * div));
@@ -887,9 +890,14 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const JoinArgs a) {
 
 }  // namespace
 
-cudaError_t launch_join(const JoinArgs &a, cudaStream_t st) {
-    const int per = JOIN_THREADS / (JG * (a.dim / 4));
-    return launch_chained(join_kernel, (a.rows + per - 1) / per, JOIN_THREADS, 0, st, a);
+cudaError_t launch_join(const JoinArgs &a, int num_sms, int n_groups, cudaStream_t st) {
+    const auto run = [&](auto kernel, int groups) {
+        const int per = JOIN_THREADS / (groups * (a.dim / 4));
+        return launch_chained(kernel, (a.rows + per - 1) / per, JOIN_THREADS, 0, st, a);
+    };
+    // as many parts as CTAs share a work row, of two streams: few with many groups
+    const int parts = 2 * (num_sms / (n_groups * (a.q_heads / a.group)) + 1);
+    return parts > 8 ? run(join_kernel<4, 8>, 4) : run(join_kernel<1, 4>, 1);
 }
 
 cudaError_t launch_shared(const SharedArgs &a, int num_sms, cudaStream_t st) {

@@ -254,7 +254,7 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
         j.q_heads = a.q_heads;
         j.group = a.group;
         j.dim = kv->head_dim;
-        CU_TRY(c, launch_join(j, st));
+        CU_TRY(c, launch_join(j, c->num_sms, sh->n_groups, st));
         count_launch(c, 1);
     }
     CU_TRY(c, tl.end(SCUTE_KIND_ATTENTION));
