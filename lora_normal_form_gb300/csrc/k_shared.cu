@@ -170,12 +170,12 @@ constexpr uint32_t instr_desc(int n, bool across) {
 // they share, the first request that has them all (whose row of the table is read; no
 // such request: no places), and the places of the groups before.
 struct Plan {
-    int start[SHARED_MAX_GROUPS + 1], tokens[SHARED_MAX_GROUPS], lead[SHARED_MAX_GROUPS];
+    int start[SHARED_MAX_GROUPS + 1], tokens[SHARED_MAX_GROUPS], lead[SHARED_MAX_GROUPS], blocks[SHARED_MAX_GROUPS];
     long long at[SHARED_MAX_GROUPS + 1];
     long long warp_sum[THREADS / 32];
 };
 struct Bars {
-    uint64_t kfull[4], kempty[4], vfull[4], vempty[4], qfull, qempty, sfull[2], pfull[2], ofull[2], drain;
+    uint64_t kfull[4], kempty[4], vfull[4], vempty[4], qfull, qempty, sfull[2], pfull[2], ofull[2], turn[2], drain;
     uint32_t tmem;
     int abort;
     unsigned ok[OK_RING][TT / 32];         // tokens that count, of the last tiles' keys
@@ -193,10 +193,6 @@ __device__ __forceinline__ int group_of(const SharedArgs &a, const Plan &p, int 
 }
 __device__ __forceinline__ int requests_of(const Plan &p, int g) { return p.start[g + 1] - p.start[g]; }
 __device__ __forceinline__ int tiles_of(const Plan &p, int g) { return p.lead[g] == INT32_MAX ? 0 : (p.tokens[g] + TT - 1) / TT; }
-__device__ __forceinline__ int blocks_of(const SharedArgs &a, const Plan &p, int g) {
-    return (requests_of(p, g) + 2 * a.tile_req - 1) / (2 * a.tile_req);
-}
-
 __device__ __forceinline__ void make_plan(const SharedArgs &a, Plan &p) {
     static_assert(SHARED_MAX_GROUPS + 1 <= 3 * THREADS, "three groups of a thread");
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, G = a.n_groups;
@@ -232,8 +228,9 @@ __device__ __forceinline__ void make_plan(const SharedArgs &a, Plan &p) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         const int g = 3 * t + i;
-        const int tiles = g < G ? tiles_of(p, g) : 0;
-        mine[i] = tiles ? (long long)a.kv.heads * blocks_of(a, p, g) * (tiles + ROW_COST) : 0;
+        const int tiles = g < G ? tiles_of(p, g) : 0, blocks = tiles ? (requests_of(p, g) + 2 * a.tile_req - 1) / (2 * a.tile_req) : 0;
+        if (g < G) p.blocks[g] = blocks;
+        mine[i] = (long long)a.kv.heads * blocks * (tiles + ROW_COST);
         sum += mine[i];
     }
     long long inc = sum;
@@ -277,9 +274,9 @@ struct WorkRow {
 };
 __device__ __forceinline__ WorkRow work_row(const SharedArgs &a, const Plan &p, int g, int row) {
     WorkRow w;
-    const int blocks = blocks_of(a, p, g), all = requests_of(p, g);
+    const int blocks = p.blocks[g], all = requests_of(p, g);
     w.g = g;
-    w.hk = row / blocks;
+    w.hk = blocks == 1 ? row : row / blocks;
     const int b = row - w.hk * blocks;
     w.r0 = p.start[g] + b * 2 * a.tile_req;
     w.requests = min(2 * a.tile_req, all - b * 2 * a.tile_req);
@@ -321,7 +318,7 @@ struct Walk {
     }
     __device__ __forceinline__ void group() {
         tiles = tiles_of(p, g);
-        rows = tiles ? a.kv.heads * blocks_of(a, p, g) : 0;
+        rows = a.kv.heads * p.blocks[g];
     }
     __device__ __forceinline__ void set(long long from) {
         t0 = (int)max(0ll, from - base - ROW_COST);
@@ -351,7 +348,7 @@ __device__ __forceinline__ void write_pieces(const SharedArgs &a, const Plan &p,
         {
             const int g = group_of(a, p, r, length_of(a, r));
             if (g >= 0) {
-                const int tiles = tiles_of(p, g), b = (r - p.start[g]) / (2 * a.tile_req), blocks = blocks_of(a, p, g);
+                const int tiles = tiles_of(p, g), b = (r - p.start[g]) / (2 * a.tile_req), blocks = p.blocks[g];
                 const int row = hk * blocks + b;
                 const WorkRow w = work_row(a, p, g, row);
                 const int x = !w.twin && r - w.r0 >= a.tile_req;
@@ -403,6 +400,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
             ptx::mbar_init(bar(b.sfull[i]), 1);
             ptx::mbar_init(bar(b.pfull[i]), 4);
             ptx::mbar_init(bar(b.ofull[i]), 1);
+            ptx::mbar_init(bar(b.turn[i]), 1);
         }
         ptx::mbar_init(bar(b.drain), 2);
         ptx::fence_mbar_init();
@@ -435,6 +433,20 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_col = tmem + S_COL + x * TT, o_col = tmem + O_COL + x * DC, s_at = s_col + lanes, o_at = o_col + lanes;
         unsigned s_phase = 0, o_phase = 0, p_phase = 0, q_phase = 0, seq = 0;      // seq: tiles of the CTA before this work row's
+        // The streams issue in turn, each the second product of its tile and the scores of
+        // its next: one's run under the other's softmax.  (Side by side both would wait for
+        // the products at once and for the softmax at once: 64 requests on 8192 tokens,
+        // 3.8 us a tile against NN.)
+        unsigned turn_phase = x == 0 ? 1 : 0;
+        auto my_turn = [&] {
+            const bool yes = wait_bar(bar(b.turn[x]), turn_phase, abort_flag);
+            turn_phase ^= 1;
+            return yes;
+        };
+        auto pass_turn = [&] {
+            if (lane == 0) ptx::mbar_arrive(bar(b.turn[1 - x]));
+            __syncwarp();
+        };
         bool live = true, first_row = true;
         for (; live && w.more(); w.next()) {
             const bool twin = w.w.twin;
@@ -462,6 +474,15 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                 }
                 __syncwarp();
             };
+            // Tile t's values, which the other stream takes, have come.  Both streams see every
+            // filling of a slot before it is given back: its barrier's parity tells only two
+            // fillings apart.
+            auto seen_values = [&](int t) {
+                if (!wait_bar(bar(b.vfull[slot_of(t)]), phase_of(t), abort_flag)) return false;
+                if (lane == 0) ptx::mbar_arrive(bar(b.vempty[slot_of(t)]));
+                __syncwarp();
+                return true;
+            };
             if (issues) {
                 live = wait_bar(bar(b.qfull), q_phase, abort_flag);
                 if (!live) break;
@@ -477,7 +498,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
             float top = -INFINITY, sum[4] = {0.f, 0.f, 0.f, 0.f};
             bool any = false;
             for (int t = t_first; t < w.t1; t += step) {
-                live = wait_bar(bar(b.sfull[x]), s_phase, abort_flag);
+                live = (!issues || !twin || t == w.t0 || seen_values(t - 1)) && wait_bar(bar(b.sfull[x]), s_phase, abort_flag);
                 if (!live) break;
                 s_phase ^= 1;
                 ptx::tc_fence_after();
@@ -562,7 +583,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                 if (lane == 0) ptx::mbar_arrive(bar(b.pfull[x]));
                 if (!issues) continue;
                 const int slot = slot_of(t);
-                live = wait_bar(bar(b.pfull[x]), p_phase, abort_flag) && wait_bar(bar(b.vfull[slot]), phase_of(t), abort_flag);
+                live = wait_bar(bar(b.pfull[x]), p_phase, abort_flag) && wait_bar(bar(b.vfull[slot]), phase_of(t), abort_flag) && my_turn();
                 if (!live) break;
                 p_phase ^= 1;
                 if (lane == 0) {
@@ -574,17 +595,20 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                         mma_bf16_ta(o_col, col, vd + k * (2048 >> 4), PV, adds || k > 0);
                         mma_bf16_ta(o_col, col + 16, vd + k * (2048 >> 4), PV, 1);
                     }
-                    for (int k = 0; k < uses; ++k) ptx::mma_commit(bar(b.vempty[slot]));
+                    ptx::mma_commit(bar(b.vempty[slot]));
                     if (t + step >= w.t1) ptx::mma_commit(bar(b.ofull[x]));
                 }
                 __syncwarp();
                 if (t + step < w.t1) scores(t + step);
                 if (!live) break;
+                pass_turn();
+            }
+            if (live && issues && twin && x == 1 && (w.t1 - w.t0) % 2) {      // the other stream had one tile more
+                live = my_turn();
+                if (live) pass_turn();
             }
             if (!live) break;
-            // the work row's last values have come, whichever stream's they are: a slot's
-            // parity tells only two fillings apart
-            if (issues) live = wait_bar(bar(b.vfull[slot_of(w.t1 - 1)]), phase_of(w.t1 - 1), abort_flag);
+            if (issues && twin && (w.t1 - w.t0 - 1) % 2 != x) live = seen_values(w.t1 - 1);
             if (!live) break;
             seq += w.t1 - w.t0;
             // the stream's part, 32 bytes of a row at a time
