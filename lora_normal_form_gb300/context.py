@@ -174,19 +174,23 @@ class Context:
         ``source[r]`` (-1: nothing) of ``table_in``: full pages shared, a last page in
         part the row's own (device int32 tensors; scute.h has the rules).  What is to
         be copied for that, ``kv_copy`` copies."""
-        for t in (table_in, table_out):
-            _check_table(t)
-        int32, n_in, n_out = self._dtypes()[1], len_in.numel(), source.numel()
-        cols, pitch = table_in.shape[1], []
-        for t, n in ((table_in, n_in), (table_out, n_out)):
-            pitch.append(t.stride(0) if t.shape[0] > 1 else max(cols, t.stride(0)))
-            if t.shape[0] < n or t.shape[1] != cols or pitch[-1] < cols:
-                raise ValueError("kv_fork takes two block tables of as many columns, a row of its own for each request")
-        _flat(int32, n_in, len_in)
-        _flat(int32, n_out, source, len_new, len_out, copy_from, copy_to, copy_tokens)
-        _flat(int32, 1, free_in, free_out)
-        _flat(int32, extra.numel(), extra)
-        _flat(int32, free_pages.numel(), free_pages)
+        _check_table(table_in)
+        _check_table(table_out)
+        n_in, n_out, (rows_in, cols), (rows_out, cols_out) = len_in.numel(), source.numel(), table_in.shape, table_out.shape
+        pitch = [t.stride(0) if rows > 1 else max(cols, t.stride(0)) for t, rows in ((table_in, rows_in), (table_out, rows_out))]
+        if rows_in < n_in or rows_out < n_out or cols_out != cols or min(pitch) < cols:
+            raise ValueError("kv_fork takes two block tables of as many columns, a row of its own for each request")
+        if not (len_in.dtype is source.dtype is len_out.dtype is copy_from.dtype is copy_to.dtype is copy_tokens.dtype
+                is extra.dtype is free_pages.dtype is free_in.dtype is free_out.dtype is self._dtypes()[1]
+                and len_out.nbytes == copy_from.nbytes == copy_to.nbytes == copy_tokens.nbytes == 4 * n_out
+                and free_in.nbytes == free_out.nbytes == 4
+                and len_in.is_contiguous() and source.is_contiguous() and len_out.is_contiguous()
+                and copy_from.is_contiguous() and copy_to.is_contiguous() and copy_tokens.is_contiguous()
+                and extra.is_contiguous() and free_pages.is_contiguous()):
+            raise ValueError("kv_fork takes consecutive int32 elements: lengths of the old rows; sources, lengths and "
+                             "copies of the new ones; a count for each page; the free list and its count")
+        if len_new is not None:
+            _flat(self._dtypes()[1], n_out, len_new)
         scute_kv_fork(self.handle, table_in, len_in, pitch[0], source, len_new, table_out, len_out, pitch[1], n_in, n_out,
                       cols, page_size, extra.numel(), extra, free_pages, free_pages.numel(), free_in, free_out, copy_from,
                       copy_to, copy_tokens, stream)

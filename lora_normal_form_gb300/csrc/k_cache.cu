@@ -675,10 +675,16 @@ __global__ void __launch_bounds__(256) kv_append_norm_kernel(const AppendArgs a,
 
 // 16 bytes at a time, items as in kv_append_vec_kernel; a head is `lanes` neighbouring
 // lanes' (a power of two, so that they add up by shuffles), NI items each.  Every lane
-// of a warp goes through the same number of heads.
+// of a warp goes through the same number of heads; the next ones are on their way while
+// these are worked on.  Weights enter the cosines and sines: of a pair (a, b) with weights
+// (w, v) and the head's factor f,
+//     a' = f (a (w cos) - b (v sin)),   b' = f (b (v cos) + a (w sin)),
+// four products of the item's own that are formed anew only where queries end and keys
+// begin (with weights for each head, at every head).
+constexpr int NORM_CTAS = 2;
 template <typename T, typename KV, int NI>
-__global__ void __launch_bounds__(256) kv_append_norm_vec_kernel(const AppendArgs a, const HeadNormArgs w, int per_row,
-                                                                 int lanes) {
+__global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(const AppendArgs a, const HeadNormArgs w, int per_row,
+                                                                            int lanes) {
     constexpr int VE = Piece<T>::N, U = 2;
     constexpr unsigned ALL = 0xffffffffu;
     const int rows = blockDim.x / per_row, sub = threadIdx.x / per_row, t = threadIdx.x - sub * per_row;
@@ -686,7 +692,7 @@ __global__ void __launch_bounds__(256) kv_append_norm_vec_kernel(const AppendArg
     if (row >= a.n) return;                             // whole warps: a row has 64 threads or more
     const int dim = a.kv.dim, half = a.rot / 2;
     const int joined = a.interleaved ? 0 : half / VE;
-    const int items = dim / VE - joined, heads = a.q_heads + 2 * a.kv.heads;
+    const int items = dim / VE - joined, heads = a.q_heads + 2 * a.kv.heads, k_end = a.q_heads + a.kv.heads;
     const int stride = per_row / lanes, li = t & (lanes - 1), h_first = t / lanes;
     int d0[NI], d1[NI];
     bool here[NI], two[NI], turned[NI];
@@ -701,13 +707,12 @@ __global__ void __launch_bounds__(256) kv_append_norm_vec_kernel(const AppendArg
     }
     const T *const q_row = reinterpret_cast<const T *>(a.q) + row * a.q_stride;
     const T *const k_row = reinterpret_cast<const T *>(a.k) + row * a.k_stride - a.q_heads * dim;
-    const T *const v_row = reinterpret_cast<const T *>(a.v) + row * a.v_stride - (a.q_heads + a.kv.heads) * dim;
-    uint4 x0[U][NI], x1[U][NI];
-    auto load = [&](int from) {
+    const T *const v_row = reinterpret_cast<const T *>(a.v) + row * a.v_stride - k_end * dim;
+    auto load = [&](int from, uint4 (&x0)[U][NI], uint4 (&x1)[U][NI]) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int hh = from + u * stride;
-            const T *src = (hh < a.q_heads ? q_row : hh < a.q_heads + a.kv.heads ? k_row : v_row) + hh * dim;
+            const T *src = (hh < a.q_heads ? q_row : hh < k_end ? k_row : v_row) + hh * dim;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 x0[u][i] = x1[u][i] = make_uint4(0, 0, 0, 0);
@@ -720,13 +725,16 @@ __global__ void __launch_bounds__(256) kv_append_norm_vec_kernel(const AppendArg
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int slot = a.slot_map[row];
-    load(h_first);
+    uint4 x0[U][NI], x1[U][NI];
+    load(h_first, x0, x1);
 
-    // the items' cosines and sines
+    // the items' cosines and sines (of pairs of neighbours where they are interleaved)
     float c[NI][VE], s[NI][VE];
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) c[i][e] = 1.f, s[i][e] = 0.f;
         if (!turned[i]) continue;
         const int pairs = two[i] ? VE : VE / 2, p0 = two[i] ? d0[i] : d0[i] / 2;
         auto axis_of = [&](int e) { return (e >= a.bound[0]) + (e >= a.bound[1]) + (e >= a.bound[2]); };
@@ -767,81 +775,119 @@ __global__ void __launch_bounds__(256) kv_append_norm_vec_kernel(const AppendArg
 
     T *const q_to = reinterpret_cast<T *>(a.q_out) + row * a.q_out_stride;
     KV *const k_to = reinterpret_cast<KV *>(a.kv.k) + at - a.q_heads * a.kv.head_stride;
-    KV *const v_to = reinterpret_cast<KV *>(a.kv.v) + at - (a.q_heads + a.kv.heads) * a.kv.head_stride;
+    KV *const v_to = reinterpret_cast<KV *>(a.kv.v) + at - k_end * a.kv.head_stride;
+
+    // coefficients of the first and the second piece's elements: with pairs (i, i + half)
+    // y0 = x0 ca - x1 sb, y1 = x1 cb + x0 sa; with neighbours the same within x0
+    float ca[NI][VE], sb[NI][VE], cb[NI][VE], sa[NI][VE];
+    const float *with = nullptr;               // the weights that are in them
+    bool ready = false;
+    auto coefficients = [&](const float *weight) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            float w0[VE], w1[VE];
+#pragma unroll
+            for (int e = 0; e < VE; ++e) w0[e] = w1[e] = 1.f;
+            if (weight && here[i]) {
+#pragma unroll
+                for (int e = 0; e < VE; e += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(weight + d0[i] + e);
+                    w0[e] = x.x, w0[e + 1] = x.y, w0[e + 2] = x.z, w0[e + 3] = x.w;
+                    if (!two[i]) continue;
+                    const float4 y = *reinterpret_cast<const float4 *>(weight + d1[i] + e);
+                    w1[e] = y.x, w1[e + 1] = y.y, w1[e + 2] = y.z, w1[e + 3] = y.w;
+                }
+            }
+            if (a.interleaved) {               // pair e: elements 2e and 2e + 1 (cosine 1 and sine 0 behind the turned ones)
+#pragma unroll
+                for (int e = 0; e < VE / 2; ++e) {
+                    ca[i][e] = w0[2 * e] * c[i][e], sb[i][e] = w0[2 * e + 1] * s[i][e];
+                    cb[i][e] = w0[2 * e + 1] * c[i][e], sa[i][e] = w0[2 * e] * s[i][e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    ca[i][e] = w0[e] * c[i][e], sb[i][e] = w1[e] * s[i][e];
+                    cb[i][e] = w1[e] * c[i][e], sa[i][e] = w0[e] * s[i][e];
+                }
+            }
+        }
+        with = weight;
+        ready = true;
+    };
     for (int h0 = 0;; h0 += U * stride) {
+        const bool more = h0 + U * stride < heads;
+        uint4 n0[U][NI], n1[U][NI];
+        if (more) load(h0 + U * stride + h_first, n0, n1);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int hh = h0 + h_first + u * stride;
-            const bool is_q = hh < a.q_heads, is_v = hh >= a.q_heads + a.kv.heads;
-            const float *weight = is_q ? w.q_w : is_v ? nullptr : w.k_w;
+            const bool is_q = hh < a.q_heads, is_v = hh >= k_end;
             float y0[NI][VE], y1[NI][VE];
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 Piece<T>::open(x0[u][i], y0[i]);
                 Piece<T>::open(x1[u][i], y1[i]);
             }
+            const float *weight = is_q ? w.q_w : is_v ? nullptr : w.k_w;
+            float f = 1.f;
             if (__any_sync(ALL, weight != nullptr)) {
                 auto total = [&](float z) {
                     for (int o = lanes >> 1; o; o >>= 1) z += __shfl_xor_sync(ALL, z, o);
                     return z;
                 };
-                float mean = 0.f, sum = 0.f;
                 if (w.layer) {
+                    float mean = 0.f;
 #pragma unroll
                     for (int i = 0; i < NI; ++i)
 #pragma unroll
                         for (int e = 0; e < VE; ++e) mean += y0[i][e] + y1[i][e];
                     mean = total(mean) / dim;
+                    if (weight)
+#pragma unroll
+                        for (int i = 0; i < NI; ++i)
+#pragma unroll
+                            for (int e = 0; e < VE; ++e) {
+                                if (here[i]) y0[i][e] -= mean;
+                                if (two[i]) y1[i][e] -= mean;
+                            }
                 }
+                float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        const float z0 = here[i] ? y0[i][e] - mean : 0.f, z1 = two[i] ? y1[i][e] - mean : 0.f;
-                        sum += z0 * z0 + z1 * z1;
-                    }
-                const float f = 1.f / sqrtf(total(sum) / dim + w.eps);
-                if (weight && hh < heads) {
-                    weight += is_q ? hh * w.q_stride : (hh - a.q_heads) * w.k_stride;
+                    for (int e = 0; e < VE; ++e) sum += y0[i][e] * y0[i][e] + y1[i][e] * y1[i][e];
+                sum = total(sum);
+                if (weight) f = 1.f / sqrtf(sum / dim + w.eps);
+            }
+            if (hh >= heads || (!is_q && !in)) continue;
+            if (!is_v) {
+                if (weight) weight += is_q ? hh * w.q_stride : (hh - a.q_heads) * w.k_stride;
+                if (!ready || weight != with) coefficients(weight);
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) {
-                        if (!here[i]) continue;
+                for (int i = 0; i < NI; ++i) {
+                    if (a.interleaved) {
 #pragma unroll
-                        for (int e = 0; e < VE; e += 4) {
-                            const float4 g = *reinterpret_cast<const float4 *>(weight + d0[i] + e);
-                            y0[i][e] = (y0[i][e] - mean) * f * g.x, y0[i][e + 1] = (y0[i][e + 1] - mean) * f * g.y;
-                            y0[i][e + 2] = (y0[i][e + 2] - mean) * f * g.z, y0[i][e + 3] = (y0[i][e + 3] - mean) * f * g.w;
-                            if (!two[i]) continue;
-                            const float4 k = *reinterpret_cast<const float4 *>(weight + d1[i] + e);
-                            y1[i][e] = (y1[i][e] - mean) * f * k.x, y1[i][e + 1] = (y1[i][e + 1] - mean) * f * k.y;
-                            y1[i][e + 2] = (y1[i][e + 2] - mean) * f * k.z, y1[i][e + 3] = (y1[i][e + 3] - mean) * f * k.w;
+                        for (int e = 0; e < VE / 2; ++e) {
+                            const float z = y0[i][2 * e] * ca[i][e] - y0[i][2 * e + 1] * sb[i][e];
+                            y0[i][2 * e + 1] = (y0[i][2 * e + 1] * cb[i][e] + y0[i][2 * e] * sa[i][e]) * f;
+                            y0[i][2 * e] = z * f;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) {
+                            const float z = y0[i][e] * ca[i][e] - y1[i][e] * sb[i][e];
+                            y1[i][e] = (y1[i][e] * cb[i][e] + y0[i][e] * sa[i][e]) * f;
+                            y0[i][e] = z * f;
                         }
                     }
                 }
             }
-            if (hh >= heads || (!is_q && !in)) continue;
             const float *scale = is_q ? nullptr : is_v ? a.kv.v_scale : a.kv.k_scale;
-            const float div = scale ? scale[hh - a.q_heads - (is_v ? a.kv.heads : 0)] : 1.f;
+            const float div = scale ? scale[is_v ? hh - k_end : hh - a.q_heads] : 1.f;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 if (!here[i]) continue;
-                if (turned[i] && !is_v) {
-                    if (two[i]) {
-#pragma unroll
-                        for (int e = 0; e < VE; ++e) {
-                            const float z = y0[i][e] * c[i][e] - y1[i][e] * s[i][e];
-                            y1[i][e] = y1[i][e] * c[i][e] + y0[i][e] * s[i][e];
-                            y0[i][e] = z;
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < VE / 2; ++e) {
-                            const float z = y0[i][2 * e] * c[i][e] - y0[i][2 * e + 1] * s[i][e];
-                            y0[i][2 * e + 1] = y0[i][2 * e + 1] * c[i][e] + y0[i][2 * e] * s[i][e];
-                            y0[i][2 * e] = z;
-                        }
-                    }
-                }
                 if (is_q) {
                     T *dst = q_to + hh * dim;
                     Piece<T>::store(dst + d0[i], y0[i]);
@@ -857,8 +903,11 @@ __global__ void __launch_bounds__(256) kv_append_norm_vec_kernel(const AppendArg
                 if (two[i]) Piece<T>::store(dst + d1[i], y1[i]);
             }
         }
-        if (h0 + U * stride >= heads) break;
-        load(h0 + U * stride + h_first);
+        if (!more) break;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < NI; ++i) x0[u][i] = n0[u][i], x1[u][i] = n1[u][i];
     }
 }
 

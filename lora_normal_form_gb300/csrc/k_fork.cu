@@ -273,44 +273,70 @@ __global__ void __launch_bounds__(FK_THREADS) fork_step_kernel(const ForkArgs a)
     if (STEP == 3) fork_assign(a, blockIdx.x, gridDim.x, s);
 }
 
-// ---------------------------------------------------------------- kv_copy
-// A CTA takes one row's page in one pool, 16 bytes to a thread at a time, in the order
-// in which the page's tokens and heads lie.
-constexpr int CP_THREADS = 256;
-__global__ void __launch_bounds__(CP_THREADS) kv_copy_kernel(const PageCopyArgs a) {
+// All four by one cluster, its barrier between them: where there is little to do, four
+// launches cost more than the step.
+constexpr int FK_CLUSTER = 8;
+__global__ void __cluster_dims__(FK_CLUSTER, 1, 1) __launch_bounds__(FK_THREADS) fork_cluster_kernel(const ForkArgs a) {
+    __shared__ AssignShared s;
+    const int cta = blockIdx.x;
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
-    const int i = blockIdx.x, to = a.to[i];
-    if (to == -1) return;
-    const int from = a.from[i];
-    int tokens = a.tokens ? a.tokens[i] : a.page_size;
+    auto all_done = [] {
+        __threadfence();
+        ptx::cluster_sync();
+    };
+    fork_count(a, cta, FK_CLUSTER);
+    all_done();
+    fork_claim(a, cta, FK_CLUSTER);
+    all_done();
+    fork_settle(a, cta, FK_CLUSTER, s.warp_sum);
+    all_done();
+    fork_assign(a, cta, FK_CLUSTER, s);
+}
+
+// ---------------------------------------------------------------- kv_copy
+// A CTA looks through `each` rows and copies the pages of those that have one, in one
+// pool, 16 bytes to a thread at a time, in the order in which the page's tokens and heads
+// lie.
+constexpr int CP_THREADS = 256, CP_ROWS = 32;
+__global__ void __launch_bounds__(CP_THREADS) kv_copy_kernel(const PageCopyArgs a, int each) {
+    const int lane = threadIdx.x & 31;
+    ptx::grid_dep_wait();
+    ptx::grid_dep_launch();
+    const int r0 = blockIdx.x * each, mine = r0 + lane;
+    const bool asked = lane < each && mine < a.n;
+    const int to = asked ? a.to[mine] : -1, from = asked && to != -1 ? a.from[mine] : -1;
+    int tokens = asked && a.tokens ? a.tokens[mine] : a.page_size;
     const bool out = (unsigned)from >= (unsigned)a.n_pages || (unsigned)to >= (unsigned)a.n_pages;
-    if ((out || tokens < 0 || tokens > a.page_size) && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, STATUS_PAGES);
-    if (out) return;
+    if (to != -1 && (out || tokens < 0 || tokens > a.page_size) && threadIdx.x < 32 && blockIdx.y == 0) atomicOr(a.status, STATUS_PAGES);
     tokens = tokens < 0 ? 0 : min(tokens, a.page_size);
-    char *pool = static_cast<char *>(a.pool[blockIdx.y]);
-    const char *src = pool + from * a.page_bytes;
-    char *dst = pool + to * a.page_bytes;
+    char *const pool = static_cast<char *>(a.pool[blockIdx.y]);
     // rows of one token and head, the inner of the two the one with the smaller stride
     const bool token_in = a.token_bytes < a.head_bytes;
-    const int pieces = a.row_bytes / 16, inner = token_in ? tokens : a.heads;
     const long long in_step = token_in ? a.token_bytes : a.head_bytes, out_step = token_in ? a.head_bytes : a.token_bytes;
-    const long long all = (long long)tokens * a.heads * pieces;
+    const unsigned pieces = a.row_bytes / 16;
     constexpr int U = 4;
-    for (long long e0 = threadIdx.x; e0 < all; e0 += U * CP_THREADS) {
-        uint4 x[U];
-        long long at[U];
+    for (unsigned left = __ballot_sync(0xffffffffu, !out); left; left &= left - 1) {
+        const int k = __ffs(left) - 1;
+        const char *src = pool + __shfl_sync(0xffffffffu, from, k) * a.page_bytes;
+        char *dst = pool + __shfl_sync(0xffffffffu, to, k) * a.page_bytes;
+        const unsigned count = __shfl_sync(0xffffffffu, tokens, k), inner = token_in ? count : a.heads;
+        const unsigned all = count * a.heads * pieces;              // (below 2^31, by the call's checks)
+        for (unsigned e0 = threadIdx.x; e0 < all; e0 += U * CP_THREADS) {
+            uint4 x[U];
+            long long at[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long e = e0 + u * CP_THREADS;
-            if (e >= all) continue;
-            const long long row = e / pieces, o = row / inner;
-            at[u] = o * out_step + (row - o * inner) * in_step + (e - row * pieces) * 16;
-            x[u] = *reinterpret_cast<const uint4 *>(src + at[u]);
+            for (int u = 0; u < U; ++u) {
+                const unsigned e = e0 + u * CP_THREADS;
+                if (e >= all) continue;
+                const unsigned row = e / pieces, o = row / inner;
+                at[u] = o * out_step + (row - o * inner) * in_step + (e - row * pieces) * 16;
+                x[u] = *reinterpret_cast<const uint4 *>(src + at[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (e0 + u * CP_THREADS < all) *reinterpret_cast<uint4 *>(dst + at[u]) = x[u];
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (e0 + u * CP_THREADS < all) *reinterpret_cast<uint4 *>(dst + at[u]) = x[u];
     }
 }
 
@@ -321,7 +347,12 @@ cudaError_t launch_kv_fork(const ForkArgs &a, int num_sms, int *launches, cudaSt
     const long long rows = max(a.n_in, a.n_out), items = rows * ((a.cols + FK_SPAN - 1) / FK_SPAN);
     const int most = min(num_sms, FORK_MAX_CTAS);
     const int row_grid = max(1, min(most, (a.n_out + FK_THREADS - 1) / FK_THREADS));
-    const int page_grid = max(row_grid, (int)min((long long)most, ((long long)a.n_pages + 4 * FK_THREADS - 1) / (4 * FK_THREADS)));
+    const int page_grid = max(row_grid, (int)min((long long)most, ((long long)a.n_pages + FK_THREADS - 1) / FK_THREADS));
+    // one cluster up to as many table spans and pages as its warps take in a few turns
+    if (items <= 4 * FK_CLUSTER * warps && a.n_pages <= 16 * FK_CLUSTER * FK_THREADS) {
+        *launches = 1;
+        return launch_chained(fork_cluster_kernel, FK_CLUSTER, FK_THREADS, 0, st, a);
+    }
     *launches = 4;
     cudaError_t e = launch_chained(fork_step_kernel<0>, (int)max(1ll, min(4ll * most, (items + warps - 1) / warps)), FK_THREADS, 0, st, a);
     if (e == cudaSuccess) e = launch_chained(fork_step_kernel<1>, row_grid, FK_THREADS, 0, st, a);
@@ -332,7 +363,10 @@ cudaError_t launch_kv_fork(const ForkArgs &a, int num_sms, int *launches, cudaSt
 
 cudaError_t launch_kv_copy(const PageCopyArgs &a, int num_sms, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.n, (unsigned)a.pools, 1);
+    // rows that copy nothing cost a look: many of them to a CTA where there are many
+    const long long blocks = (long long)a.n * a.pools, wanted = 8ll * num_sms;
+    const int each = (int)max(1ll, min((long long)CP_ROWS, blocks / wanted));
+    cfg.gridDim = dim3((unsigned)((a.n + each - 1) / each), (unsigned)a.pools, 1);
     cfg.blockDim = dim3(CP_THREADS, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -340,7 +374,7 @@ cudaError_t launch_kv_copy(const PageCopyArgs &a, int num_sms, cudaStream_t st) 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_copy_kernel, a);
+    return cudaLaunchKernelEx(&cfg, kv_copy_kernel, a, each);
 }
 
 }  // namespace scute

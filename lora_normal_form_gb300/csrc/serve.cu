@@ -424,6 +424,8 @@ scute_status scute_kv_copy(scute_ctx *c, const scute_kv_cache *caches, int n_cac
             return fail(c, SCUTE_ERR_SHAPE, "cache %d is not of the first one's type, size and strides", i);
     }
     if (s) return s;
+    if ((int64_t)one.page_size * one.heads * (one.dim * kv_esz(one.dtype) / 16) > 0x7fffffff)
+        return fail(c, SCUTE_ERR_UNSUPPORTED, "a page of %d tokens of %d heads is beyond 2^31 - 1 pieces of 16 bytes", one.page_size, one.heads);
     if (n == 0) return SCUTE_OK;
     if (!copy_from || !copy_to) return fail(c, SCUTE_ERR_ARG, "null argument");
     DeviceGuard dg(c->device);
