@@ -675,13 +675,8 @@ __global__ void __launch_bounds__(256) kv_append_norm_kernel(const AppendArgs a,
 
 // 16 bytes at a time, items as in kv_append_vec_kernel; a head is `lanes` neighbouring
 // lanes' (a power of two, so that they add up by shuffles), NI items each.  Every lane
-// of a warp goes through the same number of heads; the next ones are on their way while
-// these are worked on.  Weights enter the cosines and sines: of a pair (a, b) with weights
-// (w, v) and the head's factor f,
-//     a' = f (a (w cos) - b (v sin)),   b' = f (b (v cos) + a (w sin)),
-// four products of the item's own that are formed anew only where queries end and keys
-// begin (with weights for each head, at every head).
-constexpr int NORM_CTAS = 2;
+// of a warp goes through the same number of heads.
+constexpr int NORM_CTAS = 4;
 template <typename T, typename KV, int NI>
 __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(const AppendArgs a, const HeadNormArgs w, int per_row,
                                                                             int lanes) {
@@ -733,8 +728,6 @@ __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(cons
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) c[i][e] = 1.f, s[i][e] = 0.f;
         if (!turned[i]) continue;
         const int pairs = two[i] ? VE : VE / 2, p0 = two[i] ? d0[i] : d0[i] / 2;
         auto axis_of = [&](int e) { return (e >= a.bound[0]) + (e >= a.bound[1]) + (e >= a.bound[2]); };
@@ -777,48 +770,8 @@ __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(cons
     KV *const k_to = reinterpret_cast<KV *>(a.kv.k) + at - a.q_heads * a.kv.head_stride;
     KV *const v_to = reinterpret_cast<KV *>(a.kv.v) + at - k_end * a.kv.head_stride;
 
-    // coefficients of the first and the second piece's elements: with pairs (i, i + half)
-    // y0 = x0 ca - x1 sb, y1 = x1 cb + x0 sa; with neighbours the same within x0
-    float ca[NI][VE], sb[NI][VE], cb[NI][VE], sa[NI][VE];
-    const float *with = nullptr;               // the weights that are in them
-    bool ready = false;
-    auto coefficients = [&](const float *weight) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            float w0[VE], w1[VE];
-#pragma unroll
-            for (int e = 0; e < VE; ++e) w0[e] = w1[e] = 1.f;
-            if (weight && here[i]) {
-#pragma unroll
-                for (int e = 0; e < VE; e += 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(weight + d0[i] + e);
-                    w0[e] = x.x, w0[e + 1] = x.y, w0[e + 2] = x.z, w0[e + 3] = x.w;
-                    if (!two[i]) continue;
-                    const float4 y = *reinterpret_cast<const float4 *>(weight + d1[i] + e);
-                    w1[e] = y.x, w1[e + 1] = y.y, w1[e + 2] = y.z, w1[e + 3] = y.w;
-                }
-            }
-            if (a.interleaved) {               // pair e: elements 2e and 2e + 1 (cosine 1 and sine 0 behind the turned ones)
-#pragma unroll
-                for (int e = 0; e < VE / 2; ++e) {
-                    ca[i][e] = w0[2 * e] * c[i][e], sb[i][e] = w0[2 * e + 1] * s[i][e];
-                    cb[i][e] = w0[2 * e + 1] * c[i][e], sa[i][e] = w0[2 * e] * s[i][e];
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < VE; ++e) {
-                    ca[i][e] = w0[e] * c[i][e], sb[i][e] = w1[e] * s[i][e];
-                    cb[i][e] = w1[e] * c[i][e], sa[i][e] = w0[e] * s[i][e];
-                }
-            }
-        }
-        with = weight;
-        ready = true;
-    };
     for (int h0 = 0;; h0 += U * stride) {
         const bool more = h0 + U * stride < heads;
-        uint4 n0[U][NI], n1[U][NI];
-        if (more) load(h0 + U * stride + h_first, n0, n1);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int hh = h0 + h_first + u * stride;
@@ -863,22 +816,32 @@ __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(cons
             if (hh >= heads || (!is_q && !in)) continue;
             if (!is_v) {
                 if (weight) weight += is_q ? hh * w.q_stride : (hh - a.q_heads) * w.k_stride;
-                if (!ready || weight != with) coefficients(weight);
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
+                    if (weight && here[i]) {
+#pragma unroll
+                        for (int e = 0; e < VE; e += 4) {
+                            const float4 x = *reinterpret_cast<const float4 *>(weight + d0[i] + e);
+                            y0[i][e] *= x.x * f, y0[i][e + 1] *= x.y * f, y0[i][e + 2] *= x.z * f, y0[i][e + 3] *= x.w * f;
+                            if (!two[i]) continue;
+                            const float4 y = *reinterpret_cast<const float4 *>(weight + d1[i] + e);
+                            y1[i][e] *= y.x * f, y1[i][e + 1] *= y.y * f, y1[i][e + 2] *= y.z * f, y1[i][e + 3] *= y.w * f;
+                        }
+                    }
+                    if (!turned[i]) continue;
                     if (a.interleaved) {
 #pragma unroll
                         for (int e = 0; e < VE / 2; ++e) {
-                            const float z = y0[i][2 * e] * ca[i][e] - y0[i][2 * e + 1] * sb[i][e];
-                            y0[i][2 * e + 1] = (y0[i][2 * e + 1] * cb[i][e] + y0[i][2 * e] * sa[i][e]) * f;
-                            y0[i][2 * e] = z * f;
+                            const float z = y0[i][2 * e] * c[i][e] - y0[i][2 * e + 1] * s[i][e];
+                            y0[i][2 * e + 1] = y0[i][2 * e + 1] * c[i][e] + y0[i][2 * e] * s[i][e];
+                            y0[i][2 * e] = z;
                         }
                     } else {
 #pragma unroll
                         for (int e = 0; e < VE; ++e) {
-                            const float z = y0[i][e] * ca[i][e] - y1[i][e] * sb[i][e];
-                            y1[i][e] = (y1[i][e] * cb[i][e] + y0[i][e] * sa[i][e]) * f;
-                            y0[i][e] = z * f;
+                            const float z = y0[i][e] * c[i][e] - y1[i][e] * s[i][e];
+                            y1[i][e] = y1[i][e] * c[i][e] + y0[i][e] * s[i][e];
+                            y0[i][e] = z;
                         }
                     }
                 }
@@ -904,10 +867,7 @@ __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(cons
             }
         }
         if (!more) break;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < NI; ++i) x0[u][i] = n0[u][i], x1[u][i] = n1[u][i];
+        load(h0 + U * stride + h_first, x0, x1);
     }
 }
 
