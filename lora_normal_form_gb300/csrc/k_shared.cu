@@ -136,12 +136,30 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32])
         : "memory");
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// D (+)= A B^T with A in tensor memory.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+// The products and their commits are issued by one elected thread of a whole warp (one
+// that has branched off issues them three times as slowly where other warps compute: its
+// operands go through the warp's own registers; measured, 16 products under FMAs 3.3
+// against 0.9 thousand cycles).
+// D (+)= A B^T from shared memory, and with A in tensor memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "{\n\t.reg .pred p, one;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|one, 0xffffffff;\n\t"
+        "@one tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+    asm volatile(
+        "{\n\t.reg .pred p, one;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|one, 0xffffffff;\n\t"
+        "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
+}
+// Arrive once on `bar` when the products before are done.
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred one;\n\telect.sync _|one, 0xffffffff;\n\t"
+        "@one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
         : "memory");
 }
 // A slab is 64 elements (128 bytes) of each of 128 rows, 8 rows a 1024-byte atom whose
@@ -419,7 +437,9 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
     ptx::grid_dep_launch();
     make_plan(a, p);                       // (its barriers order what was written above)
     ptx::tc_fence_after();
-    const uint32_t tmem = b.tmem;
+    // a number that every lane has, as one that the whole warp has
+    auto same = [](auto y) { return __shfl_sync(ALL, y, 0); };
+    const uint32_t tmem = same(b.tmem);
     const Cut cut(a, p);
     const int cta = blockIdx.x;
     Walk w(a, p, cut, cta);
@@ -428,7 +448,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
         // ------------------------------------------------ a stream: its softmax, a thread to a row; its first
         // warp issues its products
         constexpr uint32_t QK = instr_desc(TT, false), PV = instr_desc(DC, true);
-        const int x = warp >> 2, i = (warp & 3) * 32 + lane;
+        const int x = same(warp >> 2), i = (warp & 3) * 32 + lane;
         const bool issues = (warp & 3) == 0;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_col = tmem + S_COL + x * TT, o_col = tmem + O_COL + x * DC, s_at = s_col + lanes, o_at = o_col + lanes;
@@ -460,19 +480,16 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                 const int slot = slot_of(t);
                 live = wait_bar(bar(b.kfull[slot]), phase_of(t), abort_flag);
                 if (!live) return;
-                if (lane == 0) {
-                    ptx::tc_fence_after();
-                    const uint64_t qd = slab_desc(q_at + (twin ? 0 : x) * TB, 16), kd = slab_desc(k_at + slot * TB, 16);
+                ptx::tc_fence_after();
+                const uint64_t qd = same(slab_desc(q_at + (twin ? 0 : x) * TB, 16)), kd = same(slab_desc(k_at + slot * TB, 16));
 #pragma unroll
-                    for (int k = 0; k < DC / 16; ++k) {
-                        const uint32_t off = ((k / 4) * SLAB + (k % 4) * 32) >> 4;
-                        ptx::mma_bf16(s_col, qd + off, kd + off, QK, k > 0);
-                    }
-                    ptx::mma_commit(bar(b.sfull[x]));
-                    for (int k = 0; k < uses; ++k) ptx::mma_commit(bar(b.kempty[slot]));
-                    if (t + step >= w.t1) ptx::mma_commit(bar(b.qempty));
+                for (int k = 0; k < DC / 16; ++k) {
+                    const uint32_t off = ((k / 4) * SLAB + (k % 4) * 32) >> 4;
+                    mma_ss(s_col, qd + off, kd + off, QK, k > 0);
                 }
-                __syncwarp();
+                commit(bar(b.sfull[x]));
+                for (int k = 0; k < uses; ++k) commit(bar(b.kempty[slot]));
+                if (t + step >= w.t1) commit(bar(b.qempty));
             };
             // Tile t's values, which the other stream takes, have come.  Both streams see every
             // filling of a slot before it is given back: its barrier's parity tells only two
@@ -586,19 +603,16 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                 live = wait_bar(bar(b.pfull[x]), p_phase, abort_flag) && wait_bar(bar(b.vfull[slot]), phase_of(t), abort_flag) && my_turn();
                 if (!live) break;
                 p_phase ^= 1;
-                if (lane == 0) {
-                    ptx::tc_fence_after();
-                    const uint64_t vd = slab_desc(v_at + slot * TB, SLAB);
+                ptx::tc_fence_after();
+                const uint64_t vd = same(slab_desc(v_at + slot * TB, SLAB));
 #pragma unroll
-                    for (int k = 0; k < TT / 16; ++k) {
-                        const uint32_t col = s_col + (k / 2) * 32 + (k % 2) * 8;
-                        mma_bf16_ta(o_col, col, vd + k * (2048 >> 4), PV, adds || k > 0);
-                        mma_bf16_ta(o_col, col + 16, vd + k * (2048 >> 4), PV, 1);
-                    }
-                    ptx::mma_commit(bar(b.vempty[slot]));
-                    if (t + step >= w.t1) ptx::mma_commit(bar(b.ofull[x]));
+                for (int k = 0; k < TT / 16; ++k) {
+                    const uint32_t col = s_col + (k / 2) * 32 + (k % 2) * 8;
+                    mma_ts(o_col, col, vd + k * (2048 >> 4), PV, adds || k > 0);
+                    mma_ts(o_col, col + 16, vd + k * (2048 >> 4), PV, 1);
                 }
-                __syncwarp();
+                commit(bar(b.vempty[slot]));
+                if (t + step >= w.t1) commit(bar(b.ofull[x]));
                 if (t + step < w.t1) scores(t + step);
                 if (!live) break;
                 pass_turn();
@@ -639,8 +653,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
         if (first_row) write_pieces(a, p, cut);
         if (issues) {
             // nothing may be under way when tensor and shared memory are given back
-            if (lane == 0) ptx::mma_commit(bar(b.drain));
-            __syncwarp();
+            commit(bar(b.drain));
             const uint64_t t0 = ptx::globaltimer();
             while (!__all_sync(ALL, ptx::mbar_try_wait(bar(b.drain), 0)) && __all_sync(ALL, ptx::globaltimer() - t0 < WAIT_NS)) {}
         }
