@@ -94,6 +94,27 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
     return y;
 }
+// Two 32-bit numbers side by side, and operations on both.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+    uint64_t y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(lo), "f"(hi));
+    return y;
+}
+__device__ __forceinline__ float2 apart(uint64_t x) {
+    float2 y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t fma_two(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+    return y;
+}
+__device__ __forceinline__ uint64_t add_two(uint64_t a, uint64_t b) {
+    uint64_t y;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
 __device__ __noinline__ float capped(float x, float cap) { return cap * LOG2E * tanhf(x / cap); }
 // Two e4m3 values (16 bits of a word) as two bf16 ones, exactly: 4 bits of significand.
 __device__ __forceinline__ uint32_t to_bf16(uint32_t pair) {
@@ -512,7 +533,8 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
             first_row = false;
             const float scale = (a.kv.k_scale ? a.kv.k_scale[w.w.hk] : 1.f) * a.scale;
             const float mul = a.softcap > 0.f ? scale : scale * LOG2E;
-            float top = -INFINITY, sum[4] = {0.f, 0.f, 0.f, 0.f};
+            float top = -INFINITY;
+            uint64_t sum[2] = {0, 0};                          // of the even and the odd tokens' weights, each in two
             bool any = false;
             for (int t = t_first; t < w.t1; t += step) {
                 live = (!issues || !twin || t == w.t0 || seen_values(t - 1)) && wait_bar(bar(b.sfull[x]), s_phase, abort_flag);
@@ -541,24 +563,35 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                     tmem_stored();
                     f = 1.f;
                 }
-                float mx = -INFINITY;
+                // (a negative factor turns the scores' order round)
+                const float sign = f < 0.f ? -1.f : 1.f;
+                float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto take = [&](const uint32_t (&y)[32]) {
+                    if (f < 0.f) {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2)
+                            most[k / 2 & 3] = fmaxf(fmaxf(-__uint_as_float(y[k]), -__uint_as_float(y[k + 1])), most[k / 2 & 3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2)
+                            most[k / 2 & 3] = fmaxf(fmaxf(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), most[k / 2 & 3]);
+                    }
+                };
                 tmem_load(s_at, r);
 #pragma unroll
                 for (int c = 0; c < TT / 32; c += 2) {
                     tmem_loaded(r);
                     tmem_load(s_at + (c + 1) * 32, r2);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(r[k]) * f);
+                    take(r);
                     tmem_loaded(r2);
                     if (c + 2 < TT / 32) tmem_load(s_at + (c + 2) * 32, r);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(r2[k]) * f);
+                    take(r2);
                 }
+                const float mx = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) * (f * sign);
                 if (__any_sync(ALL, mx > top + 8.f)) {
                     const float to = fmaxf(mx, top), al = to == top ? 1.f : exp2f(top - to);
                     top = to;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) sum[k] *= al;
+                    sum[0] = fma_two(sum[0], two(al, al), 0), sum[1] = fma_two(sum[1], two(al, al), 0);
                     if (any) {
 #pragma unroll 1
                         for (int c = 0; c < DC / 32; ++c) {
@@ -574,6 +607,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                 const bool adds = any;
                 any = true;
                 const float ref = top == -INFINITY ? 0.f : top;
+                const uint64_t f2 = two(f, f), ref2 = two(-ref, -ref);
                 tmem_load(s_at, r);
 #pragma unroll
                 for (int c = 0; c < TT / 32; ++c) {
@@ -584,13 +618,14 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                     uint32_t w2[32];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        const float p0 = pow2(fmaf(__uint_as_float(now[2 * k]), f, -ref));
-                        const float p1 = pow2(fmaf(__uint_as_float(now[2 * k + 1]), f, -ref));
-                        sum[k & 1] += p0;
-                        sum[2 + (k & 1)] += p1;
+                        const float2 e = apart(fma_two(two(__uint_as_float(now[2 * k]), __uint_as_float(now[2 * k + 1])), f2, ref2));
+                        const float p0 = pow2(e.x), p1 = pow2(e.y);
+                        const uint64_t both = two(p0, p1);
+                        sum[k & 1] = add_two(sum[k & 1], both);
                         const uint32_t hi = pack_bf16(p0, p1);
+                        const float2 left = apart(add_two(both, two(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xffff0000u))));
                         w2[k] = hi;
-                        w2[16 + k] = pack_bf16(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
+                        w2[16 + k] = pack_bf16(left.x, left.y);
                     }
                     tmem_store(s_at + c * 32, w2);
                 }
@@ -627,7 +662,8 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
             seq += w.t1 - w.t0;
             // the stream's part, 32 bytes of a row at a time
             const int n = stream_requests(a, w.w, x) * G, at = part_row(a, w.w, cta, x);
-            float l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            const float2 l0 = apart(sum[0]), l1 = apart(sum[1]);
+            const float l = (l0.x + l0.y) + (l1.x + l1.y);
             if (l != l && top == -INFINITY) top = 0.f;         // no number: not an empty part
             if (i < n) a.stat[at + i] = make_float2(any ? top : -INFINITY, any ? l : 0.f);
             if (any) {
