@@ -278,10 +278,12 @@ __device__ __forceinline__ void make_plan(const SharedArgs &a, Plan &p) {
         const long long y = __shfl_up_sync(ALL, inc, o);
         if (lane >= o) inc += y;
     }
-    if (lane == 31) p.warp_sum[warp] = inc;
-    __syncthreads();
     long long at = inc - sum;
-    for (int w = 0; w < warp; ++w) at += p.warp_sum[w];
+    if (G >= 96) {                         // (fewer are all the first warp's)
+        if (lane == 31) p.warp_sum[warp] = inc;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) at += p.warp_sum[w];
+    }
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         const int g = 3 * t + i;
@@ -608,17 +610,11 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                 any = true;
                 const float ref = top == -INFINITY ? 0.f : top;
                 const uint64_t f2 = two(f, f), ref2 = two(-ref, -ref);
-                tmem_load(s_at, r);
-#pragma unroll
-                for (int c = 0; c < TT / 32; ++c) {
-                    uint32_t(&now)[32] = c & 1 ? r2 : r;
-                    uint32_t(&then)[32] = c & 1 ? r : r2;
-                    tmem_loaded(now);
-                    if (c + 1 < TT / 32) tmem_load(s_at + (c + 1) * 32, then);
+                auto weights = [&](const uint32_t (&y)[32], uint32_t at) {
                     uint32_t w2[32];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        const float2 e = apart(fma_two(two(__uint_as_float(now[2 * k]), __uint_as_float(now[2 * k + 1])), f2, ref2));
+                        const float2 e = apart(fma_two(two(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), f2, ref2));
                         const float p0 = pow2(e.x), p1 = pow2(e.y);
                         const uint64_t both = two(p0, p1);
                         sum[k & 1] = add_two(sum[k & 1], both);
@@ -627,7 +623,17 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                         w2[k] = hi;
                         w2[16 + k] = pack_bf16(left.x, left.y);
                     }
-                    tmem_store(s_at + c * 32, w2);
+                    tmem_store(at, w2);
+                };
+                tmem_load(s_at, r);
+#pragma unroll
+                for (int c = 0; c < TT / 32; c += 2) {
+                    tmem_loaded(r);
+                    tmem_load(s_at + (c + 1) * 32, r2);
+                    weights(r, s_at + c * 32);
+                    tmem_loaded(r2);
+                    if (c + 2 < TT / 32) tmem_load(s_at + (c + 2) * 32, r);
+                    weights(r2, s_at + (c + 1) * 32);
                 }
                 tmem_stored();
                 ptx::tc_fence_before();
@@ -825,16 +831,15 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                 constexpr int QL = DC / 8, QR = 32 / QL;       // lanes of a row, rows of an instruction
                 const int x = keys ? 0 : 1, n = stream_requests(a, w.w, x);
                 const int row = lw * 32 + lane, in = row / G, r = w.w.r0 + x * a.tile_req + in;
-                const bool real = in < n && length_of(a, r) >= tokens;
-                const long long own = real ? r * a.q_stride + (long long)(w.w.hk * G + row - in * G) * D : -1;
+                // in pieces of 16 bytes (rows of requests without the shared tokens are of no use, and no harm)
+                const int own = in < n ? (int)((r * a.q_stride + (long long)(w.w.hk * G + row - in * G) * D) / 8) : -1;
                 const int q_piece = lane % QL;
                 const uint32_t to = q_at + x * TB;
-#pragma unroll 4
+                const uint4 *const q = reinterpret_cast<const uint4 *>(a.q);
+#pragma unroll 8
                 for (int k = 0; k < 32 / QR; ++k) {
-                    const int in_tile = k * QR + lane / QL;
-                    const long long from = __shfl_sync(ALL, own, in_tile);
-                    const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(a.q) + (from >= 0 ? from + q_piece * 8 : 0);
-                    if (q_piece * 8 < D) copy16(to + place_of(lw * 32 + in_tile, q_piece), src, from >= 0);
+                    const int in_tile = k * QR + lane / QL, at = __shfl_sync(ALL, own, in_tile);
+                    if (q_piece * 8 < D) copy16(to + place_of(lw * 32 + in_tile, q_piece), at >= 0 ? q + at + q_piece : q, at >= 0);
                 }
             }
             sent(bar(b.qfull));
@@ -857,8 +862,14 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                     told(bar(full[slot]));
                 } else {
                     copy(ring + slot * TB, now);
-                    if (t + 1 < w.t1) now = rows_of(t + 1, page);
-                    sent(bar(full[slot]));
+                    if (t == w.t0) {                           // the first products wait for these
+                        sent(bar(full[slot]));
+                        if (t + 1 < w.t1) now = rows_of(t + 1, page);
+                        all_told();
+                    } else {
+                        if (t + 1 < w.t1) now = rows_of(t + 1, page);
+                        sent(bar(full[slot]));
+                    }
                 }
                 page = page_of(t + 2);
                 if (++slot == SLOTS) slot = 0, phase ^= 1;

@@ -210,7 +210,7 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
     // by type and size: heads that the shared kernel's tiles hold (its sums are those of
     // 16-bit products, and 128 elements and rows are what its tensor memory takes)
     const bool together = sh && sh->n_groups > 0 && kv->dtype != SCUTE_KV_FP32 && kv->head_dim <= SHARED_MAX_DIM &&
-                          a.group <= SHARED_MAX_GROUP_HEADS;
+                          a.group <= SHARED_MAX_GROUP_HEADS && t->n_req * t->q_stride / 8 < 0x7fffffff;
     SharedArgs b{};
     if (together) {
         char *work = static_cast<char *>(sh->work);
