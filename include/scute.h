@@ -425,9 +425,8 @@ scute_status scute_kv_resize(scute_ctx *ctx, const int32_t *len_in, const int32_
  *                       counts as -1, a len_new outside 0..len_in[source] as the
  *                       nearest inside, a len_in outside 0..table_cols * page_size
  *                       likewise; each is recorded (SCUTE_ERR_PAGES);
- *   table_out, len_out  device int32 [n_out][table_out_stride], [n_out]; neither
- *                       may overlap table_in or len_in.  Entries behind a row's
- *                       pages are left as they were;
+ *   table_out, len_out  device int32 [n_out][table_out_stride], [n_out].  Entries
+ *                       behind a row's pages are left as they were;
  *   extra               device int32 [n_pages], changed in place.  A page number
  *                       outside 0..n_pages - 1 is taken over uncounted and
  *                       recorded, as is a page with more rows than holders;
@@ -435,6 +434,8 @@ scute_status scute_kv_resize(scute_ctx *ctx, const int32_t *len_in, const int32_
  *                       entries from the new count on keep what they held, and
  *                       pages beyond n_free_max entries are lost (SCUTE_ERR_PAGES);
  *   copy_from, copy_to, copy_tokens   device int32 [n_out].
+ * No output may overlap an input or another output, but for free_out, which may be
+ * free_in.
  * n_in and n_out are 0..SCUTE_MAX_REQUESTS, n_pages 0..2^30, table_cols * page_size
  * and a table's entries at most 2^31 - 1.  What the step does is fixed by the
  * arguments alone. */

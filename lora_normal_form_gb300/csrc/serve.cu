@@ -364,12 +364,23 @@ scute_status scute_kv_fork(scute_ctx *c, const scute_fork *f, void *stream) {
         (f->n_in > 0 && (!f->table_in || !f->len_in)) ||
         (f->n_out > 0 && (!f->source || !f->table_out || !f->len_out || !f->copy_from || !f->copy_to || !f->copy_tokens)))
         return fail(c, SCUTE_ERR_ARG, "null argument");
-    if (f->n_in > 0 && f->n_out > 0) {
-        const struct { const int32_t *p; int64_t n; } in[2] = {{f->table_in, (f->n_in - 1) * f->table_in_stride + f->table_cols}, {f->len_in, f->n_in}},
-                                       out[2] = {{f->table_out, (f->n_out - 1) * f->table_out_stride + f->table_cols}, {f->len_out, f->n_out}};
+    // what is written may lie neither over what is read nor over anything else that is
+    // written: the steps read their inputs until the last one
+    const auto table = [&](int n, int64_t pitch) { return n > 0 ? (n - 1) * pitch + f->table_cols : 0; };
+    const struct {
+        const int32_t *p;
+        int64_t n;
+    } in[] = {{f->table_in, table(f->n_in, f->table_in_stride)}, {f->len_in, f->n_in}, {f->source, f->n_out},
+              {f->len_new, f->len_new ? f->n_out : 0}},
+      out[] = {{f->table_out, table(f->n_out, f->table_out_stride)}, {f->len_out, f->n_out}, {f->copy_from, f->n_out},
+               {f->copy_to, f->n_out}, {f->copy_tokens, f->n_out}, {f->extra, f->n_pages}, {f->free_pages, f->n_free_max},
+               {f->free_out, 1}};
+    const auto overlap = [](const auto &x, const auto &y) { return x.n > 0 && y.n > 0 && x.p < y.p + y.n && y.p < x.p + x.n; };
+    for (const auto &y : out) {
         for (const auto &x : in)
-            for (const auto &y : out)
-                if (x.p < y.p + y.n && y.p < x.p + x.n) return fail(c, SCUTE_ERR_ARG, "new rows overlap the old ones");
+            if (overlap(x, y)) return fail(c, SCUTE_ERR_ARG, "an output overlaps an input");
+        for (const auto &x : out)
+            if (&x != &y && overlap(x, y)) return fail(c, SCUTE_ERR_ARG, "two outputs overlap");
     }
     DeviceGuard dg(c->device);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

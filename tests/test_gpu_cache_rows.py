@@ -370,3 +370,165 @@ def test_attention_between_first_tokens_and_window_nothing_is_read(scute, contex
     assert ctx.sync_status() == 0
     kept = [[x[OB.seen(len(x), window, sinks)] for x in kv] for kv in tokens]
     check_attend(out, lse, q, kept, kind, 4, softcap=20.0)
+
+
+# ---------------------------------------------------------------- graphs, streams, alignment
+def test_fork_and_copy_in_a_graph_on_another_stream(scute, contexts):
+    """A captured fork and copy, replayed on other sources and lengths."""
+    ctx, g = contexts["bf16"], np.random.default_rng(21)
+    f = Fork(g, 30, 30, 16, 12, spare=40)
+    dev = lambda x: i32(np.asarray(x, np.int64))  # noqa: E731
+    table, lens, source, new = dev(f.table), dev(f.len_in), dev(f.source), dev(f.len_new)
+    extra0, free0 = dev(f.extra), torch.zeros(f.n_pages, dtype=torch.int32, device="cuda")
+    free0[:len(f.free)] = dev(f.free)
+    extra, free, count = extra0.clone(), free0.clone(), dev([0])
+    out = torch.zeros(30, 12, dtype=torch.int32, device="cuda")
+    vec = [torch.zeros(30, dtype=torch.int32, device="cuda") for _ in range(4)]
+    k0 = torch.randn(f.n_pages, 2, 16, 32, device="cuda").bfloat16()
+    k, v = k0.clone(), k0 + 1
+    v0 = v.clone()
+    caches = scute.KvCaches([scute.KvCache(k, v)])
+    s = torch.cuda.Stream()
+
+    def step():
+        extra.copy_(extra0), free.copy_(free0), count.fill_(len(f.free)), k.copy_(k0), v.copy_(v0)
+        ctx.kv_fork(table, lens, source, out, vec[0], 16, extra, free, count, count, *vec[1:], len_new=new)
+        ctx.kv_copy(caches, *vec[1:])
+
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        src = g.integers(-1, 30, 30)
+        want = np.where(src >= 0, (f.len_in[src] * g.random(30)).astype(np.int64), 0)
+        source.copy_(dev(src)), new.copy_(dev(want))
+        graph.replay()
+        ok = ctx.sync_status()
+        ref = OB.fork(f.table, f.len_in, src, want, out.cpu().numpy(), 16, f.extra, f.free)
+        assert ok == (0 if ref["ok"] else PAGES)
+        for t, name in zip(vec, ("len_out", "copy_from", "copy_to", "copy_tokens")):
+            assert np.array_equal(t.cpu().numpy(), ref[name])
+        assert np.array_equal(out.cpu().numpy(), ref["table"]) and np.array_equal(extra.cpu().numpy(), ref["extra"])
+        assert free[:int(count)].cpu().tolist() == ref["free"]
+        kk = k0.clone()
+        for a, b, n in zip(ref["copy_from"], ref["copy_to"], ref["copy_tokens"]):
+            if b >= 0:
+                kk[b, :, :n] = k0[a, :, :n]
+        assert torch.equal(k, kk) and torch.equal(v[:, :, :, 0], torch.where(kk != k0, kk + 1, v0)[:, :, :, 0])
+
+
+def test_append_norm_weights_of_any_alignment_and_positions_out_of_range(scute, contexts):
+    """Weights that begin at any element, and strided ones, give what aligned ones give;
+    slots and positions outside are left out and recorded."""
+    ctx, g = contexts["bf16"], np.random.default_rng(8)
+    n, H, D = 33, 2, 64
+    draw = lambda h: torch.from_numpy(g.standard_normal((n, h, D), dtype=np.float32)).bfloat16().cuda()  # noqa: E731
+    q, k, v = draw(4), draw(H), draw(H)
+    cs = torch.empty(50, D, device="cuda")
+    ctx.rope_table(cs, 10000.0)
+    slots, pos = np.arange(n), g.integers(0, 50, n)
+    w, each = torch.rand(D, device="cuda") + 0.5, torch.rand(4, D, device="cuda") + 0.5
+    odd = torch.zeros(D + 1, device="cuda")[1:].copy_(w)
+    wide = torch.zeros(4, D + 3, device="cuda")[:, :D].copy_(each)
+
+    def run(norm, slots=slots, pos=pos):
+        pools = [torch.zeros(3, H, 16, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        out = torch.empty_like(q)
+        ctx.kv_append(scute.KvCache(*pools), i32(slots), k, v, q=q, q_out=out, rope=scute.Rope(cs, i32(pos)), norm=norm)
+        return out, pools[0], pools[1], ctx.sync_status()
+
+    for a, b in ((scute.HeadNorm(w, w), scute.HeadNorm(odd, odd)), (scute.HeadNorm(each, w), scute.HeadNorm(wide, odd))):
+        x, y = run(a), run(b)
+        assert x[3] == y[3] == 0 and torch.equal(x[2], y[2])
+        # the two kernels add squares in another order: a bf16 step at most, at few elements
+        for s, t in zip(x[:2], y[:2]):
+            far = (s.float() - t.float()).abs() > 2.0 ** -8 * s.float().abs()
+            assert not far.any()
+    bad_slots, bad_pos = slots.copy(), pos.copy()
+    bad_slots[3], bad_pos[5], bad_pos[6] = 3 * 16, 50, -1
+    clipped = pos.copy()
+    clipped[5], clipped[6] = 49, 0
+    without = slots.copy()
+    without[3] = -1
+    for norm in (scute.HeadNorm(w, w), scute.HeadNorm(odd, odd)):
+        x, y = run(norm, bad_slots, bad_pos), run(norm, without, clipped)
+        assert x[3] == PAGES and y[3] == 0
+        assert all(torch.equal(s, t) for s, t in zip(x[:3], y[:3]))
+
+
+def test_append_norm_zero_heads_and_infinities_stay_in_their_heads(scute, contexts):
+    """A head of zeros stays zero; one with an infinity or no number leaves the others as they were."""
+    ctx = contexts["fp32"]
+    n, H, D = 3, 4, 32
+    q = torch.randn(n, H, D, device="cuda")
+    q[0, 1] = 0.0
+    bad = q.clone()
+    bad[1, 2, 5], bad[2, 0, 0] = float("inf"), float("nan")
+    w = torch.ones(D, device="cuda")
+    out = []
+    for x in (q, bad):
+        pools = [torch.zeros(1, H, 16, D, device="cuda") for _ in range(2)]
+        y = torch.empty_like(x)
+        ctx.kv_append(scute.KvCache(*pools), i32([0, 1, 2]), x, x, q=x, q_out=y, norm=scute.HeadNorm(w, w))
+        out.append(y)
+    assert ctx.sync_status() == 0 and not out[0][0, 1].any()
+    same = torch.ones(n, H, dtype=torch.bool)
+    same[1, 2] = same[2, 0] = False
+    assert torch.equal(out[0][same], out[1][same])
+
+
+# ---------------------------------------------------------------- refusals
+def test_refusals_of_forks_copies_norms_and_sinks(scute, contexts):
+    ctx = contexts["bf16"]
+    whole = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    good = dict(table_in=whole(2, 4), len_in=whole(2), source=whole(3), table_out=whole(3, 4), len_out=whole(3), page_size=16,
+                extra=whole(9), free_pages=whole(9), free_in=whole(1), free_out=whole(1), copy_from=whole(3), copy_to=whole(3),
+                copy_tokens=whole(3), len_new=whole(3))
+    ctx.kv_fork(**good)
+    both = whole(6)
+    bad = [dict(page_size=0), dict(page_size=1 << 30), dict(table_out=whole(3, 5)), dict(table_out=whole(2, 4)), dict(table_in=whole(1, 4)),
+           dict(len_out=good["len_in"]), dict(len_out=good["len_new"]), dict(copy_from=good["source"]), dict(copy_to=good["copy_from"]),
+           dict(table_out=good["table_in"].expand(2, 4)), dict(len_out=whole(2)), dict(copy_tokens=whole(4)), dict(len_new=whole(2)),
+           dict(free_out=whole(2)), dict(free_in=good["free_pages"][:1], free_out=good["free_pages"][:1]),
+           dict(extra=good["free_pages"]), dict(len_in=whole(2).float()), dict(source=whole(3).long()), dict(extra=whole(18)[::2]),
+           dict(table_in=whole(4, 2).t()), dict(table_out=whole(1, 4).expand(3, 4)), dict(len_out=both[:3], copy_from=both[2:5])]
+    for i, kw in enumerate(bad):
+        with pytest.raises((ValueError, scute.ScuteError)):
+            ctx.kv_fork(**{**good, **kw})
+            raise AssertionError(i)
+    pool = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+    cache = lambda *s, **kw: scute.KvCache(pool(*s), pool(*s), **kw)  # noqa: E731
+    one = cache(4, 2, 16, 64)
+    ctx.kv_copy(scute.KvCaches([one, cache(4, 2, 16, 64)]), whole(2) + 1, whole(2) - 1)
+    bad = [lambda: scute.KvCaches([]), lambda: scute.KvCaches([pool(4, 2, 16, 64)]),
+           lambda: ctx.kv_copy(scute.KvCaches([one, cache(5, 2, 16, 64)]), whole(2), whole(2)),
+           lambda: ctx.kv_copy(scute.KvCaches([one, cache(4, 2, 16, 64, token_major=True)]), whole(2), whole(2)),
+           lambda: ctx.kv_copy(scute.KvCaches([scute.KvCache(*[pool(4, 2, 16, 64, t=torch.float32)] * 2)]), whole(2), whole(2)),
+           lambda: ctx.kv_copy(scute.KvCaches([one]), whole(2), whole(3)), lambda: ctx.kv_copy(scute.KvCaches([one]), whole(2).long(), whole(2)),
+           lambda: ctx.kv_copy(scute.KvCaches([one]), whole(2), whole(2), whole(1)),
+           lambda: ctx.kv_copy(scute.KvCaches([one] * 1025), whole(2), whole(2))]
+    w, k, q = torch.ones(64, device="cuda"), pool(3, 2, 64), pool(3, 4, 64)
+    append = lambda norm, **kw: ctx.kv_append(one, whole(3), k, k, norm=norm, **kw)  # noqa: E731
+    append(scute.HeadNorm(w, w), q=q, q_out=q)
+    bad += [lambda: scute.HeadNorm(), lambda: scute.HeadNorm(w.double()), lambda: scute.HeadNorm(w.bfloat16()), lambda: scute.HeadNorm(w.view(1, 1, 64)),
+            lambda: scute.HeadNorm(torch.ones(128, device="cuda")[::2]), lambda: scute.HeadNorm(w.view(1, 64).expand(4, 64)),
+            lambda: append(scute.HeadNorm(torch.ones(32, device="cuda")), q=q, q_out=q),
+            lambda: append(scute.HeadNorm(torch.ones(2, 64, device="cuda")), q=q, q_out=q),
+            lambda: append(scute.HeadNorm(k_w=torch.ones(4, 64, device="cuda"))), lambda: append(scute.HeadNorm(w, w, eps=-1.0)),
+            lambda: append(scute.HeadNorm(w, w, eps=float("nan"))), lambda: append(scute.HeadNorm(w), q=q)]
+    lens, table = whole(3), scute.KvCache(pool(4, 2, 16, 64), pool(4, 2, 16, 64), whole(3, 2))
+    ctx.paged_attention(table, q, lens, q, window=3, sinks=1 << 30)
+    bad += [lambda: ctx.paged_attention(table, q, lens, q, window=3, sinks=-1),
+            lambda: ctx.paged_attention(table, q, lens, q, window=3, sinks=(1 << 30) + 1)]
+    for i, call in enumerate(bad):
+        with pytest.raises((ValueError, scute.ScuteError)):
+            call()
+            raise AssertionError(i)
+    for null in (lambda: scute.load().scute_kv_fork(ctx.handle, None, None), lambda: scute.load().scute_kv_copy(ctx.handle, None, 1, None, None, None, 1, None),
+                 lambda: scute.load().scute_paged_attention_shared(ctx.handle, table.ref, None, None, None),
+                 lambda: scute.load().scute_kv_fork(None, None, None)):
+        assert null() == 1                    # SCUTE_ERR_ARG
+    assert ctx.sync_status() == 0
