@@ -492,6 +492,8 @@ struct AttendArgs {
 size_t attend_part_floats(int num_sms);
 int attend_ctrs(int num_sms);
 cudaError_t launch_attend(const AttendArgs &a, int num_sms, cudaStream_t st);
+cudaError_t launch_attend_sinks(const AttendArgs &a, int num_sms, cudaStream_t st);
+cudaError_t launch_attend_own(const AttendArgs &a, int num_sms, cudaStream_t st);      // writes parts, for launch_join
 
 // ---------------------------------------------------------------- the beginning that a group's requests share
 constexpr int SHARED_MAX_GROUPS = 1024, SHARED_MAX_DIM = 128, SHARED_MAX_GROUP_HEADS = 128;

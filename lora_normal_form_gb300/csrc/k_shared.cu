@@ -5,7 +5,7 @@
 //     S [rows x tokens] = Q K^T,   O [rows x D] = P V,   P = 2^(S - m).
 // What it leaves is not an output but parts, a row's maximum m, sum l and unnormalised
 // O over some of the tokens, which the one-token attention takes in when it ends the
-// request's row over the tokens of its own (k_attend.cu).
+// request's row over the tokens of its own (k_attend.cuh).
 //
 // What bounds it.  A token costs 2 x D x size bytes and 2 x 2 x rows x D operations (the
 // second product twice over, see below, so 3 x 2): with bf16 keys 1.5 x rows
@@ -14,7 +14,7 @@
 //
 // Layout.  Work rows are (group, key/value head, up to 2 x 128 rows), their tiles of 128
 // tokens one sequence that is cut into equal contiguous ranges, one per CTA, as in
-// k_attend.cu.  In a CTA four warps bring keys and four values to shared memory, each to
+// k_attend.cuh.  In a CTA four warps bring keys and four values to shared memory, each to
 // a ring of its own, and two warpgroups each run a stream of its own: scores in tensor
 // memory (tcgen05.mma, issued by one of its threads), read back (a thread has a row), their
 // weights written over them, the second product from there, into outputs that stay in
@@ -23,7 +23,7 @@
 // other's softmax.
 //
 // Weights go to the second product as two bf16 numbers, one rounded and what that left
-// (16 bits of a weight, 2^-17 of it, as in k_attend.cu), l sums them in 32 bits.  The
+// (16 bits of a weight, 2^-17 of it, as in k_attend.cuh), l sums them in 32 bits.  The
 // reference m moves only when a score passes it by more than 2^8, so that outputs are
 // seldom scaled.  Tokens behind the shared beginning's end are zero in shared memory and
 // their scores minus infinity.

@@ -239,7 +239,9 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
         CU_TRY(c, launch_shared(b, c->num_sms, st));
         count_launch(c, 1);
     }
-    CU_TRY(c, launch_attend(a, c->num_sms, st));
+    CU_TRY(c, together ? launch_attend_own(a, c->num_sms, st)
+              : sinks && t->window ? launch_attend_sinks(a, c->num_sms, st)
+                                   : launch_attend(a, c->num_sms, st));
     count_launch(c, 1);
     if (together) {
         JoinArgs j{};
