@@ -481,11 +481,12 @@ struct AttendArgs {
     int *ctr;                  // arrivals at such a row (zero between launches)
     int *status;
     int hold;                  // 1: stages are never given back (test hook of the waits' end)
-    // of a batch whose groups share the beginnings of their contexts (k_shared.cu; null:
-    // none): a request's row begins behind them, and its outputs stay parts, row (request,
-    // head) of stat and part_o
+    // k_attend_own.cu: groups that share the beginnings of their contexts (k_shared.cu), and
+    // the parts, of which request r's are own_at[r] .. own_at[r + 1) - 1, part p of head h the
+    // row p q_heads + h of stat and part_o
     const int32_t *start, *shared_len;
     int n_groups;
+    int *own_at;
     float2 *stat;
     float *part_o;
 };
@@ -494,11 +495,12 @@ int attend_ctrs(int num_sms);
 cudaError_t launch_attend(const AttendArgs &a, int num_sms, cudaStream_t st);
 cudaError_t launch_attend_sinks(const AttendArgs &a, int num_sms, cudaStream_t st);
 cudaError_t launch_attend_own(const AttendArgs &a, int num_sms, cudaStream_t st);      // writes parts, for launch_join
+long long own_rows(long long n_req, long long q_heads, int num_sms);                     // of them, at most
 
 // ---------------------------------------------------------------- the beginning that a group's requests share
 constexpr int SHARED_MAX_GROUPS = 1024, SHARED_MAX_DIM = 128, SHARED_MAX_GROUP_HEADS = 128;
 constexpr int SHARED_TWIN = 1 << 30;
-// Parts: rows of (m, l) and of D outputs, the batch's own (request, head) first.  The heads
+// Parts: rows of (m, l) and of D outputs, those of the requests' own tokens first.  The heads
 // of request r on key/value head h have those of CTAs piece.x .. piece.y (SHARED_TWIN
 // taken out; -1: none): rows piece.z + 256 CTA .. of piece.w & 0xffff rows, with
 // SHARED_TWIN as many again directly behind, the request's first head the one at
@@ -514,6 +516,7 @@ struct SharedArgs {
     int page_shift;
     const int32_t *start, *shared_len;
     int n_groups;
+    int first_row;             // rows before these parts
     int4 *piece;
     float2 *stat;
     float *o;
@@ -522,6 +525,7 @@ struct SharedArgs {
 };
 struct JoinArgs {
     const int4 *piece;
+    const int *own_at;
     const float2 *stat;
     const float *o;
     const float *v_scale;
@@ -557,8 +561,8 @@ __device__ __forceinline__ int shared_group(const Args &a, int r, int length, in
     return n > 0 && length >= *tokens && shared_start(a, lo) <= r && r < shared_start(a, lo + 1) ? lo : -1;
 }
 #endif
-// rows of parts that a batch may need
-inline long long shared_rows(long long n_req, long long q_heads, int num_sms) { return 3 * n_req * q_heads + 256ll * num_sms; }
+// rows of parts that a batch may need, beside its own
+inline long long shared_rows(long long n_req, long long q_heads, int num_sms) { return 2 * n_req * q_heads + 256ll * num_sms; }
 cudaError_t launch_shared(const SharedArgs &a, int num_sms, cudaStream_t st);
 cudaError_t launch_join(const JoinArgs &a, int num_sms, int n_groups, cudaStream_t st);
 

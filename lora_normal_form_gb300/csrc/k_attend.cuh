@@ -47,7 +47,8 @@ namespace scute {
 namespace {
 
 // What a request sees, a kernel for each: its tokens from first on (all, or a window's);
-// a window's and the first few (sinks); those behind what its group shares (k_shared.cu).
+// a window's and the first few (sinks); those behind what its group shares (k_shared.cu;
+// k_attend_own.cu alone).
 enum { PLAIN, SINKS, SHARED };
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
@@ -224,6 +225,7 @@ struct MmaMath {
     static constexpr int TT = 16 * MT, HC = 8 * NT;
     static constexpr int P_BYTES = 0;
     static constexpr int KE = FP8 ? 16 : 8;               // elements of 16 bytes
+    static constexpr int NQ = NT;
     static constexpr int KP = DC / (4 * KE);              // key pieces of a lane, each four lanes wide
     static constexpr int VE = FP8 && DC > 64 ? 16 : 8;    // elements of a value piece, eight lanes wide
     static constexpr int VP = DC / (8 * VE);
@@ -253,21 +255,45 @@ struct MmaMath {
     }
     // The row's queries, [nh][D] in shared memory: the fragments' elements are those
     // of the keys' pieces.
+    static constexpr int QE = KE / 8;                     // 16-byte pieces of a query for each of a key
     __device__ __forceinline__ void queries(uint32_t qs, int nh, int D, float scale) {
+        uint4 x[NT][KP][QE];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int h = nt * 8 + g;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int p = 0; p < KP; ++p)
 #pragma unroll
-                for (int e = 0; e < KE / 8; ++e) {
-                    const int d = (p * 4 + c) * KE + e * 8;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (h < nh && d < D) x = lds16(qs + (h * D + d) * 2);
-                    qf[nt][p][e * 4 + 0] = x.x;
-                    qf[nt][p][e * 4 + 1] = x.y;
-                    qf[nt][p][e * 4 + 2] = x.z;
-                    qf[nt][p][e * 4 + 3] = x.w;
+                for (int e = 0; e < QE; ++e) {
+                    const int h = nt * 8 + g, d = (p * 4 + c) * KE + e * 8;
+                    x[nt][p][e] = make_uint4(0, 0, 0, 0);
+                    if (h < nh && d < D) x[nt][p][e] = lds16(qs + (h * D + d) * 2);
+                }
+        queries(x, scale);
+    }
+    // The same from memory, read ahead.
+    __device__ __forceinline__ void read_queries(const IO *q, int nh, int D, uint4 (&x)[NT][KP][QE]) const {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int p = 0; p < KP; ++p)
+#pragma unroll
+                for (int e = 0; e < QE; ++e) {
+                    const int h = nt * 8 + g, d = (p * 4 + c) * KE + e * 8;
+                    x[nt][p][e] = make_uint4(0, 0, 0, 0);
+                    if (h < nh && d < D) x[nt][p][e] = *reinterpret_cast<const uint4 *>(q + (long long)h * D + d);
+                }
+    }
+    __device__ __forceinline__ void queries(const uint4 (&x)[NT][KP][QE], float scale) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int p = 0; p < KP; ++p)
+#pragma unroll
+                for (int e = 0; e < QE; ++e) {
+                    qf[nt][p][e * 4 + 0] = x[nt][p][e].x;
+                    qf[nt][p][e * 4 + 1] = x[nt][p][e].y;
+                    qf[nt][p][e * 4 + 2] = x[nt][p][e].z;
+                    qf[nt][p][e * 4 + 3] = x[nt][p][e].w;
                 }
             float back = 1.f;
             if constexpr (FP8) {
@@ -499,6 +525,25 @@ struct MmaMath {
                                                                       o[nt][j][i + 1][1] * f[1], o[nt][j][i + 1][3] * f[1]);
                 }
         }
+    }
+    // The outputs of the first nh heads as they are, relative to the warp's own maxima.
+    __device__ __forceinline__ void part(float *to, int D, int nh) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int h = nt * 8 + 2 * c + k;
+                if (h >= nh) continue;
+#pragma unroll
+                for (int j = 0; j < VP; ++j)
+#pragma unroll
+                    for (int i = 0; i < OT; i += 2) {
+                        const int d = (j * 8 + g) * VE + 2 * i;
+                        if (d < D)
+                            *reinterpret_cast<float4 *>(to + (long long)h * D + d) =
+                                make_float4(o[nt][j][i][k], o[nt][j][i][k + 2], o[nt][j][i + 1][k], o[nt][j][i + 1][k + 2]);
+                    }
+            }
     }
     // Merge the maxima of CW warps and write this warp's outputs.
     template <int CW>
@@ -838,14 +883,6 @@ __device__ __forceinline__ void put(const AttendArgs &a, int r, int h, int d, fl
     }
 }
 
-// Or, of a batch with shared beginnings, the unnormalised outputs of the request's own
-// tokens, for launch_join.
-__device__ __forceinline__ void put_part(const AttendArgs &a, int r, int h, int d, float4 x, float m, float l) {
-    const long long row = (long long)r * a.q_heads + h;
-    *reinterpret_cast<float4 *>(a.part_o + row * a.kv.dim + d) = x;
-    if (d == 0) a.stat[row] = make_float2(m, l);
-}
-
 // A row that several CTAs share, as its joiner needs it.
 struct SharedRow {
     int r, hk, h0, nh, c0, c1;          // request, heads; its first and last CTA
@@ -857,7 +894,7 @@ struct SharedRow {
 // is a race, and a row joined in other groups has other bits.  A row whose parts fit
 // is joined in one group, alone or beside another; one whose parts do not, in groups
 // of as many as fit alone.
-template <typename IO, int THREADS, int MODE>
+template <typename IO, int THREADS>
 __device__ __forceinline__ void join_parts(const AttendArgs &a, const SharedRow &head, const SharedRow &tail, bool last_head,
                                            bool last_tail, uint8_t *buf, int room, int t) {
     constexpr int IT = 2;                // groups of four outputs of a thread at a time
@@ -951,10 +988,6 @@ __device__ __forceinline__ void join_parts(const AttendArgs &a, const SharedRow 
                 const int e = g0 + t + i * THREADS;
                 if (e >= items) break;
                 const int h = e / (D / 4), d = 4 * (e - h * (D / 4));
-                if constexpr (MODE == SHARED) {
-                    put_part(a, row.r, row.h0 + h, d, x[i], m[i], l[i]);
-                    continue;
-                }
                 put<IO>(a, row.r, row.h0 + h, d, x[i], l[i] == 0.f ? 0.f : vs / l[i]);
                 if (a.lse && d == 0) a.lse[(long long)row.r * a.q_heads + row.h0 + h] = (m[i] + log2f(l[i])) * LN2;
             }
@@ -1020,17 +1053,12 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
     if (row_bytes < M::ROW)
         for (int i = threadIdx.x; i < stages * S::STAGE / 16; i += S::THREADS)
             reinterpret_cast<uint4 *>(s_ring)[i] = make_uint4(0, 0, 0, 0);
-    // (with shared beginnings the launch before is k_shared.cu's, which has waited for what
-    // this one reads: only this one's end waits for it, for launch_join's sake)
-    if constexpr (MODE != SHARED) ptx::grid_dep_wait();
+    ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     plan_places<MODE>(a, TT, places_at, s_warp);
     Walk<MODE> w(a, places_at, HC, TT, MIN_TILES);
     const int cta = blockIdx.x;
-    if (cta >= w.ctas) {
-        if constexpr (MODE == SHARED) ptx::grid_dep_wait();
-        return;
-    }
+    if (cta >= w.ctas) return;
     w.open(cta);
 
     if (warp < PW) {
@@ -1185,7 +1213,6 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
         // nothing of this warp's may be on its way when the CTA ends
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (*s_abort && lane == 0) atomicOr(a.status, STATUS_TIMEOUT);
-        if constexpr (MODE == SHARED) ptx::grid_dep_wait();
         return;
     }
 
@@ -1253,13 +1280,9 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
             const float vs = a.kv.v_scale ? a.kv.v_scale[w.hk] : 1.f;
             for (int i = t; i < nh * (D / 4); i += CW * 32) {
                 const int h = i / (D / 4), d = 4 * (i - h * (D / 4));
-                if constexpr (MODE == SHARED) {
-                    put_part(a, w.r, h0 + h, d, merged(h, d), s_top[h], s_sum[h]);
-                } else {
-                    put<IO>(a, w.r, h0 + h, d, merged(h, d), s_sum[h] == 0.f ? 0.f : vs / s_sum[h]);
-                }
+                put<IO>(a, w.r, h0 + h, d, merged(h, d), s_sum[h] == 0.f ? 0.f : vs / s_sum[h]);
             }
-            if (MODE != SHARED && a.lse && t < nh) a.lse[(long long)w.r * a.q_heads + h0 + t] = (s_top[t] + log2f(s_sum[t])) * LN2;
+            if (a.lse && t < nh) a.lse[(long long)w.r * a.q_heads + h0 + t] = (s_top[t] + log2f(s_sum[t])) * LN2;
         } else {
             const PartView p = part_of(a, 2 * cta + (w.t0 == 0 ? 1 : 0));
             for (int i = t; i < nh * (D / 4); i += CW * 32) {
@@ -1275,7 +1298,6 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
     if (!live && lane == 0) atomicOr(a.status, STATUS_TIMEOUT);
     // arrive at the shared rows; the last to arrive joins
     if (head.r < 0 && tail.r < 0) {
-        if constexpr (MODE == SHARED) ptx::grid_dep_wait();
         return;
     }
     sync_threads<CW * 32>();
@@ -1293,8 +1315,7 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
     sync_threads<CW * 32>();
     const bool last_head = s_last[0], last_tail = s_last[1];
     if (last_head || last_tail)          // the ring is empty by now
-        join_parts<IO, CW * 32, MODE>(a, head, tail, last_head, last_tail, s_ring, stages * S::STAGE, t);
-    if constexpr (MODE == SHARED) ptx::grid_dep_wait();
+        join_parts<IO, CW * 32>(a, head, tail, last_head, last_tail, s_ring, stages * S::STAGE, t);
 }
 
 template <typename M, int DC, int CW, int PW, int CTAS, int MODE>
@@ -1339,8 +1360,7 @@ template <bool FP8, int MODE>
 cudaError_t launch_mma(const AttendArgs &a, int num_sms, cudaStream_t st) {
     const int D = a.kv.dim;
     const bool wide = a.group > 8;
-    if constexpr (MODE != SHARED)              // (k_shared.cu takes heads of up to 128 elements)
-        if (D > 128) return launch_shape<MmaMath<FP8, 256, 1>, 256, 4, 2, 2, MODE>(a, num_sms, st);
+    if (D > 128) return launch_shape<MmaMath<FP8, 256, 1>, 256, 4, 2, 2, MODE>(a, num_sms, st);
     if (D > 64)
         return wide ? launch_shape<MmaMath<FP8, 128, 2>, 128, 4, 2, 2, MODE>(a, num_sms, st)
                     : launch_shape<MmaMath<FP8, 128, 1>, 128, 2, 1, 4, MODE>(a, num_sms, st);
@@ -1364,10 +1384,9 @@ template <int MODE>
 cudaError_t launch_attend_mode(const AttendArgs &a, int num_sms, cudaStream_t st) {
     if (a.kv.dtype == KV_BF16) return launch_mma<false, MODE>(a, num_sms, st);
     if (a.kv.dtype == KV_E4M3) return launch_mma<true, MODE>(a, num_sms, st);
-    if constexpr (MODE == SHARED) return cudaErrorInvalidValue;      // (16-bit products: no 32-bit caches)
-    else if (a.kv.dim <= 64) return launch_fma<64, 2, 1, 5, MODE>(a, num_sms, st);
-    else if (a.kv.dim <= 128) return launch_fma<128, 2, 1, 4, MODE>(a, num_sms, st);
-    else return launch_fma<256, 2, 1, 3, MODE>(a, num_sms, st);
+    if (a.kv.dim <= 64) return launch_fma<64, 2, 1, 5, MODE>(a, num_sms, st);
+    if (a.kv.dim <= 128) return launch_fma<128, 2, 1, 4, MODE>(a, num_sms, st);
+    return launch_fma<256, 2, 1, 3, MODE>(a, num_sms, st);
 }
 
 }  // namespace

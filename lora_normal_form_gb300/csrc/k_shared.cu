@@ -323,7 +323,7 @@ __device__ __forceinline__ WorkRow work_row(const SharedArgs &a, const Plan &p, 
     w.requests = min(2 * a.tile_req, all - b * 2 * a.tile_req);
     w.twin = w.requests <= a.tile_req;
     // twice a row's room: a twin's streams each leave all of the rows
-    w.first_row = a.n_req * a.kv.heads * a.group + 2 * a.group * (p.start[g] * a.kv.heads + w.hk * all + b * 2 * a.tile_req);
+    w.first_row = a.first_row + 2 * a.group * (p.start[g] * a.kv.heads + w.hk * all + b * 2 * a.tile_req);
     return w;
 }
 __device__ __forceinline__ int stream_requests(const SharedArgs &a, const WorkRow &w, int x) {
@@ -918,7 +918,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const JoinArgs a) {
     if (real) {
         const int4 piece = a.piece[(long long)r * (a.q_heads / a.group) + hk];
         const int twin = piece.y >= 0 && piece.y & SHARED_TWIN ? 1 : 0, n = piece.w & 0xffff, i = (piece.w >> 16) + h - hk * a.group;
-        const int parts = 1 + (piece.y < 0 ? 0 : ((piece.y & ~SHARED_TWIN) - piece.x + 1) << twin);
+        const int own = a.own_at[r], owns = a.own_at[r + 1] - own;
+        const int parts = owns + (piece.y < 0 ? 0 : ((piece.y & ~SHARED_TWIN) - piece.x + 1) << twin);
 #pragma unroll 1
         for (int k0 = part0; k0 < parts; k0 += JG * B) {
             float2 s[B];
@@ -928,9 +929,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const JoinArgs a) {
                 const int at = k0 + k * JG;
                 s[k] = make_float2(-INFINITY, 0.f);
                 if (at >= parts) continue;
-                // the head's own part is the first one
-                const int shared = at - 1;
-                const int from = at == 0 ? row : piece.z + 256 * (piece.x + (shared >> twin)) + (shared & twin) * n + i;
+                // the parts of its own tokens are the first ones
+                const int shared = at - owns;
+                const int from = shared < 0 ? (own + at) * a.q_heads + h
+                                            : piece.z + 256 * (piece.x + (shared >> twin)) + (shared & twin) * n + i;
                 s[k] = a.stat[from];
                 y[k] = *reinterpret_cast<const float4 *>(a.o + (long long)from * a.dim + d);
             }

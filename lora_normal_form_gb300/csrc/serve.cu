@@ -137,13 +137,14 @@ scute_status append(scute_ctx *c, const scute_kv_cache *kv, const int32_t *slot_
 
 // The parts of scute_shared's workspace, and its bytes (-1: too large).
 struct SharedWork {
-    int64_t piece, stat, o, bytes;
+    int64_t own_at, stat, o, own_rows, bytes;
 };
 SharedWork shared_work(int64_t n_req, int64_t q_heads, int64_t kv_heads, int64_t dim, int num_sms) {
-    const int64_t rows = shared_rows(n_req, q_heads, num_sms);
     SharedWork w;
-    w.piece = 0;
-    w.stat = w.piece + 16 * n_req * kv_heads;
+    w.own_rows = own_rows(n_req, q_heads, num_sms);
+    const int64_t rows = w.own_rows + shared_rows(n_req, q_heads, num_sms);
+    w.own_at = 16 * n_req * kv_heads;
+    w.stat = (w.own_at + 4 * (n_req + 1) + 31) / 32 * 32;
     w.o = (w.stat + 8 * rows + 31) / 32 * 32;
     w.bytes = rows > 0x7fffffff ? -1 : w.o + 4 * rows * dim;
     return w;
@@ -227,7 +228,9 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
         b.start = a.start = sh->start;
         b.shared_len = a.shared_len = sh->len;
         b.n_groups = a.n_groups = sh->n_groups;
-        b.piece = reinterpret_cast<int4 *>(work + w.piece);
+        b.first_row = (int)w.own_rows;
+        b.piece = reinterpret_cast<int4 *>(work);
+        a.own_at = reinterpret_cast<int *>(work + w.own_at);
         b.stat = a.stat = reinterpret_cast<float2 *>(work + w.stat);
         b.o = a.part_o = reinterpret_cast<float *>(work + w.o);
         b.status = a.status;
@@ -246,6 +249,7 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
     if (together) {
         JoinArgs j{};
         j.piece = b.piece;
+        j.own_at = a.own_at;
         j.stat = b.stat;
         j.o = b.o;
         j.v_scale = kv->v_scale;
