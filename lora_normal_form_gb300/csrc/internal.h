@@ -495,6 +495,7 @@ int attend_ctrs(int num_sms);
 cudaError_t launch_attend(const AttendArgs &a, int num_sms, cudaStream_t st);
 cudaError_t launch_attend_sinks(const AttendArgs &a, int num_sms, cudaStream_t st);
 cudaError_t launch_attend_own(const AttendArgs &a, int num_sms, cudaStream_t st);      // writes parts, for launch_join
+cudaError_t launch_attend_own_sinks(const AttendArgs &a, int num_sms, cudaStream_t st);  // the same of a window and first tokens
 long long own_rows(long long n_req, long long q_heads, int num_sms);                     // of them, at most
 
 // ---------------------------------------------------------------- the beginning that a group's requests share
@@ -524,7 +525,7 @@ struct SharedArgs {
     int hold;
 };
 struct JoinArgs {
-    const int4 *piece;
+    const int4 *piece;         // null: nothing shared
     const int *own_at;
     const float2 *stat;
     const float *o;
@@ -564,7 +565,9 @@ __device__ __forceinline__ int shared_group(const Args &a, int r, int length, in
 // rows of parts that a batch may need, beside its own
 inline long long shared_rows(long long n_req, long long q_heads, int num_sms) { return 2 * n_req * q_heads + 256ll * num_sms; }
 cudaError_t launch_shared(const SharedArgs &a, int num_sms, cudaStream_t st);
-cudaError_t launch_join(const JoinArgs &a, int num_sms, int n_groups, cudaStream_t st);
+// parts: about how many there are of a head
+cudaError_t launch_join(const JoinArgs &a, int parts, cudaStream_t st);
+int shared_parts(int n_groups, int kv_heads, int num_sms);
 
 // ---------------------------------------------------------------- norms around a sub-block
 struct NormArgs {

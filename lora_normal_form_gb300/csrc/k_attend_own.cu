@@ -308,5 +308,8 @@ long long own_rows(long long n_req, long long q_heads, int num_sms) {
 cudaError_t launch_attend_own(const AttendArgs &a, int num_sms, cudaStream_t st) {
     return a.kv.dtype == KV_E4M3 ? launch_own_type<true, SHARED>(a, num_sms, st) : launch_own_type<false, SHARED>(a, num_sms, st);
 }
+cudaError_t launch_attend_own_sinks(const AttendArgs &a, int num_sms, cudaStream_t st) {
+    return a.kv.dtype == KV_E4M3 ? launch_own_type<true, SINKS>(a, num_sms, st) : launch_own_type<false, SINKS>(a, num_sms, st);
+}
 
 }  // namespace scute

@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const JoinArgs a) {
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     const int r = real ? row / a.q_heads : 0, h = row - r * a.q_heads, hk = h / a.group;
     if (real) {
-        const int4 piece = a.piece[(long long)r * (a.q_heads / a.group) + hk];
+        const int4 piece = a.piece ? a.piece[(long long)r * (a.q_heads / a.group) + hk] : make_int4(0, -1, 0, 0);
         const int twin = piece.y >= 0 && piece.y & SHARED_TWIN ? 1 : 0, n = piece.w & 0xffff, i = (piece.w >> 16) + h - hk * a.group;
         const int own = a.own_at[r], owns = a.own_at[r + 1] - own;
         const int parts = owns + (piece.y < 0 ? 0 : ((piece.y & ~SHARED_TWIN) - piece.x + 1) << twin);
@@ -976,15 +976,16 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const JoinArgs a) {
 
 }  // namespace
 
-cudaError_t launch_join(const JoinArgs &a, int num_sms, int n_groups, cudaStream_t st) {
+cudaError_t launch_join(const JoinArgs &a, int parts, cudaStream_t st) {
     const auto run = [&](auto kernel, int groups) {
         const int per = JOIN_THREADS / (groups * (a.dim / 4));
         return launch_chained(kernel, (a.rows + per - 1) / per, JOIN_THREADS, 0, st, a);
     };
-    // as many parts as CTAs share a work row, of two streams: few with many groups
-    const int parts = 2 * (num_sms / (n_groups * (a.q_heads / a.group)) + 1);
-    return parts > 8 ? run(join_kernel<4, 8>, 4) : run(join_kernel<1, 4>, 1);
+    return parts > 8 ? run(join_kernel<2, 8>, 2) : run(join_kernel<1, 4>, 1);
 }
+
+// The parts of a work row: as many as CTAs share it, of two streams; few with many groups.
+int shared_parts(int n_groups, int kv_heads, int num_sms) { return 2 * (num_sms / (n_groups * kv_heads) + 1); }
 
 cudaError_t launch_shared(const SharedArgs &a, int num_sms, cudaStream_t st) {
     const bool wide = a.kv.dim > 64;

@@ -135,6 +135,9 @@ scute_status append(scute_ctx *c, const scute_kv_cache *kv, const int32_t *slot_
     return SCUTE_OK;
 }
 
+// Rows of a window and first tokens that are short enough for warps on their own: NN
+constexpr int SHORT_ROW = 2048;
+
 // The parts of scute_shared's workspace, and its bytes (-1: too large).
 struct SharedWork {
     int64_t own_at, stat, o, own_rows, bytes;
@@ -236,22 +239,34 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
         b.status = a.status;
         b.hold = a.hold;
     }
+    // and with sinks by the visible tokens, where the parts find room in the context's workspace
+    bool by_warps = false;
+    if (sinks && t->window && kv->dtype != SCUTE_KV_FP32 && kv->head_dim <= SHARED_MAX_DIM && (int64_t)t->window + sinks <= SHORT_ROW) {
+        const int64_t rows = own_rows(t->n_req, t->q_heads, c->num_sms), at = (t->n_req + 1 + 7) / 8 * 8;
+        by_warps = at + rows * (2 + kv->head_dim) <= (int64_t)attend_part_floats(c->num_sms);
+        if (by_warps) {
+            a.own_at = reinterpret_cast<int *>(c->att_part);
+            a.part_o = c->att_part + at;
+            a.stat = reinterpret_cast<float2 *>(a.part_o + rows * kv->head_dim);
+        }
+    }
     TimedLaunch tl{c, st};
     CU_TRY(c, tl.begin());
     if (together) {
         CU_TRY(c, launch_shared(b, c->num_sms, st));
         count_launch(c, 1);
     }
-    CU_TRY(c, together ? launch_attend_own(a, c->num_sms, st)
+    CU_TRY(c, together   ? launch_attend_own(a, c->num_sms, st)
+              : by_warps ? launch_attend_own_sinks(a, c->num_sms, st)
               : sinks && t->window ? launch_attend_sinks(a, c->num_sms, st)
                                    : launch_attend(a, c->num_sms, st));
     count_launch(c, 1);
-    if (together) {
+    if (together || by_warps) {
         JoinArgs j{};
         j.piece = b.piece;
         j.own_at = a.own_at;
-        j.stat = b.stat;
-        j.o = b.o;
+        j.stat = a.stat;
+        j.o = a.part_o;
         j.v_scale = kv->v_scale;
         j.out = a.out;
         j.out_stride = a.out_stride;
@@ -260,7 +275,7 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
         j.q_heads = a.q_heads;
         j.group = a.group;
         j.dim = kv->head_dim;
-        CU_TRY(c, launch_join(j, c->num_sms, sh->n_groups, st));
+        CU_TRY(c, launch_join(j, together ? shared_parts(sh->n_groups, kv->kv_heads, c->num_sms) : 0, st));
         count_launch(c, 1);
     }
     CU_TRY(c, tl.end(SCUTE_KIND_ATTENTION));
