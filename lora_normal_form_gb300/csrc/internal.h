@@ -495,7 +495,7 @@ int attend_ctrs(int num_sms);
 cudaError_t launch_attend(const AttendArgs &a, int num_sms, cudaStream_t st);
 cudaError_t launch_attend_sinks(const AttendArgs &a, int num_sms, cudaStream_t st);
 cudaError_t launch_attend_own(const AttendArgs &a, int num_sms, cudaStream_t st);      // writes parts, for launch_join
-cudaError_t launch_attend_own_sinks(const AttendArgs &a, int num_sms, cudaStream_t st);  // the same of a window and first tokens
+cudaError_t launch_attend_own_sinks(const AttendArgs &a, int num_sms, cudaStream_t st);  // the same of an e4m3 cache's windows and first tokens
 long long own_rows(long long n_req, long long q_heads, int num_sms);                     // of them, at most
 
 // ---------------------------------------------------------------- the beginning that a group's requests share

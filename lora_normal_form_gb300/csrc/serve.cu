@@ -135,7 +135,12 @@ scute_status append(scute_ctx *c, const scute_kv_cache *kv, const int32_t *slot_
     return SCUTE_OK;
 }
 
-// Rows of a window and first tokens that are short enough for warps on their own: NN
+// Windows and first tokens of an 8-bit cache go to warps on their own (k_attend_own.cu)
+// where there are two rows or more to an SM, of at most this many tokens.  Device times in
+// us, 8 key/value heads of 128, by CTAs and by warps: 200 requests, window 1000, 78.4 and
+// 66.3, window 200, 44.5 and 34.1; 64 requests, window 200, 19.2 and 14.1, 2000, 38.1 and
+// 36.8, 4000, 45.5 and 48.4; 16 requests (128 rows), window 1000, 14.1 and 14.8.  A bf16
+// cache's rows are bound by memory sooner: 200 requests, window 1000, 81.3 and 90.4.
 constexpr int SHORT_ROW = 2048;
 
 // The parts of scute_shared's workspace, and its bytes (-1: too large).
@@ -241,7 +246,8 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
     }
     // and with sinks by the visible tokens, where the parts find room in the context's workspace
     bool by_warps = false;
-    if (sinks && t->window && kv->dtype != SCUTE_KV_FP32 && kv->head_dim <= SHARED_MAX_DIM && (int64_t)t->window + sinks <= SHORT_ROW) {
+    if (sinks && t->window && kv->dtype == SCUTE_KV_E4M3 && kv->head_dim <= SHARED_MAX_DIM && (int64_t)t->window + sinks <= SHORT_ROW &&
+        (int64_t)t->n_req * kv->kv_heads >= 2 * c->num_sms) {
         const int64_t rows = own_rows(t->n_req, t->q_heads, c->num_sms), at = (t->n_req + 1 + 7) / 8 * 8;
         by_warps = at + rows * (2 + kv->head_dim) <= (int64_t)attend_part_floats(c->num_sms);
         if (by_warps) {
