@@ -238,7 +238,8 @@ __device__ __forceinline__ void fork_assign(const ForkArgs &a, int cta, int ctas
     range_of(a, cta, ctas, &p0, &p1);
     for (int base = p0; base < p1; base += FK_THREADS) {
         const int p = base + t, e = p < p1 ? now(a.extra + p) : 0;
-        const bool gone = e < 0;                        // (the claims are settled)
+        const bool gone = e < 0 && e > FK_CLAIM;        // the pages that `settle` counted
+        bad |= e <= FK_CLAIM;                           // (claims are settled: no count at all)
         const int k = rank + cta_exclusive(gone, s.warp_sum, &total);
         rank += total;
         if (!gone) continue;

@@ -532,3 +532,22 @@ def test_refusals_of_forks_copies_norms_and_sinks(scute, contexts):
                  lambda: scute.load().scute_kv_fork(None, None, None)):
         assert null() == 1                    # SCUTE_ERR_ARG
     assert ctx.sync_status() == 0
+
+
+def test_fork_of_counts_that_are_no_counts(scute, contexts):
+    """Counts far below any that rows can leave (a buffer that was never set) are recorded,
+    and nothing is written beside the tables."""
+    for n_in, n_out, page, cols in [(5, 40, 16, 6), (300, 300, 8, 5), (1030, 1030, 16, 12)]:
+        g = np.random.default_rng(n_in)
+        f = Fork(g, n_in, n_out, page, cols, spare=3)
+        wild = np.array([-2 ** 31, -2 ** 31 + 1, -2 ** 31 + 7, -2 ** 30 - 1, -2 ** 30, -9, 2 ** 31 - 1, 0])
+        extra = i32(wild[g.integers(0, len(wild), f.n_pages)])
+        wide = torch.full((n_out, cols + 3), -7, dtype=torch.int32, device="cuda")
+        free, count = i32(np.pad(f.free, (0, f.n_pages - len(f.free)))), i32([len(f.free)])
+        out = [torch.full((n_out,), -5, dtype=torch.int32, device="cuda") for _ in range(4)]
+        contexts["bf16"].kv_fork(i32(f.table), i32(f.len_in), i32(f.source), wide[:, :cols], out[0], page, extra, free, count, count,
+                                 *out[1:], len_new=i32(f.len_new))
+        assert contexts["bf16"].sync_status() == PAGES
+        assert torch.all(wide[:, cols:] == -7) and int(wide[:, :cols].max()) < f.n_pages
+        assert 0 <= int(count) <= f.n_pages and torch.all(free[:int(count)] < f.n_pages)
+        assert -1 <= int(out[2].min()) and int(out[2].max()) < f.n_pages
