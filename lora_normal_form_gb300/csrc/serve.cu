@@ -398,14 +398,15 @@ scute_status scute_kv_fork(scute_ctx *c, const scute_fork *f, void *stream) {
         const int32_t *p;
         int64_t n;
     } in[] = {{f->table_in, table(f->n_in, f->table_in_stride)}, {f->len_in, f->n_in}, {f->source, f->n_out},
-              {f->len_new, f->len_new ? f->n_out : 0}},
+              {f->len_new, f->len_new ? f->n_out : 0}, {f->free_in, 1}},
       out[] = {{f->table_out, table(f->n_out, f->table_out_stride)}, {f->len_out, f->n_out}, {f->copy_from, f->n_out},
                {f->copy_to, f->n_out}, {f->copy_tokens, f->n_out}, {f->extra, f->n_pages}, {f->free_pages, f->n_free_max},
                {f->free_out, 1}};
     const auto overlap = [](const auto &x, const auto &y) { return x.n > 0 && y.n > 0 && x.p < y.p + y.n && y.p < x.p + x.n; };
     for (const auto &y : out) {
         for (const auto &x : in)
-            if (overlap(x, y)) return fail(c, SCUTE_ERR_ARG, "an output overlaps an input");
+            if (overlap(x, y) && !(x.p == f->free_in && y.p == f->free_out))
+                return fail(c, SCUTE_ERR_ARG, "an output overlaps an input");
         for (const auto &x : out)
             if (&x != &y && overlap(x, y)) return fail(c, SCUTE_ERR_ARG, "two outputs overlap");
     }

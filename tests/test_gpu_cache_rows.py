@@ -551,3 +551,15 @@ def test_fork_of_counts_that_are_no_counts(scute, contexts):
         assert torch.all(wide[:, cols:] == -7) and int(wide[:, :cols].max()) < f.n_pages
         assert 0 <= int(count) <= f.n_pages and torch.all(free[:int(count)] < f.n_pages)
         assert -1 <= int(out[2].min()) and int(out[2].max()) < f.n_pages
+
+
+def test_fork_refuses_outputs_over_the_list_s_count(scute, contexts):
+    whole = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    both = whole(3)
+    for name in ("len_out", "copy_to", "extra", "free_pages"):
+        good = dict(table_in=whole(2, 4), len_in=whole(2), source=whole(3), table_out=whole(3, 4), len_out=whole(3), page_size=16,
+                    extra=whole(3), free_pages=whole(3), free_in=both[1:2], free_out=whole(1), copy_from=whole(3),
+                    copy_to=whole(3), copy_tokens=whole(3))
+        contexts["bf16"].kv_fork(**good)
+        with pytest.raises(scute.ScuteError):
+            contexts["bf16"].kv_fork(**{**good, name: both})
