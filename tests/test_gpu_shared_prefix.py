@@ -372,3 +372,27 @@ def test_shared_refusals(scute, contexts):
             raise AssertionError(i)
     ctx.paged_attention(b.cache, b.q, lens, out, shared=good)
     assert ctx.sync_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("all_shared", [True, False])
+def test_shared_as_many_tokens_as_a_row_may_have(scute, contexts, kind, all_shared):
+    """A row of almost 2^30 tokens, all of one page of 127 tokens, shared or the request's own.
+    Every score is 0 and every value of an element the same power of two, so that a CTA's
+    or warp's sums are whole multiples of it (fewer than 2^24) and exact; the at most 2500
+    parts add up in 32 bits, 2500 x 2^-24 < 2^-12 off at most, and the quotient, that far
+    from a power of two, rounds to it (2^-9 or more)."""
+    page, D = 127, 16
+    cols = 2 ** 30 // page
+    n = page * cols
+    as_kv = lambda x: x.expand(1, 1, page, D).contiguous().to(DT[kind])  # noqa: E731
+    v = 2.0 ** (torch.arange(D, device="cuda") % 5 - 2)
+    cache = scute.KvCache(as_kv(torch.zeros(D, device="cuda")), as_kv(v), torch.zeros(1, cols, dtype=torch.int32, device="cuda"))
+    ctx = contexts["bf16"]
+    q, lse = torch.ones(1, 2, D, dtype=torch.bfloat16, device="cuda"), torch.empty(1, 2, device="cuda")
+    out = torch.full_like(q, float("nan"))
+    sh = scute.Shared(i32([0, 1]), i32([n if all_shared else 0]), ctx.shared_work(cache, 1, 2))
+    ctx.paged_attention(cache, q, i32([n]), out, lse=lse, shared=sh)
+    assert ctx.sync_status() == 0
+    assert torch.equal(out, v.bfloat16().expand(1, 2, D))
+    assert np.allclose(lse.cpu().numpy(), np.log(n), rtol=0, atol=1e-4)
