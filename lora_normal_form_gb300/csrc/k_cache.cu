@@ -675,16 +675,24 @@ __global__ void __launch_bounds__(256) kv_append_norm_kernel(const AppendArgs a,
 
 // 16 bytes at a time, items as in kv_append_vec_kernel; a head is `lanes` neighbouring
 // lanes' (a power of two, so that they add up by shuffles), NI items each.  Every lane
-// of a warp goes through the same number of heads.
-constexpr int NORM_CTAS = 4;
+// of a warp goes through the same number of heads, whose pieces it copies to a ring of
+// its own in shared memory ahead of their use, asynchronously: no other thread reads
+// them, so that nothing waits but the thread itself.
+// Bound by memory and by the arithmetic beside it: 8772 rows of 32 + 2 x 8 heads of 128,
+// bf16, three axes, take 40.3 us, 5470 GB/s (81 % of the copy rate; without the norm
+// 38.0).  The same rows fetched to registers, two heads at a time: 54.8 (four CTAs on an
+// SM; two 65.7, three 56.7); with the ring and four CTAs, whose 64 registers spill, 44.4,
+// with two 47.4; a ring of three or six heads 48.2 and 50.6 (four: 48.1, before the
+// arithmetic went two numbers at a time and to one reciprocal root).
+constexpr int NORM_CTAS = 3;
 template <typename T, typename KV, int NI>
 __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(const AppendArgs a, const HeadNormArgs w, int per_row,
                                                                             int lanes) {
-    constexpr int VE = Piece<T>::N, U = 2;
+    constexpr int VE = Piece<T>::N, NORM_RING = NI == 1 ? 4 : 3;
     constexpr unsigned ALL = 0xffffffffu;
     const int rows = blockDim.x / per_row, sub = threadIdx.x / per_row, t = threadIdx.x - sub * per_row;
     const int row = blockIdx.x * rows + sub;
-    if (row >= a.n) return;                             // whole warps: a row has 64 threads or more
+    if (row >= a.n) return;                             // whole warps: a row has 32 threads or more
     const int dim = a.kv.dim, half = a.rot / 2;
     const int joined = a.interleaved ? 0 : half / VE;
     const int items = dim / VE - joined, heads = a.q_heads + 2 * a.kv.heads, k_end = a.q_heads + a.kv.heads;
@@ -703,25 +711,33 @@ __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(cons
     const T *const q_row = reinterpret_cast<const T *>(a.q) + row * a.q_stride;
     const T *const k_row = reinterpret_cast<const T *>(a.k) + row * a.k_stride - a.q_heads * dim;
     const T *const v_row = reinterpret_cast<const T *>(a.v) + row * a.v_stride - k_end * dim;
-    auto load = [&](int from, uint4 (&x0)[U][NI], uint4 (&x1)[U][NI]) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int hh = from + u * stride;
+    const float inv_dim = 1.f / dim;
+    auto times = [](float *y, const float *weight, float f) {       // four elements
+        const float4 x = *reinterpret_cast<const float4 *>(weight);
+        const uint64_t f2 = ptx::two(f, f);
+        const float2 a = ptx::apart(ptx::mul_two(ptx::two(y[0], y[1]), ptx::mul_two(ptx::two(x.x, x.y), f2)));
+        const float2 b = ptx::apart(ptx::mul_two(ptx::two(y[2], y[3]), ptx::mul_two(ptx::two(x.z, x.w), f2)));
+        y[0] = a.x, y[1] = a.y, y[2] = b.x, y[3] = b.y;
+    };
+    // the thread's own pieces of head hh, to its own place of ring slot `slot`
+    extern __shared__ uint4 ring[];
+    auto place = [&](int slot, int piece) { return ring + (slot * 2 * NI + piece) * 256 + threadIdx.x; };
+    auto fetch = [&](int hh, int slot) {
+        if (hh < heads) {
             const T *src = (hh < a.q_heads ? q_row : hh < k_end ? k_row : v_row) + hh * dim;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                x0[u][i] = x1[u][i] = make_uint4(0, 0, 0, 0);
-                if (hh >= heads || !here[i]) continue;
-                x0[u][i] = *reinterpret_cast<const uint4 *>(src + d0[i]);
-                if (two[i]) x1[u][i] = *reinterpret_cast<const uint4 *>(src + d1[i]);
+                if (here[i]) ptx::cp_async16(ptx::smem_u32(place(slot, 2 * i)), src + d0[i]);
+                if (two[i]) ptx::cp_async16(ptx::smem_u32(place(slot, 2 * i + 1)), src + d1[i]);
             }
         }
+        ptx::cp_async_commit();                         // (a group for every head, so that they can be counted)
     };
     ptx::grid_dep_wait();
     ptx::grid_dep_launch();
     const int slot = a.slot_map[row];
-    uint4 x0[U][NI], x1[U][NI];
-    load(h_first, x0, x1);
+#pragma unroll
+    for (int k = 0; k < NORM_RING; ++k) fetch(h_first + k * stride, k);
 
     // the items' cosines and sines (of pairs of neighbours where they are interleaved)
     float c[NI][VE], s[NI][VE];
@@ -770,50 +786,54 @@ __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(cons
     KV *const k_to = reinterpret_cast<KV *>(a.kv.k) + at - a.q_heads * a.kv.head_stride;
     KV *const v_to = reinterpret_cast<KV *>(a.kv.v) + at - k_end * a.kv.head_stride;
 
-    for (int h0 = 0;; h0 += U * stride) {
-        const bool more = h0 + U * stride < heads;
+    int at_slot = 0;
+    for (int h0 = 0; h0 < heads; h0 += stride) {
+        const int hh = h0 + h_first;
+        asm volatile("cp.async.wait_group %0;" ::"n"(NORM_RING - 1) : "memory");
+        const bool is_q = hh < a.q_heads, is_v = hh >= k_end;
+        float y0[NI][VE], y1[NI][VE];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int hh = h0 + h_first + u * stride;
-            const bool is_q = hh < a.q_heads, is_v = hh >= k_end;
-            float y0[NI][VE], y1[NI][VE];
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                Piece<T>::open(x0[u][i], y0[i]);
-                Piece<T>::open(x1[u][i], y1[i]);
-            }
-            const float *weight = is_q ? w.q_w : is_v ? nullptr : w.k_w;
-            float f = 1.f;
-            if (__any_sync(ALL, weight != nullptr)) {
-                auto total = [&](float z) {
-                    for (int o = lanes >> 1; o; o >>= 1) z += __shfl_xor_sync(ALL, z, o);
-                    return z;
-                };
-                if (w.layer) {
-                    float mean = 0.f;
-#pragma unroll
-                    for (int i = 0; i < NI; ++i)
-#pragma unroll
-                        for (int e = 0; e < VE; ++e) mean += y0[i][e] + y1[i][e];
-                    mean = total(mean) / dim;
-                    if (weight)
-#pragma unroll
-                        for (int i = 0; i < NI; ++i)
-#pragma unroll
-                            for (int e = 0; e < VE; ++e) {
-                                if (here[i]) y0[i][e] -= mean;
-                                if (two[i]) y1[i][e] -= mean;
-                            }
-                }
-                float sum = 0.f;
+        for (int i = 0; i < NI; ++i) {
+            const uint4 none = make_uint4(0, 0, 0, 0);
+            Piece<T>::open(hh < heads && here[i] ? *place(at_slot, 2 * i) : none, y0[i]);
+            Piece<T>::open(hh < heads && two[i] ? *place(at_slot, 2 * i + 1) : none, y1[i]);
+        }
+        const float *weight = is_q ? w.q_w : is_v ? nullptr : w.k_w;
+        float f = 1.f;
+        if (__any_sync(ALL, weight != nullptr)) {
+            auto total = [&](float z) {
+                for (int o = lanes >> 1; o; o >>= 1) z += __shfl_xor_sync(ALL, z, o);
+                return z;
+            };
+            if (w.layer) {
+                float mean = 0.f;
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) sum += y0[i][e] * y0[i][e] + y1[i][e] * y1[i][e];
-                sum = total(sum);
-                if (weight) f = 1.f / sqrtf(sum / dim + w.eps);
+                    for (int e = 0; e < VE; ++e) mean += y0[i][e] + y1[i][e];
+                mean = total(mean) * inv_dim;
+                if (weight)
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+#pragma unroll
+                        for (int e = 0; e < VE; ++e) {
+                            if (here[i]) y0[i][e] -= mean;
+                            if (two[i]) y1[i][e] -= mean;
+                        }
             }
-            if (hh >= heads || (!is_q && !in)) continue;
+            uint64_t squares = 0;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int e = 0; e < VE; e += 2) {
+                    const uint64_t p0 = ptx::two(y0[i][e], y0[i][e + 1]), p1 = ptx::two(y1[i][e], y1[i][e + 1]);
+                    squares = ptx::fma_two(p1, p1, ptx::fma_two(p0, p0, squares));
+                }
+            const float2 sum = ptx::apart(squares);
+            const float mean2 = total(sum.x + sum.y) * inv_dim;
+            if (weight) f = rsqrtf(mean2 + w.eps);
+        }
+        if (hh < heads && (is_q || in)) {
             if (!is_v) {
                 if (weight) weight += is_q ? hh * w.q_stride : (hh - a.q_heads) * w.k_stride;
 #pragma unroll
@@ -821,11 +841,8 @@ __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(cons
                     if (weight && here[i]) {
 #pragma unroll
                         for (int e = 0; e < VE; e += 4) {
-                            const float4 x = *reinterpret_cast<const float4 *>(weight + d0[i] + e);
-                            y0[i][e] *= x.x * f, y0[i][e + 1] *= x.y * f, y0[i][e + 2] *= x.z * f, y0[i][e + 3] *= x.w * f;
-                            if (!two[i]) continue;
-                            const float4 y = *reinterpret_cast<const float4 *>(weight + d1[i] + e);
-                            y1[i][e] *= y.x * f, y1[i][e + 1] *= y.y * f, y1[i][e + 2] *= y.z * f, y1[i][e + 3] *= y.w * f;
+                            times(y0[i] + e, weight + d0[i] + e, f);
+                            if (two[i]) times(y1[i] + e, weight + d1[i] + e, f);
                         }
                     }
                     if (!turned[i]) continue;
@@ -838,10 +855,12 @@ __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(cons
                         }
                     } else {
 #pragma unroll
-                        for (int e = 0; e < VE; ++e) {
-                            const float z = y0[i][e] * c[i][e] - y1[i][e] * s[i][e];
-                            y1[i][e] = y1[i][e] * c[i][e] + y0[i][e] * s[i][e];
-                            y0[i][e] = z;
+                        for (int e = 0; e < VE; e += 2) {
+                            const uint64_t p0 = ptx::two(y0[i][e], y0[i][e + 1]), p1 = ptx::two(y1[i][e], y1[i][e + 1]);
+                            const uint64_t cc = ptx::two(c[i][e], c[i][e + 1]), ss = ptx::two(s[i][e], s[i][e + 1]);
+                            const float2 z0 = ptx::apart(ptx::fma_two(p0, cc, ptx::mul_two(ptx::mul_two(p1, ss), ptx::two(-1.f, -1.f))));
+                            const float2 z1 = ptx::apart(ptx::fma_two(p1, cc, ptx::mul_two(p0, ss)));
+                            y0[i][e] = z0.x, y0[i][e + 1] = z0.y, y1[i][e] = z1.x, y1[i][e + 1] = z1.y;
                         }
                     }
                 }
@@ -866,8 +885,8 @@ __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(cons
                 if (two[i]) Piece<T>::store(dst + d1[i], y1[i]);
             }
         }
-        if (!more) break;
-        load(h0 + U * stride + h_first, x0, x1);
+        fetch(hh + NORM_RING * stride, at_slot);
+        if (++at_slot == NORM_RING) at_slot = 0;
     }
 }
 
@@ -935,8 +954,14 @@ cudaError_t launch_kv_append_norm(bool f32, const AppendArgs &a, const HeadNormA
         const int ve = f32 ? 4 : 8, items = a.kv.dim / ve - (a.interleaved ? 0 : a.rot / 2 / ve);
         int lanes = 1;
         while (lanes < items && lanes < 32) lanes *= 2;
-        const int per_row = a.n <= 4 * num_sms ? 256 : 64, rows = 256 / per_row, grid = (a.n + rows - 1) / rows;
-        const auto run = [&](auto kernel) { return launch_chained(kernel, grid, 256, 0, st, a, w, per_row, lanes); };
+        // Threads of a row: many where there are few rows, for the call's latency, a warp where
+        // there are many (its cosines and weights are then fetched once for more heads).  Times in
+        // us with 256, 128, 64 and 32, bf16: 64 rows 3.2, 3.8, 5.3, 8.6; 300 4.1, 4.1, 5.5, 8.7; 608
+        // 6.9, 5.3, 5.6, 8.8; 2000 20.5, 16.8, 15.1, 15.0; 8772 74.7, 55.5, 43.8, 40.3, fp32 81.7,
+        // 68.0, 67.4, 70.7.
+        const int per_row = a.n <= 2 * num_sms ? 256 : a.n <= 4 * num_sms ? 128 : f32 || a.n <= 16 * num_sms ? 64 : 32;
+        const int rows = 256 / per_row, grid = (a.n + rows - 1) / rows, ring = (items > 32 ? 2 * 3 : 4) * 2 * 256 * 16;
+        const auto run = [&](auto kernel) { return launch_chained(kernel, grid, 256, ring, st, a, w, per_row, lanes); };
         if (f32) return items > 32 ? run(kv_append_norm_vec_kernel<float, float, 2>) : run(kv_append_norm_vec_kernel<float, float, 1>);
         if (a.kv.dtype == KV_E4M3) return run(kv_append_norm_vec_kernel<__nv_bfloat16, __nv_fp8_e4m3, 1>);
         return run(kv_append_norm_vec_kernel<__nv_bfloat16, __nv_bfloat16, 1>);

@@ -94,27 +94,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
     return y;
 }
-// Two 32-bit numbers side by side, and operations on both.
-__device__ __forceinline__ uint64_t two(float lo, float hi) {
-    uint64_t y;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(lo), "f"(hi));
-    return y;
-}
-__device__ __forceinline__ float2 apart(uint64_t x) {
-    float2 y;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
-    return y;
-}
-__device__ __forceinline__ uint64_t fma_two(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t y;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
-    return y;
-}
-__device__ __forceinline__ uint64_t add_two(uint64_t a, uint64_t b) {
-    uint64_t y;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
-    return y;
-}
 __device__ __noinline__ float capped(float x, float cap) { return cap * LOG2E * tanhf(x / cap); }
 // Two e4m3 values (16 bits of a word) as two bf16 ones, exactly: 4 bits of significand.
 __device__ __forceinline__ uint32_t to_bf16(uint32_t pair) {
@@ -593,7 +572,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                 if (__any_sync(ALL, mx > top + 8.f)) {
                     const float to = fmaxf(mx, top), al = to == top ? 1.f : exp2f(top - to);
                     top = to;
-                    sum[0] = fma_two(sum[0], two(al, al), 0), sum[1] = fma_two(sum[1], two(al, al), 0);
+                    sum[0] = ptx::fma_two(sum[0], ptx::two(al, al), 0), sum[1] = ptx::fma_two(sum[1], ptx::two(al, al), 0);
                     if (any) {
 #pragma unroll 1
                         for (int c = 0; c < DC / 32; ++c) {
@@ -609,17 +588,17 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
                 const bool adds = any;
                 any = true;
                 const float ref = top == -INFINITY ? 0.f : top;
-                const uint64_t f2 = two(f, f), ref2 = two(-ref, -ref);
+                const uint64_t f2 = ptx::two(f, f), ref2 = ptx::two(-ref, -ref);
                 auto weights = [&](const uint32_t (&y)[32], uint32_t at) {
                     uint32_t w2[32];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        const float2 e = apart(fma_two(two(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), f2, ref2));
+                        const float2 e = ptx::apart(ptx::fma_two(ptx::two(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), f2, ref2));
                         const float p0 = pow2(e.x), p1 = pow2(e.y);
-                        const uint64_t both = two(p0, p1);
-                        sum[k & 1] = add_two(sum[k & 1], both);
+                        const uint64_t both = ptx::two(p0, p1);
+                        sum[k & 1] = ptx::add_two(sum[k & 1], both);
                         const uint32_t hi = pack_bf16(p0, p1);
-                        const float2 left = apart(add_two(both, two(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xffff0000u))));
+                        const float2 left = ptx::apart(ptx::add_two(both, ptx::two(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xffff0000u))));
                         w2[k] = hi;
                         w2[16 + k] = pack_bf16(left.x, left.y);
                     }
@@ -668,7 +647,7 @@ __global__ void __launch_bounds__(THREADS, 1) shared_kernel(const SharedArgs a) 
             seq += w.t1 - w.t0;
             // the stream's part, 32 bytes of a row at a time
             const int n = stream_requests(a, w.w, x) * G, at = part_row(a, w.w, cta, x);
-            const float2 l0 = apart(sum[0]), l1 = apart(sum[1]);
+            const float2 l0 = ptx::apart(sum[0]), l1 = ptx::apart(sum[1]);
             const float l = (l0.x + l0.y) + (l1.x + l1.y);
             if (l != l && top == -INFINITY) top = 0.f;         // no number: not an empty part
             if (i < n) a.stat[at + i] = make_float2(any ? top : -INFINITY, any ? l : 0.f);
