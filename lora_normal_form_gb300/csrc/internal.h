@@ -482,11 +482,11 @@ struct AttendArgs {
     int *status;
     int hold;                  // 1: stages are never given back (test hook of the waits' end)
     // k_attend_own.cu: groups that share the beginnings of their contexts (k_shared.cu), and
-    // the parts, of which request r's are own_at[r] .. own_at[r + 1) - 1, part p of head h the
+    // the parts, of which request r has own_at[r].y from own_at[r].x on, part p of head h the
     // row p q_heads + h of stat and part_o
     const int32_t *start, *shared_len;
     int n_groups;
-    int *own_at;
+    int2 *own_at;
     float2 *stat;
     float *part_o;
 };
@@ -496,7 +496,7 @@ cudaError_t launch_attend(const AttendArgs &a, int num_sms, cudaStream_t st);
 cudaError_t launch_attend_sinks(const AttendArgs &a, int num_sms, cudaStream_t st);
 cudaError_t launch_attend_own(const AttendArgs &a, int num_sms, cudaStream_t st);      // writes parts, for launch_join
 cudaError_t launch_attend_own_sinks(const AttendArgs &a, int num_sms, cudaStream_t st);  // the same of an e4m3 cache's windows and first tokens
-long long own_rows(long long n_req, long long q_heads, int num_sms);                     // of them, at most
+long long own_rows(long long n_req, int q_heads, int kv_heads, int num_sms);             // of them, at most
 
 // ---------------------------------------------------------------- the beginning that a group's requests share
 constexpr int SHARED_MAX_GROUPS = 1024, SHARED_MAX_DIM = 128, SHARED_MAX_GROUP_HEADS = 128;
@@ -526,7 +526,7 @@ struct SharedArgs {
 };
 struct JoinArgs {
     const int4 *piece;         // null: nothing shared
-    const int *own_at;
+    const int2 *own_at;
     const float2 *stat;
     const float *o;
     const float *v_scale;

@@ -897,7 +897,8 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const JoinArgs a) {
     if (real) {
         const int4 piece = a.piece ? a.piece[(long long)r * (a.q_heads / a.group) + hk] : make_int4(0, -1, 0, 0);
         const int twin = piece.y >= 0 && piece.y & SHARED_TWIN ? 1 : 0, n = piece.w & 0xffff, i = (piece.w >> 16) + h - hk * a.group;
-        const int own = a.own_at[r], owns = a.own_at[r + 1] - own;
+        const int2 its = a.own_at[r];
+        const int own = its.x, owns = its.y;
         const int parts = owns + (piece.y < 0 ? 0 : ((piece.y & ~SHARED_TWIN) - piece.x + 1) << twin);
 #pragma unroll 1
         for (int k0 = part0; k0 < parts; k0 += JG * B) {

@@ -135,13 +135,20 @@ scute_status append(scute_ctx *c, const scute_kv_cache *kv, const int32_t *slot_
     return SCUTE_OK;
 }
 
-// Windows and first tokens of an 8-bit cache go to warps on their own (k_attend_own.cu)
-// where there are two rows or more to an SM, of at most this many tokens.  Device times in
-// us, 8 key/value heads of 128, by CTAs and by warps: 200 requests, window 1000, 78.4 and
-// 66.3, window 200, 44.5 and 34.1; 64 requests, window 200, 19.2 and 14.1, 2000, 38.1 and
-// 36.8, 4000, 45.5 and 48.4; 16 requests (128 rows), window 1000, 14.1 and 14.8.  A bf16
-// cache's rows are bound by memory sooner: 200 requests, window 1000, 81.3 and 90.4.
-constexpr int SHORT_ROW = 2048;
+// Windows and first tokens go to warps on their own (k_attend_own.cu) where there are two
+// rows (of a request and key/value head) to an SM or, with more than eight query heads to
+// a key, one; up to as many tokens as this.  Device times in us, by CTAs and by warps,
+// heads of 128:
+//     4 to a key, e4m3    64 requests, window 200 17.2 and 14.5, 1000 26.7 and 19.4, 8000 60.0
+//                         and 50.4, 30000 152 and 132; 200, window 1000 64.1 and 36.8, 8000 162
+//                         and 129; 40 (320 rows), window 200 12.4 and 14.0, 1000 18.8 and
+//                         15.8; 16 (128 rows) 11.5 and 12.8, 12.3 and 14.3
+//     the same, bf16      64 requests, 200 16.6 and 13.6, 2000 35.2 and 35.2, 4000 53.3 and
+//                         55.6; 200, 200 33.6 and 24.4, 2000 90.6 and 89.6, 8000 243 and 253
+//     16 to a key, e4m3   64 requests (256 rows), window 1000 32.8 and 21.4, 30000 161 and
+//                         104; bf16 31.6 and 20.8, 169 and 143
+//     1 to a key of 64, e4m3: 64 requests, window 4000 44.5 and 42.5, 30000 171 and 185
+int own_row_limit(int dtype, int group) { return group > 8 ? 0x7fffffff : dtype == SCUTE_KV_E4M3 ? 16384 : 2048; }
 
 // The parts of scute_shared's workspace, and its bytes (-1: too large).
 struct SharedWork {
@@ -149,10 +156,10 @@ struct SharedWork {
 };
 SharedWork shared_work(int64_t n_req, int64_t q_heads, int64_t kv_heads, int64_t dim, int num_sms) {
     SharedWork w;
-    w.own_rows = own_rows(n_req, q_heads, num_sms);
+    w.own_rows = own_rows(n_req, (int)q_heads, (int)kv_heads, num_sms);
     const int64_t rows = w.own_rows + shared_rows(n_req, q_heads, num_sms);
     w.own_at = 16 * n_req * kv_heads;
-    w.stat = (w.own_at + 4 * (n_req + 1) + 31) / 32 * 32;
+    w.stat = (w.own_at + 8 * n_req + 31) / 32 * 32;
     w.o = (w.stat + 8 * rows + 31) / 32 * 32;
     w.bytes = rows > 0x7fffffff ? -1 : w.o + 4 * rows * dim;
     return w;
@@ -238,20 +245,21 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
         b.n_groups = a.n_groups = sh->n_groups;
         b.first_row = (int)w.own_rows;
         b.piece = reinterpret_cast<int4 *>(work);
-        a.own_at = reinterpret_cast<int *>(work + w.own_at);
+        a.own_at = reinterpret_cast<int2 *>(work + w.own_at);
         b.stat = a.stat = reinterpret_cast<float2 *>(work + w.stat);
         b.o = a.part_o = reinterpret_cast<float *>(work + w.o);
         b.status = a.status;
         b.hold = a.hold;
     }
-    // and with sinks by the visible tokens, where the parts find room in the context's workspace
+    // and with sinks by rows and visible tokens, where the parts find room in the context's workspace
     bool by_warps = false;
-    if (sinks && t->window && kv->dtype == SCUTE_KV_E4M3 && kv->head_dim <= SHARED_MAX_DIM && (int64_t)t->window + sinks <= SHORT_ROW &&
-        (int64_t)t->n_req * kv->kv_heads >= 2 * c->num_sms) {
-        const int64_t rows = own_rows(t->n_req, t->q_heads, c->num_sms), at = (t->n_req + 1 + 7) / 8 * 8;
+    if (sinks && t->window && kv->dtype != SCUTE_KV_FP32 && kv->head_dim <= SHARED_MAX_DIM &&
+        (int64_t)t->window + sinks <= own_row_limit(kv->dtype, a.group) &&
+        (int64_t)t->n_req * kv->kv_heads >= (a.group > 8 ? 1 : 2) * c->num_sms) {
+        const int64_t rows = own_rows(t->n_req, t->q_heads, kv->kv_heads, c->num_sms), at = (2 * t->n_req + 7) / 8 * 8;
         by_warps = at + rows * (2 + kv->head_dim) <= (int64_t)attend_part_floats(c->num_sms);
         if (by_warps) {
-            a.own_at = reinterpret_cast<int *>(c->att_part);
+            a.own_at = reinterpret_cast<int2 *>(c->att_part);
             a.part_o = c->att_part + at;
             a.stat = reinterpret_cast<float2 *>(a.part_o + rows * kv->head_dim);
         }

@@ -565,3 +565,32 @@ def test_fork_refuses_outputs_over_the_list_s_count(scute, contexts):
         contexts["bf16"].kv_fork(**good)
         with pytest.raises(scute.ScuteError):
             contexts["bf16"].kv_fork(**{**good, name: both})
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("window,sinks", [(1, 1), (20, 17), (100, 400), (300, 5)])
+@pytest.mark.parametrize("n,H,group,D,page,token_major", [
+    (160, 2, 4, 128, 16, False), (160, 2, 3, 80, 24, True), (160, 2, 12, 64, 1, False), (90, 4, 1, 64, 7, True), (80, 2, 40, 128, 16, False),
+    (3, 400, 1, 16, 16, False), (1, 2600, 1, 16, 16, True)])
+def test_attention_window_and_first_tokens_of_many_rows(scute, contexts, kind, window, sinks, n, H, group, D, page, token_major):
+    """Rows enough for warps on their own: several requests in a warp's range, ranges that
+    end in a request, heads that have more ranges than one or fewer warps than heads."""
+    g = np.random.default_rng([window, n, H, D])
+    lens = [int(x) for x in np.where(g.random(n) < 0.2, 0, g.integers(1, 500, n))]
+    lens[-1] = 700
+    cache, tokens = make_cache(scute, g, lens, H, D, page, kind, token_major, scales=kind == "fp8")
+    q = torch.from_numpy(g.standard_normal((n, H * group, D), dtype=np.float32) * 1.5).cuda().bfloat16()
+    out, lse = torch.full_like(q, float("nan")), torch.empty(q.shape[:2], device="cuda")
+    ctx, was = contexts["bf16"], None
+    before = ctx.launch_count()
+    for _ in range(2):
+        ctx.paged_attention(cache, q, i32(lens), out, lse=lse, window=window, sinks=sinks)
+        assert ctx.sync_status() == 0
+        assert was is None or (torch.equal(out, was[0]) and torch.equal(lse, was[1]))
+        was = out.clone(), lse.clone()
+    assert ctx.launch_count() - before == 4                  # the rows' kernel and the join of its parts
+    check_attend(out, lse, q, [[x[OB.seen(len(x), window, sinks)] for x in kv] for kv in tokens], kind, group)
+    # more tokens than the rule lets, with up to eight heads to a key: the other kernel
+    ctx.paged_attention(cache, q, i32(lens), out, lse=lse, window=1 << 20, sinks=sinks)
+    assert ctx.sync_status() == 0
+    check_attend(out, lse, q, tokens, kind, group)

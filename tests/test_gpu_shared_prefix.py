@@ -396,3 +396,11 @@ def test_shared_as_many_tokens_as_a_row_may_have(scute, contexts, kind, all_shar
     assert ctx.sync_status() == 0
     assert torch.equal(out, v.bfloat16().expand(1, 2, D))
     assert np.allclose(lse.cpu().numpy(), np.log(n), rtol=0, atol=1e-4)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("n,H", [(3, 400), (1, 2600)])
+def test_shared_many_heads(scute, contexts, kind, n, H):
+    """More key/value heads than the requests' own tokens have warps for."""
+    g = np.random.default_rng([n, H])
+    Batch(scute, g, [(n, 40, lambda j: 300 + 50 * j)], H, 1, 16, 16, kind, scales=kind == "fp8").run(contexts["bf16"])
