@@ -304,13 +304,17 @@ scute_status scute_index_tokens_noalloc(const int8_t *method_of_adapter, int32_t
  * The adapted layer computes a transformer block's projections; the calls of
  * this section do what a serving step needs between them, on the context's
  * device and in its dtype: cache pages and slots for every request's new
- * tokens (scute_kv_resize), rotary positions and the cache write
- * (scute_kv_append), attention of one new token of each request over the
- * paged cache (scute_paged_attention), and the norms, gate and residual that
- * close a sub-block (scute_residual_norm).  The article leaves these to the
- * serving engine; they have no counterpart in it.
+ * tokens (scute_kv_resize), rows that continue other rows and share their
+ * pages (scute_kv_fork, and scute_kv_copy for the pages that they cannot share),
+ * rotary positions and the cache write (scute_kv_append, with norms of every
+ * head first scute_kv_append_norm), attention of one new token of each request
+ * over the paged cache (scute_paged_attention; over a context's first tokens and
+ * its last ones scute_paged_attention_sinks; of requests that share the
+ * beginnings of their contexts scute_paged_attention_shared), and the norms,
+ * gate and residual that close a sub-block (scute_residual_norm).  The article
+ * leaves these to the serving engine; they have no counterpart in it.
  *
- * All four are asynchronous on `stream`, allocate nothing and can be captured
+ * All are asynchronous on `stream`, allocate nothing and can be captured
  * in a CUDA graph.  They read lengths, tables and slots on the device, so a
  * captured step stays valid while those change.  Arguments the host can see
  * are checked before anything is enqueued; what only the device can see (a
@@ -318,7 +322,8 @@ scute_status scute_index_tokens_noalloc(const int8_t *method_of_adapter, int32_t
  * never reads or writes out of range and is recorded in the status word:
  * scute_sync_status then returns SCUTE_ERR_PAGES.  Calls on one context must
  * be ordered on the device (they share its workspace, 30 MB on 152 SMs, which
- * scute_create allocates). */
+ * scute_create allocates; attention of shared beginnings has its own from the
+ * caller besides). */
 
 /* Element type of a cache: BF16 or E4M3 (8-bit float, 4 exponent and 3
  * mantissa bits) in a bf16 context, FP32 in an fp32 context. */

@@ -572,7 +572,8 @@ __global__ void __launch_bounds__(256, 4) kv_append_vec_kernel(const AppendArgs 
 // read once, held in registers, and written once.
 //
 // Any strides and rotary halves: a warp takes a head, a lane its pairs (and the
-// elements behind them) lane, lane + 32, ...
+// elements behind them) lane, lane + 32, ...  Bound by the single elements' loads and
+// stores: 8772 rows that by pieces of 16 bytes take 40.3 us take 369 this way, 64 10.8.
 template <typename T>
 __global__ void __launch_bounds__(256) kv_append_norm_kernel(const AppendArgs a, const HeadNormArgs w) {
     constexpr int UNITS = 8;                        // of a lane: 256 elements without pairs

@@ -22,7 +22,9 @@ namespace {
 //           old entry, or the page of rank L - 1 - n - F, whose own thread finds the
 //           row through the bits; the others of the P are written to the list.
 // No step waits for another's threads, so that the order in which the device works
-// decides nothing.
+// decides nothing.  Bound by latency, a chain of three or four dependent loads in every
+// step and the launches (or the cluster's barriers) between: 64 beams of 200 to 8192 tokens
+// 12 us, one prompt to 64 samples 13.4, 4096 beams 19 (counts and tables are 0.5 MB).
 constexpr int FK_THREADS = 512;
 constexpr int FK_LIST = 0, FK_FREED = 16, FK_BITS = FK_FREED + FORK_MAX_CTAS;    // the workspace's parts
 constexpr int FK_CLAIM = -(1 << 30);                  // claims are below, counts above
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(FK_THREADS) fork_step_kernel(const ForkArgs a)
 }
 
 // All four by one cluster, its barrier between them: where there is little to do, four
-// launches cost more than the step.
+// launches cost more than the step (64 beams with kv_copy: 15.5 us, 17.3 by four).
 constexpr int FK_CLUSTER = 8;
 __global__ void __cluster_dims__(FK_CLUSTER, 1, 1) __launch_bounds__(FK_THREADS) fork_cluster_kernel(const ForkArgs a) {
     __shared__ AssignShared s;
@@ -297,8 +299,10 @@ __global__ void __cluster_dims__(FK_CLUSTER, 1, 1) __launch_bounds__(FK_THREADS)
 
 // ---------------------------------------------------------------- kv_copy
 // A CTA looks through `each` rows and copies the pages of those that have one, in one
-// pool, 16 bytes to a thread at a time, in the order in which the page's tokens and heads
-// lie.
+// pool, 16 bytes to a thread at a time, four of them on their way, in the order in which the
+// page's tokens and heads lie.  Bound by memory where many rows copy (4096 beams, some 2000
+// pages of one layer, 33 MB read and written: 16 us), else by its launch and the chain from
+// the list to the page (64 rows 5 us).
 constexpr int CP_THREADS = 256, CP_ROWS = 32;
 __global__ void __launch_bounds__(CP_THREADS) kv_copy_kernel(const PageCopyArgs a, int each) {
     const int lane = threadIdx.x & 31;
