@@ -24,8 +24,8 @@ namespace scute {
 
 namespace {
 
-// Eight warps on an SM, whose rings are three tiles: twelve with two tiles take 1.5 us more
-// behind 64 requests' shared beginning.
+// Eight warps on an SM, whose rings are three tiles: twelve with two tiles take 39.7 us behind
+// 64 requests' shared beginning (39.0) and 58.8 to 59.1 behind the 250's (59.4).
 constexpr int OWN_WARPS = 4;           // of a CTA
 constexpr int OWN_CTAS = 2;            // of an SM, at most
 constexpr int OWN_RING = 6;            // tiles of a warp's ring, at most
