@@ -606,14 +606,16 @@ scute_status scute_paged_attention_sinks(scute_ctx *ctx, const scute_kv_cache *k
  *               this call alone uses until it has ended; nothing in it needs to be set
  *               before, or is kept for the next call;
  *   a->window   must be 0.
- * Heads of more than 128 elements, more than 128 query heads to a key/value head, and FP32
- * caches are read for each request alone, as in scute_paged_attention. */
+ *   always      0: a beginning of so few tokens, or of so few requests, that reading it once
+ *               saves nothing is read for each request alone; 1: none is for that reason.
+ * Caches of FP32, of heads of more than 128 elements and of more than 128 query heads to a
+ * key/value head are read for each request alone in any case. */
 #define SCUTE_MAX_GROUPS 1024
 typedef struct {
     const int32_t *start, *len;
     void *work;
     int64_t work_bytes;
-    int32_t n_groups;
+    int32_t n_groups, always;
 } scute_shared;
 scute_status scute_paged_attention_shared(scute_ctx *ctx, const scute_kv_cache *kv, const scute_attention *a,
                                           const scute_shared *s, void *stream);

@@ -122,7 +122,7 @@ class _HeadNormStruct(ctypes.Structure):
 
 class _SharedStruct(ctypes.Structure):
     _fields_ = [("start", ctypes.c_void_p), ("len", ctypes.c_void_p), ("work", ctypes.c_void_p),
-                ("work_bytes", ctypes.c_int64), ("n_groups", ctypes.c_int32)]
+                ("work_bytes", ctypes.c_int64), ("n_groups", ctypes.c_int32), ("always", ctypes.c_int32)]
 
 
 class _ForkStruct(ctypes.Structure):
@@ -250,15 +250,16 @@ class Shared:
     """Groups of a batch whose requests share the beginnings of their contexts
     (scute_shared): requests ``start[g]`` .. ``start[g + 1] - 1`` the first ``length[g]``
     tokens (device int32 [groups + 1] and [groups]).  ``work``: a tensor of
-    ``Context.shared_work``, for one call at a time."""
+    ``Context.shared_work``, for one call at a time.  ``always``: beginnings too short, or
+    of too few requests, to gain from it are read for the group too."""
 
-    def __init__(self, start, length, work):
+    def __init__(self, start, length, work, always: bool = False):
         _flat(_torch().int32, length.numel() + 1, start)
         _flat(_torch().int32, length.numel(), length)
         if not work.is_contiguous():
             raise ValueError("the workspace is consecutive bytes")
         self.tensors = (start, length, work)
-        self.struct = _SharedStruct(ptr(start), ptr(length), ptr(work), work.nbytes, length.numel())
+        self.struct = _SharedStruct(ptr(start), ptr(length), ptr(work), work.nbytes, length.numel(), 1 if always else 0)
         self.ref = ctypes.byref(self.struct)
 
 

@@ -486,6 +486,7 @@ struct AttendArgs {
     // row p q_heads + h of stat and part_o
     const int32_t *start, *shared_len;
     int n_groups;
+    int always;                // every group's beginning is read for the group
     int2 *own_at;
     float2 *stat;
     float *part_o;
@@ -517,6 +518,7 @@ struct SharedArgs {
     int page_shift;
     const int32_t *start, *shared_len;
     int n_groups;
+    int always;
     int first_row;             // rows before these parts
     int4 *piece;
     float2 *stat;
@@ -536,6 +538,22 @@ struct JoinArgs {
     int rows, q_heads, group, dim;
 };
 #ifdef __CUDACC__
+// Whether a group's beginning is read for the group, or for each of its requests as if it
+// were their own: by the tokens not read, and what a row's parts cost beside.  Device times of
+// all launches in us, together and alone, 8 key/value heads of 128, 100 tokens of their own:
+//     bf16  1 x 64 requests, 128 tokens 19.5 and 18.3, 512 22.2 and 27.1; 12 x 64 of 64 heads, 64
+//           82.0 and 75.7, 128 81.0 and 93.5; 16 x 4, 256 24.7 and 21.2, 512 28.5 and 27.3, 1024
+//           36.5 and 41.5; 100 x 2, 256 58.1 and 43.6, 1024 117 and 145; 4 x 2, 30000 95 and
+//           102; 12 groups of one on one head, 90000 105 and 100
+//     e4m3  (alone twice as fast, together as fast) 1 x 64, 256 23.5 and 19.7, 512 23.3 and 24.7;
+//           12 x 64, 128 83.3 and 85.1, 256 89.9 and 111; 16 x 4, 1024 37.4 and 32.8; 1 x 4 on
+//           60000 69.2 and 77.4; 4 x 2, 30000 107 and 78, 4 x 3 107 and 117
+template <typename Args>
+__device__ __forceinline__ bool read_together(const Args &a, int requests, int tokens) {
+    const bool e4m3 = a.kv.dtype == KV_E4M3;
+    return a.always ? requests > 0 && tokens > 0
+                    : tokens >= (e4m3 ? 256 : 128) && (long long)(requests - (e4m3 ? 3 : 1)) * tokens >= (e4m3 ? 2048 : 1024);
+}
 // A request's length as it counts, a group's first request, and the group whose shared
 // tokens a request of `length` has (-1: none): both kernels ask the same questions of the
 // same numbers.
@@ -557,9 +575,9 @@ __device__ __forceinline__ int shared_group(const Args &a, int r, int length, in
         if (shared_start(a, mid) <= r) lo = mid;
         else hi = mid - 1;
     }
-    const int cap = a.kv.table_cols * a.kv.page_size, n = a.shared_len[lo];
+    const int cap = a.kv.table_cols * a.kv.page_size, n = a.shared_len[lo], first = shared_start(a, lo), end = shared_start(a, lo + 1);
     *tokens = n > cap ? cap : n;
-    return n > 0 && length >= *tokens && shared_start(a, lo) <= r && r < shared_start(a, lo + 1) ? lo : -1;
+    return length >= *tokens && first <= r && r < end && read_together(a, end - first, *tokens) ? lo : -1;
 }
 #endif
 // rows of parts that a batch may need, beside its own

@@ -193,7 +193,7 @@ constexpr uint32_t instr_desc(int n, bool across) {
 
 // ---------------------------------------------------------------- the plan
 // Groups, made by every CTA for itself: requests start[g] .. start[g + 1), the tokens
-// they share, the first request that has them all (whose row of the table is read; no
+// they share (0 where that is not worth it), the first request that has them all (whose row of the table is read; no
 // such request: no places), and the places of the groups before.
 struct Plan {
     int start[SHARED_MAX_GROUPS + 1], tokens[SHARED_MAX_GROUPS], lead[SHARED_MAX_GROUPS], blocks[SHARED_MAX_GROUPS];
@@ -238,7 +238,8 @@ __device__ __forceinline__ void make_plan(const SharedArgs &a, Plan &p) {
         p.start[g] = min(max(start[i], 0), a.n_req);
         if (g == G) break;
         bad |= tokens[i] < 0 || tokens[i] > cap;
-        p.tokens[g] = min(max(tokens[i], 0), cap);
+        tokens[i] = min(max(tokens[i], 0), cap);
+        p.tokens[g] = read_together(a, min(max(start[i + 1], 0), a.n_req) - p.start[g], tokens[i]) ? tokens[i] : 0;
         p.lead[g] = INT32_MAX;
     }
     __syncthreads();

@@ -243,6 +243,7 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
         b.start = a.start = sh->start;
         b.shared_len = a.shared_len = sh->len;
         b.n_groups = a.n_groups = sh->n_groups;
+        b.always = a.always = sh->always != 0;
         b.first_row = (int)w.own_rows;
         b.piece = reinterpret_cast<int4 *>(work);
         a.own_at = reinterpret_cast<int2 *>(work + w.own_at);

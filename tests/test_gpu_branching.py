@@ -80,7 +80,7 @@ def test_prompts_samples_and_beams(scute, kind):
     def attend(at, q, i, groups):
         """One query of every row over its context: groups of (first row, rows, shared tokens)."""
         start = [0] + [a + m for a, m, _ in groups]
-        sh = scute.Shared(i32(start), i32([t for _, _, t in groups]), ctx.shared_work(views[at][i], n, heads))
+        sh = scute.Shared(i32(start), i32([t for _, _, t in groups]), ctx.shared_work(views[at][i], n, heads), always=True)
         out, lse = torch.full_like(q, float("nan")), torch.empty(n, heads, device="cuda")
         ctx.paged_attention(views[at][i], q, length[at], out, lse=lse, shared=sh)
         tokens = [held(at, r, i) for r in range(n)]

@@ -94,11 +94,11 @@ class Batch:
         q = torch.from_numpy(g.standard_normal((len(rows), H * group, D), dtype=np.float32) * spread)
         self.q = q.cuda().to(DT["fp32" if kind == "fp32" else "bf16"])
 
-    def run(self, ctx, times=2, **kw):
+    def run(self, ctx, times=2, always=True, **kw):
         n, heads = self.q.shape[:2]
         work = ctx.shared_work(self.cache, n, heads)
         work.fill_(255)                                   # not a number, whatever is read of it
-        sh = self.scute.Shared(i32(self.start), i32(self.shared), work)
+        sh = self.scute.Shared(i32(self.start), i32(self.shared), work, always=always)
         out, lse = torch.full_like(self.q, float("nan")), torch.empty(n, heads, device="cuda")
         lens, was = i32(self.lens), None
         for _ in range(times):
@@ -177,7 +177,7 @@ def test_shared_nothing(scute, contexts):
     b.start, b.shared = [0, 0, 7, 7], [50, 0, 12]
     b.run(ctx)
     empty = torch.empty(0, 8, 64, dtype=torch.bfloat16, device="cuda")
-    ctx.paged_attention(b.cache, empty, i32([]), empty, shared=scute.Shared(i32([0, 0]), i32([5]), ctx.shared_work(b.cache, 0, 8)))
+    ctx.paged_attention(b.cache, empty, i32([]), empty, shared=scute.Shared(i32([0, 0]), i32([5]), ctx.shared_work(b.cache, 0, 8), always=True))
     assert ctx.sync_status() == 0
 
 
@@ -192,7 +192,7 @@ def test_shared_strided_in_place_on_another_stream_without_lse(scute, contexts):
     q.copy_(b.q)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
-    lens, sh = i32(b.lens), scute.Shared(i32(b.start), i32(b.shared), ctx.shared_work(b.cache, n, 8))
+    lens, sh = i32(b.lens), scute.Shared(i32(b.start), i32(b.shared), ctx.shared_work(b.cache, n, 8), always=True)
     with torch.cuda.stream(s):
         ctx.paged_attention(b.cache, q, lens, q, shared=sh)
     s.synchronize()
@@ -206,7 +206,7 @@ def test_shared_graph_replay_with_other_lengths_and_groups(scute, contexts):
     b = Batch(scute, g, [(4, 320, lambda j: 320 + 40 * j), (3, 160, lambda j: 200 + j)], 2, 4, 128, 16, "bf16")
     n, full = 7, list(b.lens)
     lens, start, common = i32(full), i32(b.start), i32(b.shared)
-    sh = scute.Shared(start, common, ctx.shared_work(b.cache, n, 8))
+    sh = scute.Shared(start, common, ctx.shared_work(b.cache, n, 8), always=True)
     out, lse = torch.empty_like(b.q), torch.empty(n, 8, device="cuda")
     ctx.paged_attention(b.cache, b.q, lens, out, lse=lse, shared=sh)
     torch.cuda.synchronize()
@@ -233,7 +233,7 @@ def test_shared_out_of_range_is_recorded(scute, contexts):
     out, lse, lens = torch.empty_like(b.q), torch.empty(n, 8, device="cuda"), i32(b.lens)
 
     def run(start, common, cache=b.cache, lens=lens):
-        sh = scute.Shared(i32(start), i32(common), ctx.shared_work(cache, n, 8))
+        sh = scute.Shared(i32(start), i32(common), ctx.shared_work(cache, n, 8), always=True)
         ctx.paged_attention(cache, b.q, lens, out, lse=lse, shared=sh)
         return ctx.sync_status()
 
@@ -275,7 +275,7 @@ def test_shared_offsets_beyond_32_bits(scute, contexts, kind):
     cache, lens = scute.KvCache(*pools, table), i32([70, 80])
     q = torch.from_numpy(g.standard_normal((2, 4, D), dtype=np.float32)).cuda().bfloat16()
     out, lse = torch.empty_like(q), torch.empty(2, 4, device="cuda")
-    ctx.paged_attention(cache, q, lens, out, lse=lse, shared=scute.Shared(i32([0, 2]), i32([64]), ctx.shared_work(cache, 2, 4)))
+    ctx.paged_attention(cache, q, lens, out, lse=lse, shared=scute.Shared(i32([0, 2]), i32([64]), ctx.shared_work(cache, 2, 4), always=True))
     assert ctx.sync_status() == 0
     kk, vv = f64(tok[0]), f64(tok[1])
     tokens = [(np.concatenate([kk[p].transpose(1, 0, 2) for p in row])[:n], np.concatenate([vv[p].transpose(1, 0, 2) for p in row])[:n])
@@ -310,7 +310,7 @@ def test_shared_keeps_the_bits_of_its_weights(scute, contexts, kind, D, group):
     for common in (2, 1):
         out = torch.empty_like(q)
         ctx.paged_attention(cache, q, i32([2] * n), out, scale=1.0,
-                            shared=scute.Shared(i32([0, n]), i32([common]), ctx.shared_work(cache, n, group)))
+                            shared=scute.Shared(i32([0, n]), i32([common]), ctx.shared_work(cache, n, group), always=True))
         assert ctx.sync_status() == 0
         err = np.abs(f64(out) - ref)
         assert np.all(err <= 2.0 ** -20 + 2.0 ** -17 + 2.0 ** -8 * np.abs(ref))
@@ -325,7 +325,7 @@ def test_shared_long_tail_of_small_weights(scute, contexts, kind):
     cache = scute.KvCache(k.to(DT[kind]).cuda(), v.to(DT[kind]).cuda(), i32(np.tile(np.arange(L // 16), (n, 1))))
     q = torch.full((n, 1, D), 1.5, device="cuda").bfloat16()
     out, lse = torch.empty_like(q), torch.empty(n, 1, device="cuda")
-    ctx.paged_attention(cache, q, i32([L] * n), out, lse=lse, shared=scute.Shared(i32([0, n]), i32([L - 8]), ctx.shared_work(cache, n, 1)))
+    ctx.paged_attention(cache, q, i32([L] * n), out, lse=lse, shared=scute.Shared(i32([0, n]), i32([L - 8]), ctx.shared_work(cache, n, 1), always=True))
     assert ctx.sync_status() == 0
     check_attend(out, lse, q, [(f64(k).reshape(-1, 1, D), f64(v).reshape(-1, 1, D))] * n, kind, 1)
 
@@ -337,7 +337,7 @@ def test_shared_whose_waits_run_out_reports_and_recovers(scute, contexts, kind, 
     ctx, g = contexts["bf16"], np.random.default_rng(D)
     b = Batch(scute, g, [(n, 150000 if D == 64 else 80000, lambda j: (150000 if D == 64 else 80000) + j)], 2, 4, D, 16, kind)
     work = ctx.shared_work(b.cache, n, 8)
-    sh = scute.Shared(i32(b.start), i32(b.shared), work)
+    sh = scute.Shared(i32(b.start), i32(b.shared), work, always=True)
     out, lens = torch.empty_like(b.q), i32(b.lens)
     scute.scute_debug_inject(ctx.handle, scute.INJECT_STALL_ATTENTION)
     t0 = time.time()
@@ -355,16 +355,16 @@ def test_shared_refusals(scute, contexts):
     b = Batch(scute, g, [(3, 32, lambda j: 40)], 2, 4, 64, 16, "bf16")
     work = ctx.shared_work(b.cache, 3, 8)
     lens, out = i32(b.lens), torch.empty_like(b.q)
-    good = scute.Shared(i32(b.start), i32(b.shared), work)
+    good = scute.Shared(i32(b.start), i32(b.shared), work, always=True)
     ctx.paged_attention(b.cache, b.q, lens, out, shared=good)
     bad = [lambda: ctx.paged_attention(b.cache, b.q, lens, out, shared=good, window=8),
            lambda: ctx.paged_attention(b.cache, b.q, lens, out, shared=good, sinks=3),
-           lambda: ctx.paged_attention(b.cache, b.q, lens, out, shared=scute.Shared(i32(b.start), i32(b.shared), work[:-32])),
-           lambda: ctx.paged_attention(b.cache, b.q, lens, out, shared=scute.Shared(i32(b.start), i32(b.shared), work[8:])),
-           lambda: ctx.paged_attention(b.cache, b.q, lens, out, shared=scute.Shared(i32([0] * 1026), i32([0] * 1025), work)),
-           lambda: scute.Shared(i32(b.start), i32([1, 2]), work), lambda: scute.Shared(i32(b.start).float(), i32(b.shared), work),
-           lambda: scute.Shared(i32(b.start), i32(b.shared).long(), work), lambda: scute.Shared(i32([0, 1, 2, 3])[::3], i32([1]), work),
-           lambda: scute.Shared(i32(b.start), i32(b.shared), work[::2]),
+           lambda: ctx.paged_attention(b.cache, b.q, lens, out, shared=scute.Shared(i32(b.start), i32(b.shared), work[:-32], always=True)),
+           lambda: ctx.paged_attention(b.cache, b.q, lens, out, shared=scute.Shared(i32(b.start), i32(b.shared), work[8:], always=True)),
+           lambda: ctx.paged_attention(b.cache, b.q, lens, out, shared=scute.Shared(i32([0] * 1026), i32([0] * 1025), work, always=True)),
+           lambda: scute.Shared(i32(b.start), i32([1, 2]), work, always=True), lambda: scute.Shared(i32(b.start).float(), i32(b.shared), work, always=True),
+           lambda: scute.Shared(i32(b.start), i32(b.shared).long(), work, always=True), lambda: scute.Shared(i32([0, 1, 2, 3])[::3], i32([1]), work, always=True),
+           lambda: scute.Shared(i32(b.start), i32(b.shared), work[::2], always=True),
            lambda: ctx.shared_work(b.cache, 16385, 8), lambda: ctx.shared_work(b.cache, -1, 8), lambda: ctx.shared_work(b.cache, 3, 7)]
     for i, call in enumerate(bad):
         with pytest.raises((ValueError, scute.ScuteError)):
@@ -391,7 +391,7 @@ def test_shared_as_many_tokens_as_a_row_may_have(scute, contexts, kind, all_shar
     ctx = contexts["bf16"]
     q, lse = torch.ones(1, 2, D, dtype=torch.bfloat16, device="cuda"), torch.empty(1, 2, device="cuda")
     out = torch.full_like(q, float("nan"))
-    sh = scute.Shared(i32([0, 1]), i32([n if all_shared else 0]), ctx.shared_work(cache, 1, 2))
+    sh = scute.Shared(i32([0, 1]), i32([n if all_shared else 0]), ctx.shared_work(cache, 1, 2), always=True)
     ctx.paged_attention(cache, q, i32([n]), out, lse=lse, shared=sh)
     assert ctx.sync_status() == 0
     assert torch.equal(out, v.bfloat16().expand(1, 2, D))
@@ -404,3 +404,14 @@ def test_shared_many_heads(scute, contexts, kind, n, H):
     """More key/value heads than the requests' own tokens have warps for."""
     g = np.random.default_rng([n, H])
     Batch(scute, g, [(n, 40, lambda j: 300 + 50 * j)], H, 1, 16, 16, kind, scales=kind == "fp8").run(contexts["bf16"])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_shared_only_where_it_saves(scute, contexts, kind):
+    """Groups on both sides of what is read together: by tokens, by requests, by both."""
+    g = np.random.default_rng(4)
+    sizes = [(9, 127), (9, 128), (8, 146), (8, 147), (2, 1023), (2, 1024), (1, 3000), (12, 255), (12, 256), (11, 255), (11, 256), (4, 2047),
+             (4, 2048), (3, 5000), (30, 400)]
+    b = Batch(scute, g, [(n, t, (lambda t: lambda j: t + 7 * j - (j == 2))(t)) for n, t in sizes], 1, 4, 64, 16, kind, before=1, behind=2)
+    for always in (False, True):
+        b.run(contexts["bf16"], always=always)
