@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_vec_kernel(const AppendArgs 
 //
 // Any strides and rotary halves: a warp takes a head, a lane its pairs (and the
 // elements behind them) lane, lane + 32, ...  Bound by the single elements' loads and
-// stores: 8772 rows that by pieces of 16 bytes take 40.3 us take 369 this way, 64 10.8.
+// stores: 8772 rows that by pieces of 16 bytes take 38.8 us take 369 this way, 64 10.8.
 template <typename T>
 __global__ void __launch_bounds__(256) kv_append_norm_kernel(const AppendArgs a, const HeadNormArgs w) {
     constexpr int UNITS = 8;                        // of a lane: 256 elements without pairs
@@ -674,41 +674,39 @@ __global__ void __launch_bounds__(256) kv_append_norm_kernel(const AppendArgs a,
     }
 }
 
-// 16 bytes at a time, items as in kv_append_vec_kernel; a head is `lanes` neighbouring
-// lanes' (a power of two, so that they add up by shuffles), NI items each.  Every lane
-// of a warp goes through the same number of heads, whose pieces it copies to a ring of
-// its own in shared memory ahead of their use, asynchronously: no other thread reads
-// them, so that nothing waits but the thread itself.
+// 16 bytes at a time.  A head is cut into items of two pieces: those that the pairs
+// (i, i + half) join, and behind them any two; with interleaved pairs, any two.  It is
+// `lanes` neighbouring lanes' (a power of two, so that they add up by shuffles), one
+// item each.  Every lane of a warp goes through the same number of heads, whose pieces
+// it copies to a ring of its own in shared memory ahead of their use, asynchronously: no
+// other thread reads them, so that nothing waits but the thread itself.
 // Bound by memory and by the arithmetic beside it: 8772 rows of 32 + 2 x 8 heads of 128,
-// bf16, three axes, take 40.3 us, 5470 GB/s (81 % of the copy rate; without the norm
+// bf16, three axes, take 38.8 us, 5670 GB/s (84 % of the copy rate; without the norm
 // 38.0).  The same rows fetched to registers, two heads at a time: 54.8 (four CTAs on an
 // SM; two 65.7, three 56.7); with the ring and four CTAs, whose 64 registers spill, 44.4,
-// with two 47.4; a ring of three or six heads 48.2 and 50.6 (four: 48.1, before the
-// arithmetic went two numbers at a time and to one reciprocal root).
-constexpr int NORM_CTAS = 3;
-template <typename T, typename KV, int NI>
+// with two 47.4 (three: 40.3); a ring of three or six heads 48.2 and 50.6 (four: 48.1,
+// before the arithmetic went two numbers at a time and to one reciprocal root).  Items of
+// one piece where the rotation joins none: 40.3, and 5848 rows of 64 + 2 x 16 heads of 96,
+// 48 elements of them turned in neighbours, 77.8 us against 43.0.
+constexpr int NORM_CTAS = 3, NORM_RING = 4;
+template <typename T, typename KV>
 __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(const AppendArgs a, const HeadNormArgs w, int per_row,
                                                                             int lanes) {
-    constexpr int VE = Piece<T>::N, NORM_RING = NI == 1 ? 4 : 3;
+    constexpr int VE = Piece<T>::N, HV = VE / 2;
     constexpr unsigned ALL = 0xffffffffu;
     const int rows = blockDim.x / per_row, sub = threadIdx.x / per_row, t = threadIdx.x - sub * per_row;
     const int row = blockIdx.x * rows + sub;
     if (row >= a.n) return;                             // whole warps: a row has 32 threads or more
     const int dim = a.kv.dim, half = a.rot / 2;
-    const int joined = a.interleaved ? 0 : half / VE;
-    const int items = dim / VE - joined, heads = a.q_heads + 2 * a.kv.heads, k_end = a.q_heads + a.kv.heads;
-    const int stride = per_row / lanes, li = t & (lanes - 1), h_first = t / lanes;
-    int d0[NI], d1[NI];
-    bool here[NI], two[NI], turned[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int item = li + i * lanes;
-        here[i] = item < items;
-        two[i] = item < joined;
-        d0[i] = (two[i] ? item : item + joined) * VE;
-        d1[i] = d0[i] + half;
-        turned[i] = here[i] && (two[i] || (a.interleaved && d0[i] < a.rot));
-    }
+    const int items = dim / (2 * VE), heads = a.q_heads + 2 * a.kv.heads, k_end = a.q_heads + a.kv.heads;
+    const int stride = per_row / lanes, item = t & (lanes - 1), h_first = t / lanes;
+    const bool here = item < items, joins = !a.interleaved && item * VE < half;
+    // the item's two pieces, whether they are turned, and the first pairs of their angles (with
+    // joined pieces of VE pairs, HV of them each)
+    const int d0 = a.interleaved || joins ? item * VE : half + item * VE;
+    const int d1 = d0 + (a.interleaved ? dim / 2 : joins ? half : dim / 2 - half);
+    const bool turned0 = here && (joins || (a.interleaved && d0 < a.rot)), turned1 = here && (joins || (a.interleaved && d1 < a.rot));
+    const int p0 = a.interleaved ? d0 / 2 : d0, p1 = a.interleaved ? d1 / 2 : d0 + HV;
     const T *const q_row = reinterpret_cast<const T *>(a.q) + row * a.q_stride;
     const T *const k_row = reinterpret_cast<const T *>(a.k) + row * a.k_stride - a.q_heads * dim;
     const T *const v_row = reinterpret_cast<const T *>(a.v) + row * a.v_stride - k_end * dim;
@@ -722,15 +720,12 @@ __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(cons
     };
     // the thread's own pieces of head hh, to its own place of ring slot `slot`
     extern __shared__ uint4 ring[];
-    auto place = [&](int slot, int piece) { return ring + (slot * 2 * NI + piece) * 256 + threadIdx.x; };
+    auto place = [&](int slot, int piece) { return ring + (slot * 2 + piece) * 256 + threadIdx.x; };
     auto fetch = [&](int hh, int slot) {
-        if (hh < heads) {
+        if (hh < heads && here) {
             const T *src = (hh < a.q_heads ? q_row : hh < k_end ? k_row : v_row) + hh * dim;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                if (here[i]) ptx::cp_async16(ptx::smem_u32(place(slot, 2 * i)), src + d0[i]);
-                if (two[i]) ptx::cp_async16(ptx::smem_u32(place(slot, 2 * i + 1)), src + d1[i]);
-            }
+            ptx::cp_async16(ptx::smem_u32(place(slot, 0)), src + d0);
+            ptx::cp_async16(ptx::smem_u32(place(slot, 1)), src + d1);
         }
         ptx::cp_async_commit();                         // (a group for every head, so that they can be counted)
     };
@@ -740,13 +735,13 @@ __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(cons
 #pragma unroll
     for (int k = 0; k < NORM_RING; ++k) fetch(h_first + k * stride, k);
 
-    // the items' cosines and sines (of pairs of neighbours where they are interleaved)
-    float c[NI][VE], s[NI][VE];
+    // the cosines and sines of HV pairs of each piece
+    float c[VE], s[VE];
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        if (!turned[i]) continue;
-        const int pairs = two[i] ? VE : VE / 2, p0 = two[i] ? d0[i] : d0[i] / 2;
+    for (int i = 0; i < 2; ++i) {
+        if (i ? !turned1 : !turned0) continue;
+        const int first = i ? p1 : p0;
         auto axis_of = [&](int e) { return (e >= a.bound[0]) + (e >= a.bound[1]) + (e >= a.bound[2]); };
         auto row_of = [&](int ax) {
             int p = a.positions[ax * a.axis_stride + row];
@@ -754,28 +749,24 @@ __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(cons
                 bad = true;
                 p = p < 0 ? 0 : a.n_pos - 1;
             }
-            return a.cos_sin + (long long)p * a.rot + p0;
+            return a.cos_sin + (long long)p * a.rot + first;
         };
-        const int ax = axis_of(p0);
+        const int ax = axis_of(first);
         const float *at = row_of(ax);
-        if (pairs % 4 == 0 && a.table16 && ax == axis_of(p0 + pairs - 1)) {
-#pragma unroll
-            for (int e = 0; e < VE; e += 4) {
-                if (e >= pairs) break;
-                const float4 x = *reinterpret_cast<const float4 *>(at + e), y = *reinterpret_cast<const float4 *>(at + half + e);
-                c[i][e] = x.x, c[i][e + 1] = x.y, c[i][e + 2] = x.z, c[i][e + 3] = x.w;
-                s[i][e] = y.x, s[i][e + 1] = y.y, s[i][e + 2] = y.z, s[i][e + 3] = y.w;
-            }
+        float *ci = c + i * HV, *si = s + i * HV;
+        if (HV == 4 && a.table16 && ax == axis_of(first + HV - 1)) {
+            const float4 x = *reinterpret_cast<const float4 *>(at), y = *reinterpret_cast<const float4 *>(at + half);
+            ci[0] = x.x, ci[1] = x.y, ci[HV - 2] = x.z, ci[HV - 1] = x.w;
+            si[0] = y.x, si[1] = y.y, si[HV - 2] = y.z, si[HV - 1] = y.w;
         } else {
             int last_ax = ax;
 #pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                if (e >= pairs) break;
-                const int next = axis_of(p0 + e);
+            for (int e = 0; e < HV; ++e) {
+                const int next = axis_of(first + e);
                 if (next != last_ax) at = row_of(next);
                 last_ax = next;
-                c[i][e] = at[e];
-                s[i][e] = at[half + e];
+                ci[e] = at[e];
+                si[e] = at[half + e];
             }
         }
     }
@@ -792,13 +783,10 @@ __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(cons
         const int hh = h0 + h_first;
         asm volatile("cp.async.wait_group %0;" ::"n"(NORM_RING - 1) : "memory");
         const bool is_q = hh < a.q_heads, is_v = hh >= k_end;
-        float y0[NI][VE], y1[NI][VE];
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const uint4 none = make_uint4(0, 0, 0, 0);
-            Piece<T>::open(hh < heads && here[i] ? *place(at_slot, 2 * i) : none, y0[i]);
-            Piece<T>::open(hh < heads && two[i] ? *place(at_slot, 2 * i + 1) : none, y1[i]);
-        }
+        float y0[VE], y1[VE];
+        const uint4 none = make_uint4(0, 0, 0, 0);
+        Piece<T>::open(hh < heads && here ? *place(at_slot, 0) : none, y0);
+        Piece<T>::open(hh < heads && here ? *place(at_slot, 1) : none, y1);
         const float *weight = is_q ? w.q_w : is_v ? nullptr : w.k_w;
         float f = 1.f;
         if (__any_sync(ALL, weight != nullptr)) {
@@ -809,81 +797,66 @@ __global__ void __launch_bounds__(256, NORM_CTAS) kv_append_norm_vec_kernel(cons
             if (w.layer) {
                 float mean = 0.f;
 #pragma unroll
-                for (int i = 0; i < NI; ++i)
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) mean += y0[i][e] + y1[i][e];
+                for (int e = 0; e < VE; ++e) mean += y0[e] + y1[e];
                 mean = total(mean) * inv_dim;
-                if (weight)
+                if (weight && here)
 #pragma unroll
-                    for (int i = 0; i < NI; ++i)
-#pragma unroll
-                        for (int e = 0; e < VE; ++e) {
-                            if (here[i]) y0[i][e] -= mean;
-                            if (two[i]) y1[i][e] -= mean;
-                        }
+                    for (int e = 0; e < VE; ++e) y0[e] -= mean, y1[e] -= mean;
             }
             uint64_t squares = 0;
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
-#pragma unroll
-                for (int e = 0; e < VE; e += 2) {
-                    const uint64_t p0 = ptx::two(y0[i][e], y0[i][e + 1]), p1 = ptx::two(y1[i][e], y1[i][e + 1]);
-                    squares = ptx::fma_two(p1, p1, ptx::fma_two(p0, p0, squares));
-                }
+            for (int e = 0; e < VE; e += 2) {
+                const uint64_t z0 = ptx::two(y0[e], y0[e + 1]), z1 = ptx::two(y1[e], y1[e + 1]);
+                squares = ptx::fma_two(z1, z1, ptx::fma_two(z0, z0, squares));
+            }
             const float2 sum = ptx::apart(squares);
             const float mean2 = total(sum.x + sum.y) * inv_dim;
             if (weight) f = rsqrtf(mean2 + w.eps);
         }
-        if (hh < heads && (is_q || in)) {
-            if (!is_v) {
-                if (weight) weight += is_q ? hh * w.q_stride : (hh - a.q_heads) * w.k_stride;
+        if (hh < heads && here && (is_q || in)) {
+            if (weight) {
+                weight += is_q ? hh * w.q_stride : (hh - a.q_heads) * w.k_stride;
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    if (weight && here[i]) {
-#pragma unroll
-                        for (int e = 0; e < VE; e += 4) {
-                            times(y0[i] + e, weight + d0[i] + e, f);
-                            if (two[i]) times(y1[i] + e, weight + d1[i] + e, f);
-                        }
-                    }
-                    if (!turned[i]) continue;
-                    if (a.interleaved) {
-#pragma unroll
-                        for (int e = 0; e < VE / 2; ++e) {
-                            const float z = y0[i][2 * e] * c[i][e] - y0[i][2 * e + 1] * s[i][e];
-                            y0[i][2 * e + 1] = y0[i][2 * e + 1] * c[i][e] + y0[i][2 * e] * s[i][e];
-                            y0[i][2 * e] = z;
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < VE; e += 2) {
-                            const uint64_t p0 = ptx::two(y0[i][e], y0[i][e + 1]), p1 = ptx::two(y1[i][e], y1[i][e + 1]);
-                            const uint64_t cc = ptx::two(c[i][e], c[i][e + 1]), ss = ptx::two(s[i][e], s[i][e + 1]);
-                            const float2 z0 = ptx::apart(ptx::fma_two(p0, cc, ptx::mul_two(ptx::mul_two(p1, ss), ptx::two(-1.f, -1.f))));
-                            const float2 z1 = ptx::apart(ptx::fma_two(p1, cc, ptx::mul_two(p0, ss)));
-                            y0[i][e] = z0.x, y0[i][e + 1] = z0.y, y1[i][e] = z1.x, y1[i][e + 1] = z1.y;
-                        }
-                    }
+                for (int e = 0; e < VE; e += 4) {
+                    times(y0 + e, weight + d0 + e, f);
+                    times(y1 + e, weight + d1 + e, f);
                 }
+            }
+            if (!is_v && joins) {
+#pragma unroll
+                for (int e = 0; e < VE; e += 2) {
+                    const uint64_t z0 = ptx::two(y0[e], y0[e + 1]), z1 = ptx::two(y1[e], y1[e + 1]);
+                    const uint64_t cc = ptx::two(c[e], c[e + 1]), ss = ptx::two(s[e], s[e + 1]);
+                    const float2 x0 = ptx::apart(ptx::fma_two(z0, cc, ptx::mul_two(ptx::mul_two(z1, ss), ptx::two(-1.f, -1.f))));
+                    const float2 x1 = ptx::apart(ptx::fma_two(z1, cc, ptx::mul_two(z0, ss)));
+                    y0[e] = x0.x, y0[e + 1] = x0.y, y1[e] = x1.x, y1[e + 1] = x1.y;
+                }
+            } else if (!is_v && a.interleaved) {
+                auto turn = [&](float *y, const float *ci, const float *si) {
+#pragma unroll
+                    for (int e = 0; e < HV; ++e) {
+                        const float z = y[2 * e] * ci[e] - y[2 * e + 1] * si[e];
+                        y[2 * e + 1] = y[2 * e + 1] * ci[e] + y[2 * e] * si[e];
+                        y[2 * e] = z;
+                    }
+                };
+                if (turned0) turn(y0, c, s);
+                if (turned1) turn(y1, c + HV, s + HV);
             }
             const float *scale = is_q ? nullptr : is_v ? a.kv.v_scale : a.kv.k_scale;
             const float div = scale ? scale[is_v ? hh - k_end : hh - a.q_heads] : 1.f;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                if (!here[i]) continue;
-                if (is_q) {
-                    T *dst = q_to + hh * dim;
-                    Piece<T>::store(dst + d0[i], y0[i]);
-                    if (two[i]) Piece<T>::store(dst + d1[i], y1[i]);
-                    continue;
-                }
+            if (is_q) {
+                T *dst = q_to + hh * dim;
+                Piece<T>::store(dst + d0, y0);
+                Piece<T>::store(dst + d1, y1);
+            } else {
                 if (scale) {
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) y0[i][e] /= div, y1[i][e] /= div;
+                    for (int e = 0; e < VE; ++e) y0[e] /= div, y1[e] /= div;
                 }
                 KV *dst = (is_v ? v_to : k_to) + hh * a.kv.head_stride;
-                Piece<T>::store(dst + d0[i], y0[i]);
-                if (two[i]) Piece<T>::store(dst + d1[i], y1[i]);
+                Piece<T>::store(dst + d0, y0);
+                Piece<T>::store(dst + d1, y1);
             }
         }
         fetch(hh + NORM_RING * stride, at_slot);
@@ -952,20 +925,20 @@ cudaError_t launch_kv_append_norm(bool f32, const AppendArgs &a, const HeadNormA
     const bool weights16 = ((reinterpret_cast<uintptr_t>(w.q_w) | reinterpret_cast<uintptr_t>(w.k_w)) & 15) == 0 &&
                            (w.q_stride | w.k_stride) % 4 == 0;
     if (weights16 && (f32 ? by_pieces<float>(a) : by_pieces<__nv_bfloat16>(a))) {
-        const int ve = f32 ? 4 : 8, items = a.kv.dim / ve - (a.interleaved ? 0 : a.rot / 2 / ve);
+        const int items = a.kv.dim / (f32 ? 8 : 16);
         int lanes = 1;
-        while (lanes < items && lanes < 32) lanes *= 2;
+        while (lanes < items) lanes *= 2;
         // Threads of a row: many where there are few rows, for the call's latency, a warp where
         // there are many (its cosines and weights are then fetched once for more heads).  Times in
-        // us with 256, 128, 64 and 32, bf16: 64 rows 3.2, 3.8, 5.3, 8.6; 300 4.1, 4.1, 5.5, 8.7; 608
-        // 6.9, 5.3, 5.6, 8.8; 2000 20.5, 16.8, 15.1, 15.0; 8772 74.7, 55.5, 43.8, 40.3, fp32 81.7,
-        // 68.0, 67.4, 70.7.
+        // us with 256, 128, 64 and 32, bf16: 64 rows 3.1, 3.6, 5.0, 7.9; 300 4.0, 3.9, 5.1, 8.0; 608
+        // 6.7, 5.1, 5.1, 8.0; 2000 19.8, 16.1, 14.5, 14.3; 8772 72.3, 53.2, 42.3, 38.7, fp32 81.6,
+        // 67.4, 67.3, 70.1.
         const int per_row = a.n <= 2 * num_sms ? 256 : a.n <= 4 * num_sms ? 128 : f32 || a.n <= 16 * num_sms ? 64 : 32;
-        const int rows = 256 / per_row, grid = (a.n + rows - 1) / rows, ring = (items > 32 ? 2 * 3 : 4) * 2 * 256 * 16;
-        const auto run = [&](auto kernel) { return launch_chained(kernel, grid, 256, ring, st, a, w, per_row, lanes); };
-        if (f32) return items > 32 ? run(kv_append_norm_vec_kernel<float, float, 2>) : run(kv_append_norm_vec_kernel<float, float, 1>);
-        if (a.kv.dtype == KV_E4M3) return run(kv_append_norm_vec_kernel<__nv_bfloat16, __nv_fp8_e4m3, 1>);
-        return run(kv_append_norm_vec_kernel<__nv_bfloat16, __nv_bfloat16, 1>);
+        const int rows = 256 / per_row, grid = (a.n + rows - 1) / rows;
+        const auto run = [&](auto kernel) { return launch_chained(kernel, grid, 256, NORM_RING * 2 * 256 * 16, st, a, w, per_row, lanes); };
+        if (f32) return run(kv_append_norm_vec_kernel<float, float>);
+        if (a.kv.dtype == KV_E4M3) return run(kv_append_norm_vec_kernel<__nv_bfloat16, __nv_fp8_e4m3>);
+        return run(kv_append_norm_vec_kernel<__nv_bfloat16, __nv_bfloat16>);
     }
     if (f32) return launch_chained(kv_append_norm_kernel<float>, a.n, 256, 0, st, a, w);
     return launch_chained(kv_append_norm_kernel<__nv_bfloat16>, a.n, 256, 0, st, a, w);
