@@ -14,7 +14,9 @@ namespace {
 //           one number does neither: most pages of a beam's new row are its old
 //           one's).  Afterwards extra[p] < 0 says that nobody holds page p whole;
 //   claim   a new row whose last page, filled in part, is such a page claims it:
-//           the smallest row's mark stays, r - INT_MAX, below every count;
+//           the smallest row's mark stays, r - INT_MAX, below every count.  Every page
+//           that a new row took whole is looked at again: counts that held fewer rows
+//           than the tables named would give it up or to another row, and are recorded;
 //   settle  rows whose claim stayed keep the page, others that end in part get their
 //           bit set (they copy); pages left without holder are counted by ranges;
 //   assign  with L = F + P entries in the list (F old ones, P pages given up, in the
@@ -24,7 +26,8 @@ namespace {
 // No step waits for another's threads, so that the order in which the device works
 // decides nothing.  Bound by latency, a chain of three or four dependent loads in every
 // step and the launches (or the cluster's barriers) between: 64 beams of 200 to 8192 tokens
-// 12 us, one prompt to 64 samples 13.4, 4096 beams 19 (counts and tables are 0.5 MB).
+// 12.5 us, one prompt to 64 samples 15, 4096 beams 13.7 (counts and tables are 0.5 MB);
+// without the second look at pages held whole 11.1, 12.8 and 12.8.
 constexpr int FK_THREADS = 512;
 constexpr int FK_LIST = 0, FK_FREED = 16, FK_BITS = FK_FREED + FORK_MAX_CTAS;    // the workspace's parts
 constexpr int FK_CLAIM = -(1 << 30);                  // claims are below, counts above
@@ -108,11 +111,37 @@ __device__ __forceinline__ int last_page(const ForkArgs &a, int r, NewRow *x) {
 }
 
 __device__ __forceinline__ void fork_claim(const ForkArgs &a, int cta, int ctas) {
-    for (int r = cta * FK_THREADS + threadIdx.x; r < a.n_out; r += ctas * FK_THREADS) {
-        NewRow x;
-        const int p = last_page(a, r, &x);
-        if (in_pool(a, p) && now(a.extra + p) < 0) atomicMin(a.extra + p, r - INT32_MAX);
+    const int lane = threadIdx.x & 31, claiming = min((a.n_out + FK_THREADS - 1) / FK_THREADS, ctas - 1);
+    bool bad = false;
+    if (cta < claiming) {
+        for (int r = cta * FK_THREADS + threadIdx.x; r < a.n_out; r += claiming * FK_THREADS) {
+            NewRow x;
+            const int p = last_page(a, r, &x), e = in_pool(a, p) ? now(a.extra + p) : 0;
+            if (e >= 0) continue;
+            bad |= e < -1 && e > FK_CLAIM;             // more rows than holders: the claim takes the count's place
+            atomicMin(a.extra + p, r - INT32_MAX);
+        }
+    } else {                                           // beside them, so that neither waits for the other's loads
+        const int spans = (a.cols + FK_SPAN - 1) / FK_SPAN;
+        const long long items = (long long)a.n_out * spans, step = (long long)(ctas - claiming) * (FK_THREADS / 32);
+#pragma unroll 1
+        for (long long i = (long long)(cta - claiming) * (FK_THREADS / 32) + (threadIdx.x >> 5); i < items; i += step) {
+            const int r = (int)(i / spans), j0 = (int)(i - (long long)r * spans) * FK_SPAN;
+            const int32_t *to = a.table_out + r * a.out_stride;
+            int q[FK_SPAN / 32];
+#pragma unroll
+            for (int k = 0; k < FK_SPAN / 32; ++k) {
+                const int j = j0 + k * 32 + lane;
+                q[k] = j < a.cols ? now(to + j) : -1;  // (asked for before the row's tokens are known)
+            }
+            bool seen = false;                         // recorded by the first step
+            const int full = page_index(a, new_row(a, r, &seen).len);
+#pragma unroll
+            for (int k = 0; k < FK_SPAN / 32; ++k)
+                if (j0 + k * 32 + lane < full && in_pool(a, q[k])) bad |= now(a.extra + q[k]) < 0;
+        }
     }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, STATUS_PAGES);
 }
 
 // Exclusive prefix sum over the CTA's threads; *total receives the sum.
@@ -277,7 +306,8 @@ __global__ void __launch_bounds__(FK_THREADS) fork_step_kernel(const ForkArgs a)
 }
 
 // All four by one cluster, its barrier between them: where there is little to do, four
-// launches cost more than the step (64 beams with kv_copy: 15.5 us, 17.3 by four).
+// launches cost more than the step (64 beams with kv_copy: a call through Python 40 us, by four
+// launches 49; in a graph, where launches cost less, 17.3 and 16.3).
 constexpr int FK_CLUSTER = 8;
 __global__ void __cluster_dims__(FK_CLUSTER, 1, 1) __launch_bounds__(FK_THREADS) fork_cluster_kernel(const ForkArgs a) {
     __shared__ AssignShared s;
@@ -352,6 +382,7 @@ cudaError_t launch_kv_fork(const ForkArgs &a, int num_sms, int *launches, cudaSt
     const long long rows = max(a.n_in, a.n_out), items = rows * ((a.cols + FK_SPAN - 1) / FK_SPAN);
     const int most = min(num_sms, FORK_MAX_CTAS);
     const int row_grid = max(1, min(most, (a.n_out + FK_THREADS - 1) / FK_THREADS));
+    const int span_grid = (int)max(1ll, min(4ll * most, (items + warps - 1) / warps));
     const int page_grid = max(row_grid, (int)min((long long)most, ((long long)a.n_pages + FK_THREADS - 1) / FK_THREADS));
     // one cluster up to as many table spans and pages as its warps take in a few turns
     if (items <= 4 * FK_CLUSTER * warps && a.n_pages <= 16 * FK_CLUSTER * FK_THREADS) {
@@ -359,8 +390,8 @@ cudaError_t launch_kv_fork(const ForkArgs &a, int num_sms, int *launches, cudaSt
         return launch_chained(fork_cluster_kernel, FK_CLUSTER, FK_THREADS, 0, st, a);
     }
     *launches = 4;
-    cudaError_t e = launch_chained(fork_step_kernel<0>, (int)max(1ll, min(4ll * most, (items + warps - 1) / warps)), FK_THREADS, 0, st, a);
-    if (e == cudaSuccess) e = launch_chained(fork_step_kernel<1>, row_grid, FK_THREADS, 0, st, a);
+    cudaError_t e = launch_chained(fork_step_kernel<0>, span_grid, FK_THREADS, 0, st, a);
+    if (e == cudaSuccess) e = launch_chained(fork_step_kernel<1>, row_grid + span_grid, FK_THREADS, 0, st, a);
     if (e == cudaSuccess) e = launch_chained(fork_step_kernel<2>, page_grid, FK_THREADS, 0, st, a);
     if (e == cudaSuccess) e = launch_chained(fork_step_kernel<3>, page_grid, FK_THREADS, 0, st, a);
     return e;

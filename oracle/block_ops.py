@@ -141,19 +141,25 @@ def fork(table_in, len_in, source, len_new, table_out, page_size, extra, free, n
         want = have if len_new is None or s < 0 else int(len_new[r])
         ok = ok and 0 <= want <= have
         rows.append((s, min(max(want, 0), have)))
+    lost, won = [0] * n_pages, [0] * n_pages           # rows of the old table with a page, and new ones with all of it
     for r in range(n_in):
         for j in range(ceil_div(old[r], page_size)):
             if inside(table_in[r, j]):
-                extra[table_in[r, j]] -= 1
+                lost[table_in[r, j]] += 1
             else:
                 ok = False
     for r, (s, n) in enumerate(rows):
         for j in range(n // page_size):
             table[r, j] = table_in[s, j]
             if inside(table_in[s, j]):
-                extra[table_in[s, j]] += 1
+                won[table_in[s, j]] += 1
             else:
                 ok = False
+    for p in range(n_pages):
+        # more rows had the page than its count allows: it has fewer holders than none, or none
+        # though a new row has it
+        extra[p] += won[p] - lost[p]
+        ok = ok and extra[p] >= -1 and (extra[p] >= 0 or not won[p])
     n_out = len(rows)
     len_out, copies = [n for _, n in rows], []
     copy_from, copy_to, copy_tokens = ([-1] * n_out, [-1] * n_out, [0] * n_out)
@@ -174,7 +180,6 @@ def fork(table_in, len_in, source, len_new, table_out, page_size, extra, free, n
     for p in range(n_pages):
         if extra[p] < 0:
             if p not in claimed:
-                ok = ok and extra[p] == -1
                 free.append(p)
             extra[p] = 0
     for r, p, full, rest in copies:

@@ -93,6 +93,20 @@ def test_head_norm_and_seen_pins():
     assert OB.seen(9, 3, 100) == list(range(9)) and OB.seen(0, 3, 2) == [] and OB.seen(9, 0, 2) == list(range(9))
 
 
+def test_fork_counts_rows_by_themselves():
+    """More rows of a page than its count allows: noticed where the page is given up, or to another
+    row, though a row has it, and where its count falls below nobody; and only there."""
+    two = np.array([[0], [0]])
+    go = lambda lens, source, extra, new=None: OB.fork(two, lens, source, new, np.full((len(source), 1), -1), 16, [extra], [])  # noqa: E731
+    out = go([16, 16], [0], 0)
+    assert not out["ok"] and out["table"].tolist() == [[0]] and out["free"] == [0]
+    assert not go([5, 5], [0], 0)["ok"] and not go([16, 16], [0, 1], 0, [16, 5])["ok"] and not go([16, 16], [-1], 0)["ok"]
+    assert not go([16, 16], [1], 0)["ok"] and not go([16, 16], [0], 0, [5])["ok"]
+    for lens, source, new in (([16, 16], [0], None), ([16, 16], [0, 1], [16, 0]), ([16, 16], [-1], None)):
+        assert go(lens, source, 1, new)["ok"]
+    assert go([16, 16], [0, 1], 0)["ok"]               # nobody lets go: nothing is given away
+
+
 # ---------------------------------------------------------------- the binding
 STRUCTS = {"scute_head_norm": "_HeadNormStruct", "scute_fork": "_ForkStruct", "scute_shared": "_SharedStruct"}
 

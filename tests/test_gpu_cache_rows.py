@@ -594,3 +594,40 @@ def test_attention_window_and_first_tokens_of_many_rows(scute, contexts, kind, w
     ctx.paged_attention(cache, q, i32(lens), out, lse=lse, window=1 << 20, sinks=sinks)
     assert ctx.sync_status() == 0
     check_attend(out, lse, q, tokens, kind, group)
+
+
+def counted_short():
+    """Old tables with more rows of a page than its count allows: (table, len_in, source, len_new, extra, whether
+    the step can go on without giving a held page away), pages of 16 tokens."""
+    two, whole, part = [[0], [0]], [16, 16], [5, 5]
+    return [(two, whole, [0], None, [0], False),              # kept whole by one: given up all the same
+            (two, whole, [1], None, [0], False), (two, whole, [-1, 1], None, [0], False),
+            (two, whole, [-1, -1, 0], None, [0], False),      # the same, counted down and up
+            (two, part, [0], None, [0], False),               # below nobody, and claimed
+            (two, part, [1, 0, 1], None, [0], False),
+            (two, whole, [0, 1], [16, 5], [0], False),        # one's whole, another ends in it
+            (two, whole, [0], [5], [0], False),
+            (two, whole, [-1], None, [0], False),             # nobody's, below nobody
+            ([[0, 1], [0, 2], [0, 3]], [32, 20, 16], [0], None, [1, 0, 0, 0], False),
+            (two, whole, [0], None, [1], True), (two, part, [0], None, [1], True), (two, whole, [0, 1], [16, 5], [1], True),
+            (two, whole, [-1], None, [1], True), ([[0], [0]], whole, [-1], None, [2], True),
+            ([[0, 1], [0, 2], [0, 3]], [32, 20, 16], [0, 1], None, [2, 0, 0, 0], True)]
+
+
+@pytest.mark.parametrize("case", range(len(counted_short())))
+@pytest.mark.parametrize("beside", [0, 1030])
+def test_fork_records_pages_of_more_rows_than_their_count(scute, contexts, case, beside):
+    """A page that a row still names is not given up, or to a row that ends in it, without a word; alone
+    (one cluster) and beside many healthy rows (four launches)."""
+    table, len_in, source, len_new, extra, fine = counted_short()[case]
+    f = Fork(np.random.default_rng(case), beside, beside, 16, 2, spare=beside + 4)
+    n, at = beside, f.n_pages
+    f.table = np.concatenate([f.table, np.full((len(table), 2), -1)])
+    for r, row in enumerate(table):
+        f.table[n + r, :len(row)] = np.array(row) + at
+    f.len_in = np.concatenate([f.len_in, len_in]).astype(np.int64)
+    f.extra, f.n_pages = np.concatenate([f.extra, extra]), at + len(extra)
+    new = [16 * 2 if s < 0 else len_in[s] for s in source] if len_new is None else len_new
+    f.len_new = np.concatenate([f.len_new, [0 if s < 0 else x for s, x in zip(source, new)]]).astype(np.int64)
+    f.source = np.concatenate([f.source, [s if s < 0 else s + n for s in source]]).astype(np.int64)
+    assert f.run(contexts["bf16"])[0]["ok"] == fine
