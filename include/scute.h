@@ -433,13 +433,13 @@ scute_status scute_kv_resize(scute_ctx *ctx, const int32_t *len_in, const int32_
  *   table_out, len_out  device int32 [n_out][table_out_stride], [n_out].  Entries
  *                       behind a row's pages are left as they were;
  *   extra               device int32 [n_pages], changed in place.  A page number
- *                       outside 0..n_pages - 1 is taken over uncounted and
- *                       recorded.  So is a page with more rows in the old table
- *                       than holders, when the step leaves it a count below -1,
- *                       or nobody though a new row takes it whole (it is given
- *                       up, or stays with a row that ends in it, all the same;
- *                       an old table that names such pages, all of which stay
- *                       held, is not noticed);
+ *                       outside 0..n_pages - 1, of the old table or of the free
+ *                       list, is taken over uncounted and recorded.  So is a page
+ *                       with more rows in the old table than holders, when the
+ *                       step leaves it a count below -1, or nobody though a new
+ *                       row takes it whole (it is given up, or stays with a row
+ *                       that ends in it, all the same; an old table that names
+ *                       such pages, all of which stay held, is not noticed);
  *   free_pages, n_free_max, free_in, free_out   the list as for scute_kv_resize;
  *                       entries from the new count on keep what they held, and
  *                       pages beyond n_free_max entries are lost (SCUTE_ERR_PAGES);

@@ -261,7 +261,9 @@ __device__ __forceinline__ void fork_assign(const ForkArgs &a, int cta, int ctas
             a.copy_from[r] = -1;
             a.copy_tokens[r] = 0;
         } else if (at < F) {
-            give(r, a.free_pages[at]);
+            const int page = a.free_pages[at];
+            bad |= !in_pool(a, page);
+            give(r, page);
         }
     }
     // pages that nobody holds any more

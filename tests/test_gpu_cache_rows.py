@@ -631,3 +631,22 @@ def test_fork_records_pages_of_more_rows_than_their_count(scute, contexts, case,
     f.len_new = np.concatenate([f.len_new, [0 if s < 0 else x for s, x in zip(source, new)]]).astype(np.int64)
     f.source = np.concatenate([f.source, [s if s < 0 else s + n for s in source]]).astype(np.int64)
     assert f.run(contexts["bf16"])[0]["ok"] == fine
+
+
+@pytest.mark.parametrize("n", [3, 1030])
+@pytest.mark.parametrize("outside", [0, -1, 2 ** 31 - 1])
+def test_fork_records_pages_of_the_list_that_are_none(scute, contexts, n, outside):
+    """A number outside the pool that the free list hands to a row that copies; one that stays in the list is
+    nobody's yet."""
+    f = object.__new__(Fork)
+    f.page, f.cols, f.n_pages = 16, 3, 2 * n + 5           # every old row ends in its page, and two new ones in it
+    f.table = np.full((n, 3), -1)
+    f.table[:, 0] = np.arange(n)
+    f.len_in, f.extra = np.full(n, 5), np.zeros(f.n_pages, np.int64)
+    f.source, f.len_new = np.repeat(np.arange(n), 2), np.full(2 * n, 4)
+    outside = outside or f.n_pages
+    for place, fine in ((-1, False), (5, False), (4, True)):     # five entries are left
+        f.free = list(range(n, 2 * n + 5))
+        f.free[place] = outside
+        ref = f.run(contexts["bf16"])[0]
+        assert ref["ok"] == fine and np.count_nonzero(ref["copy_from"] >= 0) == n
