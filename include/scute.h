@@ -606,7 +606,7 @@ scute_status scute_paged_attention_sinks(scute_ctx *ctx, const scute_kv_cache *k
  *               [n_groups], 0..table_cols * page_size.  What lies outside counts as the
  *               nearest inside and is recorded (SCUTE_ERR_PAGES), as is a start that
  *               falls, with which the groups' outputs are undefined;
- *   n_groups    0..SCUTE_MAX_GROUPS;
+ *   n_groups    0..SCUTE_MAX_GROUPS (0: start, len and work are not read);
  *   work        device memory of at least scute_shared_bytes, 32-byte aligned, that
  *               this call alone uses until it has ended; nothing in it needs to be set
  *               before, or is kept for the next call;

@@ -585,6 +585,7 @@ inline long long shared_rows(long long n_req, long long q_heads, int num_sms) { 
 cudaError_t launch_shared(const SharedArgs &a, int num_sms, cudaStream_t st);
 // parts: about how many there are of a head
 cudaError_t launch_join(const JoinArgs &a, int parts, cudaStream_t st);
+cudaError_t launch_check_groups(const AttendArgs &a, cudaStream_t st);      // behind launch_attend
 int shared_parts(int n_groups, int kv_heads, int num_sms);
 
 // ---------------------------------------------------------------- norms around a sub-block

@@ -884,6 +884,22 @@ cudaError_t launch_shape(const SharedArgs &a, int num_sms, cudaStream_t st) {
     return launch_chained(kernel, num_sms, THREADS, S::SMEM, st, a);
 }
 
+// ---------------------------------------------------------------- groups that no kernel reads
+// The status of the groups' numbers (make_plan's), where each request is read alone.  Launched
+// behind that attention, whose CTAs have all waited for what is read here, and beside it: 0.3 to
+// 0.5 us of a call of 12 to 48.
+__global__ void __launch_bounds__(256) check_groups_kernel(const int32_t *start, const int32_t *length, int groups, int n_req, int cap,
+                                                           int *status) {
+    ptx::grid_dep_launch();
+    bool bad = false;
+    for (int g = threadIdx.x; g <= groups; g += 256) {
+        const int from = start[g];
+        bad |= from < 0 || from > n_req || (g < groups && (start[g + 1] < from || length[g] < 0 || length[g] > cap));
+    }
+    if (bad) atomicOr(status, STATUS_PAGES);
+    ptx::grid_dep_wait();
+}
+
 // ---------------------------------------------------------------- the parts of a request's heads, joined
 // out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the parts of a head: that of
 // its own tokens, and those of the tokens its group shares, in the order of their CTAs.
@@ -966,6 +982,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const JoinArgs a) {
 }
 
 }  // namespace
+
+cudaError_t launch_check_groups(const AttendArgs &a, cudaStream_t st) {
+    return launch_chained(check_groups_kernel, 1, 256, 0, st, a.start, a.shared_len, a.n_groups, a.n_req, a.kv.table_cols * a.kv.page_size, a.status);
+}
 
 cudaError_t launch_join(const JoinArgs &a, int parts, cudaStream_t st) {
     const auto run = [&](auto kernel, int groups) {

@@ -228,6 +228,12 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
     const bool together = sh && sh->n_groups > 0 && kv->dtype != SCUTE_KV_FP32 && kv->head_dim <= SHARED_MAX_DIM &&
                           a.group <= SHARED_MAX_GROUP_HEADS && t->n_req * t->q_stride / 8 < 0x7fffffff;
     SharedArgs b{};
+    if (sh) {
+        a.start = sh->start;
+        a.shared_len = sh->len;
+        a.n_groups = sh->n_groups;
+        a.always = sh->always != 0;
+    }
     if (together) {
         char *work = static_cast<char *>(sh->work);
         b.kv = a.kv;
@@ -240,10 +246,10 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
         b.scale = a.scale;
         b.softcap = a.softcap;
         b.page_shift = a.page_shift;
-        b.start = a.start = sh->start;
-        b.shared_len = a.shared_len = sh->len;
-        b.n_groups = a.n_groups = sh->n_groups;
-        b.always = a.always = sh->always != 0;
+        b.start = a.start;
+        b.shared_len = a.shared_len;
+        b.n_groups = a.n_groups;
+        b.always = a.always;
         b.first_row = (int)w.own_rows;
         b.piece = reinterpret_cast<int4 *>(work);
         a.own_at = reinterpret_cast<int2 *>(work + w.own_at);
@@ -276,6 +282,10 @@ scute_status attend(scute_ctx *c, const scute_kv_cache *kv, const scute_attentio
               : sinks && t->window ? launch_attend_sinks(a, c->num_sms, st)
                                    : launch_attend(a, c->num_sms, st));
     count_launch(c, 1);
+    if (sh && !together && sh->n_groups > 0) {
+        CU_TRY(c, launch_check_groups(a, st));
+        count_launch(c, 1);
+    }
     if (together || by_warps) {
         JoinArgs j{};
         j.piece = b.piece;

@@ -415,3 +415,38 @@ def test_shared_only_where_it_saves(scute, contexts, kind):
     b = Batch(scute, g, [(n, t, (lambda t: lambda j: t + 7 * j - (j == 2))(t)) for n, t in sizes], 1, 4, 64, 16, kind, before=1, behind=2)
     for always in (False, True):
         b.run(contexts["bf16"], always=always)
+
+
+@pytest.mark.parametrize("kind,H,group,D", [("fp32", 2, 4, 64), ("bf16", 1, 2, 256), ("fp8", 2, 2, 192), ("bf16", 1, 130, 32)])
+def test_shared_out_of_range_is_recorded_whatever_reads_the_cache(scute, contexts, kind, H, group, D):
+    """Starts and lengths outside are recorded for caches whose requests are read one by one, too."""
+    ctx, g = ctx_of(contexts, kind), np.random.default_rng(5)
+    b = Batch(scute, g, [(4, 320, lambda j: 320 + 40 * j)], H, group, D, 16, kind, behind=2)
+    n, cap, lens = 6, b.table.shape[1] * 16, i32(b.lens)
+    out, lse = torch.empty_like(b.q), torch.empty(n, H * group, device="cuda")
+    work = ctx.shared_work(b.cache, n, H * group)
+
+    def run(start, common, always=True):
+        ctx.paged_attention(b.cache, b.q, lens, out, lse=lse, shared=scute.Shared(i32(start), i32(common), work, always=always))
+        return ctx.sync_status()
+
+    many = [0] + [4] * 300
+    for start, common in (([-3, 4], [320]), ([0, 4, 99], [320, 5]), ([0, 4], [-5]), ([0, 4], [cap + 1]), ([4, 0], [320]), ([0, 5, 2], [320, 1]),
+                          ([6, 6, 0, 6], [1, 1, 1]), (many, [320] * 299 + [cap + 1]), (many[:-1] + [3], [320] * 300), ([7], [])):
+        for always in (True, False):
+            assert run(start, common, always) == (PAGES if common else 0)      # (no groups: nothing is read of them)
+            check_attend(out, lse, b.q, b.tokens, kind, group)
+    for start, common in (([0, 4], [320]), ([0, 6], [cap]), ([2, 2, 4], [0, 9]), (many, [320] * 300), ([6, 6], [cap])):
+        assert run(start, common) == 0
+    check_attend(out, lse, b.q, b.tokens, kind, group)
+    # the numbers are those of the call's place on the stream, changed before and after it
+    start, common = i32([0, 4]), i32([cap + 7])
+    sh = scute.Shared(start, common, work)
+    for _ in range(20):
+        common.fill_(320)
+        ctx.paged_attention(b.cache, b.q, lens, out, lse=lse, shared=sh)
+        common.fill_(cap + 7)
+    assert ctx.sync_status() == 0
+    ctx.paged_attention(b.cache, b.q, lens, out, lse=lse, shared=sh)
+    common.fill_(320)
+    assert ctx.sync_status() == PAGES
