@@ -650,3 +650,37 @@ def test_fork_records_pages_of_the_list_that_are_none(scute, contexts, n, outsid
         f.free[place] = outside
         ref = f.run(contexts["bf16"])[0]
         assert ref["ok"] == fine and np.count_nonzero(ref["copy_from"] >= 0) == n
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "fp8"])
+@pytest.mark.parametrize("window,sinks", [(1, 1), (20, 17), (64, 33), (100, 400), (100000, 5)])
+@pytest.mark.parametrize("H,group,D,page,token_major", [(2, 4, 256, 16, False), (1, 3, 192, 24, True), (1, 9, 144, 8, False)])
+def test_attention_window_and_first_tokens_of_wide_heads(scute, contexts, kind, window, sinks, H, group, D, page, token_major):
+    g = np.random.default_rng([window, sinks, D])
+    lens = EDGES + [5000]
+    cache, tokens = make_cache(scute, g, lens, H, D, page, kind, token_major, scales=kind == "fp8")
+    q = torch.from_numpy(g.standard_normal((len(lens), H * group, D), dtype=np.float32) * 1.5)
+    q = q.cuda().to(DT["fp32" if kind == "fp32" else "bf16"])
+    out, lse = torch.full_like(q, float("nan")), torch.empty(q.shape[:2], device="cuda")
+    ctx, was = ctx_of(contexts, kind), None
+    for _ in range(2):
+        ctx.paged_attention(cache, q, i32(lens), out, lse=lse, window=window, sinks=sinks)
+        assert ctx.sync_status() == 0
+        assert was is None or (torch.equal(out, was[0]) and torch.equal(lse, was[1]))
+        was = out.clone(), lse.clone()
+    check_attend(out, lse, q, [[x[OB.seen(len(x), window, sinks)] for x in kv] for kv in tokens], kind, group)
+
+
+@pytest.mark.parametrize("kind,group,D", [("fp8", 2, 64), ("bf16", 2, 64), ("bf16", 4, 128), ("fp8", 1, 32)])
+def test_attention_window_and_first_tokens_of_most_requests(scute, contexts, kind, group, D):
+    """The most requests a call takes, read by warps on their own, with whatever rings the list leaves them; or by
+    CTAs, where their parts are more than the context's workspace holds."""
+    g = np.random.default_rng([16384, D])
+    lens = [int(x) for x in g.integers(0, 60, 16384)]
+    cache, tokens = make_cache(scute, g, lens, 1, D, 16, kind, False)
+    q = torch.from_numpy(g.standard_normal((16384, group, D), dtype=np.float32) * 1.5).cuda().bfloat16()
+    out, lse = torch.full_like(q, float("nan")), torch.empty(q.shape[:2], device="cuda")
+    ctx = contexts["bf16"]
+    ctx.paged_attention(cache, q, i32(lens), out, lse=lse, window=20, sinks=5)
+    assert ctx.sync_status() == 0
+    check_attend(out, lse, q, [[x[OB.seen(len(x), 20, 5)] for x in kv] for kv in tokens], kind, group)

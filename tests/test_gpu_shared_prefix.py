@@ -450,3 +450,11 @@ def test_shared_out_of_range_is_recorded_whatever_reads_the_cache(scute, context
     ctx.paged_attention(b.cache, b.q, lens, out, lse=lse, shared=sh)
     common.fill_(320)
     assert ctx.sync_status() == PAGES
+
+
+@pytest.mark.parametrize("kind,group,D", [("fp8", 2, 64), ("bf16", 4, 128), ("fp8", 9, 128)])
+def test_shared_most_requests_of_wide_heads(scute, contexts, kind, group, D):
+    """The list of the most requests beside the rings of wide heads: one CTA on an SM with rings of five tiles,
+    and (e4m3, heads of 64) two with rings of two."""
+    g = np.random.default_rng([16384, D])
+    Batch(scute, g, [(16000, 30, lambda j: 30 + j % 3), (300, 20, lambda j: 20)], 1, group, D, 16, kind, behind=84).run(contexts["bf16"])
