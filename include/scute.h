@@ -537,7 +537,8 @@ scute_status scute_kv_append(scute_ctx *ctx, const scute_kv_cache *kv, const int
  *              head_dim;
  *   eps        >= 0.
  * rope NULL: no turning, of q as of k (q may then be given).  q NULL: q_w is not
- * read.  Everything else as for scute_kv_append. */
+ * read.  (q_heads + 2 kv_heads) * head_dim is at most 2^31 - 1.  Everything else as
+ * for scute_kv_append. */
 typedef struct {
     const float *q_w, *k_w;
     int64_t q_w_stride, k_w_stride;

@@ -72,6 +72,8 @@ scute_status append(scute_ctx *c, const scute_kv_cache *kv, const int32_t *slot_
         for (int64_t stride : {norm->q_w ? norm->q_w_stride : 0, norm->k_w ? norm->k_w_stride : 0})
             if (stride != 0 && stride < kv->head_dim)
                 return fail(c, SCUTE_ERR_SHAPE, "norm weights %lld apart", (long long)stride);
+        if ((q ? q_row : 0) + 2 * kv_row > 0x7fffffff)        // elements of a row are counted in 32 bits there
+            return fail(c, SCUTE_ERR_UNSUPPORTED, "rows of %lld elements with norms", (long long)((q ? q_row : 0) + 2 * kv_row));
         if (!aligned(norm->q_w, 4) || !aligned(norm->k_w, 4)) return fail(c, SCUTE_ERR_ARG, "weights are not aligned to their elements");
         w.q_w = q ? norm->q_w : nullptr;
         w.k_w = norm->k_w;

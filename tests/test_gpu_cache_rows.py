@@ -684,3 +684,16 @@ def test_attention_window_and_first_tokens_of_most_requests(scute, contexts, kin
     ctx.paged_attention(cache, q, i32(lens), out, lse=lse, window=20, sinks=5)
     assert ctx.sync_status() == 0
     check_attend(out, lse, q, [[x[OB.seen(len(x), 20, 5)] for x in kv] for kv in tokens], kind, group)
+
+
+def test_append_norm_refuses_rows_that_32_bits_do_not_count(scute, contexts):
+    ctx, heads, D = contexts["bf16"], 1 << 22, 256
+    pool, w, n = torch.zeros(2, 1, 16, D, dtype=torch.bfloat16, device="cuda"), torch.ones(D, device="cuda"), 1
+    cache, norm = scute.KvCache(pool, pool), scute.HeadNorm(w, w)
+    slots, k = i32([-1]), torch.zeros(D, dtype=torch.bfloat16, device="cuda")
+    cache.struct.kv_heads = heads
+    for q_heads in (0, 8):
+        q = k if q_heads else None
+        with pytest.raises(scute.ScuteError, match="elements"):
+            scute.scute_kv_append_norm(ctx.handle, cache, slots, n, k, heads * D, k, heads * D, q, q_heads * D, q_heads, q, q_heads * D, norm=norm)
+    assert ctx.sync_status() == 0
