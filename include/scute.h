@@ -363,7 +363,10 @@ typedef struct {
  * ceil(len_in[r] / page_size)) and shall have len_new[r].
  *   - A request that shrinks (to 0: it has ended) gives up its last pages.
  *     They go on top of the free list, in the order of requests and, within
- *     one, of its table.  Its table row is left as it is.
+ *     one, of its table.  Its table row is left as it is.  This call counts no
+ *     holders: of a request that shares pages with others (scute_kv_fork) it
+ *     would give up pages that the others still read, and nothing would notice.
+ *     Such a request is ended or shortened by scute_kv_fork;
  *   - A request that grows takes its pages from the top of the free list (the
  *     ones just given up included), in the order of requests; they are
  *     written behind its old ones in its row.  Requests are served while both
@@ -592,7 +595,9 @@ scute_status scute_paged_attention(scute_ctx *ctx, const scute_kv_cache *kv, con
 /* The same over the first tokens of a context and its last ones: request r's new
  * token sees the cached tokens t < sinks and t >= kv_len[r] - a->window, each
  * once, and with a->window = 0 all of them.  The tokens between are not read.
- * sinks is 0 (scute_paged_attention) .. 2^30; everything else as above. */
+ * Keys are taken as they are cached, turned at their own positions (a model that gives
+ * its first tokens new positions as the window moves needs keys cached unturned, and
+ * another call).  sinks is 0 (scute_paged_attention) .. 2^30; everything else as above. */
 scute_status scute_paged_attention_sinks(scute_ctx *ctx, const scute_kv_cache *kv, const scute_attention *a,
                                          int32_t sinks, void *stream);
 
@@ -602,7 +607,9 @@ scute_status scute_paged_attention_sinks(scute_ctx *ctx, const scute_kv_cache *k
  * whose first len[g] cached tokens lie in the same pages: each of their rows of the
  * block table names them (of a request with fewer tokens no row is read for them; it
  * is attended alone, as are requests before start[0] and from start[n_groups] on).  The
- * result is that of scute_paged_attention, summed in another order.
+ * result is that of scute_paged_attention, summed in another order; where a beginning is
+ * read for the group, a weight is rounded to 16 bits (an error of 2^-17 of it) with an
+ * E4M3 cache as with a BF16 one.
  *   start       device int32 [n_groups + 1], not falling, 0..n_req; len device int32
  *               [n_groups], 0..table_cols * page_size.  What lies outside counts as the
  *               nearest inside and is recorded (SCUTE_ERR_PAGES), as is a start that

@@ -115,7 +115,9 @@ class Context:
                   slot_map, positions, token_req, stream=None):
         """Pages for every request's new length, slots for its new tokens (device
         int32 tensors; scute.h has the layout).  The step has ``slot_map.numel()``
-        token rows."""
+        token rows.  Requests that share pages (``kv_fork``) are ended and shortened
+        by ``kv_fork``, not here: their pages would go to the free list while
+        others read them."""
         _check_table(block_table)
         n, (requests, cols) = len_in.numel(), block_table.shape
         rows, n_free = slot_map.numel(), free_pages.numel()

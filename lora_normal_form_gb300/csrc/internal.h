@@ -496,7 +496,7 @@ int attend_ctrs(int num_sms);
 cudaError_t launch_attend(const AttendArgs &a, int num_sms, cudaStream_t st);
 cudaError_t launch_attend_sinks(const AttendArgs &a, int num_sms, cudaStream_t st);
 cudaError_t launch_attend_own(const AttendArgs &a, int num_sms, cudaStream_t st);      // writes parts, for launch_join
-cudaError_t launch_attend_own_sinks(const AttendArgs &a, int num_sms, cudaStream_t st);  // the same of an e4m3 cache's windows and first tokens
+cudaError_t launch_attend_own_sinks(const AttendArgs &a, int num_sms, cudaStream_t st);  // the same of windows and first tokens
 long long own_rows(long long n_req, int q_heads, int kv_heads, int num_sms);             // of them, at most
 
 // ---------------------------------------------------------------- the beginning that a group's requests share
@@ -548,6 +548,11 @@ struct JoinArgs {
 //     e4m3  (alone twice as fast, together as fast) 1 x 64, 256 23.5 and 19.7, 512 23.3 and 24.7;
 //           12 x 64, 128 83.3 and 85.1, 256 89.9 and 111; 16 x 4, 1024 37.4 and 32.8; 1 x 4 on
 //           60000 69.2 and 77.4; 4 x 2, 30000 107 and 78, 4 x 3 107 and 117
+// By requests and tokens of a group alone, so that next to its borders it takes the slower side:
+// of these, 1 x 64 on 128 bf16 tokens (6 %) and on 256 e4m3 ones (19 %), 16 x 4 on 512 bf16 ones
+// (4 %), and 4 x 3 on 30000 e4m3 ones (9 %).  The number of groups, of key/value heads and of
+// heads to a key, which the parts' cost depends on too, are not in it; other numbers of heads
+// than these were not measured.
 template <typename Args>
 __device__ __forceinline__ bool read_together(const Args &a, int requests, int tokens) {
     const bool e4m3 = a.kv.dtype == KV_E4M3;

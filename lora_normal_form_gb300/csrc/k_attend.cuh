@@ -1297,9 +1297,7 @@ __global__ void __launch_bounds__(32 * (CW + PW), CTAS) attend_kernel(const Atte
     // a fetching warp may have ended before the wait that ran out
     if (!live && lane == 0) atomicOr(a.status, STATUS_TIMEOUT);
     // arrive at the shared rows; the last to arrive joins
-    if (head.r < 0 && tail.r < 0) {
-        return;
-    }
+    if (head.r < 0 && tail.r < 0) return;
     sync_threads<CW * 32>();
     if (t < 2) {
         const SharedRow &row = t ? tail : head;

@@ -681,8 +681,8 @@ __global__ void __launch_bounds__(256) kv_append_norm_kernel(const AppendArgs a,
 // it copies to a ring of its own in shared memory ahead of their use, asynchronously: no
 // other thread reads them, so that nothing waits but the thread itself.
 // Bound by memory and by the arithmetic beside it: 8772 rows of 32 + 2 x 8 heads of 128,
-// bf16, three axes, take 38.8 us, 5670 GB/s (84 % of the copy rate; without the norm
-// 38.0).  The same rows fetched to registers, two heads at a time: 54.8 (four CTAs on an
+// bf16, take 38.8 us, 5670 GB/s (84 % of the copy rate; without the norm 35.7; with positions of
+// three axes 39.6 and 36.8; to an e4m3 cache 44.9 and 37.8).  The same rows fetched to registers, two heads at a time: 54.8 (four CTAs on an
 // SM; two 65.7, three 56.7); with the ring and four CTAs, whose 64 registers spill, 44.4,
 // with two 47.4 (three: 40.3); a ring of three or six heads 48.2 and 50.6 (four: 48.1,
 // before the arithmetic went two numbers at a time and to one reciprocal root).  Items of

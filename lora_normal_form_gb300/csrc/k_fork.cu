@@ -332,9 +332,9 @@ __global__ void __cluster_dims__(FK_CLUSTER, 1, 1) __launch_bounds__(FK_THREADS)
 // ---------------------------------------------------------------- kv_copy
 // A CTA looks through `each` rows and copies the pages of those that have one, in one
 // pool, 16 bytes to a thread at a time, four of them on their way, in the order in which the
-// page's tokens and heads lie.  Bound by memory where many rows copy (4096 beams, some 2000
-// pages of one layer, 33 MB read and written: 16 us), else by its launch and the chain from
-// the list to the page (64 rows 5 us).
+// page's tokens and heads lie.  Bound by memory where many rows copy (4096 beams, some 1150
+// pages of one layer in part, 9300 tokens, 38 MB read and 38 written: 16 us), else by its launch
+// and the chain from the list to the page (64 rows 5 us).
 constexpr int CP_THREADS = 256, CP_ROWS = 32;
 __global__ void __launch_bounds__(CP_THREADS) kv_copy_kernel(const PageCopyArgs a, int each) {
     const int lane = threadIdx.x & 31;

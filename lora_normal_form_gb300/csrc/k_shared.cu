@@ -4,8 +4,8 @@
 // group instead of once for each request:
 //     S [rows x tokens] = Q K^T,   O [rows x D] = P V,   P = 2^(S - m).
 // What it leaves is not an output but parts, a row's maximum m, sum l and unnormalised
-// O over some of the tokens, which the one-token attention takes in when it ends the
-// request's row over the tokens of its own (k_attend.cuh).
+// O over some of the tokens; the requests' own tokens leave theirs (k_attend_own.cu), and
+// join_kernel below puts the parts of a row together.
 //
 // What bounds it.  A token costs 2 x D x size bytes and 2 x 2 x rows x D operations (the
 // second product twice over, see below, so 3 x 2): with bf16 keys 1.5 x rows
@@ -23,7 +23,8 @@
 // other's softmax.
 //
 // Weights go to the second product as two bf16 numbers, one rounded and what that left
-// (16 bits of a weight, 2^-17 of it, as in k_attend.cuh), l sums them in 32 bits.  The
+// (16 bits of a weight, 2^-17 of it: as in k_attend.cuh with a bf16 cache, where an e4m3
+// one's weights have 22), l sums them in 32 bits.  The
 // reference m moves only when a score passes it by more than 2^8, so that outputs are
 // seldom scaled.  Tokens behind the shared beginning's end are zero in shared memory and
 // their scores minus infinity.
@@ -374,19 +375,17 @@ __device__ __forceinline__ void write_pieces(const SharedArgs &a, const Plan &p,
     for (long long i = (long long)blockIdx.x * (LOAD / 2) + t; i < (long long)a.n_req * H; i += (long long)gridDim.x * (LOAD / 2)) {
         const int r = (int)(i / H), hk = (int)(i - (long long)r * H);
         int4 piece = make_int4(0, -1, 0, 0);
-        {
-            const int g = group_of(a, p, r, length_of(a, r));
-            if (g >= 0) {
-                const int tiles = tiles_of(p, g), b = (r - p.start[g]) / (2 * a.tile_req), blocks = p.blocks[g];
-                const int row = hk * blocks + b;
-                const WorkRow w = work_row(a, p, g, row);
-                const int x = !w.twin && r - w.r0 >= a.tile_req;
-                const long long base = p.at[g] + (long long)row * (tiles + ROW_COST) + ROW_COST;
-                piece.x = cut.owner(base);
-                piece.y = cut.owner(base + tiles - 1) | (w.twin ? SHARED_TWIN : 0);
-                piece.z = part_row(a, w, 0, x);
-                piece.w = stream_requests(a, w, x) * a.group | (r - w.r0 - x * a.tile_req) * a.group << 16;
-            }
+        const int g = group_of(a, p, r, length_of(a, r));
+        if (g >= 0) {
+            const int tiles = tiles_of(p, g), b = (r - p.start[g]) / (2 * a.tile_req), blocks = p.blocks[g];
+            const int row = hk * blocks + b;
+            const WorkRow w = work_row(a, p, g, row);
+            const int x = !w.twin && r - w.r0 >= a.tile_req;
+            const long long base = p.at[g] + (long long)row * (tiles + ROW_COST) + ROW_COST;
+            piece.x = cut.owner(base);
+            piece.y = cut.owner(base + tiles - 1) | (w.twin ? SHARED_TWIN : 0);
+            piece.z = part_row(a, w, 0, x);
+            piece.w = stream_requests(a, w, x) * a.group | (r - w.r0 - x * a.tile_req) * a.group << 16;
         }
         a.piece[i] = piece;
     }
