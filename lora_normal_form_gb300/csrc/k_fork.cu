@@ -65,7 +65,7 @@ __device__ __forceinline__ int now(const int *p) { return *(const volatile int *
 
 __device__ __forceinline__ void fork_count(const ForkArgs &a, int cta, int ctas) {
     const int lane = threadIdx.x & 31;
-    const int rows = max(a.n_in, a.n_out), spans = (a.cols + FK_SPAN - 1) / FK_SPAN;
+    const int rows = max(a.n_in, a.n_out), spans = (a.cols - 1) / FK_SPAN + 1;
     const long long items = (long long)rows * spans, step = (long long)ctas * (FK_THREADS / 32);
     bool bad = false;
     for (long long i = (long long)cta * (FK_THREADS / 32) + (threadIdx.x >> 5); i < items; i += step) {
@@ -122,7 +122,7 @@ __device__ __forceinline__ void fork_claim(const ForkArgs &a, int cta, int ctas)
             atomicMin(a.extra + p, r - INT32_MAX);
         }
     } else {                                           // beside them, so that neither waits for the other's loads
-        const int spans = (a.cols + FK_SPAN - 1) / FK_SPAN;
+        const int spans = (a.cols - 1) / FK_SPAN + 1;
         const long long items = (long long)a.n_out * spans, step = (long long)(ctas - claiming) * (FK_THREADS / 32);
 #pragma unroll 1
         for (long long i = (long long)(cta - claiming) * (FK_THREADS / 32) + (threadIdx.x >> 5); i < items; i += step) {
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(CP_THREADS) kv_copy_kernel(const PageCopyArgs 
 
 cudaError_t launch_kv_fork(const ForkArgs &a, int num_sms, int *launches, cudaStream_t st) {
     const int warps = FK_THREADS / 32;
-    const long long rows = max(a.n_in, a.n_out), items = rows * ((a.cols + FK_SPAN - 1) / FK_SPAN);
+    const long long rows = max(a.n_in, a.n_out), items = rows * ((a.cols - 1) / FK_SPAN + 1);
     const int most = min(num_sms, FORK_MAX_CTAS);
     const int row_grid = max(1, min(most, (a.n_out + FK_THREADS - 1) / FK_THREADS));
     const int span_grid = (int)max(1ll, min(4ll * most, (items + warps - 1) / warps));

@@ -697,3 +697,22 @@ def test_append_norm_refuses_rows_that_32_bits_do_not_count(scute, contexts):
         with pytest.raises(scute.ScuteError, match="elements"):
             scute.scute_kv_append_norm(ctx.handle, cache, slots, n, k, heads * D, k, heads * D, q, q_heads * D, q_heads, q, q_heads * D, norm=norm)
     assert ctx.sync_status() == 0
+
+
+def test_fork_of_the_widest_table(scute, contexts):
+    """A row of as many entries as a table may have, few of them pages."""
+    cols, n, m, pages = 2 ** 31 - 1, 5000, 4099, 6000
+    g = np.random.default_rng(31)
+    order = g.permutation(pages)
+    ref = OB.fork(order[None, :n], [n], [0], [m], np.full((1, n), -1), 1, [0] * pages, order[n:].tolist())
+    whole = lambda x: i32(np.asarray(x, np.int64))  # noqa: E731
+    table, out = (torch.empty(1, cols, dtype=torch.int32, device="cuda") for _ in range(2))
+    table[0, :n], out[0, :n + 9] = whole(order[:n]), -1
+    extra, free, count = whole([0] * pages), whole([0] * pages), whole([pages - n])
+    free[:pages - n] = whole(order[n:])
+    vec = [whole([7]) for _ in range(4)]
+    contexts["bf16"].kv_fork(table, whole([n]), whole([0]), out, vec[0], 1, extra, free, count, count, *vec[1:], len_new=whole([m]))
+    assert contexts["bf16"].sync_status() == 0
+    assert [int(x) for x in vec] == [m, -1, -1, 0] and ref["ok"] and not extra.any()
+    assert out[0, :n].cpu().tolist() == ref["table"][0].tolist() and torch.all(out[0, n:n + 9] == -1)
+    assert free[:int(count)].cpu().tolist() == ref["free"] and torch.equal(table[0, :n], whole(order[:n]))
