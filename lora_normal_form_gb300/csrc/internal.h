@@ -436,6 +436,7 @@ struct ForkArgs {
     long long out_stride;
     int n_in, n_out, cols, page_size, n_pages;
     int page_shift;            // log2 of the page size, or -1
+    int claiming, parts;       // CTAs that claim, warps that look through a row (launch_kv_fork)
     int32_t *extra, *free_pages;
     long long n_free_max;
     const int32_t *free_in;

@@ -26,7 +26,7 @@ namespace {
 // No step waits for another's threads, so that the order in which the device works
 // decides nothing.  Bound by latency, a chain of three or four dependent loads in every
 // step and the launches (or the cluster's barriers) between: 64 beams of 200 to 8192 tokens
-// 12.5 us, one prompt to 64 samples 15, 4096 beams 13.7 (counts and tables are 0.5 MB);
+// 12.5 us, one prompt to 64 samples 15.4, 4096 beams 13.5 (counts and tables are 0.5 MB);
 // without the second look at pages held whole 11.1, 12.8 and 12.8.
 constexpr int FK_THREADS = 512;
 constexpr int FK_LIST = 0, FK_FREED = 16, FK_BITS = FK_FREED + FORK_MAX_CTAS;    // the workspace's parts
@@ -111,10 +111,10 @@ __device__ __forceinline__ int last_page(const ForkArgs &a, int r, NewRow *x) {
 }
 
 __device__ __forceinline__ void fork_claim(const ForkArgs &a, int cta, int ctas) {
-    const int lane = threadIdx.x & 31, claiming = min((a.n_out + FK_THREADS - 1) / FK_THREADS, ctas - 1);
+    const int lane = threadIdx.x & 31;
     bool bad = false;
-    if (cta < claiming) {
-        for (int r = cta * FK_THREADS + threadIdx.x; r < a.n_out; r += claiming * FK_THREADS) {
+    if (cta < a.claiming) {
+        for (int r = cta * FK_THREADS + threadIdx.x; r < a.n_out; r += a.claiming * FK_THREADS) {
             NewRow x;
             const int p = last_page(a, r, &x), e = in_pool(a, p) ? now(a.extra + p) : 0;
             if (e >= 0) continue;
@@ -122,23 +122,31 @@ __device__ __forceinline__ void fork_claim(const ForkArgs &a, int cta, int ctas)
             atomicMin(a.extra + p, r - INT32_MAX);
         }
     } else {                                           // beside them, so that neither waits for the other's loads
-        const int spans = (a.cols - 1) / FK_SPAN + 1;
-        const long long items = (long long)a.n_out * spans, step = (long long)(ctas - claiming) * (FK_THREADS / 32);
+        const int spans = (a.cols - 1) / FK_SPAN + 1, items = a.n_out * a.parts, step = (ctas - a.claiming) * (FK_THREADS / 32);
 #pragma unroll 1
-        for (long long i = (long long)(cta - claiming) * (FK_THREADS / 32) + (threadIdx.x >> 5); i < items; i += step) {
-            const int r = (int)(i / spans), j0 = (int)(i - (long long)r * spans) * FK_SPAN;
+        for (int i = (cta - a.claiming) * (FK_THREADS / 32) + (threadIdx.x >> 5); i < items; i += step) {
+            const int r = i / a.parts;
             const int32_t *to = a.table_out + r * a.out_stride;
-            int q[FK_SPAN / 32];
+            const int first = i - r * a.parts;
+            int full = a.cols;                         // of the first span's entries, asked for before the row's tokens are known
+#pragma unroll 1
+            for (int s = first; s < spans; s += a.parts) {
+                const int j0 = s * FK_SPAN;
+                if (j0 >= full) break;
+                int q[FK_SPAN / 32], e[FK_SPAN / 32], any = 0;
 #pragma unroll
-            for (int k = 0; k < FK_SPAN / 32; ++k) {
-                const int j = j0 + k * 32 + lane;
-                q[k] = j < a.cols ? now(to + j) : -1;  // (asked for before the row's tokens are known)
+                for (int k = 0; k < FK_SPAN / 32; ++k) {
+                    const int j = j0 + k * 32 + lane;
+                    q[k] = j < full ? now(to + j) : -1;
+                }
+                bool seen = false;                     // recorded by the first step
+                if (s == first) full = page_index(a, new_row(a, r, &seen).len);
+#pragma unroll
+                for (int k = 0; k < FK_SPAN / 32; ++k) e[k] = j0 + k * 32 + lane < full && in_pool(a, q[k]) ? now(a.extra + q[k]) : 0;
+#pragma unroll
+                for (int k = 0; k < FK_SPAN / 32; ++k) any |= e[k];
+                bad |= any < 0;
             }
-            bool seen = false;                         // recorded by the first step
-            const int full = page_index(a, new_row(a, r, &seen).len);
-#pragma unroll
-            for (int k = 0; k < FK_SPAN / 32; ++k)
-                if (j0 + k * 32 + lane < full && in_pool(a, q[k])) bad |= now(a.extra + q[k]) < 0;
         }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, STATUS_PAGES);
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(FK_THREADS) fork_step_kernel(const ForkArgs a)
 
 // All four by one cluster, its barrier between them: where there is little to do, four
 // launches cost more than the step (64 beams with kv_copy: a call through Python 40 us, by four
-// launches 49; in a graph, where launches cost less, 17.3 and 16.3).
+// launches 49; in a graph, where launches cost less, 17.4 and 16.3).
 constexpr int FK_CLUSTER = 8;
 __global__ void __cluster_dims__(FK_CLUSTER, 1, 1) __launch_bounds__(FK_THREADS) fork_cluster_kernel(const ForkArgs a) {
     __shared__ AssignShared s;
@@ -379,21 +387,31 @@ __global__ void __launch_bounds__(CP_THREADS) kv_copy_kernel(const PageCopyArgs 
 
 }  // namespace
 
-cudaError_t launch_kv_fork(const ForkArgs &a, int num_sms, int *launches, cudaStream_t st) {
+cudaError_t launch_kv_fork(const ForkArgs &args, int num_sms, int *launches, cudaStream_t st) {
+    ForkArgs a = args;
     const int warps = FK_THREADS / 32;
     const long long rows = max(a.n_in, a.n_out), items = rows * ((a.cols - 1) / FK_SPAN + 1);
     const int most = min(num_sms, FORK_MAX_CTAS);
     const int row_grid = max(1, min(most, (a.n_out + FK_THREADS - 1) / FK_THREADS));
     const int span_grid = (int)max(1ll, min(4ll * most, (items + warps - 1) / warps));
     const int page_grid = max(row_grid, (int)min((long long)most, ((long long)a.n_pages + FK_THREADS - 1) / FK_THREADS));
+    // the claiming step's CTAs: a thread to a row; and warps to a row's entries, two turns of all of
+    // them for all rows (4096 rows of up to 32 pages in tables of 8192 columns 75 us, with four turns
+    // 80, with a span of every row to each warp in turn 102; without the look 68)
+    const auto claims = [&](int grid) {
+        a.claiming = min(row_grid, grid - 1);
+        a.parts = min((a.cols - 1) / FK_SPAN + 1, max(1, 2 * (grid - a.claiming) * warps / max(a.n_out, 1)));
+        return grid;
+    };
     // one cluster up to as many table spans and pages as its warps take in a few turns
     if (items <= 4 * FK_CLUSTER * warps && a.n_pages <= 16 * FK_CLUSTER * FK_THREADS) {
         *launches = 1;
+        claims(FK_CLUSTER);
         return launch_chained(fork_cluster_kernel, FK_CLUSTER, FK_THREADS, 0, st, a);
     }
     *launches = 4;
     cudaError_t e = launch_chained(fork_step_kernel<0>, span_grid, FK_THREADS, 0, st, a);
-    if (e == cudaSuccess) e = launch_chained(fork_step_kernel<1>, row_grid + span_grid, FK_THREADS, 0, st, a);
+    if (e == cudaSuccess) e = launch_chained(fork_step_kernel<1>, claims(row_grid + span_grid), FK_THREADS, 0, st, a);
     if (e == cudaSuccess) e = launch_chained(fork_step_kernel<2>, page_grid, FK_THREADS, 0, st, a);
     if (e == cudaSuccess) e = launch_chained(fork_step_kernel<3>, page_grid, FK_THREADS, 0, st, a);
     return e;

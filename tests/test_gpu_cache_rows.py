@@ -716,3 +716,18 @@ def test_fork_of_the_widest_table(scute, contexts):
     assert [int(x) for x in vec] == [m, -1, -1, 0] and ref["ok"] and not extra.any()
     assert out[0, :n].cpu().tolist() == ref["table"][0].tolist() and torch.all(out[0, n:n + 9] == -1)
     assert free[:int(count)].cpu().tolist() == ref["free"] and torch.equal(table[0, :n], whole(order[:n]))
+
+
+@pytest.mark.parametrize("n,cols", [(60, 2000), (600, 300), (2, 40000)])
+def test_fork_looks_at_every_page_that_rows_take_whole(scute, contexts, n, cols):
+    """A page of more rows than its count allows, at any place of a long row."""
+    f = object.__new__(Fork)
+    f.page, f.cols, f.n_pages, f.free = 1, cols, n * cols + 2, [n * cols, n * cols + 1]
+    own = np.random.default_rng(n).permutation(n * cols).reshape(n, cols)
+    f.extra, f.source, f.len_new = np.zeros(f.n_pages, np.int64), np.arange(n), np.full(n, cols)
+    for r, j in ((n // 2, None), (0, 0), (n - 1, cols - 1), (n // 2, 255), (1, 256), (n - 1, cols // 2 + 1)):
+        f.table = np.concatenate([own, np.full((1, cols), -1)])
+        f.len_in = np.append(np.full(n, cols), 0 if j is None else 1)
+        if j is not None:
+            f.table[n, 0] = own[r, j]                       # the last old row, which nobody continues
+        assert f.run(contexts["bf16"])[0]["ok"] == (j is None)
