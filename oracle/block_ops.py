@@ -189,5 +189,7 @@ def fork(table_in, len_in, source, len_new, table_out, page_size, extra, free, n
         table[r, full] = copy_to[r] = free.pop()
         copy_from[r], copy_tokens[r] = p, rest
         ok = ok and inside(copy_to[r])
+    if n_free_max is not None and len(free) > n_free_max:     # the list's end: what is beyond it is lost
+        ok, free = False, free[:n_free_max]
     return {"table": table, "len_out": np.array(len_out, np.int64), "extra": np.array(extra, np.int64), "free": free,
             "copy_from": np.array(copy_from), "copy_to": np.array(copy_to), "copy_tokens": np.array(copy_tokens), "ok": ok}

@@ -128,3 +128,104 @@ def test_prompts_samples_and_beams(scute, kind):
     at = branch(at, np.full(n, -1), np.zeros(n, np.int64))
     assert int(count) == total and sorted(free.tolist()) == list(range(total)) and not extra.any()
     ctx.close()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_captured_steps_of_two_contexts_at_once(scute, kind):
+    """A step of beams (fork, copy, growth, normed append, shared and windowed attention) captured as a graph for
+    each of two contexts, both replayed on streams of their own at the same time, on other choices and lengths
+    each time: the bits of the same steps run one after the other without a graph."""
+    g = np.random.default_rng(6)
+    prompts, width, H, group, D, page, cols, total, steps = [500, 77, 16, 901], 5, 2, 4, 64, 16, 80, 700, 6
+    n, heads = len(prompts) * width, H * group
+    whole = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    cs = torch.empty(2048, D, device="cuda")
+    # prompts in whole pages: every row's table begins with them
+    table0, length0, extra0, at = np.full((n, cols), -1), np.repeat(prompts, width), np.zeros(total, np.int64), 0
+    for p, m in enumerate(prompts):
+        k = m // page
+        table0[p * width:(p + 1) * width, :k] = np.arange(at, at + k)
+        extra0[at:at + k], at = width - 1, at + k
+        if m % page:
+            for r in range(p * width, (p + 1) * width):
+                table0[r, k], at = at, at + 1
+    free0 = np.pad(np.arange(at, total), (0, at))
+    pool0 = [torch.randn(total, H, page, D, device="cuda", generator=torch.Generator(device="cuda").manual_seed(i)).bfloat16() for i in range(2)]
+    choices = [(np.repeat(np.arange(len(prompts)) * width, width) + g.integers(0, width, n)).astype(np.int64) for _ in range(steps)]
+    start = i32(np.arange(len(prompts) + 1) * width)
+    common = i32([m // page * page for m in prompts])
+    w = torch.rand(D, device="cuda") + 0.5
+
+    class Server:
+        def __init__(self, seed):
+            self.ctx = scute.Context(dtype="bf16", max_tokens=64, max_adapters=1, max_layers=1)
+            self.ctx.rope_table(cs, 10000.0)
+            self.pools = [x.clone() if kind == "bf16" else x.to(torch.float8_e4m3fn) for x in pool0]
+            self.tables, self.length = [i32(table0), whole(n, cols) - 1], [i32(length0), whole(n)]
+            self.extra, self.free, self.count = i32(extra0), i32(free0), i32([total - at])
+            self.cache = [scute.KvCache(*self.pools, t) for t in self.tables]
+            self.both = scute.KvCaches([self.cache[0]])
+            self.vec, self.cu, self.one = [whole(n) for _ in range(7)], whole(n + 1), whole(n) + 1
+            gen = torch.Generator(device="cuda").manual_seed(seed)
+            self.q, self.k, self.v = (torch.randn(n, h, D, device="cuda", generator=gen).bfloat16() for h in (heads, H, H))
+            self.qr, self.out, self.win = (torch.zeros(n, heads, D, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+            self.lse = torch.zeros(n, heads, device="cuda")
+            self.source, self.want = whole(n), whole(n)
+            self.shared = [scute.Shared(start, common, self.ctx.shared_work(c, n, heads), always=True) for c in self.cache]
+            self.rope, self.norm = scute.Rope(cs, self.vec[5]), scute.HeadNorm(w, w)
+
+        def half(self, a):
+            b, ctx, (cf, ct, cn, slots, new, pos, req) = 1 - a, self.ctx, self.vec
+            ctx.kv_fork(self.tables[a], self.length[a], self.source, self.tables[b], self.length[b], page, self.extra, self.free, self.count,
+                        self.count, cf, ct, cn)
+            ctx.kv_copy(self.both, cf, ct, cn)
+            torch.add(self.length[b], self.one, out=self.want)
+            ctx.kv_resize(self.length[b], self.want, self.tables[b], page, self.free, self.count, self.count, self.length[b], self.cu, slots,
+                          pos, req)
+            ctx.kv_append(self.cache[b], slots, self.k, self.v, q=self.q, q_out=self.qr, rope=self.rope, norm=self.norm)
+            ctx.paged_attention(self.cache[b], self.qr, self.length[b], self.out, lse=self.lse, shared=self.shared[b])
+            ctx.paged_attention(self.cache[b], self.qr, self.length[b], self.win, window=60, sinks=5)
+
+        def seen(self):
+            return [x.clone() for x in (self.out, self.lse, self.win, *self.length, self.extra, self.count, *(p.view(torch.uint8) for p in self.pools))]
+
+    def advance(s, i):
+        s.source.copy_(i32(choices[i]))
+
+    plain = [Server(s) for s in (1, 2)]
+    want = [[], []]
+    for i in range(steps):
+        for j, s in enumerate(plain):
+            advance(s, i)
+            s.half(i % 2)
+            want[j].append(s.seen())
+            assert s.ctx.sync_status() == 0
+    servers, streams = [Server(s) for s in (1, 2)], [torch.cuda.Stream() for _ in range(2)]
+    graphs = []
+    for s in servers:
+        pair = []
+        for a in (0, 1):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                s.half(a)
+            pair.append(graph)
+        graphs.append(pair)
+    torch.cuda.synchronize()
+    got = [[], []]
+    for i in range(steps):
+        for s in servers:
+            advance(s, i)
+        torch.cuda.synchronize()
+        for s, pair, stream in zip(servers, graphs, streams):
+            with torch.cuda.stream(stream):
+                pair[i % 2].replay()
+        torch.cuda.synchronize()
+        for j, s in enumerate(servers):
+            got[j].append(s.seen())
+            assert s.ctx.sync_status() == 0
+    for j in range(2):
+        for x, y in zip(got[j], want[j]):
+            assert all(torch.equal(p, q) for p, q in zip(x, y))
+    assert not torch.equal(got[0][-1][0], got[1][-1][0])
+    for s in plain + servers:
+        s.ctx.close()

@@ -731,3 +731,42 @@ def test_fork_looks_at_every_page_that_rows_take_whole(scute, contexts, n, cols)
         if j is not None:
             f.table[n, 0] = own[r, j]                       # the last old row, which nobody continues
         assert f.run(contexts["bf16"])[0]["ok"] == (j is None)
+
+
+@pytest.mark.parametrize("n", [5, 700])
+def test_fork_of_lists_too_short_for_what_comes_back(scute, contexts, n):
+    """Pages beyond the list's room are lost and recorded; rows that copy take them before."""
+    whole = lambda x: i32(np.asarray(x, np.int64))  # noqa: E731
+    for room, copies in ((0, 0), (3, 0), (n - 1, 2), (n, 0), (n + 2, 2), (2 * n + 2, 0)):
+        # old rows of two pages, the second in part; a third of them goes on, the first `copies` twice
+        table, extra, free = np.arange(2 * n).reshape(n, 2), [0] * (2 * n + 2), [2 * n, 2 * n + 1][:room]
+        source = list(range(n // 3)) + list(range(copies))
+        ref = OB.fork(table, [20] * n, source, None, np.full((len(source), 2), -1), 16, extra, free, room)
+        got, counts, count = torch.full((len(source), 2), -1, dtype=torch.int32, device="cuda"), whole(extra), whole([len(free)])
+        slots = torch.full((room + 4,), -9, dtype=torch.int32, device="cuda")
+        slots[:len(free)] = whole(free)
+        vec = [torch.zeros(len(source), dtype=torch.int32, device="cuda") for _ in range(4)]
+        contexts["bf16"].kv_fork(whole(table), whole([20] * n), whole(source), got, vec[0], 16, counts, slots[:room], count, count, *vec[1:])
+        assert contexts["bf16"].sync_status() == (0 if ref["ok"] else PAGES)
+        assert int(count) == len(ref["free"]) and slots[:int(count)].cpu().tolist() == ref["free"] and torch.all(slots[room:] == -9)
+        assert np.array_equal(got.cpu().numpy(), ref["table"]) and np.array_equal(counts.cpu().numpy(), ref["extra"])
+        for t, name in zip(vec, ("len_out", "copy_from", "copy_to", "copy_tokens")):
+            assert np.array_equal(t.cpu().numpy(), ref[name])
+
+
+def test_fork_of_no_rows_and_no_pages(scute, contexts):
+    none, one = torch.zeros(0, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    table = torch.zeros(0, 4, dtype=torch.int32, device="cuda")
+    out = torch.full((1,), 7, dtype=torch.int32, device="cuda")
+    ctx = contexts["bf16"]
+    ctx.kv_fork(table, none, none, table, none, 16, none, none, one, out, none, none, none)
+    assert ctx.sync_status() == 0 and int(out) == 0
+    # all rows let go, none taken; rows without tokens of rows without tokens
+    extra, free, count = torch.zeros(9, dtype=torch.int32, device="cuda"), torch.zeros(9, dtype=torch.int32, device="cuda"), one.clone()
+    ctx.kv_fork(i32([[3, 1], [8, -1]]), i32([17, 16]), none, table[:, :2], none, 16, extra, free, count, count, none, none, none)
+    assert ctx.sync_status() == 0 and int(count) == 3 and free[:3].tolist() == [1, 3, 8] and not extra.any()
+    vec = [torch.full((2,), 7, dtype=torch.int32, device="cuda") for _ in range(4)]
+    wide = torch.full((2, 2), -7, dtype=torch.int32, device="cuda")
+    ctx.kv_fork(i32([[-1, -1]]), i32([0]), i32([0, -1]), wide, vec[0], 16, extra, free, count, count, *vec[1:])
+    assert ctx.sync_status() == 0 and int(count) == 3 and torch.all(wide == -7)
+    assert [x.tolist() for x in vec] == [[0, 0], [-1, -1], [-1, -1], [0, 0]]
