@@ -574,7 +574,8 @@ scute_status scute_kv_append_norm(scute_ctx *ctx, const scute_kv_cache *kv, cons
  * over all requests; q_heads a multiple of kv_heads.  Scores, softmax
  * statistics and sums are held in 32 bits.  What is rounded to fewer on the way:
  * a weight as it is multiplied with a value, to 16 bits with a BF16 cache (an error
- * of 2^-17 of it), 22 with an E4M3 one, none with FP32; and queries before an E4M3
+ * of 2^-17 of it), 22 with an E4M3 one (or to 2^-32 of the largest weight, what is
+ * coarser), none with FP32; and queries before an E4M3
  * cache's keys, below 2^-22 of their head's largest element.  The work is cut over the
  * whole batch's tokens, whatever request they belong to, and joined in a fixed
  * order: the same call gives the same bits. */
